@@ -394,10 +394,11 @@ def _run_own(s):
         dx, dw, db = nv.layernorm_backward(s["dy"], s["x"], s["weight"], s["mean"], s["rstd"], dsum=s["dsum"])
         return dict(dx=dx, dweight=dw, dbias=db)
     if s["op"] == "adamw":
-        nv.adamw([nv.AdamWTensor(t["param"], t["grad"], t["m"], t["v"], t.get("m_scale"), t.get("v_scale"),
-                                 weight_decay=t["decay"], copy=t["copy"]) for t in s["tensors"]],
-                 lr=LR, beta1=BETA1, beta2=BETA2, eps=EPS_ADAM, step=s["step"], rounding=s["rounding"], seed=s["seed"],
-                 grad_scale=s["grad_scale"])
+        if "list" not in s:  # a training program lays its tensors' list out once
+            s["list"] = nv.AdamWList([nv.AdamWTensor(t["param"], t["grad"], t["m"], t["v"], t.get("m_scale"), t.get("v_scale"),
+                                                     weight_decay=t["decay"], copy=t["copy"]) for t in s["tensors"]])
+        nv.adamw(s["list"], lr=LR, beta1=BETA1, beta2=BETA2, eps=EPS_ADAM, step=s["step"], rounding=s["rounding"],
+                 seed=s["seed"], grad_scale=s["grad_scale"])
         return _updated(s)
     opts = dict(causal=s["causal"], window=s["window"], scale=s["scale"])
     if s["cu"] is not None:
