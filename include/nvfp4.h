@@ -60,6 +60,7 @@ extern "C" {
 #define NVFP4_E_UNSUPPORTED (-5) /* unknown enum, RHT with a 2D layout, bad n_outs, K mismatch */
 #define NVFP4_E_WORKSPACE (-6)   /* workspace NULL or smaller than nvfp4_workspace_bytes() */
 #define NVFP4_E_HIP (-7)         /* a HIP launch failed */
+#define NVFP4_E_VALUE (-8)       /* a scalar argument out of its range (training operators) */
 
 /* layouts of one quantised output of an input x[rows][cols] */
 #define NVFP4_ROW_1D 0 /* 1D blocks of 16 along cols; stored [rows][cols] */
@@ -343,6 +344,193 @@ int mxfp4_gemm(const mxfp4_tensor *a, const mxfp4_tensor *b, void *c, int32_t c_
  */
 int nvfp4_codec_selftest(int which, const float *in_f32, const uint16_t *in_u16, uint8_t *out_u8, int64_t n,
                          void *stream);
+
+/* ------------------------------------------------------------------------
+ * Training operators: what a pretraining step runs beside its 4-bit products.
+ * The page names none of them; their formulas stand with each entry point.
+ * The conventions above hold (device pointers of the caller's, nothing
+ * allocated, nothing kept, checks before anything is enqueued, any stream),
+ * with these differences: sizes need not be multiples of 16, and NVFP4_F32 /
+ * NVFP4_BF16 name the element types.  Inputs must be finite.  Results do not
+ * depend on the order in which workgroups run: no sum is formed by atomics.
+ * ------------------------------------------------------------------------ */
+
+/* One layer norm over the rows of x[rows][cols]. */
+typedef struct {
+  const void *x;         /* [rows][cols], x_dtype, row stride ld_x */
+  const void *residual;  /* NULL, or [rows][cols], x_dtype, row stride ld_residual */
+  const void *weight;    /* [cols], w_dtype */
+  const void *bias;      /* NULL (zeros), or [cols], w_dtype */
+  void *y;               /* [rows][cols], y_dtype, row stride ld_y */
+  void *sum;             /* with a residual: [rows][cols], x_dtype, row stride ld_sum; else NULL */
+  float *mean;           /* [rows] */
+  float *rstd;           /* [rows] */
+  float *amax;           /* NULL, or 1 float */
+  int64_t rows, cols;
+  int64_t ld_x, ld_residual, ld_y, ld_sum; /* elements */
+  int32_t x_dtype, y_dtype, w_dtype;       /* NVFP4_F32 or NVFP4_BF16 */
+  float eps;                               /* >= 0 */
+} nvfp4_layernorm_args;
+
+/*
+ * nvfp4_layernorm -- s = x + residual (rounded to x_dtype and stored to sum;
+ * s = x without a residual), mean = sum_c s / cols,
+ * rstd = 1 / sqrt(sum_c (s - mean)^2 / cols + eps),
+ * y = (s - mean) * rstd * weight + bias.
+ * All arithmetic in binary32; y is rounded once.  *amax becomes
+ * max(*amax, max |y|) over the stored y (an atomic maximum: the caller
+ * initialises it), which is what NVFP4_AMAX_GIVEN asks of a quantisation of y
+ * without the RHT.  y may be x or residual, sum may be x or residual.
+ * rows < 2^31, cols <= 32768.  One kernel.  Pointers that are 16-byte aligned, row
+ * strides that are multiples of 16 bytes and cols % 8 == 0 give 16-byte
+ * accesses; element-aligned ones are accepted and slower.
+ */
+int nvfp4_layernorm(const nvfp4_layernorm_args *args, void *stream);
+
+/* The gradient of one layer norm. */
+typedef struct {
+  const void *dy;       /* [rows][cols], y_dtype, row stride ld_dy: the gradient of y */
+  const void *x;        /* [rows][cols], x_dtype, row stride ld_x: what was normalised (sum, with a residual) */
+  const void *weight;   /* [cols], w_dtype */
+  const float *mean;    /* [rows], of the forward call */
+  const float *rstd;    /* [rows], of the forward call */
+  const void *dsum;     /* NULL, or [rows][cols], x_dtype, row stride ld_dsum: the gradient that reaches x by other paths */
+  void *dx;             /* [rows][cols], x_dtype, row stride ld_dx */
+  float *dweight;       /* NULL, or [cols] */
+  float *dbias;         /* NULL, or [cols] */
+  float *amax;          /* NULL, or 1 float: becomes max(*amax, max |dx|) over the stored dx */
+  int64_t rows, cols;
+  int64_t ld_dy, ld_x, ld_dsum, ld_dx;
+  int32_t x_dtype, y_dtype, w_dtype;
+} nvfp4_layernorm_backward_args;
+
+/*
+ * nvfp4_layernorm_backward -- with h = (x - mean) * rstd and a = dy * weight:
+ *   dx = rstd * (a - mean_c(a) - h * mean_c(a * h)) (+ dsum)
+ *   dweight = sum_rows dy * h,  dbias = sum_rows dy   (overwritten, binary32)
+ *   workspace  device scratch of nvfp4_layernorm_backward_workspace_bytes(rows,
+ *              cols) bytes, 16-byte aligned (not needed when dweight and dbias
+ *              are NULL): per-workgroup partial sums, added in a fixed order.
+ * dx may be dy or dsum.  One kernel, and a second one for dweight and dbias.
+ */
+int nvfp4_layernorm_backward(const nvfp4_layernorm_backward_args *args, void *workspace, size_t workspace_bytes,
+                             void *stream);
+size_t nvfp4_layernorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/* A bf16 tensor [batch][tokens][heads][head_dim] with the last dimension
+ * contiguous; strides in elements.  With packed sequences the tokens of all
+ * sequences follow each other and batch_stride is not used. */
+typedef struct {
+  void *data;
+  int64_t batch_stride, token_stride, head_stride;
+} nvfp4_heads;
+
+/* What an attention call works on. */
+typedef struct {
+  int64_t batch;       /* sequences, >= 1 */
+  int64_t q_len;       /* queries of each sequence (packed: the most that any has), 1 .. 2^30 */
+  int64_t k_len;       /* keys of each sequence (packed: the most that any has), 1 .. 2^30 */
+  int32_t heads;       /* query heads, a multiple of kv_heads: head h reads key head h / (heads / kv_heads) */
+  int32_t kv_heads;
+  int32_t head_dim;    /* a multiple of 8, 8 .. 128 */
+  int32_t causal;      /* 1: of a sequence with q queries and k keys, query i sees the keys j <= i + k - q */
+  int64_t window;      /* 0, or with causal: query i sees only j > i + k - q - window, too */
+  const int32_t *cu_q; /* NULL, or device [batch + 1]: packed sequences, sequence b has tokens cu_q[b] .. cu_q[b+1]-1 */
+  const int32_t *cu_k; /* as cu_q, for keys and values; both or neither */
+  int64_t total_q;     /* packed: tokens of q; else batch * q_len */
+  int64_t total_k;     /* packed: tokens of k; else batch * k_len */
+  float scale;         /* > 0 */
+} nvfp4_attention_shape;
+
+/*
+ * nvfp4_attention -- o = softmax(scale * q k^T, over the keys in sight) v, and
+ * lse[head][token] = log sum_j exp(scale * q k_j) (natural logarithm), which
+ * the gradient reads; token counts over all sequences (packed: the token
+ * itself; else batch index * q_len + query).  A query that sees no key has
+ * o = 0 and lse = -inf.  Sequences may be empty in the packed form; tokens
+ * that belong to no sequence are not written.  cu values outside
+ * [0, total] or descending are read as clamped to it, so that no
+ * access leaves the tensors.
+ *   q, o: heads heads; k, v: kv_heads.  data 16-byte aligned, strides
+ *   multiples of 8, |token_stride| < 2^24 and not negative.  lse: device float [heads][total_q].
+ * Products on the bf16 MFMA with binary32 accumulation; the softmax is
+ * binary32, its probabilities are rounded to bf16 for the product with v.
+ * One kernel.
+ */
+int nvfp4_attention(const nvfp4_attention_shape *shape, const nvfp4_heads *q, const nvfp4_heads *k,
+                    const nvfp4_heads *v, const nvfp4_heads *o, float *lse, void *stream);
+
+/*
+ * nvfp4_attention_backward -- with p = exp(scale * q k^T - lse) over the keys
+ * in sight, delta = sum_d do * o, ds = p * (do v^T - delta):
+ *   dq = scale * ds k,  dk = scale * ds^T q,  dv = p^T do
+ * (dk and dv summed over the query heads that share a key head, in a fixed
+ * order).  o and lse are nvfp4_attention's.  dq, dk and dv are written for
+ * every token of a sequence (zero where nothing is in sight).
+ *   workspace  nvfp4_attention_backward_workspace_bytes(shape) bytes of device
+ *              scratch, 16-byte aligned, not initialised.
+ * p and ds are rounded to bf16 for their products.
+ */
+int nvfp4_attention_backward(const nvfp4_attention_shape *shape, const nvfp4_heads *q, const nvfp4_heads *k,
+                             const nvfp4_heads *v, const nvfp4_heads *o, const float *lse, const nvfp4_heads *d_o,
+                             const nvfp4_heads *dq, const nvfp4_heads *dk, const nvfp4_heads *dv, void *workspace,
+                             size_t workspace_bytes, void *stream);
+size_t nvfp4_attention_backward_workspace_bytes(const nvfp4_attention_shape *shape);
+
+/* One tensor of an AdamW step, n contiguous elements. */
+typedef struct {
+  void *param;         /* param_dtype, updated */
+  const void *grad;    /* grad_dtype */
+  void *m;             /* state 32: float [n]; state 8: E4M3 bytes [n] */
+  void *v;             /* state 32: float [n]; state 8: E4M3 bytes [n] of sqrt(v) */
+  uint8_t *m_scale;    /* state 8: E8M0 bytes [ceil(n / 32)]; else NULL */
+  uint8_t *v_scale;    /* state 8: E8M0 bytes [ceil(n / 32)]; else NULL */
+  void *copy;          /* NULL, or bf16 [n]: the new parameter rounded to nearest */
+  float *amax;         /* NULL, or 1 float: becomes max(*amax, max |copy|) (without a copy: of the stored param) */
+  int64_t n;           /* 0 .. 2^34 */
+  int32_t param_dtype; /* NVFP4_F32 or NVFP4_BF16 */
+  int32_t grad_dtype;  /* NVFP4_F32 or NVFP4_BF16 */
+  int32_t state_bits;  /* 32 or 8 */
+  float weight_decay;  /* >= 0 */
+} nvfp4_adamw_tensor;
+
+typedef struct {
+  float lr;            /* >= 0 */
+  double beta1, beta2; /* [0, 1) */
+  float eps;           /* > 0 */
+  int32_t rounding;    /* NVFP4_RTN or NVFP4_SR: of 8-bit states, and of bf16 params */
+  int64_t step;        /* t = 1, 2, ..., below 2^47 */
+  uint64_t seed;       /* Philox key of NVFP4_SR */
+  const float *grad_scale; /* NULL, or device float: multiplies every gradient */
+} nvfp4_adamw_config;
+
+/*
+ * nvfp4_adamw -- one AdamW step (Loshchilov and Hutter, "Decoupled weight
+ * decay regularization") of every tensor, binary32 arithmetic:
+ *   g = grad * grad_scale, m = beta1 m + (1 - beta1) g,
+ *   v = beta2 v + (1 - beta2) g^2,
+ *   param = param (1 - lr weight_decay)
+ *           - lr (m / (1 - beta1^t)) / (sqrt(v) / sqrt(1 - beta2^t) + eps).
+ * 8-bit states hold m and r = sqrt(v) in blocks of 32 consecutive elements:
+ * the block's scale is 2^e (E8M0 byte e + 127), e the least integer >= -126
+ * with max |x| <= 448 * 2^e, its elements x / 2^e in E4M3.  NVFP4_SR rounds |x| / 2^e
+ * up with the probability of its place between its two E4M3 neighbours, by a
+ * 16-bit uniform; a non-zero r is never stored as zero (its square root
+ * divides).  bf16 params under NVFP4_SR add 16 uniform bits below the kept
+ * ones and truncate.  The uniforms of element i of tensor index (its place in
+ * `tensors`) are half i & 1 of word (i mod 8) / 2 of Philox4x32-10(key = seed,
+ * counter = (i / 8, 4 index + which, step mod 2^32, 0x41440000 + step / 2^32)),
+ * which = 0 for m, 1 for r, 2 for the param: a step gives the same result
+ * whenever it is run, and calls over different tensors want different seeds.
+ * m = v = 0 (8-bit: zero bytes, any scales) starts.
+ *   tensors  host array of n_tensors >= 1; at most one amax, copy, param or
+ *            state buffer of one belongs to another.
+ * Arrays that are 16-byte aligned (E4M3 bytes: 8) give wide accesses;
+ * element-aligned ones are accepted and slower.  lr, step and the other
+ * scalars are taken at the call: a captured graph repeats them.
+ * One kernel for every 40 tensors.
+ */
+int nvfp4_adamw(const nvfp4_adamw_tensor *tensors, int64_t n_tensors, const nvfp4_adamw_config *config, void *stream);
 
 #ifdef __cplusplus
 }

@@ -61,6 +61,44 @@ class nvfp4_quant_job(ctypes.Structure):
                 ("outs", ctypes.POINTER(nvfp4_quant_output)), ("n_outs", ctypes.c_int32)]
 
 
+class nvfp4_layernorm_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "residual", "weight", "bias", "y", "sum", "mean", "rstd", "amax")] + [
+        (n, ctypes.c_int64) for n in ("rows", "cols", "ld_x", "ld_residual", "ld_y", "ld_sum")] + [
+        (n, ctypes.c_int32) for n in ("x_dtype", "y_dtype", "w_dtype")] + [("eps", ctypes.c_float)]
+
+
+class nvfp4_layernorm_backward_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dy", "x", "weight", "mean", "rstd", "dsum", "dx", "dweight", "dbias",
+                                               "amax")] + [
+        (n, ctypes.c_int64) for n in ("rows", "cols", "ld_dy", "ld_x", "ld_dsum", "ld_dx")] + [
+        (n, ctypes.c_int32) for n in ("x_dtype", "y_dtype", "w_dtype")]
+
+
+class nvfp4_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class nvfp4_attention_shape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("q_len", ctypes.c_int64), ("k_len", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("window", ctypes.c_int64), ("cu_q", ctypes.c_void_p),
+                ("cu_k", ctypes.c_void_p), ("total_q", ctypes.c_int64), ("total_k", ctypes.c_int64),
+                ("scale", ctypes.c_float)]
+
+
+class nvfp4_adamw_tensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "m", "v", "m_scale", "v_scale", "copy", "amax")] + [
+        ("n", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+        ("state_bits", ctypes.c_int32), ("weight_decay", ctypes.c_float)]
+
+
+class nvfp4_adamw_config(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_float), ("rounding", ctypes.c_int32), ("step", ctypes.c_int64),
+                ("seed", ctypes.c_uint64), ("grad_scale", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -104,6 +142,22 @@ def lib() -> ctypes.CDLL:
     L.mxfp4_dequantize.argtypes = [ctypes.POINTER(mxfp4_tensor), P, i64, P]
     L.mxfp4_gemm.restype = i32
     L.mxfp4_gemm.argtypes = [ctypes.POINTER(mxfp4_tensor), ctypes.POINTER(mxfp4_tensor), P, ctypes.c_int32, i64, P]
+    A = ctypes.POINTER
+    L.nvfp4_layernorm.restype = i32
+    L.nvfp4_layernorm.argtypes = [A(nvfp4_layernorm_args), P]
+    L.nvfp4_layernorm_backward.restype = i32
+    L.nvfp4_layernorm_backward.argtypes = [A(nvfp4_layernorm_backward_args), P, ctypes.c_size_t, P]
+    L.nvfp4_layernorm_backward_workspace_bytes.restype = ctypes.c_size_t
+    L.nvfp4_layernorm_backward_workspace_bytes.argtypes = [i64, i64]
+    H = A(nvfp4_heads)
+    L.nvfp4_attention.restype = i32
+    L.nvfp4_attention.argtypes = [A(nvfp4_attention_shape), H, H, H, H, P, P]
+    L.nvfp4_attention_backward.restype = i32
+    L.nvfp4_attention_backward.argtypes = [A(nvfp4_attention_shape), H, H, H, H, P, H, H, H, H, P, ctypes.c_size_t, P]
+    L.nvfp4_attention_backward_workspace_bytes.restype = ctypes.c_size_t
+    L.nvfp4_attention_backward_workspace_bytes.argtypes = [A(nvfp4_attention_shape)]
+    L.nvfp4_adamw.restype = i32
+    L.nvfp4_adamw.argtypes = [A(nvfp4_adamw_tensor), i64, A(nvfp4_adamw_config), P]
     _lib = L
     return L
 
@@ -446,3 +500,318 @@ def mx_gemm(a: MXTensor, b: MXTensor, out_dtype="f32", stream=None):
     with _on_stream(stream):
         c = torch.empty((a.rows, b.rows), dtype=dt, device=a.codes.device)
     return mxfp4_gemm(a, b, c, stream)
+
+
+# ---------------------------------------------------------------------------
+# training operators: layer norm, attention, AdamW (see include/nvfp4.h)
+# ---------------------------------------------------------------------------
+def _dtype(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float32:
+        return F32
+    raise TypeError("float32 or bfloat16 is wanted, not %s" % t.dtype)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _matrix(t, like, what, dtype=None):
+    """Checks that t is a [rows][cols] device tensor as `like`, its rows contiguous."""
+    if t.shape != like.shape or t.dim() != 2 or t.device != like.device or not t.is_cuda:
+        raise ValueError("%s: a device tensor of shape %s is wanted" % (what, tuple(like.shape)))
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s: contiguous rows are wanted" % what)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s: %s is wanted" % (what, dtype))
+
+
+def _row_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vector(t, n, like, what, dtype=None):
+    if t.dim() != 1 or t.shape[0] != n or t.device != like.device or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s: a contiguous vector of %d elements on %s is wanted" % (what, n, like.device))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s: %s is wanted" % (what, dtype))
+
+
+def nvfp4_layernorm(x, weight, bias, eps, y, mean, rstd, residual=None, sum=None, amax=None, stream=None):
+    """y = layer norm of x (or of x + residual, which goes to sum) over the rows of [rows][cols], with the rows' mean
+    and 1 / standard deviation; *amax is raised to max |y|."""
+    import torch
+    rows, cols = x.shape
+    _matrix(x, x, "x")
+    _matrix(y, x, "y")
+    for t, what in ((residual, "residual"), (sum, "sum")):
+        if t is not None:
+            _matrix(t, x, what, x.dtype)
+    _vector(weight, cols, x, "weight")
+    if bias is not None:
+        _vector(bias, cols, x, "bias", weight.dtype)
+    _vector(mean, rows, x, "mean", torch.float32)
+    _vector(rstd, rows, x, "rstd", torch.float32)
+    if amax is not None:
+        _vector(amax, 1, x, "amax", torch.float32)
+    a = nvfp4_layernorm_args(x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), y.data_ptr(), _ptr(sum),
+                             mean.data_ptr(), rstd.data_ptr(), _ptr(amax), rows, cols, _row_stride(x),
+                             0 if residual is None else _row_stride(residual), _row_stride(y),
+                             0 if sum is None else _row_stride(sum), _dtype(x), _dtype(y), _dtype(weight), eps)
+    _check(lib().nvfp4_layernorm(ctypes.byref(a), _stream(stream)), "nvfp4_layernorm")
+    return y
+
+
+def nvfp4_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, dsum=None, amax=None, workspace=None,
+                             stream=None):
+    """dx, dweight and dbias (each of the two may be None) of a layer norm of x; dsum is added to dx."""
+    import torch
+    rows, cols = x.shape
+    _matrix(x, x, "x")
+    _matrix(dy, x, "dy")
+    _matrix(dx, x, "dx", x.dtype)
+    if dsum is not None:
+        _matrix(dsum, x, "dsum", x.dtype)
+    _vector(weight, cols, x, "weight")
+    _vector(mean, rows, x, "mean", torch.float32)
+    _vector(rstd, rows, x, "rstd", torch.float32)
+    for t, n, what in ((dweight, cols, "dweight"), (dbias, cols, "dbias"), (amax, 1, "amax")):
+        if t is not None:
+            _vector(t, n, x, what, torch.float32)
+    a = nvfp4_layernorm_backward_args(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                                      _ptr(dsum), dx.data_ptr(), _ptr(dweight), _ptr(dbias), _ptr(amax), rows, cols,
+                                      _row_stride(dy), _row_stride(x), 0 if dsum is None else _row_stride(dsum),
+                                      _row_stride(dx), _dtype(x), _dtype(dy), _dtype(weight))
+    _check(lib().nvfp4_layernorm_backward(ctypes.byref(a), _ptr(workspace), _nbytes(workspace), _stream(stream)),
+           "nvfp4_layernorm_backward")
+    return dx
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def layernorm(x, weight, bias=None, eps=1e-5, residual=None, amax=None, out_dtype=None, stream=None):
+    """Allocates and computes (y, mean, rstd, sum): y of x's dtype or `out_dtype`; sum is x + residual, or None."""
+    import torch
+    with _on_stream(stream):
+        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        stats = torch.empty((2, x.shape[0]), dtype=torch.float32, device=x.device)
+        total = None if residual is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    nvfp4_layernorm(x, weight, bias, eps, y, stats[0], stats[1], residual, total, amax, stream)
+    return y, stats[0], stats[1], total
+
+
+def layernorm_backward(dy, x, weight, mean, rstd, dsum=None, amax=None, workspace=None, stream=None):
+    """Allocates and computes (dx, dweight, dbias)."""
+    import torch
+    rows, cols = x.shape
+    with _on_stream(stream):
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        dw = torch.empty((2, cols), dtype=torch.float32, device=x.device)
+        if workspace is None:
+            workspace = torch.empty(lib().nvfp4_layernorm_backward_workspace_bytes(rows, cols), dtype=torch.uint8,
+                                    device=x.device)
+    nvfp4_layernorm_backward(dy, x, weight, mean, rstd, dx, dw[0], dw[1], dsum, amax, workspace, stream)
+    return dx, dw[0], dw[1]
+
+
+def _heads(t) -> nvfp4_heads:
+    """[batch][tokens][heads][dim], or packed [tokens][heads][dim]."""
+    st = t.stride()  # of a dimension of one element: anything, and not used
+    return nvfp4_heads(t.data_ptr(), st[0] if t.dim() == 4 and t.shape[0] > 1 else 0,
+                       st[-3] if t.shape[-3] > 1 else t.shape[-2] * t.shape[-1], st[-2] if t.shape[-2] > 1 else 0)
+
+
+def _attention_shape(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k) -> nvfp4_attention_shape:
+    import torch
+    packed = cu_q is not None
+    if packed != (cu_k is not None) or (packed and (max_q is None or max_k is None)):
+        raise ValueError("packed sequences need cu_q, cu_k, max_q and max_k")
+    for t, what in ((q, "q"), (k, "k"), (v, "v")):
+        if t.dtype != torch.bfloat16:
+            raise TypeError("%s: bfloat16 is wanted, not %s" % (what, t.dtype))
+        if t.dim() != (3 if packed else 4) or not t.is_cuda or t.device != q.device:
+            raise ValueError("%s: a device tensor [%stokens][heads][dim] is wanted" % (what, "" if packed else "batch]["))
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError("%s: a contiguous last dimension is wanted" % what)
+    if k.shape != v.shape or k.shape[-1] != q.shape[-1] or (not packed and k.shape[0] != q.shape[0]):
+        raise ValueError("q, k and v do not fit: %s, %s, %s" % (tuple(q.shape), tuple(k.shape), tuple(v.shape)))
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    if not packed:
+        b, nq, nk = q.shape[0], q.shape[1], k.shape[1]
+        return nvfp4_attention_shape(b, nq, nk, q.shape[2], k.shape[2], q.shape[3], int(causal), window, None, None,
+                                     b * nq, b * nk, scale)
+    for t, what in ((cu_q, "cu_q"), (cu_k, "cu_k")):
+        _vector(t, cu_q.shape[0], q, what, torch.int32)
+    return nvfp4_attention_shape(cu_q.shape[0] - 1, max_q, max_k, q.shape[1], k.shape[1], q.shape[2], int(causal), window,
+                                 cu_q.data_ptr(), cu_k.data_ptr(), q.shape[0], k.shape[0], scale)
+
+
+def _as(t, like, what):
+    import torch
+    if t.shape != like.shape or t.dtype != torch.bfloat16 or t.device != like.device or (
+            t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError("%s: a bfloat16 tensor of shape %s is wanted" % (what, tuple(like.shape)))
+
+
+def _lse(lse, s, like):
+    import torch
+    if lse.shape != (s.heads, s.total_q) or lse.dtype != torch.float32 or lse.device != like.device or (
+            not lse.is_contiguous()):
+        raise ValueError("lse: a contiguous float32 tensor of shape %s is wanted" % ((s.heads, s.total_q),))
+
+
+def nvfp4_attention(q, k, v, o, lse, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None, max_k=None,
+                    stream=None):
+    """o = softmax(scale q k^T) v and lse [heads][all queries] for [batch][tokens][heads][dim] tensors, or packed
+    [tokens][heads][dim] ones with cu_q, cu_k (int32 [batch + 1], device) and the longest lengths max_q, max_k."""
+    s = _attention_shape(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
+    _as(o, q, "o")
+    _lse(lse, s, q)
+    h = [ctypes.byref(_heads(t)) for t in (q, k, v, o)]
+    _check(lib().nvfp4_attention(ctypes.byref(s), *h, lse.data_ptr(), _stream(stream)), "nvfp4_attention")
+    return o
+
+
+def nvfp4_attention_backward(d_o, q, k, v, o, lse, dq, dk, dv, workspace, causal=True, window=0, scale=None, cu_q=None,
+                             cu_k=None, max_q=None, max_k=None, stream=None):
+    """dq, dk and dv of nvfp4_attention with the same arguments."""
+    s = _attention_shape(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
+    for t, like, what in ((d_o, q, "d_o"), (o, q, "o"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+        _as(t, like, what)
+    _lse(lse, s, q)
+    h = [ctypes.byref(_heads(t)) for t in (q, k, v, o)]
+    g = [ctypes.byref(_heads(t)) for t in (d_o, dq, dk, dv)]
+    _check(lib().nvfp4_attention_backward(ctypes.byref(s), *h, lse.data_ptr(), *g, _ptr(workspace), _nbytes(workspace),
+                                          _stream(stream)), "nvfp4_attention_backward")
+    return dq, dk, dv
+
+
+def new_attention_workspace(q, k, v, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None, max_k=None):
+    """A workspace of nvfp4_attention_backward for these arguments (one per stream)."""
+    import torch
+    s = _attention_shape(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
+    return torch.empty(lib().nvfp4_attention_backward_workspace_bytes(ctypes.byref(s)), dtype=torch.uint8,
+                       device=q.device)
+
+
+def attention(q, k, v, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None, max_k=None, stream=None):
+    """Allocates and computes (o, lse)."""
+    import torch
+    tokens = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
+    with _on_stream(stream):
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty((q.shape[-2], tokens), dtype=torch.float32, device=q.device)
+    nvfp4_attention(q, k, v, o, lse, causal, window, scale, cu_q, cu_k, max_q, max_k, stream)
+    return o, lse
+
+
+def attention_backward(d_o, q, k, v, o, lse, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None,
+                       max_k=None, workspace=None, stream=None):
+    """Allocates and computes (dq, dk, dv)."""
+    import torch
+    opts = (causal, window, scale, cu_q, cu_k, max_q, max_k)
+    with _on_stream(stream):
+        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+        if workspace is None:
+            workspace = new_attention_workspace(q, k, v, *opts)
+    return nvfp4_attention_backward(d_o, q, k, v, o, lse, dq, dk, dv, workspace, *opts, stream)
+
+
+@dataclass
+class AdamWTensor:
+    """One tensor of an AdamW step: param and grad float32 or bfloat16; m, v float32 (32-bit states), or uint8 with
+    their block scales (8-bit states: v holds sqrt(v)); copy: bfloat16, or None; amax: float32 [1], or None."""
+    param: "object"
+    grad: "object"
+    m: "object"
+    v: "object"
+    m_scale: "object" = None
+    v_scale: "object" = None
+    weight_decay: float = 0.0
+    copy: "object" = None
+    amax: "object" = None
+
+    def c_struct(self) -> nvfp4_adamw_tensor:
+        import torch
+        n, bits = self.param.numel(), 8 if self.m.dtype == torch.uint8 else 32
+        state = torch.uint8 if bits == 8 else torch.float32
+        wanted = [(self.param, n, None, "param"), (self.grad, n, None, "grad"), (self.m, n, state, "m"),
+                  (self.v, n, state, "v"), (self.copy, n, torch.bfloat16, "copy"), (self.amax, 1, torch.float32, "amax")]
+        if bits == 8:
+            blocks = (n + 31) // 32
+            wanted += [(self.m_scale, blocks, torch.uint8, "m_scale"), (self.v_scale, blocks, torch.uint8, "v_scale")]
+            if self.m_scale is None or self.v_scale is None:
+                raise ValueError("8-bit states need m_scale and v_scale")
+        elif self.m_scale is not None or self.v_scale is not None:
+            raise ValueError("32-bit states have no scales")
+        for t, size, dtype, what in wanted:
+            if t is None:
+                continue
+            if t.numel() != size or not t.is_contiguous() or not t.is_cuda or t.device != self.param.device:
+                raise ValueError("%s: a contiguous device tensor of %d elements is wanted" % (what, size))
+            if dtype is not None and t.dtype != dtype:
+                raise TypeError("%s: %s is wanted, not %s" % (what, dtype, t.dtype))
+        return nvfp4_adamw_tensor(self.param.data_ptr(), self.grad.data_ptr(), self.m.data_ptr(), self.v.data_ptr(),
+                                  _ptr(self.m_scale), _ptr(self.v_scale), _ptr(self.copy), _ptr(self.amax), n,
+                                  _dtype(self.param), _dtype(self.grad), bits, self.weight_decay)
+
+
+def adamw_tensor(param, grad, state_bits=32, weight_decay=0.0, copy=None, amax=None) -> AdamWTensor:
+    """An AdamWTensor with new zero states of 32 or 8 bits."""
+    import torch
+    if state_bits not in (8, 32):
+        raise ValueError("state_bits: 8 or 32 is wanted")
+    n, device = param.numel(), param.device
+    if state_bits == 32:
+        m, v = (torch.zeros(param.shape, dtype=torch.float32, device=device) for _ in range(2))
+        return AdamWTensor(param, grad, m, v, None, None, weight_decay, copy, amax)
+    m, v = (torch.zeros(param.shape, dtype=torch.uint8, device=device) for _ in range(2))
+    ms, vs = (torch.ones((n + 31) // 32, dtype=torch.uint8, device=device) for _ in range(2))
+    return AdamWTensor(param, grad, m, v, ms, vs, weight_decay, copy, amax)
+
+
+class AdamWList:
+    """The tensors of an AdamW step with their descriptors laid out once; the buffers stay the same from step to step
+    (a gradient's may be replaced by set_grad)."""
+
+    def __init__(self, tensors: Sequence[AdamWTensor]):
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise ValueError("no tensors")
+        self.array = (nvfp4_adamw_tensor * len(self.tensors))(*[t.c_struct() for t in self.tensors])
+
+    def set_grad(self, index: int, grad):
+        t = self.tensors[index]
+        old, t.grad = t.grad, grad
+        try:
+            self.array[index] = t.c_struct()
+        except Exception:
+            t.grad = old
+            raise
+
+
+def adamw(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, rounding="rtn", seed=0, grad_scale=None, stream=None):
+    """One AdamW step (number `step`, from 1) of an AdamWList, or of a sequence of AdamWTensor."""
+    import torch
+    if not isinstance(tensors, AdamWList):
+        tensors = AdamWList(tensors)
+    if grad_scale is not None:
+        _vector(grad_scale, 1, tensors.tensors[0].param, "grad_scale", torch.float32)
+    c = nvfp4_adamw_config(lr, beta1, beta2, eps, ROUNDINGS.get(rounding, rounding), step, seed, _ptr(grad_scale))
+    _check(lib().nvfp4_adamw(tensors.array, len(tensors.array), ctypes.byref(c), _stream(stream)), "nvfp4_adamw")
+
+
+def adamw_state_values(t: AdamWTensor):
+    """(m, v) of a tensor as float32, whatever its states are held in."""
+    import torch
+    if t.m_scale is None:
+        return t.m.clone(), t.v.clone()
+    n = t.m.numel()
+    m, r = (torch.repeat_interleave(torch.exp2(s.float() - 127), 32)[:n].view(c.shape) * c.view(torch.float8_e4m3fn).float()
+            for c, s in ((t.m, t.m_scale), (t.v, t.v_scale)))
+    return m, r * r

@@ -1,0 +1,216 @@
+// One AdamW step over many tensors (include/nvfp4.h: nvfp4_adamw).
+//
+// Memory-bound: every element's parameter, gradient and two states are read
+// and written once.  A workgroup takes one chunk of one tensor; the tensors'
+// descriptors travel as kernel arguments, so that a step needs neither a
+// device table nor a copy.  A thread holds 8 consecutive elements at a time;
+// four neighbouring lanes hold a block of 32 of an 8-bit state, so that block
+// maxima need two DPP steps.
+#include "train_device.hpp"
+#include "train_kernels.hpp"
+
+namespace nvfp4 {
+namespace {
+
+// maximum over the 4 lanes that share a block of 32 elements
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, dpp<0xB1>(v));  // quad_perm [1,0,3,2]
+  return fmaxf(v, dpp<0x4E>(v));  // quad_perm [2,3,0,1]
+}
+
+// 2^k as a float, k in [-126, 127]
+__device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
+
+// The block exponent of a maximum: the least e >= -126 with top <= 448 * 2^e.
+// 448 = 1.75 * 2^8, so the exponent field counts up where the mantissa passes
+// 1.75 (0x600000): 0x600001 + 0x1FFFFF carries.
+__device__ __forceinline__ int block_exponent(float top) {
+  const int e = (int)((__float_as_uint(top) + 0x1FFFFFu) >> 23) - 135;
+  return e > -126 ? e : -126;
+}
+
+// |x| / 2^e as an E4M3 code: steps of 2^(max(exponent, -6) - 3), whose count c
+// (at most 16, the next binade) adds to the code of the binade.  SR: a 16-bit
+// uniform.  positive: a non-zero x gives a non-zero code.
+template <bool SR>
+__device__ __forceinline__ uint32_t e4m3_code(float x, int e, uint32_t u16, bool positive) {
+  const float y = fabsf(x) * pow2(-e);
+  int ey = (int)(__float_as_uint(y) >> 23) - 127;
+  ey = ey > -6 ? ey : -6;
+  const float t = y * pow2(3 - ey);
+  float c = SR ? floorf(t + (float)u16 * 1.52587890625e-05f) : rintf(t);
+  if (positive && y > 0.0f) c = fmaxf(c, 1.0f);
+  return (uint32_t)((ey + 6) * 8 + (int)c) | (__float_as_uint(x) >> 31 << 7);
+}
+
+__device__ __forceinline__ float e4m3_signed(uint32_t c) { 
+  const float v = e4m3_value(c & 127u);
+  return c & 128u ? -v : v;
+}
+
+// 8 state elements: their codes and the quad's scale.  Lanes outside the
+// tensor hold zeros.
+template <bool SR>
+__device__ __forceinline__ uint2 encode8(const float x[8], const uint32_t w[4], bool positive, int *e) {
+  float top = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+  *e = block_exponent(quad_max(top));
+  uint32_t q[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) q[j >> 2] |= e4m3_code<SR>(x[j], *e, SR ? u16_of(w, j) : 0u, positive) << (8 * (j & 3));
+  return make_uint2(q[0], q[1]);
+}
+
+__device__ __forceinline__ void decode8(uint2 q, uint32_t scale, float x[8]) {
+  const float s = __builtin_ldexpf(1.0f, (int)scale - 127);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = e4m3_signed(((j < 4 ? q.x : q.y) >> (8 * (j & 3))) & 255u) * s;
+}
+
+// 8 elements, `have` of them in the tensor
+template <typename T>
+__device__ __forceinline__ void get8(const T *p, bool vec, int have, float v[8]) {
+  if (vec && have == 8) {
+    load8(p, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < have ? load1(p + j) : 0.0f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void put8(T *p, bool vec, int have, const float v[8]) {
+  if (vec && have == 8) {
+    store8(p, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < have) store1(p + j, v[j]);
+  }
+}
+__device__ __forceinline__ uint2 get_codes(const uint8_t *p, bool vec, int have) {
+  if (vec && have == 8) return *reinterpret_cast<const uint2 *>(p);
+  uint32_t q[2] = {0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < have) q[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+  return make_uint2(q[0], q[1]);
+}
+__device__ __forceinline__ void put_codes(uint8_t *p, bool vec, int have, uint2 q) {
+  if (vec && have == 8) {
+    *reinterpret_cast<uint2 *>(p) = q;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < have) p[j] = (uint8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3)));
+  }
+}
+
+// the four words that serve a group of 8 elements (which: 0 m, 1 r, 2 param)
+__device__ __forceinline__ void draw(const AdamArgs &a, uint32_t index, uint32_t which, int64_t group, uint32_t w[4]) {
+  w[0] = (uint32_t)group;
+  w[1] = 4u * index + which;
+  w[2] = a.step_lo;
+  w[3] = a.tag;
+  philox4x32_10(a.seed_lo, a.seed_hi, w);
+}
+
+// elements i0 .. i0 + 7 of a tensor; returns the maximum of what is stored
+template <typename TP, typename TG, bool S8, bool SR>
+__device__ __forceinline__ float step8(const AdamArgs &a, const AdamTensor &t, float gs, int64_t i0) {
+  const int64_t left = t.n - i0;
+  const int have = left >= 8 ? 8 : left > 0 ? (int)left : 0;
+  const bool vec = t.flags & AF_VEC;
+  float p[8], g[8], m[8], v[8];
+  uint32_t w[4];
+  get8((const TP *)t.param + i0, vec, have, p);
+  get8((const TG *)t.grad + i0, vec, have, g);
+  if constexpr (S8) {
+    const uint2 qm = get_codes((const uint8_t *)t.m + i0, vec, have), qv = get_codes((const uint8_t *)t.v + i0, vec, have);
+    decode8(qm, have ? t.m_scale[i0 >> 5] : 0u, m);
+    decode8(qv, have ? t.v_scale[i0 >> 5] : 0u, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= v[j];
+  } else {
+    get8((const float *)t.m + i0, vec, have, m);
+    get8((const float *)t.v + i0, vec, have, v);
+  }
+  float r[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = g[j] * gs;
+    m[j] = m[j] * a.beta1 + x * a.one_minus_beta1;
+    v[j] = v[j] * a.beta2 + x * x * a.one_minus_beta2;
+    r[j] = sqrtf(v[j]);
+    p[j] = p[j] * t.keep - a.lr * ((m[j] * a.correct1) / (r[j] * a.correct2 + a.eps));
+  }
+  if constexpr (SR && sizeof(TP) == 2) {
+    draw(a, t.index, 2u, i0 >> 3, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = __uint_as_float((__float_as_uint(p[j]) + u16_of(w, j)) & 0xFFFF0000u);
+  }
+  put8((TP *)t.param + i0, vec, have, p);
+  if (t.copy) put8(t.copy + i0, vec, have, p);
+  if constexpr (S8) {
+    int e;
+    if (SR) draw(a, t.index, 0u, i0 >> 3, w);
+    put_codes((uint8_t *)t.m + i0, vec, have, encode8<SR>(m, w, false, &e));
+    const bool leader = have && (threadIdx.x & 3) == 0;
+    if (leader) t.m_scale[i0 >> 5] = (uint8_t)(e + 127);
+    if (SR) draw(a, t.index, 1u, i0 >> 3, w);
+    put_codes((uint8_t *)t.v + i0, vec, have, encode8<SR>(r, w, true, &e));
+    if (leader) t.v_scale[i0 >> 5] = (uint8_t)(e + 127);
+  } else {
+    put8((float *)t.m + i0, vec, have, m);
+    put8((float *)t.v + i0, vec, have, v);
+  }
+  float top = 0.0f;
+  if (t.amax) {
+    const bool bf16 = t.copy || sizeof(TP) == 2;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(bf16 ? round_bf16(p[j]) : p[j]));
+  }
+  return top;
+}
+
+template <typename TP, typename TG, bool S8, bool SR>
+__device__ __forceinline__ void chunk(const AdamArgs &a, const AdamTensor &t, int64_t first) {
+  const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
+  float top = 0.0f;
+  // whole workgroups take part in every step (block maxima cross lanes)
+  for (int64_t i = first; i < first + kAdamChunk && i < t.n; i += 8 * kAdamThreads)
+    top = fmaxf(top, step8<TP, TG, S8, SR>(a, t, gs, i + 8 * threadIdx.x));
+  if (t.amax) fold_max(t.amax, top);
+}
+
+template <bool SR>
+__global__ __launch_bounds__(kAdamThreads) void adamw_kernel(const AdamArgs a) {
+  int i = 0;
+  for (int step = 32; step; step >>= 1)  // the first tensor that ends behind this workgroup
+    if (i + step <= a.count - 1 && a.t[i + step - 1].end <= blockIdx.x) i += step;
+  const AdamTensor &t = a.t[i];
+  const int64_t first = (int64_t)(blockIdx.x - (i ? a.t[i - 1].end : 0u)) * kAdamChunk;
+  switch (t.flags & 7u) {
+    case 0: chunk<float, float, false, SR>(a, t, first); break;
+    case AF_PARAM_BF16: chunk<uint16_t, float, false, SR>(a, t, first); break;
+    case AF_GRAD_BF16: chunk<float, uint16_t, false, SR>(a, t, first); break;
+    case AF_PARAM_BF16 | AF_GRAD_BF16: chunk<uint16_t, uint16_t, false, SR>(a, t, first); break;
+    case AF_STATE8: chunk<float, float, true, SR>(a, t, first); break;
+    case AF_STATE8 | AF_PARAM_BF16: chunk<uint16_t, float, true, SR>(a, t, first); break;
+    case AF_STATE8 | AF_GRAD_BF16: chunk<float, uint16_t, true, SR>(a, t, first); break;
+    default: chunk<uint16_t, uint16_t, true, SR>(a, t, first); break;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const AdamArgs &a, hipStream_t s) {
+  const unsigned grid = a.t[a.count - 1].end;
+  if (a.sr)
+    adamw_kernel<true><<<grid, kAdamThreads, 0, s>>>(a);
+  else
+    adamw_kernel<false><<<grid, kAdamThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

@@ -197,6 +197,7 @@ const char *nvfp4_status_string(int status) {
     case NVFP4_E_UNSUPPORTED: return "unsupported combination of arguments";
     case NVFP4_E_WORKSPACE: return "workspace missing or too small";
     case NVFP4_E_HIP: return "HIP launch failed";
+    case NVFP4_E_VALUE: return "a scalar argument out of its range";
     default: return "unknown status";
   }
 }

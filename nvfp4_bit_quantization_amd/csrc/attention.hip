@@ -1,0 +1,547 @@
+// Attention over the keys in sight and its gradient (include/nvfp4.h:
+// nvfp4_attention, nvfp4_attention_backward).
+//
+// All products run on the 32x32x16 bf16 MFMA, of which lane l (n = l & 31,
+// h = l >> 5) holds: of A, row n, and of B, column n, the eight inner indices
+// 8 h .. 8 h + 7; of the result, column n and the rows 8 (i / 4) + 4 h + i % 4,
+// i = 0 .. 15.  Every product is laid out so that its result is the next one's
+// B operand without crossing lanes: scores are formed with the index the next
+// product sums over in their rows, and that product's A operand is read from
+// LDS in the same order of that index (4 h .. 4 h + 3, then 8 + 4 h .. 11 + 4 h
+// of each 16) by the transposing LDS read.
+#include "gemm_device.hpp"
+#include "train_device.hpp"
+#include "train_kernels.hpp"
+
+namespace nvfp4 {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+constexpr int kThreads = 256;
+constexpr int kTile = 64;               // rows of a staged tile
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLow = -1e30f;          // below every score; finite, so that differences stay numbers
+
+__device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+  return z;
+}
+// row of result register i in half h
+__device__ __forceinline__ int row_of(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
+
+// the other half's value
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+
+// ------------------------------------------------------------ sequences ----
+struct Seq {
+  int64_t q0, k0;  // first tokens
+  int nq, nk;
+  int64_t bq, bk;  // sequence index for the batch stride (0 when packed)
+};
+__device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) { return v < lo ? lo : v > hi ? hi : v; }
+__device__ __forceinline__ Seq sequence(const AttnArgs &a, int b) {
+  Seq s;
+  if (a.cu_q) {
+    s.q0 = clamp64(a.cu_q[b], 0, a.total_q);
+    s.k0 = clamp64(a.cu_k[b], 0, a.total_k);
+    s.nq = (int)clamp64(clamp64(a.cu_q[b + 1], s.q0, a.total_q) - s.q0, 0, a.q_len);
+    s.nk = (int)clamp64(clamp64(a.cu_k[b + 1], s.k0, a.total_k) - s.k0, 0, a.k_len);
+    s.bq = s.bk = 0;
+  } else {
+    s.q0 = s.k0 = 0;
+    s.nq = a.q_len;
+    s.nk = a.k_len;
+    s.bq = s.bk = b;
+  }
+  return s;
+}
+// token index over all sequences of a sequence's first query
+__device__ __forceinline__ int64_t first_row(const AttnArgs &a, const Seq &s, int b) {
+  return a.cu_q ? s.q0 : (int64_t)b * a.q_len;
+}
+__device__ __forceinline__ uint16_t *at(const Heads &t, int64_t seq, int64_t token, int head) {
+  return t.p + seq * t.sb + token * t.st + (int64_t)head * t.sh;
+}
+
+// keys [lo, hi) that query i sees; off = nk - nq
+__device__ __forceinline__ void sight(const AttnArgs &a, int i, int nk, int off, int &lo, int &hi) {
+  lo = 0;
+  hi = nk;
+  if (a.causal) {
+    const int64_t end = (int64_t)i + off + 1;
+    hi = (int)clamp64(end, 0, nk);
+    if (a.window) lo = (int)clamp64(end - a.window, 0, nk);
+  }
+}
+
+// ---------------------------------------------------------------- tiles ----
+// A tile of 64 rows of D elements in LDS, rows of 2 D bytes, in which chunk c
+// (16 bytes) of row r stands at c ^ spread(r): both reads below then meet every
+// group of banks equally, the plain one (32 rows at one chunk) and the
+// transposing one (4 rows at 4 neighbouring chunks).
+template <int D>
+__device__ __forceinline__ uint32_t spread(uint32_t r) {
+  if constexpr (D == 128)
+    return ((r & 3u) << 2) | ((r >> 2) & 3u);
+  else
+    return (((r >> 1) & 1u) << 2) | ((r >> 2) & 3u);  // two rows to 256 bytes
+}
+
+// Transfer rows row0 .. row0 + 63 of a head (rows past `rows` repeat the last
+// one, chunks past head_dim the first: their products are masked, or meet
+// zeros) into the tile at LDS address lds.  Four waves, D / 32 transfers each.
+template <int D>
+__device__ __forceinline__ void fetch_tile(const uint16_t *head, int64_t stride, int row0, int rows, int chunks,
+                                           uint32_t lds, int wave, int lane) {
+  constexpr int kRowChunks = D / 8, kRows = 64 / kRowChunks;  // rows of one transfer
+  const uint8_t *base = uniform_ptr((const uint8_t *)(head + (int64_t)row0 * stride));
+  const int left = rows - row0 - 1;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const int r = (wave * (D / 32) + i) * kRows + lane / kRowChunks;
+    const uint32_t c = (uint32_t)(lane % kRowChunks) ^ spread<D>(r);
+    const uint32_t voff = (uint32_t)(r < left ? r : left) * (uint32_t)(stride * 2) + ((int)c < chunks ? c : 0u) * 16u;
+    dma16(base, voff, __builtin_amdgcn_readfirstlane(lds + (uint32_t)(wave * (D / 32) + i) * 1024u));
+  }
+}
+
+// A operand from rows r0 .. r0 + 31 as they stand: row n, elements 16 c + 8 h ...
+template <int D>
+__device__ __forceinline__ bf16x8 read_rows(const uint8_t *tile, int r0, int c, int lane) {
+  const uint32_t r = (uint32_t)(r0 + (lane & 31)), p = (uint32_t)(2 * c + (lane >> 5)) ^ spread<D>(r);
+  return *reinterpret_cast<const bf16x8 *>(tile + r * (2 * D) + p * 16);
+}
+// A operand from the transposed tile: row = element 32 dt + n, inner index =
+// tile rows r0 + 4 h .. and r0 + 8 + 4 h ..
+template <int D>
+__device__ __forceinline__ bf16x8 read_cols(const uint8_t *tile, int r0, int dt, int lane) {
+  const int i = lane & 15, g = lane >> 4;
+  const uint32_t r = (uint32_t)(r0 + 4 * (g >> 1) + (i >> 2));
+  const uint32_t c = (uint32_t)(dt * 4 + (g & 1) * 2 + ((i & 3) >> 1)), sub = (uint32_t)(i & 1) * 8;
+  const uint8_t *p0 = tile + r * (2 * D) + ((c ^ spread<D>(r)) * 16) + sub;
+  const uint8_t *p1 = tile + (r + 8) * (2 * D) + ((c ^ spread<D>(r + 8)) * 16) + sub;
+  typedef short i16x8 __attribute__((ext_vector_type(8)));
+  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)p0);
+  const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)p1);
+  const i16x8 v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// B operand of a row held by its lane: elements 16 c + 8 h .. of `row`, zero
+// from head_dim on
+__device__ __forceinline__ bf16x8 load_row(const uint16_t *row, int c, int chunks, int h) {
+  uint4 q = make_uint4(0, 0, 0, 0);
+  if (2 * c + h < chunks) q = *reinterpret_cast<const uint4 *>(row + 16 * c + 8 * h);
+  return __builtin_bit_cast(bf16x8, q);
+}
+
+// eight result registers as a B operand
+__device__ __forceinline__ bf16x8 pack8(const f32x16 &v, int first) {
+  uint4 q;
+  q.x = pack_bf16(v[first], v[first + 1]);
+  q.y = pack_bf16(v[first + 2], v[first + 3]);
+  q.z = pack_bf16(v[first + 4], v[first + 5]);
+  q.w = pack_bf16(v[first + 6], v[first + 7]);
+  return __builtin_bit_cast(bf16x8, q);
+}
+
+// result columns as rows of memory: lane n's column, its elements times f
+template <int D>
+__device__ __forceinline__ void store_cols(uint16_t *row, const f32x16 *acc, float f, int dim, int h) {
+#pragma unroll
+  for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int d = dt * 32 + 8 * g + 4 * h;
+      if (d < dim)
+        *reinterpret_cast<uint2 *>(row + d) = make_uint2(pack_bf16(acc[dt][4 * g] * f, acc[dt][4 * g + 1] * f),
+                                                         pack_bf16(acc[dt][4 * g + 2] * f, acc[dt][4 * g + 3] * f));
+    }
+}
+
+__device__ __forceinline__ void tile_barrier() {
+  NVFP4_WAIT_VMCNT(0);
+  NVFP4_WAIT_LGKM0();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// workgroup -> (sequence, head, tile): neighbours share a key head, heavy
+// tiles of a causal pass first, a contiguous range to each XCD
+struct Work {
+  int b, head, tile;
+};
+__device__ __forceinline__ Work work_of(const AttnArgs &a, int tiles, int group) {
+  uint32_t w = xcd_tile(blockIdx.x, gridDim.x);
+  Work r;
+  const int g = (int)(w % (uint32_t)group);
+  w /= (uint32_t)group;
+  r.tile = (int)(w % (uint32_t)tiles);
+  w /= (uint32_t)tiles;
+  const int hk = (int)(w % (uint32_t)a.kv_heads);
+  r.b = (int)(w / (uint32_t)a.kv_heads);
+  r.head = hk * group + g;
+  return r;
+}
+
+// -------------------------------------------------------------- forward ----
+constexpr int kQueries = 128;  // queries of a workgroup: 32 per wave
+
+// One wave holds 32 queries as columns: scores^T = K Q^T, o^T = V^T p^T.
+// Running maximum and sum per query stay in its two lanes.
+template <int D>
+__global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
+  __shared__ __align__(1024) uint8_t lds[2][2][kTile * D * 2];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+  const int group = a.heads / a.kv_heads, tiles = (a.q_len + kQueries - 1) / kQueries;
+  Work w = work_of(a, tiles, group);
+  if (a.causal) w.tile = tiles - 1 - w.tile;
+  const Seq s = sequence(a, w.b);
+  const int first = w.tile * kQueries;
+  if (first >= s.nq) return;
+  const int last = (first + kQueries < s.nq ? first + kQueries : s.nq) - 1, off = s.nk - s.nq;
+  const int hk = w.head / group, chunks = a.dim / 8;
+  const uint16_t *kh = at(a.k, s.bk, s.k0, hk), *vh = at(a.v, s.bk, s.k0, hk);
+
+  const int mine = first + wave * 32 + (lane & 31), qi = mine < s.nq ? mine : s.nq - 1;
+  bf16x8 q[D / 16];
+  const uint16_t *qrow = at(a.q, s.bq, s.q0 + qi, w.head);
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) q[c] = load_row(qrow, c, chunks, h);
+
+  int lo, hi, unused, begin, end;
+  sight(a, qi, s.nk, off, lo, hi);
+  sight(a, first, s.nk, off, begin, unused);
+  sight(a, last, s.nk, off, unused, end);
+  // what all, and what any, of the wave's queries see
+  const int w0 = first + wave * 32 < s.nq ? first + wave * 32 : s.nq - 1, w1 = w0 + 31 < s.nq ? w0 + 31 : s.nq - 1;
+  int any_lo, all_lo, any_hi, all_hi;
+  sight(a, w0, s.nk, off, any_lo, all_hi);
+  sight(a, w1, s.nk, off, all_lo, any_hi);
+
+  f32x16 o[D / 32];
+#pragma unroll
+  for (int dt = 0; dt < D / 32; ++dt) o[dt] = zero16();
+  float top = kLow, sum = 0.0f;
+  const float c2 = a.scale * kLog2e;
+
+  const int t0 = begin / kTile, t1 = end > begin ? (end + kTile - 1) / kTile : t0;
+  if (t0 < t1) {
+    fetch_tile<D>(kh, a.k.st, t0 * kTile, s.nk, chunks, lds_addr(lds[0][0]), wave, lane);
+    fetch_tile<D>(vh, a.v.st, t0 * kTile, s.nk, chunks, lds_addr(lds[0][1]), wave, lane);
+  }
+  for (int t = t0; t < t1; ++t) {
+    const int stage = (t - t0) & 1, k0 = t * kTile;
+    tile_barrier();  // this tile is in LDS, and every wave has read the previous one
+    if (t + 1 < t1) {
+      fetch_tile<D>(kh, a.k.st, k0 + kTile, s.nk, chunks, lds_addr(lds[stage ^ 1][0]), wave, lane);
+      fetch_tile<D>(vh, a.v.st, k0 + kTile, s.nk, chunks, lds_addr(lds[stage ^ 1][1]), wave, lane);
+    }
+    if (k0 >= any_hi || k0 + kTile <= any_lo) continue;  // nothing in the wave's sight
+    const uint8_t *kt = lds[stage][0], *vt = lds[stage][1];
+    f32x16 p[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      p[u] = zero16();
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) p[u] = mfma(read_rows<D>(kt, u * 32, c, lane), q[c], p[u]);
+    }
+    if (k0 + kTile > all_hi || k0 < all_lo) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int j = k0 + u * 32 + row_of(i, h);
+          if (j >= hi || j < lo) p[u][i] = -INFINITY;
+        }
+    }
+    float m = fmaxf(p[0][0], p[1][0]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) m = fmaxf(m, fmaxf(p[0][i], p[1][i]));
+    m = fmaxf(m, other_half(m)) * c2;
+    // The exponents' reference follows the maximum only when that has risen by
+    // more than 8 (a factor of 256 in p): results do not depend on it
+    if (__any(m > top + 8.0f)) {
+      const float next = fmaxf(top, m), f = __builtin_amdgcn_exp2f(top - next);
+      top = next;
+      sum *= f;
+#pragma unroll
+      for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[dt][i] *= f;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        p[u][i] = __builtin_amdgcn_exp2f(fmaf(p[u][i], c2, -top));
+        sum += p[u][i];
+      }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const bf16x8 b = pack8(p[u], 8 * c);
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt) o[dt] = mfma(read_cols<D>(vt, u * 32 + c * 16, dt, lane), b, o[dt]);
+      }
+  }
+  sum += other_half(sum);
+  if (mine >= s.nq) return;
+  const bool none = sum == 0.0f;
+  store_cols<D>(at(a.o, s.bq, s.q0 + mine, w.head), o, none ? 0.0f : 1.0f / sum, a.dim, h);
+  if (h == 0)
+    a.lse[(int64_t)w.head * a.total_q + first_row(a, s, w.b) + mine] =
+        none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+// ------------------------------------------------------------- gradient ----
+// delta = sum_d do * o, 16 lanes to a row
+__global__ __launch_bounds__(kThreads) void attention_delta_kernel(AttnArgs a) {
+  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);  // (sequence, query) or token
+  const int head = blockIdx.y, c = threadIdx.x & 15;
+  float v = 0.0f;
+  if (row < a.total_q && c * 8 < a.dim) {
+    const int64_t b = a.cu_q ? 0 : row / a.q_len, i = a.cu_q ? row : row % a.q_len;
+    float x[8], y[8];
+    load8(at(a.o, b, i, head) + c * 8, x);
+    load8(at(a.d_o, b, i, head) + c * 8, y);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v = fmaf(x[j], y[j], v);
+  }
+  v += dpp<0x128>(v);
+  v += dpp<0x124>(v);
+  v += dpp<0x122>(v);
+  v += dpp<0x121>(v);
+  if (row < a.total_q && c == 0) a.delta[(int64_t)head * a.total_q + row] = v;
+}
+
+// dQ: a wave holds 32 queries as columns; scores^T = K Q^T, dP^T = V dO^T,
+// dQ^T = K^T dS^T.
+template <int D>
+__global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
+  __shared__ __align__(1024) uint8_t lds[2][2][kTile * D * 2];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+  const int group = a.heads / a.kv_heads, tiles = (a.q_len + kQueries - 1) / kQueries;
+  Work w = work_of(a, tiles, group);
+  if (a.causal) w.tile = tiles - 1 - w.tile;
+  const Seq s = sequence(a, w.b);
+  const int first = w.tile * kQueries;
+  if (first >= s.nq) return;
+  const int last = (first + kQueries < s.nq ? first + kQueries : s.nq) - 1, off = s.nk - s.nq;
+  const int hk = w.head / group, chunks = a.dim / 8;
+  const uint16_t *kh = at(a.k, s.bk, s.k0, hk), *vh = at(a.v, s.bk, s.k0, hk);
+
+  const int mine = first + wave * 32 + (lane & 31), qi = mine < s.nq ? mine : s.nq - 1;
+  bf16x8 q[D / 16], g[D / 16];
+  const uint16_t *qrow = at(a.q, s.bq, s.q0 + qi, w.head), *grow = at(a.d_o, s.bq, s.q0 + qi, w.head);
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    q[c] = load_row(qrow, c, chunks, h);
+    g[c] = load_row(grow, c, chunks, h);
+  }
+  const int64_t stat = (int64_t)w.head * a.total_q + first_row(a, s, w.b) + qi;
+  const float lse2 = a.lse[stat] * kLog2e, delta = a.delta[stat];
+
+  int lo, hi, unused, begin, end;
+  sight(a, qi, s.nk, off, lo, hi);
+  sight(a, first, s.nk, off, begin, unused);
+  sight(a, last, s.nk, off, unused, end);
+  const int w0 = first + wave * 32 < s.nq ? first + wave * 32 : s.nq - 1, w1 = w0 + 31 < s.nq ? w0 + 31 : s.nq - 1;
+  int any_lo, all_lo, any_hi, all_hi;
+  sight(a, w0, s.nk, off, any_lo, all_hi);
+  sight(a, w1, s.nk, off, all_lo, any_hi);
+
+  f32x16 acc[D / 32];
+#pragma unroll
+  for (int dt = 0; dt < D / 32; ++dt) acc[dt] = zero16();
+  const float c2 = a.scale * kLog2e;
+  const int t0 = begin / kTile, t1 = end > begin ? (end + kTile - 1) / kTile : t0;
+  if (t0 < t1) {
+    fetch_tile<D>(kh, a.k.st, t0 * kTile, s.nk, chunks, lds_addr(lds[0][0]), wave, lane);
+    fetch_tile<D>(vh, a.v.st, t0 * kTile, s.nk, chunks, lds_addr(lds[0][1]), wave, lane);
+  }
+  for (int t = t0; t < t1; ++t) {
+    const int stage = (t - t0) & 1, k0 = t * kTile;
+    tile_barrier();
+    if (t + 1 < t1) {
+      fetch_tile<D>(kh, a.k.st, k0 + kTile, s.nk, chunks, lds_addr(lds[stage ^ 1][0]), wave, lane);
+      fetch_tile<D>(vh, a.v.st, k0 + kTile, s.nk, chunks, lds_addr(lds[stage ^ 1][1]), wave, lane);
+    }
+    if (k0 >= any_hi || k0 + kTile <= any_lo) continue;
+    const uint8_t *kt = lds[stage][0], *vt = lds[stage][1];
+    const bool masked = k0 + kTile > all_hi || k0 < all_lo;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      f32x16 p = zero16(), d = zero16();
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) p = mfma(read_rows<D>(kt, u * 32, c, lane), q[c], p);
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) d = mfma(read_rows<D>(vt, u * 32, c, lane), g[c], d);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        float e = __builtin_amdgcn_exp2f(fmaf(p[i], c2, -lse2));
+        if (masked) {
+          const int j = k0 + u * 32 + row_of(i, h);
+          e = j < hi && j >= lo ? e : 0.0f;
+        }
+        p[i] = e * (d[i] - delta);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const bf16x8 b = pack8(p, 8 * c);
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt) acc[dt] = mfma(read_cols<D>(kt, u * 32 + c * 16, dt, lane), b, acc[dt]);
+      }
+    }
+  }
+  if (mine < s.nq) store_cols<D>(at(a.dq, s.bq, s.q0 + mine, w.head), acc, a.scale, a.dim, h);
+}
+
+// dK, dV: a wave holds 32 keys as columns; scores = Q K^T, dP = dO V^T,
+// dV^T = dO^T P, dK^T = Q^T dS, summed over the query heads of the key head.
+constexpr int kKeys = 128;  // keys of a workgroup
+
+template <int D>
+__global__ __launch_bounds__(kThreads, 1) void attention_dkv_kernel(AttnArgs a) {
+  __shared__ __align__(1024) uint8_t lds[2][2][kTile * D * 2];
+  __shared__ __align__(16) float stats[2][2][kTile];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
+  const int group = a.heads / a.kv_heads, tiles = (a.k_len + kKeys - 1) / kKeys;
+  const Work w = work_of(a, tiles, 1);
+  const int hk = w.head;
+  const Seq s = sequence(a, w.b);
+  const int first = w.tile * kKeys;
+  if (first >= s.nk) return;
+  const int last = (first + kKeys < s.nk ? first + kKeys : s.nk) - 1, off = s.nk - s.nq;
+  const int chunks = a.dim / 8;
+
+  const int mine = first + wave * 32 + (lane & 31), ki = mine < s.nk ? mine : s.nk - 1;
+  bf16x8 k[D / 16], v[D / 16];
+  const uint16_t *krow = at(a.k, s.bk, s.k0 + ki, hk), *vrow = at(a.v, s.bk, s.k0 + ki, hk);
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    k[c] = load_row(krow, c, chunks, h);
+    v[c] = load_row(vrow, c, chunks, h);
+  }
+  // the queries that see key j: j - off <= i < j - off + window, with causal
+  int lo = 0, hi = s.nq, begin = 0, end = s.nq, any_lo = 0, any_hi = s.nq, all_lo = 0, all_hi = s.nq;
+  if (a.causal) {
+    const int w0 = first + wave * 32, w1 = w0 + 31;
+    lo = (int)clamp64((int64_t)ki - off, 0, s.nq);
+    begin = (int)clamp64((int64_t)first - off, 0, s.nq);
+    any_lo = (int)clamp64((int64_t)w0 - off, 0, s.nq);
+    all_lo = (int)clamp64((int64_t)w1 - off, 0, s.nq);
+    if (a.window) {
+      hi = (int)clamp64((int64_t)ki - off + a.window, 0, s.nq);
+      end = (int)clamp64((int64_t)last - off + a.window, 0, s.nq);
+      any_hi = (int)clamp64((int64_t)w1 - off + a.window, 0, s.nq);
+      all_hi = (int)clamp64((int64_t)w0 - off + a.window, 0, s.nq);
+    }
+  }
+  f32x16 dk[D / 32], dv[D / 32];
+#pragma unroll
+  for (int dt = 0; dt < D / 32; ++dt) {
+    dk[dt] = zero16();
+    dv[dt] = zero16();
+  }
+  const float c2 = a.scale * kLog2e;
+  const int t0 = begin / kTile, t1 = end > begin ? (end + kTile - 1) / kTile : t0, steps = (t1 - t0) * group;
+  const int64_t row0 = first_row(a, s, w.b);
+  const auto fetch = [&](int step, int stage) {
+    const int head = hk * group + step / (t1 - t0), i0 = (t0 + step % (t1 - t0)) * kTile;
+    fetch_tile<D>(at(a.q, s.bq, s.q0, head), a.q.st, i0, s.nq, chunks, lds_addr(lds[stage][0]), wave, lane);
+    fetch_tile<D>(at(a.d_o, s.bq, s.q0, head), a.d_o.st, i0, s.nq, chunks, lds_addr(lds[stage][1]), wave, lane);
+    if (wave < 2) {
+      const float *src = (wave ? a.delta : a.lse) + (int64_t)head * a.total_q + row0 + i0;
+      const int left = s.nq - i0 - 1;
+      dma4(uniform_ptr((const uint8_t *)src), (uint32_t)(lane < left ? lane : left) * 4u,
+           __builtin_amdgcn_readfirstlane(lds_addr(stats[stage][wave])));
+    }
+  };
+  if (steps > 0) fetch(0, 0);
+  for (int step = 0; step < steps; ++step) {
+    const int stage = step & 1, i0 = (t0 + step % (t1 - t0)) * kTile;
+    tile_barrier();
+    if (step + 1 < steps) fetch(step + 1, stage ^ 1);
+    if (i0 >= any_hi || i0 + kTile <= any_lo) continue;
+    const uint8_t *qt = lds[stage][0], *gt = lds[stage][1];
+    const bool masked = i0 + kTile > all_hi || i0 < all_lo;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      f32x16 p = zero16(), d = zero16();
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) p = mfma(read_rows<D>(qt, u * 32, c, lane), k[c], p);
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) d = mfma(read_rows<D>(gt, u * 32, c, lane), v[c], d);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float4 lse = *reinterpret_cast<const float4 *>(&stats[stage][0][u * 32 + 8 * b + 4 * h]);
+        const float4 del = *reinterpret_cast<const float4 *>(&stats[stage][1][u * 32 + 8 * b + 4 * h]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int i = 4 * b + r;
+          const float l = r == 0 ? lse.x : r == 1 ? lse.y : r == 2 ? lse.z : lse.w;
+          const float e = r == 0 ? del.x : r == 1 ? del.y : r == 2 ? del.z : del.w;
+          float x = __builtin_amdgcn_exp2f(fmaf(p[i], c2, -l * kLog2e));
+          if (masked) {
+            const int qi = i0 + u * 32 + row_of(i, h);
+            x = qi < hi && qi >= lo ? x : 0.0f;
+          }
+          p[i] = x;
+          d[i] = x * (d[i] - e);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const bf16x8 b0 = pack8(p, 8 * c), b1 = pack8(d, 8 * c);
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt) {
+          dv[dt] = mfma(read_cols<D>(gt, u * 32 + c * 16, dt, lane), b0, dv[dt]);
+          dk[dt] = mfma(read_cols<D>(qt, u * 32 + c * 16, dt, lane), b1, dk[dt]);
+        }
+      }
+    }
+  }
+  if (mine >= s.nk) return;
+  store_cols<D>(at(a.dk, s.bk, s.k0 + mine, hk), dk, a.scale, a.dim, h);
+  store_cols<D>(at(a.dv, s.bk, s.k0 + mine, hk), dv, 1.0f, a.dim, h);
+}
+
+}  // namespace
+
+hipError_t launch_attention(const AttnArgs &a, hipStream_t s) {
+  const int64_t grid = (int64_t)a.batch * a.heads * ((a.q_len + kQueries - 1) / kQueries);
+  if (a.dim <= 64)
+    attention_kernel<64><<<(unsigned)grid, kThreads, 0, s>>>(a);
+  else
+    attention_kernel<128><<<(unsigned)grid, kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_attention_backward(const AttnArgs &a, hipStream_t s) {
+  const int64_t q_grid = (int64_t)a.batch * a.heads * ((a.q_len + kQueries - 1) / kQueries);
+  const int64_t k_grid = (int64_t)a.batch * a.kv_heads * ((a.k_len + kKeys - 1) / kKeys);
+  if (a.total_q > 0)
+    attention_delta_kernel<<<dim3((unsigned)((a.total_q + 15) / 16), (unsigned)a.heads), kThreads, 0, s>>>(a);
+  if (a.dim <= 64) {
+    attention_dkv_kernel<64><<<(unsigned)k_grid, kThreads, 0, s>>>(a);
+    attention_dq_kernel<64><<<(unsigned)q_grid, kThreads, 0, s>>>(a);
+  } else {
+    attention_dkv_kernel<128><<<(unsigned)k_grid, kThreads, 0, s>>>(a);
+    attention_dq_kernel<128><<<(unsigned)q_grid, kThreads, 0, s>>>(a);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,278 @@
+// C ABI of the training operators: argument validation on the host, then
+// kernel launches on the caller's stream.  The entry points and their
+// contracts are declared and documented in include/nvfp4.h.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <stdlib.h>
+
+#include "nvfp4.h"
+#include "train_kernels.hpp"
+
+using namespace nvfp4;
+
+namespace {
+
+bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+bool dtype_ok(int32_t t) { return t == NVFP4_F32 || t == NVFP4_BF16; }
+size_t size_of(int32_t t) { return t == NVFP4_BF16 ? 2 : 4; }
+
+// the launches' status; with NVFP4_SYNC_CHECK=1 (read once) also the kernels'
+int finish(hipError_t e, hipStream_t s) {
+  if (e != hipSuccess) return NVFP4_E_HIP;
+  static const bool check = [] {
+    const char *v = getenv("NVFP4_SYNC_CHECK");
+    return v && v[0] == '1';
+  }();
+  if (check && (hipStreamSynchronize(s) != hipSuccess || hipGetLastError() != hipSuccess)) return NVFP4_E_HIP;
+  return NVFP4_OK;
+}
+
+int norm_shape(int64_t rows, int64_t cols) {
+  return rows <= 0 || rows >= ((int64_t)1 << 31) || cols <= 0 || cols > kNormMaxCols ? NVFP4_E_SHAPE : NVFP4_OK;
+}
+
+// one bf16 tensor of an attention call; outputs must not overlap themselves
+int check_heads(const nvfp4_heads *t, const nvfp4_attention_shape *s, int32_t heads, bool output) {
+  if (!t || !t->data) return NVFP4_E_NULL;
+  const bool batched = !s->cu_q && s->batch > 1;
+  if (t->token_stride < 0 || t->token_stride >= ((int64_t)1 << 24) || t->head_stride < 0 ||
+      (batched && t->batch_stride < 0))
+    return NVFP4_E_LD;
+  if (output && (t->token_stride < s->head_dim || (heads > 1 && t->head_stride < s->head_dim) ||
+                 (batched && t->batch_stride < s->head_dim)))
+    return NVFP4_E_LD;
+  if (!aligned(t->data, 16) || t->token_stride % 8 || t->head_stride % 8 || (batched && t->batch_stride % 8))
+    return NVFP4_E_ALIGN;
+  return NVFP4_OK;
+}
+
+int check_shape(const nvfp4_attention_shape *s) {
+  if (!s) return NVFP4_E_NULL;
+  const int64_t most = (int64_t)1 << 30;
+  if (s->batch < 1 || s->batch > most || s->q_len < 1 || s->q_len > most || s->k_len < 1 || s->k_len > most ||
+      s->heads < 1 || s->heads > 65535 || s->kv_heads < 1 || s->heads % s->kv_heads)
+    return NVFP4_E_SHAPE;
+  if (s->head_dim < 8 || s->head_dim > 128 || s->head_dim % 8) return NVFP4_E_UNSUPPORTED;
+  if (s->causal != 0 && s->causal != 1) return NVFP4_E_UNSUPPORTED;
+  if (s->window < 0 || (s->window > 0 && !s->causal)) return NVFP4_E_UNSUPPORTED;
+  if (!s->cu_q != !s->cu_k) return NVFP4_E_NULL;
+  if (s->cu_q) {
+    if (s->total_q < 0 || s->total_k < 0 || s->total_q >= ((int64_t)1 << 31) || s->total_k >= ((int64_t)1 << 31))
+      return NVFP4_E_SHAPE;
+    if (!aligned(s->cu_q, 4) || !aligned(s->cu_k, 4)) return NVFP4_E_ALIGN;
+  } else if (s->total_q != s->batch * s->q_len || s->total_k != s->batch * s->k_len) {
+    return NVFP4_E_SHAPE;
+  }
+  if (!(s->scale > 0.0f) || !isfinite(s->scale)) return NVFP4_E_VALUE;
+  // workgroups and rows are counted in 32 bits: at least 64 queries or keys to a workgroup, 16 rows to one of the rows'
+  const int64_t limit = (int64_t)1 << 31;
+  const int64_t tiles = (s->q_len > s->k_len ? s->q_len : s->k_len) / 64 + 1;
+  if (s->batch > limit / tiles / s->heads || s->total_q / 16 >= limit - 1) return NVFP4_E_SHAPE;
+  return NVFP4_OK;
+}
+
+Heads heads_of(const nvfp4_heads *t) {
+  return Heads{(uint16_t *)t->data, t->batch_stride, t->token_stride, t->head_stride};
+}
+
+AttnArgs attn_args(const nvfp4_attention_shape *s) {
+  AttnArgs a = {};
+  a.cu_q = s->cu_q;
+  a.cu_k = s->cu_k;
+  a.total_q = s->total_q;
+  a.total_k = s->total_k;
+  a.window = s->window;
+  a.q_len = (int)s->q_len;
+  a.k_len = (int)s->k_len;
+  a.batch = (int)s->batch;
+  a.heads = s->heads;
+  a.kv_heads = s->kv_heads;
+  a.dim = s->head_dim;
+  a.causal = s->causal;
+  a.scale = s->scale;
+  return a;
+}
+
+int check_adamw(const nvfp4_adamw_tensor &t) {
+  if (t.n < 0 || t.n > ((int64_t)1 << 34)) return NVFP4_E_SHAPE;
+  if (!dtype_ok(t.param_dtype) || !dtype_ok(t.grad_dtype) || (t.state_bits != 32 && t.state_bits != 8))
+    return NVFP4_E_UNSUPPORTED;
+  if (!(t.weight_decay >= 0.0f) || !isfinite(t.weight_decay)) return NVFP4_E_VALUE;
+  if (t.n == 0) return NVFP4_OK;
+  if (!t.param || !t.grad || !t.m || !t.v) return NVFP4_E_NULL;
+  if (t.state_bits == 8 && (!t.m_scale || !t.v_scale)) return NVFP4_E_NULL;
+  if (!aligned(t.param, size_of(t.param_dtype)) || !aligned(t.grad, size_of(t.grad_dtype)) ||
+      (t.copy && !aligned(t.copy, 2)) || (t.amax && !aligned(t.amax, 4)))
+    return NVFP4_E_ALIGN;
+  if (t.state_bits == 32 && (!aligned(t.m, 4) || !aligned(t.v, 4))) return NVFP4_E_ALIGN;
+  return NVFP4_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int nvfp4_layernorm(const nvfp4_layernorm_args *a, void *stream) {
+  if (!a || !a->x || !a->weight || !a->y || !a->mean || !a->rstd) return NVFP4_E_NULL;
+  if (a->residual && !a->sum) return NVFP4_E_NULL;
+  if (const int st = norm_shape(a->rows, a->cols)) return st;
+  if (!dtype_ok(a->x_dtype) || !dtype_ok(a->y_dtype) || !dtype_ok(a->w_dtype)) return NVFP4_E_UNSUPPORTED;
+  if (a->sum && !a->residual) return NVFP4_E_UNSUPPORTED;
+  if (a->ld_x < a->cols || a->ld_y < a->cols || (a->residual && (a->ld_residual < a->cols || a->ld_sum < a->cols)))
+    return NVFP4_E_LD;
+  const size_t xs = size_of(a->x_dtype), ws = size_of(a->w_dtype);
+  if (!aligned(a->x, xs) || !aligned(a->y, size_of(a->y_dtype)) || !aligned(a->weight, ws) ||
+      (a->bias && !aligned(a->bias, ws)) || (a->residual && (!aligned(a->residual, xs) || !aligned(a->sum, xs))) ||
+      !aligned(a->mean, 4) || !aligned(a->rstd, 4) || (a->amax && !aligned(a->amax, 4)))
+    return NVFP4_E_ALIGN;
+  if (!(a->eps >= 0.0f) || !isfinite(a->eps)) return NVFP4_E_VALUE;
+  hipStream_t s = (hipStream_t)stream;
+  return finish(launch_layernorm(*a, s), s);
+}
+
+size_t nvfp4_layernorm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  if (norm_shape(rows, cols) != NVFP4_OK) return 0;
+  return (size_t)layernorm_backward_parts(rows, cols) * 2 * (size_t)cols * sizeof(float);
+}
+
+int nvfp4_layernorm_backward(const nvfp4_layernorm_backward_args *a, void *workspace, size_t workspace_bytes,
+                             void *stream) {
+  if (!a || !a->dy || !a->x || !a->weight || !a->mean || !a->rstd || !a->dx) return NVFP4_E_NULL;
+  if (const int st = norm_shape(a->rows, a->cols)) return st;
+  if (!dtype_ok(a->x_dtype) || !dtype_ok(a->y_dtype) || !dtype_ok(a->w_dtype)) return NVFP4_E_UNSUPPORTED;
+  if (a->ld_x < a->cols || a->ld_dy < a->cols || a->ld_dx < a->cols || (a->dsum && a->ld_dsum < a->cols))
+    return NVFP4_E_LD;
+  const size_t xs = size_of(a->x_dtype);
+  if (!aligned(a->x, xs) || !aligned(a->dx, xs) || (a->dsum && !aligned(a->dsum, xs)) ||
+      !aligned(a->dy, size_of(a->y_dtype)) || !aligned(a->weight, size_of(a->w_dtype)) || !aligned(a->mean, 4) ||
+      !aligned(a->rstd, 4) || (a->dweight && !aligned(a->dweight, 4)) || (a->dbias && !aligned(a->dbias, 4)) ||
+      (a->amax && !aligned(a->amax, 4)))
+    return NVFP4_E_ALIGN;
+  const bool sums = a->dweight || a->dbias;
+  if (sums) {
+    if (!workspace || workspace_bytes < nvfp4_layernorm_backward_workspace_bytes(a->rows, a->cols))
+      return NVFP4_E_WORKSPACE;
+    if (!aligned(workspace, 16)) return NVFP4_E_ALIGN;
+  }
+  hipStream_t s = (hipStream_t)stream;
+  return finish(launch_layernorm_backward(*a, sums ? (float *)workspace : nullptr, s), s);
+}
+
+int nvfp4_attention(const nvfp4_attention_shape *shape, const nvfp4_heads *q, const nvfp4_heads *k,
+                    const nvfp4_heads *v, const nvfp4_heads *o, float *lse, void *stream) {
+  if (const int st = check_shape(shape)) return st;
+  if (!lse) return NVFP4_E_NULL;
+  if (!aligned(lse, 4)) return NVFP4_E_ALIGN;
+  int st = check_heads(q, shape, shape->heads, false);
+  if (!st) st = check_heads(k, shape, shape->kv_heads, false);
+  if (!st) st = check_heads(v, shape, shape->kv_heads, false);
+  if (!st) st = check_heads(o, shape, shape->heads, true);
+  if (st) return st;
+  AttnArgs a = attn_args(shape);
+  a.q = heads_of(q);
+  a.k = heads_of(k);
+  a.v = heads_of(v);
+  a.o = heads_of(o);
+  a.lse = lse;
+  hipStream_t s = (hipStream_t)stream;
+  return finish(launch_attention(a, s), s);
+}
+
+size_t nvfp4_attention_backward_workspace_bytes(const nvfp4_attention_shape *shape) {
+  if (check_shape(shape) != NVFP4_OK) return 0;
+  return (((size_t)shape->heads * (size_t)shape->total_q * sizeof(float) + 255) & ~(size_t)255) + 256;
+}
+
+int nvfp4_attention_backward(const nvfp4_attention_shape *shape, const nvfp4_heads *q, const nvfp4_heads *k,
+                             const nvfp4_heads *v, const nvfp4_heads *o, const float *lse, const nvfp4_heads *d_o,
+                             const nvfp4_heads *dq, const nvfp4_heads *dk, const nvfp4_heads *dv, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+  if (const int st = check_shape(shape)) return st;
+  if (!lse) return NVFP4_E_NULL;
+  if (!aligned(lse, 4)) return NVFP4_E_ALIGN;
+  const nvfp4_heads *by_q[4] = {q, o, d_o, dq}, *by_k[4] = {k, v, dk, dv};
+  for (int i = 0; i < 4; ++i) {
+    if (const int st = check_heads(by_q[i], shape, shape->heads, i == 3)) return st;
+    if (const int st = check_heads(by_k[i], shape, shape->kv_heads, i >= 2)) return st;
+  }
+  if (!workspace || workspace_bytes < nvfp4_attention_backward_workspace_bytes(shape)) return NVFP4_E_WORKSPACE;
+  if (!aligned(workspace, 16)) return NVFP4_E_ALIGN;
+  AttnArgs a = attn_args(shape);
+  a.q = heads_of(q);
+  a.k = heads_of(k);
+  a.v = heads_of(v);
+  a.o = heads_of(o);
+  a.d_o = heads_of(d_o);
+  a.dq = heads_of(dq);
+  a.dk = heads_of(dk);
+  a.dv = heads_of(dv);
+  a.lse = const_cast<float *>(lse);
+  a.delta = (float *)workspace;
+  hipStream_t s = (hipStream_t)stream;
+  return finish(launch_attention_backward(a, s), s);
+}
+
+int nvfp4_adamw(const nvfp4_adamw_tensor *tensors, int64_t n_tensors, const nvfp4_adamw_config *c, void *stream) {
+  if (!tensors || !c) return NVFP4_E_NULL;
+  if (n_tensors < 1 || n_tensors >= ((int64_t)1 << 30)) return NVFP4_E_SHAPE;
+  if (c->rounding != NVFP4_RTN && c->rounding != NVFP4_SR) return NVFP4_E_UNSUPPORTED;
+  if (!(c->lr >= 0.0f) || !isfinite(c->lr) || !(c->beta1 >= 0.0 && c->beta1 < 1.0) ||
+      !(c->beta2 >= 0.0 && c->beta2 < 1.0) || !(c->eps > 0.0f) || !isfinite(c->eps) || c->step < 1 ||
+      c->step >= ((int64_t)1 << 47))
+    return NVFP4_E_VALUE;
+  if (c->grad_scale && !aligned(c->grad_scale, 4)) return NVFP4_E_ALIGN;
+  for (int64_t i = 0; i < n_tensors; ++i)
+    if (const int st = check_adamw(tensors[i])) return st;
+
+  AdamArgs a = {};
+  a.sr = c->rounding == NVFP4_SR;
+  a.lr = c->lr;
+  a.beta1 = (float)c->beta1;
+  a.one_minus_beta1 = (float)(1.0 - c->beta1);
+  a.beta2 = (float)c->beta2;
+  a.one_minus_beta2 = (float)(1.0 - c->beta2);
+  a.eps = c->eps;
+  a.correct1 = (float)(1.0 / (1.0 - pow(c->beta1, (double)c->step)));
+  a.correct2 = (float)(1.0 / sqrt(1.0 - pow(c->beta2, (double)c->step)));
+  a.seed_lo = (uint32_t)c->seed;
+  a.seed_hi = (uint32_t)(c->seed >> 32);
+  a.step_lo = (uint32_t)c->step;
+  a.tag = 0x41440000u + (uint32_t)(c->step >> 32);
+  a.grad_scale = c->grad_scale;
+  hipStream_t s = (hipStream_t)stream;
+  uint32_t end = 0;
+  for (int64_t i = 0; i <= n_tensors; ++i) {
+    const bool more = i < n_tensors;
+    // at most 2^22 workgroups a tensor: the running count stays in 32 bits
+    if (a.count && (!more || a.count == kAdamTensors || end > (1u << 30))) {
+      if (launch_adamw(a, s) != hipSuccess) return NVFP4_E_HIP;
+      a.count = 0;
+      end = 0;
+    }
+    if (!more || tensors[i].n == 0) continue;
+    const nvfp4_adamw_tensor &t = tensors[i];
+    AdamTensor &d = a.t[a.count++];
+    d.param = t.param;
+    d.grad = t.grad;
+    d.m = t.m;
+    d.v = t.v;
+    d.m_scale = t.m_scale;
+    d.v_scale = t.v_scale;
+    d.copy = (uint16_t *)t.copy;
+    d.amax = t.amax;
+    d.n = t.n;
+    d.keep = (float)(1.0 - (double)c->lr * t.weight_decay);
+    d.index = (uint32_t)i;
+    d.flags = (t.param_dtype == NVFP4_BF16 ? AF_PARAM_BF16 : 0u) | (t.grad_dtype == NVFP4_BF16 ? AF_GRAD_BF16 : 0u) |
+              (t.state_bits == 8 ? AF_STATE8 : 0u);
+    const size_t sa = t.state_bits == 8 ? 8 : 16;
+    if (aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.m, sa) && aligned(t.v, sa) && aligned(t.copy, 16))
+      d.flags |= AF_VEC;
+    end += (uint32_t)((t.n + kAdamChunk - 1) / kAdamChunk);
+    d.end = end;
+  }
+  return finish(hipSuccess, s);
+}
+
+}  // extern "C"

@@ -1,0 +1,86 @@
+// Device helpers of the training operators (gfx950): groups of 8 elements in
+// binary32, and reductions over a wave.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "nvfp4_device.hpp"
+
+namespace nvfp4 {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// two values as bf16, nearest-even, the first in the low half
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const f32x2 v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+__device__ __forceinline__ float round_bf16(float a) { return __uint_as_float(pack_bf16(0.0f, a) & 0xFFFF0000u); }
+
+// 8 consecutive elements, 16-byte aligned
+__device__ __forceinline__ void load8(const uint16_t *p, float v[8]) {
+  const uint4 q = *reinterpret_cast<const uint4 *>(p);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = bf16_at(q, j);
+}
+__device__ __forceinline__ void load8(const float *p, float v[8]) {
+  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ uint4 packed8(const float v[8]) {
+  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(uint16_t *p, const float v[8]) { *reinterpret_cast<uint4 *>(p) = packed8(v); }
+__device__ __forceinline__ void store8(float *p, const float v[8]) {
+  reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ float load1(const uint16_t *p) { return bf16_lo(*p); }
+__device__ __forceinline__ float load1(const float *p) { return *p; }
+__device__ __forceinline__ void store1(uint16_t *p, float v) { *p = (uint16_t)pack_bf16(v, 0.0f); }
+__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
+
+// v as an element of the type keeps it
+template <typename T>
+__device__ __forceinline__ float rounded(float v);
+template <>
+__device__ __forceinline__ float rounded<uint16_t>(float v) { return round_bf16(v); }
+template <>
+__device__ __forceinline__ float rounded<float>(float v) { return v; }
+
+// Sum and maximum over the 64 lanes, in every lane: four DPP steps inside the
+// rows of 16 lanes, then the rows by two lane permutes.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<0x128>(v);  // row_ror:8
+  v += dpp<0x124>(v);
+  v += dpp<0x122>(v);
+  v += dpp<0x121>(v);
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
+  return v;
+}
+__device__ __forceinline__ float wave_max(float v) {
+  v = fmaxf(v, dpp<0x128>(v));
+  v = fmaxf(v, dpp<0x124>(v));
+  v = fmaxf(v, dpp<0x122>(v));
+  v = fmaxf(v, dpp<0x121>(v));
+  v = fmaxf(v, __shfl_xor(v, 16));
+  v = fmaxf(v, __shfl_xor(v, 32));
+  return v;
+}
+
+// fold a wave's maximum of non-negative floats into *out: bit patterns of
+// non-negative floats order as their values do, and a maximum does not depend
+// on the order of the atomics
+__device__ __forceinline__ void fold_max(float *out, float v) {
+  v = wave_max(v);
+  if ((threadIdx.x & 63) == 0 && v > 0.0f) atomicMax(reinterpret_cast<unsigned int *>(out), __float_as_uint(v));
+}
+
+}  // namespace nvfp4

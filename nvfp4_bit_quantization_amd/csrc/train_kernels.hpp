@@ -1,0 +1,76 @@
+// Kernel argument blocks and launch helpers of the training operators (layer
+// norm, AdamW, attention), shared by train_api.cpp and their translation units.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "nvfp4.h"
+
+namespace nvfp4 {
+
+// ---------------------------------------------------------------- norm ----
+constexpr int64_t kNormMaxCols = 32768;
+
+hipError_t launch_layernorm(const nvfp4_layernorm_args &a, hipStream_t s);
+// workgroups of the gradient kernel = rows of its partial sums [parts][2][cols]
+int64_t layernorm_backward_parts(int64_t rows, int64_t cols);
+hipError_t launch_layernorm_backward(const nvfp4_layernorm_backward_args &a, float *partials, hipStream_t s);
+
+// --------------------------------------------------------------- adamw ----
+constexpr int kAdamTensors = 40;       // tensors of one launch: their descriptors travel as kernel arguments
+constexpr int kAdamThreads = 256;
+constexpr int kAdamChunk = 4096;       // elements of one workgroup (a multiple of 8 * kAdamThreads)
+
+// flags of AdamTensor
+enum AdamFlags : uint32_t { AF_PARAM_BF16 = 1, AF_GRAD_BF16 = 2, AF_STATE8 = 4, AF_VEC = 8 };
+
+struct AdamTensor {
+  void *param;
+  const void *grad;
+  void *m, *v;
+  uint8_t *m_scale, *v_scale;
+  uint16_t *copy;
+  float *amax;
+  int64_t n;
+  float keep;      // 1 - lr * weight_decay
+  uint32_t flags;
+  uint32_t index;  // place in the caller's list
+  uint32_t end;    // workgroups of this and the earlier tensors of the launch
+};
+
+struct AdamArgs {
+  AdamTensor t[kAdamTensors];
+  int count;
+  int sr;
+  float lr, beta1, one_minus_beta1, beta2, one_minus_beta2, eps;
+  float correct1, correct2;  // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
+  uint32_t seed_lo, seed_hi, step_lo, tag;
+  const float *grad_scale;
+};
+
+hipError_t launch_adamw(const AdamArgs &a, hipStream_t s);
+
+// ----------------------------------------------------------- attention ----
+struct Heads {
+  uint16_t *p;
+  int64_t sb, st, sh;  // elements between sequences, tokens, heads
+};
+
+struct AttnArgs {
+  Heads q, k, v, o, d_o, dq, dk, dv;
+  float *lse;    // [heads][total_q]
+  float *delta;  // gradient: [heads][total_q]
+  const int32_t *cu_q, *cu_k;
+  int64_t total_q, total_k;
+  int64_t window;  // 0: none
+  int q_len, k_len;
+  int batch, heads, kv_heads, dim;
+  int causal;
+  float scale;
+};
+
+hipError_t launch_attention(const AttnArgs &a, hipStream_t s);
+hipError_t launch_attention_backward(const AttnArgs &a, hipStream_t s);
+
+}  // namespace nvfp4
