@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import List, Optional, Sequence
 
@@ -144,18 +145,17 @@ def lib() -> ctypes.CDLL:
     L.mxfp4_gemm.argtypes = [ctypes.POINTER(mxfp4_tensor), ctypes.POINTER(mxfp4_tensor), P, ctypes.c_int32, i64, P]
     A = ctypes.POINTER
     L.nvfp4_layernorm.restype = i32
-    L.nvfp4_layernorm.argtypes = [A(nvfp4_layernorm_args), P]
+    L.nvfp4_layernorm.argtypes = [P, P]  # the structures by address, or packed
     L.nvfp4_layernorm_backward.restype = i32
-    L.nvfp4_layernorm_backward.argtypes = [A(nvfp4_layernorm_backward_args), P, ctypes.c_size_t, P]
+    L.nvfp4_layernorm_backward.argtypes = [P, P, ctypes.c_size_t, P]
     L.nvfp4_layernorm_backward_workspace_bytes.restype = ctypes.c_size_t
     L.nvfp4_layernorm_backward_workspace_bytes.argtypes = [i64, i64]
-    H = A(nvfp4_heads)
     L.nvfp4_attention.restype = i32
-    L.nvfp4_attention.argtypes = [A(nvfp4_attention_shape), H, H, H, H, P, P]
+    L.nvfp4_attention.argtypes = [P, P, P, P, P, P, P]
     L.nvfp4_attention_backward.restype = i32
-    L.nvfp4_attention_backward.argtypes = [A(nvfp4_attention_shape), H, H, H, H, P, H, H, H, H, P, ctypes.c_size_t, P]
+    L.nvfp4_attention_backward.argtypes = [P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
     L.nvfp4_attention_backward_workspace_bytes.restype = ctypes.c_size_t
-    L.nvfp4_attention_backward_workspace_bytes.argtypes = [A(nvfp4_attention_shape)]
+    L.nvfp4_attention_backward_workspace_bytes.argtypes = [P]
     L.nvfp4_adamw.restype = i32
     L.nvfp4_adamw.argtypes = [A(nvfp4_adamw_tensor), i64, A(nvfp4_adamw_config), P]
     _lib = L
@@ -504,222 +504,301 @@ def mx_gemm(a: MXTensor, b: MXTensor, out_dtype="f32", stream=None):
 
 # ---------------------------------------------------------------------------
 # training operators: layer norm, attention, AdamW (see include/nvfp4.h)
+#
+# Their smallest calls take less time on the GPU than Python needs to describe
+# them, so arguments are packed straight into the C structures' layout, outputs
+# that were allocated here are not looked over again, and the stream's handle
+# is taken without a stream object.
 # ---------------------------------------------------------------------------
+_NORM = struct.Struct("@9P6q3if")
+_NORM_GRAD = struct.Struct("@10P6q3i4x")
+_SHAPE = struct.Struct("@3q4iq2P2qf4x")
+_HEADS = struct.Struct("@P3q")
+
+
 def _dtype(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
+    name = str(t.dtype)
+    if name == "torch.bfloat16":
         return BF16
-    if t.dtype == torch.float32:
+    if name == "torch.float32":
         return F32
-    raise TypeError("float32 or bfloat16 is wanted, not %s" % t.dtype)
+    raise TypeError("float32 or bfloat16 is wanted, not %s" % name)
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _matrix(t, like, what, dtype=None):
-    """Checks that t is a [rows][cols] device tensor as `like`, its rows contiguous."""
-    if t.shape != like.shape or t.dim() != 2 or t.device != like.device or not t.is_cuda:
-        raise ValueError("%s: a device tensor of shape %s is wanted" % (what, tuple(like.shape)))
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError("%s: contiguous rows are wanted" % what)
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError("%s: %s is wanted" % (what, dtype))
-
-
-def _row_stride(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _vector(t, n, like, what, dtype=None):
-    if t.dim() != 1 or t.shape[0] != n or t.device != like.device or (n > 1 and t.stride(0) != 1):
-        raise ValueError("%s: a contiguous vector of %d elements on %s is wanted" % (what, n, like.device))
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError("%s: %s is wanted" % (what, dtype))
-
-
-def nvfp4_layernorm(x, weight, bias, eps, y, mean, rstd, residual=None, sum=None, amax=None, stream=None):
-    """y = layer norm of x (or of x + residual, which goes to sum) over the rows of [rows][cols], with the rows' mean
-    and 1 / standard deviation; *amax is raised to max |y|."""
-    import torch
-    rows, cols = x.shape
-    _matrix(x, x, "x")
-    _matrix(y, x, "y")
-    for t, what in ((residual, "residual"), (sum, "sum")):
-        if t is not None:
-            _matrix(t, x, what, x.dtype)
-    _vector(weight, cols, x, "weight")
-    if bias is not None:
-        _vector(bias, cols, x, "bias", weight.dtype)
-    _vector(mean, rows, x, "mean", torch.float32)
-    _vector(rstd, rows, x, "rstd", torch.float32)
-    if amax is not None:
-        _vector(amax, 1, x, "amax", torch.float32)
-    a = nvfp4_layernorm_args(x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), y.data_ptr(), _ptr(sum),
-                             mean.data_ptr(), rstd.data_ptr(), _ptr(amax), rows, cols, _row_stride(x),
-                             0 if residual is None else _row_stride(residual), _row_stride(y),
-                             0 if sum is None else _row_stride(sum), _dtype(x), _dtype(y), _dtype(weight), eps)
-    _check(lib().nvfp4_layernorm(ctypes.byref(a), _stream(stream)), "nvfp4_layernorm")
-    return y
-
-
-def nvfp4_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, dsum=None, amax=None, workspace=None,
-                             stream=None):
-    """dx, dweight and dbias (each of the two may be None) of a layer norm of x; dsum is added to dx."""
-    import torch
-    rows, cols = x.shape
-    _matrix(x, x, "x")
-    _matrix(dy, x, "dy")
-    _matrix(dx, x, "dx", x.dtype)
-    if dsum is not None:
-        _matrix(dsum, x, "dsum", x.dtype)
-    _vector(weight, cols, x, "weight")
-    _vector(mean, rows, x, "mean", torch.float32)
-    _vector(rstd, rows, x, "rstd", torch.float32)
-    for t, n, what in ((dweight, cols, "dweight"), (dbias, cols, "dbias"), (amax, 1, "amax")):
-        if t is not None:
-            _vector(t, n, x, what, torch.float32)
-    a = nvfp4_layernorm_backward_args(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-                                      _ptr(dsum), dx.data_ptr(), _ptr(dweight), _ptr(dbias), _ptr(amax), rows, cols,
-                                      _row_stride(dy), _row_stride(x), 0 if dsum is None else _row_stride(dsum),
-                                      _row_stride(dx), _dtype(x), _dtype(dy), _dtype(weight))
-    _check(lib().nvfp4_layernorm_backward(ctypes.byref(a), _ptr(workspace), _nbytes(workspace), _stream(stream)),
-           "nvfp4_layernorm_backward")
-    return dx
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _nbytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
+def _raw_stream(stream, device_index) -> int:
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(device_index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _on_device(t, what) -> int:
+    if not t.is_cuda:
+        raise ValueError("%s: a device tensor is wanted" % what)
+    return t.get_device()
+
+
+def _matrix(t, shape, device, what, dtype=None):
+    """Checks that t is a device tensor of a [rows][cols] shape with contiguous rows."""
+    if t.get_device() != device or t.shape != shape:
+        raise ValueError("%s: a tensor of shape %s on device %d is wanted" % (what, tuple(shape), device))
+    if t.stride(1) != 1 and shape[1] > 1:
+        raise ValueError("%s: contiguous rows are wanted" % what)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s: %s is wanted, not %s" % (what, dtype, t.dtype))
+
+
+def _row_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vector(t, n, device, what, dtype=None):
+    if t.dim() != 1 or t.numel() != n or t.get_device() != device or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s: a contiguous vector of %d elements on device %d is wanted" % (what, n, device))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s: %s is wanted, not %s" % (what, dtype, t.dtype))
+
+
+def _layernorm_inputs(x, weight, bias, residual, amax):
+    """(rows, cols, device) of the checked inputs of a layer norm."""
+    device = _on_device(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x: [rows][cols] is wanted")
+    shape = x.shape
+    _matrix(x, shape, device, "x")
+    if residual is not None:
+        _matrix(residual, shape, device, "residual", x.dtype)
+    _vector(weight, shape[1], device, "weight")
+    if bias is not None:
+        _vector(bias, shape[1], device, "bias", weight.dtype)
+    if amax is not None:
+        import torch
+        _vector(amax, 1, device, "amax", torch.float32)
+    return shape, device
+
+
+def _layernorm(x, weight, bias, eps, y, mean, rstd, residual, total, amax, shape, device, stream):
+    a = _NORM.pack(x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), y.data_ptr(), _ptr(total), mean, rstd,
+                   _ptr(amax), shape[0], shape[1], _row_stride(x), 0 if residual is None else _row_stride(residual),
+                   _row_stride(y), 0 if total is None else _row_stride(total), _dtype(x), _dtype(y), _dtype(weight), eps)
+    _check(lib().nvfp4_layernorm(a, _raw_stream(stream, device)), "nvfp4_layernorm")
+
+
+def nvfp4_layernorm(x, weight, bias, eps, y, mean, rstd, residual=None, sum=None, amax=None, stream=None):
+    """y = layer norm of x (or of x + residual, which goes to sum) over the rows of [rows][cols], with the rows' mean
+    and 1 / standard deviation; *amax is raised to max |y|."""
+    import torch
+    shape, device = _layernorm_inputs(x, weight, bias, residual, amax)
+    _matrix(y, shape, device, "y")
+    if sum is not None:
+        _matrix(sum, shape, device, "sum", x.dtype)
+    _vector(mean, shape[0], device, "mean", torch.float32)
+    _vector(rstd, shape[0], device, "rstd", torch.float32)
+    _layernorm(x, weight, bias, eps, y, mean.data_ptr(), rstd.data_ptr(), residual, sum, amax, shape, device, stream)
+    return y
+
+
 def layernorm(x, weight, bias=None, eps=1e-5, residual=None, amax=None, out_dtype=None, stream=None):
     """Allocates and computes (y, mean, rstd, sum): y of x's dtype or `out_dtype`; sum is x + residual, or None."""
+    if stream is not None:
+        with _on_stream(stream):
+            return layernorm(x, weight, bias, eps, residual, amax, out_dtype)
     import torch
-    with _on_stream(stream):
-        y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-        stats = torch.empty((2, x.shape[0]), dtype=torch.float32, device=x.device)
-        total = None if residual is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    nvfp4_layernorm(x, weight, bias, eps, y, stats[0], stats[1], residual, total, amax, stream)
-    return y, stats[0], stats[1], total
+    shape, device = _layernorm_inputs(x, weight, bias, residual, amax)
+    y = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
+    mean, rstd = torch.empty((2, shape[0]), dtype=torch.float32, device=x.device).unbind()
+    total = None if residual is None else torch.empty(shape, dtype=x.dtype, device=x.device)
+    _layernorm(x, weight, bias, eps, y, mean.data_ptr(), rstd.data_ptr(), residual, total, amax, shape, device, None)
+    return y, mean, rstd, total
+
+
+def _layernorm_backward_inputs(dy, x, weight, mean, rstd, dsum, amax):
+    import torch
+    device = _on_device(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x: [rows][cols] is wanted")
+    shape = x.shape
+    _matrix(x, shape, device, "x")
+    _matrix(dy, shape, device, "dy")
+    if dsum is not None:
+        _matrix(dsum, shape, device, "dsum", x.dtype)
+    _vector(weight, shape[1], device, "weight")
+    _vector(mean, shape[0], device, "mean", torch.float32)
+    _vector(rstd, shape[0], device, "rstd", torch.float32)
+    if amax is not None:
+        _vector(amax, 1, device, "amax", torch.float32)
+    return shape, device
+
+
+def _layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, dsum, amax, workspace, shape, device, stream):
+    a = _NORM_GRAD.pack(dy.data_ptr(), x.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(dsum),
+                        dx.data_ptr(), _ptr(dweight), _ptr(dbias), _ptr(amax), shape[0], shape[1], _row_stride(dy),
+                        _row_stride(x), 0 if dsum is None else _row_stride(dsum), _row_stride(dx), _dtype(x), _dtype(dy),
+                        _dtype(weight))
+    _check(lib().nvfp4_layernorm_backward(a, _ptr(workspace), _nbytes(workspace), _raw_stream(stream, device)),
+           "nvfp4_layernorm_backward")
+
+
+def nvfp4_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, dsum=None, amax=None, workspace=None,
+                             stream=None):
+    """dx, dweight and dbias (each of the two may be None) of a layer norm of x; dsum is added to dx."""
+    import torch
+    shape, device = _layernorm_backward_inputs(dy, x, weight, mean, rstd, dsum, amax)
+    _matrix(dx, shape, device, "dx", x.dtype)
+    for t, what in ((dweight, "dweight"), (dbias, "dbias")):
+        if t is not None:
+            _vector(t, shape[1], device, what, torch.float32)
+    if workspace is not None and workspace.get_device() != device:
+        raise ValueError("workspace: a tensor on device %d is wanted" % device)
+    _layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, dsum, amax, workspace, shape, device, stream)
+    return dx
 
 
 def layernorm_backward(dy, x, weight, mean, rstd, dsum=None, amax=None, workspace=None, stream=None):
     """Allocates and computes (dx, dweight, dbias)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return layernorm_backward(dy, x, weight, mean, rstd, dsum, amax, workspace)
     import torch
-    rows, cols = x.shape
-    with _on_stream(stream):
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw = torch.empty((2, cols), dtype=torch.float32, device=x.device)
-        if workspace is None:
-            workspace = torch.empty(lib().nvfp4_layernorm_backward_workspace_bytes(rows, cols), dtype=torch.uint8,
-                                    device=x.device)
-    nvfp4_layernorm_backward(dy, x, weight, mean, rstd, dx, dw[0], dw[1], dsum, amax, workspace, stream)
-    return dx, dw[0], dw[1]
+    shape, device = _layernorm_backward_inputs(dy, x, weight, mean, rstd, dsum, amax)
+    dx = torch.empty(shape, dtype=x.dtype, device=x.device)
+    dweight, dbias = torch.empty((2, shape[1]), dtype=torch.float32, device=x.device).unbind()
+    if workspace is None:
+        workspace = torch.empty(lib().nvfp4_layernorm_backward_workspace_bytes(*shape), dtype=torch.uint8, device=x.device)
+    elif workspace.get_device() != device:
+        raise ValueError("workspace: a tensor on device %d is wanted" % device)
+    _layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, dsum, amax, workspace, shape, device, None)
+    return dx, dweight, dbias
 
 
-def _heads(t) -> nvfp4_heads:
-    """[batch][tokens][heads][dim], or packed [tokens][heads][dim]."""
+def _heads(t, shape) -> bytes:
+    """The C form of [batch][tokens][heads][dim], or of packed [tokens][heads][dim]."""
     st = t.stride()  # of a dimension of one element: anything, and not used
-    return nvfp4_heads(t.data_ptr(), st[0] if t.dim() == 4 and t.shape[0] > 1 else 0,
-                       st[-3] if t.shape[-3] > 1 else t.shape[-2] * t.shape[-1], st[-2] if t.shape[-2] > 1 else 0)
+    return _HEADS.pack(t.data_ptr(), st[0] if len(shape) == 4 and shape[0] > 1 else 0,
+                       st[-3] if shape[-3] > 1 else shape[-2] * shape[-1], st[-2] if shape[-2] > 1 else 0)
 
 
-def _attention_shape(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k) -> nvfp4_attention_shape:
+def _attention_inputs(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k):
+    """(C shape, heads, query tokens, device) of the checked inputs of an attention call."""
     import torch
     packed = cu_q is not None
     if packed != (cu_k is not None) or (packed and (max_q is None or max_k is None)):
         raise ValueError("packed sequences need cu_q, cu_k, max_q and max_k")
+    bf16, device, dims = torch.bfloat16, q.get_device(), 3 if packed else 4
     for t, what in ((q, "q"), (k, "k"), (v, "v")):
-        if t.dtype != torch.bfloat16:
+        if t.dtype != bf16:
             raise TypeError("%s: bfloat16 is wanted, not %s" % (what, t.dtype))
-        if t.dim() != (3 if packed else 4) or not t.is_cuda or t.device != q.device:
+        if t.dim() != dims or device < 0 or t.get_device() != device:
             raise ValueError("%s: a device tensor [%stokens][heads][dim] is wanted" % (what, "" if packed else "batch]["))
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError("%s: a contiguous last dimension is wanted" % what)
-    if k.shape != v.shape or k.shape[-1] != q.shape[-1] or (not packed and k.shape[0] != q.shape[0]):
-        raise ValueError("q, k and v do not fit: %s, %s, %s" % (tuple(q.shape), tuple(k.shape), tuple(v.shape)))
+    sq, sk = q.shape, k.shape
+    if v.shape != sk or sk[-1] != sq[-1] or (not packed and sk[0] != sq[0]):
+        raise ValueError("q, k and v do not fit: %s, %s, %s" % (tuple(sq), tuple(sk), tuple(v.shape)))
     if scale is None:
-        scale = q.shape[-1] ** -0.5
+        scale = sq[-1] ** -0.5
     if not packed:
-        b, nq, nk = q.shape[0], q.shape[1], k.shape[1]
-        return nvfp4_attention_shape(b, nq, nk, q.shape[2], k.shape[2], q.shape[3], int(causal), window, None, None,
-                                     b * nq, b * nk, scale)
-    for t, what in ((cu_q, "cu_q"), (cu_k, "cu_k")):
-        _vector(t, cu_q.shape[0], q, what, torch.int32)
-    return nvfp4_attention_shape(cu_q.shape[0] - 1, max_q, max_k, q.shape[1], k.shape[1], q.shape[2], int(causal), window,
-                                 cu_q.data_ptr(), cu_k.data_ptr(), q.shape[0], k.shape[0], scale)
+        b, nq, h, d = sq
+        nk = sk[1]
+        return _SHAPE.pack(b, nq, nk, h, sk[2], d, causal, window, 0, 0, b * nq, b * nk, scale), sq, sk, h, b * nq, device
+    n = cu_q.shape[0]
+    _vector(cu_q, n, device, "cu_q", torch.int32)
+    _vector(cu_k, n, device, "cu_k", torch.int32)
+    return (_SHAPE.pack(n - 1, max_q, max_k, sq[1], sk[1], sq[2], causal, window, cu_q.data_ptr(), cu_k.data_ptr(), sq[0],
+                        sk[0], scale), sq, sk, sq[1], sq[0], device)
 
 
-def _as(t, like, what):
+def _as(t, shape, device, what):
     import torch
-    if t.shape != like.shape or t.dtype != torch.bfloat16 or t.device != like.device or (
-            t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError("%s: a bfloat16 tensor of shape %s is wanted" % (what, tuple(like.shape)))
+    if t.shape != shape or t.dtype != torch.bfloat16 or t.get_device() != device or (t.stride(-1) != 1 and shape[-1] > 1):
+        raise ValueError("%s: a bfloat16 tensor of shape %s on device %d is wanted" % (what, tuple(shape), device))
 
 
-def _lse(lse, s, like):
+def _lse(lse, heads, tokens, device):
     import torch
-    if lse.shape != (s.heads, s.total_q) or lse.dtype != torch.float32 or lse.device != like.device or (
-            not lse.is_contiguous()):
-        raise ValueError("lse: a contiguous float32 tensor of shape %s is wanted" % ((s.heads, s.total_q),))
+    if lse.shape != (heads, tokens) or lse.dtype != torch.float32 or lse.get_device() != device or not lse.is_contiguous():
+        raise ValueError("lse: a contiguous float32 tensor of shape %s on device %d is wanted" % ((heads, tokens), device))
 
 
 def nvfp4_attention(q, k, v, o, lse, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None, max_k=None,
                     stream=None):
     """o = softmax(scale q k^T) v and lse [heads][all queries] for [batch][tokens][heads][dim] tensors, or packed
     [tokens][heads][dim] ones with cu_q, cu_k (int32 [batch + 1], device) and the longest lengths max_q, max_k."""
-    s = _attention_shape(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
-    _as(o, q, "o")
-    _lse(lse, s, q)
-    h = [ctypes.byref(_heads(t)) for t in (q, k, v, o)]
-    _check(lib().nvfp4_attention(ctypes.byref(s), *h, lse.data_ptr(), _stream(stream)), "nvfp4_attention")
+    s, sq, sk, heads, tokens, device = _attention_inputs(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
+    _as(o, sq, device, "o")
+    _lse(lse, heads, tokens, device)
+    _check(lib().nvfp4_attention(s, _heads(q, sq), _heads(k, sk), _heads(v, sk), _heads(o, sq), lse.data_ptr(),
+                                 _raw_stream(stream, device)), "nvfp4_attention")
     return o
+
+
+def attention(q, k, v, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None, max_k=None, stream=None):
+    """Allocates and computes (o, lse)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return attention(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
+    import torch
+    s, sq, sk, heads, tokens, device = _attention_inputs(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
+    o = torch.empty(sq, dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((heads, tokens), dtype=torch.float32, device=q.device)
+    _check(lib().nvfp4_attention(s, _heads(q, sq), _heads(k, sk), _heads(v, sk), _heads(o, sq), lse.data_ptr(),
+                                 _raw_stream(None, device)), "nvfp4_attention")
+    return o, lse
+
+
+def _attention_backward(s, d_o, q, k, v, o, lse, dq, dk, dv, workspace, sq, sk, stream):
+    _check(lib().nvfp4_attention_backward(s, _heads(q, sq), _heads(k, sk), _heads(v, sk), _heads(o, sq), lse.data_ptr(),
+                                          _heads(d_o, sq), _heads(dq, sq), _heads(dk, sk), _heads(dv, sk),
+                                          _ptr(workspace), _nbytes(workspace), stream), "nvfp4_attention_backward")
 
 
 def nvfp4_attention_backward(d_o, q, k, v, o, lse, dq, dk, dv, workspace, causal=True, window=0, scale=None, cu_q=None,
                              cu_k=None, max_q=None, max_k=None, stream=None):
     """dq, dk and dv of nvfp4_attention with the same arguments."""
-    s = _attention_shape(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
-    for t, like, what in ((d_o, q, "d_o"), (o, q, "o"), (dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
-        _as(t, like, what)
-    _lse(lse, s, q)
-    h = [ctypes.byref(_heads(t)) for t in (q, k, v, o)]
-    g = [ctypes.byref(_heads(t)) for t in (d_o, dq, dk, dv)]
-    _check(lib().nvfp4_attention_backward(ctypes.byref(s), *h, lse.data_ptr(), *g, _ptr(workspace), _nbytes(workspace),
-                                          _stream(stream)), "nvfp4_attention_backward")
+    s, sq, sk, heads, tokens, device = _attention_inputs(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
+    for t, shape, what in ((d_o, sq, "d_o"), (o, sq, "o"), (dq, sq, "dq"), (dk, sk, "dk"), (dv, sk, "dv")):
+        _as(t, shape, device, what)
+    _lse(lse, heads, tokens, device)
+    if workspace is not None and workspace.get_device() != device:
+        raise ValueError("workspace: a tensor on device %d is wanted" % device)
+    _attention_backward(s, d_o, q, k, v, o, lse, dq, dk, dv, workspace, sq, sk, _raw_stream(stream, device))
     return dq, dk, dv
 
 
 def new_attention_workspace(q, k, v, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None, max_k=None):
     """A workspace of nvfp4_attention_backward for these arguments (one per stream)."""
     import torch
-    s = _attention_shape(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
-    return torch.empty(lib().nvfp4_attention_backward_workspace_bytes(ctypes.byref(s)), dtype=torch.uint8,
-                       device=q.device)
-
-
-def attention(q, k, v, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None, max_k=None, stream=None):
-    """Allocates and computes (o, lse)."""
-    import torch
-    tokens = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
-    with _on_stream(stream):
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty((q.shape[-2], tokens), dtype=torch.float32, device=q.device)
-    nvfp4_attention(q, k, v, o, lse, causal, window, scale, cu_q, cu_k, max_q, max_k, stream)
-    return o, lse
+    s = _attention_inputs(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)[0]
+    return torch.empty(lib().nvfp4_attention_backward_workspace_bytes(s), dtype=torch.uint8, device=q.device)
 
 
 def attention_backward(d_o, q, k, v, o, lse, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None,
                        max_k=None, workspace=None, stream=None):
     """Allocates and computes (dq, dk, dv)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return attention_backward(d_o, q, k, v, o, lse, causal, window, scale, cu_q, cu_k, max_q, max_k, workspace)
     import torch
-    opts = (causal, window, scale, cu_q, cu_k, max_q, max_k)
-    with _on_stream(stream):
-        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
-        if workspace is None:
-            workspace = new_attention_workspace(q, k, v, *opts)
-    return nvfp4_attention_backward(d_o, q, k, v, o, lse, dq, dk, dv, workspace, *opts, stream)
+    s, sq, sk, heads, tokens, device = _attention_inputs(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
+    _as(d_o, sq, device, "d_o")
+    _as(o, sq, device, "o")
+    _lse(lse, heads, tokens, device)
+    dq = torch.empty(sq, dtype=torch.bfloat16, device=q.device)
+    dk, dv = (torch.empty(sk, dtype=torch.bfloat16, device=q.device) for _ in range(2))
+    if workspace is None:
+        workspace = torch.empty(lib().nvfp4_attention_backward_workspace_bytes(s), dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != device:
+        raise ValueError("workspace: a tensor on device %d is wanted" % device)
+    _attention_backward(s, d_o, q, k, v, o, lse, dq, dk, dv, workspace, sq, sk, _raw_stream(None, device))
+    return dq, dk, dv
 
 
 @dataclass
@@ -784,9 +863,14 @@ class AdamWList:
         if not self.tensors:
             raise ValueError("no tensors")
         self.array = (nvfp4_adamw_tensor * len(self.tensors))(*[t.c_struct() for t in self.tensors])
+        self.device = self.tensors[0].param.get_device()
+        if any(t.param.get_device() != self.device for t in self.tensors):
+            raise ValueError("the tensors are on several devices")
 
     def set_grad(self, index: int, grad):
         t = self.tensors[index]
+        if grad.get_device() != self.device:
+            raise ValueError("grad: a tensor on device %d is wanted" % self.device)
         old, t.grad = t.grad, grad
         try:
             self.array[index] = t.c_struct()
@@ -801,9 +885,10 @@ def adamw(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, rounding="rtn",
     if not isinstance(tensors, AdamWList):
         tensors = AdamWList(tensors)
     if grad_scale is not None:
-        _vector(grad_scale, 1, tensors.tensors[0].param, "grad_scale", torch.float32)
+        _vector(grad_scale, 1, tensors.device, "grad_scale", torch.float32)
     c = nvfp4_adamw_config(lr, beta1, beta2, eps, ROUNDINGS.get(rounding, rounding), step, seed, _ptr(grad_scale))
-    _check(lib().nvfp4_adamw(tensors.array, len(tensors.array), ctypes.byref(c), _stream(stream)), "nvfp4_adamw")
+    _check(lib().nvfp4_adamw(tensors.array, len(tensors.array), ctypes.byref(c), _raw_stream(stream, tensors.device)),
+           "nvfp4_adamw")
 
 
 def adamw_state_values(t: AdamWTensor):
