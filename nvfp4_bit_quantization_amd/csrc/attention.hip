@@ -39,8 +39,15 @@ __device__ __forceinline__ f32x16 zero16() {
 // row of result register i in half h
 __device__ __forceinline__ int row_of(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
 
-// the other half's value
-__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+// the larger, and the sum, of a lane's value and the other half's
+__device__ __forceinline__ float half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
 
 // ------------------------------------------------------------ sequences ----
 struct Seq {
@@ -85,57 +92,99 @@ __device__ __forceinline__ void sight(const AttnArgs &a, int i, int nk, int off,
 }
 
 // ---------------------------------------------------------------- tiles ----
-// A tile of 64 rows of D elements in LDS, rows of 2 D bytes, in which chunk c
-// (16 bytes) of row r stands at c ^ spread(r): both reads below then meet every
-// group of banks equally, the plain one (32 rows at one chunk) and the
-// transposing one (4 rows at 4 neighbouring chunks).
+// A tile of 64 rows of D elements in LDS.  It is filled by direct transfers of
+// 1024 bytes, whose lanes' 16 bytes land next to each other: a segment of 4
+// (D = 128) or 8 (D = 64) rows.  Chunks (16 bytes) are permuted within a row by
+// which address each lane reads, chunk c of row r standing at c ^ spread(r),
+// and segments are 16 bytes further apart than they are long.  Both reads below
+// then meet every group of banks equally, the plain one (32 rows at one chunk)
+// and the transposing one (4 rows at 4 neighbouring chunks), and all reads of a
+// lane stand at fixed distances from four (plain) and D / 32 (transposing)
+// addresses, as the instructions' immediate offsets.
 template <int D>
-__device__ __forceinline__ uint32_t spread(uint32_t r) {
-  if constexpr (D == 128)
-    return ((r & 3u) << 2) | ((r >> 2) & 3u);
-  else
-    return (((r >> 1) & 1u) << 2) | ((r >> 2) & 3u);  // two rows to 256 bytes
-}
+struct Tile {
+  static constexpr int kChunks = D / 8, kSegRows = 64 / kChunks;
+  static constexpr uint32_t kSeg = 1024 + 16, kBytes = kTile / kSegRows * kSeg;
+  static __device__ __forceinline__ uint32_t spread(uint32_t r) {
+    return D == 128 ? (r & 3u) << 2 : ((r >> 1) & 1u) << 2 | ((r >> 2) & 1u) << 1;
+  }
+};
 
 // Transfer rows row0 .. row0 + 63 of a head (rows past `rows` repeat the last
 // one, chunks past head_dim the first: their products are masked, or meet
-// zeros) into the tile at LDS address lds.  Four waves, D / 32 transfers each.
+// zeros) into the tile at LDS address lds.  Each of four waves fills D / 32
+// segments.
 template <int D>
 __device__ __forceinline__ void fetch_tile(const uint16_t *head, int64_t stride, int row0, int rows, int chunks,
                                            uint32_t lds, int wave, int lane) {
-  constexpr int kRowChunks = D / 8, kRows = 64 / kRowChunks;  // rows of one transfer
+  typedef Tile<D> T;
   const uint8_t *base = uniform_ptr((const uint8_t *)(head + (int64_t)row0 * stride));
-  const int left = rows - row0 - 1;
+  asm volatile("" : "+v"(lane));  // the offsets are formed here, not kept in registers
+  const uint32_t r = (uint32_t)lane / T::kChunks, pitch = (uint32_t)stride * 2u;
+  uint32_t c = ((uint32_t)lane % T::kChunks) ^ T::spread(r);
+  c = (int)c < chunks ? c * 16u : 0u;
+  const int left = rows - row0;
+  if (left >= kTile) {
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    const int r = (wave * (D / 32) + i) * kRows + lane / kRowChunks;
-    const uint32_t c = (uint32_t)(lane % kRowChunks) ^ spread<D>(r);
-    const uint32_t voff = (uint32_t)(r < left ? r : left) * (uint32_t)(stride * 2) + ((int)c < chunks ? c : 0u) * 16u;
-    dma16(base, voff, __builtin_amdgcn_readfirstlane(lds + (uint32_t)(wave * (D / 32) + i) * 1024u));
+    for (int i = 0; i < D / 32; ++i) {
+      const int seg = wave * (D / 32) + i;
+      dma16(uniform_ptr(base + (uint64_t)(seg * T::kSegRows) * pitch), r * pitch + c,
+            __builtin_amdgcn_readfirstlane(lds + (uint32_t)seg * T::kSeg));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const int seg = wave * (D / 32) + i, row = seg * T::kSegRows + (int)r;
+      dma16(base, (uint32_t)(row < left ? row : left - 1) * pitch + c,
+            __builtin_amdgcn_readfirstlane(lds + (uint32_t)seg * T::kSeg));
+    }
   }
 }
 
-// A operand from rows r0 .. r0 + 31 as they stand: row n, elements 16 c + 8 h ...
+// a lane's addresses within a tile
 template <int D>
-__device__ __forceinline__ bf16x8 read_rows(const uint8_t *tile, int r0, int c, int lane) {
-  const uint32_t r = (uint32_t)(r0 + (lane & 31)), p = (uint32_t)(2 * c + (lane >> 5)) ^ spread<D>(r);
-  return *reinterpret_cast<const bf16x8 *>(tile + r * (2 * D) + p * 16);
-}
-// A operand from the transposed tile: row = element 32 dt + n, inner index =
-// tile rows r0 + 4 h .. and r0 + 8 + 4 h ..
-template <int D>
-__device__ __forceinline__ bf16x8 read_cols(const uint8_t *tile, int r0, int dt, int lane) {
-  const int i = lane & 15, g = lane >> 4;
-  const uint32_t r = (uint32_t)(r0 + 4 * (g >> 1) + (i >> 2));
-  const uint32_t c = (uint32_t)(dt * 4 + (g & 1) * 2 + ((i & 3) >> 1)), sub = (uint32_t)(i & 1) * 8;
-  const uint8_t *p0 = tile + r * (2 * D) + ((c ^ spread<D>(r)) * 16) + sub;
-  const uint8_t *p1 = tile + (r + 8) * (2 * D) + ((c ^ spread<D>(r + 8)) * 16) + sub;
-  typedef short i16x8 __attribute__((ext_vector_type(8)));
-  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)p0);
-  const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)p1);
-  const i16x8 v = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  return __builtin_bit_cast(bf16x8, v);
-}
+struct Reads {
+  uint32_t row[4], col[D / 32];
+  __device__ __forceinline__ Reads(int lane, uint32_t at) {
+    typedef Tile<D> T;
+    const uint32_t n = lane & 31, h = lane >> 5, i = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (uint32_t k = 0; k < 4; ++k) {
+      const uint32_t c = (D == 128 ? 4 * k : 2 * k) + h;
+      row[k] = n / T::kSegRows * T::kSeg + n % T::kSegRows * (2 * D) + (c ^ T::spread(n)) * 16 + at;
+    }
+#pragma unroll
+    for (uint32_t dt = 0; dt < D / 32; ++dt) {
+      const uint32_t r = 4 * (g >> 1) + (i >> 2), c = dt * 4 + (g & 1) * 2 + ((i & 3) >> 1);
+      col[dt] = r / T::kSegRows * T::kSeg + r % T::kSegRows * (2 * D) + (c ^ T::spread(r)) * 16 + (i & 1) * 8 + at;
+    }
+  }
+  // to the tile `by` bytes on
+  __device__ __forceinline__ void move(uint32_t by) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) row[k] += by;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) col[k] += by;
+  }
+  // A operand from rows r0 .. r0 + 31 (r0 = 0, 32) as they stand: row n,
+  // elements 16 c + 8 h ..; `tile`: bytes to another tile
+  __device__ __forceinline__ bf16x8 rows(uint32_t tile, int r0, int c) const {
+    const uint32_t a = row[D == 128 ? c >> 1 : c] + tile + (uint32_t)(r0 / Tile<D>::kSegRows) * Tile<D>::kSeg +
+                       (D == 128 ? (c & 1) * 32u : 0u);
+    return *(const __attribute__((address_space(3))) bf16x8 *)a;
+  }
+  // A operand from the transposed tile: row = element 32 dt + n, inner index =
+  // tile rows r0 + 4 h .. and r0 + 8 + 4 h .. (r0 = 0, 16, 32, 48)
+  __device__ __forceinline__ bf16x8 cols(uint32_t tile, int r0, int dt) const {
+    typedef short i16x8 __attribute__((ext_vector_type(8)));
+    constexpr uint32_t k8 = 8 / Tile<D>::kSegRows * Tile<D>::kSeg;
+    const uint32_t a = col[dt] + tile + (uint32_t)(r0 / 8) * k8;
+    const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)a);
+    const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(a + k8));
+    const i16x8 v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(bf16x8, v);
+  }
+};
 
 // B operand of a row held by its lane: elements 16 c + 8 h .. of `row`, zero
 // from head_dim on
@@ -201,7 +250,8 @@ constexpr int kQueries = 128;  // queries of a workgroup: 32 per wave
 // Running maximum and sum per query stay in its two lanes.
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
-  __shared__ __align__(1024) uint8_t lds[2][2][kTile * D * 2];
+  __shared__ __align__(16) uint8_t lds[4 * Tile<D>::kBytes];
+  constexpr uint32_t kB = Tile<D>::kBytes;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
   const int group = a.heads / a.kv_heads, tiles = (a.q_len + kQueries - 1) / kQueries;
   Work w = work_of(a, tiles, group);
@@ -234,27 +284,28 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   for (int dt = 0; dt < D / 32; ++dt) o[dt] = zero16();
   float top = kLow, sum = 0.0f;
   const float c2 = a.scale * kLog2e;
+  Reads<D> in(lane, lds_addr(lds));
 
   const int t0 = begin / kTile, t1 = end > begin ? (end + kTile - 1) / kTile : t0;
   if (t0 < t1) {
-    fetch_tile<D>(kh, a.k.st, t0 * kTile, s.nk, chunks, lds_addr(lds[0][0]), wave, lane);
-    fetch_tile<D>(vh, a.v.st, t0 * kTile, s.nk, chunks, lds_addr(lds[0][1]), wave, lane);
+    fetch_tile<D>(kh, a.k.st, t0 * kTile, s.nk, chunks, lds_addr(lds), wave, lane);
+    fetch_tile<D>(vh, a.v.st, t0 * kTile, s.nk, chunks, lds_addr(lds) + kB, wave, lane);
   }
   for (int t = t0; t < t1; ++t) {
     const int stage = (t - t0) & 1, k0 = t * kTile;
+    if (t > t0) in.move(stage ? 2 * kB : 0u - 2 * kB);
     tile_barrier();  // this tile is in LDS, and every wave has read the previous one
     if (t + 1 < t1) {
-      fetch_tile<D>(kh, a.k.st, k0 + kTile, s.nk, chunks, lds_addr(lds[stage ^ 1][0]), wave, lane);
-      fetch_tile<D>(vh, a.v.st, k0 + kTile, s.nk, chunks, lds_addr(lds[stage ^ 1][1]), wave, lane);
+      fetch_tile<D>(kh, a.k.st, k0 + kTile, s.nk, chunks, lds_addr(lds) + (uint32_t)(stage ^ 1) * 2 * kB, wave, lane);
+      fetch_tile<D>(vh, a.v.st, k0 + kTile, s.nk, chunks, lds_addr(lds) + (uint32_t)(stage ^ 1) * 2 * kB + kB, wave, lane);
     }
     if (k0 >= any_hi || k0 + kTile <= any_lo) continue;  // nothing in the wave's sight
-    const uint8_t *kt = lds[stage][0], *vt = lds[stage][1];
     f32x16 p[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       p[u] = zero16();
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) p[u] = mfma(read_rows<D>(kt, u * 32, c, lane), q[c], p[u]);
+      for (int c = 0; c < D / 16; ++c) p[u] = mfma(in.rows(0, u * 32, c), q[c], p[u]);
     }
     if (k0 + kTile > all_hi || k0 < all_lo) {
 #pragma unroll
@@ -268,7 +319,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
     float m = fmaxf(p[0][0], p[1][0]);
 #pragma unroll
     for (int i = 1; i < 16; ++i) m = fmaxf(m, fmaxf(p[0][i], p[1][i]));
-    m = fmaxf(m, other_half(m)) * c2;
+    m = half_max(m) * c2;
     // The exponents' reference follows the maximum only when that has risen by
     // more than 8 (a factor of 256 in p): results do not depend on it
     if (__any(m > top + 8.0f)) {
@@ -293,10 +344,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
       for (int c = 0; c < 2; ++c) {
         const bf16x8 b = pack8(p[u], 8 * c);
 #pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt) o[dt] = mfma(read_cols<D>(vt, u * 32 + c * 16, dt, lane), b, o[dt]);
+        for (int dt = 0; dt < D / 32; ++dt) o[dt] = mfma(in.cols(kB, u * 32 + c * 16, dt), b, o[dt]);
       }
   }
-  sum += other_half(sum);
+  sum = half_sum(sum);
   if (mine >= s.nq) return;
   const bool none = sum == 0.0f;
   store_cols<D>(at(a.o, s.bq, s.q0 + mine, w.head), o, none ? 0.0f : 1.0f / sum, a.dim, h);
@@ -306,7 +357,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
 }
 
 // ------------------------------------------------------------- gradient ----
-// delta = sum_d do * o, 16 lanes to a row
+// delta = sum_d do * o, 16 lanes to a row; and lse in powers of two beside it
 __global__ __launch_bounds__(kThreads) void attention_delta_kernel(AttnArgs a) {
   const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);  // (sequence, query) or token
   const int head = blockIdx.y, c = threadIdx.x & 15;
@@ -323,14 +374,20 @@ __global__ __launch_bounds__(kThreads) void attention_delta_kernel(AttnArgs a) {
   v += dpp<0x124>(v);
   v += dpp<0x122>(v);
   v += dpp<0x121>(v);
-  if (row < a.total_q && c == 0) a.delta[(int64_t)head * a.total_q + row] = v;
+  if (row < a.total_q && c == 0) {
+    const int64_t i = (int64_t)head * a.total_q + row;
+    a.delta[i] = v;
+    const float lse = a.lse[i] * kLog2e;
+    a.lse2[i] = lse == -INFINITY ? 0.0f : lse;  // all of such a row is masked: exp2(-inf - 0) = 0
+  }
 }
 
 // dQ: a wave holds 32 queries as columns; scores^T = K Q^T, dP^T = V dO^T,
 // dQ^T = K^T dS^T.
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
-  __shared__ __align__(1024) uint8_t lds[2][2][kTile * D * 2];
+  __shared__ __align__(16) uint8_t lds[4 * Tile<D>::kBytes];
+  constexpr uint32_t kB = Tile<D>::kBytes;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
   const int group = a.heads / a.kv_heads, tiles = (a.q_len + kQueries - 1) / kQueries;
   Work w = work_of(a, tiles, group);
@@ -351,7 +408,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
     g[c] = load_row(grow, c, chunks, h);
   }
   const int64_t stat = (int64_t)w.head * a.total_q + first_row(a, s, w.b) + qi;
-  const float lse2 = a.lse[stat] * kLog2e, delta = a.delta[stat];
+  const float lse2 = a.lse2[stat], delta = a.delta[stat];
 
   int lo, hi, unused, begin, end;
   sight(a, qi, s.nk, off, lo, hi);
@@ -366,42 +423,43 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt) acc[dt] = zero16();
   const float c2 = a.scale * kLog2e;
+  Reads<D> in(lane, lds_addr(lds));
   const int t0 = begin / kTile, t1 = end > begin ? (end + kTile - 1) / kTile : t0;
   if (t0 < t1) {
-    fetch_tile<D>(kh, a.k.st, t0 * kTile, s.nk, chunks, lds_addr(lds[0][0]), wave, lane);
-    fetch_tile<D>(vh, a.v.st, t0 * kTile, s.nk, chunks, lds_addr(lds[0][1]), wave, lane);
+    fetch_tile<D>(kh, a.k.st, t0 * kTile, s.nk, chunks, lds_addr(lds), wave, lane);
+    fetch_tile<D>(vh, a.v.st, t0 * kTile, s.nk, chunks, lds_addr(lds) + kB, wave, lane);
   }
   for (int t = t0; t < t1; ++t) {
     const int stage = (t - t0) & 1, k0 = t * kTile;
+    if (t > t0) in.move(stage ? 2 * kB : 0u - 2 * kB);
     tile_barrier();
     if (t + 1 < t1) {
-      fetch_tile<D>(kh, a.k.st, k0 + kTile, s.nk, chunks, lds_addr(lds[stage ^ 1][0]), wave, lane);
-      fetch_tile<D>(vh, a.v.st, k0 + kTile, s.nk, chunks, lds_addr(lds[stage ^ 1][1]), wave, lane);
+      fetch_tile<D>(kh, a.k.st, k0 + kTile, s.nk, chunks, lds_addr(lds) + (uint32_t)(stage ^ 1) * 2 * kB, wave, lane);
+      fetch_tile<D>(vh, a.v.st, k0 + kTile, s.nk, chunks, lds_addr(lds) + (uint32_t)(stage ^ 1) * 2 * kB + kB, wave, lane);
     }
     if (k0 >= any_hi || k0 + kTile <= any_lo) continue;
-    const uint8_t *kt = lds[stage][0], *vt = lds[stage][1];
     const bool masked = k0 + kTile > all_hi || k0 < all_lo;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       f32x16 p = zero16(), d = zero16();
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) p = mfma(read_rows<D>(kt, u * 32, c, lane), q[c], p);
+      for (int c = 0; c < D / 16; ++c) p = mfma(in.rows(0, u * 32, c), q[c], p);
+      if (masked) {
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) d = mfma(read_rows<D>(vt, u * 32, c, lane), g[c], d);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float e = __builtin_amdgcn_exp2f(fmaf(p[i], c2, -lse2));
-        if (masked) {
+        for (int i = 0; i < 16; ++i) {
           const int j = k0 + u * 32 + row_of(i, h);
-          e = j < hi && j >= lo ? e : 0.0f;
+          p[i] = j < hi && j >= lo ? p[i] : -INFINITY;
         }
-        p[i] = e * (d[i] - delta);
       }
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) d = mfma(in.rows(kB, u * 32, c), g[c], d);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], c2, -lse2)) * (d[i] - delta);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const bf16x8 b = pack8(p, 8 * c);
 #pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt) acc[dt] = mfma(read_cols<D>(kt, u * 32 + c * 16, dt, lane), b, acc[dt]);
+        for (int dt = 0; dt < D / 32; ++dt) acc[dt] = mfma(in.cols(0, u * 32 + c * 16, dt), b, acc[dt]);
       }
     }
   }
@@ -413,13 +471,18 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
 constexpr int kKeys = 128;  // keys of a workgroup
 
 template <int D>
-__global__ __launch_bounds__(kThreads, 1) void attention_dkv_kernel(AttnArgs a) {
-  __shared__ __align__(1024) uint8_t lds[2][2][kTile * D * 2];
+__global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttnArgs a) {
+  __shared__ __align__(16) uint8_t lds[4 * Tile<D>::kBytes];
+  constexpr uint32_t kB = Tile<D>::kBytes;
   __shared__ __align__(16) float stats[2][2][kTile];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
   const int group = a.heads / a.kv_heads, tiles = (a.k_len + kKeys - 1) / kKeys;
-  const Work w = work_of(a, tiles, 1);
+  Work w = work_of(a, tiles, 1);
   const int hk = w.head;
+  // Key tiles of a causal pass differ in work, falling along the sequence.
+  // Every second head walks them from the end, so that the workgroups that a
+  // compute unit holds at a time add up to the same.
+  if ((w.b * a.kv_heads + hk) & 1) w.tile = tiles - 1 - w.tile;
   const Seq s = sequence(a, w.b);
   const int first = w.tile * kKeys;
   if (first >= s.nk) return;
@@ -434,21 +497,16 @@ __global__ __launch_bounds__(kThreads, 1) void attention_dkv_kernel(AttnArgs a) 
     k[c] = load_row(krow, c, chunks, h);
     v[c] = load_row(vrow, c, chunks, h);
   }
-  // the queries that see key j: j - off <= i < j - off + window, with causal
-  int lo = 0, hi = s.nq, begin = 0, end = s.nq, any_lo = 0, any_hi = s.nq, all_lo = 0, all_hi = s.nq;
-  if (a.causal) {
-    const int w0 = first + wave * 32, w1 = w0 + 31;
-    lo = (int)clamp64((int64_t)ki - off, 0, s.nq);
-    begin = (int)clamp64((int64_t)first - off, 0, s.nq);
-    any_lo = (int)clamp64((int64_t)w0 - off, 0, s.nq);
-    all_lo = (int)clamp64((int64_t)w1 - off, 0, s.nq);
-    if (a.window) {
-      hi = (int)clamp64((int64_t)ki - off + a.window, 0, s.nq);
-      end = (int)clamp64((int64_t)last - off + a.window, 0, s.nq);
-      any_hi = (int)clamp64((int64_t)w1 - off + a.window, 0, s.nq);
-      all_hi = (int)clamp64((int64_t)w0 - off + a.window, 0, s.nq);
-    }
-  }
+  // the queries [lo, hi) that see key j: j - off <= i < j - off + window, with causal
+  const auto seen_by = [&](int j, int &lo, int &hi) {
+    lo = a.causal ? (int)clamp64((int64_t)j - off, 0, s.nq) : 0;
+    hi = a.window ? (int)clamp64((int64_t)j - off + a.window, 0, s.nq) : s.nq;
+  };
+  int begin, end, any_lo, any_hi, all_lo, all_hi, unused;
+  seen_by(first, begin, unused);
+  seen_by(last, unused, end);
+  seen_by(first + wave * 32, any_lo, all_hi);
+  seen_by(first + wave * 32 + 31, all_lo, any_hi);
   f32x16 dk[D / 32], dv[D / 32];
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt) {
@@ -456,62 +514,77 @@ __global__ __launch_bounds__(kThreads, 1) void attention_dkv_kernel(AttnArgs a) 
     dv[dt] = zero16();
   }
   const float c2 = a.scale * kLog2e;
-  const int t0 = begin / kTile, t1 = end > begin ? (end + kTile - 1) / kTile : t0, steps = (t1 - t0) * group;
+  const int t0 = begin / kTile, t1 = end > begin ? (end + kTile - 1) / kTile : t0;
   const int64_t row0 = first_row(a, s, w.b);
-  const auto fetch = [&](int step, int stage) {
-    const int head = hk * group + step / (t1 - t0), i0 = (t0 + step % (t1 - t0)) * kTile;
-    fetch_tile<D>(at(a.q, s.bq, s.q0, head), a.q.st, i0, s.nq, chunks, lds_addr(lds[stage][0]), wave, lane);
-    fetch_tile<D>(at(a.d_o, s.bq, s.q0, head), a.d_o.st, i0, s.nq, chunks, lds_addr(lds[stage][1]), wave, lane);
+  const auto fetch = [&](int head, int t, int stage) {
+    const int i0 = t * kTile;
+    const uint32_t to = lds_addr(lds) + (uint32_t)stage * 2 * kB;
+    fetch_tile<D>(at(a.q, s.bq, s.q0, head), a.q.st, i0, s.nq, chunks, to, wave, lane);
+    fetch_tile<D>(at(a.d_o, s.bq, s.q0, head), a.d_o.st, i0, s.nq, chunks, to + kB, wave, lane);
     if (wave < 2) {
-      const float *src = (wave ? a.delta : a.lse) + (int64_t)head * a.total_q + row0 + i0;
+      const float *src = (wave ? a.delta : a.lse2) + (int64_t)head * a.total_q + row0 + i0;
       const int left = s.nq - i0 - 1;
       dma4(uniform_ptr((const uint8_t *)src), (uint32_t)(lane < left ? lane : left) * 4u,
            __builtin_amdgcn_readfirstlane(lds_addr(stats[stage][wave])));
     }
   };
-  if (steps > 0) fetch(0, 0);
-  for (int step = 0; step < steps; ++step) {
-    const int stage = step & 1, i0 = (t0 + step % (t1 - t0)) * kTile;
-    tile_barrier();
-    if (step + 1 < steps) fetch(step + 1, stage ^ 1);
-    if (i0 >= any_hi || i0 + kTile <= any_lo) continue;
-    const uint8_t *qt = lds[stage][0], *gt = lds[stage][1];
-    const bool masked = i0 + kTile > all_hi || i0 < all_lo;
+  Reads<D> in(lane, lds_addr(lds));
+  int head = hk * group, t = t0, stage = 0;
+  bool more = t0 < t1;
+  if (more) fetch(head, t, 0);
+  while (more) {
+    const int i0 = t * kTile;
+    tile_barrier();  // this tile is in LDS, and every wave has read the previous one
+    if (++t == t1) {
+      t = t0;
+      ++head;
+    }
+    more = head < (hk + 1) * group;
+    if (more) fetch(head, t, stage ^ 1);
+    if (i0 < any_hi && i0 + kTile > any_lo) {
+      const bool masked = i0 + kTile > all_hi || i0 < all_lo;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      f32x16 p = zero16(), d = zero16();
+      for (int u = 0; u < 2; ++u) {
+        f32x16 p = zero16(), d = zero16();
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) p = mfma(read_rows<D>(qt, u * 32, c, lane), k[c], p);
+        for (int c = 0; c < D / 16; ++c) p = mfma(in.rows(0, u * 32, c), k[c], p);
+        if (masked) {
+          int l = lane, lo, hi;
+          asm volatile("" : "+v"(l));  // the limits are formed here, not kept in registers
+          seen_by(first + wave * 32 + (l & 31), lo, hi);
+          lo -= i0 + u * 32;
+          hi -= i0 + u * 32;
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) d = mfma(read_rows<D>(gt, u * 32, c, lane), v[c], d);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const float4 lse = *reinterpret_cast<const float4 *>(&stats[stage][0][u * 32 + 8 * b + 4 * h]);
-        const float4 del = *reinterpret_cast<const float4 *>(&stats[stage][1][u * 32 + 8 * b + 4 * h]);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = 4 * b + r;
-          const float l = r == 0 ? lse.x : r == 1 ? lse.y : r == 2 ? lse.z : lse.w;
-          const float e = r == 0 ? del.x : r == 1 ? del.y : r == 2 ? del.z : del.w;
-          float x = __builtin_amdgcn_exp2f(fmaf(p[i], c2, -l * kLog2e));
-          if (masked) {
-            const int qi = i0 + u * 32 + row_of(i, h);
-            x = qi < hi && qi >= lo ? x : 0.0f;
-          }
-          p[i] = x;
-          d[i] = x * (d[i] - e);
+          for (int i = 0; i < 16; ++i) p[i] = row_of(i, l >> 5) < hi && row_of(i, l >> 5) >= lo ? p[i] : -INFINITY;
         }
-      }
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const bf16x8 b0 = pack8(p, 8 * c), b1 = pack8(d, 8 * c);
+        for (int c = 0; c < D / 16; ++c) d = mfma(in.rows(kB, u * 32, c), v[c], d);
 #pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt) {
-          dv[dt] = mfma(read_cols<D>(gt, u * 32 + c * 16, dt, lane), b0, dv[dt]);
-          dk[dt] = mfma(read_cols<D>(qt, u * 32 + c * 16, dt, lane), b1, dk[dt]);
+        for (int b = 0; b < 4; ++b) {
+          const float4 lse = *reinterpret_cast<const float4 *>(&stats[stage][0][u * 32 + 8 * b + 4 * h]);
+          const float4 del = *reinterpret_cast<const float4 *>(&stats[stage][1][u * 32 + 8 * b + 4 * h]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = 4 * b + r;
+            const float l = r == 0 ? lse.x : r == 1 ? lse.y : r == 2 ? lse.z : lse.w;
+            const float e = r == 0 ? del.x : r == 1 ? del.y : r == 2 ? del.z : del.w;
+            p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], c2, -l));
+            d[i] = p[i] * (d[i] - e);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const bf16x8 b0 = pack8(p, 8 * c), b1 = pack8(d, 8 * c);
+#pragma unroll
+          for (int dt = 0; dt < D / 32; ++dt) {
+            dv[dt] = mfma(in.cols(kB, u * 32 + c * 16, dt), b0, dv[dt]);
+            dk[dt] = mfma(in.cols(0, u * 32 + c * 16, dt), b1, dk[dt]);
+          }
         }
       }
     }
+    in.move(stage ? 0u - 2 * kB : 2 * kB);
+    stage ^= 1;
   }
   if (mine >= s.nk) return;
   store_cols<D>(at(a.dk, s.bk, s.k0 + mine, hk), dk, a.scale, a.dim, h);

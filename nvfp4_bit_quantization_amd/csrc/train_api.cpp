@@ -76,6 +76,11 @@ Heads heads_of(const nvfp4_heads *t) {
   return Heads{(uint16_t *)t->data, t->batch_stride, t->token_stride, t->head_stride};
 }
 
+// one float for every query of every head, in whole 256 bytes (not none)
+size_t stat_bytes(const nvfp4_attention_shape *s) {
+  return ((size_t)s->heads * (size_t)s->total_q * sizeof(float) + 511) & ~(size_t)255;
+}
+
 AttnArgs attn_args(const nvfp4_attention_shape *s) {
   AttnArgs a = {};
   a.cu_q = s->cu_q;
@@ -181,7 +186,7 @@ int nvfp4_attention(const nvfp4_attention_shape *shape, const nvfp4_heads *q, co
 
 size_t nvfp4_attention_backward_workspace_bytes(const nvfp4_attention_shape *shape) {
   if (check_shape(shape) != NVFP4_OK) return 0;
-  return (((size_t)shape->heads * (size_t)shape->total_q * sizeof(float) + 255) & ~(size_t)255) + 256;
+  return 2 * stat_bytes(shape);
 }
 
 int nvfp4_attention_backward(const nvfp4_attention_shape *shape, const nvfp4_heads *q, const nvfp4_heads *k,
@@ -209,6 +214,7 @@ int nvfp4_attention_backward(const nvfp4_attention_shape *shape, const nvfp4_hea
   a.dv = heads_of(dv);
   a.lse = const_cast<float *>(lse);
   a.delta = (float *)workspace;
+  a.lse2 = (float *)((char *)workspace + stat_bytes(shape));
   hipStream_t s = (hipStream_t)stream;
   return finish(launch_attention_backward(a, s), s);
 }
