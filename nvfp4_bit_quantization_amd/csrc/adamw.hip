@@ -29,43 +29,52 @@ __device__ __forceinline__ int block_exponent(float top) {
   return e > -126 ? e : -126;
 }
 
-// |x| / 2^e as an E4M3 code: steps of 2^(max(exponent, -6) - 3), whose count c
-// (at most 16, the next binade) adds to the code of the binade.  SR: a 16-bit
-// uniform.  positive: a non-zero x gives a non-zero code.
-template <bool SR>
-__device__ __forceinline__ uint32_t e4m3_code(float x, int e, uint32_t u16, bool positive) {
-  const float y = fabsf(x) * pow2(-e);
-  int ey = (int)(__float_as_uint(y) >> 23) - 127;
-  ey = ey > -6 ? ey : -6;
-  const float t = y * pow2(3 - ey);
-  float c = SR ? floorf(t + (float)u16 * 1.52587890625e-05f) : rintf(t);
-  if (positive && y > 0.0f) c = fmaxf(c, 1.0f);
-  return (uint32_t)((ey + 6) * 8 + (int)c) | (__float_as_uint(x) >> 31 << 7);
-}
-
-__device__ __forceinline__ float e4m3_signed(uint32_t c) { 
-  const float v = e4m3_value(c & 127u);
-  return c & 128u ? -v : v;
-}
-
-// 8 state elements: their codes and the quad's scale.  Lanes outside the
-// tensor hold zeros.
+// 8 state elements: their E4M3 codes under the quad's scale 2^e.  Lanes
+// outside the tensor hold zeros.  The gfx950 FP8 conversions round y = x / 2^e
+// (|y| <= 448) to nearest, or up iff the place of |y| between its neighbours,
+// in 2^-20, and the random operand's upper 20 bits sum to 2^20 or more.  With
+// the 16-bit uniform u in the upper half that is floor(|y| / step + u / 65536),
+// exactly (checked on the device over all binades).  positive: x >= 0, and what
+// is not zero is raised to the least E4M3 value before it is rounded, so that it
+// cannot vanish.
 template <bool SR>
 __device__ __forceinline__ uint2 encode8(const float x[8], const uint32_t w[4], bool positive, int *e) {
   float top = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
   *e = block_exponent(quad_max(top));
-  uint32_t q[2] = {0u, 0u};
+  const float inv = pow2(-*e);
+  int q[2] = {0, 0};
+  float y[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) q[j >> 2] |= e4m3_code<SR>(x[j], *e, SR ? u16_of(w, j) : 0u, positive) << (8 * (j & 3));
-  return make_uint2(q[0], q[1]);
+  for (int j = 0; j < 8; ++j) {
+    y[j] = x[j] * inv;
+    if (positive) y[j] = x[j] > 0.0f ? fmaxf(y[j], 0.001953125f) : 0.0f;
+  }
+  if constexpr (SR) {
+    q[0] = __builtin_amdgcn_cvt_sr_fp8_f32(y[0], w[0] << 16, q[0], 0);
+    q[0] = __builtin_amdgcn_cvt_sr_fp8_f32(y[1], w[0] & 0xFFFF0000u, q[0], 1);
+    q[0] = __builtin_amdgcn_cvt_sr_fp8_f32(y[2], w[1] << 16, q[0], 2);
+    q[0] = __builtin_amdgcn_cvt_sr_fp8_f32(y[3], w[1] & 0xFFFF0000u, q[0], 3);
+    q[1] = __builtin_amdgcn_cvt_sr_fp8_f32(y[4], w[2] << 16, q[1], 0);
+    q[1] = __builtin_amdgcn_cvt_sr_fp8_f32(y[5], w[2] & 0xFFFF0000u, q[1], 1);
+    q[1] = __builtin_amdgcn_cvt_sr_fp8_f32(y[6], w[3] << 16, q[1], 2);
+    q[1] = __builtin_amdgcn_cvt_sr_fp8_f32(y[7], w[3] & 0xFFFF0000u, q[1], 3);
+  } else {
+    q[0] = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], q[0], false);
+    q[0] = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], q[0], true);
+    q[1] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4], y[5], q[1], false);
+    q[1] = __builtin_amdgcn_cvt_pk_fp8_f32(y[6], y[7], q[1], true);
+  }
+  return make_uint2((uint32_t)q[0], (uint32_t)q[1]);
 }
 
 __device__ __forceinline__ void decode8(uint2 q, uint32_t scale, float x[8]) {
   const float s = __builtin_ldexpf(1.0f, (int)scale - 127);
+  const f32x2 v[4] = {__builtin_amdgcn_cvt_pk_f32_fp8((int)q.x, false), __builtin_amdgcn_cvt_pk_f32_fp8((int)q.x, true),
+                      __builtin_amdgcn_cvt_pk_f32_fp8((int)q.y, false), __builtin_amdgcn_cvt_pk_f32_fp8((int)q.y, true)};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) x[j] = e4m3_signed(((j < 4 ? q.x : q.y) >> (8 * (j & 3))) & 255u) * s;
+  for (int j = 0; j < 8; ++j) x[j] = v[j >> 1][j & 1] * s;
 }
 
 // 8 elements, `have` of them in the tensor
@@ -141,8 +150,10 @@ __device__ __forceinline__ float step8(const AdamArgs &a, const AdamTensor &t, f
     const float x = g[j] * gs;
     m[j] = m[j] * a.beta1 + x * a.one_minus_beta1;
     v[j] = v[j] * a.beta2 + x * x * a.one_minus_beta2;
-    r[j] = sqrtf(v[j]);
-    p[j] = p[j] * t.keep - a.lr * ((m[j] * a.correct1) / (r[j] * a.correct2 + a.eps));
+    // the square root and reciprocal instructions: 1 unit in the last place
+    // each, next to the update's ten other roundings
+    r[j] = __builtin_amdgcn_sqrtf(v[j]);
+    p[j] = p[j] * t.keep - a.lr * ((m[j] * a.correct1) * __builtin_amdgcn_rcpf(r[j] * a.correct2 + a.eps));
   }
   if constexpr (SR && sizeof(TP) == 2) {
     draw(a, t.index, 2u, i0 >> 3, w);
