@@ -39,16 +39,6 @@ __device__ __forceinline__ f32x16 zero16() {
 // row of result register i in half h
 __device__ __forceinline__ int row_of(int i, int h) { return 8 * (i >> 2) + 4 * h + (i & 3); }
 
-// the larger, and the sum, of a lane's value and the other half's
-__device__ __forceinline__ float half_max(float v) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-__device__ __forceinline__ float half_sum(float v) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-
 // ------------------------------------------------------------ sequences ----
 struct Seq {
   int64_t q0, k0;  // first tokens
@@ -319,7 +309,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
     float m = fmaxf(p[0][0], p[1][0]);
 #pragma unroll
     for (int i = 1; i < 16; ++i) m = fmaxf(m, fmaxf(p[0][i], p[1][i]));
-    m = half_max(m) * c2;
+    m = swapped32(m, [](float x, float y) { return fmaxf(x, y); }) * c2;
     // The exponents' reference follows the maximum only when that has risen by
     // more than 8 (a factor of 256 in p): results do not depend on it
     if (__any(m > top + 8.0f)) {
@@ -347,7 +337,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
         for (int dt = 0; dt < D / 32; ++dt) o[dt] = mfma(in.cols(kB, u * 32 + c * 16, dt), b, o[dt]);
       }
   }
-  sum = half_sum(sum);
+  sum = swapped32(sum, [](float x, float y) { return x + y; });
   if (mine >= s.nq) return;
   const bool none = sum == 0.0f;
   store_cols<D>(at(a.o, s.bq, s.q0 + mine, w.head), o, none ? 0.0f : 1.0f / sum, a.dim, h);

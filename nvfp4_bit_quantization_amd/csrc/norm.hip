@@ -3,7 +3,7 @@
 //
 // A row is held in registers: TPR threads (whole waves) each hold V groups of
 // 8 elements, so that mean, centred second moment and the result come from one
-// read of the row.  Rows of up to 2048 elements belong to one wave each (no
+// read of the row.  Rows of up to 1024 elements belong to one wave each (no
 // LDS), longer ones to up to 16 waves that exchange their sums through LDS.
 // Workgroups walk over rows with the weights kept in registers.
 #include "train_device.hpp"
@@ -20,27 +20,66 @@ __device__ __forceinline__ int64_t column(int v, int j, int t, int tpr) {
   return VEC ? (int64_t)(v * tpr + t) * 8 + j : (int64_t)(v * 8 + j) * tpr + t;
 }
 
-// a thread's share of a row, zero outside [0, cols)
+// a thread's share of a row as it stands in memory, zero outside [0, cols):
+// what is loaded ahead for the next row
+template <typename T>
+struct Group;  // 8 elements
+template <>
+struct Group<uint16_t> {
+  uint4 q;
+  __device__ __forceinline__ void load(const uint16_t *p) { q = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load1(int j, const uint16_t *p, bool in) {
+    const uint32_t x = in ? *p : 0u;
+    uint32_t &w = (j >> 1) == 0 ? q.x : (j >> 1) == 1 ? q.y : (j >> 1) == 2 ? q.z : q.w;
+    w = j & 1 ? w | x << 16 : x;
+  }
+  __device__ __forceinline__ float at(int j) const { return bf16_at(q, j); }
+};
+template <>
+struct Group<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float *p) {
+    a = reinterpret_cast<const float4 *>(p)[0];
+    b = reinterpret_cast<const float4 *>(p)[1];
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load1(int j, const float *p, bool in) {
+    const float x = in ? *p : 0.0f;
+    (j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : j == 3 ? a.w : j == 4 ? b.x : j == 5 ? b.y : j == 6 ? b.z : b.w) = x;
+  }
+  __device__ __forceinline__ float at(int j) const {
+    return j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : j == 3 ? a.w : j == 4 ? b.x : j == 5 ? b.y : j == 6 ? b.z : b.w;
+  }
+};
+
 template <bool VEC, int V, typename T>
-__device__ __forceinline__ void load_row(const T *row, int cols, int t, int tpr, float out[V][8]) {
+__device__ __forceinline__ void fetch_row(const T *row, int cols, int t, int tpr, Group<T> g[V]) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if constexpr (VEC) {
       const int64_t c = column<true, V>(v, 0, t, tpr);
-      if (c < cols) {
-        load8(row + c, out[v]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) out[v][j] = 0.0f;
-      }
+      if (c < cols)
+        g[v].load(row + c);
+      else
+        g[v].zero();
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int64_t c = column<false, V>(v, j, t, tpr);
-        out[v][j] = c < cols ? load1(row + c) : 0.0f;
+        g[v].load1(j, row + c, c < cols);
       }
     }
   }
+}
+template <bool VEC, int V, typename T>
+__device__ __forceinline__ void load_row(const T *row, int cols, int t, int tpr, float out[V][8]) {
+  Group<T> g[V];
+  fetch_row<VEC, V>(row, cols, t, tpr, g);
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) out[v][j] = g[v].at(j);
 }
 
 template <bool VEC, int V, typename T>
@@ -68,24 +107,25 @@ __device__ __forceinline__ void load_weight(const void *w, int bf16, int cols, i
     load_row<VEC, V>((const float *)w, cols, t, tpr, out);
 }
 
-// the sum of v over the waves of a row; `slot`: LDS of 16 floats
-__device__ __forceinline__ float row_sum(float v, int waves, float *slot) {
-  v = wave_sum(v);
-  if (waves == 1) return v;
-  if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = 0.0f;
-  for (int w = 0; w < waves; ++w) v += slot[w];
-  return v;
-}
-
-// blockDim = (TPR, rows per workgroup); more than one row only when TPR = 64
+// blockDim = (TPR, rows per workgroup); more than one row only when TPR = 64.
+// The next row is loaded while this one is worked on.  Each wave takes the mean
+// of its part and the sum of squares about that; one exchange joins them (n_w
+// elements, mean_w, q_w to a wave):
+//   mean = sum n_w mean_w / n,  q = sum q_w + n_w (mean_w - mean)^2
 template <typename TX, typename TY, bool VEC, int V, int NT>
 __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
-  __shared__ float slots[2][16];
-  const int t = threadIdx.x, tpr = blockDim.x, waves = tpr >> 6;
+  __shared__ float2 slots[2][16];
+  __shared__ float counts[16];
+  const int t = threadIdx.x, tpr = blockDim.x, waves = tpr >> 6, wave = t >> 6;
   const int cols = (int)a.cols;
   const float inv = 1.0f / (float)cols;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  Group<TX> gx[V], gr[V];
+  if (r < a.rows) {
+    fetch_row<VEC, V>((const TX *)a.x + r * a.ld_x, cols, t, tpr, gx);
+    if (a.residual) fetch_row<VEC, V>((const TX *)a.residual + r * a.ld_residual, cols, t, tpr, gr);
+  }
   float w[V][8], b[V][8], top = 0.0f;
   load_weight<VEC, V>(a.weight, a.w_dtype == NVFP4_BF16, cols, t, tpr, w);
   if (a.bias) {
@@ -96,34 +136,60 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) b[v][j] = 0.0f;
   }
-  for (int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; r < a.rows; r += (int64_t)gridDim.x * blockDim.y) {
+  int mine = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mine += column<VEC, V>(v, j, t, tpr) < cols;
+  const float count = wave_sum((float)mine), inv_w = count > 0.0f ? 1.0f / count : 0.0f;
+  if (waves > 1 && (t & 63) == 0) counts[wave] = count;
+  int turn = 0;
+  for (; r < a.rows; r += step) {
     float x[V][8];
-    load_row<VEC, V>((const TX *)a.x + r * a.ld_x, cols, t, tpr, x);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[v][j] = gx[v].at(j);
     if (a.residual) {
-      float q[V][8];
-      load_row<VEC, V>((const TX *)a.residual + r * a.ld_residual, cols, t, tpr, q);
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[v][j] = rounded<TX>(x[v][j] + q[v][j]);
-      store_row<VEC, V>((TX *)a.sum + r * a.ld_sum, cols, t, tpr, x);
+        for (int j = 0; j < 8; ++j) x[v][j] = rounded<TX>(x[v][j] + gr[v].at(j));
     }
+    if (r + step < a.rows) {
+      fetch_row<VEC, V>((const TX *)a.x + (r + step) * a.ld_x, cols, t, tpr, gx);
+      if (a.residual) fetch_row<VEC, V>((const TX *)a.residual + (r + step) * a.ld_residual, cols, t, tpr, gr);
+    }
+    if (a.residual) store_row<VEC, V>((TX *)a.sum + r * a.ld_sum, cols, t, tpr, x);
     float s = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += x[v][j];
-    const float mean = row_sum(s, waves, slots[0]) * inv;
-    s = 0.0f;
+    float mean = wave_sum(s) * inv_w, q = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float d = column<VEC, V>(v, j, t, tpr) < cols ? x[v][j] - mean : 0.0f;
-        x[v][j] = d;
-        s = fmaf(d, d, s);
+        q = fmaf(d, d, q);
       }
-    const float rstd = 1.0f / sqrtf(row_sum(s, waves, slots[1]) * inv + a.eps);
+    q = wave_sum(q);
+    if (waves > 1) {
+      // two sets of slots in turn: a set is written again only after a barrier
+      // that every wave passed with its reads of it done
+      if ((t & 63) == 0) slots[turn][wave] = make_float2(mean, q);
+      __syncthreads();
+      mean = q = 0.0f;
+      for (int i = 0; i < waves; ++i) mean = fmaf(counts[i], slots[turn][i].x, mean);
+      mean *= inv;
+      for (int i = 0; i < waves; ++i) {
+        const float d = slots[turn][i].x - mean;
+        q += fmaf(counts[i] * d, d, slots[turn][i].y);
+      }
+      turn ^= 1;
+    }
+    const float rstd = 1.0f / sqrtf(fmaf(q, inv, a.eps));
     if (t == 0) {
       a.mean[r] = mean;
       a.rstd[r] = rstd;
@@ -132,17 +198,17 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float y = rounded<TY>(fmaf(x[v][j] * rstd, w[v][j], b[v][j]));
+        const float y = rounded<TY>(fmaf((x[v][j] - mean) * rstd, w[v][j], b[v][j]));
         x[v][j] = y;
-        top = fmaxf(top, fabsf(y));  // columns past the end hold 0
+        if (a.amax && column<VEC, V>(v, j, t, tpr) < cols) top = fmaxf(top, fabsf(y));
       }
     store_row<VEC, V>((TY *)a.y + r * a.ld_y, cols, t, tpr, x);
   }
   if (a.amax) fold_max(a.amax, top);
 }
 
-// The gradient: a row's two sums in one exchange; the sums over rows stay in
-// registers and are written once per workgroup, [blockIdx][dweight, dbias][cols].
+// The gradient: a row's two sums in one exchange, the next row loaded ahead;
+// the sums over rows stay in registers and are written once per workgroup, [blockIdx][dweight, dbias][cols].
 template <typename TX, typename TY, bool VEC, int V, int NT>
 __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_backward_args a, float *partials) {
   __shared__ float2 slots[2][16];
@@ -156,12 +222,31 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[v][j] = db[v][j] = 0.0f;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
+  int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  Group<TX> gx[V], gd[V];
+  Group<TY> gy[V];
+  float next_mean = 0.0f, next_rstd = 0.0f;
+  const auto fetch = [&](int64_t row) {
+    fetch_row<VEC, V>((const TX *)a.x + row * a.ld_x, cols, t, tpr, gx);
+    fetch_row<VEC, V>((const TY *)a.dy + row * a.ld_dy, cols, t, tpr, gy);
+    next_mean = a.mean[row];
+    next_rstd = a.rstd[row];
+  };
+  if (r < a.rows) fetch(r);
   int turn = 0;
-  for (int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; r < a.rows; r += (int64_t)gridDim.x * blockDim.y) {
+  for (; r < a.rows; r += step) {
     float x[V][8], g[V][8];
-    load_row<VEC, V>((const TX *)a.x + r * a.ld_x, cols, t, tpr, x);
-    load_row<VEC, V>((const TY *)a.dy + r * a.ld_dy, cols, t, tpr, g);
-    const float mean = a.mean[r], rstd = a.rstd[r];
+    const float mean = next_mean, rstd = next_rstd;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[v][j] = gx[v].at(j);
+        g[v][j] = gy[v].at(j);
+      }
+    if (a.dsum) fetch_row<VEC, V>((const TX *)a.dsum + r * a.ld_dsum, cols, t, tpr, gd);
+    if (r + step < a.rows) fetch(r + step);
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -196,18 +281,19 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[v][j] = rstd * (g[v][j] - fmaf(x[v][j], c2, c1));
     if (a.dsum) {
-      load_row<VEC, V>((const TX *)a.dsum + r * a.ld_dsum, cols, t, tpr, g);
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[v][j] += g[v][j];
+        for (int j = 0; j < 8; ++j) x[v][j] += gd[v].at(j);
     }
     store_row<VEC, V>((TX *)a.dx + r * a.ld_dx, cols, t, tpr, x);
+    if (a.amax) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (column<VEC, V>(v, j, t, tpr) < cols) top = fmaxf(top, fabsf(rounded<TX>(x[v][j])));
+        for (int j = 0; j < 8; ++j)
+          if (column<VEC, V>(v, j, t, tpr) < cols) top = fmaxf(top, fabsf(rounded<TX>(x[v][j])));
+    }
   }
   if (a.amax) fold_max(a.amax, top);
   if (!partials) return;
@@ -244,8 +330,17 @@ __global__ __launch_bounds__(1024) void layernorm_reduce_kernel(const float *par
   __shared__ float sums[16][64];
   const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
   float s = 0.0f;
-  if (c < 2 * cols)
-    for (int64_t p = threadIdx.y; p < parts; p += 16) s += partials[p * 2 * cols + c];
+  if (c < 2 * cols) {
+    int64_t p = threadIdx.y;
+    for (; p + 7 * 16 < parts; p += 8 * 16) {  // eight loads in flight
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = partials[(p + i * 16) * 2 * cols + c];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += v[i];
+    }
+    for (; p < parts; p += 16) s += partials[p * 2 * cols + c];
+  }
   sums[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
   if (threadIdx.y != 0 || c >= 2 * cols) return;
@@ -260,18 +355,25 @@ bool at16(const void *p, int64_t ld, int32_t dtype) {
   return ((uintptr_t)p & 15u) == 0 && ld % (dtype == NVFP4_BF16 ? 8 : 4) == 0;
 }
 
-// How a row of `cols` elements is split: groups of 8 per thread, threads per
-// row and rows per workgroup, and the workgroup size the kernel is built for.
+// How a row of `cols` elements is split: groups of 8 per thread, the workgroup
+// size the kernel is built for, and threads per row and rows per workgroup.
 struct Split {
   int v, nt;
   dim3 block;
+  int waves() const { return (int)(block.x * block.y) / 64; }
 };
 Split split_of(int64_t cols) {
   if (cols <= 512) return {1, 256, dim3(64, 4)};
   if (cols <= 1024) return {2, 512, dim3(64, 4)};
-  if (cols <= 2048) return {4, 256, dim3(64, 4)};
-  if (cols <= 8192) return {2, 512, dim3((unsigned)((cols + 1023) / 1024 * 64))};
+  if (cols <= 16384) return {2, cols <= 8192 ? 512 : 1024, dim3((unsigned)((cols + 1023) / 1024 * 64))};
   return {4, 1024, dim3((unsigned)((cols + 2047) / 2048 * 64))};
+}
+// Workgroups: what the 256 compute units hold at a time (by registers, 16
+// waves each, 12 of the gradient's), so that all run from the start and each
+// walks over its share of the rows.
+int64_t resident(const Split &p, int64_t rows, int waves) {
+  const int64_t groups = (rows + p.block.y - 1) / p.block.y, most = 256 * (waves / p.waves() > 1 ? waves / p.waves() : 1);
+  return groups < most ? groups : most;
 }
 
 template <typename TX, typename TY, bool VEC, int V, int NT>
@@ -287,10 +389,10 @@ template <typename TX, typename TY, bool VEC, typename A>
 void pick_split(const Split &p, const A &a, float *partials, unsigned grid, hipStream_t s) {
   if (p.v == 1)
     run<TX, TY, VEC, 1, 256>(a, partials, grid, p.block, s);
-  else if (p.v == 2)
+  else if (p.v == 2 && p.nt == 512)
     run<TX, TY, VEC, 2, 512>(a, partials, grid, p.block, s);
-  else if (p.nt == 256)
-    run<TX, TY, VEC, 4, 256>(a, partials, grid, p.block, s);
+  else if (p.v == 2)
+    run<TX, TY, VEC, 2, 1024>(a, partials, grid, p.block, s);
   else
     run<TX, TY, VEC, 4, 1024>(a, partials, grid, p.block, s);
 }
@@ -320,16 +422,12 @@ hipError_t launch_layernorm(const nvfp4_layernorm_args &a, hipStream_t s) {
   const bool vec = a.cols % 8 == 0 && at16(a.x, a.ld_x, a.x_dtype) && at16(a.y, a.ld_y, a.y_dtype) &&
                    at16(a.weight, 0, a.w_dtype) && at16(a.bias, 0, a.w_dtype) &&
                    (!a.residual || (at16(a.residual, a.ld_residual, a.x_dtype) && at16(a.sum, a.ld_sum, a.x_dtype)));
-  const int64_t groups = (a.rows + p.block.y - 1) / p.block.y;
-  const unsigned grid = (unsigned)(groups < 2048 ? groups : 2048);
-  pick(vec, p, a, nullptr, grid, s);
+  pick(vec, p, a, nullptr, (unsigned)resident(p, a.rows, 16), s);
   return hipGetLastError();
 }
 
 int64_t layernorm_backward_parts(int64_t rows, int64_t cols) {
-  const Split p = split_of(cols);
-  const int64_t groups = (rows + p.block.y - 1) / p.block.y;
-  return groups < 512 ? groups : 512;
+  return resident(split_of(cols), rows, 12);
 }
 
 hipError_t launch_layernorm_backward(const nvfp4_layernorm_backward_args &a, float *partials, hipStream_t s) {

@@ -51,18 +51,29 @@ template <>
 __device__ __forceinline__ float rounded<float>(float v) { return v; }
 
 // Sum and maximum over the 64 lanes, in every lane: four DPP steps inside the
-// rows of 16 lanes, then the rows by two lane permutes.
+// rows of 16 lanes, then the row and half swaps (which hand both rows' or
+// halves' values to both).
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+template <typename F>
+__device__ __forceinline__ float swapped16(float v, F f) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+template <typename F>
+__device__ __forceinline__ float swapped32(float v, F f) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 __device__ __forceinline__ float wave_sum(float v) {
   v += dpp<0x128>(v);  // row_ror:8
   v += dpp<0x124>(v);
   v += dpp<0x122>(v);
   v += dpp<0x121>(v);
-  v += __shfl_xor(v, 16);
-  v += __shfl_xor(v, 32);
+  v = swapped16(v, [](float a, float b) { return a + b; });
+  v = swapped32(v, [](float a, float b) { return a + b; });
   return v;
 }
 __device__ __forceinline__ float wave_max(float v) {
@@ -70,8 +81,8 @@ __device__ __forceinline__ float wave_max(float v) {
   v = fmaxf(v, dpp<0x124>(v));
   v = fmaxf(v, dpp<0x122>(v));
   v = fmaxf(v, dpp<0x121>(v));
-  v = fmaxf(v, __shfl_xor(v, 16));
-  v = fmaxf(v, __shfl_xor(v, 32));
+  v = swapped16(v, [](float a, float b) { return fmaxf(a, b); });
+  v = swapped32(v, [](float a, float b) { return fmaxf(a, b); });
   return v;
 }
 
