@@ -23,6 +23,8 @@ typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
 
 constexpr int kThreads = 256;
 constexpr int kTile = 64;               // rows of a staged tile
+// instruction classes of sched_group_barrier
+constexpr int kValu = 0x2, kMfma = 0x8, kDsRead = 0x100;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kLow = -1e30f;          // below every score; finite, so that differences stay numbers
@@ -290,13 +292,20 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
       fetch_tile<D>(vh, a.v.st, k0 + kTile, s.nk, chunks, lds_addr(lds) + (uint32_t)(stage ^ 1) * 2 * kB + kB, wave, lane);
     }
     if (k0 >= any_hi || k0 + kTile <= any_lo) continue;  // nothing in the wave's sight
-    f32x16 p[2];
+    f32x16 p[2] = {zero16(), zero16()};
+    bf16x8 kf[2 * (D / 16)];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      p[u] = zero16();
+    for (int c = 0; c < 2 * (D / 16); ++c) kf[c] = in.rows(0, (c & 1) * 32, c >> 1);
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) p[u] = mfma(in.rows(0, u * 32, c), q[c], p[u]);
+    for (int c = 0; c < 2 * (D / 16); ++c) p[c & 1] = mfma(kf[c], q[c >> 1], p[c & 1]);
+    // half of the operands ahead of the products, the others between them
+    __builtin_amdgcn_sched_group_barrier(kDsRead, D / 16, 0);
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+      __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
     }
+    __builtin_amdgcn_sched_group_barrier(kMfma, D / 16, 0);
     if (k0 + kTile > all_hi || k0 < all_lo) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
@@ -321,21 +330,36 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[dt][i] *= f;
     }
+    bf16x8 vf[4][D / 32];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        p[u][i] = __builtin_amdgcn_exp2f(fmaf(p[u][i], c2, -top));
-        sum += p[u][i];
+      for (int dt = 0; dt < D / 32; ++dt) vf[c][dt] = in.cols(kB, c * 16, dt);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+#pragma unroll
+      for (int i = 8 * (c & 1); i < 8 * (c & 1) + 8; ++i) {
+        p[c >> 1][i] = __builtin_amdgcn_exp2f(fmaf(p[c >> 1][i], c2, -top));
+        sum += p[c >> 1][i];
       }
+      const bf16x8 b = pack8(p[c >> 1], 8 * (c & 1));
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+      for (int dt = 0; dt < D / 32; ++dt) o[dt] = mfma(vf[c][dt], b, o[dt]);
+    }
+    // the first 16 keys' operands and probabilities, then each 16 keys'
+    // products between the next ones'
+    __builtin_amdgcn_sched_group_barrier(kDsRead, D / 16, 0);
+    __builtin_amdgcn_sched_group_barrier(kValu, 28, 0);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const bf16x8 b = pack8(p[u], 8 * c);
+    for (int c = 0; c < 3; ++c) {
 #pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt) o[dt] = mfma(in.cols(kB, u * 32 + c * 16, dt), b, o[dt]);
+      for (int dt = 0; dt < D / 32; ++dt) {
+        __builtin_amdgcn_sched_group_barrier(kDsRead, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kValu, 28 / (D / 32), 0);
       }
+    }
+    __builtin_amdgcn_sched_group_barrier(kMfma, D / 32, 0);
   }
   sum = swapped32(sum, [](float x, float y) { return x + y; });
   if (mine >= s.nq) return;
