@@ -96,17 +96,18 @@ __device__ __forceinline__ void sight(const AttnArgs &a, int i, int nk, int off,
 template <int D>
 struct Tile {
   static constexpr int kChunks = D / 8, kSegRows = 64 / kChunks;
-  static constexpr uint32_t kSeg = 1024 + 16, kBytes = kTile / kSegRows * kSeg;
+  static constexpr uint32_t kSeg = 1024 + 16;
+  static constexpr uint32_t bytes(int rows) { return (uint32_t)(rows / kSegRows) * kSeg; }
   static __device__ __forceinline__ uint32_t spread(uint32_t r) {
     return D == 128 ? (r & 3u) << 2 : ((r >> 1) & 1u) << 2 | ((r >> 2) & 1u) << 1;
   }
 };
 
-// Transfer rows row0 .. row0 + 63 of a head (rows past `rows` repeat the last
-// one, chunks past head_dim the first: their products are masked, or meet
-// zeros) into the tile at LDS address lds.  Each of four waves fills D / 32
-// segments.
-template <int D>
+// Transfer rows row0 .. row0 + R - 1 of a head (rows past `rows` repeat the
+// last one, chunks past head_dim the first: their products are masked, or meet
+// zeros) into the tile at LDS address lds.  Each of four waves fills a quarter
+// of its segments.
+template <int D, int R>
 __device__ __forceinline__ void fetch_tile(const uint16_t *head, int64_t stride, int row0, int rows, int chunks,
                                            uint32_t lds, int wave, int lane) {
   typedef Tile<D> T;
@@ -116,17 +117,18 @@ __device__ __forceinline__ void fetch_tile(const uint16_t *head, int64_t stride,
   uint32_t c = ((uint32_t)lane % T::kChunks) ^ T::spread(r);
   c = (int)c < chunks ? c * 16u : 0u;
   const int left = rows - row0;
-  if (left >= kTile) {
+  constexpr int kSegs = R / T::kSegRows / 4;
+  if (left >= R) {
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const int seg = wave * (D / 32) + i;
+    for (int i = 0; i < kSegs; ++i) {
+      const int seg = wave * kSegs + i;
       dma16(uniform_ptr(base + (uint64_t)(seg * T::kSegRows) * pitch), r * pitch + c,
             __builtin_amdgcn_readfirstlane(lds + (uint32_t)seg * T::kSeg));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const int seg = wave * (D / 32) + i, row = seg * T::kSegRows + (int)r;
+    for (int i = 0; i < kSegs; ++i) {
+      const int seg = wave * kSegs + i, row = seg * T::kSegRows + (int)r;
       dma16(base, (uint32_t)(row < left ? row : left - 1) * pitch + c,
             __builtin_amdgcn_readfirstlane(lds + (uint32_t)seg * T::kSeg));
     }
@@ -164,6 +166,9 @@ struct Reads {
     const uint32_t a = row[D == 128 ? c >> 1 : c] + tile + (uint32_t)(r0 / Tile<D>::kSegRows) * Tile<D>::kSeg +
                        (D == 128 ? (c & 1) * 32u : 0u);
     return *(const __attribute__((address_space(3))) bf16x8 *)a;
+  }
+  __device__ __forceinline__ void set_row(int c, bf16x8 v) const {
+    *(__attribute__((address_space(3))) bf16x8 *)(row[D == 128 ? c >> 1 : c] + (D == 128 ? (c & 1) * 32u : 0u)) = v;
   }
   // A operand from the transposed tile: row = element 32 dt + n, inner index =
   // tile rows r0 + 4 h .. and r0 + 8 + 4 h .. (r0 = 0, 16, 32, 48)
@@ -242,8 +247,8 @@ constexpr int kQueries = 128;  // queries of a workgroup: 32 per wave
 // Running maximum and sum per query stay in its two lanes.
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
-  __shared__ __align__(16) uint8_t lds[4 * Tile<D>::kBytes];
-  constexpr uint32_t kB = Tile<D>::kBytes;
+  __shared__ __align__(16) uint8_t lds[4 * Tile<D>::bytes(kTile)];
+  constexpr uint32_t kB = Tile<D>::bytes(kTile);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
   const int group = a.heads / a.kv_heads, tiles = (a.q_len + kQueries - 1) / kQueries;
   Work w = work_of(a, tiles, group);
@@ -280,16 +285,16 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
 
   const int t0 = begin / kTile, t1 = end > begin ? (end + kTile - 1) / kTile : t0;
   if (t0 < t1) {
-    fetch_tile<D>(kh, a.k.st, t0 * kTile, s.nk, chunks, lds_addr(lds), wave, lane);
-    fetch_tile<D>(vh, a.v.st, t0 * kTile, s.nk, chunks, lds_addr(lds) + kB, wave, lane);
+    fetch_tile<D, kTile>(kh, a.k.st, t0 * kTile, s.nk, chunks, lds_addr(lds), wave, lane);
+    fetch_tile<D, kTile>(vh, a.v.st, t0 * kTile, s.nk, chunks, lds_addr(lds) + kB, wave, lane);
   }
   for (int t = t0; t < t1; ++t) {
     const int stage = (t - t0) & 1, k0 = t * kTile;
     if (t > t0) in.move(stage ? 2 * kB : 0u - 2 * kB);
     tile_barrier();  // this tile is in LDS, and every wave has read the previous one
     if (t + 1 < t1) {
-      fetch_tile<D>(kh, a.k.st, k0 + kTile, s.nk, chunks, lds_addr(lds) + (uint32_t)(stage ^ 1) * 2 * kB, wave, lane);
-      fetch_tile<D>(vh, a.v.st, k0 + kTile, s.nk, chunks, lds_addr(lds) + (uint32_t)(stage ^ 1) * 2 * kB + kB, wave, lane);
+      fetch_tile<D, kTile>(kh, a.k.st, k0 + kTile, s.nk, chunks, lds_addr(lds) + (uint32_t)(stage ^ 1) * 2 * kB, wave, lane);
+      fetch_tile<D, kTile>(vh, a.v.st, k0 + kTile, s.nk, chunks, lds_addr(lds) + (uint32_t)(stage ^ 1) * 2 * kB + kB, wave, lane);
     }
     if (k0 >= any_hi || k0 + kTile <= any_lo) continue;  // nothing in the wave's sight
     f32x16 p[2] = {zero16(), zero16()};
@@ -371,7 +376,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
 }
 
 // ------------------------------------------------------------- gradient ----
-// delta = sum_d do * o, 16 lanes to a row; and lse in powers of two beside it
+// -delta = -sum_d do * o, 16 lanes to a row, and -lse / scale beside it: what
+// the products' accumulators start from
 __global__ __launch_bounds__(kThreads) void attention_delta_kernel(AttnArgs a) {
   const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);  // (sequence, query) or token
   const int head = blockIdx.y, c = threadIdx.x & 15;
@@ -390,9 +396,9 @@ __global__ __launch_bounds__(kThreads) void attention_delta_kernel(AttnArgs a) {
   v += dpp<0x121>(v);
   if (row < a.total_q && c == 0) {
     const int64_t i = (int64_t)head * a.total_q + row;
-    a.delta[i] = v;
-    const float lse = a.lse[i] * kLog2e;
-    a.lse2[i] = lse == -INFINITY ? 0.0f : lse;  // all of such a row is masked: exp2(-inf - 0) = 0
+    a.delta[i] = -v;
+    const float lse = a.lse[i];
+    a.lse2[i] = lse == -INFINITY ? 0.0f : -lse / a.scale;  // all of such a row is masked: exp2(-inf - 0) = 0
   }
 }
 
@@ -400,8 +406,8 @@ __global__ __launch_bounds__(kThreads) void attention_delta_kernel(AttnArgs a) {
 // dQ^T = K^T dS^T.
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
-  __shared__ __align__(16) uint8_t lds[4 * Tile<D>::kBytes];
-  constexpr uint32_t kB = Tile<D>::kBytes;
+  __shared__ __align__(16) uint8_t lds[4 * Tile<D>::bytes(kTile)];
+  constexpr uint32_t kB = Tile<D>::bytes(kTile);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
   const int group = a.heads / a.kv_heads, tiles = (a.q_len + kQueries - 1) / kQueries;
   Work w = work_of(a, tiles, group);
@@ -422,7 +428,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
     g[c] = load_row(grow, c, chunks, h);
   }
   const int64_t stat = (int64_t)w.head * a.total_q + first_row(a, s, w.b) + qi;
-  const float lse2 = a.lse2[stat], delta = a.delta[stat];
+  const float start = a.lse2[stat] * (a.scale * kLog2e), delta = a.delta[stat];
 
   int lo, hi, unused, begin, end;
   sight(a, qi, s.nk, off, lo, hi);
@@ -440,16 +446,16 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
   Reads<D> in(lane, lds_addr(lds));
   const int t0 = begin / kTile, t1 = end > begin ? (end + kTile - 1) / kTile : t0;
   if (t0 < t1) {
-    fetch_tile<D>(kh, a.k.st, t0 * kTile, s.nk, chunks, lds_addr(lds), wave, lane);
-    fetch_tile<D>(vh, a.v.st, t0 * kTile, s.nk, chunks, lds_addr(lds) + kB, wave, lane);
+    fetch_tile<D, kTile>(kh, a.k.st, t0 * kTile, s.nk, chunks, lds_addr(lds), wave, lane);
+    fetch_tile<D, kTile>(vh, a.v.st, t0 * kTile, s.nk, chunks, lds_addr(lds) + kB, wave, lane);
   }
   for (int t = t0; t < t1; ++t) {
     const int stage = (t - t0) & 1, k0 = t * kTile;
     if (t > t0) in.move(stage ? 2 * kB : 0u - 2 * kB);
     tile_barrier();
     if (t + 1 < t1) {
-      fetch_tile<D>(kh, a.k.st, k0 + kTile, s.nk, chunks, lds_addr(lds) + (uint32_t)(stage ^ 1) * 2 * kB, wave, lane);
-      fetch_tile<D>(vh, a.v.st, k0 + kTile, s.nk, chunks, lds_addr(lds) + (uint32_t)(stage ^ 1) * 2 * kB + kB, wave, lane);
+      fetch_tile<D, kTile>(kh, a.k.st, k0 + kTile, s.nk, chunks, lds_addr(lds) + (uint32_t)(stage ^ 1) * 2 * kB, wave, lane);
+      fetch_tile<D, kTile>(vh, a.v.st, k0 + kTile, s.nk, chunks, lds_addr(lds) + (uint32_t)(stage ^ 1) * 2 * kB + kB, wave, lane);
     }
     if (k0 >= any_hi || k0 + kTile <= any_lo) continue;
     const bool masked = k0 + kTile > all_hi || k0 < all_lo;
@@ -468,7 +474,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) d = mfma(in.rows(kB, u * 32, c), g[c], d);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], c2, -lse2)) * (d[i] - delta);
+      for (int i = 0; i < 16; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], c2, start)) * (d[i] + delta);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const bf16x8 b = pack8(p, 8 * c);
@@ -482,13 +488,18 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
 
 // dK, dV: a wave holds 32 keys as columns; scores = Q K^T, dP = dO V^T,
 // dV^T = dO^T P, dK^T = Q^T dS, summed over the query heads of the key head.
+// The keys' operands stay in registers and the values' in LDS: with both in
+// registers nothing is left of the 256 that two waves per SIMD have each to
+// read operands ahead.  Queries come in tiles of 32 rows, so that two
+// workgroups fit a compute unit's LDS.
 constexpr int kKeys = 128;  // keys of a workgroup
+constexpr int kRows = 32;   // queries of a tile
 
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttnArgs a) {
-  __shared__ __align__(16) uint8_t lds[4 * Tile<D>::kBytes];
-  constexpr uint32_t kB = Tile<D>::kBytes;
-  __shared__ __align__(16) float stats[2][2][kTile];
+  constexpr uint32_t kB = Tile<D>::bytes(kRows), kV = Tile<D>::bytes(kKeys);
+  __shared__ __align__(16) uint8_t lds[4 * kB + kV];
+  __shared__ __align__(16) float stats[2][2][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
   const int group = a.heads / a.kv_heads, tiles = (a.k_len + kKeys - 1) / kKeys;
   Work w = work_of(a, tiles, 1);
@@ -504,23 +515,26 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttnArgs a) 
   const int chunks = a.dim / 8;
 
   const int mine = first + wave * 32 + (lane & 31), ki = mine < s.nk ? mine : s.nk - 1;
-  bf16x8 k[D / 16], v[D / 16];
+  bf16x8 k[D / 16];
   const uint16_t *krow = at(a.k, s.bk, s.k0 + ki, hk), *vrow = at(a.v, s.bk, s.k0 + ki, hk);
+  const uint32_t v_at = lds_addr(lds) + 4 * kB + (uint32_t)wave * Tile<D>::bytes(32);
+  Reads<D> in(lane, lds_addr(lds));
+  const Reads<D> values(lane, v_at);  // the wave's own 32 rows, written and read by it alone
 #pragma unroll
   for (int c = 0; c < D / 16; ++c) {
     k[c] = load_row(krow, c, chunks, h);
-    v[c] = load_row(vrow, c, chunks, h);
+    values.set_row(c, load_row(vrow, c, chunks, h));
   }
   // the queries [lo, hi) that see key j: j - off <= i < j - off + window, with causal
   const auto seen_by = [&](int j, int &lo, int &hi) {
     lo = a.causal ? (int)clamp64((int64_t)j - off, 0, s.nq) : 0;
     hi = a.window ? (int)clamp64((int64_t)j - off + a.window, 0, s.nq) : s.nq;
   };
-  int begin, end, any_lo, any_hi, all_lo, all_hi, unused;
+  int begin, end, all_lo, all_hi, unused;
   seen_by(first, begin, unused);
   seen_by(last, unused, end);
-  seen_by(first + wave * 32, any_lo, all_hi);
-  seen_by(first + wave * 32 + 31, all_lo, any_hi);
+  seen_by(first + wave * 32, unused, all_hi);
+  seen_by(first + wave * 32 + 31, all_lo, unused);
   f32x16 dk[D / 32], dv[D / 32];
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt) {
@@ -528,13 +542,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttnArgs a) 
     dv[dt] = zero16();
   }
   const float c2 = a.scale * kLog2e;
-  const int t0 = begin / kTile, t1 = end > begin ? (end + kTile - 1) / kTile : t0;
+  const int t0 = begin / kRows, t1 = end > begin ? (end + kRows - 1) / kRows : t0;
   const int64_t row0 = first_row(a, s, w.b);
   const auto fetch = [&](int head, int t, int stage) {
-    const int i0 = t * kTile;
+    const int i0 = t * kRows;
     const uint32_t to = lds_addr(lds) + (uint32_t)stage * 2 * kB;
-    fetch_tile<D>(at(a.q, s.bq, s.q0, head), a.q.st, i0, s.nq, chunks, to, wave, lane);
-    fetch_tile<D>(at(a.d_o, s.bq, s.q0, head), a.d_o.st, i0, s.nq, chunks, to + kB, wave, lane);
+    fetch_tile<D, kRows>(at(a.q, s.bq, s.q0, head), a.q.st, i0, s.nq, chunks, to, wave, lane);
+    fetch_tile<D, kRows>(at(a.d_o, s.bq, s.q0, head), a.d_o.st, i0, s.nq, chunks, to + kB, wave, lane);
     if (wave < 2) {
       const float *src = (wave ? a.delta : a.lse2) + (int64_t)head * a.total_q + row0 + i0;
       const int left = s.nq - i0 - 1;
@@ -542,12 +556,11 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttnArgs a) 
            __builtin_amdgcn_readfirstlane(lds_addr(stats[stage][wave])));
     }
   };
-  Reads<D> in(lane, lds_addr(lds));
   int head = hk * group, t = t0, stage = 0;
   bool more = t0 < t1;
   if (more) fetch(head, t, 0);
   while (more) {
-    const int i0 = t * kTile;
+    const int i0 = t * kRows;
     tile_barrier();  // this tile is in LDS, and every wave has read the previous one
     if (++t == t1) {
       t = t0;
@@ -555,47 +568,71 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttnArgs a) 
     }
     more = head < (hk + 1) * group;
     if (more) fetch(head, t, stage ^ 1);
-    if (i0 < any_hi && i0 + kTile > any_lo) {
-      const bool masked = i0 + kTile > all_hi || i0 < all_lo;
+    // the accumulators start from -lse / scale and -delta
+    constexpr int kN = D / 16;
+    f32x16 p, d;
+    int l = lane;
+    asm volatile("" : "+v"(l));  // what is formed of it stays out of registers between tiles
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        f32x16 p = zero16(), d = zero16();
+    for (int b = 0; b < 4; ++b) {
+      const float4 x = *reinterpret_cast<const float4 *>(&stats[stage][0][8 * b + 4 * (l >> 5)]);
+      const float4 y = *reinterpret_cast<const float4 *>(&stats[stage][1][8 * b + 4 * (l >> 5)]);
+      p[4 * b] = x.x, p[4 * b + 1] = x.y, p[4 * b + 2] = x.z, p[4 * b + 3] = x.w;
+      d[4 * b] = y.x, d[4 * b + 1] = y.y, d[4 * b + 2] = y.z, d[4 * b + 3] = y.w;
+    }
+    // Operands are read two steps ahead of their products.  The order below
+    // is the one wanted; scheduling stays within a step.
+    bf16x8 qa[kN], ga[kN], va[kN], t[2 * kN];
+    const auto read_step = [&](int c) {
+      qa[c] = in.rows(0, 0, c);
+      ga[c] = in.rows(kB, 0, c);
+      va[c] = values.rows(0, 0, c);
+    };
+    // product 2 dt + w of the 16 queries c: w = 0: dV from dO, 1: dK from Q
+    const auto read_cols = [&](int i) { t[i] = in.cols(i & 1 ? 0 : kB, i / kN * 16, i % kN / 2); };
+    read_step(0);
+    read_step(1);
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) p = mfma(in.rows(0, u * 32, c), k[c], p);
-        if (masked) {
-          int l = lane, lo, hi;
-          asm volatile("" : "+v"(l));  // the limits are formed here, not kept in registers
-          seen_by(first + wave * 32 + (l & 31), lo, hi);
-          lo -= i0 + u * 32;
-          hi -= i0 + u * 32;
+    for (int c = 0; c < kN; ++c) {
+      if (c + 2 < kN)
+        read_step(c + 2);
+      else
+        read_cols(2 * (c + 2 - kN)), read_cols(2 * (c + 2 - kN) + 1);
+      p = mfma(qa[c], k[c], p);
+      d = mfma(ga[c], va[c], d);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (i0 + kRows > all_hi || i0 < all_lo) {
+      int lo, hi;
+      asm volatile("" : "+v"(l));
+      seen_by(first + wave * 32 + (l & 31), lo, hi);
+      lo -= i0;
+      hi -= i0;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) p[i] = row_of(i, l >> 5) < hi && row_of(i, l >> 5) >= lo ? p[i] : -INFINITY;
-        }
+      for (int i = 0; i < 16; ++i) p[i] = row_of(i, l >> 5) < hi && row_of(i, l >> 5) >= lo ? p[i] : -INFINITY;
+    }
+    const auto element = [&](int i) {
+      p[i] = __builtin_amdgcn_exp2f(p[i] * c2);
+      d[i] = p[i] * d[i];
+    };
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) d = mfma(in.rows(kB, u * 32, c), v[c], d);
+    for (int i = 0; i < 8; ++i) element(i);
+    bf16x8 b0 = pack8(p, 0), b1 = pack8(d, 0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const float4 lse = *reinterpret_cast<const float4 *>(&stats[stage][0][u * 32 + 8 * b + 4 * h]);
-          const float4 del = *reinterpret_cast<const float4 *>(&stats[stage][1][u * 32 + 8 * b + 4 * h]);
+    for (int i = 0; i < 2 * kN; ++i) {
+      if (i + 4 < 2 * kN) read_cols(i + 4);
+      f32x16 &acc = i & 1 ? dk[i % kN / 2] : dv[i % kN / 2];
+      acc = mfma(t[i], i & 1 ? b1 : b0, acc);
+      if (i < kN) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int i = 4 * b + r;
-            const float l = r == 0 ? lse.x : r == 1 ? lse.y : r == 2 ? lse.z : lse.w;
-            const float e = r == 0 ? del.x : r == 1 ? del.y : r == 2 ? del.z : del.w;
-            p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], c2, -l));
-            d[i] = p[i] * (d[i] - e);
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const bf16x8 b0 = pack8(p, 8 * c), b1 = pack8(d, 8 * c);
-#pragma unroll
-          for (int dt = 0; dt < D / 32; ++dt) {
-            dv[dt] = mfma(in.cols(kB, u * 32 + c * 16, dt), b0, dv[dt]);
-            dk[dt] = mfma(in.cols(0, u * 32 + c * 16, dt), b1, dk[dt]);
-          }
-        }
+        for (int j = 0; j < 8 / kN; ++j) element(8 + i * (8 / kN) + j);
       }
+      if (i == kN - 1) {
+        b0 = pack8(p, 8);
+        b1 = pack8(d, 8);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
     in.move(stage ? 0u - 2 * kB : 2 * kB);
     stage ^= 1;
