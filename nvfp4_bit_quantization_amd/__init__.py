@@ -540,6 +540,12 @@ def _raw_stream(stream, device_index) -> int:
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+def _floats(rows, cols, device):
+    """A new contiguous float32 [rows][cols] (the quickest of torch's ways)."""
+    import torch
+    return torch.empty_strided((rows, cols), (cols, 1), dtype=torch.float32, device=device)
+
+
 def _on_device(t, what) -> int:
     if not t.is_cuda:
         raise ValueError("%s: a device tensor is wanted" % what)
@@ -573,7 +579,8 @@ def _layernorm_inputs(x, weight, bias, residual, amax):
     if x.dim() != 2:
         raise ValueError("x: [rows][cols] is wanted")
     shape = x.shape
-    _matrix(x, shape, device, "x")
+    if x.stride(1) != 1 and shape[1] > 1:
+        raise ValueError("x: contiguous rows are wanted")
     if residual is not None:
         _matrix(residual, shape, device, "residual", x.dtype)
     _vector(weight, shape[1], device, "weight")
@@ -613,9 +620,9 @@ def layernorm(x, weight, bias=None, eps=1e-5, residual=None, amax=None, out_dtyp
             return layernorm(x, weight, bias, eps, residual, amax, out_dtype)
     import torch
     shape, device = _layernorm_inputs(x, weight, bias, residual, amax)
-    y = torch.empty(shape, dtype=out_dtype or x.dtype, device=x.device)
-    mean, rstd = torch.empty((2, shape[0]), dtype=torch.float32, device=x.device).unbind()
-    total = None if residual is None else torch.empty(shape, dtype=x.dtype, device=x.device)
+    y = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
+    mean, rstd = _floats(2, shape[0], x.device).unbind()
+    total = None if residual is None else torch.empty_like(x, memory_format=torch.contiguous_format)
     _layernorm(x, weight, bias, eps, y, mean.data_ptr(), rstd.data_ptr(), residual, total, amax, shape, device, None)
     return y, mean, rstd, total
 
@@ -626,7 +633,8 @@ def _layernorm_backward_inputs(dy, x, weight, mean, rstd, dsum, amax):
     if x.dim() != 2:
         raise ValueError("x: [rows][cols] is wanted")
     shape = x.shape
-    _matrix(x, shape, device, "x")
+    if x.stride(1) != 1 and shape[1] > 1:
+        raise ValueError("x: contiguous rows are wanted")
     _matrix(dy, shape, device, "dy")
     if dsum is not None:
         _matrix(dsum, shape, device, "dsum", x.dtype)
@@ -669,10 +677,10 @@ def layernorm_backward(dy, x, weight, mean, rstd, dsum=None, amax=None, workspac
             return layernorm_backward(dy, x, weight, mean, rstd, dsum, amax, workspace)
     import torch
     shape, device = _layernorm_backward_inputs(dy, x, weight, mean, rstd, dsum, amax)
-    dx = torch.empty(shape, dtype=x.dtype, device=x.device)
-    dweight, dbias = torch.empty((2, shape[1]), dtype=torch.float32, device=x.device).unbind()
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+    dweight, dbias = _floats(2, shape[1], x.device).unbind()
     if workspace is None:
-        workspace = torch.empty(lib().nvfp4_layernorm_backward_workspace_bytes(*shape), dtype=torch.uint8, device=x.device)
+        workspace = _floats(1, lib().nvfp4_layernorm_backward_workspace_bytes(*shape) // 4, x.device)
     elif workspace.get_device() != device:
         raise ValueError("workspace: a tensor on device %d is wanted" % device)
     _layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, dsum, amax, workspace, shape, device, None)
@@ -747,8 +755,8 @@ def attention(q, k, v, causal=True, window=0, scale=None, cu_q=None, cu_k=None, 
             return attention(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
     import torch
     s, sq, sk, heads, tokens, device = _attention_inputs(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
-    o = torch.empty(sq, dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((heads, tokens), dtype=torch.float32, device=q.device)
+    o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    lse = _floats(heads, tokens, q.device)
     _check(lib().nvfp4_attention(s, _heads(q, sq), _heads(k, sk), _heads(v, sk), _heads(o, sq), lse.data_ptr(),
                                  _raw_stream(None, device)), "nvfp4_attention")
     return o, lse
@@ -791,10 +799,11 @@ def attention_backward(d_o, q, k, v, o, lse, causal=True, window=0, scale=None, 
     _as(d_o, sq, device, "d_o")
     _as(o, sq, device, "o")
     _lse(lse, heads, tokens, device)
-    dq = torch.empty(sq, dtype=torch.bfloat16, device=q.device)
-    dk, dv = (torch.empty(sk, dtype=torch.bfloat16, device=q.device) for _ in range(2))
+    dense = torch.contiguous_format
+    dq, dk, dv = torch.empty_like(q, memory_format=dense), torch.empty_like(k, memory_format=dense), torch.empty_like(
+        v, memory_format=dense)
     if workspace is None:
-        workspace = torch.empty(lib().nvfp4_attention_backward_workspace_bytes(s), dtype=torch.uint8, device=q.device)
+        workspace = _floats(1, lib().nvfp4_attention_backward_workspace_bytes(s) // 4, q.device)
     elif workspace.get_device() != device:
         raise ValueError("workspace: a tensor on device %d is wanted" % device)
     _attention_backward(s, d_o, q, k, v, o, lse, dq, dk, dv, workspace, sq, sk, _raw_stream(None, device))

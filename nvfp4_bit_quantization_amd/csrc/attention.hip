@@ -376,34 +376,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
 }
 
 // ------------------------------------------------------------- gradient ----
-// -delta = -sum_d do * o, 16 lanes to a row, and -lse / scale beside it: what
-// the products' accumulators start from
-__global__ __launch_bounds__(kThreads) void attention_delta_kernel(AttnArgs a) {
-  const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);  // (sequence, query) or token
-  const int head = blockIdx.y, c = threadIdx.x & 15;
-  float v = 0.0f;
-  if (row < a.total_q && c * 8 < a.dim) {
-    const int64_t b = a.cu_q ? 0 : row / a.q_len, i = a.cu_q ? row : row % a.q_len;
-    float x[8], y[8];
-    load8(at(a.o, b, i, head) + c * 8, x);
-    load8(at(a.d_o, b, i, head) + c * 8, y);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v = fmaf(x[j], y[j], v);
-  }
-  v += dpp<0x128>(v);
-  v += dpp<0x124>(v);
-  v += dpp<0x122>(v);
-  v += dpp<0x121>(v);
-  if (row < a.total_q && c == 0) {
-    const int64_t i = (int64_t)head * a.total_q + row;
-    a.delta[i] = -v;
-    const float lse = a.lse[i];
-    a.lse2[i] = lse == -INFINITY ? 0.0f : -lse / a.scale;  // all of such a row is masked: exp2(-inf - 0) = 0
-  }
-}
-
 // dQ: a wave holds 32 queries as columns; scores^T = K Q^T, dP^T = V dO^T,
-// dQ^T = K^T dS^T.
+// dQ^T = K^T dS^T.  It forms delta = sum_d do * o on the way, and leaves
+// -delta and -lse / scale, from which the accumulators of the dK, dV pass start.
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
   __shared__ __align__(16) uint8_t lds[4 * Tile<D>::bytes(kTile)];
@@ -427,8 +402,21 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
     q[c] = load_row(qrow, c, chunks, h);
     g[c] = load_row(grow, c, chunks, h);
   }
+  const uint16_t *orow = at(a.o, s.bq, s.q0 + qi, w.head);
+  float delta = 0.0f;
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    const uint4 x = __builtin_bit_cast(uint4, load_row(orow, c, chunks, h)), y = __builtin_bit_cast(uint4, g[c]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) delta = fmaf(bf16_at(x, j), bf16_at(y, j), delta);
+  }
+  delta = swapped32(delta, [](float x, float y) { return x + y; });
   const int64_t stat = (int64_t)w.head * a.total_q + first_row(a, s, w.b) + qi;
-  const float start = a.lse2[stat] * (a.scale * kLog2e), delta = a.delta[stat];
+  const float lse = a.lse[stat], start = lse == -INFINITY ? 0.0f : -lse * kLog2e;  // all of such a row is masked
+  if (h == 0 && mine < s.nq) {
+    a.minus_delta[stat] = -delta;
+    a.minus_lse[stat] = lse == -INFINITY ? 0.0f : -lse / a.scale;
+  }
 
   int lo, hi, unused, begin, end;
   sight(a, qi, s.nk, off, lo, hi);
@@ -474,7 +462,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) d = mfma(in.rows(kB, u * 32, c), g[c], d);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], c2, start)) * (d[i] + delta);
+      for (int i = 0; i < 16; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], c2, start)) * (d[i] - delta);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const bf16x8 b = pack8(p, 8 * c);
@@ -490,13 +478,13 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
 // dV^T = dO^T P, dK^T = Q^T dS, summed over the query heads of the key head.
 // The keys' operands stay in registers and the values' in LDS: with both in
 // registers nothing is left of the 256 that two waves per SIMD have each to
-// read operands ahead.  Queries come in tiles of 32 rows, so that two
-// workgroups fit a compute unit's LDS.
+// read operands ahead.  Queries come in tiles of 32 rows (D = 128), so that two
+// workgroups fit a compute unit's LDS, or 64 (D = 64).
 constexpr int kKeys = 128;  // keys of a workgroup
-constexpr int kRows = 32;   // queries of a tile
 
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttnArgs a) {
+  constexpr int kRows = D == 128 ? 32 : 64;
   constexpr uint32_t kB = Tile<D>::bytes(kRows), kV = Tile<D>::bytes(kKeys);
   __shared__ __align__(16) uint8_t lds[4 * kB + kV];
   __shared__ __align__(16) float stats[2][2][64];
@@ -550,7 +538,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttnArgs a) 
     fetch_tile<D, kRows>(at(a.q, s.bq, s.q0, head), a.q.st, i0, s.nq, chunks, to, wave, lane);
     fetch_tile<D, kRows>(at(a.d_o, s.bq, s.q0, head), a.d_o.st, i0, s.nq, chunks, to + kB, wave, lane);
     if (wave < 2) {
-      const float *src = (wave ? a.delta : a.lse2) + (int64_t)head * a.total_q + row0 + i0;
+      const float *src = (wave ? a.minus_delta : a.minus_lse) + (int64_t)head * a.total_q + row0 + i0;
       const int left = s.nq - i0 - 1;
       dma4(uniform_ptr((const uint8_t *)src), (uint32_t)(lane < left ? lane : left) * 4u,
            __builtin_amdgcn_readfirstlane(lds_addr(stats[stage][wave])));
@@ -568,71 +556,74 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttnArgs a) 
     }
     more = head < (hk + 1) * group;
     if (more) fetch(head, t, stage ^ 1);
-    // the accumulators start from -lse / scale and -delta
-    constexpr int kN = D / 16;
-    f32x16 p, d;
-    int l = lane;
-    asm volatile("" : "+v"(l));  // what is formed of it stays out of registers between tiles
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const float4 x = *reinterpret_cast<const float4 *>(&stats[stage][0][8 * b + 4 * (l >> 5)]);
-      const float4 y = *reinterpret_cast<const float4 *>(&stats[stage][1][8 * b + 4 * (l >> 5)]);
-      p[4 * b] = x.x, p[4 * b + 1] = x.y, p[4 * b + 2] = x.z, p[4 * b + 3] = x.w;
-      d[4 * b] = y.x, d[4 * b + 1] = y.y, d[4 * b + 2] = y.z, d[4 * b + 3] = y.w;
-    }
-    // Operands are read two steps ahead of their products.  The order below
-    // is the one wanted; scheduling stays within a step.
-    bf16x8 qa[kN], ga[kN], va[kN], t[2 * kN];
-    const auto read_step = [&](int c) {
-      qa[c] = in.rows(0, 0, c);
-      ga[c] = in.rows(kB, 0, c);
-      va[c] = values.rows(0, 0, c);
-    };
-    // product 2 dt + w of the 16 queries c: w = 0: dV from dO, 1: dK from Q
-    const auto read_cols = [&](int i) { t[i] = in.cols(i & 1 ? 0 : kB, i / kN * 16, i % kN / 2); };
-    read_step(0);
-    read_step(1);
+    for (int u = 0; u < kRows / 32; ++u) {
+      // the accumulators start from -lse / scale and -delta
+      constexpr int kN = D / 16;
+      f32x16 p, d;
+      int l = lane;
+      asm volatile("" : "+v"(l));  // what is formed of it stays out of registers between tiles
 #pragma unroll
-    for (int c = 0; c < kN; ++c) {
-      if (c + 2 < kN)
-        read_step(c + 2);
-      else
-        read_cols(2 * (c + 2 - kN)), read_cols(2 * (c + 2 - kN) + 1);
-      p = mfma(qa[c], k[c], p);
-      d = mfma(ga[c], va[c], d);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    if (i0 + kRows > all_hi || i0 < all_lo) {
-      int lo, hi;
-      asm volatile("" : "+v"(l));
-      seen_by(first + wave * 32 + (l & 31), lo, hi);
-      lo -= i0;
-      hi -= i0;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) p[i] = row_of(i, l >> 5) < hi && row_of(i, l >> 5) >= lo ? p[i] : -INFINITY;
-    }
-    const auto element = [&](int i) {
-      p[i] = __builtin_amdgcn_exp2f(p[i] * c2);
-      d[i] = p[i] * d[i];
-    };
-#pragma unroll
-    for (int i = 0; i < 8; ++i) element(i);
-    bf16x8 b0 = pack8(p, 0), b1 = pack8(d, 0);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < 2 * kN; ++i) {
-      if (i + 4 < 2 * kN) read_cols(i + 4);
-      f32x16 &acc = i & 1 ? dk[i % kN / 2] : dv[i % kN / 2];
-      acc = mfma(t[i], i & 1 ? b1 : b0, acc);
-      if (i < kN) {
-#pragma unroll
-        for (int j = 0; j < 8 / kN; ++j) element(8 + i * (8 / kN) + j);
+      for (int b = 0; b < 4; ++b) {
+        const float4 x = *reinterpret_cast<const float4 *>(&stats[stage][0][32 * u + 8 * b + 4 * (l >> 5)]);
+        const float4 y = *reinterpret_cast<const float4 *>(&stats[stage][1][32 * u + 8 * b + 4 * (l >> 5)]);
+        p[4 * b] = x.x, p[4 * b + 1] = x.y, p[4 * b + 2] = x.z, p[4 * b + 3] = x.w;
+        d[4 * b] = y.x, d[4 * b + 1] = y.y, d[4 * b + 2] = y.z, d[4 * b + 3] = y.w;
       }
-      if (i == kN - 1) {
-        b0 = pack8(p, 8);
-        b1 = pack8(d, 8);
+      // Operands are read two steps ahead of their products.  The order below
+      // is the one wanted; scheduling stays within a step.
+      bf16x8 qa[kN], ga[kN], va[kN], t[2 * kN];
+      const auto read_step = [&](int c) {
+        qa[c] = in.rows(0, 32 * u, c);
+        ga[c] = in.rows(kB, 32 * u, c);
+        va[c] = values.rows(0, 0, c);
+      };
+      // product 2 dt + w of the 16 queries c: w = 0: dV from dO, 1: dK from Q
+      const auto read_cols = [&](int i) { t[i] = in.cols(i & 1 ? 0 : kB, 32 * u + i / kN * 16, i % kN / 2); };
+      read_step(0);
+      read_step(1);
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        if (c + 2 < kN)
+          read_step(c + 2);
+        else
+          read_cols(2 * (c + 2 - kN)), read_cols(2 * (c + 2 - kN) + 1);
+        p = mfma(qa[c], k[c], p);
+        d = mfma(ga[c], va[c], d);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      if (i0 + 32 * u + 32 > all_hi || i0 + 32 * u < all_lo) {
+        int lo, hi;
+        asm volatile("" : "+v"(l));
+        seen_by(first + wave * 32 + (l & 31), lo, hi);
+        lo -= i0 + 32 * u;
+        hi -= i0 + 32 * u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) p[i] = row_of(i, l >> 5) < hi && row_of(i, l >> 5) >= lo ? p[i] : -INFINITY;
+      }
+      const auto element = [&](int i) {
+        p[i] = __builtin_amdgcn_exp2f(p[i] * c2);
+        d[i] = p[i] * d[i];
+      };
+#pragma unroll
+      for (int i = 0; i < 8; ++i) element(i);
+      bf16x8 b0 = pack8(p, 0), b1 = pack8(d, 0);
       __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 2 * kN; ++i) {
+        if (i + 4 < 2 * kN) read_cols(i + 4);
+        f32x16 &acc = i & 1 ? dk[i % kN / 2] : dv[i % kN / 2];
+        acc = mfma(t[i], i & 1 ? b1 : b0, acc);
+        if (i < kN) {
+#pragma unroll
+          for (int j = 0; j < 8 / kN; ++j) element(8 + i * (8 / kN) + j);
+        }
+        if (i == kN - 1) {
+          b0 = pack8(p, 8);
+          b1 = pack8(d, 8);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     in.move(stage ? 0u - 2 * kB : 2 * kB);
     stage ^= 1;
@@ -656,14 +647,12 @@ hipError_t launch_attention(const AttnArgs &a, hipStream_t s) {
 hipError_t launch_attention_backward(const AttnArgs &a, hipStream_t s) {
   const int64_t q_grid = (int64_t)a.batch * a.heads * ((a.q_len + kQueries - 1) / kQueries);
   const int64_t k_grid = (int64_t)a.batch * a.kv_heads * ((a.k_len + kKeys - 1) / kKeys);
-  if (a.total_q > 0)
-    attention_delta_kernel<<<dim3((unsigned)((a.total_q + 15) / 16), (unsigned)a.heads), kThreads, 0, s>>>(a);
   if (a.dim <= 64) {
-    attention_dkv_kernel<64><<<(unsigned)k_grid, kThreads, 0, s>>>(a);
     attention_dq_kernel<64><<<(unsigned)q_grid, kThreads, 0, s>>>(a);
+    attention_dkv_kernel<64><<<(unsigned)k_grid, kThreads, 0, s>>>(a);
   } else {
-    attention_dkv_kernel<128><<<(unsigned)k_grid, kThreads, 0, s>>>(a);
     attention_dq_kernel<128><<<(unsigned)q_grid, kThreads, 0, s>>>(a);
+    attention_dkv_kernel<128><<<(unsigned)k_grid, kThreads, 0, s>>>(a);
   }
   return hipGetLastError();
 }

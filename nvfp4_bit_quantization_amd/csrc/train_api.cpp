@@ -213,8 +213,8 @@ int nvfp4_attention_backward(const nvfp4_attention_shape *shape, const nvfp4_hea
   a.dk = heads_of(dk);
   a.dv = heads_of(dv);
   a.lse = const_cast<float *>(lse);
-  a.delta = (float *)workspace;
-  a.lse2 = (float *)((char *)workspace + stat_bytes(shape));
+  a.minus_delta = (float *)workspace;
+  a.minus_lse = (float *)((char *)workspace + stat_bytes(shape));
   hipStream_t s = (hipStream_t)stream;
   return finish(launch_attention_backward(a, s), s);
 }

@@ -60,8 +60,7 @@ struct Heads {
 struct AttnArgs {
   Heads q, k, v, o, d_o, dq, dk, dv;
   float *lse;    // [heads][total_q]
-  float *delta;  // gradient: [heads][total_q], and as lse2 the lse in powers of two
-  float *lse2;
+  float *minus_delta, *minus_lse;  // gradient: [heads][total_q], -delta and -lse / scale
   const int32_t *cu_q, *cu_k;
   int64_t total_q, total_k;
   int64_t window;  // 0: none
