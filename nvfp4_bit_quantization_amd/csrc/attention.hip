@@ -222,21 +222,22 @@ __device__ __forceinline__ void tile_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// workgroup -> (sequence, head, tile): neighbours share a key head, heavy
-// tiles of a causal pass first, a contiguous range to each XCD
+// workgroup -> (head, sequence, tile): neighbours share a key head, a contiguous
+// range to each XCD.  Heads are outermost, so that packed sequences' uneven
+// lengths spread over the XCDs alike; with fewer key heads than XCDs packed
+// sequences are dealt round-robin instead.
 struct Work {
   int b, head, tile;
 };
 __device__ __forceinline__ Work work_of(const AttnArgs &a, int tiles, int group) {
-  uint32_t w = xcd_tile(blockIdx.x, gridDim.x);
+  uint32_t w = a.cu_q && a.kv_heads < 8 ? blockIdx.x : xcd_tile(blockIdx.x, gridDim.x);
   Work r;
   const int g = (int)(w % (uint32_t)group);
   w /= (uint32_t)group;
   r.tile = (int)(w % (uint32_t)tiles);
   w /= (uint32_t)tiles;
-  const int hk = (int)(w % (uint32_t)a.kv_heads);
-  r.b = (int)(w / (uint32_t)a.kv_heads);
-  r.head = hk * group + g;
+  r.b = (int)(w % (uint32_t)a.batch);
+  r.head = (int)(w / (uint32_t)a.batch) * group + g;
   return r;
 }
 
@@ -493,9 +494,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttnArgs a) 
   Work w = work_of(a, tiles, 1);
   const int hk = w.head;
   // Key tiles of a causal pass differ in work, falling along the sequence.
-  // Every second head walks them from the end, so that the workgroups that a
+  // Every second sequence walks them from the end, so that the workgroups that a
   // compute unit holds at a time add up to the same.
-  if ((w.b * a.kv_heads + hk) & 1) w.tile = tiles - 1 - w.tile;
+  if ((hk * a.batch + w.b) & 1) w.tile = tiles - 1 - w.tile;
   const Seq s = sequence(a, w.b);
   const int first = w.tile * kKeys;
   if (first >= s.nk) return;
