@@ -126,7 +126,7 @@ __device__ __forceinline__ void draw(const AdamArgs &a, uint32_t index, uint32_t
 
 // elements i0 .. i0 + 7 of a tensor; returns the maximum of what is stored
 template <typename TP, typename TG, bool S8, bool SR>
-__device__ __forceinline__ float step8(const AdamArgs &a, const AdamTensor &t, float gs, int64_t i0) {
+__device__ __forceinline__ float step8(const AdamArgs &a, const AdamTensor &t, const AdamExtra &x, float gs, int64_t i0) {
   const int64_t left = t.n - i0;
   const int have = left >= 8 ? 8 : left > 0 ? (int)left : 0;
   const bool vec = t.flags & AF_VEC;
@@ -136,8 +136,8 @@ __device__ __forceinline__ float step8(const AdamArgs &a, const AdamTensor &t, f
   get8((const TG *)t.grad + i0, vec, have, g);
   if constexpr (S8) {
     const uint2 qm = get_codes((const uint8_t *)t.m + i0, vec, have), qv = get_codes((const uint8_t *)t.v + i0, vec, have);
-    decode8(qm, have ? t.m_scale[i0 >> 5] : 0u, m);
-    decode8(qv, have ? t.v_scale[i0 >> 5] : 0u, v);
+    decode8(qm, have ? x.m_scale[i0 >> 5] : 0u, m);
+    decode8(qv, have ? x.v_scale[i0 >> 5] : 0u, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= v[j];
   } else {
@@ -147,9 +147,9 @@ __device__ __forceinline__ float step8(const AdamArgs &a, const AdamTensor &t, f
   float r[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float x = g[j] * gs;
-    m[j] = m[j] * a.beta1 + x * a.one_minus_beta1;
-    v[j] = v[j] * a.beta2 + x * x * a.one_minus_beta2;
+    const float y = g[j] * gs;
+    m[j] = m[j] * a.beta1 + y * a.one_minus_beta1;
+    v[j] = v[j] * a.beta2 + y * y * a.one_minus_beta2;
     // the square root and reciprocal instructions: 1 unit in the last place
     // each, next to the update's ten other roundings
     r[j] = __builtin_amdgcn_sqrtf(v[j]);
@@ -161,23 +161,23 @@ __device__ __forceinline__ float step8(const AdamArgs &a, const AdamTensor &t, f
     for (int j = 0; j < 8; ++j) p[j] = __uint_as_float((__float_as_uint(p[j]) + u16_of(w, j)) & 0xFFFF0000u);
   }
   put8((TP *)t.param + i0, vec, have, p);
-  if (t.copy) put8(t.copy + i0, vec, have, p);
+  if (x.copy) put8(x.copy + i0, vec, have, p);
   if constexpr (S8) {
     int e;
     if (SR) draw(a, t.index, 0u, i0 >> 3, w);
     put_codes((uint8_t *)t.m + i0, vec, have, encode8<SR>(m, w, false, &e));
     const bool leader = have && (threadIdx.x & 3) == 0;
-    if (leader) t.m_scale[i0 >> 5] = (uint8_t)(e + 127);
+    if (leader) x.m_scale[i0 >> 5] = (uint8_t)(e + 127);
     if (SR) draw(a, t.index, 1u, i0 >> 3, w);
     put_codes((uint8_t *)t.v + i0, vec, have, encode8<SR>(r, w, true, &e));
-    if (leader) t.v_scale[i0 >> 5] = (uint8_t)(e + 127);
+    if (leader) x.v_scale[i0 >> 5] = (uint8_t)(e + 127);
   } else {
     put8((float *)t.m + i0, vec, have, m);
     put8((float *)t.v + i0, vec, have, v);
   }
   float top = 0.0f;
-  if (t.amax) {
-    const bool bf16 = t.copy || sizeof(TP) == 2;
+  if (x.amax) {
+    const bool bf16 = x.copy || sizeof(TP) == 2;
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(bf16 ? round_bf16(p[j]) : p[j]));
   }
@@ -185,38 +185,39 @@ __device__ __forceinline__ float step8(const AdamArgs &a, const AdamTensor &t, f
 }
 
 template <typename TP, typename TG, bool S8, bool SR>
-__device__ __forceinline__ void chunk(const AdamArgs &a, const AdamTensor &t, int64_t first) {
+__device__ __forceinline__ void chunk(const AdamArgs &a, const AdamTensor &t, const AdamExtra &x, int64_t first) {
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
   float top = 0.0f;
   // whole workgroups take part in every step (block maxima cross lanes)
   for (int64_t i = first; i < first + kAdamChunk && i < t.n; i += 8 * kAdamThreads)
-    top = fmaxf(top, step8<TP, TG, S8, SR>(a, t, gs, i + 8 * threadIdx.x));
-  if (t.amax) fold_max(t.amax, top);
+    top = fmaxf(top, step8<TP, TG, S8, SR>(a, t, x, gs, i + 8 * threadIdx.x));
+  if (x.amax) fold_max(x.amax, top);
 }
 
 template <bool SR>
 __global__ __launch_bounds__(kAdamThreads) void adamw_kernel(const AdamArgs a) {
   int i = 0;
-  for (int step = 32; step; step >>= 1)  // the first tensor that ends behind this workgroup
-    if (i + step <= a.count - 1 && a.t[i + step - 1].end <= blockIdx.x) i += step;
-  const AdamTensor &t = a.t[i];
-  const int64_t first = (int64_t)(blockIdx.x - (i ? a.t[i - 1].end : 0u)) * kAdamChunk;
+  for (int step = 64; step; step >>= 1)  // the first tensor that ends behind this workgroup
+    if (i + step <= a.count - 1 && a.tensor(i + step - 1).end <= blockIdx.x) i += step;
+  const AdamTensor &t = a.tensor(i);
+  const AdamExtra x = t.flags & AF_EXTRA ? a.extra((int)(t.flags >> AF_EXTRA_SHIFT)) : AdamExtra{};
+  const int64_t first = (int64_t)(blockIdx.x - (i ? a.tensor(i - 1).end : 0u)) * kAdamChunk;
   switch (t.flags & 7u) {
-    case 0: chunk<float, float, false, SR>(a, t, first); break;
-    case AF_PARAM_BF16: chunk<uint16_t, float, false, SR>(a, t, first); break;
-    case AF_GRAD_BF16: chunk<float, uint16_t, false, SR>(a, t, first); break;
-    case AF_PARAM_BF16 | AF_GRAD_BF16: chunk<uint16_t, uint16_t, false, SR>(a, t, first); break;
-    case AF_STATE8: chunk<float, float, true, SR>(a, t, first); break;
-    case AF_STATE8 | AF_PARAM_BF16: chunk<uint16_t, float, true, SR>(a, t, first); break;
-    case AF_STATE8 | AF_GRAD_BF16: chunk<float, uint16_t, true, SR>(a, t, first); break;
-    default: chunk<uint16_t, uint16_t, true, SR>(a, t, first); break;
+    case 0: chunk<float, float, false, SR>(a, t, x, first); break;
+    case AF_PARAM_BF16: chunk<uint16_t, float, false, SR>(a, t, x, first); break;
+    case AF_GRAD_BF16: chunk<float, uint16_t, false, SR>(a, t, x, first); break;
+    case AF_PARAM_BF16 | AF_GRAD_BF16: chunk<uint16_t, uint16_t, false, SR>(a, t, x, first); break;
+    case AF_STATE8: chunk<float, float, true, SR>(a, t, x, first); break;
+    case AF_STATE8 | AF_PARAM_BF16: chunk<uint16_t, float, true, SR>(a, t, x, first); break;
+    case AF_STATE8 | AF_GRAD_BF16: chunk<float, uint16_t, true, SR>(a, t, x, first); break;
+    default: chunk<uint16_t, uint16_t, true, SR>(a, t, x, first); break;
   }
 }
 
 }  // namespace
 
 hipError_t launch_adamw(const AdamArgs &a, hipStream_t s) {
-  const unsigned grid = a.t[a.count - 1].end;
+  const unsigned grid = a.tensor(a.count - 1).end;
   if (a.sr)
     adamw_kernel<true><<<grid, kAdamThreads, 0, s>>>(a);
   else

@@ -5,6 +5,7 @@
 #include <math.h>
 #include <stdint.h>
 #include <stdlib.h>
+#include <string.h>
 
 #include "nvfp4.h"
 #include "train_kernels.hpp"
@@ -248,25 +249,23 @@ int nvfp4_adamw(const nvfp4_adamw_tensor *tensors, int64_t n_tensors, const nvfp
   a.grad_scale = c->grad_scale;
   hipStream_t s = (hipStream_t)stream;
   uint32_t end = 0;
+  int extras = 0;
   for (int64_t i = 0; i <= n_tensors; ++i) {
-    const bool more = i < n_tensors;
+    const bool more = i < n_tensors, extra = more && (tensors[i].m_scale || tensors[i].copy || tensors[i].amax);
     // at most 2^22 workgroups a tensor: the running count stays in 32 bits
-    if (a.count && (!more || a.count == kAdamTensors || end > (1u << 30))) {
+    if (a.count && (!more || end > (1u << 30) ||
+                    (a.count + 1) * kAdamTensorWords + (extras + extra) * kAdamExtraWords > kAdamWords)) {
       if (launch_adamw(a, s) != hipSuccess) return NVFP4_E_HIP;
-      a.count = 0;
+      a.count = extras = 0;
       end = 0;
     }
     if (!more || tensors[i].n == 0) continue;
     const nvfp4_adamw_tensor &t = tensors[i];
-    AdamTensor &d = a.t[a.count++];
+    AdamTensor d;
     d.param = t.param;
     d.grad = t.grad;
     d.m = t.m;
     d.v = t.v;
-    d.m_scale = t.m_scale;
-    d.v_scale = t.v_scale;
-    d.copy = (uint16_t *)t.copy;
-    d.amax = t.amax;
     d.n = t.n;
     d.keep = (float)(1.0 - (double)c->lr * t.weight_decay);
     d.index = (uint32_t)i;
@@ -275,8 +274,14 @@ int nvfp4_adamw(const nvfp4_adamw_tensor *tensors, int64_t n_tensors, const nvfp
     const size_t sa = t.state_bits == 8 ? 8 : 16;
     if (aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.m, sa) && aligned(t.v, sa) && aligned(t.copy, 16))
       d.flags |= AF_VEC;
+    if (extra) {
+      const AdamExtra e = {t.m_scale, t.v_scale, (uint16_t *)t.copy, t.amax};
+      d.flags |= AF_EXTRA | (uint32_t)extras << AF_EXTRA_SHIFT;
+      memcpy(a.words + kAdamWords - ++extras * kAdamExtraWords, &e, sizeof e);
+    }
     end += (uint32_t)((t.n + kAdamChunk - 1) / kAdamChunk);
     d.end = end;
+    memcpy(a.words + a.count++ * kAdamTensorWords, &d, sizeof d);
   }
   return finish(hipSuccess, s);
 }

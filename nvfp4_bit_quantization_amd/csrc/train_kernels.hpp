@@ -18,36 +18,48 @@ int64_t layernorm_backward_parts(int64_t rows, int64_t cols);
 hipError_t launch_layernorm_backward(const nvfp4_layernorm_backward_args &a, float *partials, hipStream_t s);
 
 // --------------------------------------------------------------- adamw ----
-constexpr int kAdamTensors = 40;       // tensors of one launch: their descriptors travel as kernel arguments
 constexpr int kAdamThreads = 256;
-constexpr int kAdamChunk = 4096;       // elements of one workgroup (a multiple of 8 * kAdamThreads)
+constexpr int kAdamChunk = 4096;  // elements of one workgroup (a multiple of 8 * kAdamThreads)
 
-// flags of AdamTensor
-enum AdamFlags : uint32_t { AF_PARAM_BF16 = 1, AF_GRAD_BF16 = 2, AF_STATE8 = 4, AF_VEC = 8 };
+enum AdamFlags : uint32_t {
+  AF_PARAM_BF16 = 1, AF_GRAD_BF16 = 2, AF_STATE8 = 4, AF_VEC = 8,
+  AF_EXTRA = 16,      // has an AdamExtra
+  AF_EXTRA_SHIFT = 8  // its number, from bit 8 on
+};
 
 struct AdamTensor {
   void *param;
   const void *grad;
   void *m, *v;
-  uint8_t *m_scale, *v_scale;
-  uint16_t *copy;
-  float *amax;
   int64_t n;
   float keep;      // 1 - lr * weight_decay
   uint32_t flags;
   uint32_t index;  // place in the caller's list
   uint32_t end;    // workgroups of this and the earlier tensors of the launch
 };
+struct AdamExtra {  // what not every tensor has
+  uint8_t *m_scale, *v_scale;
+  uint16_t *copy;
+  float *amax;
+};
 
+// The descriptors travel as kernel arguments: AdamTensors from the front of
+// the words, AdamExtras from the back, as many as 4 KiB of arguments hold (71
+// tensors without extras, 45 with).
+constexpr int kAdamWords = 500, kAdamTensorWords = sizeof(AdamTensor) / 8, kAdamExtraWords = sizeof(AdamExtra) / 8;
 struct AdamArgs {
-  AdamTensor t[kAdamTensors];
+  uint64_t words[kAdamWords];
   int count;
   int sr;
   float lr, beta1, one_minus_beta1, beta2, one_minus_beta2, eps;
   float correct1, correct2;  // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
   uint32_t seed_lo, seed_hi, step_lo, tag;
   const float *grad_scale;
+
+  __host__ __device__ const AdamTensor &tensor(int i) const { return ((const AdamTensor *)words)[i]; }
+  __host__ __device__ const AdamExtra &extra(int i) const { return ((const AdamExtra *)(words + kAdamWords))[-1 - i]; }
 };
+static_assert(sizeof(AdamTensor) == 56 && sizeof(AdamExtra) == 32 && sizeof(AdamArgs) <= 4096, "kernel arguments");
 
 hipError_t launch_adamw(const AdamArgs &a, hipStream_t s);
 

@@ -246,7 +246,7 @@ hipError_t launch_layernorm(const nvfp4_layernorm_args &, hipStream_t) { ++launc
 int64_t layernorm_backward_parts(int64_t rows, int64_t) { return rows < 512 ? rows : 512; }
 hipError_t launch_layernorm_backward(const nvfp4_layernorm_backward_args &, float *, hipStream_t) { ++launched; return hipErrorInvalidValue; }
 int64_t adam_ends = 0, adam_tensors = 0;
-hipError_t launch_adamw(const AdamArgs &a, hipStream_t) { ++launched; adam_ends += a.t[a.count - 1].end; adam_tensors += a.count; return hipSuccess; }
+hipError_t launch_adamw(const AdamArgs &a, hipStream_t) { ++launched; adam_ends += a.tensor(a.count - 1).end; adam_tensors += a.count; return hipSuccess; }
 hipError_t launch_attention(const AttnArgs &, hipStream_t) { ++launched; return hipErrorInvalidValue; }
 hipError_t launch_attention_backward(const AttnArgs &, hipStream_t) { ++launched; return hipErrorInvalidValue; }
 }
