@@ -453,12 +453,17 @@ typedef struct {
  * access leaves the tensors.
  *   q, o: heads heads; k, v: kv_heads.  data 16-byte aligned, strides
  *   multiples of 8, |token_stride| < 2^24 and not negative.  lse: device float [heads][total_q].
+ *   workspace  nvfp4_attention_workspace_bytes(shape) bytes of device scratch,
+ *              16-byte aligned, not initialised: 0 (workspace may be NULL) but
+ *              where few queries meet many keys and the keys are split.
  * Products on the bf16 MFMA with binary32 accumulation; the softmax is
  * binary32, its probabilities are rounded to bf16 for the product with v.
- * One kernel.
+ * One kernel, or two where the keys are split.
  */
 int nvfp4_attention(const nvfp4_attention_shape *shape, const nvfp4_heads *q, const nvfp4_heads *k,
-                    const nvfp4_heads *v, const nvfp4_heads *o, float *lse, void *stream);
+                    const nvfp4_heads *v, const nvfp4_heads *o, float *lse, void *workspace, size_t workspace_bytes,
+                    void *stream);
+size_t nvfp4_attention_workspace_bytes(const nvfp4_attention_shape *shape);
 
 /*
  * nvfp4_attention_backward -- with p = exp(scale * q k^T - lse) over the keys
@@ -469,7 +474,7 @@ int nvfp4_attention(const nvfp4_attention_shape *shape, const nvfp4_heads *q, co
  * every token of a sequence (zero where nothing is in sight).
  *   workspace  nvfp4_attention_backward_workspace_bytes(shape) bytes of device
  *              scratch, 16-byte aligned, not initialised.
- * p and ds are rounded to bf16 for their products.
+ * p and ds are rounded to bf16 for their products.  Two to four kernels.
  */
 int nvfp4_attention_backward(const nvfp4_attention_shape *shape, const nvfp4_heads *q, const nvfp4_heads *k,
                              const nvfp4_heads *v, const nvfp4_heads *o, const float *lse, const nvfp4_heads *d_o,

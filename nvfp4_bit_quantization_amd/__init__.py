@@ -151,7 +151,9 @@ def lib() -> ctypes.CDLL:
     L.nvfp4_layernorm_backward_workspace_bytes.restype = ctypes.c_size_t
     L.nvfp4_layernorm_backward_workspace_bytes.argtypes = [i64, i64]
     L.nvfp4_attention.restype = i32
-    L.nvfp4_attention.argtypes = [P, P, P, P, P, P, P]
+    L.nvfp4_attention.argtypes = [P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    L.nvfp4_attention_workspace_bytes.restype = ctypes.c_size_t
+    L.nvfp4_attention_workspace_bytes.argtypes = [P]
     L.nvfp4_attention_backward.restype = i32
     L.nvfp4_attention_backward.argtypes = [P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
     L.nvfp4_attention_backward_workspace_bytes.restype = ctypes.c_size_t
@@ -737,28 +739,39 @@ def _lse(lse, heads, tokens, device):
 
 
 def nvfp4_attention(q, k, v, o, lse, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None, max_k=None,
-                    stream=None):
+                    workspace=None, stream=None):
     """o = softmax(scale q k^T) v and lse [heads][all queries] for [batch][tokens][heads][dim] tensors, or packed
-    [tokens][heads][dim] ones with cu_q, cu_k (int32 [batch + 1], device) and the longest lengths max_q, max_k."""
+    [tokens][heads][dim] ones with cu_q, cu_k (int32 [batch + 1], device) and the longest lengths max_q, max_k.
+    workspace: new_attention_workspace's, where one is needed."""
     s, sq, sk, heads, tokens, device = _attention_inputs(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
     _as(o, sq, device, "o")
     _lse(lse, heads, tokens, device)
+    if workspace is not None and workspace.get_device() != device:
+        raise ValueError("workspace: a tensor on device %d is wanted" % device)
     _check(lib().nvfp4_attention(s, _heads(q, sq), _heads(k, sk), _heads(v, sk), _heads(o, sq), lse.data_ptr(),
-                                 _raw_stream(stream, device)), "nvfp4_attention")
+                                 _ptr(workspace), _nbytes(workspace), _raw_stream(stream, device)), "nvfp4_attention")
     return o
 
 
-def attention(q, k, v, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None, max_k=None, stream=None):
+def attention(q, k, v, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None, max_k=None, workspace=None,
+              stream=None):
     """Allocates and computes (o, lse)."""
     if stream is not None:
         with _on_stream(stream):
-            return attention(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
+            return attention(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k, workspace)
     import torch
     s, sq, sk, heads, tokens, device = _attention_inputs(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
+    L = lib()
     o = torch.empty_like(q, memory_format=torch.contiguous_format)
     lse = _floats(heads, tokens, q.device)
-    _check(lib().nvfp4_attention(s, _heads(q, sq), _heads(k, sk), _heads(v, sk), _heads(o, sq), lse.data_ptr(),
-                                 _raw_stream(None, device)), "nvfp4_attention")
+    if workspace is None:
+        need = L.nvfp4_attention_workspace_bytes(s)
+        if need:
+            workspace = _floats(1, need // 4, q.device)
+    elif workspace.get_device() != device:
+        raise ValueError("workspace: a tensor on device %d is wanted" % device)
+    _check(L.nvfp4_attention(s, _heads(q, sq), _heads(k, sk), _heads(v, sk), _heads(o, sq), lse.data_ptr(), _ptr(workspace),
+                             _nbytes(workspace), _raw_stream(None, device)), "nvfp4_attention")
     return o, lse
 
 
@@ -782,10 +795,11 @@ def nvfp4_attention_backward(d_o, q, k, v, o, lse, dq, dk, dv, workspace, causal
 
 
 def new_attention_workspace(q, k, v, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None, max_k=None):
-    """A workspace of nvfp4_attention_backward for these arguments (one per stream)."""
+    """A workspace of nvfp4_attention and nvfp4_attention_backward for these arguments (one per stream)."""
     import torch
     s = _attention_inputs(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)[0]
-    return torch.empty(lib().nvfp4_attention_backward_workspace_bytes(s), dtype=torch.uint8, device=q.device)
+    need = max(lib().nvfp4_attention_backward_workspace_bytes(s), lib().nvfp4_attention_workspace_bytes(s))
+    return torch.empty(need, dtype=torch.uint8, device=q.device)
 
 
 def attention_backward(d_o, q, k, v, o, lse, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None,

@@ -227,18 +227,44 @@ __device__ __forceinline__ void tile_barrier() {
 // lengths spread over the XCDs alike; with fewer key heads than XCDs packed
 // sequences are dealt round-robin instead.
 struct Work {
-  int b, head, tile;
+  int b, head, tile, part;
 };
-__device__ __forceinline__ Work work_of(const AttnArgs &a, int tiles, int group) {
+__device__ __forceinline__ Work work_of(const AttnArgs &a, int tiles, int group, int parts) {
   uint32_t w = a.cu_q && a.kv_heads < 8 ? blockIdx.x : xcd_tile(blockIdx.x, gridDim.x);
   Work r;
   const int g = (int)(w % (uint32_t)group);
   w /= (uint32_t)group;
+  r.part = (int)(w % (uint32_t)parts);
+  w /= (uint32_t)parts;
   r.tile = (int)(w % (uint32_t)tiles);
   w /= (uint32_t)tiles;
   r.b = (int)(w % (uint32_t)a.batch);
   r.head = (int)(w / (uint32_t)a.batch) * group + g;
   return r;
+}
+// the steps [lo, hi) of part `part` of `parts`
+__device__ __forceinline__ void part_of(int part, int parts, int &lo, int &hi) {
+  const int n = hi - lo, at = lo;
+  lo = at + (int)((int64_t)n * part / parts);
+  hi = at + (int)((int64_t)n * (part + 1) / parts);
+}
+
+// a row of a part's binary32 results, [part][head][row][D]
+template <int D>
+__device__ __forceinline__ float *part_row(float *p, int part, int heads, int head, int64_t rows, int64_t row) {
+  return p + (((int64_t)part * heads + head) * rows + row) * D;
+}
+template <int D>
+__device__ __forceinline__ void store_part(float *row, const f32x16 *acc, float f, int dim, int h) {
+#pragma unroll
+  for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int d = dt * 32 + 8 * g + 4 * h;
+      if (d < dim)
+        *reinterpret_cast<float4 *>(row + d) =
+            make_float4(acc[dt][4 * g] * f, acc[dt][4 * g + 1] * f, acc[dt][4 * g + 2] * f, acc[dt][4 * g + 3] * f);
+    }
 }
 
 // -------------------------------------------------------------- forward ----
@@ -252,7 +278,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   constexpr uint32_t kB = Tile<D>::bytes(kTile);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
   const int group = a.heads / a.kv_heads, tiles = (a.q_len + kQueries - 1) / kQueries;
-  Work w = work_of(a, tiles, group);
+  Work w = work_of(a, tiles, group, a.q_parts);
   if (a.causal) w.tile = tiles - 1 - w.tile;
   const Seq s = sequence(a, w.b);
   const int first = w.tile * kQueries;
@@ -284,7 +310,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   const float c2 = a.scale * kLog2e;
   Reads<D> in(lane, lds_addr(lds));
 
-  const int t0 = begin / kTile, t1 = end > begin ? (end + kTile - 1) / kTile : t0;
+  int t0 = begin / kTile, t1 = end > begin ? (end + kTile - 1) / kTile : t0;
+  part_of(w.part, a.q_parts, t0, t1);
   if (t0 < t1) {
     fetch_tile<D, kTile>(kh, a.k.st, t0 * kTile, s.nk, chunks, lds_addr(lds), wave, lane);
     fetch_tile<D, kTile>(vh, a.v.st, t0 * kTile, s.nk, chunks, lds_addr(lds) + kB, wave, lane);
@@ -370,10 +397,68 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   sum = swapped32(sum, [](float x, float y) { return x + y; });
   if (mine >= s.nq) return;
   const bool none = sum == 0.0f;
-  store_cols<D>(at(a.o, s.bq, s.q0 + mine, w.head), o, none ? 0.0f : 1.0f / sum, a.dim, h);
-  if (h == 0)
-    a.lse[(int64_t)w.head * a.total_q + first_row(a, s, w.b) + mine] =
-        none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+  const float f = none ? 0.0f : 1.0f / sum, lse = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+  const int64_t row = first_row(a, s, w.b) + mine;
+  if (a.q_parts > 1) {
+    store_part<D>(part_row<D>(a.q_part, w.part, a.heads, w.head, a.total_q, row), o, f, a.dim, h);
+    if (h == 0) a.lse_part[((int64_t)w.part * a.heads + w.head) * a.total_q + row] = lse;
+    return;
+  }
+  store_cols<D>(at(a.o, s.bq, s.q0 + mine, w.head), o, f, a.dim, h);
+  if (h == 0) a.lse[(int64_t)w.head * a.total_q + row] = lse;
+}
+
+// Parts joined: 128 rows of a head to a workgroup, 16 threads to a row.
+// WHAT = kJoinO: o = sum_p exp(lse_p - lse) o_p, lse = log sum_p exp(lse_p);
+// else sums over the parts in their order: dQ, or dK and dV.
+enum { kJoinO, kJoinQ, kJoinKV };
+template <int D, int WHAT>
+__global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs a) {
+  const bool kv = WHAT == kJoinKV;
+  const int heads = kv ? a.kv_heads : a.heads, parts = kv ? a.k_parts : a.q_parts;
+  const int64_t rows = kv ? a.total_k : a.total_q;
+  const int tiles = ((kv ? a.k_len : a.q_len) + 127) / 128, c = (int)threadIdx.x & 15;
+  uint32_t w = blockIdx.x;
+  const int tile = (int)(w % (uint32_t)tiles);
+  w /= (uint32_t)tiles;
+  const int b = (int)(w % (uint32_t)a.batch), head = (int)(w / (uint32_t)a.batch);
+  const Seq s = sequence(a, b);
+  const int n = kv ? s.nk : s.nq;
+  const int64_t row0 = !a.cu_q ? (int64_t)b * n : kv ? s.k0 : s.q0;
+  if (c * 8 >= a.dim) return;
+  for (int i = tile * 128 + (int)(threadIdx.x >> 4); i < tile * 128 + 128 && i < n; i += 16) {
+    const int64_t row = row0 + i;
+    if constexpr (WHAT == kJoinO) {
+      float top = -INFINITY, sum = 0.0f, o[8] = {};
+      for (int p = 0; p < parts; ++p) top = fmaxf(top, a.lse_part[((int64_t)p * heads + head) * rows + row]);
+      if (top > -INFINITY)
+        for (int p = 0; p < parts; ++p) {
+          const float f = __builtin_amdgcn_exp2f((a.lse_part[((int64_t)p * heads + head) * rows + row] - top) * kLog2e);
+          float v[8];
+          load8(part_row<D>(a.q_part, p, heads, head, rows, row) + c * 8, v);
+          sum += f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = fmaf(f, v[j], o[j]);
+        }
+      const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] *= f;
+      store8(at(a.o, s.bq, s.q0 + i, head) + c * 8, o);
+      if (c == 0) a.lse[(int64_t)head * rows + row] = sum > 0.0f ? top + __builtin_amdgcn_logf(sum) * kLn2 : -INFINITY;
+    } else {
+      for (int k = 0; k < (kv ? 2 : 1); ++k) {
+        float *from = kv ? (k ? a.v_part : a.k_part) : a.q_part, sum[8] = {};
+        for (int p = 0; p < parts; ++p) {
+          float v[8];
+          load8(part_row<D>(from, p, heads, head, rows, row) + c * 8, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum[j] += v[j];
+        }
+        const Heads &to = kv ? (k ? a.dv : a.dk) : a.dq;
+        store8(at(to, kv ? s.bk : s.bq, (kv ? s.k0 : s.q0) + i, head) + c * 8, sum);
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------- gradient ----
@@ -386,7 +471,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
   constexpr uint32_t kB = Tile<D>::bytes(kTile);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
   const int group = a.heads / a.kv_heads, tiles = (a.q_len + kQueries - 1) / kQueries;
-  Work w = work_of(a, tiles, group);
+  Work w = work_of(a, tiles, group, a.q_parts);
   if (a.causal) w.tile = tiles - 1 - w.tile;
   const Seq s = sequence(a, w.b);
   const int first = w.tile * kQueries;
@@ -414,7 +499,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
   delta = swapped32(delta, [](float x, float y) { return x + y; });
   const int64_t stat = (int64_t)w.head * a.total_q + first_row(a, s, w.b) + qi;
   const float lse = a.lse[stat], start = lse == -INFINITY ? 0.0f : -lse * kLog2e;  // all of such a row is masked
-  if (h == 0 && mine < s.nq) {
+  if (h == 0 && mine < s.nq && w.part == 0) {
     a.minus_delta[stat] = -delta;
     a.minus_lse[stat] = lse == -INFINITY ? 0.0f : -lse / a.scale;
   }
@@ -433,7 +518,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
   for (int dt = 0; dt < D / 32; ++dt) acc[dt] = zero16();
   const float c2 = a.scale * kLog2e;
   Reads<D> in(lane, lds_addr(lds));
-  const int t0 = begin / kTile, t1 = end > begin ? (end + kTile - 1) / kTile : t0;
+  int t0 = begin / kTile, t1 = end > begin ? (end + kTile - 1) / kTile : t0;
+  part_of(w.part, a.q_parts, t0, t1);
   if (t0 < t1) {
     fetch_tile<D, kTile>(kh, a.k.st, t0 * kTile, s.nk, chunks, lds_addr(lds), wave, lane);
     fetch_tile<D, kTile>(vh, a.v.st, t0 * kTile, s.nk, chunks, lds_addr(lds) + kB, wave, lane);
@@ -472,7 +558,12 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
       }
     }
   }
-  if (mine < s.nq) store_cols<D>(at(a.dq, s.bq, s.q0 + mine, w.head), acc, a.scale, a.dim, h);
+  if (mine >= s.nq) return;
+  if (a.q_parts > 1)
+    store_part<D>(part_row<D>(a.q_part, w.part, a.heads, w.head, a.total_q, first_row(a, s, w.b) + mine), acc, a.scale,
+                  a.dim, h);
+  else
+    store_cols<D>(at(a.dq, s.bq, s.q0 + mine, w.head), acc, a.scale, a.dim, h);
 }
 
 // dK, dV: a wave holds 32 keys as columns; scores = Q K^T, dP = dO V^T,
@@ -484,19 +575,20 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
 constexpr int kKeys = 128;  // keys of a workgroup
 
 template <int D>
-__global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attention_dkv_kernel(AttnArgs a) {
   constexpr int kRows = D == 128 ? 32 : 64;
   constexpr uint32_t kB = Tile<D>::bytes(kRows), kV = Tile<D>::bytes(kKeys);
   __shared__ __align__(16) uint8_t lds[4 * kB + kV];
   __shared__ __align__(16) float stats[2][2][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
   const int group = a.heads / a.kv_heads, tiles = (a.k_len + kKeys - 1) / kKeys;
-  Work w = work_of(a, tiles, 1);
+  Work w = work_of(a, tiles, 1, a.k_parts);
   const int hk = w.head;
   // Key tiles of a causal pass differ in work, falling along the sequence.
-  // Every second sequence walks them from the end, so that the workgroups that a
-  // compute unit holds at a time add up to the same.
-  if ((hk * a.batch + w.b) & 1) w.tile = tiles - 1 - w.tile;
+  // Where all workgroups are resident at once, two to a compute unit, every
+  // second sequence is walked from its end, so that the two add up to the same;
+  // else heavy tiles come first.
+  if (gridDim.x <= 512 && ((hk * a.batch + w.b) & 1)) w.tile = tiles - 1 - w.tile;
   const Seq s = sequence(a, w.b);
   const int first = w.tile * kKeys;
   if (first >= s.nk) return;
@@ -545,18 +637,23 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttnArgs a) 
            __builtin_amdgcn_readfirstlane(lds_addr(stats[stage][wave])));
     }
   };
+  // steps: the query tiles of each of the query heads in turn
+  int step = 0, steps = (t1 - t0) * group;
+  part_of(w.part, a.k_parts, step, steps);
   int head = hk * group, t = t0, stage = 0;
-  bool more = t0 < t1;
-  if (more) fetch(head, t, 0);
-  while (more) {
+  if (step < steps) {
+    head += step / (t1 - t0);
+    t += step % (t1 - t0);
+    fetch(head, t, 0);
+  }
+  for (; step < steps; ++step) {
     const int i0 = t * kRows;
     tile_barrier();  // this tile is in LDS, and every wave has read the previous one
     if (++t == t1) {
       t = t0;
       ++head;
     }
-    more = head < (hk + 1) * group;
-    if (more) fetch(head, t, stage ^ 1);
+    if (step + 1 < steps) fetch(head, t, stage ^ 1);
 #pragma unroll
     for (int u = 0; u < kRows / 32; ++u) {
       // the accumulators start from -lse / scale and -delta
@@ -630,32 +727,81 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dkv_kernel(AttnArgs a) 
     stage ^= 1;
   }
   if (mine >= s.nk) return;
+  if (a.k_parts > 1) {
+    const int64_t row = (a.cu_q ? s.k0 : (int64_t)w.b * a.k_len) + mine;
+    store_part<D>(part_row<D>(a.k_part, w.part, a.kv_heads, hk, a.total_k, row), dk, a.scale, a.dim, h);
+    store_part<D>(part_row<D>(a.v_part, w.part, a.kv_heads, hk, a.total_k, row), dv, 1.0f, a.dim, h);
+    return;
+  }
   store_cols<D>(at(a.dk, s.bk, s.k0 + mine, hk), dk, a.scale, a.dim, h);
   store_cols<D>(at(a.dv, s.bk, s.k0 + mine, hk), dv, 1.0f, a.dim, h);
 }
 
 }  // namespace
 
-hipError_t launch_attention(const AttnArgs &a, hipStream_t s) {
-  const int64_t grid = (int64_t)a.batch * a.heads * ((a.q_len + kQueries - 1) / kQueries);
-  if (a.dim <= 64)
-    attention_kernel<64><<<(unsigned)grid, kThreads, 0, s>>>(a);
-  else
-    attention_kernel<128><<<(unsigned)grid, kThreads, 0, s>>>(a);
+namespace {
+
+int64_t tiles_of(int64_t n) { return (n + 127) / 128; }
+
+// Workgroups that a pass over the rows of `heads` heads has without parts
+// (packed: an estimate, the lengths being on the device).
+int64_t units(const AttnArgs &a, int64_t len, int64_t total, int heads) {
+  if (!a.cu_q) return heads * a.batch * tiles_of(len);
+  const int64_t most = tiles_of(total) > a.batch ? tiles_of(total) : a.batch;
+  return heads * (most > 0 ? most : 1);
+}
+// keys that a query has in sight at most
+int64_t sight_of(const AttnArgs &a) { return a.window && a.window < a.k_len ? a.window : a.k_len; }
+
+}  // namespace
+
+// Keys split where the queries' tiles alone leave compute units idle: parts of
+// at least 8 tiles of 64 keys, up to 512 workgroups, joined by a second kernel.
+int attention_q_parts(const AttnArgs &a) {
+  const int64_t n = units(a, a.q_len, a.total_q, a.heads), steps = sight_of(a) / kTile;
+  int64_t parts = n >= 256 ? 1 : 512 / n;
+  if (parts > steps / 8) parts = steps / 8;
+  return (int)(parts < 1 ? 1 : parts > 16 ? 16 : parts);
+}
+// Queries split for dK and dV where key tiles leave the two workgroups that a
+// compute unit holds unbalanced or idle: parts of at least 32 tiles of 32
+// queries, up to 1024 workgroups.
+int attention_k_parts(const AttnArgs &a) {
+  const int64_t n = units(a, a.k_len, a.total_k, a.kv_heads);
+  const int64_t rows = a.window && a.window < a.q_len ? a.window : a.causal ? (a.q_len + 1) / 2 : a.q_len;
+  int64_t parts = (1024 + n - 1) / n;
+  if (parts > rows / 32 * (a.heads / a.kv_heads) / 32) parts = rows / 32 * (a.heads / a.kv_heads) / 32;
+  return (int)(parts < 1 ? 1 : parts > 16 ? 16 : parts);
+}
+
+namespace {
+template <int D>
+hipError_t forward(const AttnArgs &a, unsigned rows, hipStream_t s) {
+  attention_kernel<D><<<rows * (unsigned)a.q_parts, kThreads, 0, s>>>(a);
+  if (a.q_parts > 1) attention_join_kernel<D, kJoinO><<<rows, kThreads, 0, s>>>(a);
   return hipGetLastError();
+}
+template <int D>
+hipError_t backward(const AttnArgs &a, unsigned rows, unsigned keys, hipStream_t s) {
+  attention_dq_kernel<D><<<rows * (unsigned)a.q_parts, kThreads, 0, s>>>(a);
+  attention_dkv_kernel<D><<<keys * (unsigned)a.k_parts, kThreads, 0, s>>>(a);
+  if (a.q_parts > 1) attention_join_kernel<D, kJoinQ><<<rows, kThreads, 0, s>>>(a);
+  if (a.k_parts > 1) attention_join_kernel<D, kJoinKV><<<keys, kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+}  // namespace
+
+static_assert(kQueries == 128 && kKeys == 128, "tiles_of");
+
+hipError_t launch_attention(const AttnArgs &a, hipStream_t s) {
+  const unsigned rows = (unsigned)(a.batch * a.heads * tiles_of(a.q_len));
+  return a.dim <= 64 ? forward<64>(a, rows, s) : forward<128>(a, rows, s);
 }
 
 hipError_t launch_attention_backward(const AttnArgs &a, hipStream_t s) {
-  const int64_t q_grid = (int64_t)a.batch * a.heads * ((a.q_len + kQueries - 1) / kQueries);
-  const int64_t k_grid = (int64_t)a.batch * a.kv_heads * ((a.k_len + kKeys - 1) / kKeys);
-  if (a.dim <= 64) {
-    attention_dq_kernel<64><<<(unsigned)q_grid, kThreads, 0, s>>>(a);
-    attention_dkv_kernel<64><<<(unsigned)k_grid, kThreads, 0, s>>>(a);
-  } else {
-    attention_dq_kernel<128><<<(unsigned)q_grid, kThreads, 0, s>>>(a);
-    attention_dkv_kernel<128><<<(unsigned)k_grid, kThreads, 0, s>>>(a);
-  }
-  return hipGetLastError();
+  const unsigned rows = (unsigned)(a.batch * a.heads * tiles_of(a.q_len));
+  const unsigned keys = (unsigned)(a.batch * a.kv_heads * tiles_of(a.k_len));
+  return a.dim <= 64 ? backward<64>(a, rows, keys, s) : backward<128>(a, rows, keys, s);
 }
 
 }  // namespace nvfp4

@@ -66,20 +66,14 @@ int check_shape(const nvfp4_attention_shape *s) {
     return NVFP4_E_SHAPE;
   }
   if (!(s->scale > 0.0f) || !isfinite(s->scale)) return NVFP4_E_VALUE;
-  // workgroups and rows are counted in 32 bits: at least 64 queries or keys to a workgroup, 16 rows to one of the rows'
-  const int64_t limit = (int64_t)1 << 31;
-  const int64_t tiles = (s->q_len > s->k_len ? s->q_len : s->k_len) / 64 + 1;
-  if (s->batch > limit / tiles / s->heads || s->total_q / 16 >= limit - 1) return NVFP4_E_SHAPE;
+  // workgroups are counted in 32 bits, and a tile may be split into up to 16 parts
+  const int64_t limit = (int64_t)1 << 27, tiles = (s->q_len > s->k_len ? s->q_len : s->k_len) / 128 + 1;
+  if (s->batch > limit / tiles / s->heads) return NVFP4_E_SHAPE;
   return NVFP4_OK;
 }
 
 Heads heads_of(const nvfp4_heads *t) {
   return Heads{(uint16_t *)t->data, t->batch_stride, t->token_stride, t->head_stride};
-}
-
-// one float for every query of every head, in whole 256 bytes (not none)
-size_t stat_bytes(const nvfp4_attention_shape *s) {
-  return ((size_t)s->heads * (size_t)s->total_q * sizeof(float) + 511) & ~(size_t)255;
 }
 
 AttnArgs attn_args(const nvfp4_attention_shape *s) {
@@ -98,6 +92,43 @@ AttnArgs attn_args(const nvfp4_attention_shape *s) {
   a.causal = s->causal;
   a.scale = s->scale;
   return a;
+}
+
+// Buffers of a workspace, one after another in whole 256 bytes.
+struct Carver {
+  char *base;
+  size_t used;
+  float *floats(size_t n) {
+    float *p = base ? (float *)(base + used) : nullptr;
+    used += (n * sizeof(float) + 255) & ~(size_t)255;
+    return p;
+  }
+};
+size_t padded_dim(const AttnArgs &a) { return a.dim <= 64 ? 64 : 128; }
+size_t carve_forward(AttnArgs &a, void *workspace) {
+  Carver c = {(char *)workspace, 0};
+  a.q_parts = attention_q_parts(a);
+  if (a.q_parts > 1) {
+    const size_t rows = (size_t)a.q_parts * a.heads * a.total_q;
+    a.q_part = c.floats(rows * padded_dim(a));
+    a.lse_part = c.floats(rows);
+  }
+  return c.used;
+}
+size_t carve_backward(AttnArgs &a, void *workspace) {
+  Carver c = {(char *)workspace, 0};
+  const size_t stats = (size_t)a.heads * a.total_q;
+  a.minus_delta = c.floats(stats + 1);
+  a.minus_lse = c.floats(stats + 1);
+  a.q_parts = attention_q_parts(a);
+  a.k_parts = attention_k_parts(a);
+  if (a.q_parts > 1) a.q_part = c.floats(a.q_parts * stats * padded_dim(a));
+  if (a.k_parts > 1) {
+    const size_t rows = (size_t)a.k_parts * a.kv_heads * a.total_k;
+    a.k_part = c.floats(rows * padded_dim(a));
+    a.v_part = c.floats(rows * padded_dim(a));
+  }
+  return c.used;
 }
 
 int check_adamw(const nvfp4_adamw_tensor &t) {
@@ -165,8 +196,15 @@ int nvfp4_layernorm_backward(const nvfp4_layernorm_backward_args *a, void *works
   return finish(launch_layernorm_backward(*a, sums ? (float *)workspace : nullptr, s), s);
 }
 
+size_t nvfp4_attention_workspace_bytes(const nvfp4_attention_shape *shape) {
+  if (check_shape(shape) != NVFP4_OK) return 0;
+  AttnArgs a = attn_args(shape);
+  return carve_forward(a, nullptr);
+}
+
 int nvfp4_attention(const nvfp4_attention_shape *shape, const nvfp4_heads *q, const nvfp4_heads *k,
-                    const nvfp4_heads *v, const nvfp4_heads *o, float *lse, void *stream) {
+                    const nvfp4_heads *v, const nvfp4_heads *o, float *lse, void *workspace, size_t workspace_bytes,
+                    void *stream) {
   if (const int st = check_shape(shape)) return st;
   if (!lse) return NVFP4_E_NULL;
   if (!aligned(lse, 4)) return NVFP4_E_ALIGN;
@@ -175,19 +213,24 @@ int nvfp4_attention(const nvfp4_attention_shape *shape, const nvfp4_heads *q, co
   if (!st) st = check_heads(v, shape, shape->kv_heads, false);
   if (!st) st = check_heads(o, shape, shape->heads, true);
   if (st) return st;
+  const size_t need = nvfp4_attention_workspace_bytes(shape);
+  if (need && (!workspace || workspace_bytes < need)) return NVFP4_E_WORKSPACE;
+  if (need && !aligned(workspace, 16)) return NVFP4_E_ALIGN;
   AttnArgs a = attn_args(shape);
   a.q = heads_of(q);
   a.k = heads_of(k);
   a.v = heads_of(v);
   a.o = heads_of(o);
   a.lse = lse;
+  carve_forward(a, workspace);
   hipStream_t s = (hipStream_t)stream;
   return finish(launch_attention(a, s), s);
 }
 
 size_t nvfp4_attention_backward_workspace_bytes(const nvfp4_attention_shape *shape) {
   if (check_shape(shape) != NVFP4_OK) return 0;
-  return 2 * stat_bytes(shape);
+  AttnArgs a = attn_args(shape);
+  return carve_backward(a, nullptr);
 }
 
 int nvfp4_attention_backward(const nvfp4_attention_shape *shape, const nvfp4_heads *q, const nvfp4_heads *k,
@@ -214,8 +257,7 @@ int nvfp4_attention_backward(const nvfp4_attention_shape *shape, const nvfp4_hea
   a.dk = heads_of(dk);
   a.dv = heads_of(dv);
   a.lse = const_cast<float *>(lse);
-  a.minus_delta = (float *)workspace;
-  a.minus_lse = (float *)((char *)workspace + stat_bytes(shape));
+  carve_backward(a, workspace);
   hipStream_t s = (hipStream_t)stream;
   return finish(launch_attention_backward(a, s), s);
 }

@@ -73,6 +73,10 @@ struct AttnArgs {
   Heads q, k, v, o, d_o, dq, dk, dv;
   float *lse;    // [heads][total_q]
   float *minus_delta, *minus_lse;  // gradient: [heads][total_q], -delta and -lse / scale
+  // parts of a split pass, in binary32: [part][heads][total_q][D] and
+  // [part][heads][total_q]; [part][kv_heads][total_k][D]; D = 64 or 128
+  int q_parts, k_parts;
+  float *q_part, *lse_part, *k_part, *v_part;
   const int32_t *cu_q, *cu_k;
   int64_t total_q, total_k;
   int64_t window;  // 0: none
@@ -82,6 +86,9 @@ struct AttnArgs {
   float scale;
 };
 
+// parts that the shape's passes are split into, from its sizes alone
+int attention_q_parts(const AttnArgs &a);
+int attention_k_parts(const AttnArgs &a);
 hipError_t launch_attention(const AttnArgs &a, hipStream_t s);
 hipError_t launch_attention_backward(const AttnArgs &a, hipStream_t s);
 

@@ -116,6 +116,8 @@ CASES = [  # batch, queries, keys, heads, key heads, dim, causal, window
     (1, 100, 40, 2, 1, 128, True, 0), (1, 128, 128, 1, 1, 128, False, 0), (3, 129, 257, 2, 1, 128, True, 0),
     (1, 300, 200, 2, 2, 40, True, 17), (1, 257, 513, 6, 2, 96, True, 64), (1, 500, 500, 2, 1, 128, True, 1),
     (1, 640, 640, 8, 2, 128, True, 100), (1, 1000, 777, 2, 1, 64, False, 0), (1, 1025, 2049, 4, 1, 128, True, 0),
+    (1, 3, 5000, 2, 1, 128, True, 0), (2, 1, 4096, 8, 2, 64, True, 0), (1, 200, 3000, 4, 1, 80, False, 0),
+    (1, 2100, 300, 8, 1, 64, False, 0), (1, 1, 3333, 3, 1, 128, True, 1500), (1, 900, 2600, 2, 1, 128, True, 1300),
     (1, 511, 1, 2, 1, 128, False, 0), (1, 130, 1, 2, 1, 64, True, 0), (2, 383, 385, 2, 1, 120, True, 1000)]
 
 
@@ -136,7 +138,8 @@ def test_dense(nv, case):
 PACKED = [  # query lengths, key lengths, heads, key heads, dim, causal, window
     ([5, 0, 130, 1, 64], None, 4, 2, 64, True, 0), ([200, 33, 7], [100, 70, 0], 2, 1, 128, True, 0),
     ([0, 300], [40, 500], 4, 1, 128, True, 50), ([64, 64, 64], [64, 1, 130], 2, 2, 80, False, 0), ([0, 0], [3, 0], 1, 1, 64, True, 0),
-    ([1] * 40, None, 2, 1, 64, True, 0)]
+    ([1] * 40, None, 2, 1, 64, True, 0), ([3, 0, 60], [2500, 100, 1300], 2, 1, 128, True, 0),
+    ([1500, 2, 0], [200, 3000, 5], 6, 1, 64, False, 0)]
 
 
 @pytest.mark.parametrize("case", PACKED, ids=str)
@@ -159,8 +162,8 @@ def test_packed(nv, case):
                 cu_k=torch.tensor(ck, dtype=torch.int32, device="cuda"), max_q=max(max(nq), 1), max_k=max(max(nk), 1))
     o, lse = torch.full_like(q, 7.0), torch.full((h, q.shape[0]), 7.0, device="cuda")
     dq, dk, dv = torch.full_like(q, 7.0), torch.full_like(k, 7.0), torch.full_like(v, 7.0)
-    nv.nvfp4_attention(q, k, v, o, lse, **opts)
     ws = nv.new_attention_workspace(q, k, v, **opts)
+    nv.nvfp4_attention(q, k, v, o, lse, workspace=ws, **opts)
     nv.nvfp4_attention_backward(do, q, k, v, o, lse, dq, dk, dv, ws, **opts)
     for i in range(len(nq)):
         a, b = slice(cq[i], cq[i + 1]), slice(ck[i], ck[i + 1])

@@ -94,11 +94,11 @@ def _heads(**kw):
     return nv.nvfp4_heads(**a)
 
 
-def _attention(L, s, lse=FAKE, **kw):
+def _attention(L, s, lse=FAKE, ws=None, nbytes=0, **kw):
     t = {n: _heads() for n in ("q", "k", "v", "o")}
     t.update(kw)
     return L.nvfp4_attention(ctypes.byref(s), *[None if t[n] is None else ctypes.byref(t[n]) for n in ("q", "k", "v", "o")],
-                             lse, None)
+                             lse, ws, nbytes, None)
 
 
 SHAPES = [(dict(batch=0), SHAPE), (dict(q_len=0, total_q=0), SHAPE), (dict(k_len=0, total_k=0), SHAPE), (dict(heads=0), SHAPE),
@@ -148,6 +148,17 @@ def test_attention_outputs_do_not_overlap(L):
         assert _attention(L, s, o=_heads(**bad)) == LD
     assert _attention(L, s, lse=None) == NULL
     assert _attention(L, s, lse=FAKE + 2) == ALIGN
+
+
+def test_attention_workspace(L):
+    """Keys are split, and a workspace is wanted, where few queries meet many keys; not for other shapes."""
+    assert L.nvfp4_attention_workspace_bytes(ctypes.byref(_shape())) == 0
+    s = _shape(batch=1, q_len=4, k_len=8192, total_q=4, total_k=8192)
+    need = L.nvfp4_attention_workspace_bytes(ctypes.byref(s))
+    assert need >= 4 * (2 * 4 * 4 * 64)
+    assert _attention(L, s) == WORKSPACE
+    assert _attention(L, s, ws=FAKE, nbytes=need - 1) == WORKSPACE
+    assert _attention(L, s, ws=FAKE + 8, nbytes=need) == ALIGN
 
 
 def test_attention_backward_workspace(L):
@@ -247,6 +258,8 @@ int64_t layernorm_backward_parts(int64_t rows, int64_t) { return rows < 512 ? ro
 hipError_t launch_layernorm_backward(const nvfp4_layernorm_backward_args &, float *, hipStream_t) { ++launched; return hipErrorInvalidValue; }
 int64_t adam_ends = 0, adam_tensors = 0;
 hipError_t launch_adamw(const AdamArgs &a, hipStream_t) { ++launched; adam_ends += a.tensor(a.count - 1).end; adam_tensors += a.count; return hipSuccess; }
+int attention_q_parts(const AttnArgs &) { return 2; }
+int attention_k_parts(const AttnArgs &) { return 3; }
 hipError_t launch_attention(const AttnArgs &, hipStream_t) { ++launched; return hipErrorInvalidValue; }
 hipError_t launch_attention_backward(const AttnArgs &, hipStream_t) { ++launched; return hipErrorInvalidValue; }
 }
@@ -264,12 +277,12 @@ int main() {
   CHECK(nvfp4_layernorm_backward_workspace_bytes((int64_t)1 << 30, 32768) == (size_t)512 * 2 * 32768 * 4);
   nvfp4_attention_shape s; memset(&s, 0, sizeof s);
   nvfp4_heads h = {FAKE, 0, 64, 64};
-  CHECK(nvfp4_attention(nullptr, &h, &h, &h, &h, (float *)FAKE, nullptr) == NVFP4_E_NULL);
-  CHECK(nvfp4_attention(&s, &h, &h, &h, &h, (float *)FAKE, nullptr) == NVFP4_E_SHAPE);
+  CHECK(nvfp4_attention(nullptr, &h, &h, &h, &h, (float *)FAKE, nullptr, 0, nullptr) == NVFP4_E_NULL);
+  CHECK(nvfp4_attention(&s, &h, &h, &h, &h, (float *)FAKE, nullptr, 0, nullptr) == NVFP4_E_SHAPE);
   s.batch = INT64_MAX; s.q_len = INT64_MAX; s.k_len = INT64_MAX; s.heads = s.kv_heads = 1; s.head_dim = 64; s.scale = 1;
-  CHECK(nvfp4_attention(&s, &h, &h, &h, &h, (float *)FAKE, nullptr) == NVFP4_E_SHAPE);
+  CHECK(nvfp4_attention(&s, &h, &h, &h, &h, (float *)FAKE, nullptr, 0, nullptr) == NVFP4_E_SHAPE);
   s.batch = 1 << 30; s.q_len = s.k_len = 1 << 30; s.total_q = s.total_k = (int64_t)1 << 60; s.heads = s.kv_heads = 65535;
-  CHECK(nvfp4_attention(&s, &h, &h, &h, &h, (float *)FAKE, nullptr) == NVFP4_E_SHAPE);
+  CHECK(nvfp4_attention(&s, &h, &h, &h, &h, (float *)FAKE, nullptr, 0, nullptr) == NVFP4_E_SHAPE);
   CHECK(nvfp4_attention_backward_workspace_bytes(&s) == 0);
   CHECK(nvfp4::launched == 0);
   /* more tensors than one launch takes, and more workgroups than one grid: cut into launches */
