@@ -452,7 +452,7 @@ typedef struct {
  * [0, total] or descending are read as clamped to it, so that no
  * access leaves the tensors.
  *   q, o: heads heads; k, v: kv_heads.  data 16-byte aligned, strides
- *   multiples of 8, |token_stride| < 2^24 and not negative.  lse: device float [heads][total_q].
+ *   multiples of 8 and not negative, token_stride < 2^23.  lse: device float [heads][total_q].
  *   workspace  nvfp4_attention_workspace_bytes(shape) bytes of device scratch,
  *              16-byte aligned, not initialised: 0 (workspace may be NULL) but
  *              where few queries meet many keys and the keys are split.

@@ -72,14 +72,15 @@ __device__ __forceinline__ uint16_t *at(const Heads &t, int64_t seq, int64_t tok
   return t.p + seq * t.sb + token * t.st + (int64_t)head * t.sh;
 }
 
-// keys [lo, hi) that query i sees; off = nk - nq
+// keys [lo, hi) that query i sees; off = nk - nq.  Lengths and the window are
+// at most 2^30, which keeps these sums in 32 bits.
+__device__ __forceinline__ int within(int v, int hi) { return v < 0 ? 0 : v > hi ? hi : v; }
 __device__ __forceinline__ void sight(const AttnArgs &a, int i, int nk, int off, int &lo, int &hi) {
   lo = 0;
   hi = nk;
   if (a.causal) {
-    const int64_t end = (int64_t)i + off + 1;
-    hi = (int)clamp64(end, 0, nk);
-    if (a.window) lo = (int)clamp64(end - a.window, 0, nk);
+    hi = within(i + off + 1, nk);
+    if (a.window) lo = within(i + off + 1 - a.window, nk);
   }
 }
 
@@ -116,22 +117,13 @@ __device__ __forceinline__ void fetch_tile(const uint16_t *head, int64_t stride,
   const uint32_t r = (uint32_t)lane / T::kChunks, pitch = (uint32_t)stride * 2u;
   uint32_t c = ((uint32_t)lane % T::kChunks) ^ T::spread(r);
   c = (int)c < chunks ? c * 16u : 0u;
-  const int left = rows - row0;
+  const int left = rows - row0 - 1;
   constexpr int kSegs = R / T::kSegRows / 4;
-  if (left >= R) {
 #pragma unroll
-    for (int i = 0; i < kSegs; ++i) {
-      const int seg = wave * kSegs + i;
-      dma16(uniform_ptr(base + (uint64_t)(seg * T::kSegRows) * pitch), r * pitch + c,
-            __builtin_amdgcn_readfirstlane(lds + (uint32_t)seg * T::kSeg));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kSegs; ++i) {
-      const int seg = wave * kSegs + i, row = seg * T::kSegRows + (int)r;
-      dma16(base, (uint32_t)(row < left ? row : left - 1) * pitch + c,
-            __builtin_amdgcn_readfirstlane(lds + (uint32_t)seg * T::kSeg));
-    }
+  for (int i = 0; i < kSegs; ++i) {
+    const int seg = wave * kSegs + i, row = seg * T::kSegRows + (int)r;
+    dma16(base, __umul24((uint32_t)(row < left ? row : left), pitch) + c,
+          __builtin_amdgcn_readfirstlane(lds + (uint32_t)seg * T::kSeg));
   }
 }
 
@@ -183,12 +175,20 @@ struct Reads {
   }
 };
 
-// B operand of a row held by its lane: elements 16 c + 8 h .. of `row`, zero
+// B operands of a row held by its lane: elements 16 c + 8 h .. of `row`, zero
 // from head_dim on
-__device__ __forceinline__ bf16x8 load_row(const uint16_t *row, int c, int chunks, int h) {
-  uint4 q = make_uint4(0, 0, 0, 0);
-  if (2 * c + h < chunks) q = *reinterpret_cast<const uint4 *>(row + 16 * c + 8 * h);
-  return __builtin_bit_cast(bf16x8, q);
+template <int D>
+__device__ __forceinline__ void load_row(const uint16_t *row, int chunks, int h, bf16x8 out[D / 16]) {
+  uint4 q[D / 16];
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) q[c] = *reinterpret_cast<const uint4 *>(row + 8 * (2 * c + h < chunks ? 2 * c + h : 0));
+  if (chunks < D / 8) {
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+      if (2 * c + h >= chunks) q[c] = make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) out[c] = __builtin_bit_cast(bf16x8, q[c]);
 }
 
 // eight result registers as a B operand
@@ -204,12 +204,13 @@ __device__ __forceinline__ bf16x8 pack8(const f32x16 &v, int first) {
 // result columns as rows of memory: lane n's column, its elements times f
 template <int D>
 __device__ __forceinline__ void store_cols(uint16_t *row, const f32x16 *acc, float f, int dim, int h) {
+  const bool whole = dim == D;
 #pragma unroll
   for (int dt = 0; dt < D / 32; ++dt)
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int d = dt * 32 + 8 * g + 4 * h;
-      if (d < dim)
+      if (whole || d < dim)
         *reinterpret_cast<uint2 *>(row + d) = make_uint2(pack_bf16(acc[dt][4 * g] * f, acc[dt][4 * g + 1] * f),
                                                          pack_bf16(acc[dt][4 * g + 2] * f, acc[dt][4 * g + 3] * f));
     }
@@ -229,24 +230,32 @@ __device__ __forceinline__ void tile_barrier() {
 struct Work {
   int b, head, tile, part;
 };
-__device__ __forceinline__ Work work_of(const AttnArgs &a, int tiles, int group, int parts) {
+// n / d and n % d
+__device__ __forceinline__ uint32_t split_off(uint32_t &n, const Divisor &d) {
+  const uint32_t q = (uint32_t)(((uint64_t)n * d.by) >> d.shift), r = n - q * d.d;
+  n = q;
+  return r;
+}
+__device__ __forceinline__ Work work_of(const AttnArgs &a, const Divisor &tiles, int parts, bool by_group) {
   uint32_t w = a.cu_q && a.kv_heads < 8 ? blockIdx.x : xcd_tile(blockIdx.x, gridDim.x);
   Work r;
-  const int g = (int)(w % (uint32_t)group);
-  w /= (uint32_t)group;
-  r.part = (int)(w % (uint32_t)parts);
-  w /= (uint32_t)parts;
-  r.tile = (int)(w % (uint32_t)tiles);
-  w /= (uint32_t)tiles;
-  r.b = (int)(w % (uint32_t)a.batch);
-  r.head = (int)(w / (uint32_t)a.batch) * group + g;
+  const int g = by_group ? (int)split_off(w, a.by_group) : 0;
+  r.part = 0;
+  if (parts > 1) {
+    r.part = (int)(w % (uint32_t)parts);
+    w /= (uint32_t)parts;
+  }
+  r.tile = (int)split_off(w, tiles);
+  r.b = (int)split_off(w, a.by_batch);
+  r.head = by_group ? (int)(w * a.by_group.d) + g : (int)w;
   return r;
 }
 // the steps [lo, hi) of part `part` of `parts`
 __device__ __forceinline__ void part_of(int part, int parts, int &lo, int &hi) {
   const int n = hi - lo, at = lo;
-  lo = at + (int)((int64_t)n * part / parts);
-  hi = at + (int)((int64_t)n * (part + 1) / parts);
+  if (parts == 1) return;
+  lo = at + (int)((uint32_t)(n * part) / (uint32_t)parts);  // below 2^26 steps, at most 16 parts
+  hi = at + (int)((uint32_t)(n * (part + 1)) / (uint32_t)parts);
 }
 
 // a row of a part's binary32 results, [part][head][row][D]
@@ -277,21 +286,21 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   __shared__ __align__(16) uint8_t lds[4 * Tile<D>::bytes(kTile)];
   constexpr uint32_t kB = Tile<D>::bytes(kTile);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
-  const int group = a.heads / a.kv_heads, tiles = (a.q_len + kQueries - 1) / kQueries;
-  Work w = work_of(a, tiles, group, a.q_parts);
-  if (a.causal) w.tile = tiles - 1 - w.tile;
+  Work w = work_of(a, a.by_q_tiles, a.q_parts, true);
+  if (a.causal) w.tile = (int)a.by_q_tiles.d - 1 - w.tile;
   const Seq s = sequence(a, w.b);
   const int first = w.tile * kQueries;
   if (first >= s.nq) return;
   const int last = (first + kQueries < s.nq ? first + kQueries : s.nq) - 1, off = s.nk - s.nq;
-  const int hk = w.head / group, chunks = a.dim / 8;
+  uint32_t of_head = (uint32_t)w.head;
+  split_off(of_head, a.by_group);
+  const int hk = (int)of_head, chunks = a.dim / 8;
   const uint16_t *kh = at(a.k, s.bk, s.k0, hk), *vh = at(a.v, s.bk, s.k0, hk);
 
   const int mine = first + wave * 32 + (lane & 31), qi = mine < s.nq ? mine : s.nq - 1;
   bf16x8 q[D / 16];
   const uint16_t *qrow = at(a.q, s.bq, s.q0 + qi, w.head);
-#pragma unroll
-  for (int c = 0; c < D / 16; ++c) q[c] = load_row(qrow, c, chunks, h);
+  load_row<D>(qrow, chunks, h, q);
 
   int lo, hi, unused, begin, end;
   sight(a, qi, s.nk, off, lo, hi);
@@ -470,29 +479,29 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
   __shared__ __align__(16) uint8_t lds[4 * Tile<D>::bytes(kTile)];
   constexpr uint32_t kB = Tile<D>::bytes(kTile);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
-  const int group = a.heads / a.kv_heads, tiles = (a.q_len + kQueries - 1) / kQueries;
-  Work w = work_of(a, tiles, group, a.q_parts);
-  if (a.causal) w.tile = tiles - 1 - w.tile;
+  Work w = work_of(a, a.by_q_tiles, a.q_parts, true);
+  if (a.causal) w.tile = (int)a.by_q_tiles.d - 1 - w.tile;
   const Seq s = sequence(a, w.b);
   const int first = w.tile * kQueries;
   if (first >= s.nq) return;
   const int last = (first + kQueries < s.nq ? first + kQueries : s.nq) - 1, off = s.nk - s.nq;
-  const int hk = w.head / group, chunks = a.dim / 8;
+  uint32_t of_head = (uint32_t)w.head;
+  split_off(of_head, a.by_group);
+  const int hk = (int)of_head, chunks = a.dim / 8;
   const uint16_t *kh = at(a.k, s.bk, s.k0, hk), *vh = at(a.v, s.bk, s.k0, hk);
 
   const int mine = first + wave * 32 + (lane & 31), qi = mine < s.nq ? mine : s.nq - 1;
   bf16x8 q[D / 16], g[D / 16];
   const uint16_t *qrow = at(a.q, s.bq, s.q0 + qi, w.head), *grow = at(a.d_o, s.bq, s.q0 + qi, w.head);
-#pragma unroll
-  for (int c = 0; c < D / 16; ++c) {
-    q[c] = load_row(qrow, c, chunks, h);
-    g[c] = load_row(grow, c, chunks, h);
-  }
+  load_row<D>(qrow, chunks, h, q);
+  load_row<D>(grow, chunks, h, g);
   const uint16_t *orow = at(a.o, s.bq, s.q0 + qi, w.head);
   float delta = 0.0f;
+  bf16x8 o[D / 16];
+  load_row<D>(orow, chunks, h, o);
 #pragma unroll
   for (int c = 0; c < D / 16; ++c) {
-    const uint4 x = __builtin_bit_cast(uint4, load_row(orow, c, chunks, h)), y = __builtin_bit_cast(uint4, g[c]);
+    const uint4 x = __builtin_bit_cast(uint4, o[c]), y = __builtin_bit_cast(uint4, g[c]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) delta = fmaf(bf16_at(x, j), bf16_at(y, j), delta);
   }
@@ -581,8 +590,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attention_dkv_kerne
   __shared__ __align__(16) uint8_t lds[4 * kB + kV];
   __shared__ __align__(16) float stats[2][2][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
-  const int group = a.heads / a.kv_heads, tiles = (a.k_len + kKeys - 1) / kKeys;
-  Work w = work_of(a, tiles, 1, a.k_parts);
+  const int group = (int)a.by_group.d, tiles = (int)a.by_k_tiles.d;
+  Work w = work_of(a, a.by_k_tiles, a.k_parts, false);
   const int hk = w.head;
   // Key tiles of a causal pass differ in work, falling along the sequence.
   // Where all workgroups are resident at once, two to a compute unit, every
@@ -601,15 +610,17 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attention_dkv_kerne
   const uint32_t v_at = lds_addr(lds) + 4 * kB + (uint32_t)wave * Tile<D>::bytes(32);
   Reads<D> in(lane, lds_addr(lds));
   const Reads<D> values(lane, v_at);  // the wave's own 32 rows, written and read by it alone
+  load_row<D>(krow, chunks, h, k);
+  {
+    bf16x8 v[D / 16];
+    load_row<D>(vrow, chunks, h, v);
 #pragma unroll
-  for (int c = 0; c < D / 16; ++c) {
-    k[c] = load_row(krow, c, chunks, h);
-    values.set_row(c, load_row(vrow, c, chunks, h));
+    for (int c = 0; c < D / 16; ++c) values.set_row(c, v[c]);
   }
   // the queries [lo, hi) that see key j: j - off <= i < j - off + window, with causal
   const auto seen_by = [&](int j, int &lo, int &hi) {
-    lo = a.causal ? (int)clamp64((int64_t)j - off, 0, s.nq) : 0;
-    hi = a.window ? (int)clamp64((int64_t)j - off + a.window, 0, s.nq) : s.nq;
+    lo = a.causal ? within(j - off, s.nq) : 0;
+    hi = a.window ? within(j - off + a.window, s.nq) : s.nq;
   };
   int begin, end, all_lo, all_hi, unused;
   seen_by(first, begin, unused);
@@ -642,8 +653,10 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attention_dkv_kerne
   part_of(w.part, a.k_parts, step, steps);
   int head = hk * group, t = t0, stage = 0;
   if (step < steps) {
-    head += step / (t1 - t0);
-    t += step % (t1 - t0);
+    if (step > 0) {
+      head += step / (t1 - t0);
+      t += step % (t1 - t0);
+    }
     fetch(head, t, 0);
   }
   for (; step < steps; ++step) {

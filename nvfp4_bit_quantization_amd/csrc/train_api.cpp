@@ -37,7 +37,7 @@ int norm_shape(int64_t rows, int64_t cols) {
 int check_heads(const nvfp4_heads *t, const nvfp4_attention_shape *s, int32_t heads, bool output) {
   if (!t || !t->data) return NVFP4_E_NULL;
   const bool batched = !s->cu_q && s->batch > 1;
-  if (t->token_stride < 0 || t->token_stride >= ((int64_t)1 << 24) || t->head_stride < 0 ||
+  if (t->token_stride < 0 || t->token_stride >= ((int64_t)1 << 23) || t->head_stride < 0 ||
       (batched && t->batch_stride < 0))
     return NVFP4_E_LD;
   if (output && (t->token_stride < s->head_dim || (heads > 1 && t->head_stride < s->head_dim) ||
@@ -69,6 +69,8 @@ int check_shape(const nvfp4_attention_shape *s) {
   // workgroups are counted in 32 bits, and a tile may be split into up to 16 parts
   const int64_t limit = (int64_t)1 << 27, tiles = (s->q_len > s->k_len ? s->q_len : s->k_len) / 128 + 1;
   if (s->batch > limit / tiles / s->heads) return NVFP4_E_SHAPE;
+  // and a key tile's steps over its heads' query tiles in 26 bits
+  if ((s->q_len / 32 + 1) * (s->heads / s->kv_heads) >= (int64_t)1 << 26) return NVFP4_E_SHAPE;
   return NVFP4_OK;
 }
 
@@ -82,7 +84,7 @@ AttnArgs attn_args(const nvfp4_attention_shape *s) {
   a.cu_k = s->cu_k;
   a.total_q = s->total_q;
   a.total_k = s->total_k;
-  a.window = s->window;
+  a.window = s->window < ((int64_t)1 << 30) ? (int)s->window : 1 << 30;  // no length exceeds that
   a.q_len = (int)s->q_len;
   a.k_len = (int)s->k_len;
   a.batch = (int)s->batch;
@@ -91,6 +93,10 @@ AttnArgs attn_args(const nvfp4_attention_shape *s) {
   a.dim = s->head_dim;
   a.causal = s->causal;
   a.scale = s->scale;
+  a.by_group = divisor((uint32_t)(s->heads / s->kv_heads));
+  a.by_batch = divisor((uint32_t)s->batch);
+  a.by_q_tiles = divisor((uint32_t)((s->q_len + 127) / 128));
+  a.by_k_tiles = divisor((uint32_t)((s->k_len + 127) / 128));
   return a;
 }
 

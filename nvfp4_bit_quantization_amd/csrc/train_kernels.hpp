@@ -69,6 +69,19 @@ struct Heads {
   int64_t sb, st, sh;  // elements between sequences, tokens, heads
 };
 
+// division of a 31-bit n by d as a product: n / d = (n by) >> shift with
+// by = ceil(2^shift / d) and shift = 31 + ceil(log2 d), since the excess
+// n (by d - 2^shift) / (d 2^shift) < n / 2^31 / d stays below 1 / d
+struct Divisor {
+  uint32_t d, by, shift;
+};
+inline Divisor divisor(uint32_t d) {
+  Divisor r = {d, 0u, 31u};
+  while (((uint64_t)1 << (r.shift - 31)) < d) ++r.shift;
+  r.by = (uint32_t)((((uint64_t)1 << r.shift) + d - 1) / d);
+  return r;
+}
+
 struct AttnArgs {
   Heads q, k, v, o, d_o, dq, dk, dv;
   float *lse;    // [heads][total_q]
@@ -79,11 +92,12 @@ struct AttnArgs {
   float *q_part, *lse_part, *k_part, *v_part;
   const int32_t *cu_q, *cu_k;
   int64_t total_q, total_k;
-  int64_t window;  // 0: none
+  int window;  // 0: none
   int q_len, k_len;
   int batch, heads, kv_heads, dim;
   int causal;
   float scale;
+  Divisor by_group, by_batch, by_q_tiles, by_k_tiles;  // heads of a key head, sequences, tiles of 128 rows
 };
 
 // parts that the shape's passes are split into, from its sizes alone

@@ -109,6 +109,7 @@ SHAPES = [(dict(batch=0), SHAPE), (dict(q_len=0, total_q=0), SHAPE), (dict(k_len
           (dict(cu_q=FAKE, cu_k=FAKE, total_k=1 << 31), SHAPE), (dict(cu_q=FAKE + 2, cu_k=FAKE), ALIGN),
           (dict(scale=0.0), VALUE), (dict(scale=-1.0), VALUE), (dict(scale=float("nan")), VALUE),
           (dict(scale=float("inf")), VALUE), (dict(q_len=(1 << 30) + 1, total_q=(1 << 31) + 2), SHAPE),
+          (dict(batch=1, q_len=1 << 30, k_len=128, heads=2, kv_heads=1, total_q=1 << 30, total_k=128), SHAPE),
           (dict(batch=1 << 29, q_len=64, k_len=64, total_q=1 << 35, total_k=1 << 35), SHAPE)]
 
 
@@ -122,7 +123,7 @@ def test_attention_shape_refusals(L, change, status):
 
 
 TENSORS = [(dict(data=None), NULL), (dict(data=FAKE + 8), ALIGN), (dict(token_stride=260), ALIGN), (dict(head_stride=60), ALIGN),
-           (dict(batch_stride=4), ALIGN), (dict(token_stride=-256), LD), (dict(token_stride=1 << 24), LD),
+           (dict(batch_stride=4), ALIGN), (dict(token_stride=-256), LD), (dict(token_stride=1 << 23), LD),
            (dict(head_stride=-64), LD), (dict(batch_stride=-8), LD)]
 
 
@@ -294,6 +295,19 @@ int main() {
   c.beta1 = 0.9; c.beta2 = 0.99; c.eps = 1e-8f; c.step = ((int64_t)1 << 47) - 1; c.seed = ~0ull;
   CHECK(nvfp4_adamw(t, 1000, &c, nullptr) == NVFP4_OK);
   CHECK(nvfp4::adam_tensors == 900 && nvfp4::adam_ends == 900 * (((int64_t)1 << 34) / nvfp4::kAdamChunk));
+  /* division by a product: at the borders of every quotient, for small, round and large divisors */
+  for (uint64_t k = 0; k < 3000; ++k) {
+    const uint32_t d = k < 2000 ? (uint32_t)k + 1 : k < 2090 ? (1u << (k - 2000) / 3) + (uint32_t)(k % 3) - 1 : (uint32_t)(k * 2654435761u % 0x7FFFFFFFu) + 1;
+    if (d == 0) continue;
+    const nvfp4::Divisor v = nvfp4::divisor(d);
+    for (uint64_t q = 0, j = 0; j < 200; ++j, q = j < 100 ? j : (0x7FFFFFFFull / d) - (199 - j)) {
+      for (uint64_t r = 0; r < 2; ++r) {
+        const uint64_t n = r ? q * d + d - 1 : q * d;
+        if (n > 0x7FFFFFFF || q > 0x7FFFFFFF) continue;
+        CHECK((n * v.by) >> v.shift == n / d);
+      }
+    }
+  }
   printf("ok\n");
   return 0;
 }
