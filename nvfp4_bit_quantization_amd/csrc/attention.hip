@@ -175,6 +175,27 @@ struct Reads {
   }
 };
 
+// Scores out of sight: of 32 rows from r0 on (register i of half h is row
+// row_of(i, h)) those below lo and from hi on become -inf.  Which of the two
+// limits falls within the rows is uniform over the wave.
+template <int N>
+__device__ __forceinline__ void hide(f32x16 (&p)[N], int lo, int hi, bool below, bool above, int h) {
+  if (above) {
+    const int n = hi - 4 * h;
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) p[u][i] = n > 32 * u + row_of(i, 0) ? p[u][i] : -INFINITY;
+  }
+  if (below) {
+    const int n = lo - 4 * h;
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) p[u][i] = n <= 32 * u + row_of(i, 0) ? p[u][i] : -INFINITY;
+  }
+}
+
 // B operands of a row held by its lane: elements 16 c + 8 h .. of `row`, zero
 // from head_dim on
 template <int D>
@@ -348,15 +369,7 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
       __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
     }
     __builtin_amdgcn_sched_group_barrier(kMfma, D / 16, 0);
-    if (k0 + kTile > all_hi || k0 < all_lo) {
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int j = k0 + u * 32 + row_of(i, h);
-          if (j >= hi || j < lo) p[u][i] = -INFINITY;
-        }
-    }
+    hide(p, lo - k0, hi - k0, k0 < all_lo, k0 + kTile > all_hi, h);
     float m = fmaxf(p[0][0], p[1][0]);
 #pragma unroll
     for (int i = 1; i < 16; ++i) m = fmaxf(m, fmaxf(p[0][i], p[1][i]));
@@ -542,28 +555,47 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
       fetch_tile<D, kTile>(vh, a.v.st, k0 + kTile, s.nk, chunks, lds_addr(lds) + (uint32_t)(stage ^ 1) * 2 * kB + kB, wave, lane);
     }
     if (k0 >= any_hi || k0 + kTile <= any_lo) continue;
-    const bool masked = k0 + kTile > all_hi || k0 < all_lo;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      f32x16 p = zero16(), d = zero16();
+      // as in the dK, dV pass: operands two steps ahead, products between the
+      // exponentials of the other 16 keys
+      constexpr int kN = D / 16, kM = D / 32;
+      f32x16 pd[1] = {zero16()}, d = zero16();
+      f32x16 &p = pd[0];
+      bf16x8 ka[kN], va[kN], t[2 * kM];
+      const auto read_step = [&](int c) {
+        ka[c] = in.rows(0, u * 32, c);
+        va[c] = in.rows(kB, u * 32, c);
+      };
+      const auto read_cols = [&](int i) { t[i] = in.cols(0, u * 32 + i / kM * 16, i % kM); };
+      read_step(0);
+      read_step(1);
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) p = mfma(in.rows(0, u * 32, c), q[c], p);
-      if (masked) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int j = k0 + u * 32 + row_of(i, h);
-          p[i] = j < hi && j >= lo ? p[i] : -INFINITY;
-        }
+      for (int c = 0; c < kN; ++c) {
+        if (c + 2 < kN)
+          read_step(c + 2);
+        else
+          read_cols(c + 2 - kN);
+        p = mfma(ka[c], q[c], p);
+        d = mfma(va[c], g[c], d);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      hide(pd, lo - k0 - u * 32, hi - k0 - u * 32, k0 + u * 32 < all_lo, k0 + u * 32 + 32 > all_hi, h);
+      const auto element = [&](int i) { p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], c2, start)) * (d[i] - delta); };
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) d = mfma(in.rows(kB, u * 32, c), g[c], d);
+      for (int i = 0; i < 8; ++i) element(i);
+      bf16x8 b = pack8(p, 0);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) p[i] = __builtin_amdgcn_exp2f(fmaf(p[i], c2, start)) * (d[i] - delta);
+      for (int i = 0; i < 2 * kM; ++i) {
+        if (i + 2 < 2 * kM) read_cols(i + 2);
+        acc[i % kM] = mfma(t[i], b, acc[i % kM]);
+        if (i < kM) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const bf16x8 b = pack8(p, 8 * c);
-#pragma unroll
-        for (int dt = 0; dt < D / 32; ++dt) acc[dt] = mfma(in.cols(0, u * 32 + c * 16, dt), b, acc[dt]);
+          for (int j = 0; j < 8 / kM; ++j) element(8 + i * (8 / kM) + j);
+        }
+        if (i == kM - 1) b = pack8(p, 8);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
@@ -671,7 +703,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attention_dkv_kerne
     for (int u = 0; u < kRows / 32; ++u) {
       // the accumulators start from -lse / scale and -delta
       constexpr int kN = D / 16;
-      f32x16 p, d;
+      f32x16 pd[1], d;
+      f32x16 &p = pd[0];
       int l = lane;
       asm volatile("" : "+v"(l));  // what is formed of it stays out of registers between tiles
 #pragma unroll
@@ -707,10 +740,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attention_dkv_kerne
         int lo, hi;
         asm volatile("" : "+v"(l));
         seen_by(first + wave * 32 + (l & 31), lo, hi);
-        lo -= i0 + 32 * u;
-        hi -= i0 + 32 * u;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = row_of(i, l >> 5) < hi && row_of(i, l >> 5) >= lo ? p[i] : -INFINITY;
+        hide(pd, lo - i0 - 32 * u, hi - i0 - 32 * u, i0 + 32 * u < all_lo, i0 + 32 * u + 32 > all_hi, l >> 5);
       }
       const auto element = [&](int i) {
         p[i] = __builtin_amdgcn_exp2f(p[i] * c2);
