@@ -27,7 +27,7 @@ constexpr int kTile = 64;               // rows of a staged tile
 constexpr int kValu = 0x2, kMfma = 0x8, kDsRead = 0x100;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr float kLow = -1e30f;          // below every score; finite, so that differences stay numbers
+constexpr float kLow = -3e38f;          // below every score; finite, so that differences stay numbers
 
 __device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);

@@ -302,7 +302,7 @@ int nvfp4_adamw(const nvfp4_adamw_tensor *tensors, int64_t n_tensors, const nvfp
     const bool more = i < n_tensors, extra = more && (tensors[i].m_scale || tensors[i].copy || tensors[i].amax);
     // at most 2^22 workgroups a tensor: the running count stays in 32 bits
     if (a.count && (!more || end > (1u << 30) ||
-                    (a.count + 1) * kAdamTensorWords + (extras + extra) * kAdamExtraWords > kAdamWords)) {
+                    (a.count + 1) * sizeof(AdamTensor) + (extras + extra) * sizeof(AdamExtra) > kAdamBytes)) {
       if (launch_adamw(a, s) != hipSuccess) return NVFP4_E_HIP;
       a.count = extras = 0;
       end = 0;
@@ -325,11 +325,11 @@ int nvfp4_adamw(const nvfp4_adamw_tensor *tensors, int64_t n_tensors, const nvfp
     if (extra) {
       const AdamExtra e = {t.m_scale, t.v_scale, (uint16_t *)t.copy, t.amax};
       d.flags |= AF_EXTRA | (uint32_t)extras << AF_EXTRA_SHIFT;
-      memcpy(a.words + kAdamWords - ++extras * kAdamExtraWords, &e, sizeof e);
+      memcpy(a.bytes + kAdamBytes - ++extras * sizeof e, &e, sizeof e);
     }
     end += (uint32_t)((t.n + kAdamChunk - 1) / kAdamChunk);
     d.end = end;
-    memcpy(a.words + a.count++ * kAdamTensorWords, &d, sizeof d);
+    memcpy(a.bytes + a.count++ * sizeof d, &d, sizeof d);
   }
   return finish(hipSuccess, s);
 }

@@ -44,11 +44,11 @@ struct AdamExtra {  // what not every tensor has
 };
 
 // The descriptors travel as kernel arguments: AdamTensors from the front of
-// the words, AdamExtras from the back, as many as 4 KiB of arguments hold (71
+// the bytes, AdamExtras from the back, as many as 4 KiB of arguments hold (71
 // tensors without extras, 45 with).
-constexpr int kAdamWords = 500, kAdamTensorWords = sizeof(AdamTensor) / 8, kAdamExtraWords = sizeof(AdamExtra) / 8;
+constexpr int kAdamBytes = 4000;
 struct AdamArgs {
-  uint64_t words[kAdamWords];
+  alignas(8) unsigned char bytes[kAdamBytes];
   int count;
   int sr;
   float lr, beta1, one_minus_beta1, beta2, one_minus_beta2, eps;
@@ -56,8 +56,8 @@ struct AdamArgs {
   uint32_t seed_lo, seed_hi, step_lo, tag;
   const float *grad_scale;
 
-  __host__ __device__ const AdamTensor &tensor(int i) const { return ((const AdamTensor *)words)[i]; }
-  __host__ __device__ const AdamExtra &extra(int i) const { return ((const AdamExtra *)(words + kAdamWords))[-1 - i]; }
+  __host__ __device__ const AdamTensor &tensor(int i) const { return ((const AdamTensor *)bytes)[i]; }
+  __host__ __device__ const AdamExtra &extra(int i) const { return ((const AdamExtra *)(bytes + kAdamBytes))[-1 - i]; }
 };
 static_assert(sizeof(AdamTensor) == 56 && sizeof(AdamExtra) == 32 && sizeof(AdamArgs) <= 4096, "kernel arguments");
 
