@@ -16,8 +16,8 @@ namespace {
 // can be read 16 bytes at a time, else elements TPR apart, which keeps single
 // element accesses of a wave contiguous
 template <bool VEC, int V>
-__device__ __forceinline__ int64_t column(int v, int j, int t, int tpr) {
-  return VEC ? (int64_t)(v * tpr + t) * 8 + j : (int64_t)(v * 8 + j) * tpr + t;
+__device__ __forceinline__ int column(int v, int j, int t, int tpr) {
+  return VEC ? (v * tpr + t) * 8 + j : (v * 8 + j) * tpr + t;
 }
 
 // a thread's share of a row as it stands in memory, zero outside [0, cols):
@@ -30,7 +30,7 @@ struct Group<uint16_t> {
   __device__ __forceinline__ void load(const uint16_t *p) { q = *reinterpret_cast<const uint4 *>(p); }
   __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void load1(int j, const uint16_t *p, bool in) {
-    const uint32_t x = in ? *p : 0u;
+    const uint32_t x = *p & (in ? 0xFFFFu : 0u);
     uint32_t &w = (j >> 1) == 0 ? q.x : (j >> 1) == 1 ? q.y : (j >> 1) == 2 ? q.z : q.w;
     w = j & 1 ? w | x << 16 : x;
   }
@@ -45,7 +45,7 @@ struct Group<float> {
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
   __device__ __forceinline__ void load1(int j, const float *p, bool in) {
-    const float x = in ? *p : 0.0f;
+    const float y = *p, x = in ? y : 0.0f;
     (j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : j == 3 ? a.w : j == 4 ? b.x : j == 5 ? b.y : j == 6 ? b.z : b.w) = x;
   }
   __device__ __forceinline__ float at(int j) const {
@@ -57,17 +57,16 @@ template <bool VEC, int V, typename T>
 __device__ __forceinline__ void fetch_row(const T *row, int cols, int t, int tpr, Group<T> g[V]) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
+    // loads without branches: past the end from the row's start, and dropped
     if constexpr (VEC) {
-      const int64_t c = column<true, V>(v, 0, t, tpr);
-      if (c < cols)
-        g[v].load(row + c);
-      else
-        g[v].zero();
+      const int c = column<true, V>(v, 0, t, tpr);
+      g[v].load(row + (c < cols ? c : 0));
+      if (c >= cols) g[v].zero();
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int64_t c = column<false, V>(v, j, t, tpr);
-        g[v].load1(j, row + c, c < cols);
+        const int c = column<false, V>(v, j, t, tpr);
+        g[v].load1(j, row + (c < cols ? c : 0), c < cols);
       }
     }
   }
@@ -87,18 +86,22 @@ __device__ __forceinline__ void store_row(T *row, int cols, int t, int tpr, cons
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if constexpr (VEC) {
-      const int64_t c = column<true, V>(v, 0, t, tpr);
+      const int c = column<true, V>(v, 0, t, tpr);
       if (c < cols) store8(row + c, in[v]);
+    } else if (column<false, V>(v, 8, 0, tpr) <= cols) {  // the whole row's threads
+#pragma unroll
+      for (int j = 0; j < 8; ++j) store1(row + column<false, V>(v, j, t, tpr), in[v][j]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int64_t c = column<false, V>(v, j, t, tpr);
+        const int c = column<false, V>(v, j, t, tpr);
         if (c < cols) store1(row + c, in[v][j]);
       }
     }
   }
 }
 
+// a thread's share of a weight
 template <bool VEC, int V>
 __device__ __forceinline__ void load_weight(const void *w, int bf16, int cols, int t, int tpr, float out[V][8]) {
   if (bf16)
@@ -106,6 +109,10 @@ __device__ __forceinline__ void load_weight(const void *w, int bf16, int cols, i
   else
     load_row<VEC, V>((const float *)w, cols, t, tpr, out);
 }
+// Workgroups of up to 512 threads keep the weights in registers and load the
+// next row ahead.  Those of 1024 have 128 registers to a thread, which a row
+// of more than 8192 elements takes up: they read both when they are due.
+constexpr bool holds(int nt) { return nt <= 512; }
 
 // blockDim = (TPR, rows per workgroup); more than one row only when TPR = 64.
 // The next row is loaded while this one is worked on.  Each wave takes the mean
@@ -121,21 +128,23 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
   const float inv = 1.0f / (float)cols;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  constexpr bool kHold = holds(NT);
+  const bool w_bf16 = a.w_dtype == NVFP4_BF16;
   Group<TX> gx[V], gr[V];
-  if (r < a.rows) {
+  if (kHold && r < a.rows) {
     fetch_row<VEC, V>((const TX *)a.x + r * a.ld_x, cols, t, tpr, gx);
     if (a.residual) fetch_row<VEC, V>((const TX *)a.residual + r * a.ld_residual, cols, t, tpr, gr);
   }
   float w[V][8], b[V][8], top = 0.0f;
-  load_weight<VEC, V>(a.weight, a.w_dtype == NVFP4_BF16, cols, t, tpr, w);
-  if (a.bias) {
-    load_weight<VEC, V>(a.bias, a.w_dtype == NVFP4_BF16, cols, t, tpr, b);
-  } else {
+  const auto weights = [&] {
+    load_weight<VEC, V>(a.weight, w_bf16, cols, t, tpr, w);
+    if (a.bias) load_weight<VEC, V>(a.bias, w_bf16, cols, t, tpr, b);
+  };
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+  for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) b[v][j] = 0.0f;
-  }
+    for (int j = 0; j < 8; ++j) b[v][j] = 0.0f;
+  if (kHold) weights();
   int mine = 0;
 #pragma unroll
   for (int v = 0; v < V; ++v)
@@ -146,6 +155,10 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
   int turn = 0;
   for (; r < a.rows; r += step) {
     float x[V][8];
+    if (!kHold) {
+      fetch_row<VEC, V>((const TX *)a.x + r * a.ld_x, cols, t, tpr, gx);
+      if (a.residual) fetch_row<VEC, V>((const TX *)a.residual + r * a.ld_residual, cols, t, tpr, gr);
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -156,7 +169,7 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[v][j] = rounded<TX>(x[v][j] + gr[v].at(j));
     }
-    if (r + step < a.rows) {
+    if (kHold && r + step < a.rows) {
       fetch_row<VEC, V>((const TX *)a.x + (r + step) * a.ld_x, cols, t, tpr, gx);
       if (a.residual) fetch_row<VEC, V>((const TX *)a.residual + (r + step) * a.ld_residual, cols, t, tpr, gr);
     }
@@ -194,6 +207,7 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
       a.mean[r] = mean;
       a.rstd[r] = rstd;
     }
+    if (!kHold) weights();
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -207,59 +221,63 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
   if (a.amax) fold_max(a.amax, top);
 }
 
-// The gradient: a row's two sums in one exchange, the next row loaded ahead;
-// the sums over rows stay in registers and are written once per workgroup, [blockIdx][dweight, dbias][cols].
+// The gradient: a row's two sums in one exchange; h and dy * weight are formed
+// twice from the row as it was loaded, before and after that, which keeps fewer
+// registers than holding them.  The sums over rows stay in registers and are
+// written once per workgroup, [blockIdx][dweight, dbias][cols].
 template <typename TX, typename TY, bool VEC, int V, int NT>
 __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_backward_args a, float *partials) {
   __shared__ float2 slots[2][16];
-  __shared__ float both[4][64 * 8];
+  __shared__ float both[NT == 1024 ? 1 : 4][8][64];
+  constexpr bool kHold = holds(NT);
   const int t = threadIdx.x, tpr = blockDim.x, waves = tpr >> 6;
   const int cols = (int)a.cols;
   const float inv = 1.0f / (float)cols;
+  const bool w_bf16 = a.w_dtype == NVFP4_BF16;
   float w[V][8], dw[V][8], db[V][8], top = 0.0f;
-  load_weight<VEC, V>(a.weight, a.w_dtype == NVFP4_BF16, cols, t, tpr, w);
+  if (kHold) load_weight<VEC, V>(a.weight, w_bf16, cols, t, tpr, w);
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[v][j] = db[v][j] = 0.0f;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
   int64_t r = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  Group<TX> gx[V], gd[V];
-  Group<TY> gy[V];
-  float next_mean = 0.0f, next_rstd = 0.0f;
-  const auto fetch = [&](int64_t row) {
-    fetch_row<VEC, V>((const TX *)a.x + row * a.ld_x, cols, t, tpr, gx);
-    fetch_row<VEC, V>((const TY *)a.dy + row * a.ld_dy, cols, t, tpr, gy);
-    next_mean = a.mean[row];
-    next_rstd = a.rstd[row];
+  Group<TX> gx[V], next_x[V], gd[V];
+  Group<TY> gy[V], next_y[V];
+  float mean = 0.0f, rstd = 0.0f, next_mean = 0.0f, next_rstd = 0.0f;
+  const auto fetch = [&](int64_t row, Group<TX> *x, Group<TY> *y, float &m, float &s) {
+    fetch_row<VEC, V>((const TX *)a.x + row * a.ld_x, cols, t, tpr, x);
+    fetch_row<VEC, V>((const TY *)a.dy + row * a.ld_dy, cols, t, tpr, y);
+    m = a.mean[row];
+    s = a.rstd[row];
   };
-  if (r < a.rows) fetch(r);
+  if (kHold && r < a.rows) fetch(r, next_x, next_y, next_mean, next_rstd);
   int turn = 0;
   for (; r < a.rows; r += step) {
-    float x[V][8], g[V][8];
-    const float mean = next_mean, rstd = next_rstd;
+    if (kHold) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[v][j] = gx[v].at(j);
-        g[v][j] = gy[v].at(j);
+      for (int v = 0; v < V; ++v) {
+        gx[v] = next_x[v];
+        gy[v] = next_y[v];
       }
-    if (a.dsum) fetch_row<VEC, V>((const TX *)a.dsum + r * a.ld_dsum, cols, t, tpr, gd);
-    if (r + step < a.rows) fetch(r + step);
+      mean = next_mean;
+      rstd = next_rstd;
+      if (a.dsum) fetch_row<VEC, V>((const TX *)a.dsum + r * a.ld_dsum, cols, t, tpr, gd);
+      if (r + step < a.rows) fetch(r + step, next_x, next_y, next_mean, next_rstd);
+    } else {
+      fetch(r, gx, gy, mean, rstd);
+      load_weight<VEC, V>(a.weight, w_bf16, cols, t, tpr, w);
+    }
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {  // past the end: dy = w = 0
-        const float h = (x[v][j] - mean) * rstd, dy = g[v][j];
+        const float h = (gx[v].at(j) - mean) * rstd, dy = gy[v].at(j), q = dy * w[v][j];
         dw[v][j] = fmaf(dy, h, dw[v][j]);
         db[v][j] += dy;
-        const float q = dy * w[v][j];
         s1 += q;
         s2 = fmaf(q, h, s2);
-        x[v][j] = h;
-        g[v][j] = q;
       }
     s1 = wave_sum(s1);
     s2 = wave_sum(s2);
@@ -276,10 +294,18 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
       turn ^= 1;
     }
     const float c1 = s1 * inv, c2 = s2 * inv;
+    if (!kHold) {
+      if (a.dsum) fetch_row<VEC, V>((const TX *)a.dsum + r * a.ld_dsum, cols, t, tpr, gd);
+      load_weight<VEC, V>(a.weight, w_bf16, cols, t, tpr, w);
+    }
+    float x[V][8];
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[v][j] = rstd * (g[v][j] - fmaf(x[v][j], c2, c1));
+      for (int j = 0; j < 8; ++j) {
+        const float h = (gx[v].at(j) - mean) * rstd;
+        x[v][j] = rstd * (gy[v].at(j) * w[v][j] - fmaf(h, c2, c1));
+      }
     if (a.dsum) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
@@ -298,28 +324,29 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
   if (a.amax) fold_max(a.amax, top);
   if (!partials) return;
   float *out = partials + (int64_t)blockIdx.x * 2 * cols;
+  if (blockDim.y == 1) {
+    store_row<VEC, V>(out, cols, t, tpr, dw);
+    store_row<VEC, V>(out + cols, cols, t, tpr, db);
+    return;
+  }
+  // the rows of the workgroup's four waves, added in their order: each wave
+  // joins two of the eight elements of every thread's group
+  if constexpr (NT != 1024) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k, out += cols) {
-    if (blockDim.y == 1) {
-      store_row<VEC, V>(out, cols, t, tpr, k ? db : dw);
-      continue;
-    }
+    for (int k = 0; k < 2; ++k, out += cols)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {  // the rows of the workgroup's waves, added in their order
-      __syncthreads();
+      for (int v = 0; v < V; ++v) {
+        if (k || v) __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 8; ++j) both[threadIdx.y][j * 64 + t] = k ? db[v][j] : dw[v][j];
-      __syncthreads();
-      if (threadIdx.y == 0) {
+        for (int j = 0; j < 8; ++j) both[threadIdx.y][j][t] = k ? db[v][j] : dw[v][j];
+        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float s = 0.0f;
-          for (int y = 0; y < (int)blockDim.y; ++y) s += both[y][j * 64 + t];
-          const int64_t c = column<VEC, V>(v, j, t, tpr);
+        for (int i = 0; i < 2; ++i) {
+          const int j = 2 * threadIdx.y + i, c = column<VEC, V>(v, j, t, tpr);
+          const float s = (both[0][j][t] + both[1][j][t]) + (both[2][j][t] + both[3][j][t]);
           if (c < cols) out[c] = s;
         }
       }
-    }
   }
 }
 
@@ -426,8 +453,12 @@ hipError_t launch_layernorm(const nvfp4_layernorm_args &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// of the gradient: at least four rows to a workgroup beyond one to a compute
+// unit, since each adds a row to what the second kernel reads
 int64_t layernorm_backward_parts(int64_t rows, int64_t cols) {
-  return resident(split_of(cols), rows, 12);
+  const Split p = split_of(cols);
+  const int64_t most = resident(p, rows, 12), few = (rows / p.block.y + 3) / 4;
+  return most <= 256 || most < few ? most : few > 256 ? few : 256;
 }
 
 hipError_t launch_layernorm_backward(const nvfp4_layernorm_backward_args &a, float *partials, hipStream_t s) {
