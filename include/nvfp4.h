@@ -381,9 +381,8 @@ typedef struct {
  * max(*amax, max |y|) over the stored y (an atomic maximum: the caller
  * initialises it), which is what NVFP4_AMAX_GIVEN asks of a quantisation of y
  * without the RHT.  y may be x or residual, sum may be x or residual.
- * rows < 2^31, cols <= 32768.  One kernel.  Pointers that are 16-byte aligned, row
- * strides that are multiples of 16 bytes and cols % 8 == 0 give 16-byte
- * accesses; element-aligned ones are accepted and slower.
+ * rows < 2^31, cols <= 32768.  One kernel.  Pointers need their elements'
+ * alignment; rows that begin on 16 bytes are quickest.
  */
 int nvfp4_layernorm(const nvfp4_layernorm_args *args, void *stream);
 
@@ -530,8 +529,7 @@ typedef struct {
  * m = v = 0 (8-bit: zero bytes, any scales) starts.
  *   tensors  host array of n_tensors >= 1; at most one amax, copy, param or
  *            state buffer of one belongs to another.
- * Arrays that are 16-byte aligned (E4M3 bytes: 8) give wide accesses;
- * element-aligned ones are accepted and slower.  lr, step and the other
+ * Arrays need their elements' alignment; those on 16 bytes are quickest.  lr, step and the other
  * scalars are taken at the call: a captured graph repeats them.
  * One kernel for every 45 to 71 tensors (fewer with scales, copies or maxima).
  */

@@ -79,8 +79,8 @@ __device__ __forceinline__ void decode8(uint2 q, uint32_t scale, float x[8]) {
 
 // 8 elements, `have` of them in the tensor
 template <typename T>
-__device__ __forceinline__ void get8(const T *p, bool vec, int have, float v[8]) {
-  if (vec && have == 8) {
+__device__ __forceinline__ void get8(const T *p, int have, float v[8]) {
+  if (have == 8) {
     load8(p, v);
   } else {
 #pragma unroll
@@ -91,19 +91,17 @@ __device__ __forceinline__ void get8(const T *p, bool vec, int have, float v[8])
 // the next step (two weights of 5120x20480: 1203 -> 1129 us; with 8-bit states,
 // whose traffic is a third, no gain there and 8 % lost on tensors that the
 // caches hold)
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ void stream8(uint16_t *p, const float v[8]) {
-  const uint4 q = packed8(v);
-  __builtin_nontemporal_store((u32x4){q.x, q.y, q.z, q.w}, reinterpret_cast<u32x4 *>(p));
+  __builtin_nontemporal_store(packed8(v), reinterpret_cast<u32x4_at2 *>(p));
 }
 __device__ __forceinline__ void stream8(float *p, const float v[8]) {
-  u32x4 *q = reinterpret_cast<u32x4 *>(p);
-  __builtin_nontemporal_store((u32x4){__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])}, q);
-  __builtin_nontemporal_store((u32x4){__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])}, q + 1);
+  f32x4_at4 *q = reinterpret_cast<f32x4_at4 *>(p);
+  __builtin_nontemporal_store((f32x4){v[0], v[1], v[2], v[3]}, q);
+  __builtin_nontemporal_store((f32x4){v[4], v[5], v[6], v[7]}, q + 1);
 }
 template <bool STREAM, typename T>
-__device__ __forceinline__ void put8(T *p, bool vec, int have, const float v[8]) {
-  if (vec && have == 8) {
+__device__ __forceinline__ void put8(T *p, int have, const float v[8]) {
+  if (have == 8) {
     if constexpr (STREAM)
       stream8(p, v);
     else
@@ -114,17 +112,22 @@ __device__ __forceinline__ void put8(T *p, bool vec, int have, const float v[8])
       if (j < have) store1(p + j, v[j]);
   }
 }
-__device__ __forceinline__ uint2 get_codes(const uint8_t *p, bool vec, int have) {
-  if (vec && have == 8) return *reinterpret_cast<const uint2 *>(p);
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 __attribute__((aligned(1))) u32x2_at1;
+__device__ __forceinline__ uint2 get_codes(const uint8_t *p, int have) {
+  if (have == 8) {
+    const u32x2 q = *reinterpret_cast<const u32x2_at1 *>(p);
+    return make_uint2(q.x, q.y);
+  }
   uint32_t q[2] = {0u, 0u};
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     if (j < have) q[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
   return make_uint2(q[0], q[1]);
 }
-__device__ __forceinline__ void put_codes(uint8_t *p, bool vec, int have, uint2 q) {
-  if (vec && have == 8) {
-    *reinterpret_cast<uint2 *>(p) = q;
+__device__ __forceinline__ void put_codes(uint8_t *p, int have, uint2 q) {
+  if (have == 8) {
+    *reinterpret_cast<u32x2_at1 *>(p) = (u32x2){q.x, q.y};
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -146,20 +149,19 @@ template <typename TP, typename TG, bool S8, bool SR>
 __device__ __forceinline__ float step8(const AdamArgs &a, const AdamTensor &t, const AdamExtra &x, float gs, int64_t i0) {
   const int64_t left = t.n - i0;
   const int have = left >= 8 ? 8 : left > 0 ? (int)left : 0;
-  const bool vec = t.flags & AF_VEC;
   float p[8], g[8], m[8], v[8];
   uint32_t w[4];
-  get8((const TP *)t.param + i0, vec, have, p);
-  get8((const TG *)t.grad + i0, vec, have, g);
+  get8((const TP *)t.param + i0, have, p);
+  get8((const TG *)t.grad + i0, have, g);
   if constexpr (S8) {
-    const uint2 qm = get_codes((const uint8_t *)t.m + i0, vec, have), qv = get_codes((const uint8_t *)t.v + i0, vec, have);
+    const uint2 qm = get_codes((const uint8_t *)t.m + i0, have), qv = get_codes((const uint8_t *)t.v + i0, have);
     decode8(qm, have ? x.m_scale[i0 >> 5] : 0u, m);
     decode8(qv, have ? x.v_scale[i0 >> 5] : 0u, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] *= v[j];
   } else {
-    get8((const float *)t.m + i0, vec, have, m);
-    get8((const float *)t.v + i0, vec, have, v);
+    get8((const float *)t.m + i0, have, m);
+    get8((const float *)t.v + i0, have, v);
   }
   float r[8];
 #pragma unroll
@@ -177,20 +179,20 @@ __device__ __forceinline__ float step8(const AdamArgs &a, const AdamTensor &t, c
 #pragma unroll
     for (int j = 0; j < 8; ++j) p[j] = __uint_as_float((__float_as_uint(p[j]) + u16_of(w, j)) & 0xFFFF0000u);
   }
-  put8<!S8>((TP *)t.param + i0, vec, have, p);
-  if (x.copy) put8<false>(x.copy + i0, vec, have, p);
+  put8<!S8>((TP *)t.param + i0, have, p);
+  if (x.copy) put8<false>(x.copy + i0, have, p);
   if constexpr (S8) {
     int e;
     if (SR) draw(a, t.index, 0u, i0 >> 3, w);
-    put_codes((uint8_t *)t.m + i0, vec, have, encode8<SR>(m, w, false, &e));
+    put_codes((uint8_t *)t.m + i0, have, encode8<SR>(m, w, false, &e));
     const bool leader = have && (threadIdx.x & 3) == 0;
     if (leader) x.m_scale[i0 >> 5] = (uint8_t)(e + 127);
     if (SR) draw(a, t.index, 1u, i0 >> 3, w);
-    put_codes((uint8_t *)t.v + i0, vec, have, encode8<SR>(r, w, true, &e));
+    put_codes((uint8_t *)t.v + i0, have, encode8<SR>(r, w, true, &e));
     if (leader) x.v_scale[i0 >> 5] = (uint8_t)(e + 127);
   } else {
-    put8<true>((float *)t.m + i0, vec, have, m);
-    put8<true>((float *)t.v + i0, vec, have, v);
+    put8<true>((float *)t.m + i0, have, m);
+    put8<true>((float *)t.v + i0, have, v);
   }
   float top = 0.0f;
   if (x.amax) {

@@ -12,102 +12,85 @@
 namespace nvfp4 {
 namespace {
 
-// element j of a thread's group v: groups of 8 consecutive elements when rows
-// can be read 16 bytes at a time, else elements TPR apart, which keeps single
-// element accesses of a wave contiguous
-template <bool VEC, int V>
-__device__ __forceinline__ int column(int v, int j, int t, int tpr) {
-  return VEC ? (v * tpr + t) * 8 + j : (v * 8 + j) * tpr + t;
-}
+// element j of a thread's group v
+__device__ __forceinline__ int column(int v, int j, int t, int tpr) { return (v * tpr + t) * 8 + j; }
 
-// a thread's share of a row as it stands in memory, zero outside [0, cols):
-// what is loaded ahead for the next row
+// 8 elements as they stand in memory: what is loaded ahead for the next row
 template <typename T>
-struct Group;  // 8 elements
+struct Group;
 template <>
 struct Group<uint16_t> {
   uint4 q;
-  __device__ __forceinline__ void load(const uint16_t *p) { q = *reinterpret_cast<const uint4 *>(p); }
+  __device__ __forceinline__ void load(const uint16_t *p) { q = load_group(p); }
   __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void load1(int j, const uint16_t *p, bool in) {
-    const uint32_t x = *p & (in ? 0xFFFFu : 0u);
-    uint32_t &w = (j >> 1) == 0 ? q.x : (j >> 1) == 1 ? q.y : (j >> 1) == 2 ? q.z : q.w;
-    w = j & 1 ? w | x << 16 : x;
+  __device__ __forceinline__ void load1(int j, const uint16_t *p) {  // into a zeroed group
+    const uint32_t x = (uint32_t)*p << (16 * (j & 1));
+    ((j >> 1) == 0 ? q.x : (j >> 1) == 1 ? q.y : (j >> 1) == 2 ? q.z : q.w) |= x;
   }
   __device__ __forceinline__ float at(int j) const { return bf16_at(q, j); }
 };
 template <>
 struct Group<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float *p) {
-    a = reinterpret_cast<const float4 *>(p)[0];
-    b = reinterpret_cast<const float4 *>(p)[1];
+  float x[8];
+  __device__ __forceinline__ void load(const float *p) { load8(p, x); }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = 0.0f;
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
-  __device__ __forceinline__ void load1(int j, const float *p, bool in) {
-    const float y = *p, x = in ? y : 0.0f;
-    (j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : j == 3 ? a.w : j == 4 ? b.x : j == 5 ? b.y : j == 6 ? b.z : b.w) = x;
-  }
-  __device__ __forceinline__ float at(int j) const {
-    return j == 0 ? a.x : j == 1 ? a.y : j == 2 ? a.z : j == 3 ? a.w : j == 4 ? b.x : j == 5 ? b.y : j == 6 ? b.z : b.w;
-  }
+  __device__ __forceinline__ void load1(int j, const float *p) { x[j] = *p; }
+  __device__ __forceinline__ float at(int j) const { return x[j]; }
 };
 
-template <bool VEC, int V, typename T>
+// a thread's share of a row, zero outside [0, cols)
+template <int V, typename T>
 __device__ __forceinline__ void fetch_row(const T *row, int cols, int t, int tpr, Group<T> g[V]) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    // loads without branches: past the end from the row's start, and dropped
-    if constexpr (VEC) {
-      const int c = column<true, V>(v, 0, t, tpr);
-      g[v].load(row + (c < cols ? c : 0));
-      if (c >= cols) g[v].zero();
+    const int c = column(v, 0, t, tpr);
+    if (c + 8 <= cols) {
+      g[v].load(row + c);
     } else {
+      g[v].zero();
+      if (c < cols) {  // the end of a width that is no multiple of 8
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = column<false, V>(v, j, t, tpr);
-        g[v].load1(j, row + (c < cols ? c : 0), c < cols);
+        for (int j = 0; j < 7; ++j)
+          if (c + j < cols) g[v].load1(j, row + c + j);
       }
     }
   }
 }
-template <bool VEC, int V, typename T>
+template <int V, typename T>
 __device__ __forceinline__ void load_row(const T *row, int cols, int t, int tpr, float out[V][8]) {
   Group<T> g[V];
-  fetch_row<VEC, V>(row, cols, t, tpr, g);
+  fetch_row<V>(row, cols, t, tpr, g);
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int j = 0; j < 8; ++j) out[v][j] = g[v].at(j);
 }
 
-template <bool VEC, int V, typename T>
+template <int V, typename T>
 __device__ __forceinline__ void store_row(T *row, int cols, int t, int tpr, const float in[V][8]) {
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    if constexpr (VEC) {
-      const int c = column<true, V>(v, 0, t, tpr);
-      if (c < cols) store8(row + c, in[v]);
-    } else if (column<false, V>(v, 8, 0, tpr) <= cols) {  // the whole row's threads
+    const int c = column(v, 0, t, tpr);
+    if (c + 8 <= cols) {
+      store8(row + c, in[v]);
+    } else if (c < cols) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) store1(row + column<false, V>(v, j, t, tpr), in[v][j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = column<false, V>(v, j, t, tpr);
-        if (c < cols) store1(row + c, in[v][j]);
-      }
+      for (int j = 0; j < 7; ++j)
+        if (c + j < cols) store1(row + c + j, in[v][j]);
     }
   }
 }
 
 // a thread's share of a weight
-template <bool VEC, int V>
+template <int V>
 __device__ __forceinline__ void load_weight(const void *w, int bf16, int cols, int t, int tpr, float out[V][8]) {
   if (bf16)
-    load_row<VEC, V>((const uint16_t *)w, cols, t, tpr, out);
+    load_row<V>((const uint16_t *)w, cols, t, tpr, out);
   else
-    load_row<VEC, V>((const float *)w, cols, t, tpr, out);
+    load_row<V>((const float *)w, cols, t, tpr, out);
 }
 // Workgroups of up to 512 threads keep the weights in registers and load the
 // next row ahead.  Those of 1024 have 128 registers to a thread, which a row
@@ -119,7 +102,7 @@ constexpr bool holds(int nt) { return nt <= 512; }
 // of its part and the sum of squares about that; one exchange joins them (n_w
 // elements, mean_w, q_w to a wave):
 //   mean = sum n_w mean_w / n,  q = sum q_w + n_w (mean_w - mean)^2
-template <typename TX, typename TY, bool VEC, int V, int NT>
+template <typename TX, typename TY, int V, int NT>
 __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
   __shared__ float2 slots[2][16];
   __shared__ float counts[16];
@@ -132,13 +115,13 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
   const bool w_bf16 = a.w_dtype == NVFP4_BF16;
   Group<TX> gx[V], gr[V];
   if (kHold && r < a.rows) {
-    fetch_row<VEC, V>((const TX *)a.x + r * a.ld_x, cols, t, tpr, gx);
-    if (a.residual) fetch_row<VEC, V>((const TX *)a.residual + r * a.ld_residual, cols, t, tpr, gr);
+    fetch_row<V>((const TX *)a.x + r * a.ld_x, cols, t, tpr, gx);
+    if (a.residual) fetch_row<V>((const TX *)a.residual + r * a.ld_residual, cols, t, tpr, gr);
   }
   float w[V][8], b[V][8], top = 0.0f;
   const auto weights = [&] {
-    load_weight<VEC, V>(a.weight, w_bf16, cols, t, tpr, w);
-    if (a.bias) load_weight<VEC, V>(a.bias, w_bf16, cols, t, tpr, b);
+    load_weight<V>(a.weight, w_bf16, cols, t, tpr, w);
+    if (a.bias) load_weight<V>(a.bias, w_bf16, cols, t, tpr, b);
   };
 #pragma unroll
   for (int v = 0; v < V; ++v)
@@ -149,15 +132,15 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mine += column<VEC, V>(v, j, t, tpr) < cols;
+    for (int j = 0; j < 8; ++j) mine += column(v, j, t, tpr) < cols;
   const float count = wave_sum((float)mine), inv_w = count > 0.0f ? 1.0f / count : 0.0f;
   if (waves > 1 && (t & 63) == 0) counts[wave] = count;
   int turn = 0;
   for (; r < a.rows; r += step) {
     float x[V][8];
     if (!kHold) {
-      fetch_row<VEC, V>((const TX *)a.x + r * a.ld_x, cols, t, tpr, gx);
-      if (a.residual) fetch_row<VEC, V>((const TX *)a.residual + r * a.ld_residual, cols, t, tpr, gr);
+      fetch_row<V>((const TX *)a.x + r * a.ld_x, cols, t, tpr, gx);
+      if (a.residual) fetch_row<V>((const TX *)a.residual + r * a.ld_residual, cols, t, tpr, gr);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -170,10 +153,10 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
         for (int j = 0; j < 8; ++j) x[v][j] = rounded<TX>(x[v][j] + gr[v].at(j));
     }
     if (kHold && r + step < a.rows) {
-      fetch_row<VEC, V>((const TX *)a.x + (r + step) * a.ld_x, cols, t, tpr, gx);
-      if (a.residual) fetch_row<VEC, V>((const TX *)a.residual + (r + step) * a.ld_residual, cols, t, tpr, gr);
+      fetch_row<V>((const TX *)a.x + (r + step) * a.ld_x, cols, t, tpr, gx);
+      if (a.residual) fetch_row<V>((const TX *)a.residual + (r + step) * a.ld_residual, cols, t, tpr, gr);
     }
-    if (a.residual) store_row<VEC, V>((TX *)a.sum + r * a.ld_sum, cols, t, tpr, x);
+    if (a.residual) store_row<V>((TX *)a.sum + r * a.ld_sum, cols, t, tpr, x);
     float s = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -184,7 +167,7 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float d = column<VEC, V>(v, j, t, tpr) < cols ? x[v][j] - mean : 0.0f;
+        const float d = column(v, j, t, tpr) < cols ? x[v][j] - mean : 0.0f;
         q = fmaf(d, d, q);
       }
     q = wave_sum(q);
@@ -214,9 +197,9 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
       for (int j = 0; j < 8; ++j) {
         const float y = rounded<TY>(fmaf((x[v][j] - mean) * rstd, w[v][j], b[v][j]));
         x[v][j] = y;
-        if (a.amax && column<VEC, V>(v, j, t, tpr) < cols) top = fmaxf(top, fabsf(y));
+        if (a.amax && column(v, j, t, tpr) < cols) top = fmaxf(top, fabsf(y));
       }
-    store_row<VEC, V>((TY *)a.y + r * a.ld_y, cols, t, tpr, x);
+    store_row<V>((TY *)a.y + r * a.ld_y, cols, t, tpr, x);
   }
   if (a.amax) fold_max(a.amax, top);
 }
@@ -225,7 +208,7 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
 // twice from the row as it was loaded, before and after that, which keeps fewer
 // registers than holding them.  The sums over rows stay in registers and are
 // written once per workgroup, [blockIdx][dweight, dbias][cols].
-template <typename TX, typename TY, bool VEC, int V, int NT>
+template <typename TX, typename TY, int V, int NT>
 __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_backward_args a, float *partials) {
   __shared__ float2 slots[2][16];
   __shared__ float both[NT == 1024 ? 1 : 4][8][64];
@@ -235,7 +218,7 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
   const float inv = 1.0f / (float)cols;
   const bool w_bf16 = a.w_dtype == NVFP4_BF16;
   float w[V][8], dw[V][8], db[V][8], top = 0.0f;
-  if (kHold) load_weight<VEC, V>(a.weight, w_bf16, cols, t, tpr, w);
+  if (kHold) load_weight<V>(a.weight, w_bf16, cols, t, tpr, w);
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -246,8 +229,8 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
   Group<TY> gy[V], next_y[V];
   float mean = 0.0f, rstd = 0.0f, next_mean = 0.0f, next_rstd = 0.0f;
   const auto fetch = [&](int64_t row, Group<TX> *x, Group<TY> *y, float &m, float &s) {
-    fetch_row<VEC, V>((const TX *)a.x + row * a.ld_x, cols, t, tpr, x);
-    fetch_row<VEC, V>((const TY *)a.dy + row * a.ld_dy, cols, t, tpr, y);
+    fetch_row<V>((const TX *)a.x + row * a.ld_x, cols, t, tpr, x);
+    fetch_row<V>((const TY *)a.dy + row * a.ld_dy, cols, t, tpr, y);
     m = a.mean[row];
     s = a.rstd[row];
   };
@@ -262,11 +245,11 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
       }
       mean = next_mean;
       rstd = next_rstd;
-      if (a.dsum) fetch_row<VEC, V>((const TX *)a.dsum + r * a.ld_dsum, cols, t, tpr, gd);
+      if (a.dsum) fetch_row<V>((const TX *)a.dsum + r * a.ld_dsum, cols, t, tpr, gd);
       if (r + step < a.rows) fetch(r + step, next_x, next_y, next_mean, next_rstd);
     } else {
       fetch(r, gx, gy, mean, rstd);
-      load_weight<VEC, V>(a.weight, w_bf16, cols, t, tpr, w);
+      load_weight<V>(a.weight, w_bf16, cols, t, tpr, w);
     }
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
@@ -295,8 +278,8 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
     }
     const float c1 = s1 * inv, c2 = s2 * inv;
     if (!kHold) {
-      if (a.dsum) fetch_row<VEC, V>((const TX *)a.dsum + r * a.ld_dsum, cols, t, tpr, gd);
-      load_weight<VEC, V>(a.weight, w_bf16, cols, t, tpr, w);
+      if (a.dsum) fetch_row<V>((const TX *)a.dsum + r * a.ld_dsum, cols, t, tpr, gd);
+      load_weight<V>(a.weight, w_bf16, cols, t, tpr, w);
     }
     float x[V][8];
 #pragma unroll
@@ -312,21 +295,21 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[v][j] += gd[v].at(j);
     }
-    store_row<VEC, V>((TX *)a.dx + r * a.ld_dx, cols, t, tpr, x);
+    store_row<V>((TX *)a.dx + r * a.ld_dx, cols, t, tpr, x);
     if (a.amax) {
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (column<VEC, V>(v, j, t, tpr) < cols) top = fmaxf(top, fabsf(rounded<TX>(x[v][j])));
+          if (column(v, j, t, tpr) < cols) top = fmaxf(top, fabsf(rounded<TX>(x[v][j])));
     }
   }
   if (a.amax) fold_max(a.amax, top);
   if (!partials) return;
   float *out = partials + (int64_t)blockIdx.x * 2 * cols;
   if (blockDim.y == 1) {
-    store_row<VEC, V>(out, cols, t, tpr, dw);
-    store_row<VEC, V>(out + cols, cols, t, tpr, db);
+    store_row<V>(out, cols, t, tpr, dw);
+    store_row<V>(out + cols, cols, t, tpr, db);
     return;
   }
   // the rows of the workgroup's four waves, added in their order: each wave
@@ -342,7 +325,7 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int j = 2 * threadIdx.y + i, c = column<VEC, V>(v, j, t, tpr);
+          const int j = 2 * threadIdx.y + i, c = column(v, j, t, tpr);
           const float s = (both[0][j][t] + both[1][j][t]) + (both[2][j][t] + both[3][j][t]);
           if (c < cols) out[c] = s;
         }
@@ -378,10 +361,6 @@ __global__ __launch_bounds__(1024) void layernorm_reduce_kernel(const float *par
   if (out) out[c < cols ? c : c - cols] = s;
 }
 
-bool at16(const void *p, int64_t ld, int32_t dtype) {
-  return ((uintptr_t)p & 15u) == 0 && ld % (dtype == NVFP4_BF16 ? 8 : 4) == 0;
-}
-
 // How a row of `cols` elements is split: groups of 8 per thread, the workgroup
 // size the kernel is built for, and threads per row and rows per workgroup.
 struct Split {
@@ -403,53 +382,43 @@ int64_t resident(const Split &p, int64_t rows, int waves) {
   return groups < most ? groups : most;
 }
 
-template <typename TX, typename TY, bool VEC, int V, int NT>
+template <typename TX, typename TY, int V, int NT>
 void run(const nvfp4_layernorm_args &a, float *, unsigned grid, dim3 block, hipStream_t s) {
-  layernorm_kernel<TX, TY, VEC, V, NT><<<grid, block, 0, s>>>(a);
+  layernorm_kernel<TX, TY, V, NT><<<grid, block, 0, s>>>(a);
 }
-template <typename TX, typename TY, bool VEC, int V, int NT>
+template <typename TX, typename TY, int V, int NT>
 void run(const nvfp4_layernorm_backward_args &a, float *partials, unsigned grid, dim3 block, hipStream_t s) {
-  layernorm_backward_kernel<TX, TY, VEC, V, NT><<<grid, block, 0, s>>>(a, partials);
+  layernorm_backward_kernel<TX, TY, V, NT><<<grid, block, 0, s>>>(a, partials);
 }
 
-template <typename TX, typename TY, bool VEC, typename A>
+template <typename TX, typename TY, typename A>
 void pick_split(const Split &p, const A &a, float *partials, unsigned grid, hipStream_t s) {
   if (p.v == 1)
-    run<TX, TY, VEC, 1, 256>(a, partials, grid, p.block, s);
+    run<TX, TY, 1, 256>(a, partials, grid, p.block, s);
   else if (p.v == 2 && p.nt == 512)
-    run<TX, TY, VEC, 2, 512>(a, partials, grid, p.block, s);
+    run<TX, TY, 2, 512>(a, partials, grid, p.block, s);
   else if (p.v == 2)
-    run<TX, TY, VEC, 2, 1024>(a, partials, grid, p.block, s);
+    run<TX, TY, 2, 1024>(a, partials, grid, p.block, s);
   else
-    run<TX, TY, VEC, 4, 1024>(a, partials, grid, p.block, s);
-}
-template <typename TX, typename TY, typename A>
-void pick_vec(bool vec, const Split &p, const A &a, float *partials, unsigned grid, hipStream_t s) {
-  if (vec)
-    pick_split<TX, TY, true>(p, a, partials, grid, s);
-  else
-    pick_split<TX, TY, false>(p, a, partials, grid, s);
+    run<TX, TY, 4, 1024>(a, partials, grid, p.block, s);
 }
 template <typename A>
-void pick(bool vec, const Split &p, const A &a, float *partials, unsigned grid, hipStream_t s) {
+void pick(const Split &p, const A &a, float *partials, unsigned grid, hipStream_t s) {
   if (a.x_dtype == NVFP4_BF16 && a.y_dtype == NVFP4_BF16)
-    pick_vec<uint16_t, uint16_t>(vec, p, a, partials, grid, s);
+    pick_split<uint16_t, uint16_t>(p, a, partials, grid, s);
   else if (a.x_dtype == NVFP4_BF16)
-    pick_vec<uint16_t, float>(vec, p, a, partials, grid, s);
+    pick_split<uint16_t, float>(p, a, partials, grid, s);
   else if (a.y_dtype == NVFP4_BF16)
-    pick_vec<float, uint16_t>(vec, p, a, partials, grid, s);
+    pick_split<float, uint16_t>(p, a, partials, grid, s);
   else
-    pick_vec<float, float>(vec, p, a, partials, grid, s);
+    pick_split<float, float>(p, a, partials, grid, s);
 }
 
 }  // namespace
 
 hipError_t launch_layernorm(const nvfp4_layernorm_args &a, hipStream_t s) {
   const Split p = split_of(a.cols);
-  const bool vec = a.cols % 8 == 0 && at16(a.x, a.ld_x, a.x_dtype) && at16(a.y, a.ld_y, a.y_dtype) &&
-                   at16(a.weight, 0, a.w_dtype) && at16(a.bias, 0, a.w_dtype) &&
-                   (!a.residual || (at16(a.residual, a.ld_residual, a.x_dtype) && at16(a.sum, a.ld_sum, a.x_dtype)));
-  pick(vec, p, a, nullptr, (unsigned)resident(p, a.rows, 16), s);
+  pick(p, a, nullptr, (unsigned)resident(p, a.rows, 16), s);
   return hipGetLastError();
 }
 
@@ -463,11 +432,8 @@ int64_t layernorm_backward_parts(int64_t rows, int64_t cols) {
 
 hipError_t launch_layernorm_backward(const nvfp4_layernorm_backward_args &a, float *partials, hipStream_t s) {
   const Split p = split_of(a.cols);
-  const bool vec = a.cols % 8 == 0 && at16(a.x, a.ld_x, a.x_dtype) && at16(a.dy, a.ld_dy, a.y_dtype) &&
-                   at16(a.weight, 0, a.w_dtype) && at16(a.dx, a.ld_dx, a.x_dtype) &&
-                   (!a.dsum || at16(a.dsum, a.ld_dsum, a.x_dtype));
   const int64_t parts = layernorm_backward_parts(a.rows, a.cols);
-  pick(vec, p, a, partials, (unsigned)parts, s);
+  pick(p, a, partials, (unsigned)parts, s);
   if (partials)
     layernorm_reduce_kernel<<<(unsigned)((2 * a.cols + 63) / 64), dim3(64, 16), 0, s>>>(partials, parts, a.cols,
                                                                                       a.dweight, a.dbias);

@@ -319,9 +319,6 @@ int nvfp4_adamw(const nvfp4_adamw_tensor *tensors, int64_t n_tensors, const nvfp
     d.index = (uint32_t)i;
     d.flags = (t.param_dtype == NVFP4_BF16 ? AF_PARAM_BF16 : 0u) | (t.grad_dtype == NVFP4_BF16 ? AF_GRAD_BF16 : 0u) |
               (t.state_bits == 8 ? AF_STATE8 : 0u);
-    const size_t sa = t.state_bits == 8 ? 8 : 16;
-    if (aligned(t.param, 16) && aligned(t.grad, 16) && aligned(t.m, sa) && aligned(t.v, sa) && aligned(t.copy, 16))
-      d.flags |= AF_VEC;
     if (extra) {
       const AdamExtra e = {t.m_scale, t.v_scale, (uint16_t *)t.copy, t.amax};
       d.flags |= AF_EXTRA | (uint32_t)extras << AF_EXTRA_SHIFT;

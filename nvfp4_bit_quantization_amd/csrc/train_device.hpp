@@ -19,23 +19,36 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 __device__ __forceinline__ float round_bf16(float a) { return __uint_as_float(pack_bf16(0.0f, a) & 0xFFFF0000u); }
 
-// 8 consecutive elements, 16-byte aligned
+// 8 consecutive elements, aligned to their own size: global accesses of 16
+// bytes need no more on this target (those that are 16-byte aligned are quicker)
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 __attribute__((aligned(2))) u32x4_at2;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef f32x4 __attribute__((aligned(4))) f32x4_at4;
+__device__ __forceinline__ uint4 load_group(const uint16_t *p) {
+  const u32x4 q = *reinterpret_cast<const u32x4_at2 *>(p);
+  return make_uint4(q.x, q.y, q.z, q.w);
+}
 __device__ __forceinline__ void load8(const uint16_t *p, float v[8]) {
-  const uint4 q = *reinterpret_cast<const uint4 *>(p);
+  const uint4 q = load_group(p);
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = bf16_at(q, j);
 }
 __device__ __forceinline__ void load8(const float *p, float v[8]) {
-  const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  const f32x4 a = reinterpret_cast<const f32x4_at4 *>(p)[0], b = reinterpret_cast<const f32x4_at4 *>(p)[1];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] = a[j];
+    v[4 + j] = b[j];
+  }
 }
-__device__ __forceinline__ uint4 packed8(const float v[8]) {
-  return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+__device__ __forceinline__ u32x4 packed8(const float v[8]) {
+  return (u32x4){pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
 }
-__device__ __forceinline__ void store8(uint16_t *p, const float v[8]) { *reinterpret_cast<uint4 *>(p) = packed8(v); }
+__device__ __forceinline__ void store8(uint16_t *p, const float v[8]) { *reinterpret_cast<u32x4_at2 *>(p) = packed8(v); }
 __device__ __forceinline__ void store8(float *p, const float v[8]) {
-  reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  reinterpret_cast<f32x4_at4 *>(p)[0] = (f32x4){v[0], v[1], v[2], v[3]};
+  reinterpret_cast<f32x4_at4 *>(p)[1] = (f32x4){v[4], v[5], v[6], v[7]};
 }
 __device__ __forceinline__ float load1(const uint16_t *p) { return bf16_lo(*p); }
 __device__ __forceinline__ float load1(const float *p) { return *p; }

@@ -22,8 +22,8 @@ constexpr int kAdamThreads = 256;
 constexpr int kAdamChunk = 4096;  // elements of one workgroup (a multiple of 8 * kAdamThreads)
 
 enum AdamFlags : uint32_t {
-  AF_PARAM_BF16 = 1, AF_GRAD_BF16 = 2, AF_STATE8 = 4, AF_VEC = 8,
-  AF_EXTRA = 16,      // has an AdamExtra
+  AF_PARAM_BF16 = 1, AF_GRAD_BF16 = 2, AF_STATE8 = 4,
+  AF_EXTRA = 8,       // has an AdamExtra
   AF_EXTRA_SHIFT = 8  // its number, from bit 8 on
 };
 
