@@ -9,6 +9,10 @@
 // product sums over in their rows, and that product's A operand is read from
 // LDS in the same order of that index (4 h .. 4 h + 3, then 8 + 4 h .. 11 + 4 h
 // of each 16) by the transposing LDS read.
+//
+// The gradient recomputes scores and dP in each of its two passes, dQ and
+// dK + dV: seven products instead of five, but no sums by atomics, whose order
+// would change results, and no binary32 buffer for dQ.
 #include "gemm_device.hpp"
 #include "train_device.hpp"
 #include "train_kernels.hpp"
@@ -89,18 +93,21 @@ __device__ __forceinline__ void sight(const AttnArgs &a, int i, int nk, int off,
 // 1024 bytes, whose lanes' 16 bytes land next to each other: a segment of 4
 // (D = 128) or 8 (D = 64) rows.  Chunks (16 bytes) are permuted within a row by
 // which address each lane reads, chunk c of row r standing at c ^ spread(r),
-// and segments are 16 bytes further apart than they are long.  Both reads below
-// then meet every group of banks equally, the plain one (32 rows at one chunk)
+// and segments are 16 (D = 128) or 32 (D = 64) bytes further apart than they
+// are long.  Both reads below then meet every group of banks equally, the plain
+// one (32 rows at one chunk; the rows that meet in a cycle are four groups of
+// four, 0, 3, 5, 6 or 1, 2, 4, 7, which 16 bytes do not keep apart for D = 64)
 // and the transposing one (4 rows at 4 neighbouring chunks), and all reads of a
-// lane stand at fixed distances from four (plain) and D / 32 (transposing)
-// addresses, as the instructions' immediate offsets.
+// lane stand at fixed distances from D / 32 addresses each, as the
+// instructions' immediate offsets.  (16 bytes for D = 64: the gradient of 2 x
+// 4096 tokens, 40 heads of 64, 8 key heads, causal, 727 us against 694.)
 template <int D>
 struct Tile {
   static constexpr int kChunks = D / 8, kSegRows = 64 / kChunks;
-  static constexpr uint32_t kSeg = 1024 + 16;
+  static constexpr uint32_t kSeg = 1024 + (D == 128 ? 16 : 32);
   static constexpr uint32_t bytes(int rows) { return (uint32_t)(rows / kSegRows) * kSeg; }
   static __device__ __forceinline__ uint32_t spread(uint32_t r) {
-    return D == 128 ? (r & 3u) << 2 : ((r >> 1) & 1u) << 2 | ((r >> 2) & 1u) << 1;
+    return D == 128 ? (r & 3u) << 2 : ((r >> 1) & 1u) << 2 | ((r >> 2) & 1u);
   }
 };
 
@@ -130,13 +137,13 @@ __device__ __forceinline__ void fetch_tile(const uint16_t *head, int64_t stride,
 // a lane's addresses within a tile
 template <int D>
 struct Reads {
-  uint32_t row[4], col[D / 32];
+  uint32_t row[D / 32], col[D / 32];
   __device__ __forceinline__ Reads(int lane, uint32_t at) {
     typedef Tile<D> T;
     const uint32_t n = lane & 31, h = lane >> 5, i = lane & 15, g = lane >> 4;
 #pragma unroll
-    for (uint32_t k = 0; k < 4; ++k) {
-      const uint32_t c = (D == 128 ? 4 * k : 2 * k) + h;
+    for (uint32_t k = 0; k < D / 32; ++k) {
+      const uint32_t c = 4 * k + h;
       row[k] = n / T::kSegRows * T::kSeg + n % T::kSegRows * (2 * D) + (c ^ T::spread(n)) * 16 + at;
     }
 #pragma unroll
@@ -148,19 +155,18 @@ struct Reads {
   // to the tile `by` bytes on
   __device__ __forceinline__ void move(uint32_t by) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) row[k] += by;
+    for (int k = 0; k < D / 32; ++k) row[k] += by;
 #pragma unroll
     for (int k = 0; k < D / 32; ++k) col[k] += by;
   }
   // A operand from rows r0 .. r0 + 31 (r0 = 0, 32) as they stand: row n,
   // elements 16 c + 8 h ..; `tile`: bytes to another tile
   __device__ __forceinline__ bf16x8 rows(uint32_t tile, int r0, int c) const {
-    const uint32_t a = row[D == 128 ? c >> 1 : c] + tile + (uint32_t)(r0 / Tile<D>::kSegRows) * Tile<D>::kSeg +
-                       (D == 128 ? (c & 1) * 32u : 0u);
+    const uint32_t a = row[c >> 1] + tile + (uint32_t)(r0 / Tile<D>::kSegRows) * Tile<D>::kSeg + (c & 1) * 32u;
     return *(const __attribute__((address_space(3))) bf16x8 *)a;
   }
   __device__ __forceinline__ void set_row(int c, bf16x8 v) const {
-    *(__attribute__((address_space(3))) bf16x8 *)(row[D == 128 ? c >> 1 : c] + (D == 128 ? (c & 1) * 32u : 0u)) = v;
+    *(__attribute__((address_space(3))) bf16x8 *)(row[c >> 1] + (c & 1) * 32u) = v;
   }
   // A operand from the transposed tile: row = element 32 dt + n, inner index =
   // tile rows r0 + 4 h .. and r0 + 8 + 4 h .. (r0 = 0, 16, 32, 48)
@@ -301,7 +307,13 @@ __device__ __forceinline__ void store_part(float *row, const f32x16 *acc, float 
 constexpr int kQueries = 128;  // queries of a workgroup: 32 per wave
 
 // One wave holds 32 queries as columns: scores^T = K Q^T, o^T = V^T p^T.
-// Running maximum and sum per query stay in its two lanes.
+// Running maximum and sum per query stay in its two lanes.  Two waves per SIMD:
+// while one waits or takes exponentials the other multiplies.
+// 8192 tokens, 40 heads of 128, 8 key heads, causal: 652-711 us on several devices, 0.97-1.05
+// PFLOP/s, the MFMA busy in 57 % of the cycles at 1.82 GHz.  Power bounds it: 8 % fewer
+// cycles (operands read ahead) left the time as it was and lowered the clock.
+// Eight waves to a workgroup, which halves the transfers, took the same time;
+// 64 queries to a wave at one wave per SIMD, which halves the LDS reads, 807 us.
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   __shared__ __align__(16) uint8_t lds[4 * Tile<D>::bytes(kTile)];
@@ -484,7 +496,9 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs a) {
 }
 
 // ------------------------------------------------------------- gradient ----
-// dQ: a wave holds 32 queries as columns; scores^T = K Q^T, dP^T = V dO^T,
+// dQ (2 x 4096 tokens, 40 heads of 128, 8 key heads, causal: 483-506 us, 1.02-1.07
+// PFLOP/s over its three products, the MFMA busy in 60 % of the cycles: power).
+// A wave holds 32 queries as columns; scores^T = K Q^T, dP^T = V dO^T,
 // dQ^T = K^T dS^T.  It forms delta = sum_d do * o on the way, and leaves
 // -delta and -lse / scale, from which the accumulators of the dK, dV pass start.
 template <int D>
@@ -613,6 +627,10 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
 // registers nothing is left of the 256 that two waves per SIMD have each to
 // read operands ahead.  Queries come in tiles of 32 rows (D = 128), so that two
 // workgroups fit a compute unit's LDS, or 64 (D = 64).
+// The same tokens as for dQ: 665-700 us, 0.98-1.03 PFLOP/s over its four
+// products, and 30 to join them with the queries in two parts (1254 us as first
+// written, one wave per SIMD; 898 with two and both operands in registers; 775
+// with values in LDS and one part).
 constexpr int kKeys = 128;  // keys of a workgroup
 
 template <int D>
