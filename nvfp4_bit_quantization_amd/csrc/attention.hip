@@ -250,12 +250,19 @@ __device__ __forceinline__ void tile_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// workgroup -> (head, sequence, tile): neighbours share a key head, a contiguous
-// range to each XCD.  Heads are outermost, so that packed sequences' uneven
-// lengths spread over the XCDs alike; with fewer key heads than XCDs packed
-// sequences are dealt round-robin instead.
+// workgroup -> (head, sequence, tile).  Key heads are innermost, so that with
+// a multiple of 8 of them each stays on one XCD (workgroups are dealt to the 8
+// XCDs in turn), and a tile's level outermost, heaviest first: what a compute
+// unit gets then adds up alike.  Against heads outermost, a range of them to
+// each XCD: gradient of 23 packed documents (4096 tokens, 16 heads of 64) 62 ->
+// 51 us, of 8 x 1024 tokens 116 -> 95, of 16384 tokens, 20 heads of 128, 4518 ->
+// 4187, forward of these 1422 -> 1329; without a causal mask 2565 -> 2581.
+// Where all workgroups are resident at once, in up to three rounds of one to a
+// compute unit, the second round goes backwards, so that it gives the lightest
+// to the units that have the heaviest (gradient of 8192 tokens, 12 heads of 64,
+// 409 -> 396 us).
 struct Work {
-  int b, head, tile, part;
+  int b, head, level, part;
 };
 // n / d and n % d
 __device__ __forceinline__ uint32_t split_off(uint32_t &n, const Divisor &d) {
@@ -263,18 +270,16 @@ __device__ __forceinline__ uint32_t split_off(uint32_t &n, const Divisor &d) {
   n = q;
   return r;
 }
-__device__ __forceinline__ Work work_of(const AttnArgs &a, const Divisor &tiles, int parts, bool by_group) {
-  uint32_t w = a.cu_q && a.kv_heads < 8 ? blockIdx.x : xcd_tile(blockIdx.x, gridDim.x);
+__device__ __forceinline__ Work work_of(const AttnArgs &a, int parts, bool by_group) {
+  uint32_t w = blockIdx.x;
+  if (gridDim.x <= 768 && (w | 255) < gridDim.x && (w >> 8 & 1)) w ^= 0xF8;
   Work r;
-  const int g = by_group ? (int)split_off(w, a.by_group) : 0;
-  r.part = 0;
-  if (parts > 1) {
-    r.part = (int)(w % (uint32_t)parts);
-    w /= (uint32_t)parts;
-  }
-  r.tile = (int)split_off(w, tiles);
+  r.head = (int)split_off(w, a.by_kv);
+  if (by_group) r.head = r.head * (int)a.by_group.d + (int)split_off(w, a.by_group);
+  r.part = (int)(w % (uint32_t)parts);
+  w /= (uint32_t)parts;
   r.b = (int)split_off(w, a.by_batch);
-  r.head = by_group ? (int)(w * a.by_group.d) + g : (int)w;
+  r.level = (int)w;
   return r;
 }
 // the steps [lo, hi) of part `part` of `parts`
@@ -319,10 +324,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   __shared__ __align__(16) uint8_t lds[4 * Tile<D>::bytes(kTile)];
   constexpr uint32_t kB = Tile<D>::bytes(kTile);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
-  Work w = work_of(a, a.by_q_tiles, a.q_parts, true);
-  if (a.causal) w.tile = (int)a.by_q_tiles.d - 1 - w.tile;
+  const Work w = work_of(a, a.q_parts, true);
   const Seq s = sequence(a, w.b);
-  const int first = w.tile * kQueries;
+  const int first = (a.q_tiles - 1 - w.level) * kQueries;  // the later, the more keys in sight
   if (first >= s.nq) return;
   const int last = (first + kQueries < s.nq ? first + kQueries : s.nq) - 1, off = s.nk - s.nq;
   uint32_t of_head = (uint32_t)w.head;
@@ -442,57 +446,59 @@ __global__ __launch_bounds__(kThreads, 2) void attention_kernel(AttnArgs a) {
   if (h == 0) a.lse[(int64_t)w.head * a.total_q + row] = lse;
 }
 
-// Parts joined: 128 rows of a head to a workgroup, 16 threads to a row.
+// Parts joined: 16 rows of a head to a workgroup, 16 threads to a row, four
+// parts' loads in flight.
 // WHAT = kJoinO: o = sum_p exp(lse_p - lse) o_p, lse = log sum_p exp(lse_p);
-// else sums over the parts in their order: dQ, or dK and dV.
+// else sums over the parts in their order: dQ, or dK (blockIdx.y = 0) and dV.
 enum { kJoinO, kJoinQ, kJoinKV };
+constexpr int kJoinRows = kThreads / 16;
 template <int D, int WHAT>
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs a) {
-  const bool kv = WHAT == kJoinKV;
+  const bool kv = WHAT == kJoinKV, v = kv && blockIdx.y;
   const int heads = kv ? a.kv_heads : a.heads, parts = kv ? a.k_parts : a.q_parts;
   const int64_t rows = kv ? a.total_k : a.total_q;
-  const int tiles = ((kv ? a.k_len : a.q_len) + 127) / 128, c = (int)threadIdx.x & 15;
+  const int tiles = ((kv ? a.k_len : a.q_len) + kJoinRows - 1) / kJoinRows, c = (int)threadIdx.x & 15;
   uint32_t w = blockIdx.x;
-  const int tile = (int)(w % (uint32_t)tiles);
+  const int i = (int)(w % (uint32_t)tiles) * kJoinRows + (int)(threadIdx.x >> 4);
   w /= (uint32_t)tiles;
   const int b = (int)(w % (uint32_t)a.batch), head = (int)(w / (uint32_t)a.batch);
   const Seq s = sequence(a, b);
   const int n = kv ? s.nk : s.nq;
-  const int64_t row0 = !a.cu_q ? (int64_t)b * n : kv ? s.k0 : s.q0;
-  if (c * 8 >= a.dim) return;
-  for (int i = tile * 128 + (int)(threadIdx.x >> 4); i < tile * 128 + 128 && i < n; i += 16) {
-    const int64_t row = row0 + i;
-    if constexpr (WHAT == kJoinO) {
-      float top = -INFINITY, sum = 0.0f, o[8] = {};
-      for (int p = 0; p < parts; ++p) top = fmaxf(top, a.lse_part[((int64_t)p * heads + head) * rows + row]);
-      if (top > -INFINITY)
-        for (int p = 0; p < parts; ++p) {
-          const float f = __builtin_amdgcn_exp2f((a.lse_part[((int64_t)p * heads + head) * rows + row] - top) * kLog2e);
-          float v[8];
-          load8(part_row<D>(a.q_part, p, heads, head, rows, row) + c * 8, v);
-          sum += f;
+  if (i >= n || c * 8 >= a.dim) return;
+  const int64_t row = (!a.cu_q ? (int64_t)b * n : kv ? s.k0 : s.q0) + i;
+  float *from = kv ? (v ? a.v_part : a.k_part) : a.q_part, sum[8] = {};
+  if constexpr (WHAT == kJoinO) {
+    const float *lse = a.lse_part + (int64_t)head * rows + row;
+    const int64_t pitch = (int64_t)heads * rows;
+    float top = -INFINITY, total = 0.0f;
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) top = fmaxf(top, lse[p * pitch]);
+    if (top > -INFINITY) {
+#pragma unroll 4
+      for (int p = 0; p < parts; ++p) {
+        const float f = __builtin_amdgcn_exp2f((lse[p * pitch] - top) * kLog2e);
+        float x[8];
+        load8(part_row<D>(from, p, heads, head, rows, row) + c * 8, x);
+        total += f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = fmaf(f, v[j], o[j]);
-        }
-      const float f = sum > 0.0f ? 1.0f / sum : 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] *= f;
-      store8(at(a.o, s.bq, s.q0 + i, head) + c * 8, o);
-      if (c == 0) a.lse[(int64_t)head * rows + row] = sum > 0.0f ? top + __builtin_amdgcn_logf(sum) * kLn2 : -INFINITY;
-    } else {
-      for (int k = 0; k < (kv ? 2 : 1); ++k) {
-        float *from = kv ? (k ? a.v_part : a.k_part) : a.q_part, sum[8] = {};
-        for (int p = 0; p < parts; ++p) {
-          float v[8];
-          load8(part_row<D>(from, p, heads, head, rows, row) + c * 8, v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) sum[j] += v[j];
-        }
-        const Heads &to = kv ? (k ? a.dv : a.dk) : a.dq;
-        store8(at(to, kv ? s.bk : s.bq, (kv ? s.k0 : s.q0) + i, head) + c * 8, sum);
+        for (int j = 0; j < 8; ++j) sum[j] = fmaf(f, x[j], sum[j]);
       }
     }
+    const float f = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] *= f;
+    if (c == 0) a.lse[(int64_t)head * a.total_q + row] = total > 0.0f ? top + __builtin_amdgcn_logf(total) * kLn2 : -INFINITY;
+  } else {
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+      float x[8];
+      load8(part_row<D>(from, p, heads, head, rows, row) + c * 8, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += x[j];
+    }
   }
+  const Heads &to = kv ? (v ? a.dv : a.dk) : WHAT == kJoinO ? a.o : a.dq;
+  store8(at(to, kv ? s.bk : s.bq, (kv ? s.k0 : s.q0) + i, head) + c * 8, sum);
 }
 
 // ------------------------------------------------------------- gradient ----
@@ -506,10 +512,9 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
   __shared__ __align__(16) uint8_t lds[4 * Tile<D>::bytes(kTile)];
   constexpr uint32_t kB = Tile<D>::bytes(kTile);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
-  Work w = work_of(a, a.by_q_tiles, a.q_parts, true);
-  if (a.causal) w.tile = (int)a.by_q_tiles.d - 1 - w.tile;
+  const Work w = work_of(a, a.q_parts, true);
   const Seq s = sequence(a, w.b);
-  const int first = w.tile * kQueries;
+  const int first = (a.q_tiles - 1 - w.level) * kQueries;  // the later, the more keys in sight
   if (first >= s.nq) return;
   const int last = (first + kQueries < s.nq ? first + kQueries : s.nq) - 1, off = s.nk - s.nq;
   uint32_t of_head = (uint32_t)w.head;
@@ -640,17 +645,13 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 3 : 2) void attention_dkv_kerne
   __shared__ __align__(16) uint8_t lds[4 * kB + kV];
   __shared__ __align__(16) float stats[2][2][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = lane >> 5;
-  const int group = (int)a.by_group.d, tiles = (int)a.by_k_tiles.d;
-  Work w = work_of(a, a.by_k_tiles, a.k_parts, false);
+  const int group = (int)a.by_group.d;
+  const Work w = work_of(a, a.k_parts, false);
   const int hk = w.head;
-  // Key tiles of a causal pass differ in work, falling along the sequence.
-  // Where all workgroups are resident at once, two to a compute unit, every
-  // second sequence is walked from its end, so that the two add up to the same;
-  // else heavy tiles come first.
-  if (gridDim.x <= 512 && ((hk * a.batch + w.b) & 1)) w.tile = tiles - 1 - w.tile;
   const Seq s = sequence(a, w.b);
-  const int first = w.tile * kKeys;
-  if (first >= s.nk) return;
+  // counted from the sequence's last tile: the earlier, the more queries see it
+  const int first = ((s.nk + kKeys - 1) / kKeys - a.k_tiles + w.level) * kKeys;
+  if (first < 0 || first >= s.nk) return;
   const int last = (first + kKeys < s.nk ? first + kKeys : s.nk) - 1, off = s.nk - s.nq;
   const int chunks = a.dim / 8;
 
@@ -824,30 +825,40 @@ int attention_q_parts(const AttnArgs &a) {
   if (parts > steps / 8) parts = steps / 8;
   return (int)(parts < 1 ? 1 : parts > 16 ? 16 : parts);
 }
-// Queries split for dK and dV where key tiles leave the two workgroups that a
-// compute unit holds unbalanced or idle: parts of at least 32 tiles of 32
-// queries, up to 1024 workgroups.
+// Queries split for dK and dV: parts of at least 8 tiles of 32 queries, up to
+// 512 workgroups, what the compute units hold of them (4 x 500 tokens, 20 heads
+// of 128, 4 key heads: 63 us against 114 with one part; 2 x 4096 without a
+// causal mask: two parts cost the 28 us that joining them takes).  Causal passes
+// whose tiles weigh unevenly gain from a second set of workgroups, dealt to
+// whichever compute unit is done, but only long parts pay for the join: 2 x 4096
+// tokens, 40 heads of 128, 8 key heads (160 tiles each) 1241 -> 1152 us; 4096
+// tokens, 16 heads (32 each) 273 -> 295.
 int attention_k_parts(const AttnArgs &a) {
   const int64_t n = units(a, a.k_len, a.total_k, a.kv_heads);
   const int64_t rows = a.window && a.window < a.q_len ? a.window : a.causal ? (a.q_len + 1) / 2 : a.q_len;
-  int64_t parts = (1024 + n - 1) / n;
-  if (parts > rows / 32 * (a.heads / a.kv_heads) / 32) parts = rows / 32 * (a.heads / a.kv_heads) / 32;
+  const int64_t steps = rows / 32 * (a.heads / a.kv_heads), twice = (1024 + n - 1) / n;
+  int64_t parts = a.causal && steps >= 48 * twice ? twice : (512 + n - 1) / n;
+  if (parts > steps / 8) parts = steps / 8;
   return (int)(parts < 1 ? 1 : parts > 16 ? 16 : parts);
 }
 
 namespace {
+unsigned join_groups(const AttnArgs &a, int heads, int len) {
+  return (unsigned)((int64_t)a.batch * heads * ((len + kJoinRows - 1) / kJoinRows));
+}
 template <int D>
 hipError_t forward(const AttnArgs &a, unsigned rows, hipStream_t s) {
   attention_kernel<D><<<rows * (unsigned)a.q_parts, kThreads, 0, s>>>(a);
-  if (a.q_parts > 1) attention_join_kernel<D, kJoinO><<<rows, kThreads, 0, s>>>(a);
+  if (a.q_parts > 1) attention_join_kernel<D, kJoinO><<<join_groups(a, a.heads, a.q_len), kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 template <int D>
 hipError_t backward(const AttnArgs &a, unsigned rows, unsigned keys, hipStream_t s) {
   attention_dq_kernel<D><<<rows * (unsigned)a.q_parts, kThreads, 0, s>>>(a);
   attention_dkv_kernel<D><<<keys * (unsigned)a.k_parts, kThreads, 0, s>>>(a);
-  if (a.q_parts > 1) attention_join_kernel<D, kJoinQ><<<rows, kThreads, 0, s>>>(a);
-  if (a.k_parts > 1) attention_join_kernel<D, kJoinKV><<<keys, kThreads, 0, s>>>(a);
+  if (a.q_parts > 1) attention_join_kernel<D, kJoinQ><<<join_groups(a, a.heads, a.q_len), kThreads, 0, s>>>(a);
+  if (a.k_parts > 1)
+    attention_join_kernel<D, kJoinKV><<<dim3(join_groups(a, a.kv_heads, a.k_len), 2), kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 }  // namespace

@@ -95,8 +95,9 @@ AttnArgs attn_args(const nvfp4_attention_shape *s) {
   a.scale = s->scale;
   a.by_group = divisor((uint32_t)(s->heads / s->kv_heads));
   a.by_batch = divisor((uint32_t)s->batch);
-  a.by_q_tiles = divisor((uint32_t)((s->q_len + 127) / 128));
-  a.by_k_tiles = divisor((uint32_t)((s->k_len + 127) / 128));
+  a.by_kv = divisor((uint32_t)s->kv_heads);
+  a.q_tiles = (a.q_len + 127) / 128;
+  a.k_tiles = (a.k_len + 127) / 128;
   return a;
 }
 

@@ -97,7 +97,8 @@ struct AttnArgs {
   int batch, heads, kv_heads, dim;
   int causal;
   float scale;
-  Divisor by_group, by_batch, by_q_tiles, by_k_tiles;  // heads of a key head, sequences, tiles of 128 rows
+  int q_tiles, k_tiles;  // tiles of 128 rows
+  Divisor by_group, by_batch, by_kv;  // heads of a key head, sequences, key heads
 };
 
 // parts that the shape's passes are split into, from its sizes alone
