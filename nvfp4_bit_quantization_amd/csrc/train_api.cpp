@@ -48,6 +48,11 @@ int check_heads(const nvfp4_heads *t, const nvfp4_attention_shape *s, int32_t he
   return NVFP4_OK;
 }
 
+// what a sequence's length cannot exceed (at least 1)
+int64_t longest(const nvfp4_attention_shape *s, int64_t len, int64_t total) {
+  return !s->cu_q || len < total ? len : total > 1 ? total : 1;
+}
+
 int check_shape(const nvfp4_attention_shape *s) {
   if (!s) return NVFP4_E_NULL;
   const int64_t most = (int64_t)1 << 30;
@@ -66,11 +71,13 @@ int check_shape(const nvfp4_attention_shape *s) {
     return NVFP4_E_SHAPE;
   }
   if (!(s->scale > 0.0f) || !isfinite(s->scale)) return NVFP4_E_VALUE;
-  // workgroups are counted in 32 bits, and a tile may be split into up to 16 parts
-  const int64_t limit = (int64_t)1 << 27, tiles = (s->q_len > s->k_len ? s->q_len : s->k_len) / 128 + 1;
+  // a launch counts its threads in 32 bits, 256 to a workgroup; tiles are split
+  // into parts only where they are few
+  const int64_t q = longest(s, s->q_len, s->total_q), k = longest(s, s->k_len, s->total_k);
+  const int64_t limit = ((int64_t)1 << 24) - 1, tiles = (q > k ? q : k) / 128 + 1;
   if (s->batch > limit / tiles / s->heads) return NVFP4_E_SHAPE;
   // and a key tile's steps over its heads' query tiles in 26 bits
-  if ((s->q_len / 32 + 1) * (s->heads / s->kv_heads) >= (int64_t)1 << 26) return NVFP4_E_SHAPE;
+  if ((q / 32 + 1) * (s->heads / s->kv_heads) >= (int64_t)1 << 26) return NVFP4_E_SHAPE;
   return NVFP4_OK;
 }
 
@@ -85,8 +92,8 @@ AttnArgs attn_args(const nvfp4_attention_shape *s) {
   a.total_q = s->total_q;
   a.total_k = s->total_k;
   a.window = s->window < ((int64_t)1 << 30) ? (int)s->window : 1 << 30;  // no length exceeds that
-  a.q_len = (int)s->q_len;
-  a.k_len = (int)s->k_len;
+  a.q_len = (int)longest(s, s->q_len, s->total_q);
+  a.k_len = (int)longest(s, s->k_len, s->total_k);
   a.batch = (int)s->batch;
   a.heads = s->heads;
   a.kv_heads = s->kv_heads;

@@ -174,6 +174,34 @@ def test_packed(nv, case):
     assert (lse[:, :cq[0]] == 7).all() and (lse[:, cq[-1]:] == 7).all()
 
 
+SHARED = [  # passes split into parts at short lengths: batch, queries, keys, heads, key heads, dim, causal, window
+    (1, 260, 260, 8, 1, 128, True, 0), (2, 256, 256, 16, 4, 64, True, 0), (1, 700, 129, 10, 2, 72, False, 0),
+    (3, 300, 310, 20, 4, 128, True, 90), (1, 2000, 140, 6, 1, 64, True, 0), (1, 96, 1100, 12, 1, 128, True, 33)]
+
+
+@pytest.mark.parametrize("case", SHARED, ids=str)
+def test_shared_key_heads(nv, case):
+    test_dense(nv, case)
+
+
+@pytest.mark.parametrize("dim,h,hk", [(64, 12, 12), (128, 10, 1), (64, 8, 2)])
+def test_packed_order(nv, dim, h, hk):
+    """Many documents of uneven lengths under a maximum above all of them, as long as the tokens or longer."""
+    say("packed attention", dim, h, hk)
+    lens = [307, 0, 88, 1, 523, 129, 64, 128, 343, 16, 256, 9]
+    g = torch.Generator(device="cuda").manual_seed(dim + h)
+    n = sum(lens)
+    q, k, v, do = _rand(g, n, h, dim), _rand(g, n, hk, dim), _rand(g, n, hk, dim), _rand(g, n, h, dim, scale=1e-3)
+    at = [sum(lens[:i]) for i in range(len(lens) + 1)]
+    cu = torch.tensor(at, dtype=torch.int32, device="cuda")
+    for most, window in ((523, 0), (n, 200), (1 << 30, 0)):
+        o, lse, dq, dk, dv = _run(nv, q, k, v, do, causal=True, window=window, cu_q=cu, cu_k=cu, max_q=most, max_k=most)
+        for i, m in enumerate(lens):
+            a = slice(at[i], at[i + 1])
+            _check_sequence(q[a], k[a], v[a], do[a], o[a], lse[:, a], dq[a], dk[a], dv[a], _see(m, m, True, window),
+                            dim ** -0.5, "maximum %d, sequence %d" % (most, i))
+
+
 def test_bad_offsets_stay_inside(nv):
     """Offsets that descend or leave the tokens are clamped: nothing faults, and sequences that are sound are right."""
     g = torch.Generator(device="cuda").manual_seed(1)

@@ -122,6 +122,19 @@ def test_attention_shape_refusals(L, change, status):
     assert L.nvfp4_attention_backward(ctypes.byref(s), h, h, h, h, FAKE, h, h, h, h, FAKE, 1 << 30, None) == status
 
 
+def test_attention_workgroup_limits(L):
+    """A launch of 2^24 workgroups of 256 threads is refused; lengths of packed sequences count up to the tokens there are."""
+    need = lambda **kw: L.nvfp4_attention_backward_workspace_bytes(ctypes.byref(_shape(**kw)))
+    packed = dict(cu_q=FAKE, cu_k=FAKE, heads=4, kv_heads=4)
+    assert need(batch=1 << 16, q_len=8192, k_len=8192, total_q=1 << 17, total_k=1 << 17, **packed) == 0
+    assert need(batch=1 << 15, q_len=8192, k_len=8192, total_q=1 << 17, total_k=1 << 17, **packed) > 0
+    assert need(batch=1 << 14, q_len=1 << 30, k_len=1 << 30, total_q=1 << 14, total_k=1 << 14, **packed) > 0
+    few = dict(batch=3, total_q=1000, total_k=1200, **packed)
+    assert need(q_len=1 << 30, k_len=1 << 30, **few) == need(q_len=1000, k_len=1200, **few) > 0
+    assert need(batch=3, q_len=5, k_len=5, total_q=0, total_k=0, **packed) > 0
+    assert _attention(L, _shape(batch=1 << 16, q_len=8192, k_len=8192, total_q=1 << 17, total_k=1 << 17, **packed)) == SHAPE
+
+
 TENSORS = [(dict(data=None), NULL), (dict(data=FAKE + 8), ALIGN), (dict(token_stride=260), ALIGN), (dict(head_stride=60), ALIGN),
            (dict(batch_stride=4), ALIGN), (dict(token_stride=-256), LD), (dict(token_stride=1 << 23), LD),
            (dict(head_stride=-64), LD), (dict(batch_stride=-8), LD)]
