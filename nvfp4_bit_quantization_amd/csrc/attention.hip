@@ -819,6 +819,8 @@ int64_t sight_of(const AttnArgs &a) { return a.window && a.window < a.k_len ? a.
 
 // Keys split where the queries' tiles alone leave compute units idle: parts of
 // at least 8 tiles of 64 keys, up to 512 workgroups, joined by a second kernel.
+// (Parts of 4 tiles: 1 query on 512 keys, 8 heads, 18 us against 15, 7 packed
+// documents of 2000 tokens 27 against 20, 1000 tokens with 8 heads 23 against 24.)
 int attention_q_parts(const AttnArgs &a) {
   const int64_t n = units(a, a.q_len, a.total_q, a.heads), steps = sight_of(a) / kTile;
   int64_t parts = n >= 256 ? 1 : 512 / n;
