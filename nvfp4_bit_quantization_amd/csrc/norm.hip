@@ -13,9 +13,12 @@
 // (4.7 TB/s; 325 us before).  Small calls take what a launch does: 3 us for
 // 256x256.  Rows need no alignment beyond their elements': 8192x5120 bf16 takes
 // 51 us with rows 5123 elements apart and 49 us without a gap, 72 us at a width
-// of 5119, whose last group goes element by element.  Above 8192 elements, where
-// neither weights nor the next row fit the registers, 2000x20480 takes 78 us
-// (2.1 TB/s) and its gradient 275 us.
+// of 5119, whose last group goes element by element.
+// Above 8192 elements neither weights nor the next row fit the registers
+// (4096x16384 bf16: 62 us, 4.3 TB/s out of a warm cache); above 16384 the
+// gradient's sums do not either: 4096x20480 bf16 takes 103 us (161 with all
+// groups' weights read at once, which spilled) and its gradient 197 in three
+// kernels, which read x and dy twice (611 in two, the sums in scratch memory).
 #include "train_device.hpp"
 #include "train_kernels.hpp"
 
@@ -51,23 +54,25 @@ struct Group<float> {
   __device__ __forceinline__ float at(int j) const { return x[j]; }
 };
 
-// a thread's share of a row, zero outside [0, cols)
+// elements c .. c + 7 of a row, zero outside [0, cols)
+template <typename T>
+__device__ __forceinline__ void fetch_group(const T *row, int cols, int c, Group<T> &g) {
+  if (c + 8 <= cols) {
+    g.load(row + c);
+  } else {
+    g.zero();
+    if (c < cols) {  // the end of a width that is no multiple of 8
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (c + j < cols) g.load1(j, row + c + j);
+    }
+  }
+}
+// a thread's share of a row
 template <int V, typename T>
 __device__ __forceinline__ void fetch_row(const T *row, int cols, int t, int tpr, Group<T> g[V]) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = column(v, 0, t, tpr);
-    if (c + 8 <= cols) {
-      g[v].load(row + c);
-    } else {
-      g[v].zero();
-      if (c < cols) {  // the end of a width that is no multiple of 8
-#pragma unroll
-        for (int j = 0; j < 7; ++j)
-          if (c + j < cols) g[v].load1(j, row + c + j);
-      }
-    }
-  }
+  for (int v = 0; v < V; ++v) fetch_group(row, cols, column(v, 0, t, tpr), g[v]);
 }
 template <int V, typename T>
 __device__ __forceinline__ void load_row(const T *row, int cols, int t, int tpr, float out[V][8]) {
@@ -79,22 +84,36 @@ __device__ __forceinline__ void load_row(const T *row, int cols, int t, int tpr,
     for (int j = 0; j < 8; ++j) out[v][j] = g[v].at(j);
 }
 
+template <typename T>
+__device__ __forceinline__ void store_group(T *row, int cols, int c, const float in[8]) {
+  if (c + 8 <= cols) {
+    store8(row + c, in);
+  } else if (c < cols) {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (c + j < cols) store1(row + c + j, in[j]);
+  }
+}
 template <int V, typename T>
 __device__ __forceinline__ void store_row(T *row, int cols, int t, int tpr, const float in[V][8]) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int c = column(v, 0, t, tpr);
-    if (c + 8 <= cols) {
-      store8(row + c, in[v]);
-    } else if (c < cols) {
-#pragma unroll
-      for (int j = 0; j < 7; ++j)
-        if (c + j < cols) store1(row + c + j, in[v][j]);
-    }
-  }
+  for (int v = 0; v < V; ++v) store_group(row, cols, column(v, 0, t, tpr), in[v]);
 }
 
-// a thread's share of a weight
+// a thread's share of a weight, or a group of it
+template <typename T>
+__device__ __forceinline__ void load_group_of(const T *w, int cols, int c, float out[8]) {
+  Group<T> g;
+  fetch_group(w, cols, c, g);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) out[j] = g.at(j);
+}
+__device__ __forceinline__ void load_weight_group(const void *w, int bf16, int cols, int c, float out[8]) {
+  if (bf16)
+    load_group_of((const uint16_t *)w, cols, c, out);
+  else
+    load_group_of((const float *)w, cols, c, out);
+}
 template <int V>
 __device__ __forceinline__ void load_weight(const void *w, int bf16, int cols, int t, int tpr, float out[V][8]) {
   if (bf16)
@@ -106,6 +125,9 @@ __device__ __forceinline__ void load_weight(const void *w, int bf16, int cols, i
 // next row ahead.  Those of 1024 have 128 registers to a thread, which a row
 // of more than 8192 elements takes up: they read both when they are due.
 constexpr bool holds(int nt) { return nt <= 512; }
+// Above 16384 elements weights are read group by group, and the gradient's sums
+// over rows are a kernel's own: beside a row their registers would spill.
+constexpr bool by_group(int v) { return v > 2; }
 
 // blockDim = (TPR, rows per workgroup); more than one row only when TPR = 64.
 // The next row is loaded while this one is worked on.  Each wave takes the mean
@@ -116,7 +138,8 @@ template <typename TX, typename TY, int V, int NT>
 __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
   __shared__ float2 slots[2][16];
   __shared__ float counts[16];
-  const int t = threadIdx.x, tpr = blockDim.x, waves = tpr >> 6, wave = t >> 6;
+  int t = threadIdx.x;
+  const int tpr = blockDim.x, waves = tpr >> 6, wave = t >> 6;
   const int cols = (int)a.cols;
   const float inv = 1.0f / (float)cols;
   const int64_t step = (int64_t)gridDim.x * blockDim.y;
@@ -147,6 +170,7 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
   if (waves > 1 && (t & 63) == 0) counts[wave] = count;
   int turn = 0;
   for (; r < a.rows; r += step) {
+    if (by_group(V)) asm volatile("" : "+v"(t));  // what is formed of it stays out of registers between rows
     float x[V][8];
     if (!kHold) {
       fetch_row<V>((const TX *)a.x + r * a.ld_x, cols, t, tpr, gx);
@@ -200,16 +224,26 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
       a.mean[r] = mean;
       a.rstd[r] = rstd;
     }
-    if (!kHold) weights();
+    if (!kHold && !by_group(V)) weights();
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+      const int c = column(v, 0, t, tpr);
+      if (by_group(V)) {
+        load_weight_group(a.weight, w_bf16, cols, c, w[v]);
+        if (a.bias) load_weight_group(a.bias, w_bf16, cols, c, b[v]);
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float y = rounded<TY>(fmaf((x[v][j] - mean) * rstd, w[v][j], b[v][j]));
         x[v][j] = y;
-        if (a.amax && column(v, j, t, tpr) < cols) top = fmaxf(top, fabsf(y));
+        if (a.amax && c + j < cols) top = fmaxf(top, fabsf(y));
       }
-    store_row<V>((TY *)a.y + r * a.ld_y, cols, t, tpr, x);
+      if (by_group(V)) {
+        store_group((TY *)a.y + r * a.ld_y, cols, c, x[v]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    if (!by_group(V)) store_row<V>((TY *)a.y + r * a.ld_y, cols, t, tpr, x);
   }
   if (a.amax) fold_max(a.amax, top);
 }
@@ -223,7 +257,8 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
   __shared__ float2 slots[2][16];
   __shared__ float both[NT == 1024 ? 1 : 4][8][64];
   constexpr bool kHold = holds(NT);
-  const int t = threadIdx.x, tpr = blockDim.x, waves = tpr >> 6;
+  int t = threadIdx.x;
+  const int tpr = blockDim.x, waves = tpr >> 6;
   const int cols = (int)a.cols;
   const float inv = 1.0f / (float)cols;
   const bool w_bf16 = a.w_dtype == NVFP4_BF16;
@@ -247,6 +282,7 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
   if (kHold && r < a.rows) fetch(r, next_x, next_y, next_mean, next_rstd);
   int turn = 0;
   for (; r < a.rows; r += step) {
+    if (by_group(V)) asm volatile("" : "+v"(t));  // what is formed of it stays out of registers between rows
     if (kHold) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -259,19 +295,27 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
       if (r + step < a.rows) fetch(r + step, next_x, next_y, next_mean, next_rstd);
     } else {
       fetch(r, gx, gy, mean, rstd);
-      load_weight<V>(a.weight, w_bf16, cols, t, tpr, w);
+      if (!by_group(V)) load_weight<V>(a.weight, w_bf16, cols, t, tpr, w);
     }
+    const auto weights = [&](int v) {
+      __builtin_amdgcn_sched_barrier(0);
+      load_weight_group(a.weight, w_bf16, cols, column(v, 0, t, tpr), w[v]);
+    };
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+      if (by_group(V)) weights(v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {  // past the end: dy = w = 0
         const float h = (gx[v].at(j) - mean) * rstd, dy = gy[v].at(j), q = dy * w[v][j];
-        dw[v][j] = fmaf(dy, h, dw[v][j]);
-        db[v][j] += dy;
+        if (!by_group(V)) {
+          dw[v][j] = fmaf(dy, h, dw[v][j]);
+          db[v][j] += dy;
+        }
         s1 += q;
         s2 = fmaf(q, h, s2);
       }
+    }
     s1 = wave_sum(s1);
     s2 = wave_sum(s2);
     if (waves > 1) {
@@ -287,35 +331,38 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
       turn ^= 1;
     }
     const float c1 = s1 * inv, c2 = s2 * inv;
-    if (!kHold) {
+    if (!kHold && !by_group(V)) {
       if (a.dsum) fetch_row<V>((const TX *)a.dsum + r * a.ld_dsum, cols, t, tpr, gd);
       load_weight<V>(a.weight, w_bf16, cols, t, tpr, w);
     }
-    float x[V][8];
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+      const int c = column(v, 0, t, tpr);
+      if (by_group(V)) {
+        if (v == 0) asm volatile("" : "+v"(t));
+        weights(v);
+        if (a.dsum) fetch_group((const TX *)a.dsum + r * a.ld_dsum, cols, c, gd[v]);
+      }
+      float x[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float h = (gx[v].at(j) - mean) * rstd;
-        x[v][j] = rstd * (gy[v].at(j) * w[v][j] - fmaf(h, c2, c1));
+        x[j] = rstd * (gy[v].at(j) * w[v][j] - fmaf(h, c2, c1));
       }
-    if (a.dsum) {
+      if (a.dsum) {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[v][j] += gd[v].at(j);
-    }
-    store_row<V>((TX *)a.dx + r * a.ld_dx, cols, t, tpr, x);
-    if (a.amax) {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
+        for (int j = 0; j < 8; ++j) x[j] += gd[v].at(j);
+      }
+      store_group((TX *)a.dx + r * a.ld_dx, cols, c, x);
+      if (a.amax) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (column(v, j, t, tpr) < cols) top = fmaxf(top, fabsf(rounded<TX>(x[v][j])));
+          if (c + j < cols) top = fmaxf(top, fabsf(rounded<TX>(x[j])));
+      }
     }
   }
   if (a.amax) fold_max(a.amax, top);
-  if (!partials) return;
+  if (by_group(V) || !partials) return;
   float *out = partials + (int64_t)blockIdx.x * 2 * cols;
   if (blockDim.y == 1) {
     store_row<V>(out, cols, t, tpr, dw);
@@ -341,6 +388,44 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
         }
       }
   }
+}
+
+// The partial sums of rows above 16384 elements: 8 columns to a thread, every
+// gridDim.x-th row, several rows' loads in flight.
+template <typename TX, typename TY>
+__global__ __launch_bounds__(256) void layernorm_columns_kernel(nvfp4_layernorm_backward_args a, float *partials) {
+  const int cols = (int)a.cols, c = (int)(blockIdx.y * 256 + threadIdx.x) * 8;
+  if (c >= cols) return;
+  float dw[8] = {}, db[8] = {};
+  const auto add = [&](const Group<TX> &x, const Group<TY> &y, float mean, float rstd) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float dy = y.at(j);
+      dw[j] = fmaf(dy, (x.at(j) - mean) * rstd, dw[j]);
+      db[j] += dy;
+    }
+  };
+  if (c + 8 <= cols) {
+#pragma unroll 4
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+      Group<TX> x;
+      Group<TY> y;
+      x.load((const TX *)a.x + r * a.ld_x + c);
+      y.load((const TY *)a.dy + r * a.ld_dy + c);
+      add(x, y, a.mean[r], a.rstd[r]);
+    }
+  } else {
+    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+      Group<TX> x;
+      Group<TY> y;
+      fetch_group((const TX *)a.x + r * a.ld_x, cols, c, x);
+      fetch_group((const TY *)a.dy + r * a.ld_dy, cols, c, y);
+      add(x, y, a.mean[r], a.rstd[r]);
+    }
+  }
+  float *out = partials + (int64_t)blockIdx.x * 2 * cols;
+  store_group(out, cols, c, dw);
+  store_group(out + cols, cols, c, db);
 }
 
 // dweight and dbias from the partial sums: a workgroup adds 64 columns, 16
@@ -399,6 +484,9 @@ void run(const nvfp4_layernorm_args &a, float *, unsigned grid, dim3 block, hipS
 }
 template <typename TX, typename TY, int V, int NT>
 void run(const nvfp4_layernorm_backward_args &a, float *partials, unsigned grid, dim3 block, hipStream_t s) {
+  if (by_group(V) && partials)  // first: dx may stand where dy or x does
+    layernorm_columns_kernel<TX, TY><<<dim3((unsigned)layernorm_backward_parts(a.rows, a.cols),
+                                            (unsigned)((a.cols + 2047) / 2048)), 256, 0, s>>>(a, partials);
   layernorm_backward_kernel<TX, TY, V, NT><<<grid, block, 0, s>>>(a, partials);
 }
 
@@ -434,9 +522,11 @@ hipError_t launch_layernorm(const nvfp4_layernorm_args &a, hipStream_t s) {
 }
 
 // of the gradient: at least four rows to a workgroup beyond one to a compute
-// unit, since each adds a row to what the second kernel reads
+// unit, since each adds a row to what the second kernel reads; of the columns'
+// kernel 16 rows, up to 128 parts
 int64_t layernorm_backward_parts(int64_t rows, int64_t cols) {
   const Split p = split_of(cols);
+  if (by_group(p.v)) return rows > 2048 ? 128 : (rows + 15) / 16;
   const int64_t most = resident(p, rows, 12), few = (rows / p.block.y + 3) / 4;
   return most <= 256 || most < few ? most : few > 256 ? few : 256;
 }
@@ -444,7 +534,7 @@ int64_t layernorm_backward_parts(int64_t rows, int64_t cols) {
 hipError_t launch_layernorm_backward(const nvfp4_layernorm_backward_args &a, float *partials, hipStream_t s) {
   const Split p = split_of(a.cols);
   const int64_t parts = layernorm_backward_parts(a.rows, a.cols);
-  pick(p, a, partials, (unsigned)parts, s);
+  pick(p, a, partials, (unsigned)(by_group(p.v) ? resident(p, a.rows, 16) : parts), s);
   if (partials)
     layernorm_reduce_kernel<<<(unsigned)((2 * a.cols + 63) / 64), dim3(64, 16), 0, s>>>(partials, parts, a.cols,
                                                                                       a.dweight, a.dbias);

@@ -130,6 +130,27 @@ def test_backward(nv, rows, cols, pad, types):
         assert (dx._base[:, cols:] == 7.0).all(), "columns past the end were written"
 
 
+@pytest.mark.parametrize("rows,cols,pad", [(37, 16393, 3), (131, 20487, 0), (600, 16392, 8), (2100, 18440, 0)])
+@pytest.mark.parametrize("types", range(len(TYPES)))
+def test_wide(nv, rows, cols, pad, types):
+    """Rows whose sums over rows are a kernel of their own, and dx in the place of dy or of x."""
+    test_forward(nv, rows, cols, pad, types)
+    test_backward(nv, rows, cols, pad, types)
+    if types != 1 or rows > 200:
+        return
+    g = _gen(cols)
+    x, dy = _rand(g, rows, cols, torch.float32, 0), _rand(g, rows, cols, torch.float32, 0)
+    w = torch.randn(cols, generator=g, device="cuda")
+    _, mean, rstd, _ = nv.layernorm(x, w, w)
+    want = nv.layernorm_backward(dy, x, w, mean, rstd)
+    for place in (0, 1):
+        t = [dy.clone(), x.clone()]
+        dw, db = torch.empty_like(w), torch.empty_like(w)
+        ws = torch.empty(nv.lib().nvfp4_layernorm_backward_workspace_bytes(rows, cols), dtype=torch.uint8, device="cuda")
+        nv.nvfp4_layernorm_backward(t[0], t[1], w, mean, rstd, t[place], dw, db, workspace=ws)
+        assert torch.equal(t[place], want[0]) and torch.equal(dw, want[1]) and torch.equal(db, want[2])
+
+
 def test_gradient_against_differences(nv):
     """d/dt of sum(dy * layernorm(x + t z)) by central differences in 64 bits is sum(dx * z); so for weight and bias."""
     rows, cols = 6, 200
