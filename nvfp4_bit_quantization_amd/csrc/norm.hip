@@ -11,22 +11,40 @@
 // in 90 us (3.7 TB/s; 159 us before rows were loaded ahead and the two
 // exchanges of a row made one), the gradient of 16384x5120 671 MB in 144 us
 // (4.7 TB/s; 325 us before).  Small calls take what a launch does: 3 us for
-// 256x256.  Rows need no alignment beyond their elements': 8192x5120 bf16 takes
-// 51 us with rows 5123 elements apart and 49 us without a gap, 72 us at a width
-// of 5119, whose last group goes element by element.
-// Above 8192 elements neither weights nor the next row fit the registers
-// (4096x16384 bf16: 62 us, 4.3 TB/s out of a warm cache); above 16384 the
-// gradient's sums do not either: 4096x20480 bf16 takes 103 us (161 with all
-// groups' weights read at once, which spilled) and its gradient 197 in three
-// kernels, which read x and dy twice (611 in two, the sums in scratch memory).
+// 256x256.  Rows need no alignment beyond their elements'.  Above 8192 elements
+// neither weights nor the next row fit the registers; above 16384 the gradient's
+// sums do not either: 4096x20480 bf16 takes 95 us (161 with all groups' weights
+// read at once, which spilled) and its gradient 195 in three kernels, which read
+// x and dy twice (611 in two, the sums in scratch memory).
 #include "train_device.hpp"
 #include "train_kernels.hpp"
 
 namespace nvfp4 {
 namespace {
 
-// element j of a thread's group v
-__device__ __forceinline__ int column(int v, int j, int t, int tpr) { return (v * tpr + t) * 8 + j; }
+// Where a thread's group v stands: columns base .. base + 7, of which the first
+// `lead` are not its own (8: the group is past the end).  At a ragged width (R:
+// no multiple of 8) the last group starts at cols - 8, so that its load is one of
+// whole 16 bytes; what it repeats of its neighbour counts as zero in sums and is
+// not stored.  Widths below 8 have base < 0 and their elements at the end.
+// Against an end read element by element, 8192 rows of 5119 bf16 take 59 us
+// instead of 73, with a residual 106 instead of 143, their gradient 70 instead of
+// 120; 16384 rows of 2049, without a residual, 47 instead of 42.  Widths that are
+// multiples of 8 have kernels without it (8192x5120: 48 us, 54 with it).
+struct Place {
+  int base, lead;
+};
+template <bool R>
+__device__ __forceinline__ Place place(int v, int t, int tpr, int cols) {
+  const int c = (v * tpr + t) * 8;
+  if (!R) return {c, c < cols ? 0 : 8};
+  const int base = c < cols - 8 ? c : cols - 8;
+  return {base, c < cols ? c - base : 8};
+}
+template <bool R>
+__device__ __forceinline__ bool own(const Place &p, int j) {
+  return R ? j >= p.lead : p.lead == 0;
+}
 
 // 8 elements as they stand in memory: what is loaded ahead for the next row
 template <typename T>
@@ -54,72 +72,63 @@ struct Group<float> {
   __device__ __forceinline__ float at(int j) const { return x[j]; }
 };
 
-// elements c .. c + 7 of a row, zero outside [0, cols)
-template <typename T>
-__device__ __forceinline__ void fetch_group(const T *row, int cols, int c, Group<T> &g) {
-  if (c + 8 <= cols) {
-    g.load(row + c);
+// a group of a row, zero past the end; TINY: the width may be below 8
+template <bool TINY, typename T>
+__device__ __forceinline__ void fetch_group(const T *row, int cols, const Place &p, Group<T> &g) {
+  if (p.lead == 8) {
+    g.zero();
+  } else if (!TINY || cols >= 8) {
+    g.load(row + p.base);
   } else {
     g.zero();
-    if (c < cols) {  // the end of a width that is no multiple of 8
 #pragma unroll
-      for (int j = 0; j < 7; ++j)
-        if (c + j < cols) g.load1(j, row + c + j);
-    }
+    for (int j = 1; j < 8; ++j)
+      if (j >= p.lead) g.load1(j, row + p.base + j);
   }
 }
 // a thread's share of a row
-template <int V, typename T>
+template <int V, bool R, typename T>
 __device__ __forceinline__ void fetch_row(const T *row, int cols, int t, int tpr, Group<T> g[V]) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) fetch_group(row, cols, column(v, 0, t, tpr), g[v]);
-}
-template <int V, typename T>
-__device__ __forceinline__ void load_row(const T *row, int cols, int t, int tpr, float out[V][8]) {
-  Group<T> g[V];
-  fetch_row<V>(row, cols, t, tpr, g);
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) out[v][j] = g[v].at(j);
+  for (int v = 0; v < V; ++v) fetch_group<(R && V == 1)>(row, cols, place<R>(v, t, tpr, cols), g[v]);
 }
 
-template <typename T>
-__device__ __forceinline__ void store_group(T *row, int cols, int c, const float in[8]) {
-  if (c + 8 <= cols) {
-    store8(row + c, in);
-  } else if (c < cols) {
+template <bool R, typename T>
+__device__ __forceinline__ void store_group(T *row, const Place &p, const float in[8]) {
+  if (p.lead == 0) {
+    store8(row + p.base, in);
+  } else if (R && p.lead < 8) {
 #pragma unroll
-    for (int j = 0; j < 7; ++j)
-      if (c + j < cols) store1(row + c + j, in[j]);
+    for (int j = 1; j < 8; ++j)
+      if (j >= p.lead) store1(row + p.base + j, in[j]);
   }
 }
-template <int V, typename T>
+template <int V, bool R, typename T>
 __device__ __forceinline__ void store_row(T *row, int cols, int t, int tpr, const float in[V][8]) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) store_group(row, cols, column(v, 0, t, tpr), in[v]);
+  for (int v = 0; v < V; ++v) store_group<R>(row, place<R>(v, t, tpr, cols), in[v]);
 }
 
-// a thread's share of a weight, or a group of it
-template <typename T>
-__device__ __forceinline__ void load_group_of(const T *w, int cols, int c, float out[8]) {
+// a group of a weight, zero where the elements are not its own
+template <bool TINY, bool R, typename T>
+__device__ __forceinline__ void load_group_of(const T *w, int cols, const Place &p, float out[8]) {
   Group<T> g;
-  fetch_group(w, cols, c, g);
+  fetch_group<TINY>(w, cols, p, g);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) out[j] = g.at(j);
+  for (int j = 0; j < 8; ++j) out[j] = !R || own<R>(p, j) ? g.at(j) : 0.0f;
 }
-__device__ __forceinline__ void load_weight_group(const void *w, int bf16, int cols, int c, float out[8]) {
+template <int V, bool R>
+__device__ __forceinline__ void load_weight_group(const void *w, int bf16, int cols, const Place &p, float out[8]) {
   if (bf16)
-    load_group_of((const uint16_t *)w, cols, c, out);
+    load_group_of<(R && V == 1), R>((const uint16_t *)w, cols, p, out);
   else
-    load_group_of((const float *)w, cols, c, out);
+    load_group_of<(R && V == 1), R>((const float *)w, cols, p, out);
 }
-template <int V>
+// a thread's share of a weight
+template <int V, bool R>
 __device__ __forceinline__ void load_weight(const void *w, int bf16, int cols, int t, int tpr, float out[V][8]) {
-  if (bf16)
-    load_row<V>((const uint16_t *)w, cols, t, tpr, out);
-  else
-    load_row<V>((const float *)w, cols, t, tpr, out);
+#pragma unroll
+  for (int v = 0; v < V; ++v) load_weight_group<V, R>(w, bf16, cols, place<R>(v, t, tpr, cols), out[v]);
 }
 // Workgroups of up to 512 threads keep the weights in registers and load the
 // next row ahead.  Those of 1024 have 128 registers to a thread, which a row
@@ -134,7 +143,7 @@ constexpr bool by_group(int v) { return v > 2; }
 // of its part and the sum of squares about that; one exchange joins them (n_w
 // elements, mean_w, q_w to a wave):
 //   mean = sum n_w mean_w / n,  q = sum q_w + n_w (mean_w - mean)^2
-template <typename TX, typename TY, int V, int NT>
+template <typename TX, typename TY, int V, int NT, bool R>
 __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
   __shared__ float2 slots[2][16];
   __shared__ float counts[16];
@@ -148,13 +157,13 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
   const bool w_bf16 = a.w_dtype == NVFP4_BF16;
   Group<TX> gx[V], gr[V];
   if (kHold && r < a.rows) {
-    fetch_row<V>((const TX *)a.x + r * a.ld_x, cols, t, tpr, gx);
-    if (a.residual) fetch_row<V>((const TX *)a.residual + r * a.ld_residual, cols, t, tpr, gr);
+    fetch_row<V, R>((const TX *)a.x + r * a.ld_x, cols, t, tpr, gx);
+    if (a.residual) fetch_row<V, R>((const TX *)a.residual + r * a.ld_residual, cols, t, tpr, gr);
   }
   float w[V][8], b[V][8], top = 0.0f;
   const auto weights = [&] {
-    load_weight<V>(a.weight, w_bf16, cols, t, tpr, w);
-    if (a.bias) load_weight<V>(a.bias, w_bf16, cols, t, tpr, b);
+    load_weight<V, R>(a.weight, w_bf16, cols, t, tpr, w);
+    if (a.bias) load_weight<V, R>(a.bias, w_bf16, cols, t, tpr, b);
   };
 #pragma unroll
   for (int v = 0; v < V; ++v)
@@ -165,7 +174,7 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mine += column(v, j, t, tpr) < cols;
+    for (int j = 0; j < 8; ++j) mine += own<R>(place<R>(v, t, tpr, cols), j);
   const float count = wave_sum((float)mine), inv_w = count > 0.0f ? 1.0f / count : 0.0f;
   if (waves > 1 && (t & 63) == 0) counts[wave] = count;
   int turn = 0;
@@ -173,8 +182,8 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
     if (by_group(V)) asm volatile("" : "+v"(t));  // what is formed of it stays out of registers between rows
     float x[V][8];
     if (!kHold) {
-      fetch_row<V>((const TX *)a.x + r * a.ld_x, cols, t, tpr, gx);
-      if (a.residual) fetch_row<V>((const TX *)a.residual + r * a.ld_residual, cols, t, tpr, gr);
+      fetch_row<V, R>((const TX *)a.x + r * a.ld_x, cols, t, tpr, gx);
+      if (a.residual) fetch_row<V, R>((const TX *)a.residual + r * a.ld_residual, cols, t, tpr, gr);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v)
@@ -187,21 +196,21 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
         for (int j = 0; j < 8; ++j) x[v][j] = rounded<TX>(x[v][j] + gr[v].at(j));
     }
     if (kHold && r + step < a.rows) {
-      fetch_row<V>((const TX *)a.x + (r + step) * a.ld_x, cols, t, tpr, gx);
-      if (a.residual) fetch_row<V>((const TX *)a.residual + (r + step) * a.ld_residual, cols, t, tpr, gr);
+      fetch_row<V, R>((const TX *)a.x + (r + step) * a.ld_x, cols, t, tpr, gx);
+      if (a.residual) fetch_row<V, R>((const TX *)a.residual + (r + step) * a.ld_residual, cols, t, tpr, gr);
     }
-    if (a.residual) store_row<V>((TX *)a.sum + r * a.ld_sum, cols, t, tpr, x);
+    if (a.residual) store_row<V, R>((TX *)a.sum + r * a.ld_sum, cols, t, tpr, x);
     float s = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s += x[v][j];
+      for (int j = 0; j < 8; ++j) s += !R || own<R>(place<R>(v, t, tpr, cols), j) ? x[v][j] : 0.0f;
     float mean = wave_sum(s) * inv_w, q = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float d = column(v, j, t, tpr) < cols ? x[v][j] - mean : 0.0f;
+        const float d = own<R>(place<R>(v, t, tpr, cols), j) ? x[v][j] - mean : 0.0f;
         q = fmaf(d, d, q);
       }
     q = wave_sum(q);
@@ -227,23 +236,23 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
     if (!kHold && !by_group(V)) weights();
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = column(v, 0, t, tpr);
+      const Place at = place<R>(v, t, tpr, cols);
       if (by_group(V)) {
-        load_weight_group(a.weight, w_bf16, cols, c, w[v]);
-        if (a.bias) load_weight_group(a.bias, w_bf16, cols, c, b[v]);
+        load_weight_group<V, R>(a.weight, w_bf16, cols, at, w[v]);
+        if (a.bias) load_weight_group<V, R>(a.bias, w_bf16, cols, at, b[v]);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float y = rounded<TY>(fmaf((x[v][j] - mean) * rstd, w[v][j], b[v][j]));
         x[v][j] = y;
-        if (a.amax && c + j < cols) top = fmaxf(top, fabsf(y));
+        if (a.amax && own<R>(at, j)) top = fmaxf(top, fabsf(y));
       }
       if (by_group(V)) {
-        store_group((TY *)a.y + r * a.ld_y, cols, c, x[v]);
+        store_group<R>((TY *)a.y + r * a.ld_y, at, x[v]);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
-    if (!by_group(V)) store_row<V>((TY *)a.y + r * a.ld_y, cols, t, tpr, x);
+    if (!by_group(V)) store_row<V, R>((TY *)a.y + r * a.ld_y, cols, t, tpr, x);
   }
   if (a.amax) fold_max(a.amax, top);
 }
@@ -252,7 +261,7 @@ __global__ __launch_bounds__(NT) void layernorm_kernel(nvfp4_layernorm_args a) {
 // twice from the row as it was loaded, before and after that, which keeps fewer
 // registers than holding them.  The sums over rows stay in registers and are
 // written once per workgroup, [blockIdx][dweight, dbias][cols].
-template <typename TX, typename TY, int V, int NT>
+template <typename TX, typename TY, int V, int NT, bool R>
 __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_backward_args a, float *partials) {
   __shared__ float2 slots[2][16];
   __shared__ float both[NT == 1024 ? 1 : 4][8][64];
@@ -263,7 +272,7 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
   const float inv = 1.0f / (float)cols;
   const bool w_bf16 = a.w_dtype == NVFP4_BF16;
   float w[V][8], dw[V][8], db[V][8], top = 0.0f;
-  if (kHold) load_weight<V>(a.weight, w_bf16, cols, t, tpr, w);
+  if (kHold) load_weight<V, R>(a.weight, w_bf16, cols, t, tpr, w);
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -274,8 +283,8 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
   Group<TY> gy[V], next_y[V];
   float mean = 0.0f, rstd = 0.0f, next_mean = 0.0f, next_rstd = 0.0f;
   const auto fetch = [&](int64_t row, Group<TX> *x, Group<TY> *y, float &m, float &s) {
-    fetch_row<V>((const TX *)a.x + row * a.ld_x, cols, t, tpr, x);
-    fetch_row<V>((const TY *)a.dy + row * a.ld_dy, cols, t, tpr, y);
+    fetch_row<V, R>((const TX *)a.x + row * a.ld_x, cols, t, tpr, x);
+    fetch_row<V, R>((const TY *)a.dy + row * a.ld_dy, cols, t, tpr, y);
     m = a.mean[row];
     s = a.rstd[row];
   };
@@ -291,22 +300,22 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
       }
       mean = next_mean;
       rstd = next_rstd;
-      if (a.dsum) fetch_row<V>((const TX *)a.dsum + r * a.ld_dsum, cols, t, tpr, gd);
+      if (a.dsum) fetch_row<V, R>((const TX *)a.dsum + r * a.ld_dsum, cols, t, tpr, gd);
       if (r + step < a.rows) fetch(r + step, next_x, next_y, next_mean, next_rstd);
     } else {
       fetch(r, gx, gy, mean, rstd);
-      if (!by_group(V)) load_weight<V>(a.weight, w_bf16, cols, t, tpr, w);
+      if (!by_group(V)) load_weight<V, R>(a.weight, w_bf16, cols, t, tpr, w);
     }
     const auto weights = [&](int v) {
       __builtin_amdgcn_sched_barrier(0);
-      load_weight_group(a.weight, w_bf16, cols, column(v, 0, t, tpr), w[v]);
+      load_weight_group<V, R>(a.weight, w_bf16, cols, place<R>(v, t, tpr, cols), w[v]);
     };
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (by_group(V)) weights(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {  // past the end: dy = w = 0
+      for (int j = 0; j < 8; ++j) {  // elements that are not its own: w = 0, and dw, db are not stored
         const float h = (gx[v].at(j) - mean) * rstd, dy = gy[v].at(j), q = dy * w[v][j];
         if (!by_group(V)) {
           dw[v][j] = fmaf(dy, h, dw[v][j]);
@@ -332,16 +341,16 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
     }
     const float c1 = s1 * inv, c2 = s2 * inv;
     if (!kHold && !by_group(V)) {
-      if (a.dsum) fetch_row<V>((const TX *)a.dsum + r * a.ld_dsum, cols, t, tpr, gd);
-      load_weight<V>(a.weight, w_bf16, cols, t, tpr, w);
+      if (a.dsum) fetch_row<V, R>((const TX *)a.dsum + r * a.ld_dsum, cols, t, tpr, gd);
+      load_weight<V, R>(a.weight, w_bf16, cols, t, tpr, w);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = column(v, 0, t, tpr);
+      const Place at = place<R>(v, t, tpr, cols);
       if (by_group(V)) {
         if (v == 0) asm volatile("" : "+v"(t));
         weights(v);
-        if (a.dsum) fetch_group((const TX *)a.dsum + r * a.ld_dsum, cols, c, gd[v]);
+        if (a.dsum) fetch_group<false>((const TX *)a.dsum + r * a.ld_dsum, cols, at, gd[v]);
       }
       float x[8];
 #pragma unroll
@@ -353,11 +362,11 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
 #pragma unroll
         for (int j = 0; j < 8; ++j) x[j] += gd[v].at(j);
       }
-      store_group((TX *)a.dx + r * a.ld_dx, cols, c, x);
+      store_group<R>((TX *)a.dx + r * a.ld_dx, at, x);
       if (a.amax) {
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (c + j < cols) top = fmaxf(top, fabsf(rounded<TX>(x[j])));
+          if (own<R>(at, j)) top = fmaxf(top, fabsf(rounded<TX>(x[j])));
       }
     }
   }
@@ -365,8 +374,8 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
   if (by_group(V) || !partials) return;
   float *out = partials + (int64_t)blockIdx.x * 2 * cols;
   if (blockDim.y == 1) {
-    store_row<V>(out, cols, t, tpr, dw);
-    store_row<V>(out + cols, cols, t, tpr, db);
+    store_row<V, R>(out, cols, t, tpr, dw);
+    store_row<V, R>(out + cols, cols, t, tpr, db);
     return;
   }
   // the rows of the workgroup's four waves, added in their order: each wave
@@ -382,9 +391,10 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int j = 2 * threadIdx.y + i, c = column(v, j, t, tpr);
+          const int j = 2 * threadIdx.y + i;
+          const Place at = place<R>(v, t, tpr, cols);
           const float s = (both[0][j][t] + both[1][j][t]) + (both[2][j][t] + both[3][j][t]);
-          if (c < cols) out[c] = s;
+          if (own<R>(at, j)) out[at.base + j] = s;
         }
       }
   }
@@ -392,40 +402,29 @@ __global__ __launch_bounds__(NT) void layernorm_backward_kernel(nvfp4_layernorm_
 
 // The partial sums of rows above 16384 elements: 8 columns to a thread, every
 // gridDim.x-th row, several rows' loads in flight.
-template <typename TX, typename TY>
+template <typename TX, typename TY, bool R>
 __global__ __launch_bounds__(256) void layernorm_columns_kernel(nvfp4_layernorm_backward_args a, float *partials) {
-  const int cols = (int)a.cols, c = (int)(blockIdx.y * 256 + threadIdx.x) * 8;
-  if (c >= cols) return;
+  const int cols = (int)a.cols;
+  const Place at = place<R>(0, (int)(blockIdx.y * 256 + threadIdx.x), 0, cols);
+  if (at.lead == 8) return;
   float dw[8] = {}, db[8] = {};
-  const auto add = [&](const Group<TX> &x, const Group<TY> &y, float mean, float rstd) {
+#pragma unroll 4
+  for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    Group<TX> x;
+    Group<TY> y;
+    x.load((const TX *)a.x + r * a.ld_x + at.base);
+    y.load((const TY *)a.dy + r * a.ld_dy + at.base);
+    const float mean = a.mean[r], rstd = a.rstd[r];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float dy = y.at(j);
       dw[j] = fmaf(dy, (x.at(j) - mean) * rstd, dw[j]);
       db[j] += dy;
     }
-  };
-  if (c + 8 <= cols) {
-#pragma unroll 4
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-      Group<TX> x;
-      Group<TY> y;
-      x.load((const TX *)a.x + r * a.ld_x + c);
-      y.load((const TY *)a.dy + r * a.ld_dy + c);
-      add(x, y, a.mean[r], a.rstd[r]);
-    }
-  } else {
-    for (int64_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
-      Group<TX> x;
-      Group<TY> y;
-      fetch_group((const TX *)a.x + r * a.ld_x, cols, c, x);
-      fetch_group((const TY *)a.dy + r * a.ld_dy, cols, c, y);
-      add(x, y, a.mean[r], a.rstd[r]);
-    }
   }
   float *out = partials + (int64_t)blockIdx.x * 2 * cols;
-  store_group(out, cols, c, dw);
-  store_group(out + cols, cols, c, db);
+  store_group<R>(out, at, dw);
+  store_group<R>(out + cols, at, db);
 }
 
 // dweight and dbias from the partial sums: a workgroup adds 64 columns, 16
@@ -478,39 +477,46 @@ int64_t resident(const Split &p, int64_t rows, int waves) {
   return groups < most ? groups : most;
 }
 
-template <typename TX, typename TY, int V, int NT>
+template <typename TX, typename TY, int V, int NT, bool R>
 void run(const nvfp4_layernorm_args &a, float *, unsigned grid, dim3 block, hipStream_t s) {
-  layernorm_kernel<TX, TY, V, NT><<<grid, block, 0, s>>>(a);
+  layernorm_kernel<TX, TY, V, NT, R><<<grid, block, 0, s>>>(a);
 }
-template <typename TX, typename TY, int V, int NT>
+template <typename TX, typename TY, int V, int NT, bool R>
 void run(const nvfp4_layernorm_backward_args &a, float *partials, unsigned grid, dim3 block, hipStream_t s) {
   if (by_group(V) && partials)  // first: dx may stand where dy or x does
-    layernorm_columns_kernel<TX, TY><<<dim3((unsigned)layernorm_backward_parts(a.rows, a.cols),
+    layernorm_columns_kernel<TX, TY, R><<<dim3((unsigned)layernorm_backward_parts(a.rows, a.cols),
                                             (unsigned)((a.cols + 2047) / 2048)), 256, 0, s>>>(a, partials);
-  layernorm_backward_kernel<TX, TY, V, NT><<<grid, block, 0, s>>>(a, partials);
+  layernorm_backward_kernel<TX, TY, V, NT, R><<<grid, block, 0, s>>>(a, partials);
 }
 
-template <typename TX, typename TY, typename A>
+template <typename TX, typename TY, bool R, typename A>
 void pick_split(const Split &p, const A &a, float *partials, unsigned grid, hipStream_t s) {
   if (p.v == 1)
-    run<TX, TY, 1, 256>(a, partials, grid, p.block, s);
+    run<TX, TY, 1, 256, R>(a, partials, grid, p.block, s);
   else if (p.v == 2 && p.nt == 512)
-    run<TX, TY, 2, 512>(a, partials, grid, p.block, s);
+    run<TX, TY, 2, 512, R>(a, partials, grid, p.block, s);
   else if (p.v == 2)
-    run<TX, TY, 2, 1024>(a, partials, grid, p.block, s);
+    run<TX, TY, 2, 1024, R>(a, partials, grid, p.block, s);
   else
-    run<TX, TY, 4, 1024>(a, partials, grid, p.block, s);
+    run<TX, TY, 4, 1024, R>(a, partials, grid, p.block, s);
+}
+template <typename TX, typename TY, typename A>
+void pick_width(const Split &p, const A &a, float *partials, unsigned grid, hipStream_t s) {
+  if (a.cols % 8)
+    pick_split<TX, TY, true>(p, a, partials, grid, s);
+  else
+    pick_split<TX, TY, false>(p, a, partials, grid, s);
 }
 template <typename A>
 void pick(const Split &p, const A &a, float *partials, unsigned grid, hipStream_t s) {
   if (a.x_dtype == NVFP4_BF16 && a.y_dtype == NVFP4_BF16)
-    pick_split<uint16_t, uint16_t>(p, a, partials, grid, s);
+    pick_width<uint16_t, uint16_t>(p, a, partials, grid, s);
   else if (a.x_dtype == NVFP4_BF16)
-    pick_split<uint16_t, float>(p, a, partials, grid, s);
+    pick_width<uint16_t, float>(p, a, partials, grid, s);
   else if (a.y_dtype == NVFP4_BF16)
-    pick_split<float, uint16_t>(p, a, partials, grid, s);
+    pick_width<float, uint16_t>(p, a, partials, grid, s);
   else
-    pick_split<float, float>(p, a, partials, grid, s);
+    pick_width<float, float>(p, a, partials, grid, s);
 }
 
 }  // namespace
