@@ -8,8 +8,8 @@
 // Workgroups walk over rows with the weights kept in registers.
 //
 // Both passes are bound by memory: 8192x5120 bf16 with a residual moves 336 MB
-// in 90 us (3.7 TB/s; 159 us before rows were loaded ahead and the two
-// exchanges of a row made one), the gradient of 16384x5120 671 MB in 144 us
+// in 88 us (3.8 TB/s; 159 us before rows were loaded ahead and the two
+// exchanges of a row made one), the gradient of 16384x5120 671 MB in 142 us
 // (4.7 TB/s; 325 us before).  Small calls take what a launch does: 3 us for
 // 256x256.  Rows need no alignment beyond their elements'.  Above 8192 elements
 // neither weights nor the next row fit the registers; above 16384 the gradient's
