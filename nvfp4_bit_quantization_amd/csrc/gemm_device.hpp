@@ -19,13 +19,14 @@ typedef __attribute__((address_space(3))) void lds_void_t;
 __device__ __forceinline__ uint32_t lds_addr(const void *p) { return (uint32_t)(size_t)(lds_void_t *)p; }
 
 // one wave-wide direct transfer: lane l's 16 (4) bytes at base + voff land at
-// LDS byte lds + 16 l (4 l).  The transfer needs a wait state after the write of
-// M0, which the compiler does not insert inside asm.
+// LDS byte lds + 16 l (4 l).  The compiler inserts no wait states inside asm: a
+// transfer needs one after the write of M0, and five after a vector instruction
+// that wrote a register of its base (a base from a lane, or reloaded from one).
 __device__ __forceinline__ void dma16(const void *base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(const void *base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
 }
 
 // a pointer the caller knows to be wave-uniform, in scalar registers (the

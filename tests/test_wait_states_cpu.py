@@ -3,7 +3,8 @@ kernels' assembly.  The transfers from global memory to LDS are written in
 inline asm, into which the compiler's own pass for them does not look.
 
 A GFX9 transfer to LDS takes its LDS address from M0 and needs a wait state (an
-instruction, or a count of s_nop) after the scalar instruction that wrote it."""
+instruction, or a count of s_nop) after the scalar instruction that wrote it, and
+any memory access needs five after a vector instruction wrote its scalar base."""
 import os
 import re
 import shutil
@@ -85,3 +86,24 @@ def test_transfer_waits_for_m0(transfers):
     for src, kernel, x, i, ins, before in transfers:
         n = _wait_states(i, ins, before, lambda y: re.match(r"s_\w+ m0\b", y))
         assert 1 <= n < FAR, "%s, %s: %d wait states between M0 and %s" % (src, kernel, n, x)
+
+
+def _scalars(text):
+    """The scalar registers named in some operands."""
+    out = set()
+    for m in re.finditer(r"\bs(?:(\d+)\b|\[(\d+):(\d+)\])", text):
+        out |= {int(m.group(1))} if m.group(1) else set(range(int(m.group(2)), int(m.group(3)) + 1))
+    return out
+
+
+def test_transfer_waits_for_its_base(transfers):
+    """A base address that the vector unit wrote (a lane's value, a reload of a spilled one) needs five wait states."""
+    for src, kernel, x, i, ins, before in transfers:
+        base = _scalars(x)
+        assert base, x
+
+        def writes(y):
+            return y.startswith("v_") and bool(base & _scalars(y.split(None, 1)[1].split(",")[0]))
+
+        n = _wait_states(i, ins, before, writes)
+        assert n >= 5, "%s, %s: %d wait states between a vector instruction and %s" % (src, kernel, n, x)
