@@ -21,22 +21,26 @@ __device__ __forceinline__ uint32_t lds_addr(const void *p) { return (uint32_t)(
 // one wave-wide direct transfer: lane l's 16 (4) bytes at base + voff land at
 // LDS byte lds + 16 l (4 l).  The compiler inserts no wait states inside asm: a
 // transfer needs one after the write of M0, and five after a vector instruction
-// that wrote a register of its base (a base from a lane, or reloaded from one).
+// that wrote a register of its base, of which uniform_ptr leaves three (all
+// five here: 2 % of the NVFP4 GEMM at 5120x5120x8192).
 __device__ __forceinline__ void dma16(const void *base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(const void *base, uint32_t voff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory", "m0");
 }
 
 // a pointer the caller knows to be wave-uniform, in scalar registers (the
-// transfers take their base address from SGPRs).  The NVFP4 fast path moves
+// transfers take their base address from SGPRs), three wait states after the
+// vector instruction that may have written them.  The NVFP4 fast path moves
 // this base by the K-tile offset; the MXFP4 kernel, which issues its ten
 // transfers back to back, was 14 % slower that way and adds the offset per lane.
 __device__ __forceinline__ const uint8_t *uniform_ptr(const uint8_t *p) {
   const uint64_t v = (uint64_t)p;
-  return (const uint8_t *)(((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32) |
-                           (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v));
+  uint64_t u = ((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32) |
+               (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
+  asm("s_nop 2" : "+s"(u));
+  return (const uint8_t *)u;
 }
 
 // vmcnt <= n (other counters untouched)
