@@ -501,7 +501,7 @@ typedef struct {
 typedef struct {
   float lr;            /* >= 0 */
   double beta1, beta2; /* [0, 1) */
-  float eps;           /* > 0 */
+  float eps;           /* a normal number, >= 2^-126 */
   int32_t rounding;    /* NVFP4_RTN or NVFP4_SR: of 8-bit states, and of bf16 params */
   int64_t step;        /* t = 1, 2, ..., below 2^47 */
   uint64_t seed;       /* Philox key of NVFP4_SR */
@@ -510,7 +510,8 @@ typedef struct {
 
 /*
  * nvfp4_adamw -- one AdamW step (Loshchilov and Hutter, "Decoupled weight
- * decay regularization") of every tensor, binary32 arithmetic:
+ * decay regularization") of every tensor, binary32 arithmetic with subnormal
+ * numbers kept (a square below 2^-150 is zero, one above 2^128 infinite):
  *   g = grad * grad_scale, m = beta1 m + (1 - beta1) g,
  *   v = beta2 v + (1 - beta2) g^2,
  *   param = param (1 - lr weight_decay)

@@ -169,17 +169,27 @@ __device__ __forceinline__ float step8(const AdamArgs &a, const AdamTensor &t, c
     get8((const float *)t.m + i0, have, m);
     get8((const float *)t.v + i0, have, v);
   }
-  float r[8];
+  float r[8], least = INFINITY;
+  // the square root and reciprocal instructions: 1 unit in the last place
+  // each, next to the update's ten other roundings.  Both read subnormal
+  // numbers as zero: the reciprocal's is at least eps, which is normal; the
+  // root takes such squares (of gradients below some 1e-18) times 2^64
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float y = g[j] * gs;
     m[j] = m[j] * a.beta1 + y * a.one_minus_beta1;
     v[j] = v[j] * a.beta2 + y * y * a.one_minus_beta2;
-    // the square root and reciprocal instructions: 1 unit in the last place
-    // each, next to the update's ten other roundings
+    least = fminf(least, v[j]);
     r[j] = __builtin_amdgcn_sqrtf(v[j]);
-    p[j] = p[j] * t.keep - a.lr * ((m[j] * a.correct1) * __builtin_amdgcn_rcpf(r[j] * a.correct2 + a.eps));
   }
+  if (least < 0x1p-126f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (v[j] < 0x1p-126f) r[j] = __builtin_amdgcn_sqrtf(v[j] * 0x1p64f) * 0x1p-32f;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    p[j] = p[j] * t.keep - a.lr * ((m[j] * a.correct1) * __builtin_amdgcn_rcpf(r[j] * a.correct2 + a.eps));
   if constexpr (SR && sizeof(TP) == 2) {
     draw(a, t.index, 2u, i0 >> 3, w);
 #pragma unroll

@@ -1,6 +1,7 @@
 // C ABI of the training operators: argument validation on the host, then
 // kernel launches on the caller's stream.  The entry points and their
 // contracts are declared and documented in include/nvfp4.h.
+#include <float.h>
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -281,7 +282,7 @@ int nvfp4_adamw(const nvfp4_adamw_tensor *tensors, int64_t n_tensors, const nvfp
   if (n_tensors < 1 || n_tensors >= ((int64_t)1 << 30)) return NVFP4_E_SHAPE;
   if (c->rounding != NVFP4_RTN && c->rounding != NVFP4_SR) return NVFP4_E_UNSUPPORTED;
   if (!(c->lr >= 0.0f) || !isfinite(c->lr) || !(c->beta1 >= 0.0 && c->beta1 < 1.0) ||
-      !(c->beta2 >= 0.0 && c->beta2 < 1.0) || !(c->eps > 0.0f) || !isfinite(c->eps) || c->step < 1 ||
+      !(c->beta2 >= 0.0 && c->beta2 < 1.0) || !(c->eps >= FLT_MIN) || !isfinite(c->eps) || c->step < 1 ||
       c->step >= ((int64_t)1 << 47))
     return NVFP4_E_VALUE;
   if (c->grad_scale && !aligned(c->grad_scale, 4)) return NVFP4_E_ALIGN;

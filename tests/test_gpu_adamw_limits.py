@@ -1,0 +1,50 @@
+"""AdamW where numbers leave the normal range, against the formulas in 64 bits."""
+import numpy as np
+import pytest
+
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+ULP, LEAST_NORMAL, HALF_LEAST = 2.0 ** -24, 2.0 ** -126, 2.0 ** -150
+
+
+@pytest.fixture(scope="module")
+def nv():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import nvfp4_bit_quantization_amd as nv
+    nv.lib()
+    return nv
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-8, 1e-20, LEAST_NORMAL])
+def test_small_gradients(nv, bits, eps):
+    """First steps on gradients of 1e-23 to 1e-12, whose squares are subnormal in binary32 up to some 1e-18, and on
+    zeros.  A product or sum of subnormal result is off by half of 2^-149, any other by 2^-24 of itself; the update's
+    other dozen operations by 16 * 2^-24."""
+    say("adamw small gradients", bits, eps)
+    n, lr, b1, b2 = 1024, float(np.float32(1e-3)), 0.9, 0.999
+    g = np.float32(10.0 ** np.linspace(-23, -12, n)) * np.where(np.arange(n) % 3 == 1, -1, 1).astype(np.float32)
+    g[::7] = 0
+    p = torch.zeros(n, device="cuda")
+    t = nv.adamw_tensor(p, torch.from_numpy(g).cuda(), state_bits=bits)
+    nv.adamw([t], lr=1e-3, beta1=b1, beta2=b2, eps=eps, step=1, rounding="sr", seed=5)
+    got, x, eps = p.double().cpu().numpy(), g.astype(np.float64), float(np.float32(eps))
+    v = (1 - b2) * x * x
+    tv = 4 * ULP * v + 2 * HALF_LEAST
+    step = [lr * np.abs(x) / (np.sqrt(np.maximum(w, 0) / (1 - b2)) + eps) for w in (v + tv, v - tv)]
+    assert np.isfinite(got).all()
+    assert (got[x == 0] == 0).all()
+    live = x != 0
+    low, high = step[0] * (1 - 16 * ULP) - HALF_LEAST, step[1] * (1 + 16 * ULP) + HALF_LEAST
+    assert ((got[live] < 0) == (x[live] > 0)).all()
+    bad = live & ((np.abs(got) < low) | (np.abs(got) > high))
+    assert not bad.any(), "%d updates; the first: gradient %g moved %g instead of %g" % (
+        bad.sum(), x[bad][0], got[bad][0], step[0][bad][0])
+    root = t.v.cpu().numpy()
+    sure = v - tv > 0
+    assert ((root & 127 if bits == 8 else root)[sure] > 0).all(), "a root is stored as zero"
