@@ -502,7 +502,7 @@ typedef struct {
   float lr;            /* >= 0 */
   double beta1, beta2; /* [0, 1) */
   float eps;           /* a normal number, >= 2^-126 */
-  int32_t rounding;    /* NVFP4_RTN or NVFP4_SR: of 8-bit states, and of bf16 params */
+  int32_t rounding;    /* of 8-bit states (NVFP4_SR, see below) and of bf16 params: NVFP4_RTN or NVFP4_SR */
   int64_t step;        /* t = 1, 2, ..., below 2^47 */
   uint64_t seed;       /* Philox key of NVFP4_SR */
   const float *grad_scale; /* NULL, or device float: multiplies every gradient */
@@ -521,7 +521,10 @@ typedef struct {
  * with max |x| <= 448 * 2^e, its elements x / 2^e in E4M3.  NVFP4_SR rounds |x| / 2^e
  * up with the probability of its place between its two E4M3 neighbours, by a
  * 16-bit uniform; a non-zero r is never stored as zero (its square root
- * divides).  bf16 params under NVFP4_SR add 16 uniform bits below the kept
+ * divides).  NVFP4_RTN rounds 8-bit states to nearest: r then stays where
+ * it is, since a step moves it by less than half of an E4M3 step, and as the bias
+ * correction fades, updates grow by up to 1 / sqrt(1 - beta2); it is there for
+ * single steps and comparisons, training wants NVFP4_SR.  bf16 params under NVFP4_SR add 16 uniform bits below the kept
  * ones and truncate.  The uniforms of element i of tensor index (its place in
  * `tensors`) are half i & 1 of word (i mod 8) / 2 of Philox4x32-10(key = seed,
  * counter = (i / 8, 4 index + which, step mod 2^32, 0x41440000 + step / 2^32)),

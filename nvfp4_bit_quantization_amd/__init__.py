@@ -889,6 +889,7 @@ class AdamWList:
         self.device = self.tensors[0].param.get_device()
         if any(t.param.get_device() != self.device for t in self.tensors):
             raise ValueError("the tensors are on several devices")
+        self.eight_bit = any(t.state_bits == 8 for t in self.array)
 
     def set_grad(self, index: int, grad):
         t = self.tensors[index]
@@ -902,13 +903,17 @@ class AdamWList:
             raise
 
 
-def adamw(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, rounding="rtn", seed=0, grad_scale=None, stream=None):
-    """One AdamW step (number `step`, from 1) of an AdamWList, or of a sequence of AdamWTensor."""
+def adamw(tensors, lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, rounding=None, seed=0, grad_scale=None, stream=None):
+    """One AdamW step (number `step`, from 1) of an AdamWList, or of a sequence of AdamWTensor.  rounding: "rtn" or
+    "sr"; None: "sr" where any states have 8 bits, else "rtn".  To nearest, an 8-bit v does not follow its gradients (a
+    step moves it by less than half of what its format resolves), and steps grow as the bias correction fades."""
     import torch
     if not isinstance(tensors, AdamWList):
         tensors = AdamWList(tensors)
     if grad_scale is not None:
         _vector(grad_scale, 1, tensors.device, "grad_scale", torch.float32)
+    if rounding is None:
+        rounding = SR if tensors.eight_bit else RTN
     c = nvfp4_adamw_config(lr, beta1, beta2, eps, ROUNDINGS.get(rounding, rounding), step, seed, _ptr(grad_scale))
     _check(lib().nvfp4_adamw(tensors.array, len(tensors.array), ctypes.byref(c), _raw_stream(stream, tensors.device)),
            "nvfp4_adamw")
