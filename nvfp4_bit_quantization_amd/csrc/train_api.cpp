@@ -15,6 +15,9 @@ using namespace nvfp4;
 
 namespace {
 
+// a launch counts its threads in 32 bits, 256 to a workgroup
+constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;
+
 bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 bool dtype_ok(int32_t t) { return t == NVFP4_F32 || t == NVFP4_BF16; }
 size_t size_of(int32_t t) { return t == NVFP4_BF16 ? 2 : 4; }
@@ -72,11 +75,10 @@ int check_shape(const nvfp4_attention_shape *s) {
     return NVFP4_E_SHAPE;
   }
   if (!(s->scale > 0.0f) || !isfinite(s->scale)) return NVFP4_E_VALUE;
-  // a launch counts its threads in 32 bits, 256 to a workgroup; tiles are split
-  // into parts only where they are few
+  // tiles are split into parts only where they are few
   const int64_t q = longest(s, s->q_len, s->total_q), k = longest(s, s->k_len, s->total_k);
-  const int64_t limit = ((int64_t)1 << 24) - 1, tiles = (q > k ? q : k) / 128 + 1;
-  if (s->batch > limit / tiles / s->heads) return NVFP4_E_SHAPE;
+  const int64_t tiles = (q > k ? q : k) / 128 + 1;
+  if (s->batch > kMaxGroups / tiles / s->heads) return NVFP4_E_SHAPE;
   // and a key tile's steps over its heads' query tiles in 26 bits
   if ((q / 32 + 1) * (s->heads / s->kv_heads) >= (int64_t)1 << 26) return NVFP4_E_SHAPE;
   return NVFP4_OK;
@@ -309,8 +311,9 @@ int nvfp4_adamw(const nvfp4_adamw_tensor *tensors, int64_t n_tensors, const nvfp
   int extras = 0;
   for (int64_t i = 0; i <= n_tensors; ++i) {
     const bool more = i < n_tensors, extra = more && (tensors[i].m_scale || tensors[i].copy || tensors[i].amax);
-    // at most 2^22 workgroups a tensor: the running count stays in 32 bits
-    if (a.count && (!more || end > (1u << 30) ||
+    // a launch counts its threads in 32 bits; a tensor has at most 2^22 workgroups
+    const uint32_t groups = more ? (uint32_t)((tensors[i].n + kAdamChunk - 1) / kAdamChunk) : 0u;
+    if (a.count && (!more || end + groups > kMaxGroups ||
                     (a.count + 1) * sizeof(AdamTensor) + (extras + extra) * sizeof(AdamExtra) > kAdamBytes)) {
       if (launch_adamw(a, s) != hipSuccess) return NVFP4_E_HIP;
       a.count = extras = 0;
@@ -333,8 +336,7 @@ int nvfp4_adamw(const nvfp4_adamw_tensor *tensors, int64_t n_tensors, const nvfp
       d.flags |= AF_EXTRA | (uint32_t)extras << AF_EXTRA_SHIFT;
       memcpy(a.bytes + kAdamBytes - ++extras * sizeof e, &e, sizeof e);
     }
-    end += (uint32_t)((t.n + kAdamChunk - 1) / kAdamChunk);
-    d.end = end;
+    d.end = end += groups;
     memcpy(a.bytes + a.count++ * sizeof d, &d, sizeof d);
   }
   return finish(hipSuccess, s);

@@ -2,11 +2,13 @@
 refuse at the borders of their contracts."""
 import ctypes
 import os
+import shutil
+import subprocess
 
 import pytest
 
 import nvfp4_bit_quantization_amd as nv
-from test_train_abi_cpu import ALIGN, FAKE, LD, NULL, SHAPE, UNSUPPORTED, VALUE, WORKSPACE, _adam, _config, _heads, _shape
+from test_train_abi_cpu import ALIGN, CSRC, FAKE, LD, NULL, ROOT, SHAPE, UNSUPPORTED, VALUE, WORKSPACE, _adam, _config, _heads, _shape
 
 
 @pytest.fixture(scope="module")
@@ -22,3 +24,65 @@ def test_adamw_eps_is_normal(L, eps, status):
     """The reciprocal instruction takes subnormal numbers for zero."""
     arr = (nv.nvfp4_adamw_tensor * 1)(_adam(n=0))  # nothing to launch
     assert L.nvfp4_adamw(arr, 1, ctypes.byref(_config(eps=eps)), None) == status
+
+
+# the entry points' host code with launches that are only counted
+DRIVER = r"""
+#include <stdio.h>
+#include <string.h>
+#include <hip/hip_runtime.h>
+#include "nvfp4.h"
+#include "train_kernels.hpp"
+namespace nvfp4 {
+int launched = 0;
+hipError_t launch_layernorm(const nvfp4_layernorm_args &, hipStream_t) { return hipSuccess; }
+int64_t layernorm_backward_parts(int64_t, int64_t) { return 1; }
+hipError_t launch_layernorm_backward(const nvfp4_layernorm_backward_args &, float *, hipStream_t) { return hipSuccess; }
+int64_t adam_groups = 0, adam_most = 0;
+hipError_t launch_adamw(const AdamArgs &a, hipStream_t) {
+  const int64_t n = a.tensor(a.count - 1).end;
+  ++launched, adam_groups += n;
+  if (n > adam_most) adam_most = n;
+  return hipSuccess;
+}
+int attention_q_parts(const AttnArgs &) { return 1; }
+int attention_k_parts(const AttnArgs &) { return 1; }
+hipError_t launch_attention(const AttnArgs &, hipStream_t) { ++launched; return hipSuccess; }
+hipError_t launch_attention_backward(const AttnArgs &, hipStream_t) { ++launched; return hipSuccess; }
+}
+#define FAKE ((void *)0x10000)
+#define CHECK(c) do { if (!(c)) { printf("check failed line %d: %s\n", __LINE__, #c); return 1; } } while (0)
+int main() {
+  // a launch of 256 threads to a workgroup counts its threads in 32 bits
+  static nvfp4_adamw_tensor t[200];
+  memset(t, 0, sizeof t);
+  for (int i = 0; i < 200; ++i) {
+    t[i].param = t[i].m = t[i].v = FAKE, t[i].grad = FAKE, t[i].state_bits = 32;
+    t[i].n = i % 3 ? ((int64_t)1 << 34) - i * 5000 : i * 1000;
+  }
+  nvfp4_adamw_config c;
+  memset(&c, 0, sizeof c);
+  c.beta1 = 0.9, c.beta2 = 0.99, c.eps = 1e-8f, c.step = 1;
+  CHECK(nvfp4_adamw(t, 200, &c, nullptr) == NVFP4_OK);
+  int64_t groups = 0;
+  for (int i = 0; i < 200; ++i) groups += (t[i].n + nvfp4::kAdamChunk - 1) / nvfp4::kAdamChunk;
+  CHECK(nvfp4::adam_groups == groups);
+  CHECK(nvfp4::adam_most < (int64_t)1 << 24);
+  printf("ok\n");
+  return 0;
+}
+"""
+
+
+def test_entry_points_without_a_gpu(tmp_path):
+    hipcc = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
+    if not os.path.exists(hipcc):
+        pytest.skip("hipcc not available")
+    drv, exe = tmp_path / "drv.cpp", tmp_path / "contract"
+    drv.write_text(DRIVER)
+    r = subprocess.run([hipcc, "-x", "hip", "--offload-arch=gfx950", "-std=c++17", "-O1", "-I", os.path.join(ROOT, "include"),
+                        "-I", CSRC, "-o", str(exe), os.path.join(CSRC, "train_api.cpp"), str(drv)],
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-4000:]
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout + r.stderr[-4000:]
