@@ -438,7 +438,7 @@ typedef struct {
   const int32_t *cu_k; /* as cu_q, for keys and values; both or neither */
   int64_t total_q;     /* packed: tokens of q; else batch * q_len */
   int64_t total_k;     /* packed: tokens of k; else batch * k_len */
-  float scale;         /* > 0 */
+  float scale;         /* 2^-120 .. 2^120 */
 } nvfp4_attention_shape;
 
 /*

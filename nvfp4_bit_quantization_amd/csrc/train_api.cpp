@@ -74,7 +74,8 @@ int check_shape(const nvfp4_attention_shape *s) {
   } else if (s->total_q != s->batch * s->q_len || s->total_k != s->batch * s->k_len) {
     return NVFP4_E_SHAPE;
   }
-  if (!(s->scale > 0.0f) || !isfinite(s->scale)) return NVFP4_E_VALUE;
+  // the gradient forms -lse / scale, all passes scale * log2(e)
+  if (!(s->scale >= 0x1p-120f && s->scale <= 0x1p120f)) return NVFP4_E_VALUE;
   // tiles are split into parts only where they are few
   const int64_t q = longest(s, s->q_len, s->total_q), k = longest(s, s->k_len, s->total_k);
   const int64_t tiles = (q > k ? q : k) / 128 + 1;

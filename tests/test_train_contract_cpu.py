@@ -26,6 +26,17 @@ def test_adamw_eps_is_normal(L, eps, status):
     assert L.nvfp4_adamw(arr, 1, ctypes.byref(_config(eps=eps)), None) == status
 
 
+@pytest.mark.parametrize("scale,good", [(1e-45, False), (1.2e-38, False), (7.5e-37, False), (2.0 ** -120, True), (1.0, True),
+                                        (2.0 ** 120, True), (1.4e36, False), (3e38, False)])
+def test_attention_scale_is_representable(L, scale, good):
+    """-lse / scale and scale * log2(e) have to be finite."""
+    s, h = _shape(scale=scale), ctypes.byref(_heads())
+    assert (L.nvfp4_attention_backward_workspace_bytes(ctypes.byref(s)) > 0) == good
+    if not good:
+        assert L.nvfp4_attention(ctypes.byref(s), h, h, h, h, FAKE, None, 0, None) == VALUE
+        assert L.nvfp4_attention_backward(ctypes.byref(s), h, h, h, h, FAKE, h, h, h, h, FAKE, 1 << 30, None) == VALUE
+
+
 # the entry points' host code with launches that are only counted
 DRIVER = r"""
 #include <stdio.h>
