@@ -427,8 +427,8 @@ typedef struct {
 /* What an attention call works on. */
 typedef struct {
   int64_t batch;       /* sequences, >= 1 */
-  int64_t q_len;       /* queries of each sequence (packed: the most that any has), 1 .. 2^30 */
-  int64_t k_len;       /* keys of each sequence (packed: the most that any has), 1 .. 2^30 */
+  int64_t q_len;       /* queries of each sequence (packed: the most that any has, may be 0), up to 2^30 */
+  int64_t k_len;       /* keys of each sequence (packed: the most that any has, may be 0), up to 2^30 */
   int32_t heads;       /* query heads, a multiple of kv_heads: head h reads key head h / (heads / kv_heads) */
   int32_t kv_heads;
   int32_t head_dim;    /* a multiple of 8, 8 .. 128 */
@@ -446,8 +446,9 @@ typedef struct {
  * lse[head][token] = log sum_j exp(scale * q k_j) (natural logarithm), which
  * the gradient reads; token counts over all sequences (packed: the token
  * itself; else batch index * q_len + query).  A query that sees no key has
- * o = 0 and lse = -inf.  Sequences may be empty in the packed form; tokens
- * that belong to no sequence are not written.  cu values outside
+ * o = 0 and lse = -inf.  Sequences may be empty in the packed form, and a
+ * tensor of no tokens may have no data; tokens that belong to no sequence are
+ * not written.  cu values outside
  * [0, total] or descending are read as clamped to it, so that no
  * access leaves the tensors.
  *   q, o: heads heads; k, v: kv_heads.  data 16-byte aligned, strides

@@ -856,10 +856,11 @@ hipError_t forward(const AttnArgs &a, unsigned rows, hipStream_t s) {
 }
 template <int D>
 hipError_t backward(const AttnArgs &a, unsigned rows, unsigned keys, hipStream_t s) {
-  attention_dq_kernel<D><<<rows * (unsigned)a.q_parts, kThreads, 0, s>>>(a);
-  attention_dkv_kernel<D><<<keys * (unsigned)a.k_parts, kThreads, 0, s>>>(a);
-  if (a.q_parts > 1) attention_join_kernel<D, kJoinQ><<<join_groups(a, a.heads, a.q_len), kThreads, 0, s>>>(a);
-  if (a.k_parts > 1)
+  // packed sequences may have no queries, or no keys: nothing of theirs to write
+  if (rows) attention_dq_kernel<D><<<rows * (unsigned)a.q_parts, kThreads, 0, s>>>(a);
+  if (keys) attention_dkv_kernel<D><<<keys * (unsigned)a.k_parts, kThreads, 0, s>>>(a);
+  if (rows && a.q_parts > 1) attention_join_kernel<D, kJoinQ><<<join_groups(a, a.heads, a.q_len), kThreads, 0, s>>>(a);
+  if (keys && a.k_parts > 1)
     attention_join_kernel<D, kJoinKV><<<dim3(join_groups(a, a.kv_heads, a.k_len), 2), kThreads, 0, s>>>(a);
   return hipGetLastError();
 }

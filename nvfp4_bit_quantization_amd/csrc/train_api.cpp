@@ -37,9 +37,11 @@ int norm_shape(int64_t rows, int64_t cols) {
   return rows <= 0 || rows >= ((int64_t)1 << 31) || cols <= 0 || cols > kNormMaxCols ? NVFP4_E_SHAPE : NVFP4_OK;
 }
 
-// one bf16 tensor of an attention call; outputs must not overlap themselves
-int check_heads(const nvfp4_heads *t, const nvfp4_attention_shape *s, int32_t heads, bool output) {
-  if (!t || !t->data) return NVFP4_E_NULL;
+// one bf16 tensor of an attention call, of queries or of keys (an empty one may
+// have no data); outputs must not overlap themselves
+int check_heads(const nvfp4_heads *t, const nvfp4_attention_shape *s, bool queries, bool output) {
+  const int32_t heads = queries ? s->heads : s->kv_heads;
+  if (!t || (!t->data && (queries ? s->total_q : s->total_k))) return NVFP4_E_NULL;
   const bool batched = !s->cu_q && s->batch > 1;
   if (t->token_stride < 0 || t->token_stride >= ((int64_t)1 << 23) || t->head_stride < 0 ||
       (batched && t->batch_stride < 0))
@@ -52,15 +54,15 @@ int check_heads(const nvfp4_heads *t, const nvfp4_attention_shape *s, int32_t he
   return NVFP4_OK;
 }
 
-// what a sequence's length cannot exceed (at least 1)
+// what a sequence's length cannot exceed (0 only with packed sequences)
 int64_t longest(const nvfp4_attention_shape *s, int64_t len, int64_t total) {
-  return !s->cu_q || len < total ? len : total > 1 ? total : 1;
+  return !s->cu_q || len < total ? len : total;
 }
 
 int check_shape(const nvfp4_attention_shape *s) {
   if (!s) return NVFP4_E_NULL;
-  const int64_t most = (int64_t)1 << 30;
-  if (s->batch < 1 || s->batch > most || s->q_len < 1 || s->q_len > most || s->k_len < 1 || s->k_len > most ||
+  const int64_t most = (int64_t)1 << 30, least = s->cu_q ? 0 : 1;
+  if (s->batch < 1 || s->batch > most || s->q_len < least || s->q_len > most || s->k_len < least || s->k_len > most ||
       s->heads < 1 || s->heads > 65535 || s->kv_heads < 1 || s->heads % s->kv_heads)
     return NVFP4_E_SHAPE;
   if (s->head_dim < 8 || s->head_dim > 128 || s->head_dim % 8) return NVFP4_E_UNSUPPORTED;
@@ -224,12 +226,12 @@ int nvfp4_attention(const nvfp4_attention_shape *shape, const nvfp4_heads *q, co
                     const nvfp4_heads *v, const nvfp4_heads *o, float *lse, void *workspace, size_t workspace_bytes,
                     void *stream) {
   if (const int st = check_shape(shape)) return st;
-  if (!lse) return NVFP4_E_NULL;
+  if (!lse && shape->total_q) return NVFP4_E_NULL;
   if (!aligned(lse, 4)) return NVFP4_E_ALIGN;
-  int st = check_heads(q, shape, shape->heads, false);
-  if (!st) st = check_heads(k, shape, shape->kv_heads, false);
-  if (!st) st = check_heads(v, shape, shape->kv_heads, false);
-  if (!st) st = check_heads(o, shape, shape->heads, true);
+  int st = check_heads(q, shape, true, false);
+  if (!st) st = check_heads(k, shape, false, false);
+  if (!st) st = check_heads(v, shape, false, false);
+  if (!st) st = check_heads(o, shape, true, true);
   if (st) return st;
   const size_t need = nvfp4_attention_workspace_bytes(shape);
   if (need && (!workspace || workspace_bytes < need)) return NVFP4_E_WORKSPACE;
@@ -241,6 +243,7 @@ int nvfp4_attention(const nvfp4_attention_shape *shape, const nvfp4_heads *q, co
   a.o = heads_of(o);
   a.lse = lse;
   carve_forward(a, workspace);
+  if (a.q_len == 0) return NVFP4_OK;  // nothing is written
   hipStream_t s = (hipStream_t)stream;
   return finish(launch_attention(a, s), s);
 }
@@ -256,12 +259,12 @@ int nvfp4_attention_backward(const nvfp4_attention_shape *shape, const nvfp4_hea
                              const nvfp4_heads *dq, const nvfp4_heads *dk, const nvfp4_heads *dv, void *workspace,
                              size_t workspace_bytes, void *stream) {
   if (const int st = check_shape(shape)) return st;
-  if (!lse) return NVFP4_E_NULL;
+  if (!lse && shape->total_q) return NVFP4_E_NULL;
   if (!aligned(lse, 4)) return NVFP4_E_ALIGN;
   const nvfp4_heads *by_q[4] = {q, o, d_o, dq}, *by_k[4] = {k, v, dk, dv};
   for (int i = 0; i < 4; ++i) {
-    if (const int st = check_heads(by_q[i], shape, shape->heads, i == 3)) return st;
-    if (const int st = check_heads(by_k[i], shape, shape->kv_heads, i >= 2)) return st;
+    if (const int st = check_heads(by_q[i], shape, true, i == 3)) return st;
+    if (const int st = check_heads(by_k[i], shape, false, i >= 2)) return st;
   }
   if (!workspace || workspace_bytes < nvfp4_attention_backward_workspace_bytes(shape)) return NVFP4_E_WORKSPACE;
   if (!aligned(workspace, 16)) return NVFP4_E_ALIGN;
@@ -276,6 +279,7 @@ int nvfp4_attention_backward(const nvfp4_attention_shape *shape, const nvfp4_hea
   a.dv = heads_of(dv);
   a.lse = const_cast<float *>(lse);
   carve_backward(a, workspace);
+  if (a.q_len == 0 && a.k_len == 0) return NVFP4_OK;  // nothing is written
   hipStream_t s = (hipStream_t)stream;
   return finish(launch_attention_backward(a, s), s);
 }

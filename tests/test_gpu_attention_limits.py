@@ -29,3 +29,34 @@ def test_scale_borders(nv, power, ones):
     do = _rand(g, 1, 200, 4, 64, scale=1e-3)
     o, lse, dq, dk, dv = _run(nv, q, k, v, do, scale=2.0 ** power)
     _check_sequence(q[0], k[0], v[0], do[0], o[0], lse, dq[0], dk[0], dv[0], _see(200, 200, True, 0), 2.0 ** power, "scale")
+
+
+@pytest.mark.parametrize("most", [0, 5])
+@pytest.mark.parametrize("nq,nk", [(0, 300), (300, 0), (0, 0)])
+def test_no_tokens(nv, nq, nk, most):
+    """Packed tensors without any tokens, under a maximum of 0 or above: queries without keys give 0 and -inf and have
+    no gradient, keys without queries neither."""
+    say("attention without tokens", nq, nk, most)
+    g = torch.Generator(device="cuda").manual_seed(nq + nk)
+    q, k, v = _rand(g, nq, 4, 64), _rand(g, nk, 2, 64), _rand(g, nk, 2, 64)
+    cu = [torch.tensor([0, n // 3, n // 3, n], dtype=torch.int32, device="cuda") for n in (nq, nk)]
+    o, lse, dq, dk, dv = _run(nv, q, k, v, torch.ones_like(q), cu_q=cu[0], cu_k=cu[1], max_q=nq or most, max_k=nk or most)
+    assert o.shape == dq.shape == q.shape and dk.shape == dv.shape == k.shape and lse.shape == (4, nq)
+    assert all((t == 0).all() for t in (o, dq, dk, dv)) and (lse == -float("inf")).all()
+
+
+def test_maximum_of_zero_cuts_to_nothing(nv):
+    """Sequences are cut to the stated maximum: with one of 0 nothing is read or written."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (_rand(g, 40, 2, 64) for _ in range(3))
+    cu = torch.tensor([0, 10, 40], dtype=torch.int32, device="cuda")
+    for max_q, max_k in ((0, 40), (40, 0), (0, 0)):
+        opts = dict(cu_q=cu, cu_k=cu, max_q=max_q, max_k=max_k)
+        o, lse = torch.full_like(q, 7.0), torch.full((2, 40), 7.0, device="cuda")
+        d = [torch.full_like(q, 7.0) for _ in range(3)]
+        ws = nv.new_attention_workspace(q, k, v, **opts)
+        nv.nvfp4_attention(q, k, v, o, lse, workspace=ws, **opts)
+        nv.nvfp4_attention_backward(q, q, k, v, o, lse, *d, ws, **opts)
+        assert (o == (0 if max_q else 7)).all() and (d[0] == (0 if max_q else 7)).all()
+        assert (lse == (-float("inf") if max_q else 7)).all()
+        assert all((t == (0 if max_k else 7)).all() for t in d[1:])

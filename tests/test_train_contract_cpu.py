@@ -79,6 +79,37 @@ int main() {
   for (int i = 0; i < 200; ++i) groups += (t[i].n + nvfp4::kAdamChunk - 1) / nvfp4::kAdamChunk;
   CHECK(nvfp4::adam_groups == groups);
   CHECK(nvfp4::adam_most < (int64_t)1 << 24);
+
+  // packed sequences: no tokens at all need no buffers, and launch nothing
+  nvfp4_attention_shape s;
+  memset(&s, 0, sizeof s);
+  s.batch = 2, s.heads = 4, s.kv_heads = 2, s.head_dim = 64, s.causal = 1, s.scale = 0.125f;
+  s.cu_q = s.cu_k = (const int32_t *)FAKE;
+  const nvfp4_heads none = {nullptr, 0, 256, 64}, some = {FAKE, 0, 256, 64}, out = {(void *)0x20000, 0, 256, 64};
+  const nvfp4_heads dq = {(void *)0x30000, 0, 256, 64}, dk = {(void *)0x40000, 0, 256, 64}, dv = {(void *)0x50000, 0, 256, 64};
+  for (int64_t most = 0; most <= 7; most += 7) {
+    s.q_len = most, s.k_len = 9, s.total_q = 0, s.total_k = 20;
+    nvfp4::launched = 0;
+    CHECK(nvfp4_attention_workspace_bytes(&s) == 0);
+    CHECK(nvfp4_attention(&s, &none, &some, &some, &none, nullptr, nullptr, 0, nullptr) == NVFP4_OK);
+    CHECK(nvfp4::launched == 0);
+    CHECK(nvfp4_attention_backward(&s, &none, &some, &some, &none, nullptr, &none, &none, &dk, &dv, FAKE, 1 << 20, nullptr) == NVFP4_OK);
+    CHECK(nvfp4::launched == 1);
+    CHECK(nvfp4_attention(&s, &none, &none, &some, &none, nullptr, nullptr, 0, nullptr) == NVFP4_E_NULL);
+    CHECK(nvfp4_attention_backward(&s, &none, &some, &some, &none, nullptr, &none, &none, &none, &dv, FAKE, 1 << 20, nullptr) == NVFP4_E_NULL);
+    s.q_len = 9, s.k_len = most, s.total_q = 20, s.total_k = 0;
+    nvfp4::launched = 0;
+    CHECK(nvfp4_attention(&s, &some, &none, &none, &out, (float *)FAKE, nullptr, 0, nullptr) == NVFP4_OK);
+    CHECK(nvfp4_attention_backward(&s, &some, &none, &none, &out, (float *)FAKE, &out, &dq, &none, &none, FAKE, 1 << 20, nullptr) == NVFP4_OK);
+    CHECK(nvfp4::launched == 2);
+    CHECK(nvfp4_attention(&s, &some, &none, &none, &out, nullptr, nullptr, 0, nullptr) == NVFP4_E_NULL);
+    CHECK(nvfp4_attention(&s, &some, &none, &none, &none, (float *)FAKE, nullptr, 0, nullptr) == NVFP4_E_NULL);
+    s.q_len = s.k_len = most, s.total_q = s.total_k = 0;
+    CHECK(nvfp4_attention_backward(&s, &none, &none, &none, &none, nullptr, &none, &none, &none, &none, FAKE, 1 << 20, nullptr) == NVFP4_OK);
+    CHECK(nvfp4::launched == 2);
+  }
+  s.cu_q = s.cu_k = nullptr;
+  CHECK(nvfp4_attention(&s, &none, &none, &none, &none, nullptr, nullptr, 0, nullptr) == NVFP4_E_SHAPE);
   printf("ok\n");
   return 0;
 }
