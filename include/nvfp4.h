@@ -57,7 +57,7 @@ extern "C" {
 #define NVFP4_E_SHAPE (-2)       /* a size <= 0, not a multiple of 16, or inconsistent */
 #define NVFP4_E_LD (-3)          /* a leading dimension smaller than the row length */
 #define NVFP4_E_ALIGN (-4)       /* x, codes or y not 16-byte aligned, or ld not a multiple of 8 */
-#define NVFP4_E_UNSUPPORTED (-5) /* unknown enum, RHT with a 2D layout, bad n_outs, K mismatch */
+#define NVFP4_E_UNSUPPORTED (-5) /* unknown enum, RHT with a 2D layout, bad n_outs, K mismatch, outputs in the place of what is still read */
 #define NVFP4_E_WORKSPACE (-6)   /* workspace NULL or smaller than nvfp4_workspace_bytes() */
 #define NVFP4_E_HIP (-7)         /* a HIP launch failed */
 #define NVFP4_E_VALUE (-8)       /* a scalar argument out of its range (training operators) */
@@ -456,6 +456,8 @@ typedef struct {
  *   workspace  nvfp4_attention_workspace_bytes(shape) bytes of device scratch,
  *              16-byte aligned, not initialised: 0 (workspace may be NULL) but
  *              where few queries meet many keys and the keys are split.
+ * o may be q, with its strides; otherwise outputs overlap neither each other nor
+ * what is read (NVFP4_E_UNSUPPORTED where they begin at the same address).
  * Products on the bf16 MFMA with binary32 accumulation; the softmax is
  * binary32, its probabilities are rounded to bf16 for the product with v.
  * One kernel, or two where the keys are split.
@@ -474,6 +476,9 @@ size_t nvfp4_attention_workspace_bytes(const nvfp4_attention_shape *shape);
  * every token of a sequence (zero where nothing is in sight).
  *   workspace  nvfp4_attention_backward_workspace_bytes(shape) bytes of device
  *              scratch, 16-byte aligned, not initialised.
+ * dq may be o, dk and dv may be k and v in either order, each with its strides;
+ * otherwise outputs overlap neither each other nor what is read
+ * (NVFP4_E_UNSUPPORTED where they begin at the same address).
  * p and ds are rounded to bf16 for their products.  Two to four kernels.
  */
 int nvfp4_attention_backward(const nvfp4_attention_shape *shape, const nvfp4_heads *q, const nvfp4_heads *k,

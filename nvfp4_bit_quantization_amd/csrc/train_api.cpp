@@ -54,6 +54,29 @@ int check_heads(const nvfp4_heads *t, const nvfp4_attention_shape *s, bool queri
   return NVFP4_OK;
 }
 
+// Whether output a may be written beside tensor b: they begin apart, or, where
+// b's elements are read before their places are written, stand alike.  (Without
+// queries or keys nothing meets.)
+bool apart(const nvfp4_heads *a, const nvfp4_heads *b) { return a->data != b->data; }
+bool apart_or_alike(const nvfp4_heads *a, const nvfp4_heads *b, const nvfp4_attention_shape *s) {
+  return apart(a, b) || (a->token_stride == b->token_stride && a->head_stride == b->head_stride &&
+                         (s->cu_q || s->batch == 1 || a->batch_stride == b->batch_stride));
+}
+
+// The first pass alone reads o, each row before it writes that of dq; the second
+// reads q and d_o anywhere, and a workgroup its keys and values before it writes theirs.
+bool gradients_apart(const nvfp4_attention_shape &s, const nvfp4_heads *q, const nvfp4_heads *k, const nvfp4_heads *v,
+                     const nvfp4_heads *o, const nvfp4_heads *d_o, const nvfp4_heads *dq, const nvfp4_heads *dk,
+                     const nvfp4_heads *dv) {
+  for (const nvfp4_heads *t : {q, k, v, d_o, dk, dv})
+    if (!apart(dq, t)) return false;
+  for (const nvfp4_heads *t : {q, o, d_o})
+    if (!apart(dk, t) || !apart(dv, t)) return false;
+  for (const nvfp4_heads *t : {k, v})
+    if (!apart_or_alike(dk, t, &s) || !apart_or_alike(dv, t, &s)) return false;
+  return apart(dk, dv) && apart_or_alike(dq, o, &s);
+}
+
 // what a sequence's length cannot exceed (0 only with packed sequences)
 int64_t longest(const nvfp4_attention_shape *s, int64_t len, int64_t total) {
   return !s->cu_q || len < total ? len : total;
@@ -236,6 +259,9 @@ int nvfp4_attention(const nvfp4_attention_shape *shape, const nvfp4_heads *q, co
   const size_t need = nvfp4_attention_workspace_bytes(shape);
   if (need && (!workspace || workspace_bytes < need)) return NVFP4_E_WORKSPACE;
   if (need && !aligned(workspace, 16)) return NVFP4_E_ALIGN;
+  // a workgroup reads its queries before it writes their rows; any reads the keys
+  if (shape->total_q && shape->total_k && (!apart(o, k) || !apart(o, v) || !apart_or_alike(o, q, shape)))
+    return NVFP4_E_UNSUPPORTED;
   AttnArgs a = attn_args(shape);
   a.q = heads_of(q);
   a.k = heads_of(k);
@@ -268,6 +294,7 @@ int nvfp4_attention_backward(const nvfp4_attention_shape *shape, const nvfp4_hea
   }
   if (!workspace || workspace_bytes < nvfp4_attention_backward_workspace_bytes(shape)) return NVFP4_E_WORKSPACE;
   if (!aligned(workspace, 16)) return NVFP4_E_ALIGN;
+  if (shape->total_q && shape->total_k && !gradients_apart(*shape, q, k, v, o, d_o, dq, dk, dv)) return NVFP4_E_UNSUPPORTED;
   AttnArgs a = attn_args(shape);
   a.q = heads_of(q);
   a.k = heads_of(k);

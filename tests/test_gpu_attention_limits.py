@@ -60,3 +60,31 @@ def test_maximum_of_zero_cuts_to_nothing(nv):
         assert (o == (0 if max_q else 7)).all() and (d[0] == (0 if max_q else 7)).all()
         assert (lse == (-float("inf") if max_q else 7)).all()
         assert all((t == (0 if max_k else 7)).all() for t in d[1:])
+
+
+@pytest.mark.parametrize("nq,nk,causal", [(200, 200, True), (70, 1700, False), (1100, 90, False)])
+def test_in_place(nv, nq, nk, causal):
+    """o in the place of q, dq of o, dk and dv of k and v (and the other way round) give the bits that memory of their
+    own gives; with few queries and with few keys the sums are split."""
+    say("attention in place", nq, nk)
+    g = torch.Generator(device="cuda").manual_seed(nq)
+    q, k, v, do = (_rand(g, 1, n, 4, 64) for n in (nq, nk, nk, nq))
+    o, lse, dq, dk, dv = _run(nv, q, k, v, do, causal=causal)
+    ws = nv.new_attention_workspace(q, k, v, causal=causal)
+    t = q.clone()
+    nv.nvfp4_attention(t, k, v, t, torch.empty_like(lse), causal=causal, workspace=ws)
+    assert torch.equal(t, o)
+    for swap in (False, True):
+        a, b, c = o.clone(), k.clone(), v.clone()
+        nv.nvfp4_attention_backward(do, q, b, c, a, lse, a, *((c, b) if swap else (b, c)), ws, causal=causal)
+        assert torch.equal(a, dq) and torch.equal(c if swap else b, dk) and torch.equal(b if swap else c, dv)
+
+
+def test_outputs_in_place_of_inputs_still_read_are_refused(nv):
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q, k, v, do = (_rand(g, 1, 64, 2, 64) for _ in range(4))
+    o, lse = nv.attention(q, k, v)
+    ws = nv.new_attention_workspace(q, k, v)
+    for dq in (q, do):
+        with pytest.raises(nv.Nvfp4Error):
+            nv.nvfp4_attention_backward(do, q, k, v, o, lse, dq, torch.empty_like(k), torch.empty_like(v), ws)

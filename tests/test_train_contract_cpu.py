@@ -37,6 +37,45 @@ def test_attention_scale_is_representable(L, scale, good):
         assert L.nvfp4_attention_backward(ctypes.byref(s), h, h, h, h, FAKE, h, h, h, h, FAKE, 1 << 30, None) == VALUE
 
 
+def _distinct(**kw):
+    """Tensors of one shape (as many query as key heads), each of its own memory but for those named as another's."""
+    t = {n: _heads(data=FAKE * (i + 1)) for i, n in enumerate(("q", "k", "v", "o", "d_o", "dq", "dk", "dv"))}
+    for name, (other, change) in kw.items():
+        t[name] = _heads(**dict(dict(data=t[other].data), **change))
+    return {n: ctypes.byref(x) for n, x in t.items()}
+
+
+OUTPUTS = [("dq", "q"), ("dq", "k"), ("dq", "v"), ("dq", "d_o"), ("dk", "q"), ("dk", "o"), ("dk", "d_o"), ("dv", "q"),
+           ("dv", "o"), ("dv", "d_o"), ("dk", "dq"), ("dv", "dq"), ("dv", "dk")]
+IN_PLACE = [("dq", "o"), ("dk", "k"), ("dk", "v"), ("dv", "k"), ("dv", "v")]
+
+
+@pytest.mark.parametrize("output,other", OUTPUTS + [("o", "k"), ("o", "v")], ids=str)
+def test_attention_outputs_keep_off_what_is_still_read(L, output, other):
+    s = _shape(heads=2, kv_heads=2)
+    t = _distinct(**{output: (other, {})})
+    if output == "o":
+        assert L.nvfp4_attention(ctypes.byref(s), t["q"], t["k"], t["v"], t["o"], FAKE * 9, None, 0, None) == UNSUPPORTED
+        return
+    need = L.nvfp4_attention_backward_workspace_bytes(ctypes.byref(s))
+    order = [t[n] for n in ("q", "k", "v", "o")], [t[n] for n in ("d_o", "dq", "dk", "dv")]
+    assert L.nvfp4_attention_backward(ctypes.byref(s), *order[0], FAKE * 9, *order[1], FAKE * 10, need, None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("output,other", IN_PLACE + [("o", "q")], ids=str)
+def test_attention_in_place_outputs_have_the_strides(L, output, other):
+    """What may stand in another tensor's place does so element by element."""
+    s = _shape(heads=2, kv_heads=2)
+    for change in (dict(token_stride=264), dict(head_stride=72), dict(batch_stride=32 * 256)):
+        t = _distinct(**{output: (other, change)})
+        if output == "o":
+            assert L.nvfp4_attention(ctypes.byref(s), t["q"], t["k"], t["v"], t["o"], FAKE * 9, None, 0, None) == UNSUPPORTED
+            continue
+        need = L.nvfp4_attention_backward_workspace_bytes(ctypes.byref(s))
+        order = [t[n] for n in ("q", "k", "v", "o")], [t[n] for n in ("d_o", "dq", "dk", "dv")]
+        assert L.nvfp4_attention_backward(ctypes.byref(s), *order[0], FAKE * 9, *order[1], FAKE * 10, need, None) == UNSUPPORTED
+
+
 # the entry points' host code with launches that are only counted
 DRIVER = r"""
 #include <stdio.h>
