@@ -535,6 +535,12 @@ def _nbytes(t) -> int:
     return 0 if t is None else t.numel() * t.element_size()
 
 
+def _scratch(t, device):
+    """Checks a workspace, whose size is taken from its elements: each has to be memory of its own."""
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on device %d is wanted" % device)
+
+
 def _raw_stream(stream, device_index) -> int:
     if stream is None:
         import torch
@@ -666,8 +672,8 @@ def nvfp4_layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, dsum
     for t, what in ((dweight, "dweight"), (dbias, "dbias")):
         if t is not None:
             _vector(t, shape[1], device, what, torch.float32)
-    if workspace is not None and workspace.get_device() != device:
-        raise ValueError("workspace: a tensor on device %d is wanted" % device)
+    if workspace is not None:
+        _scratch(workspace, device)
     _layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, dsum, amax, workspace, shape, device, stream)
     return dx
 
@@ -683,8 +689,8 @@ def layernorm_backward(dy, x, weight, mean, rstd, dsum=None, amax=None, workspac
     dweight, dbias = _floats(2, shape[1], x.device).unbind()
     if workspace is None:
         workspace = _floats(1, lib().nvfp4_layernorm_backward_workspace_bytes(*shape) // 4, x.device)
-    elif workspace.get_device() != device:
-        raise ValueError("workspace: a tensor on device %d is wanted" % device)
+    else:
+        _scratch(workspace, device)
     _layernorm_backward(dy, x, weight, mean, rstd, dx, dweight, dbias, dsum, amax, workspace, shape, device, None)
     return dx, dweight, dbias
 
@@ -746,8 +752,8 @@ def nvfp4_attention(q, k, v, o, lse, causal=True, window=0, scale=None, cu_q=Non
     s, sq, sk, heads, tokens, device = _attention_inputs(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
     _as(o, sq, device, "o")
     _lse(lse, heads, tokens, device)
-    if workspace is not None and workspace.get_device() != device:
-        raise ValueError("workspace: a tensor on device %d is wanted" % device)
+    if workspace is not None:
+        _scratch(workspace, device)
     _check(lib().nvfp4_attention(s, _heads(q, sq), _heads(k, sk), _heads(v, sk), _heads(o, sq), lse.data_ptr(),
                                  _ptr(workspace), _nbytes(workspace), _raw_stream(stream, device)), "nvfp4_attention")
     return o
@@ -768,8 +774,8 @@ def attention(q, k, v, causal=True, window=0, scale=None, cu_q=None, cu_k=None, 
         need = L.nvfp4_attention_workspace_bytes(s)
         if need:
             workspace = _floats(1, need // 4, q.device)
-    elif workspace.get_device() != device:
-        raise ValueError("workspace: a tensor on device %d is wanted" % device)
+    else:
+        _scratch(workspace, device)
     _check(L.nvfp4_attention(s, _heads(q, sq), _heads(k, sk), _heads(v, sk), _heads(o, sq), lse.data_ptr(), _ptr(workspace),
                              _nbytes(workspace), _raw_stream(None, device)), "nvfp4_attention")
     return o, lse
@@ -788,8 +794,8 @@ def nvfp4_attention_backward(d_o, q, k, v, o, lse, dq, dk, dv, workspace, causal
     for t, shape, what in ((d_o, sq, "d_o"), (o, sq, "o"), (dq, sq, "dq"), (dk, sk, "dk"), (dv, sk, "dv")):
         _as(t, shape, device, what)
     _lse(lse, heads, tokens, device)
-    if workspace is not None and workspace.get_device() != device:
-        raise ValueError("workspace: a tensor on device %d is wanted" % device)
+    if workspace is not None:
+        _scratch(workspace, device)
     _attention_backward(s, d_o, q, k, v, o, lse, dq, dk, dv, workspace, sq, sk, _raw_stream(stream, device))
     return dq, dk, dv
 
@@ -818,8 +824,8 @@ def attention_backward(d_o, q, k, v, o, lse, causal=True, window=0, scale=None, 
         v, memory_format=dense)
     if workspace is None:
         workspace = _floats(1, lib().nvfp4_attention_backward_workspace_bytes(s) // 4, q.device)
-    elif workspace.get_device() != device:
-        raise ValueError("workspace: a tensor on device %d is wanted" % device)
+    else:
+        _scratch(workspace, device)
     _attention_backward(s, d_o, q, k, v, o, lse, dq, dk, dv, workspace, sq, sk, _raw_stream(None, device))
     return dq, dk, dv
 

@@ -88,3 +88,20 @@ def test_outputs_in_place_of_inputs_still_read_are_refused(nv):
     for dq in (q, do):
         with pytest.raises(nv.Nvfp4Error):
             nv.nvfp4_attention_backward(do, q, k, v, o, lse, dq, torch.empty_like(k), torch.empty_like(v), ws)
+
+
+def test_expanded_workspaces_are_refused(nv):
+    """Their size is not the memory that they have."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q, k, v = (_rand(g, 1, 64, 2, 64) for _ in range(3))
+    wide = torch.empty(1, device="cuda").expand(1 << 20)
+    o, lse = nv.attention(q, k, v)
+    x, w = q.view(64, 128), torch.ones(128, device="cuda")
+    _, mean, rstd, _ = nv.layernorm(x, w)
+    for call in (lambda: nv.attention(q, k, v, workspace=wide), lambda: nv.attention_backward(q, q, k, v, o, lse, workspace=wide),
+                 lambda: nv.nvfp4_attention(q, k, v, o, lse, workspace=wide),
+                 lambda: nv.nvfp4_attention_backward(q, q, k, v, o, lse, *(torch.empty_like(q) for _ in range(3)), wide),
+                 lambda: nv.layernorm_backward(x, x, w, mean, rstd, workspace=wide),
+                 lambda: nv.nvfp4_layernorm_backward(x, x, w, mean, rstd, torch.empty_like(x), w.clone(), w.clone(), workspace=wide)):
+        with pytest.raises(ValueError):
+            call()

@@ -76,6 +76,15 @@ def test_attention_in_place_outputs_have_the_strides(L, output, other):
         assert L.nvfp4_attention_backward(ctypes.byref(s), *order[0], FAKE * 9, *order[1], FAKE * 10, need, None) == UNSUPPORTED
 
 
+def test_workspaces_are_memory():
+    """An expanded tensor counts more elements than it has."""
+    torch = pytest.importorskip("torch")
+    nv._scratch(torch.zeros(64), -1)
+    for bad, device in ((torch.zeros(1).expand(64), -1), (torch.zeros(8, 8).t(), -1), (torch.zeros(64), 0)):
+        with pytest.raises(ValueError):
+            nv._scratch(bad, device)
+
+
 # the entry points' host code with launches that are only counted
 DRIVER = r"""
 #include <stdio.h>
