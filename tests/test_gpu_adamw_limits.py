@@ -75,3 +75,28 @@ def test_default_rounding_of_32_bit_states_is_to_nearest(nv):
     for q, kw in zip(p, (dict(), dict(rounding="rtn"))):
         nv.adamw([nv.adamw_tensor(q, grad)], lr=2.0 ** -10, step=1, **kw)
     assert torch.equal(p[0], p[1])
+
+
+@pytest.mark.parametrize("rounding", ["rtn", "sr"])
+def test_conversion_is_the_rule(nv, rounding):
+    """8-bit states hold exactly the neighbour that their value and uniform give: with beta1 = 0 and zero states m is the
+    gradient, here values of every binade of E4M3 below a maximum that fixes the block's scale."""
+    from test_gpu_adamw import e4m3_parts, uniforms
+    n, seed = 1 << 20, 0x9876543210
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.exp2(torch.rand(n, generator=gen, device="cuda") * 21 - 12) * torch.sign(
+        torch.rand(n, generator=gen, device="cuda") - 0.5)
+    x[1::5] = torch.round(x[1::5] * 512) / 512          # ties and exact values
+    x = x.clamp(-448, 448)
+    x[::32] = 448
+    t = nv.adamw_tensor(torch.zeros(n, device="cuda"), x, state_bits=8)
+    nv.adamw([t], lr=0.0, beta1=0.0, step=3, rounding=rounding, seed=seed)
+    assert (t.m_scale == 127).all()
+    y = x.abs().double().cpu().numpy()
+    quantum = 2.0 ** (np.maximum(np.floor(np.log2(np.maximum(y, 2.0 ** -20))), -6) - 3)
+    place = y / quantum
+    want = np.floor(place + uniforms(n, 0, 0, 3, seed)) if rounding == "sr" else np.rint(place)
+    codes = t.m.cpu().numpy()
+    got, _ = e4m3_parts(codes)
+    assert np.array_equal(got, want * quantum)
+    assert ((codes >= 128) == (x.cpu().numpy() < 0)).all()
