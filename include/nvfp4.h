@@ -380,8 +380,8 @@ typedef struct {
  * All arithmetic in binary32; y is rounded once.  *amax becomes
  * max(*amax, max |y|) over the stored y (an atomic maximum: the caller
  * initialises it), which is what NVFP4_AMAX_GIVEN asks of a quantisation of y
- * without the RHT.  y may be x or residual, sum the other one or, with y apart,
- * either, each with its row stride and element type.
+ * without the RHT.  y may be x or residual and sum too, but not the same one; its
+ * rows are then as far apart (else NVFP4_E_UNSUPPORTED).
  * rows < 2^31, cols <= 32768.  One kernel.  Pointers need their elements'
  * alignment; rows that begin on 16 bytes are quickest.
  */
@@ -411,8 +411,8 @@ typedef struct {
  *   workspace  device scratch of nvfp4_layernorm_backward_workspace_bytes(rows,
  *              cols) bytes, 16-byte aligned (not needed when dweight and dbias
  *              are NULL): per-workgroup partial sums, added in a fixed order.
- * dx may be dy, x or dsum, with its row stride and element type.  One kernel, and
- * a second one for dweight and dbias; above 16384 columns a third.
+ * dx may be dy, x or dsum, with its rows as far apart (else NVFP4_E_UNSUPPORTED).
+ * One kernel, and a second one for dweight and dbias; above 16384 columns a third.
  */
 int nvfp4_layernorm_backward(const nvfp4_layernorm_backward_args *args, void *workspace, size_t workspace_bytes,
                              void *stream);

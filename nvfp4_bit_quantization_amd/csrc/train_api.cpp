@@ -37,6 +37,12 @@ int norm_shape(int64_t rows, int64_t cols) {
   return rows <= 0 || rows >= ((int64_t)1 << 31) || cols <= 0 || cols > kNormMaxCols ? NVFP4_E_SHAPE : NVFP4_OK;
 }
 
+// Whether the rows of output a may be written where those of b are read, each
+// only after all of it was read: they begin apart, or are as far apart.
+bool rows_fit(const void *a, int64_t ld_a, int32_t type_a, const void *b, int64_t ld_b, int32_t type_b, int64_t rows) {
+  return !a || a != b || rows == 1 || ld_a * (int64_t)size_of(type_a) == ld_b * (int64_t)size_of(type_b);
+}
+
 // one bf16 tensor of an attention call, of queries or of keys (an empty one may
 // have no data); outputs must not overlap themselves
 int check_heads(const nvfp4_heads *t, const nvfp4_attention_shape *s, bool queries, bool output) {
@@ -207,6 +213,12 @@ int nvfp4_layernorm(const nvfp4_layernorm_args *a, void *stream) {
       !aligned(a->mean, 4) || !aligned(a->rstd, 4) || (a->amax && !aligned(a->amax, 4)))
     return NVFP4_E_ALIGN;
   if (!(a->eps >= 0.0f) || !isfinite(a->eps)) return NVFP4_E_VALUE;
+  const int32_t xt = a->x_dtype;
+  if (a->y == a->sum || !rows_fit(a->y, a->ld_y, a->y_dtype, a->x, a->ld_x, xt, a->rows) ||
+      !rows_fit(a->y, a->ld_y, a->y_dtype, a->residual, a->ld_residual, xt, a->rows) ||
+      !rows_fit(a->sum, a->ld_sum, xt, a->x, a->ld_x, xt, a->rows) ||
+      !rows_fit(a->sum, a->ld_sum, xt, a->residual, a->ld_residual, xt, a->rows))
+    return NVFP4_E_UNSUPPORTED;
   hipStream_t s = (hipStream_t)stream;
   return finish(launch_layernorm(*a, s), s);
 }
@@ -235,6 +247,11 @@ int nvfp4_layernorm_backward(const nvfp4_layernorm_backward_args *a, void *works
       return NVFP4_E_WORKSPACE;
     if (!aligned(workspace, 16)) return NVFP4_E_ALIGN;
   }
+  const int32_t xt = a->x_dtype;
+  if (!rows_fit(a->dx, a->ld_dx, xt, a->dy, a->ld_dy, a->y_dtype, a->rows) ||
+      !rows_fit(a->dx, a->ld_dx, xt, a->x, a->ld_x, xt, a->rows) ||
+      !rows_fit(a->dx, a->ld_dx, xt, a->dsum, a->ld_dsum, xt, a->rows))
+    return NVFP4_E_UNSUPPORTED;
   hipStream_t s = (hipStream_t)stream;
   return finish(launch_layernorm_backward(*a, sums ? (float *)workspace : nullptr, s), s);
 }

@@ -8,7 +8,7 @@ import subprocess
 import pytest
 
 import nvfp4_bit_quantization_amd as nv
-from test_train_abi_cpu import ALIGN, CSRC, FAKE, LD, NULL, ROOT, SHAPE, UNSUPPORTED, VALUE, WORKSPACE, _adam, _config, _heads, _shape
+from test_train_abi_cpu import ALIGN, CSRC, FAKE, LD, NULL, ROOT, SHAPE, UNSUPPORTED, VALUE, WORKSPACE, _adam, _config, _heads, _norm, _norm_grad, _shape
 
 
 @pytest.fixture(scope="module")
@@ -83,6 +83,23 @@ def test_workspaces_are_memory():
     for bad, device in ((torch.zeros(1).expand(64), -1), (torch.zeros(8, 8).t(), -1), (torch.zeros(64), 0)):
         with pytest.raises(ValueError):
             nv._scratch(bad, device)
+
+
+@pytest.mark.parametrize("change", [
+    dict(sum=FAKE * 2, y=FAKE * 2), dict(y=FAKE * 3, ld_y=72), dict(y=FAKE * 4, ld_y=72), dict(y=FAKE * 3, y_dtype=0),
+    dict(sum=FAKE * 3, ld_sum=72), dict(sum=FAKE * 4, ld_sum=72)], ids=str)
+def test_layernorm_outputs_in_place(L, change):
+    """The two outputs stand apart, and what stands in an input's place has its rows as far apart, in bytes."""
+    a = dict(x=FAKE * 3, residual=FAKE * 4, y=FAKE * 5, sum=FAKE * 6, ld_residual=64, ld_sum=64)
+    assert L.nvfp4_layernorm(ctypes.byref(_norm(**dict(a, **change))), None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("change", [dict(dx=FAKE * 2, ld_dx=72), dict(dx=FAKE * 3, ld_dx=72), dict(dx=FAKE * 4, ld_dx=72),
+                                    dict(dx=FAKE * 2, y_dtype=0)], ids=str)
+def test_layernorm_backward_in_place(L, change):
+    a = dict(dy=FAKE * 2, x=FAKE * 3, dsum=FAKE * 4, ld_dsum=64, dx=FAKE * 5)
+    need = L.nvfp4_layernorm_backward_workspace_bytes(4, 64)
+    assert L.nvfp4_layernorm_backward(ctypes.byref(_norm_grad(**dict(a, **change))), FAKE, need, None) == UNSUPPORTED
 
 
 # the entry points' host code with launches that are only counted
