@@ -827,19 +827,24 @@ int attention_q_parts(const AttnArgs &a) {
   if (parts > steps / 8) parts = steps / 8;
   return (int)(parts < 1 ? 1 : parts > 16 ? 16 : parts);
 }
-// Queries split for dK and dV: parts of at least 8 tiles of 32 queries, up to
+// Queries split for dK and dV: parts of at least 8 steps of 32 queries, up to
 // 512 workgroups, what the compute units hold of them (4 x 500 tokens, 20 heads
 // of 128, 4 key heads: 63 us against 114 with one part; 2 x 4096 without a
 // causal mask: two parts cost the 28 us that joining them takes).  Causal passes
 // whose tiles weigh unevenly gain from a second set of workgroups, dealt to
-// whichever compute unit is done, but only long parts pay for the join: 2 x 4096
-// tokens, 40 heads of 128, 8 key heads (160 tiles each) 1241 -> 1152 us; 4096
-// tokens, 16 heads (32 each) 273 -> 295.
+// whichever compute unit is done, where that makes no more than two rounds of
+// them and parts are long enough to pay for the join.  Up to 512 tiles of keys,
+// heads of 128: 2 x 4096 tokens, 40 heads, 8 key heads (160 steps a part) 1251 ->
+// 1182 us, 8192, 8 and 8 (64) 532 -> 527, 4096, 24 and 4 (48) 407 -> 396, but 2 x
+// 3072, 24 and 8 (48) 435 -> 446; below 48, 4096, 20 and 4 (40) 350 -> 342, but
+// 3072, 16 and 4 (17) 198 -> 212.  More tiles than 512 have a round and a part as
+// they are: 6144 tokens, 16 and 16 (48) 528 -> 575 with twice as many, 12288, 8
+// and 8 (96) 1010 -> 1044, 14336 (112) 1416 -> 1415.
 int attention_k_parts(const AttnArgs &a) {
   const int64_t n = units(a, a.k_len, a.total_k, a.kv_heads);
   const int64_t rows = a.window && a.window < a.q_len ? a.window : a.causal ? (a.q_len + 1) / 2 : a.q_len;
   const int64_t steps = rows / 32 * (a.heads / a.kv_heads), twice = (1024 + n - 1) / n;
-  int64_t parts = a.causal && steps >= 48 * twice ? twice : (512 + n - 1) / n;
+  int64_t parts = a.causal && n <= 512 && steps >= 48 * twice ? twice : (512 + n - 1) / n;
   if (parts > steps / 8) parts = steps / 8;
   return (int)(parts < 1 ? 1 : parts > 16 ? 16 : parts);
 }

@@ -102,6 +102,17 @@ def test_layernorm_backward_in_place(L, change):
     assert L.nvfp4_layernorm_backward(ctypes.byref(_norm_grad(**dict(a, **change))), FAKE, need, None) == UNSUPPORTED
 
 
+@pytest.mark.parametrize("tokens,heads,kv_heads,parts", [
+    (6144, 16, 16, 1), (12288, 8, 8, 1), (4096, 16, 16, 1), (8192, 8, 8, 2), (4096, 40, 8, 4), (4096, 20, 4, 4), (4096, 24, 4, 8)])
+def test_attention_gradient_parts(L, tokens, heads, kv_heads, parts):
+    """How often dK and dV are split goes by the tiles of 128 keys: only up to 512 of them get a second set of
+    workgroups.  The parts are what the workspace holds beside two numbers for each query."""
+    s = _shape(batch=1, q_len=tokens, k_len=tokens, total_q=tokens, total_k=tokens, heads=heads, kv_heads=kv_heads, head_dim=128)
+    stats = 2 * ((4 * (heads * tokens + 1) + 255) // 256 * 256)
+    held = 2 * 4 * 128 * kv_heads * tokens
+    assert L.nvfp4_attention_backward_workspace_bytes(ctypes.byref(s)) == stats + (parts * held if parts > 1 else 0)
+
+
 # the entry points' host code with launches that are only counted
 DRIVER = r"""
 #include <stdio.h>
