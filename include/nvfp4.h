@@ -351,7 +351,9 @@ int nvfp4_codec_selftest(int which, const float *in_f32, const uint16_t *in_u16,
  * The conventions above hold (device pointers of the caller's, nothing
  * allocated, nothing kept, checks before anything is enqueued, any stream),
  * with these differences: sizes need not be multiples of 16, and NVFP4_F32 /
- * NVFP4_BF16 name the element types.  Inputs must be finite.  Results do not
+ * NVFP4_BF16 name the element types.  Inputs must be finite, and those of
+ * attention keep scale * q k^T finite; what comes out otherwise is unspecified
+ * (a maximum may leave a NaN out).  Results do not
  * depend on the order in which workgroups run: no sum is formed by atomics.
  * ------------------------------------------------------------------------ */
 

@@ -33,7 +33,8 @@ FLAGS = [
     "-I", os.path.join(ROOT, "include"), "-I", CSRC,
 ]
 
-# attention: no NaN arises from finite inputs, and maxima need no quieting
+# attention: no NaN arises from finite inputs that keep scores finite, and maxima
+# need no quieting
 FILE_FLAGS = {"attention.hip": ["-fno-honor-nans"]}
 
 

@@ -40,7 +40,7 @@ __device__ __forceinline__ int block_exponent(float top) {
 // (|y| <= 448) to nearest, or up iff the place of |y| between its neighbours,
 // in 2^-20, and the random operand's upper 20 bits sum to 2^20 or more.  With
 // the 16-bit uniform u in the upper half that is floor(|y| / step + u / 65536),
-// exactly (checked on the device over all binades).  positive: x >= 0, and what
+// exactly (the tests compare every binade down to 2^-12).  positive: x >= 0, and what
 // is not zero is raised to the least E4M3 value before it is rounded, so that it
 // cannot vanish.
 template <bool SR>

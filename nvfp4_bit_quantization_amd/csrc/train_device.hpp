@@ -101,7 +101,8 @@ __device__ __forceinline__ float wave_max(float v) {
 
 // fold a wave's maximum of non-negative floats into *out: bit patterns of
 // non-negative floats order as their values do, and a maximum does not depend
-// on the order of the atomics
+// on the order of the atomics.  An infinity is kept, a NaN is no maximum: what a
+// tensor of finite values cannot hold is not looked for.
 __device__ __forceinline__ void fold_max(float *out, float v) {
   v = wave_max(v);
   if ((threadIdx.x & 63) == 0 && v > 0.0f) atomicMax(reinterpret_cast<unsigned int *>(out), __float_as_uint(v));
