@@ -748,7 +748,7 @@ def nvfp4_attention(q, k, v, o, lse, causal=True, window=0, scale=None, cu_q=Non
                     workspace=None, stream=None):
     """o = softmax(scale q k^T) v and lse [heads][all queries] for [batch][tokens][heads][dim] tensors, or packed
     [tokens][heads][dim] ones with cu_q, cu_k (int32 [batch + 1], device) and the longest lengths max_q, max_k.
-    workspace: new_attention_workspace's, where one is needed."""
+    workspace: new_attention_workspace's, where one is needed.  Tokens of no packed sequence are not written."""
     s, sq, sk, heads, tokens, device = _attention_inputs(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
     _as(o, sq, device, "o")
     _lse(lse, heads, tokens, device)
@@ -761,7 +761,8 @@ def nvfp4_attention(q, k, v, o, lse, causal=True, window=0, scale=None, cu_q=Non
 
 def attention(q, k, v, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None, max_k=None, workspace=None,
               stream=None):
-    """Allocates and computes (o, lse)."""
+    """Allocates and computes (o, lse).  Rows of tokens that belong to no packed sequence are left uninitialised: a buffer
+    that a maximum is taken of later is better passed to nvfp4_attention, with zeros there."""
     if stream is not None:
         with _on_stream(stream):
             return attention(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k, workspace)
@@ -789,7 +790,7 @@ def _attention_backward(s, d_o, q, k, v, o, lse, dq, dk, dv, workspace, sq, sk, 
 
 def nvfp4_attention_backward(d_o, q, k, v, o, lse, dq, dk, dv, workspace, causal=True, window=0, scale=None, cu_q=None,
                              cu_k=None, max_q=None, max_k=None, stream=None):
-    """dq, dk and dv of nvfp4_attention with the same arguments."""
+    """dq, dk and dv of nvfp4_attention with the same arguments.  dq may be o, dk and dv may be k and v."""
     s, sq, sk, heads, tokens, device = _attention_inputs(q, k, v, causal, window, scale, cu_q, cu_k, max_q, max_k)
     for t, shape, what in ((d_o, sq, "d_o"), (o, sq, "o"), (dq, sq, "dq"), (dk, sk, "dk"), (dv, sk, "dv")):
         _as(t, shape, device, what)
@@ -810,7 +811,7 @@ def new_attention_workspace(q, k, v, causal=True, window=0, scale=None, cu_q=Non
 
 def attention_backward(d_o, q, k, v, o, lse, causal=True, window=0, scale=None, cu_q=None, cu_k=None, max_q=None,
                        max_k=None, workspace=None, stream=None):
-    """Allocates and computes (dq, dk, dv)."""
+    """Allocates and computes (dq, dk, dv); rows of tokens that belong to no packed sequence are left uninitialised."""
     if stream is not None:
         with _on_stream(stream):
             return attention_backward(d_o, q, k, v, o, lse, causal, window, scale, cu_q, cu_k, max_q, max_k, workspace)

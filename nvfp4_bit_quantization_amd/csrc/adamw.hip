@@ -7,9 +7,10 @@
 // four neighbouring lanes hold a block of 32 of an 8-bit state, so that block
 // maxima need two DPP steps.
 //
-// Two weights of 5120x20480 take 1140 us with 32-bit states and a bf16 copy
-// (5.9 GB, 5.15 TB/s; a copy of 2 GiB reaches 4.9) and 408 us with 8-bit states
-// (2.1 GB, 5.2 TB/s).  The 8-bit step was bound by vector instructions at
+// Two weights of 5120x20480 take 1083 to 1141 us on several devices with 32-bit
+// states and a bf16 copy (5.9 GB, 5.1-5.4 TB/s; a copy of 2 GiB reaches 4.9) and
+// 402 to 416 us with 8-bit states (2.1 GB, 5.1-5.3 TB/s, the vector unit busy in
+// 94 % of the cycles).  The 8-bit step was bound by vector instructions at
 // 623 us while E4M3 was encoded and decoded by integer steps: per 8 elements the
 // three Philox draws alone are some 40 multiplications.
 #include "train_device.hpp"

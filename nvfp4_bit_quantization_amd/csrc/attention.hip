@@ -106,8 +106,8 @@ __device__ __forceinline__ void sight(const AttnArgs &a, int i, int nk, int off,
 // four, 0, 3, 5, 6 or 1, 2, 4, 7, which 16 bytes do not keep apart for D = 64)
 // and the transposing one (4 rows at 4 neighbouring chunks), and all reads of a
 // lane stand at fixed distances from D / 32 addresses each, as the
-// instructions' immediate offsets.  (16 bytes for D = 64: the gradient of 2 x
-// 4096 tokens, 40 heads of 64, 8 key heads, causal, 727 us against 694.)
+// instructions' immediate offsets.  (16 bytes for D = 64: 5 % of the
+// gradient of 2 x 4096 tokens, 40 heads of 64, 8 key heads, causal, now 609 us.)
 template <int D>
 struct Tile {
   static constexpr int kChunks = D / 8, kSegRows = 64 / kChunks;
@@ -321,7 +321,7 @@ constexpr int kQueries = 128;  // queries of a workgroup: 32 per wave
 // One wave holds 32 queries as columns: scores^T = K Q^T, o^T = V^T p^T.
 // Running maximum and sum per query stay in its two lanes.  Two waves per SIMD:
 // while one waits or takes exponentials the other multiplies.
-// 8192 tokens, 40 heads of 128, 8 key heads, causal: 652-711 us on several devices, 0.97-1.05
+// 8192 tokens, 40 heads of 128, 8 key heads, causal: 650-711 us on several devices, 0.97-1.06
 // PFLOP/s, the MFMA busy in 57 % of the cycles at 1.82 GHz.  Power bounds it: 8 % fewer
 // cycles (operands read ahead) left the time as it was and lowered the clock.
 // Eight waves to a workgroup, which halves the transfers, took the same time;
@@ -509,7 +509,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnArgs a) {
 }
 
 // ------------------------------------------------------------- gradient ----
-// dQ (2 x 4096 tokens, 40 heads of 128, 8 key heads, causal: 483-506 us, 1.02-1.07
+// dQ (2 x 4096 tokens, 40 heads of 128, 8 key heads, causal: 477-506 us, 1.02-1.08
 // PFLOP/s over its three products, the MFMA busy in 60 % of the cycles: power).
 // A wave holds 32 queries as columns; scores^T = K Q^T, dP^T = V dO^T,
 // dQ^T = K^T dS^T.  It forms delta = sum_d do * o on the way, and leaves
@@ -639,8 +639,8 @@ __global__ __launch_bounds__(kThreads, 2) void attention_dq_kernel(AttnArgs a) {
 // registers nothing is left of the 256 that two waves per SIMD have each to
 // read operands ahead.  Queries come in tiles of 32 rows (D = 128), so that two
 // workgroups fit a compute unit's LDS, or 64 (D = 64).
-// The same tokens as for dQ: 665-700 us, 0.98-1.03 PFLOP/s over its four
-// products, and 30 to join them with the queries in two parts (1254 us as first
+// The same tokens as for dQ: 661-700 us, 0.98-1.04 PFLOP/s over its four
+// products, and 25 to join them with the queries in two parts (1254 us as first
 // written, one wave per SIMD; 898 with two and both operands in registers; 775
 // with values in LDS and one part).
 constexpr int kKeys = 128;  // keys of a workgroup

@@ -10,7 +10,7 @@
 // Both passes are bound by memory: 8192x5120 bf16 with a residual moves 336 MB
 // in 88 us (3.8 TB/s; 159 us before rows were loaded ahead and the two
 // exchanges of a row made one), the gradient of 16384x5120 671 MB in 142 us
-// (4.7 TB/s; 325 us before).  Small calls take what a launch does: 3 us for
+// (4.7 TB/s; 325 us before; 140-143 on several devices).  Small calls take what a launch does: 3 us for
 // 256x256.  Rows need no alignment beyond their elements'.  Above 8192 elements
 // neither weights nor the next row fit the registers; above 16384 the gradient's
 // sums do not either: 4096x20480 bf16 takes 95 us (161 with all groups' weights
@@ -28,9 +28,10 @@ namespace {
 // whole 16 bytes; what it repeats of its neighbour counts as zero in sums and is
 // not stored.  Widths below 8 have base < 0 and their elements at the end.
 // Against an end read element by element, 8192 rows of 5119 bf16 take 59 us
-// instead of 73, with a residual 106 instead of 143, their gradient 70 instead of
-// 120; 16384 rows of 2049, without a residual, 47 instead of 42.  Widths that are
-// multiples of 8 have kernels without it (8192x5120: 48 us, 54 with it).
+// instead of 73, with a residual 106 instead of 143 (117 with the maximum, too),
+// their gradient 70 instead of 120; 16384 rows of 2049, without a residual, 47
+// instead of 42.  Widths that are multiples of 8 have kernels without it
+// (8192x5120: 48 us, 54 with it).
 struct Place {
   int base, lead;
 };
