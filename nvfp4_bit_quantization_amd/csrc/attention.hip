@@ -843,8 +843,8 @@ int attention_q_parts(const AttnArgs &a) {
 // them and parts are long enough to pay for the join.  Up to 512 tiles of keys,
 // heads of 128: 2 x 4096 tokens, 40 heads, 8 key heads (160 steps a part) 1251 ->
 // 1182 us, 8192, 8 and 8 (64) 532 -> 527, 4096, 24 and 4 (48) 407 -> 396, but 2 x
-// 3072, 24 and 8 (48) 435 -> 446; below 48, 4096, 20 and 4 (40) 350 -> 342, but
-// 3072, 16 and 4 (17) 198 -> 212.  More tiles than 512 have a round and a part as
+// 3200, 24 and 8 (50) 454 -> 462; below 48, 4096, 20 and 4 (40) 350 -> 342, but
+// 3000, 16 and 4 (17) 183 -> 193.  More tiles than 512 have a round and a part as
 // they are: 6144 tokens, 16 and 16 (48) 528 -> 575 with twice as many, 12288, 8
 // and 8 (96) 1010 -> 1044, 14336 (112) 1416 -> 1415.
 int attention_k_parts(const AttnArgs &a) {
