@@ -57,7 +57,7 @@ extern "C" {
 #define NVFP4_E_SHAPE (-2)       /* a size <= 0, not a multiple of 16, or inconsistent */
 #define NVFP4_E_LD (-3)          /* a leading dimension smaller than the row length */
 #define NVFP4_E_ALIGN (-4)       /* x, codes or y not 16-byte aligned, or ld not a multiple of 8 */
-#define NVFP4_E_UNSUPPORTED (-5) /* unknown enum, RHT with a 2D layout, bad n_outs, K mismatch, outputs in the place of what is still read */
+#define NVFP4_E_UNSUPPORTED (-5) /* unknown enum, RHT with a 2D layout, bad n_outs, K mismatch, an output in the place of an input */
 #define NVFP4_E_WORKSPACE (-6)   /* workspace NULL or smaller than nvfp4_workspace_bytes() */
 #define NVFP4_E_HIP (-7)         /* a HIP launch failed */
 #define NVFP4_E_VALUE (-8)       /* a scalar argument out of its range (training operators) */
@@ -452,9 +452,8 @@ typedef struct {
  * itself; else batch index * q_len + query).  A query that sees no key has
  * o = 0 and lse = -inf.  Sequences may be empty in the packed form, and a
  * tensor of no tokens may have no data; tokens that belong to no sequence are
- * not written.  cu values outside
- * [0, total] or descending are read as clamped to it, so that no
- * access leaves the tensors.
+ * not written.  cu values outside [0, total] or descending are read as clamped
+ * to it, so that no access leaves the tensors.
  *   q, o: heads heads; k, v: kv_heads.  data 16-byte aligned, strides
  *   multiples of 8 and not negative, token_stride < 2^23.  lse: device float [heads][total_q].
  *   workspace  nvfp4_attention_workspace_bytes(shape) bytes of device scratch,
@@ -531,13 +530,14 @@ typedef struct {
  * with max |x| <= 448 * 2^e, its elements x / 2^e in E4M3.  NVFP4_SR rounds |x| / 2^e
  * up with the probability of its place between its two E4M3 neighbours, by a
  * 16-bit uniform; a non-zero r is never stored as zero (its square root
- * divides).  NVFP4_RTN rounds 8-bit states to nearest: r then stays where
- * it is, since a step moves it by less than half of an E4M3 step, and as the bias
+ * divides).  NVFP4_RTN rounds 8-bit states to nearest: r then stays where it is,
+ * since a step moves it by less than half of an E4M3 step, and as the bias
  * correction fades, updates grow by up to 1 / sqrt(1 - beta2); it is there for
- * single steps and comparisons, training wants NVFP4_SR.  bf16 params under NVFP4_SR add 16 uniform bits below the kept
- * ones and truncate.  The uniforms of element i of tensor index (its place in
- * `tensors`) are half i & 1 of word (i mod 8) / 2 of Philox4x32-10(key = seed,
- * counter = (i / 8, 4 index + which, step mod 2^32, 0x41440000 + step / 2^32)),
+ * single steps and comparisons, training wants NVFP4_SR.  bf16 params under
+ * NVFP4_SR add 16 uniform bits below the kept ones and truncate.  The uniforms of
+ * element i of tensor index (its place in `tensors`) are half i & 1 of word
+ * (i mod 8) / 2 of Philox4x32-10(key = seed, counter = (i / 8, 4 index + which,
+ * step mod 2^32, 0x41440000 + step / 2^32)),
  * which = 0 for m, 1 for r, 2 for the param: a step gives the same result
  * whenever it is run, and calls over different tensors want different seeds.
  * m = v = 0 (8-bit: zero bytes, any scales) starts.
