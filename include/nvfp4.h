@@ -549,6 +549,67 @@ typedef struct {
  */
 int nvfp4_adamw(const nvfp4_adamw_tensor *tensors, int64_t n_tensors, const nvfp4_adamw_config *config, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Block operators: what stands between the products of a transformer block.
+ * The training operators' conventions hold.
+ * ------------------------------------------------------------------------ */
+
+/* The query heads or the key heads of a nvfp4_qk_rope call.  data 16-byte
+ * aligned, strides multiples of 8 elements and not negative. */
+typedef struct {
+  nvfp4_heads x;       /* x_dtype: what is normalised and rotated.  Backward: the same, or no data without a weight */
+  nvfp4_heads y;       /* bf16: the result.  Backward: its gradient */
+  nvfp4_heads dx;      /* backward: x_dtype, the gradient of x */
+  const void *weight;  /* NULL: no norm; else [head_dim], w_dtype */
+  float *dweight;      /* backward with a weight: NULL, or [head_dim], overwritten */
+  int64_t heads;       /* 0: none, and nothing else is looked at */
+} nvfp4_rope_heads;
+
+typedef struct {
+  nvfp4_rope_heads q, k;     /* with weights both or neither (where both have heads) */
+  int64_t batch;             /* sequences, >= 1 */
+  int64_t tokens;            /* of each sequence; packed: of all together.  batch * tokens < 2^31; may be 0 */
+  const int64_t *positions;  /* NULL, or device [batch * tokens]: a token's position; not with cu */
+  const int32_t *cu;         /* NULL, or device [batch + 1]: packed sequences, as in nvfp4_attention_shape */
+  const double *freqs;       /* device [rot_dim / 2]: radians for each position */
+  int32_t head_dim;          /* a multiple of 8, 8 .. 128 */
+  int32_t rot_dim;           /* even, 0 .. head_dim: the first elements of a head, which are rotated */
+  int32_t interleaved;       /* 0: elements i and i + rot_dim / 2 are a pair; 1: elements 2 i and 2 i + 1 */
+  int32_t x_dtype, w_dtype;  /* NVFP4_F32 or NVFP4_BF16 */
+  float eps;                 /* with weights: a normal number, >= 2^-126 */
+  float magnitude;           /* finite; multiplies the rotated elements */
+} nvfp4_qk_rope_args;
+
+/*
+ * nvfp4_qk_rope -- for every head vector x of a token at position p, with
+ *   n = x * rstd * weight, rstd = 1 / sqrt(sum x^2 / head_dim + eps)
+ * (n = x without a weight), its pairs (n_a, n_b), i = 0 .. rot_dim / 2 - 1, at
+ * the angle t = p * freqs[i]:
+ *   y_a = magnitude * (n_a cos t - n_b sin t)
+ *   y_b = magnitude * (n_b cos t + n_a sin t),   y = n beyond rot_dim.
+ * p is positions[token], or the token's index in its sequence.  Angles are
+ * formed and reduced in 64 bits, the rest is binary32, rounded once to bf16.
+ * Tokens that belong to no packed sequence are not written.  Sums of squares
+ * have to be finite in binary32.  y may be x (bf16, with its strides: else
+ * NVFP4_E_UNSUPPORTED); otherwise outputs overlap neither each other nor what is
+ * read (NVFP4_E_UNSUPPORTED where they begin at the same address).  One kernel.
+ */
+int nvfp4_qk_rope(const nvfp4_qk_rope_args *args, void *stream);
+
+/*
+ * nvfp4_qk_rope_backward -- with g = y's gradient rotated by -t (and times
+ * magnitude), h = x * rstd and a = g * weight:
+ *   dx = rstd * (a - h * mean(a * h)),  dweight = sum over tokens and heads of g * h
+ * (dx = g without a weight; x is then not read).  Tokens of no packed sequence
+ * add nothing to dweight, and their dx is not written.  dx may be y (x bf16) or
+ * x, each with its strides.
+ *   workspace  nvfp4_qk_rope_backward_workspace_bytes(args) bytes of device
+ *              scratch, 16-byte aligned: 0 without a dweight.
+ * Sums over tokens are formed in a fixed order.  One kernel, two with a dweight.
+ */
+int nvfp4_qk_rope_backward(const nvfp4_qk_rope_args *args, void *workspace, size_t workspace_bytes, void *stream);
+size_t nvfp4_qk_rope_backward_workspace_bytes(const nvfp4_qk_rope_args *args);
+
 #ifdef __cplusplus
 }
 #endif

@@ -100,6 +100,18 @@ class nvfp4_adamw_config(ctypes.Structure):
                 ("seed", ctypes.c_uint64), ("grad_scale", ctypes.c_void_p)]
 
 
+class nvfp4_rope_heads(ctypes.Structure):
+    _fields_ = [("x", nvfp4_heads), ("y", nvfp4_heads), ("dx", nvfp4_heads), ("weight", ctypes.c_void_p),
+                ("dweight", ctypes.c_void_p), ("heads", ctypes.c_int64)]
+
+
+class nvfp4_qk_rope_args(ctypes.Structure):
+    _fields_ = [("q", nvfp4_rope_heads), ("k", nvfp4_rope_heads), ("batch", ctypes.c_int64), ("tokens", ctypes.c_int64),
+                ("positions", ctypes.c_void_p), ("cu", ctypes.c_void_p), ("freqs", ctypes.c_void_p)] + [
+        (n, ctypes.c_int32) for n in ("head_dim", "rot_dim", "interleaved", "x_dtype", "w_dtype")] + [
+        ("eps", ctypes.c_float), ("magnitude", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -160,6 +172,12 @@ def lib() -> ctypes.CDLL:
     L.nvfp4_attention_backward_workspace_bytes.argtypes = [P]
     L.nvfp4_adamw.restype = i32
     L.nvfp4_adamw.argtypes = [A(nvfp4_adamw_tensor), i64, A(nvfp4_adamw_config), P]
+    L.nvfp4_qk_rope.restype = i32
+    L.nvfp4_qk_rope.argtypes = [P, P]
+    L.nvfp4_qk_rope_backward.restype = i32
+    L.nvfp4_qk_rope_backward.argtypes = [P, P, ctypes.c_size_t, P]
+    L.nvfp4_qk_rope_backward_workspace_bytes.restype = ctypes.c_size_t
+    L.nvfp4_qk_rope_backward_workspace_bytes.argtypes = [P]
     _lib = L
     return L
 
@@ -935,3 +953,234 @@ def adamw_state_values(t: AdamWTensor):
     m, r = (torch.repeat_interleave(torch.exp2(s.float() - 127), 32)[:n].view(c.shape) * c.view(torch.float8_e4m3fn).float()
             for c, s in ((t.m, t.m_scale), (t.v, t.v_scale)))
     return m, r * r
+
+
+# ---------------------------------------------------------------------------
+# block operators: norm and rotation of query and key heads (see include/nvfp4.h)
+# ---------------------------------------------------------------------------
+def _call(name, device, *args):
+    """Calls an entry point with `device` current: a launch goes to the current device, whatever its stream."""
+    import torch
+    f = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == device:
+        _check(f(*args), name)
+    else:
+        with torch.cuda.device(device):
+            _check(f(*args), name)
+
+
+_ROPE = struct.Struct("@P3qP3qP3q2PqP3qP3qP3q2Pq2q3P5i2f4x")
+_NO_HEADS = (0, 0, 0, 0)
+_NO_SIDE = _NO_HEADS * 3 + (0, 0, 0)
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_length=4096, beta_fast=32.0, beta_slow=1.0,
+                     device="cuda"):
+    """(freqs, magnitude) of nvfp4_qk_rope for rotated heads of rot_dim elements: base^(-2 i / rot_dim) radians for each
+    position in a float64 tensor, for contexts longer by `factor` than the original_length that was trained on:
+    scaling None: as they are; "linear": all slowed by the factor; "ntk": by a larger base, so that the slowest is slowed
+    by the factor and the fastest is not; "yarn": by parts, pairs that turn less than beta_slow times in original_length
+    slowed, those that turn more than beta_fast times not, the others in proportion to their turns, with the magnitude
+    0.1 ln(factor) + 1."""
+    import math
+    import torch
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim: an even number of elements is wanted")
+    if not factor >= 1.0:
+        raise ValueError("factor: 1 or more is wanted")
+    if scaling == "ntk" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    if scaling in (None, "ntk"):
+        return f, 1.0
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling != "yarn":
+        raise ValueError("scaling: None, 'linear', 'ntk' or 'yarn' is wanted")
+    if not beta_fast > beta_slow:
+        raise ValueError("beta_fast: more than beta_slow is wanted")
+    turns = original_length * f / (2 * math.pi)
+    keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0, 1)
+    return f * keep + f / factor * (1 - keep), 0.1 * math.log(factor) + 1
+
+
+def _place(t):
+    """The C form of [batch][tokens][heads][dim] or [tokens][heads][dim], as a tuple."""
+    shape, st = t.shape, t.stride()  # of a dimension of one element: anything, and not used
+    return (t.data_ptr(), st[0] if len(shape) == 4 and shape[0] > 1 else 0,
+            st[-3] if shape[-3] > 1 else shape[-2] * shape[-1], st[-2] if shape[-2] > 1 else shape[-1])
+
+
+def _rope_tensor(t, like, device, what, dtype=None):
+    """Checks heads against those of `like` (the leading dimensions and head_dim)."""
+    shape = t.shape
+    if len(shape) != len(like) or shape[:-2] != like[:-2] or shape[-1] != like[-1] or t.get_device() != device:
+        raise ValueError("%s: a tensor [..][heads][dim] of %s on device %d is wanted" % (what, tuple(like), device))
+    if t.stride(-1) != 1:
+        raise ValueError("%s: a contiguous last dimension is wanted" % what)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s: %s is wanted, not %s" % (what, dtype, t.dtype))
+
+
+def _rope_common(ref, freqs, positions, cu, q_weight, k_weight, k):
+    """(tail of the C arguments before the scalars, rot_dim, w_dtype, device) of the checked common inputs."""
+    import torch
+    shape, device = ref.shape, _on_device(ref, "q")
+    if len(shape) != (4 if cu is None else 3) and not (cu is None and positions is not None and len(shape) == 3):
+        raise ValueError("q: [batch][tokens][heads][dim] is wanted, or [tokens][heads][dim] with cu or positions")
+    batch, tokens = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
+    if positions is not None:
+        _vector(positions, batch * tokens, device, "positions", torch.int64)
+    if cu is not None:
+        if positions is not None:
+            raise ValueError("positions or cu is wanted, not both")
+        _vector(cu, cu.numel(), device, "cu", torch.int32)
+        batch = cu.numel() - 1
+    rot = 0
+    if freqs is not None:
+        rot = 2 * freqs.numel()
+        _vector(freqs, rot // 2, device, "freqs", torch.float64)
+    if k is not None and (q_weight is None) != (k_weight is None):
+        raise ValueError("weights: both or neither are wanted")
+    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _vector(w, shape[-1], device, what)
+            if q_weight is not None and w.dtype != q_weight.dtype:
+                raise TypeError("%s: %s is wanted, not %s" % (what, q_weight.dtype, w.dtype))
+    w_dtype = F32 if q_weight is None else _dtype(q_weight)
+    return (max(batch, 1) if cu is None else batch, tokens if batch else 0, _ptr(positions), _ptr(cu), _ptr(freqs), shape[-1],
+            rot), w_dtype, device
+
+
+def nvfp4_qk_rope(q, k, q_out, k_out, freqs, positions=None, cu=None, q_weight=None, k_weight=None, eps=1e-6,
+                  interleaved=False, magnitude=1.0, stream=None):
+    """q_out and k_out (bfloat16) = the heads of q and k (k, k_out may be None), each divided by its root mean square and
+    times its weight [dim] where weights are given, and its first 2 * len(freqs) elements turned by position * freqs
+    (float64; None: norm only).  [batch][tokens][heads][dim], or [tokens][heads][dim] with cu (int32, packed sequences) or
+    positions (int64 [all tokens]; without them or cu: the index in the sequence).  q_out may be q, k_out may be k."""
+    import torch
+    common, w_dtype, device = _rope_common(q, freqs, positions, cu, q_weight, k_weight, k)
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out: both or neither are wanted")
+    for x, y, what in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is not None:
+            _rope_tensor(x, q.shape, device, what, q.dtype)
+            _rope_tensor(y, q.shape, device, what + "_out", torch.bfloat16)
+            if y.shape != x.shape:
+                raise ValueError("%s_out: a tensor of shape %s is wanted" % (what, tuple(x.shape)))
+    _rope(q, k, q_out, k_out, common, w_dtype, q_weight, k_weight, eps, interleaved, magnitude, device,
+          _raw_stream(stream, device))
+    return q_out, k_out
+
+
+def _rope(q, k, q_out, k_out, common, w_dtype, q_weight, k_weight, eps, interleaved, magnitude, device, stream):
+    second = _NO_SIDE if k is None else _place(k) + _place(k_out) + _NO_HEADS + (_ptr(k_weight), 0, k.shape[-2])
+    a = _ROPE.pack(*_place(q), *_place(q_out), *_NO_HEADS, _ptr(q_weight), 0, q.shape[-2], *second, *common,
+                   bool(interleaved), _dtype(q), w_dtype, eps, magnitude)
+    _call("nvfp4_qk_rope", device, a, stream)
+
+
+def qk_rope(q, k, freqs, positions=None, cu=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, magnitude=1.0,
+            stream=None):
+    """Allocates and computes (q_out, k_out) of nvfp4_qk_rope.  Rows of tokens that belong to no packed sequence are left
+    uninitialised."""
+    if stream is not None:
+        with _on_stream(stream):
+            return qk_rope(q, k, freqs, positions, cu, q_weight, k_weight, eps, interleaved, magnitude)
+    import torch
+    common, w_dtype, device = _rope_common(q, freqs, positions, cu, q_weight, k_weight, k)
+    dense = torch.contiguous_format
+    _rope_tensor(q, q.shape, device, "q")
+    q_out, k_out = torch.empty_like(q, dtype=torch.bfloat16, memory_format=dense), None
+    if k is not None:
+        _rope_tensor(k, q.shape, device, "k", q.dtype)
+        k_out = torch.empty_like(k, dtype=torch.bfloat16, memory_format=dense)
+    _rope(q, k, q_out, k_out, common, w_dtype, q_weight, k_weight, eps, interleaved, magnitude, device,
+          _raw_stream(None, device))
+    return q_out, k_out
+
+
+def _rope_backward_args(dy, x, dx, w, dw, heads):
+    return _NO_SIDE if dy is None else (_place(x) if x is not None and w is not None else _NO_HEADS) + _place(dy) + _place(
+        dx) + (_ptr(w), _ptr(dw), heads)
+
+
+def _rope_backward(dq_out, dk_out, q, k, dq, dk, dq_weight, dk_weight, common, w_dtype, q_weight, k_weight, eps, interleaved,
+                   magnitude, workspace, device, stream):
+    a = _ROPE.pack(*_rope_backward_args(dq_out, q, dq, q_weight, dq_weight, dq_out.shape[-2]),
+                   *_rope_backward_args(dk_out, k, dk, k_weight, dk_weight, 0 if dk_out is None else dk_out.shape[-2]), *common,
+                   bool(interleaved), _dtype(dq), w_dtype, eps, magnitude)
+    if workspace is None and (dq_weight is not None or dk_weight is not None):
+        workspace = _floats(1, lib().nvfp4_qk_rope_backward_workspace_bytes(a) // 4, dq_out.device)
+    _call("nvfp4_qk_rope_backward", device, a, _ptr(workspace), _nbytes(workspace), stream)
+
+
+def _rope_backward_inputs(dq_out, dk_out, freqs, q, k, positions, cu, q_weight, k_weight):
+    import torch
+    common, w_dtype, device = _rope_common(dq_out, freqs, positions, cu, q_weight, k_weight, dk_out)
+    for dy, x, what in ((dq_out, q, "q"), (dk_out, k, "k")):
+        if dy is None:
+            continue
+        _rope_tensor(dy, dq_out.shape, device, "d%s_out" % what, torch.bfloat16)
+        if q_weight is not None and x is None:
+            raise ValueError("%s: what was normalised is wanted" % what)
+        if x is not None:
+            _rope_tensor(x, dq_out.shape, device, what, q.dtype)
+            if x.shape != dy.shape:
+                raise ValueError("%s: a tensor of shape %s is wanted" % (what, tuple(dy.shape)))
+    return common, w_dtype, device
+
+
+def nvfp4_qk_rope_backward(dq_out, dk_out, dq, dk, freqs, q=None, k=None, positions=None, cu=None, q_weight=None,
+                           k_weight=None, eps=1e-6, interleaved=False, magnitude=1.0, dq_weight=None, dk_weight=None,
+                           workspace=None, stream=None):
+    """dq, dk (of one type) and, with weights, dq_weight and dk_weight (float32 [dim], or None) of nvfp4_qk_rope, from the
+    gradients dq_out and dk_out (bfloat16) of its results; q and k are its inputs, which only a norm needs.  dq may be dq_out
+    or q, dk likewise."""
+    import torch
+    common, w_dtype, device = _rope_backward_inputs(dq_out, dk_out, freqs, q, k, positions, cu, q_weight, k_weight)
+    for dy, dx, x, what in ((dq_out, dq, q, "dq"), (dk_out, dk, k, "dk")):
+        if (dy is None) != (dx is None):
+            raise ValueError("%s and its gradient: both or neither are wanted" % what)
+        if dy is not None:
+            _rope_tensor(dx, dy.shape, device, what, dq.dtype if x is None else x.dtype)
+            if dx.shape != dy.shape:
+                raise ValueError("%s: a tensor of shape %s is wanted" % (what, tuple(dy.shape)))
+    for dw, what in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
+        if dw is not None:
+            _vector(dw, dq.shape[-1], device, what, torch.float32)
+    if workspace is not None:
+        _scratch(workspace, device)
+    if stream is not None and workspace is None:
+        with _on_stream(stream):
+            _rope_backward(dq_out, dk_out, q, k, dq, dk, dq_weight, dk_weight, common, w_dtype, q_weight, k_weight, eps,
+                           interleaved, magnitude, None, device, _raw_stream(stream, device))
+    else:
+        _rope_backward(dq_out, dk_out, q, k, dq, dk, dq_weight, dk_weight, common, w_dtype, q_weight, k_weight, eps,
+                       interleaved, magnitude, workspace, device, _raw_stream(stream, device))
+    return dq, dk
+
+
+def qk_rope_backward(dq_out, dk_out, freqs, q=None, k=None, positions=None, cu=None, q_weight=None, k_weight=None, eps=1e-6,
+                     interleaved=False, magnitude=1.0, workspace=None, stream=None):
+    """Allocates and computes (dq, dk, dq_weight, dk_weight): dq and dk of q's type (bfloat16 without q), the weights'
+    gradients float32, or None without weights.  Rows of tokens that belong to no packed sequence are left uninitialised."""
+    if stream is not None:
+        with _on_stream(stream):
+            return qk_rope_backward(dq_out, dk_out, freqs, q, k, positions, cu, q_weight, k_weight, eps, interleaved,
+                                    magnitude, workspace)
+    import torch
+    common, w_dtype, device = _rope_backward_inputs(dq_out, dk_out, freqs, q, k, positions, cu, q_weight, k_weight)
+    dtype, dense = torch.bfloat16 if q is None else q.dtype, torch.contiguous_format
+    dq = torch.empty_like(dq_out, dtype=dtype, memory_format=dense)
+    dk = None if dk_out is None else torch.empty_like(dk_out, dtype=dtype, memory_format=dense)
+    dqw = dkw = None
+    if q_weight is not None:
+        dqw, dkw = _floats(2, dq.shape[-1], dq.device).unbind()
+        if dk is None:
+            dkw = None
+    if workspace is not None:
+        _scratch(workspace, device)
+    _rope_backward(dq_out, dk_out, q, k, dq, dk, dqw, dkw, common, w_dtype, q_weight, k_weight, eps, interleaved, magnitude,
+                   workspace, device, _raw_stream(None, device))
+    return dq, dk, dqw, dkw
