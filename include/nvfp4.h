@@ -610,6 +610,57 @@ int nvfp4_qk_rope(const nvfp4_qk_rope_args *args, void *stream);
 int nvfp4_qk_rope_backward(const nvfp4_qk_rope_args *args, void *workspace, size_t workspace_bytes, void *stream);
 size_t nvfp4_qk_rope_backward_workspace_bytes(const nvfp4_qk_rope_args *args);
 
+/* activations of the gated products */
+#define NVFP4_SILU 0      /* x / (1 + e^-x) */
+#define NVFP4_GELU 1      /* x (1 + erf(x / sqrt 2)) / 2 */
+#define NVFP4_GELU_TANH 2 /* x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2 */
+#define NVFP4_RELU 3      /* max(x, 0); its derivative at 0 is 0 */
+
+/* A bf16 matrix [rows][cols] that a gated product writes, or reads (its maxima
+ * are then not looked at). */
+typedef struct {
+  void *data;           /* 16-byte aligned */
+  int64_t ld;           /* elements between rows, a multiple of 8 */
+  float *amax_plain;    /* NULL, or 1 float: as in nvfp4_gemm_amax */
+  float *amax_rht_col;  /* NULL, or 1 float: as in nvfp4_gemm_amax */
+} nvfp4_gated_matrix;
+
+/*
+ * nvfp4_gemm_gated -- both projections of a gated feed-forward block, the
+ * activation and the product, in one kernel:
+ *   gate = A Bg^T / (S_A S_Bg),  up = A Bu^T / (S_A S_Bu)  (as nvfp4_gemm)
+ *   h[m][n] = activation(gate[m][n]) * up[m][n],
+ * formed of the binary32 products and rounded once to bf16.
+ *   a : M x K quantised tensor; b_gate, b_up : N x K ones (of either scale kind)
+ *   h : device bf16 [M][N], with the maxima that its quantisation needs, if wanted
+ *   gate, up : NULL, or where the products are kept, rounded to bf16, for the
+ *              gradient (their maxima have to be NULL)
+ * M, N and K are multiples of 16; K a multiple of 128 is quickest.  Maxima are
+ * raised by atomic maxima: the caller initialises them.  rht_seed: the signs of
+ * amax_rht_col.  Outputs overlap neither each other nor the operands.
+ */
+int nvfp4_gemm_gated(const nvfp4_tensor *a, const nvfp4_tensor *b_gate, const nvfp4_tensor *b_up, int32_t activation,
+                     const nvfp4_gated_matrix *h, const nvfp4_gated_matrix *gate, const nvfp4_gated_matrix *up,
+                     uint64_t rht_seed, void *stream);
+
+/*
+ * nvfp4_gemm_gated_backward -- the gradient of the gated product, with the
+ * product that brings it, in one kernel: dh = A B^T / (S_A S_B) is that of h (A
+ * the quantised gradient of the block's output, M x K; B the down projection's
+ * transposed weight, N x K), and
+ *   dgate = dh * up * activation'(gate),  dup = dh * activation(gate),
+ * each rounded once to bf16; dh is not rounded.  gate and up are bf16 [M][N], as
+ * nvfp4_gemm_gated kept them.  dgate and dup may stand in the place of gate and
+ * up, in either order, with the ld of what they replace (else
+ * NVFP4_E_UNSUPPORTED).  As two halves of one [M][2 N] buffer they are the
+ * operand of one product with both weights.  Maxima as in nvfp4_gemm_gated; dgate
+ * and dup may name the same ones.
+ */
+int nvfp4_gemm_gated_backward(const nvfp4_tensor *a, const nvfp4_tensor *b, int32_t activation,
+                              const nvfp4_gated_matrix *gate, const nvfp4_gated_matrix *up,
+                              const nvfp4_gated_matrix *dgate, const nvfp4_gated_matrix *dup, uint64_t rht_seed,
+                              void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -34,6 +34,8 @@ SCALE_1D16, SCALE_2D16 = 0, 1
 F32, BF16 = 0, 1
 LAYOUTS = {"row": ROW_1D, "col": COL_1D, "2d": TWO_D, "2d_t": TWO_D_T}
 ROUNDINGS = {"rtn": RTN, "sr": SR}
+SILU, GELU, GELU_TANH, RELU = 0, 1, 2, 3
+ACTIVATIONS = {"silu": SILU, "gelu": GELU, "gelu_tanh": GELU_TANH, "relu": RELU}
 
 
 class Nvfp4Error(RuntimeError):
@@ -112,6 +114,11 @@ class nvfp4_qk_rope_args(ctypes.Structure):
         ("eps", ctypes.c_float), ("magnitude", ctypes.c_float)]
 
 
+class nvfp4_gated_matrix(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("amax_plain", ctypes.c_void_p),
+                ("amax_rht_col", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -178,6 +185,10 @@ def lib() -> ctypes.CDLL:
     L.nvfp4_qk_rope_backward.argtypes = [P, P, ctypes.c_size_t, P]
     L.nvfp4_qk_rope_backward_workspace_bytes.restype = ctypes.c_size_t
     L.nvfp4_qk_rope_backward_workspace_bytes.argtypes = [P]
+    L.nvfp4_gemm_gated.restype = i32
+    L.nvfp4_gemm_gated.argtypes = [A(nvfp4_tensor), A(nvfp4_tensor), A(nvfp4_tensor), ctypes.c_int32, P, P, P, ctypes.c_uint64, P]
+    L.nvfp4_gemm_gated_backward.restype = i32
+    L.nvfp4_gemm_gated_backward.argtypes = [A(nvfp4_tensor), A(nvfp4_tensor), ctypes.c_int32, P, P, P, P, ctypes.c_uint64, P]
     _lib = L
     return L
 
@@ -1184,3 +1195,83 @@ def qk_rope_backward(dq_out, dk_out, freqs, q=None, k=None, positions=None, cu=N
     _rope_backward(dq_out, dk_out, q, k, dq, dk, dqw, dkw, common, w_dtype, q_weight, k_weight, eps, interleaved, magnitude,
                    workspace, device, _raw_stream(None, device))
     return dq, dk, dqw, dkw
+
+
+# the gated feed-forward products
+_GATED = struct.Struct("@Pq2P")
+
+
+def _gated_matrix(t, shape, device, what, amax=None, amax_rht_col=None) -> bytes:
+    """The C form of a checked bfloat16 [rows][cols]."""
+    import torch
+    _matrix(t, shape, device, what, torch.bfloat16)
+    for m in (amax, amax_rht_col):
+        if m is not None:
+            _vector(m, 1, device, what + "'s maximum", torch.float32)
+    return _GATED.pack(t.data_ptr(), _row_stride(t), _ptr(amax), _ptr(amax_rht_col))
+
+
+def _operands(*operands):
+    """Device of quantised operands that fit: all have one K, those after the first as many rows."""
+    device = operands[0].codes.get_device()
+    for q in operands:
+        if q.codes.get_device() != device or q.scales.get_device() != device or device < 0:
+            raise ValueError("operands on one device are wanted")
+        if q.cols != operands[0].cols or q.rows != operands[-1].rows and q is not operands[0]:
+            raise ValueError("operands do not fit: %s" % ", ".join("%d x %d" % (o.rows, o.cols) for o in operands))
+    return device
+
+
+def nvfp4_gemm_gated(a: QTensor, gate_weight: QTensor, up_weight: QTensor, h, gate=None, up=None, activation="silu", amax=None,
+                     amax_rht_col=None, rht_seed: int = 0, stream=None):
+    """h = activation(a gate_weight^T) * (a up_weight^T) into the bfloat16 tensor h; the products into gate and up, where
+    these are given.  *amax is raised to max |h|, *amax_rht_col to the maximum of h's column quantisation with the RHT."""
+    device = _operands(a, gate_weight, up_weight)
+    shape = (a.rows, gate_weight.rows)
+    mats = [_gated_matrix(h, shape, device, "h", amax, amax_rht_col)]
+    mats += [None if t is None else _gated_matrix(t, shape, device, what) for t, what in ((gate, "gate"), (up, "up"))]
+    _call("nvfp4_gemm_gated", device, a.c_struct(), gate_weight.c_struct(), up_weight.c_struct(),
+          ACTIVATIONS.get(activation, activation), *mats, rht_seed, _raw_stream(stream, device))
+    return h
+
+
+def gemm_gated(a: QTensor, gate_weight: QTensor, up_weight: QTensor, activation="silu", keep=True, amax=None, amax_rht_col=None,
+               rht_seed: int = 0, stream=None):
+    """Allocates and computes (h, gate, up) of nvfp4_gemm_gated; without `keep` gate and up are None, otherwise they stand
+    side by side in one buffer."""
+    import torch
+    m, n, device = a.rows, gate_weight.rows, a.codes.device
+    gate = up = None
+    with _on_stream(stream):
+        h = torch.empty((m, n), dtype=torch.bfloat16, device=device)
+        if keep:
+            both = torch.empty((m, 2 * n), dtype=torch.bfloat16, device=device)
+            gate, up = both[:, :n], both[:, n:]
+    nvfp4_gemm_gated(a, gate_weight, up_weight, h, gate, up, activation, amax, amax_rht_col, rht_seed, stream)
+    return h, gate, up
+
+
+def nvfp4_gemm_gated_backward(dy: QTensor, weight_t: QTensor, gate, up, dgate, dup, activation="silu", amax_gate=None,
+                              amax_up=None, amax_rht_gate=None, amax_rht_up=None, rht_seed: int = 0, stream=None):
+    """dgate and dup (bfloat16) of nvfp4_gemm_gated's h, whose gradient is dy weight_t^T (weight_t: the down projection's
+    weight, transposed), with the maxima of their quantisations.  dgate and dup may be gate and up, in either order."""
+    device = _operands(dy, weight_t)
+    shape = (dy.rows, weight_t.rows)
+    mats = [_gated_matrix(gate, shape, device, "gate"), _gated_matrix(up, shape, device, "up"),
+            _gated_matrix(dgate, shape, device, "dgate", amax_gate, amax_rht_gate),
+            _gated_matrix(dup, shape, device, "dup", amax_up, amax_rht_up)]
+    _call("nvfp4_gemm_gated_backward", device, dy.c_struct(), weight_t.c_struct(), ACTIVATIONS.get(activation, activation), *mats,
+          rht_seed, _raw_stream(stream, device))
+    return dgate, dup
+
+
+def gemm_gated_backward(dy: QTensor, weight_t: QTensor, gate, up, activation="silu", amax_gate=None, amax_up=None,
+                        amax_rht_gate=None, amax_rht_up=None, rht_seed: int = 0, stream=None):
+    """Allocates and computes (dgate, dup) of nvfp4_gemm_gated_backward, side by side in one buffer [rows][2 cols], which is
+    the gradient of a projection with both weights one above the other."""
+    import torch
+    m, n = dy.rows, weight_t.rows
+    with _on_stream(stream):
+        both = torch.empty((m, 2 * n), dtype=torch.bfloat16, device=dy.codes.device)
+    return nvfp4_gemm_gated_backward(dy, weight_t, gate, up, both[:, :n], both[:, n:], activation, amax_gate, amax_up,
+                                     amax_rht_gate, amax_rht_up, rht_seed, stream)

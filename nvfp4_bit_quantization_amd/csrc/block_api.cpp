@@ -147,6 +147,45 @@ size_t rope_parts(RopeArgs &r, void *workspace) {
   return used * sizeof(float);
 }
 
+// --------------------------------------------------------------- gated ----
+int check_operand(const nvfp4_tensor *t) {
+  if (!t || !t->codes || !t->scales || !t->global_scale) return NVFP4_E_NULL;
+  if (t->rows <= 0 || t->cols <= 0 || t->rows % 16 || t->cols % 16 || t->rows > ((int64_t)1 << 31)) return NVFP4_E_SHAPE;
+  if (t->scale_kind != NVFP4_SCALE_1D16 && t->scale_kind != NVFP4_SCALE_2D16) return NVFP4_E_UNSUPPORTED;
+  return aligned(t->codes, 16) ? NVFP4_OK : NVFP4_E_ALIGN;
+}
+
+int check_matrix(const nvfp4_gated_matrix *t, int64_t cols) {
+  if (!t || !t->data) return NVFP4_E_NULL;
+  if (t->ld < cols) return NVFP4_E_LD;
+  if (!aligned(t->data, 16) || t->ld % 8 || !aligned(t->amax_plain, 4) || !aligned(t->amax_rht_col, 4)) return NVFP4_E_ALIGN;
+  return NVFP4_OK;
+}
+
+// one workgroup per 128 x 64 outputs at most: the grid counts its threads in 32 bits
+bool gated_grid_ok(int64_t M, int64_t N) { return (M / 16 + 1) * (N / 16 + 1) / 32 < ((int64_t)1 << 24); }
+
+GatedArgs gated_args(const nvfp4_tensor *a, const nvfp4_tensor *b, int32_t activation, uint64_t rht_seed) {
+  GatedArgs r = {};
+  r.g.a_codes = a->codes;
+  r.g.a_scales = a->scales;
+  r.g.a_S = a->global_scale;
+  r.g.b_codes = b->codes;
+  r.g.b_scales = b->scales;
+  r.g.b_S = b->global_scale;
+  r.g.M = a->rows;
+  r.g.N = b->rows;
+  r.g.K = a->cols;
+  r.g.a_kind = a->scale_kind;
+  r.g.b_kind = b->scale_kind;
+  r.g.c_bf16 = 1;
+  r.g.rht_mask = nvfp4_rht_sign_mask(rht_seed);
+  r.activation = activation;
+  return r;
+}
+
+unsigned int *bits(float *p) { return reinterpret_cast<unsigned int *>(p); }
+
 }  // namespace
 
 extern "C" {
@@ -174,6 +213,61 @@ int nvfp4_qk_rope_backward(const nvfp4_qk_rope_args *a, void *workspace, size_t 
   if (!r.total && !need) return NVFP4_OK;  // nothing is written
   hipStream_t s = (hipStream_t)stream;
   return finish(launch_rope_backward(r, s), s);
+}
+
+int nvfp4_gemm_gated(const nvfp4_tensor *a, const nvfp4_tensor *b_gate, const nvfp4_tensor *b_up, int32_t activation,
+                     const nvfp4_gated_matrix *h, const nvfp4_gated_matrix *gate, const nvfp4_gated_matrix *up,
+                     uint64_t rht_seed, void *stream) {
+  for (const nvfp4_tensor *t : {a, b_gate, b_up})
+    if (const int st = check_operand(t)) return st;
+  if (a->cols != b_gate->cols || a->cols != b_up->cols || b_gate->rows != b_up->rows) return NVFP4_E_UNSUPPORTED;
+  if (activation < NVFP4_SILU || activation > NVFP4_RELU) return NVFP4_E_UNSUPPORTED;
+  if (!gated_grid_ok(a->rows, b_gate->rows)) return NVFP4_E_SHAPE;
+  if (const int st = check_matrix(h, b_gate->rows)) return st;
+  for (const nvfp4_gated_matrix *t : {gate, up}) {
+    if (!t) continue;
+    if (const int st = check_matrix(t, b_gate->rows)) return st;
+    if (t->amax_plain || t->amax_rht_col || t->data == h->data) return NVFP4_E_UNSUPPORTED;
+  }
+  if (gate && up && gate->data == up->data) return NVFP4_E_UNSUPPORTED;
+  GatedArgs r = gated_args(a, b_gate, activation, rht_seed);
+  r.u_codes = b_up->codes;
+  r.u_scales = b_up->scales;
+  r.u_S = b_up->global_scale;
+  r.u_kind = b_up->scale_kind;
+  r.h = (uint16_t *)h->data;
+  r.ld_h = h->ld;
+  r.amax[0] = bits(h->amax_plain);
+  r.rht[0] = bits(h->amax_rht_col);
+  if (gate) r.gate = (uint16_t *)gate->data, r.ld_gate = gate->ld;
+  if (up) r.up = (uint16_t *)up->data, r.ld_up = up->ld;
+  hipStream_t s = (hipStream_t)stream;
+  return finish(launch_gemm_gated(r, s), s);
+}
+
+int nvfp4_gemm_gated_backward(const nvfp4_tensor *a, const nvfp4_tensor *b, int32_t activation,
+                              const nvfp4_gated_matrix *gate, const nvfp4_gated_matrix *up,
+                              const nvfp4_gated_matrix *dgate, const nvfp4_gated_matrix *dup, uint64_t rht_seed,
+                              void *stream) {
+  for (const nvfp4_tensor *t : {a, b})
+    if (const int st = check_operand(t)) return st;
+  if (a->cols != b->cols || activation < NVFP4_SILU || activation > NVFP4_RELU) return NVFP4_E_UNSUPPORTED;
+  if (!gated_grid_ok(a->rows, b->rows)) return NVFP4_E_SHAPE;
+  for (const nvfp4_gated_matrix *t : {gate, up, dgate, dup})
+    if (const int st = check_matrix(t, b->rows)) return st;
+  if (dgate->data == dup->data) return NVFP4_E_UNSUPPORTED;
+  for (const nvfp4_gated_matrix *out : {dgate, dup})  // read by the lane that writes them
+    for (const nvfp4_gated_matrix *in : {gate, up})
+      if (out->data == in->data && out->ld != in->ld) return NVFP4_E_UNSUPPORTED;
+  GatedArgs r = gated_args(a, b, activation, rht_seed);
+  r.gate = (uint16_t *)gate->data, r.ld_gate = gate->ld;
+  r.up = (uint16_t *)up->data, r.ld_up = up->ld;
+  r.dgate = (uint16_t *)dgate->data, r.ld_dgate = dgate->ld;
+  r.dup = (uint16_t *)dup->data, r.ld_dup = dup->ld;
+  r.amax[0] = bits(dgate->amax_plain), r.rht[0] = bits(dgate->amax_rht_col);
+  r.amax[1] = bits(dup->amax_plain), r.rht[1] = bits(dup->amax_rht_col);
+  hipStream_t s = (hipStream_t)stream;
+  return finish(launch_gemm_gated_backward(r, s), s);
 }
 
 }  // extern "C"

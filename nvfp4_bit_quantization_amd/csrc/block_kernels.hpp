@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "nvfp4.h"
+#include "nvfp4_kernels.hpp"
 
 namespace nvfp4 {
 
@@ -44,5 +45,21 @@ int rope_lanes(int units);
 void rope_plan(RopeArgs &a);
 hipError_t launch_rope(const RopeArgs &a, hipStream_t s);
 hipError_t launch_rope_backward(const RopeArgs &a, hipStream_t s);
+
+// --------------------------------------------------------------- gated ----
+struct GatedArgs {
+  GemmArgs g;  // A, and as B the gate's weights (backward: the weights); M, N, K.  Its output fields are not used
+  const uint8_t *u_codes, *u_scales;  // the up projection's weights
+  const float *u_S;
+  int u_kind;
+  int activation;
+  uint16_t *h;             // forward: the result
+  uint16_t *gate, *up;     // forward: kept products, or null; backward: those of the forward pass
+  uint16_t *dgate, *dup;   // backward: the results
+  int64_t ld_h, ld_gate, ld_up, ld_dgate, ld_dup;
+  unsigned int *amax[2], *rht[2];  // maxima of h, or of dgate and dup (null: not wanted)
+};
+hipError_t launch_gemm_gated(const GatedArgs &a, hipStream_t s);
+hipError_t launch_gemm_gated_backward(const GatedArgs &a, hipStream_t s);
 
 }  // namespace nvfp4

@@ -128,3 +128,84 @@ def test_rope_of_nothing(L):
     a = _rope(tokens=0, cu=FAKE, **sides)
     assert L.nvfp4_qk_rope(ctypes.byref(a), None) == 0
     assert L.nvfp4_qk_rope_backward(ctypes.byref(a), None, 0, None) == 0
+
+
+def _tensor(rows=32, cols=64, **kw):
+    a = dict(codes=FAKE, scales=FAKE, global_scale=FAKE, amax=FAKE, rows=rows, cols=cols, scale_kind=0, rht=0)
+    a.update(kw)
+    return nv.nvfp4_tensor(**a)
+
+
+def _matrix(i, **kw):
+    a = dict(data=FAKE * i, ld=64, amax_plain=None, amax_rht_col=None)
+    a.update(kw)
+    return nv.nvfp4_gated_matrix(**a)
+
+
+def _gated(L, activation=0, **kw):
+    t = dict(a=_tensor(32), g=_tensor(48), u=_tensor(48), h=_matrix(2), gate=_matrix(3), up=_matrix(4))
+    t.update(kw)
+    p = lambda x: None if x is None else ctypes.byref(x)  # noqa: E731
+    return L.nvfp4_gemm_gated(p(t["a"]), p(t["g"]), p(t["u"]), activation, p(t["h"]), p(t["gate"]), p(t["up"]), 0, None)
+
+
+def _gated_back(L, activation=0, **kw):
+    t = dict(a=_tensor(32), b=_tensor(48), gate=_matrix(3), up=_matrix(4), dgate=_matrix(5), dup=_matrix(6))
+    t.update(kw)
+    p = lambda x: None if x is None else ctypes.byref(x)  # noqa: E731
+    return L.nvfp4_gemm_gated_backward(p(t["a"]), p(t["b"]), activation, p(t["gate"]), p(t["up"]), p(t["dgate"]), p(t["dup"]), 0, None)
+
+
+OPERANDS = [(None, NULL), (_tensor(codes=None), NULL), (_tensor(scales=None), NULL), (_tensor(global_scale=None), NULL),
+            (_tensor(rows=0), SHAPE), (_tensor(rows=40), SHAPE), (_tensor(cols=72), SHAPE), (_tensor(cols=0), SHAPE),
+            (_tensor(scale_kind=2), UNSUPPORTED), (_tensor(codes=FAKE + 8), ALIGN)]
+
+
+@pytest.mark.parametrize("i", range(len(OPERANDS)))
+def test_gated_operands(L, i):
+    t, status = OPERANDS[i]
+    for name in "agu":
+        assert _gated(L, **{name: t}) == status
+    for name in "ab":
+        assert _gated_back(L, **{name: t}) == status
+
+
+def test_gated_shapes_and_activations(L):
+    assert _gated(L, a=_tensor(32, 80)) == UNSUPPORTED
+    assert _gated(L, u=_tensor(64, 64)) == UNSUPPORTED
+    assert _gated(L, g=_tensor(48, 80), u=_tensor(48, 80)) == UNSUPPORTED
+    assert _gated_back(L, a=_tensor(32, 80)) == UNSUPPORTED
+    for bad in (-1, 4):
+        assert _gated(L, activation=bad) == UNSUPPORTED
+        assert _gated_back(L, activation=bad) == UNSUPPORTED
+    big = _tensor(1 << 24)
+    assert _gated(L, a=big, g=big, u=big, h=_matrix(2, ld=1 << 24)) == SHAPE
+    assert _gated_back(L, a=big, b=big) == SHAPE
+
+
+MATRICES = [(_matrix(0), NULL), (_matrix(9, ld=40), LD), (_matrix(9, ld=52), ALIGN), (nv.nvfp4_gated_matrix(FAKE + 8, 64, None, None), ALIGN),
+            (_matrix(9, amax_plain=FAKE + 2), ALIGN), (_matrix(9, amax_rht_col=FAKE + 1), ALIGN)]
+
+
+@pytest.mark.parametrize("i", range(len(MATRICES)))
+def test_gated_matrices(L, i):
+    t, status = MATRICES[i]
+    for name in ("h", "gate", "up"):
+        assert _gated(L, **{name: t}) == status
+    for name in ("gate", "up", "dgate", "dup"):
+        assert _gated_back(L, **{name: t}) == status
+
+
+def test_gated_outputs_stand_apart(L):
+    assert _gated(L, h=None) == NULL
+    assert _gated(L, gate=_matrix(2)) == UNSUPPORTED
+    assert _gated(L, up=_matrix(2)) == UNSUPPORTED
+    assert _gated(L, up=_matrix(3)) == UNSUPPORTED
+    assert _gated(L, gate=_matrix(3, amax_plain=FAKE)) == UNSUPPORTED
+    assert _gated(L, up=_matrix(4, amax_rht_col=FAKE)) == UNSUPPORTED
+    for name in ("gate", "up", "dgate", "dup"):
+        assert _gated_back(L, **{name: None}) == NULL
+    assert _gated_back(L, dup=_matrix(5)) == UNSUPPORTED
+    for out in ("dgate", "dup"):
+        for place in (3, 4):
+            assert _gated_back(L, **{out: _matrix(place, ld=128)}) == UNSUPPORTED
