@@ -96,45 +96,95 @@ __device__ __forceinline__ EpiScale scale_of(const float *a_S, const float *b_S)
   return epi_scale(g);
 }
 
-// The epilogues of a tile with TM x TN blocks of 32 x 32 to a wave.  What lies past
-// M or N is zero in the maxima.
+// The epilogue of a tile with TM x TN blocks of 32 x 32 to a wave: block row by
+// block row, the accumulators go through a slab of LDS of the wave's own, from
+// which a lane takes 8 neighbouring columns of a row, so that loads and stores
+// are of 16 bytes, and the loop over rows is short code.  A slab's rows are 32
+// banks apart every 4, as the accumulators' lane halves write them.
+// What lies past M or N is zero in the maxima.
+template <int TN>
+struct Slab {
+  static constexpr int kStride = 32 * TN + 8;  // floats between rows
+  static constexpr int kFloats = 32 * kStride; // of a wave
+};
+
+// a slab is read as another type than it was written as, by other lanes of the
+// wave: the wave's accesses to LDS keep their order, the compiler has to, too
+__device__ __forceinline__ void slab_fence() { asm volatile("" ::: "memory"); }
+__device__ __forceinline__ void store_past_caches(uint16_t *p, const u32x4 &v) {
+  __builtin_nontemporal_store(v, reinterpret_cast<u32x4 *>(p));
+}
+__device__ __forceinline__ uint32_t top_of(uint32_t top, const u32x4 &v) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) top = max(top, max(v[k] & 0x7FFFu, v[k] >> 16 & 0x7FFFu));
+  return top;
+}
+// the maximum of 32 x 32 rounded values and of their transform, a column to a lane
+__device__ __forceinline__ void slab_max(FusedMax &f, const GemmArgs &o, const uint16_t *at, int stride, uint32_t lane) {
+  uint32_t hb[16];
+#pragma unroll
+  for (int r = 0; r < 16; ++r) hb[r] = at[((r >> 2) * 8 + (lane >> 5) * 4 + (r & 3)) * stride + (lane & 31)];
+  fused_max_block(f, o, hb);
+}
+
 template <int ACT, int TM, int TN>
-__device__ __forceinline__ void gated_store(const GatedArgs &a, int64_t m0, int64_t n0, const float16v acc[TM][TN]) {
-  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5;
+__device__ __forceinline__ void gated_store(const GatedArgs &a, int64_t m0, int64_t n0, const float16v acc[TM][TN], float *lds) {
+  constexpr int S = Slab<TN>::kStride, LANES = 2 * TN, ROWS = 64 / LANES;  // lanes of a row, rows at a time
+  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  float *slab = lds + wave * Slab<TN>::kFloats;
   const EpiScale eg = scale_of(a.g.a_S, a.g.b_S), eu = scale_of(a.g.a_S, a.u_S);
   GemmArgs o = a.g;
   o.amax_plain = a.amax[0];
   o.amax_rht = a.rht[0];
-  const bool fused = o.amax_plain || o.amax_rht;
   FusedMax fm;
-  if (fused) fused_max_init(fm, o, lane);
-  const int rows = (int)min((int64_t)64 * TM, a.g.M - m0);
+  fused_max_init(fm, o, lane);
+  const int c = lane % LANES * 8, first = lane / LANES;
+  const int64_t n = n0 + (wave & 1) * (TN * 16) + c;
+  const int64_t m = m0 + (wave >> 1) * (TM * 32);
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+  for (int i = 0; i < TM; ++i) {
 #pragma unroll
-    for (int j = 0; j < TN / 2; ++j) {
-      const int64_t n = n0 + (wave & 1) * (TN * 16) + j * 32 + lr;
-      uint32_t hb[16];
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int m = (wave >> 1) * (TM * 32) + i * 32 + (r >> 2) * 8 + h * 4 + (r & 3);
-        const float gv = epi_apply(acc[i][j][r], eg), uv = epi_apply(acc[i][j + TN / 2][r], eu);
-        hb[r] = 0;
-        if (m < rows && n < a.g.N) {
-          hb[r] = bf16_rne_bits(act<ACT>(gv) * uv);
-          __builtin_nontemporal_store((uint16_t)hb[r], &a.h[(m0 + m) * a.ld_h + n]);
-          if (a.gate) __builtin_nontemporal_store((uint16_t)bf16_rne_bits(gv), &a.gate[(m0 + m) * a.ld_gate + n]);
-          if (a.up) __builtin_nontemporal_store((uint16_t)bf16_rne_bits(uv), &a.up[(m0 + m) * a.ld_up + n]);
-        }
+      for (int r = 0; r < 16; ++r)
+        slab[((r >> 2) * 8 + (lane >> 5) * 4 + (r & 3)) * S + j * 32 + (lane & 31)] = acc[i][j][r];
+    slab_fence();
+#pragma unroll 2
+    for (int r = first; r < 32; r += ROWS) {
+      const int64_t row = m + i * 32 + r;
+      float g[8], u[8], h[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        g[k] = epi_apply(slab[r * S + c + k], eg);
+        u[k] = epi_apply(slab[r * S + TN * 16 + c + k], eu);
+        h[k] = act<ACT>(g[k]) * u[k];
       }
-      if (fused) fused_max_block(fm, o, hb);
+      u32x4 hb = packed8(h);
+      if (row < a.g.M && n < a.g.N) {
+        store_past_caches(a.h + row * a.ld_h + n, hb);
+        if (a.gate) store_past_caches(a.gate + row * a.ld_gate + n, packed8(g));
+        if (a.up) store_past_caches(a.up + row * a.ld_up + n, packed8(u));
+      } else {
+        hb = (u32x4){0, 0, 0, 0};
+      }
+      fm.plain = top_of(fm.plain, hb);
+      if (o.amax_rht) *reinterpret_cast<u32x4 *>(reinterpret_cast<uint16_t *>(slab + r * S) + c) = hb;
     }
-  if (fused) fused_max_flush(fm, o);
+    slab_fence();
+    if (o.amax_rht) {
+#pragma unroll
+      for (int j = 0; j < TN / 2; ++j) slab_max(fm, o, reinterpret_cast<const uint16_t *>(slab) + j * 32, 2 * S, lane);
+      slab_fence();
+    }
+  }
+  if (o.amax_plain || o.amax_rht) fused_max_flush(fm, o);
 }
 
 template <int ACT, int TM, int TN>
-__device__ __forceinline__ void grad_store(const GatedArgs &a, int64_t m0, int64_t n0, const float16v acc[TM][TN]) {
-  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5;
+__device__ __forceinline__ void grad_store(const GatedArgs &a, int64_t m0, int64_t n0, const float16v acc[TM][TN], float *lds) {
+  constexpr int S = Slab<TN>::kStride, LANES = 4 * TN, ROWS = 64 / LANES;
+  const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  float *slab = lds + wave * Slab<TN>::kFloats;
   const EpiScale es = scale_of(a.g.a_S, a.g.b_S);
   GemmArgs o[2] = {a.g, a.g};
   FusedMax fm[2];
@@ -144,53 +194,73 @@ __device__ __forceinline__ void grad_store(const GatedArgs &a, int64_t m0, int64
     o[k].amax_rht = a.rht[k];
     fused_max_init(fm[k], o[k], lane);
   }
-  const int rows = (int)min((int64_t)64 * TM, a.g.M - m0);
+  const bool rht = a.rht[0] || a.rht[1];
+  const int c = lane % LANES * 8, first = lane / LANES;
+  const int64_t n = n0 + (wave & 1) * (TN * 32) + c;
+  const int64_t m = m0 + (wave >> 1) * (TM * 32);
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+  for (int i = 0; i < TM; ++i) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int64_t n = n0 + (wave & 1) * (TN * 32) + j * 32 + lr;
-      uint32_t gb[16], ub[16];
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int m = (wave >> 1) * (TM * 32) + i * 32 + (r >> 2) * 8 + h * 4 + (r & 3);
-        gb[r] = ub[r] = 0;
-        if (m < rows && n < a.g.N) {
-          gb[r] = a.gate[(m0 + m) * a.ld_gate + n];
-          ub[r] = a.up[(m0 + m) * a.ld_up + n];
-        }
+      for (int r = 0; r < 16; ++r)
+        slab[((r >> 2) * 8 + (lane >> 5) * 4 + (r & 3)) * S + j * 32 + (lane & 31)] = acc[i][j][r];
+    slab_fence();
+#pragma unroll 2
+    for (int r = first; r < 32; r += ROWS) {
+      const int64_t row = m + i * 32 + r;
+      const bool here = row < a.g.M && n < a.g.N;
+      uint4 g = make_uint4(0, 0, 0, 0), u = g;
+      if (here) {
+        g = load_group(a.gate + row * a.ld_gate + n);
+        u = load_group(a.up + row * a.ld_up + n);
       }
+      float dg[8], du[8];
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int m = (wave >> 1) * (TM * 32) + i * 32 + (r >> 2) * 8 + h * 4 + (r & 3);
-        const float dh = epi_apply(acc[i][j][r], es);
+      for (int k = 0; k < 8; ++k) {
+        const float dh = epi_apply(slab[r * S + c + k], es);
         float f, df;
-        act_grad<ACT>(bf16_lo(gb[r]), f, df);
-        gb[r] = bf16_rne_bits(dh * bf16_lo(ub[r]) * df);
-        ub[r] = bf16_rne_bits(dh * f);
-        if (m < rows && n < a.g.N) {
-          __builtin_nontemporal_store((uint16_t)gb[r], &a.dgate[(m0 + m) * a.ld_dgate + n]);
-          __builtin_nontemporal_store((uint16_t)ub[r], &a.dup[(m0 + m) * a.ld_dup + n]);
-        } else {
-          gb[r] = ub[r] = 0;
-        }
+        act_grad<ACT>(bf16_at(g, k), f, df);
+        dg[k] = dh * bf16_at(u, k) * df;
+        du[k] = dh * f;
       }
-      if (a.amax[0] || a.rht[0]) fused_max_block(fm[0], o[0], gb);
-      if (a.amax[1] || a.rht[1]) fused_max_block(fm[1], o[1], ub);
+      u32x4 gb = packed8(dg), ub = packed8(du);
+      if (here) {
+        store_past_caches(a.dgate + row * a.ld_dgate + n, gb);
+        store_past_caches(a.dup + row * a.ld_dup + n, ub);
+      } else {
+        gb = ub = (u32x4){0, 0, 0, 0};
+      }
+      fm[0].plain = top_of(fm[0].plain, gb);
+      fm[1].plain = top_of(fm[1].plain, ub);
+      if (rht) {
+        uint16_t *at = reinterpret_cast<uint16_t *>(slab + r * S) + c;
+        *reinterpret_cast<u32x4 *>(at) = gb;
+        *reinterpret_cast<u32x4 *>(at + TN * 32) = ub;
+      }
     }
+    slab_fence();
+    if (rht) {
+#pragma unroll
+      for (int j = 0; j < 2 * TN; ++j)
+        slab_max(fm[j / TN], o[j / TN], reinterpret_cast<const uint16_t *>(slab) + j * 32, 2 * S, lane);
+      slab_fence();
+    }
+  }
 #pragma unroll
   for (int k = 0; k < 2; ++k)
     if (a.amax[k] || a.rht[k]) fused_max_flush(fm[k], o[k]);
 }
 
+// lds: as many floats as the four waves' slabs, which no wave reads any more
 template <bool BACK, int TM, int TN>
-__device__ __forceinline__ void store_tile(const GatedArgs &a, int64_t m0, int64_t n0, const float16v acc[TM][TN]) {
-#define NVFP4_STORE(ACT)                         \
-  case ACT:                                      \
-    if (BACK)                                    \
-      grad_store<ACT, TM, TN>(a, m0, n0, acc);   \
-    else                                         \
-      gated_store<ACT, TM, TN>(a, m0, n0, acc);  \
+__device__ __forceinline__ void store_tile(const GatedArgs &a, int64_t m0, int64_t n0, const float16v acc[TM][TN], float *lds) {
+#define NVFP4_STORE(ACT)                              \
+  case ACT:                                           \
+    if (BACK)                                         \
+      grad_store<ACT, TM, TN>(a, m0, n0, acc, lds);   \
+    else                                              \
+      gated_store<ACT, TM, TN>(a, m0, n0, acc, lds);  \
     break;
   switch (a.activation) {
     NVFP4_STORE(NVFP4_SILU)
@@ -229,15 +299,24 @@ __global__ __launch_bounds__(kGThreads) void gated_fast_kernel(GatedArgs a) {
     fast_tile(EndedRows{a.g, m0, n0}, 0, (uint32_t)(a.g.K / kFBK), acc, lds);
   else
     fast_tile(GatedRows<4>{a, m0, n0}, 0, (uint32_t)(a.g.K / kFBK), acc, lds);
-  store_tile<BACK, 4, 4>(a, m0, n0, acc);
+  __syncthreads();  // no wave reads the stages any more
+  store_tile<BACK, 4, 4>(a, m0, n0, acc, reinterpret_cast<float *>(lds));
 }
 
 // any K: tiles of 64 TM x 64 TN operand rows through registers, a K-tile ahead
 template <bool BACK, int TM, int TN>
 __global__ __launch_bounds__(kGThreads) void gated_generic_kernel(GatedArgs a) {
   constexpr int BM = GemmTile<TM, TN>::BM, ROWS = GemmTile<TM, TN>::ROWS;
-  __shared__ __attribute__((aligned(16))) uint8_t lcodes[2][ROWS * kRowBytes];
-  __shared__ uint32_t lscales[2][ROWS];
+  union Shared {
+    struct {
+      uint8_t codes[2][ROWS * kRowBytes];
+      uint32_t scales[2][ROWS];
+    } stage;
+    float slabs[kGThreads / 64 * Slab<TN>::kFloats];
+  };
+  __shared__ __attribute__((aligned(16))) Shared lds;
+  auto &lcodes = lds.stage.codes;
+  auto &lscales = lds.stage.scales;
   int64_t m0, n0;
   origin<BM, BACK ? 64 * TN : 32 * TN>(a, xcd_tile(blockIdx.x, gridDim.x), m0, n0);
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -296,7 +375,7 @@ __global__ __launch_bounds__(kGThreads) void gated_generic_kernel(GatedArgs a) {
     if (kt + 1 < KT) stage_store<TM, TN>(lcodes[buf ^ 1], lscales[buf ^ 1], st);
     __syncthreads();
   }
-  store_tile<BACK, TM, TN>(a, m0, n0, acc);
+  store_tile<BACK, TM, TN>(a, m0, n0, acc, lds.slabs);
 }
 
 int64_t tiles(const GatedArgs &a, int64_t bm, int64_t bn) { return (a.g.M + bm - 1) / bm * ((a.g.N + bn - 1) / bn); }
