@@ -661,6 +661,64 @@ int nvfp4_gemm_gated_backward(const nvfp4_tensor *a, const nvfp4_tensor *b, int3
                               const nvfp4_gated_matrix *dgate, const nvfp4_gated_matrix *dup, uint64_t rht_seed,
                               void *stream);
 
+/* One matrix of an orthogonalised step, [rows][cols] contiguous. */
+typedef struct {
+  void *param;         /* NULL, or param_dtype, updated */
+  const void *grad;    /* grad_dtype */
+  float *m;            /* NULL (no momentum: u = g), or the momentum, updated */
+  void *copy;          /* with a param: NULL, or bf16: the new parameter rounded to nearest */
+  void *update;        /* NULL, or bf16: the orthogonalised matrix (there without a param) */
+  float *amax;         /* with a param: NULL, or 1 float: becomes max(*amax, max |copy|) (without a copy: of the stored param) */
+  int64_t rows, cols;  /* 0 .. 2^17; rows * cols <= 2^33 */
+  int32_t param_dtype; /* NVFP4_F32 or NVFP4_BF16 */
+  int32_t grad_dtype;  /* NVFP4_F32 or NVFP4_BF16 */
+  float weight_decay;  /* >= 0 */
+  float scale;         /* finite: multiplies lr for this matrix (for updates as large as AdamW's: 0.2 sqrt(max(rows, cols))) */
+} nvfp4_muon_tensor;
+
+typedef struct {
+  float lr;            /* >= 0 */
+  double momentum;     /* [0, 1) */
+  int32_t nesterov;    /* 0 or 1 */
+  int32_t steps;       /* of the iteration, 1 .. 16 */
+  double a, b, c;      /* its coefficients (see below) */
+  int32_t rounding;    /* of bf16 params: NVFP4_RTN or NVFP4_SR */
+  int64_t step;        /* number of the step, 0 <= step < 2^47, for NVFP4_SR's uniforms */
+  uint64_t seed;       /* Philox key of NVFP4_SR */
+  const float *grad_scale; /* NULL, or device float: multiplies every gradient */
+} nvfp4_muon_config;
+
+/*
+ * nvfp4_muon -- one step of every matrix by its orthogonalised momentum (as
+ * published for the Muon optimiser by Jordan and others):
+ *   g = grad * grad_scale, m = momentum m + (1 - momentum) g,
+ *   u = m, with nesterov (1 - momentum) g + momentum m (without m: u = g),
+ *   X = u / ||u|| (the Frobenius norm; X = 0 where u is), then `steps` times
+ *   X = a X + b (X X^T) X + c (X X^T)^2 X,
+ *   param = param (1 - lr weight_decay) - lr scale X.
+ * a = 3.4445, b = -4.7750, c = 2.0315 take singular values of 2^-8 and more to
+ * 0.7 .. 1.2 in 5 steps.  Coefficients that can take a singular value of the
+ * iteration, which starts in [0, 1], above 3.5, or |a + b s + c s^2| above 14, are
+ * refused (NVFP4_E_VALUE).
+ * Momentum, norm (binary64 sums) and parameters are binary32; the iteration's
+ * matrices are held in fp16 with powers of two as scales, their products summed
+ * in binary32: X is off by 1e-3 to 3e-3 of its norm.  bf16 params under NVFP4_SR add
+ * 16 uniform bits below the kept ones and truncate; those of element i (row-major)
+ * of tensor index (its place in `tensors`) are half i & 1 of word (i mod 8) / 2 of
+ * Philox4x32-10(key = seed, counter = (i / 8 mod 2^32, index, step mod 2^32,
+ * 0x4D550000 + step / 2^32)).
+ *   tensors    host array of n_tensors >= 1; no buffer of one that is written
+ *              belongs to another
+ *   workspace  nvfp4_muon_workspace_bytes(tensors, n_tensors) bytes of device
+ *              scratch, 16-byte aligned, not initialised
+ * Arrays need their elements' alignment.  lr, step and the other scalars are taken
+ * at the call: a captured graph repeats them.  3 + 3 steps kernels for every group
+ * of up to 30 matrices (fewer where they are large).
+ */
+int nvfp4_muon(const nvfp4_muon_tensor *tensors, int64_t n_tensors, const nvfp4_muon_config *config, void *workspace,
+               size_t workspace_bytes, void *stream);
+size_t nvfp4_muon_workspace_bytes(const nvfp4_muon_tensor *tensors, int64_t n_tensors);
+
 #ifdef __cplusplus
 }
 #endif

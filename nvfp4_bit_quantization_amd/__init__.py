@@ -119,6 +119,18 @@ class nvfp4_gated_matrix(ctypes.Structure):
                 ("amax_rht_col", ctypes.c_void_p)]
 
 
+class nvfp4_muon_tensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "m", "copy", "update", "amax")] + [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+        ("weight_decay", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class nvfp4_muon_config(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_double), ("nesterov", ctypes.c_int32), ("steps", ctypes.c_int32),
+                ("a", ctypes.c_double), ("b", ctypes.c_double), ("c", ctypes.c_double), ("rounding", ctypes.c_int32),
+                ("step", ctypes.c_int64), ("seed", ctypes.c_uint64), ("grad_scale", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -189,6 +201,10 @@ def lib() -> ctypes.CDLL:
     L.nvfp4_gemm_gated.argtypes = [A(nvfp4_tensor), A(nvfp4_tensor), A(nvfp4_tensor), ctypes.c_int32, P, P, P, ctypes.c_uint64, P]
     L.nvfp4_gemm_gated_backward.restype = i32
     L.nvfp4_gemm_gated_backward.argtypes = [A(nvfp4_tensor), A(nvfp4_tensor), ctypes.c_int32, P, P, P, P, ctypes.c_uint64, P]
+    L.nvfp4_muon.restype = i32
+    L.nvfp4_muon.argtypes = [A(nvfp4_muon_tensor), i64, A(nvfp4_muon_config), P, ctypes.c_size_t, P]
+    L.nvfp4_muon_workspace_bytes.restype = ctypes.c_size_t
+    L.nvfp4_muon_workspace_bytes.argtypes = [A(nvfp4_muon_tensor), i64]
     _lib = L
     return L
 
@@ -1275,3 +1291,118 @@ def gemm_gated_backward(dy: QTensor, weight_t: QTensor, gate, up, activation="si
         both = torch.empty((m, 2 * n), dtype=torch.bfloat16, device=dy.codes.device)
     return nvfp4_gemm_gated_backward(dy, weight_t, gate, up, both[:, :n], both[:, n:], activation, amax_gate, amax_up,
                                      amax_rht_gate, amax_rht_up, rht_seed, stream)
+
+
+# matrices stepped by their orthogonalised momentum
+MUON_COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+@dataclass
+class MuonTensor:
+    """One matrix of a Muon step: param and grad [rows][cols], float32 or bfloat16; m: float32, or None (no momentum);
+    scale multiplies the learning rate (None: 0.2 sqrt(max(rows, cols)), for updates as large as AdamW's); copy and update
+    (the orthogonalised matrix): bfloat16, or None; amax: float32 [1], or None.  Without a param the update alone is formed."""
+    param: "object"
+    grad: "object"
+    m: "object" = None
+    weight_decay: float = 0.0
+    scale: Optional[float] = None
+    copy: "object" = None
+    update: "object" = None
+    amax: "object" = None
+
+    def c_struct(self) -> nvfp4_muon_tensor:
+        import torch
+        shape = self.grad.shape
+        if len(shape) != 2:
+            raise ValueError("grad: [rows][cols] is wanted")
+        n = self.grad.numel()
+        for t, size, dtype, what in ((self.grad, n, None, "grad"), (self.param, n, None, "param"), (self.m, n, torch.float32, "m"),
+                                     (self.copy, n, torch.bfloat16, "copy"), (self.update, n, torch.bfloat16, "update"),
+                                     (self.amax, 1, torch.float32, "amax")):
+            if t is None:
+                continue
+            if t.numel() != size or (size == n and t.shape != shape and what != "amax"):
+                raise ValueError("%s: a tensor of shape %s is wanted" % (what, tuple(shape)))
+            if not t.is_contiguous() or not t.is_cuda or t.device != self.grad.device:
+                raise ValueError("%s: a contiguous tensor on grad's device is wanted" % what)
+            if dtype is not None and t.dtype != dtype:
+                raise TypeError("%s: %s is wanted, not %s" % (what, dtype, t.dtype))
+        scale = 0.2 * max(shape) ** 0.5 if self.scale is None else self.scale
+        return nvfp4_muon_tensor(_ptr(self.param), self.grad.data_ptr(), _ptr(self.m), _ptr(self.copy), _ptr(self.update),
+                                 _ptr(self.amax), shape[0], shape[1], F32 if self.param is None else _dtype(self.param),
+                                 _dtype(self.grad), self.weight_decay, scale)
+
+
+def muon_tensor(param, grad, weight_decay=0.0, scale=None, copy=None, amax=None) -> MuonTensor:
+    """A MuonTensor with a new zero momentum."""
+    import torch
+    return MuonTensor(param, grad, torch.zeros(param.shape, dtype=torch.float32, device=param.device), weight_decay, scale, copy,
+                      None, amax)
+
+
+class MuonList:
+    """The matrices of a Muon step with their descriptors laid out once; the buffers stay the same from step to step (a
+    gradient's may be replaced by set_grad)."""
+
+    def __init__(self, tensors: Sequence[MuonTensor]):
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise ValueError("no tensors")
+        self.array = (nvfp4_muon_tensor * len(self.tensors))(*[t.c_struct() for t in self.tensors])
+        self.device = self.tensors[0].grad.get_device()
+        if any(t.grad.get_device() != self.device for t in self.tensors):
+            raise ValueError("the tensors are on several devices")
+        self.workspace_bytes = lib().nvfp4_muon_workspace_bytes(self.array, len(self.array))
+
+    def set_grad(self, index: int, grad):
+        t = self.tensors[index]
+        if grad.get_device() != self.device or grad.shape != t.grad.shape:
+            raise ValueError("grad: a tensor of shape %s on device %d is wanted" % (tuple(t.grad.shape), self.device))
+        old, t.grad = t.grad, grad
+        try:
+            self.array[index] = t.c_struct()
+        except Exception:
+            t.grad = old
+            raise
+
+    def new_workspace(self):
+        """A workspace of muon for these matrices (one per stream)."""
+        import torch
+        return torch.empty(self.workspace_bytes, dtype=torch.uint8, device="cuda:%d" % self.device)
+
+
+def muon(tensors, lr, momentum=0.95, nesterov=True, steps=5, coefficients=MUON_COEFFICIENTS, rounding="rtn", seed=0, step=0,
+         grad_scale=None, workspace=None, stream=None):
+    """One step of a MuonList, or of a sequence of MuonTensor: the momentum is updated, orthogonalised by `steps`
+    Newton-Schulz iterations and taken from the parameter (see include/nvfp4.h).  rounding (of bfloat16 params): "rtn", or
+    "sr" with uniforms by seed and step.  A workspace (the list's new_workspace) is allocated where none is given."""
+    if stream is not None and workspace is None:
+        with _on_stream(stream):
+            return muon(tensors, lr, momentum, nesterov, steps, coefficients, rounding, seed, step, grad_scale)
+    import torch
+    if not isinstance(tensors, MuonList):
+        tensors = MuonList(tensors)
+    if grad_scale is not None:
+        _vector(grad_scale, 1, tensors.device, "grad_scale", torch.float32)
+    if workspace is None:
+        workspace = tensors.new_workspace()
+    else:
+        _scratch(workspace, tensors.device)
+    a, b, c = coefficients
+    config = nvfp4_muon_config(lr, momentum, bool(nesterov), steps, a, b, c, ROUNDINGS.get(rounding, rounding), step, seed,
+                               _ptr(grad_scale))
+    _call("nvfp4_muon", tensors.device, tensors.array, len(tensors.array), config, _ptr(workspace), _nbytes(workspace),
+          _raw_stream(stream, tensors.device))
+
+
+def orthogonalize(x, steps=5, coefficients=MUON_COEFFICIENTS, stream=None):
+    """The orthogonalised bfloat16 form of a matrix (float32 or bfloat16), or of every matrix of a list, in one go."""
+    import torch
+    one = torch.is_tensor(x)
+    with _on_stream(stream):
+        xs = [t.contiguous() for t in ([x] if one else x)]
+        outs = [torch.empty_like(t, dtype=torch.bfloat16) for t in xs]
+        if xs:
+            muon([MuonTensor(None, t, update=o) for t, o in zip(xs, outs)], 0.0, 0.0, False, steps, coefficients)
+    return outs[0] if one else outs

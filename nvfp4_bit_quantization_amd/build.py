@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libnvfp4.so")
 SOURCES = ["quantize.hip", "gemm.hip", "mxfp4.hip", "api.cpp", "norm.hip", "adamw.hip", "attention.hip", "train_api.cpp",
-           "rope.hip", "gated.hip", "block_api.cpp"]
+           "rope.hip", "gated.hip", "muon.hip", "block_api.cpp"]
 ARCH = "gfx950"
 
 FLAGS = [

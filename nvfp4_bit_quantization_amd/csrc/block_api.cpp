@@ -186,6 +186,169 @@ GatedArgs gated_args(const nvfp4_tensor *a, const nvfp4_tensor *b, int32_t activ
 
 unsigned int *bits(float *p) { return reinterpret_cast<unsigned int *>(p); }
 
+// ---------------------------------------------------------------- muon ----
+int check_muon(const nvfp4_muon_tensor &t, bool buffers) {
+  const int64_t side = (int64_t)1 << 17;
+  if (t.rows < 0 || t.rows > side || t.cols < 0 || t.cols > side || t.rows * t.cols > ((int64_t)1 << 33)) return NVFP4_E_SHAPE;
+  if (!dtype_ok(t.param_dtype) || !dtype_ok(t.grad_dtype)) return NVFP4_E_UNSUPPORTED;
+  if (!buffers) return NVFP4_OK;
+  if (!(t.weight_decay >= 0.0f) || !isfinite(t.weight_decay) || !isfinite(t.scale)) return NVFP4_E_VALUE;
+  if (!t.param && (t.copy || t.amax)) return NVFP4_E_UNSUPPORTED;
+  if (!t.rows || !t.cols) return NVFP4_OK;
+  if (!t.grad || (!t.param && !t.update)) return NVFP4_E_NULL;
+  if (!aligned(t.grad, size_of(t.grad_dtype)) || !aligned(t.param, size_of(t.param_dtype)) || !aligned(t.m, 4) ||
+      !aligned(t.copy, 2) || !aligned(t.update, 2) || !aligned(t.amax, 4))
+    return NVFP4_E_ALIGN;
+  // all of a gradient is read before a parameter, copy or update is written, but not before the momentum
+  if (t.m && (t.m == t.grad || t.m == t.param || t.m == t.copy || t.m == t.update)) return NVFP4_E_UNSUPPORTED;
+  if (t.param && (t.param == t.copy || t.param == t.update)) return NVFP4_E_UNSUPPORTED;
+  if (t.update && t.update == t.copy) return NVFP4_E_UNSUPPORTED;
+  return NVFP4_OK;
+}
+
+// Whether the iteration's singular values, from [0, 1], stay where fp16 holds its
+// matrices: s p(s^2) is extreme at the ends and where its derivative vanishes,
+// p(s^2) at the ends and at s^2 = -b / 2 c.
+bool muon_bounded(const nvfp4_muon_config &c) {
+  const auto p = [&](double q) { return c.a + q * (c.b + q * c.c); };
+  double top = 1.0;
+  for (int k = 0; k < c.steps; ++k) {
+    double next = 0.0;
+    const auto look = [&](double q, bool turn) {
+      if (!(q >= 0.0 && q <= top * top)) return true;
+      if (!turn) next = fmax(next, sqrt(q) * fabs(p(q)));
+      return fabs(p(q)) <= 14.0;
+    };
+    bool good = look(0.0, false) && look(top * top, false);
+    if (c.c != 0.0) {
+      const double d = 9.0 * c.b * c.b - 20.0 * c.a * c.c;
+      if (d >= 0.0) good = good && look((-3.0 * c.b - sqrt(d)) / (10.0 * c.c), false) && look((-3.0 * c.b + sqrt(d)) / (10.0 * c.c), false);
+      good = good && look(-c.b / (2.0 * c.c), true);
+    } else if (c.b != 0.0) {
+      good = good && look(-c.a / (3.0 * c.b), false);
+    }
+    if (!good || !(next <= 3.5)) return false;
+    top = next;
+  }
+  return true;
+}
+
+int64_t round_up(int64_t n, int64_t by) { return (n + by - 1) / by * by; }
+
+// rows and columns of a workgroup's tiles of this matrix
+int muon_tile(const nvfp4_muon_tensor &t) {
+  const int64_t m = t.rows < t.cols ? t.rows : t.cols;
+  return m >= 1536 ? 256 : m >= 512 ? 128 : 64;
+}
+
+// The matrices [first, last) of the list that have one tile size, those of a group:
+// as many as a launch takes, or whose last product has eight rounds of tiles.
+// `bytes` of workspace are counted; with a base it is dealt out.
+struct MuonGroup {
+  int64_t index[kMuonMats];
+  int count = 0;
+  int64_t next = 0;  // where to go on in the list
+};
+MuonGroup muon_group(const nvfp4_muon_tensor *tensors, int64_t n, int64_t from, int tile) {
+  MuonGroup g;
+  int64_t tiles = 0, i = from;
+  for (; i < n && g.count < kMuonMats && tiles < 2048; ++i) {
+    const nvfp4_muon_tensor &t = tensors[i];
+    if (!t.rows || !t.cols || muon_tile(t) != tile) continue;
+    g.index[g.count++] = i;
+    tiles += (t.rows + tile - 1) / tile * ((t.cols + tile - 1) / tile);
+  }
+  g.next = i;
+  return g;
+}
+struct MuonBuffers {
+  double *parts;
+  _Float16 *x, *xt[2], *a, *b;
+};
+size_t muon_buffers(const nvfp4_muon_tensor &t, int tile, char *base, size_t used, MuonBuffers &o) {
+  const int64_t m = round_up(t.rows < t.cols ? t.rows : t.cols, tile), n = round_up(t.rows < t.cols ? t.cols : t.rows, tile);
+  const auto take = [&](size_t bytes) {
+    char *p = base ? base + used : nullptr;
+    used += (bytes + 255) & ~(size_t)255;
+    return p;
+  };
+  o.parts = (double *)take(kMuonParts * sizeof(double));
+  o.x = (_Float16 *)take((size_t)(m * n) * 2);
+  o.xt[0] = (_Float16 *)take((size_t)(m * n) * 2);
+  o.xt[1] = (_Float16 *)take((size_t)(m * n) * 2);
+  o.a = (_Float16 *)take((size_t)(m * m) * 2);
+  o.b = (_Float16 *)take((size_t)(m * m) * 2);
+  return used;
+}
+constexpr int kTiles[3] = {256, 128, 64};
+
+hipError_t muon_run(const nvfp4_muon_tensor *tensors, const MuonGroup &g, int tile, const nvfp4_muon_config &c, MuonArgs &a,
+                    char *base, hipStream_t s) {
+  MuonBuffers buf[kMuonMats];
+  size_t used = 0;
+  uint32_t sums = 0, forms = 0, updates = 0;
+  for (int i = 0; i < g.count; ++i) {
+    const nvfp4_muon_tensor &t = tensors[g.index[i]];
+    used = muon_buffers(t, tile, base, used, buf[i]);
+    const bool turned = t.rows > t.cols;
+    const int64_t n = t.rows * t.cols, chunks = (n + kMuonChunk - 1) / kMuonChunk;
+    MuonMat &d = a.mat[i];
+    d.grad = t.grad;
+    d.m = t.m;
+    d.param = t.param;
+    d.copy = (uint16_t *)t.copy;
+    d.update = (uint16_t *)t.update;
+    d.amax = t.amax;
+    d.direct = turned ? buf[i].xt[0] : buf[i].x;
+    d.turned = turned ? buf[i].x : buf[i].xt[0];
+    d.parts = buf[i].parts;
+    d.rows = (int)t.rows;
+    d.cols = (int)t.cols;
+    d.rp = (int)round_up(t.rows, tile);
+    d.cp = (int)round_up(t.cols, tile);
+    d.keep = (float)(1.0 - (double)c.lr * t.weight_decay);
+    d.step = (float)((double)c.lr * t.scale);
+    d.flags = (t.param_dtype == NVFP4_BF16 ? MF_PARAM_BF16 : 0u) | (t.grad_dtype == NVFP4_BF16 ? MF_GRAD_BF16 : 0u) |
+              (turned ? MF_TURNED : 0u);
+    d.index = (uint32_t)g.index[i];
+    d.sums = (uint32_t)(chunks < kMuonParts ? chunks : kMuonParts);
+    d.sum_end = sums += d.sums;
+    d.tile_end = forms += (uint32_t)(d.rp / 64) * (uint32_t)(d.cp / 64);
+    d.update_end = updates += (uint32_t)chunks;
+  }
+  a.count = g.count;
+  hipError_t e = launch_muon_sums(a, s);
+  if (e == hipSuccess) e = launch_muon_form(a, s);
+  const double kx = kMuonX, ka = kMuonA;
+  for (int k = 0; k < c.steps && e == hipSuccess; ++k) {
+    NsArgs p = {};
+    p.count = g.count;
+    for (int stage = 0; stage < 3 && e == hipSuccess; ++stage) {
+      for (int i = 0; i < g.count; ++i) {
+        const MuonMat &t = a.mat[i];
+        const bool turned = t.flags & MF_TURNED, last = k + 1 == c.steps;
+        const int m = turned ? t.cp : t.rp, n = turned ? t.rp : t.cp;
+        NsMat &o = p.mat[i];
+        const MuonBuffers &b = buf[i];
+        if (stage == 0)
+          o = {b.x, b.x, nullptr, b.a, b.a, m, m, n, 0};
+        else if (stage == 1)
+          o = {b.a, b.a, b.a, b.b, b.b, m, m, m, 0};
+        else
+          o = {b.b, b.xt[k & 1], nullptr, last && turned ? nullptr : b.x, last && !turned ? nullptr : b.xt[~k & 1], m, n, m, 0};
+      }
+      p.symmetric = stage < 2;
+      p.alpha = (float)(stage == 0 ? ka / (kx * kx) : stage == 1 ? c.c / ka : 1.0 / ka);
+      p.beta = (float)c.b;
+      p.gamma = (float)(c.a * ka);
+      e = launch_muon_product(p, tile, s);
+    }
+  }
+  for (int i = 0; i < g.count; ++i)
+    if (a.mat[i].flags & MF_TURNED) a.mat[i].direct = buf[i].xt[c.steps & 1];
+  return e == hipSuccess ? launch_muon_update(a, s) : e;
+}
+
 }  // namespace
 
 extern "C" {
@@ -268,6 +431,58 @@ int nvfp4_gemm_gated_backward(const nvfp4_tensor *a, const nvfp4_tensor *b, int3
   r.amax[1] = bits(dup->amax_plain), r.rht[1] = bits(dup->amax_rht_col);
   hipStream_t s = (hipStream_t)stream;
   return finish(launch_gemm_gated_backward(r, s), s);
+}
+
+size_t nvfp4_muon_workspace_bytes(const nvfp4_muon_tensor *tensors, int64_t n_tensors) {
+  if (!tensors || n_tensors < 1 || n_tensors >= ((int64_t)1 << 30)) return 0;
+  for (int64_t i = 0; i < n_tensors; ++i)
+    if (check_muon(tensors[i], false) != NVFP4_OK) return 0;
+  size_t most = 0;
+  for (const int tile : kTiles)
+    for (int64_t at = 0; at < n_tensors;) {
+      const MuonGroup g = muon_group(tensors, n_tensors, at, tile);
+      size_t used = 0;
+      MuonBuffers b;
+      for (int i = 0; i < g.count; ++i) used = muon_buffers(tensors[g.index[i]], tile, nullptr, used, b);
+      if (used > most) most = used;
+      at = g.next;
+    }
+  return most;
+}
+
+int nvfp4_muon(const nvfp4_muon_tensor *tensors, int64_t n_tensors, const nvfp4_muon_config *c, void *workspace,
+               size_t workspace_bytes, void *stream) {
+  if (!tensors || !c) return NVFP4_E_NULL;
+  if (n_tensors < 1 || n_tensors >= ((int64_t)1 << 30)) return NVFP4_E_SHAPE;
+  if ((c->rounding != NVFP4_RTN && c->rounding != NVFP4_SR) || (c->nesterov != 0 && c->nesterov != 1)) return NVFP4_E_UNSUPPORTED;
+  if (!(c->lr >= 0.0f) || !isfinite(c->lr) || !(c->momentum >= 0.0 && c->momentum < 1.0) || c->steps < 1 || c->steps > 16 ||
+      c->step < 0 || c->step >= ((int64_t)1 << 47) || !isfinite(c->a) || !isfinite(c->b) || !isfinite(c->c) || !muon_bounded(*c))
+    return NVFP4_E_VALUE;
+  if (!aligned(c->grad_scale, 4)) return NVFP4_E_ALIGN;
+  for (int64_t i = 0; i < n_tensors; ++i)
+    if (const int st = check_muon(tensors[i], true)) return st;
+  const size_t need = nvfp4_muon_workspace_bytes(tensors, n_tensors);
+  if (need && (!workspace || workspace_bytes < need)) return NVFP4_E_WORKSPACE;
+  if (need && !aligned(workspace, 16)) return NVFP4_E_ALIGN;
+
+  MuonArgs a = {};
+  a.sr = c->rounding == NVFP4_SR;
+  a.nesterov = c->nesterov;
+  a.beta = (float)c->momentum;
+  a.one_minus_beta = (float)(1.0 - c->momentum);
+  a.seed_lo = (uint32_t)c->seed;
+  a.seed_hi = (uint32_t)(c->seed >> 32);
+  a.step_lo = (uint32_t)c->step;
+  a.tag = 0x4D550000u + (uint32_t)(c->step >> 32);
+  a.grad_scale = c->grad_scale;
+  hipStream_t s = (hipStream_t)stream;
+  for (const int tile : kTiles)
+    for (int64_t at = 0; at < n_tensors;) {
+      const MuonGroup g = muon_group(tensors, n_tensors, at, tile);
+      at = g.next;
+      if (g.count && muon_run(tensors, g, tile, *c, a, (char *)workspace, s) != hipSuccess) return NVFP4_E_HIP;
+    }
+  return finish(hipSuccess, s);
 }
 
 }  // extern "C"

@@ -62,4 +62,58 @@ struct GatedArgs {
 hipError_t launch_gemm_gated(const GatedArgs &a, hipStream_t s);
 hipError_t launch_gemm_gated_backward(const GatedArgs &a, hipStream_t s);
 
+// ---------------------------------------------------------------- muon ----
+// Matrices are worked on as m x n with m <= n ("turned" ones have more rows than
+// columns), padded with zeros to whole tiles, in fp16 times a power of two.
+constexpr float kMuonX = 1024.0f;  // of the iterate, whose singular values stay below 4
+constexpr float kMuonA = 2048.0f;  // of its square and of the polynomial in it, below 16
+constexpr int kMuonMats = 30;      // of one launch: what 4 KiB of arguments hold
+constexpr int kMuonChunk = 8192;   // elements of a workgroup of the sums and of the update
+constexpr int kMuonParts = 512;    // workgroups of a matrix's sum, at most
+
+enum MuonFlags : uint32_t { MF_PARAM_BF16 = 1, MF_GRAD_BF16 = 2, MF_TURNED = 4 };
+
+struct MuonMat {
+  const void *grad;
+  float *m;
+  void *param;
+  uint16_t *copy, *update;
+  float *amax;
+  _Float16 *direct, *turned;  // [rp][cp] as the tensor stands, and [cp][rp]
+  double *parts;
+  int rows, cols, rp, cp;     // the tensor's, and padded
+  float keep, step;           // 1 - lr * weight_decay, lr * scale
+  uint32_t flags, index;
+  uint32_t sum_end, tile_end, update_end;  // workgroups of this and the earlier matrices of the launches
+  uint32_t sums;                           // workgroups of this one's sum
+};
+struct MuonArgs {
+  MuonMat mat[kMuonMats];
+  int count, sr, nesterov;
+  float beta, one_minus_beta;
+  uint32_t seed_lo, seed_hi, step_lo, tag;
+  const float *grad_scale;
+};
+static_assert(sizeof(MuonMat) == 120 && sizeof(MuonArgs) <= 4096, "kernel arguments");
+
+// D = alpha P Q^T + beta E + gamma I of every matrix, P [M][K], Q [N][K], D and E
+// [M][N], DT [N][M]; D or DT may be null.  Symmetric: P = Q and D = DT, and only
+// tiles on and below the diagonal are formed.
+struct NsMat {
+  const _Float16 *p, *q, *e;
+  _Float16 *d, *dt;
+  int M, N, K;
+  uint32_t end;  // tiles of this and the earlier matrices
+};
+struct NsArgs {
+  NsMat mat[kMuonMats];
+  int count, symmetric;
+  float alpha, beta, gamma;
+};
+hipError_t launch_muon_sums(const MuonArgs &a, hipStream_t s);
+hipError_t launch_muon_form(const MuonArgs &a, hipStream_t s);
+// tile: 64, 128 or 256 rows and columns of a workgroup; fills the ends
+hipError_t launch_muon_product(NsArgs &a, int tile, hipStream_t s);
+hipError_t launch_muon_update(const MuonArgs &a, hipStream_t s);
+
 }  // namespace nvfp4

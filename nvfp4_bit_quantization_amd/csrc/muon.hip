@@ -1,0 +1,423 @@
+// Steps of matrices by orthogonalised updates (include/nvfp4.h: nvfp4_muon).
+//
+// The iterate is X <- (a I + b A + c A^2) X with A = X X^T, three products of
+// which two are symmetric: of those only tiles on and below the diagonal are
+// formed, and stored twice.  The polynomial takes a I in, so that the third
+// product needs nothing but its operands.  All products are "TN" (both operands
+// contiguous in K), for which X is kept as it is and transposed: the epilogue
+// writes both.
+//
+// Operands are fp16, sums binary32.  Against the definition in 64 bits the
+// result is off by 1.2e-3 to 2e-3 of its norm, by rounding X, A and the
+// polynomial to 11 bits five times; bf16, the usual choice, is off by 8 times
+// that.  Powers of two keep the values in fp16's normal range (kMuonX, kMuonA).
+#include "block_kernels.hpp"
+#include "gemm_device.hpp"
+#include "train_device.hpp"
+
+namespace nvfp4 {
+namespace {
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// ------------------------------------------------------------- products ----
+// Tiles of 64 T x 64 T by four waves, 2 x 2 of them, T x T blocks of 32 x 32 to a
+// wave; K-tiles of 32 (64 bytes of a row, in four chunks permuted within it) in
+// four LDS stages filled by direct transfers three K-tiles ahead.
+constexpr int kStages = 4;
+template <int T>
+struct Ns {
+  static constexpr int kTile = 64 * T;
+  static constexpr int kStageBytes = 2 * kTile * 64;
+  static constexpr int kMoves = 2 * T;                 // transfers of a wave to a stage
+  static constexpr int kStride = 32 * T + 8;           // floats between rows of an epilogue slab
+  static constexpr int kSlab = 32 * kStride;
+  static constexpr int kLds = kStages * kStageBytes;
+  static_assert(4 * kSlab * 4 <= kLds, "the epilogue's slabs");
+};
+
+template <int T>
+struct NsFrags {
+  half8 a[T], b[T];
+};
+template <int T>
+__device__ __forceinline__ void read_frags(NsFrags<T> &f, const uint8_t *stage, const uint32_t at[2 * T]) {
+#pragma unroll
+  for (int i = 0; i < T; ++i) f.a[i] = *reinterpret_cast<const half8 *>(stage + at[i]);
+#pragma unroll
+  for (int i = 0; i < T; ++i) f.b[i] = *reinterpret_cast<const half8 *>(stage + at[T + i]);
+}
+template <int T>
+__device__ __forceinline__ void multiply(f32x16 acc[T][T], const NsFrags<T> &f) {
+#pragma unroll
+  for (int i = 0; i < T; ++i)
+#pragma unroll
+    for (int j = 0; j < T; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+}
+
+__device__ __forceinline__ void slab_fence() { asm volatile("" ::: "memory"); }
+
+// 32 rows of `row0` onwards, 32 T columns of `col0` onwards of the result, from a
+// slab of them
+template <int T>
+__device__ __forceinline__ void store_rows(const NsArgs &a, _Float16 *d, const _Float16 *e, int64_t ld, int64_t row0, int64_t col0,
+                                           const float *slab, uint32_t lane) {
+  constexpr int LANES = 4 * T, ROWS = 64 / LANES;
+  const int c = lane % LANES * 8;
+#pragma unroll 2
+  for (int r = lane / LANES; r < 32; r += ROWS) {
+    const int64_t at = (row0 + r) * ld + col0 + c;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = a.alpha * slab[r * Ns<T>::kStride + c + k];
+    if (e) {
+      const half8 x = *reinterpret_cast<const half8 *>(e + at);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] = fmaf(a.beta, (float)x[k], v[k]);
+        if (row0 + r == col0 + c + k) v[k] += a.gamma;
+      }
+    }
+    half8 y;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = (_Float16)v[k];
+    *reinterpret_cast<half8 *>(d + at) = y;
+  }
+}
+
+template <int T>
+__global__ __launch_bounds__(256, T == 4 ? 1 : 2) void ns_product_kernel(NsArgs a) {
+  using N = Ns<T>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[N::kLds];
+  // the matrix and the tile
+  uint32_t tile = xcd_tile(blockIdx.x, gridDim.x);
+  int which = 0;
+  while (tile >= a.mat[which].end) ++which;
+  const NsMat &t = a.mat[which];
+  if (which) tile -= a.mat[which - 1].end;
+  int64_t m0, n0;
+  if (a.symmetric) {  // tile = I (I + 1) / 2 + J, J <= I
+    uint32_t i = (uint32_t)((sqrtf(8.0f * (float)tile + 1.0f) - 1.0f) * 0.5f);
+    while (i * (i + 1) / 2 > tile) --i;
+    while ((i + 1) * (i + 2) / 2 <= tile) ++i;
+    m0 = (int64_t)i * N::kTile;
+    n0 = (int64_t)(tile - i * (i + 1) / 2) * N::kTile;
+  } else {
+    const uint32_t tiles_m = t.M / N::kTile, tiles_n = t.N / N::kTile;
+    const uint32_t group = tile / (kGroupM * tiles_n), first_m = group * kGroupM;
+    const uint32_t gm = tiles_m - first_m < kGroupM ? tiles_m - first_m : kGroupM;
+    const uint32_t local = tile - group * kGroupM * tiles_n;
+    m0 = (int64_t)(first_m + local % gm) * N::kTile;
+    n0 = (int64_t)(local / gm) * N::kTile;
+  }
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const uint32_t wm = wave >> 1, wn = wave & 1, lr = lane & 31, h = lane >> 5;
+
+  // transfers: waves 0 and 1 fill the rows of P, 2 and 3 those of Q
+  const uint8_t *base = reinterpret_cast<const uint8_t *>(wave < 2 ? t.p + m0 * t.K : t.q + n0 * t.K);
+  uint32_t off[N::kMoves];
+#pragma unroll
+  for (int i = 0; i < N::kMoves; ++i) {
+    const uint32_t q = (wave * N::kMoves + i) * 64 + lane, row = q >> 2;
+    off[i] = (row % N::kTile) * (uint32_t)(t.K * 2) + ((q & 3u) ^ swz(row)) * 16u;
+  }
+  // fragments: lane half h takes chunk 2 s + h of its row in sub-step s
+  uint32_t at0[2 * T], at1[2 * T];
+#pragma unroll
+  for (int i = 0; i < T; ++i) {
+    const uint32_t ra = wm * (32 * T) + i * 32 + lr, rb = N::kTile + wn * (32 * T) + i * 32 + lr;
+    at0[i] = (ra * 4 + (h ^ swz(ra))) * 16;
+    at1[i] = (ra * 4 + ((2 + h) ^ swz(ra))) * 16;
+    at0[T + i] = (rb * 4 + (h ^ swz(rb))) * 16;
+    at1[T + i] = (rb * 4 + ((2 + h) ^ swz(rb))) * 16;
+  }
+  f32x16 acc[T][T];
+#pragma unroll
+  for (int i = 0; i < T; ++i)
+#pragma unroll
+    for (int j = 0; j < T; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  const uint32_t lds0 = lds_addr(lds), KT = (uint32_t)(t.K / 32), last = KT - 1;
+  const auto issue = [&](uint32_t kt, uint32_t stage) {  // past the end: the last K-tile again, into a stage nobody reads
+    const uint8_t *b = uniform_ptr(base + (uint64_t)(kt < last ? kt : last) * 64u);
+#pragma unroll
+    for (int i = 0; i < N::kMoves; ++i)
+      dma16(b, off[i], __builtin_amdgcn_readfirstlane(lds0 + stage * N::kStageBytes + (wave * N::kMoves + i) * 1024u));
+  };
+  issue(0, 0);
+  issue(1, 1);
+  issue(2, 2);
+  NVFP4_WAIT_VMCNT(2 * N::kMoves);  // this wave's part of K-tile 0 is in LDS
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  NsFrags<T> f, g;
+  read_frags<T>(f, lds, at0);
+  for (uint32_t kt = 0; kt < KT; ++kt) {
+    const uint8_t *stage = lds + (kt & 3u) * N::kStageBytes;
+    read_frags<T>(g, stage, at1);
+    issue(kt + 3, (kt + 3) & 3u);  // its stage was read before the last barrier
+    multiply<T>(acc, f);
+    __builtin_amdgcn_sched_barrier(0);
+    NVFP4_WAIT_LGKM0();               // this wave's reads of the stage are complete
+    NVFP4_WAIT_VMCNT(2 * N::kMoves);  // its part of K-tile kt + 1 is in LDS
+    __builtin_amdgcn_s_barrier();     // every wave's
+    asm volatile("" ::: "memory");
+    read_frags<T>(f, lds + ((kt + 1) & 3u) * N::kStageBytes, at0);  // after the last K-tile: not used
+    multiply<T>(acc, g);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  NVFP4_WAIT_VMCNT(0);
+  __syncthreads();  // no wave reads the stages, and no transfer writes them, any more
+
+  float *slab = reinterpret_cast<float *>(lds) + wave * N::kSlab;
+  const int64_t mw = m0 + wm * (32 * T), nw = n0 + wn * (32 * T);
+  if (t.d) {
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+#pragma unroll
+      for (int j = 0; j < T; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) slab[((r >> 2) * 8 + h * 4 + (r & 3)) * N::kStride + j * 32 + lr] = acc[i][j][r];
+      slab_fence();
+      store_rows<T>(a, t.d, t.e, t.N, mw + i * 32, nw, slab, lane);
+      slab_fence();
+    }
+  }
+  if (t.dt && !(a.symmetric && m0 == n0)) {
+#pragma unroll
+    for (int j = 0; j < T; ++j) {
+#pragma unroll
+      for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<f32x4 *>(&slab[lr * N::kStride + i * 32 + q * 8 + h * 4]) =
+              (f32x4){acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+      slab_fence();
+      store_rows<T>(a, t.dt, t.e, t.M, nw + j * 32, mw, slab, lane);
+      slab_fence();
+    }
+  }
+}
+
+// ---------------------------------------------------------- elementwise ----
+// the matrix of a workgroup, and its number within it
+template <typename End>
+__device__ __forceinline__ const MuonMat &mat_of(const MuonArgs &a, uint32_t &group, End end) {
+  int which = 0;
+  while (group >= end(a.mat[which])) ++which;
+  if (which) group -= end(a.mat[which - 1]);
+  return a.mat[which];
+}
+
+// up to 8 elements from p, zero past `n`
+template <typename T>
+__device__ __forceinline__ void load_some(const T *p, int64_t n, float v[8]) {
+  if (n >= 8) {
+    load8(p, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? load1(p + j) : 0.0f;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_some(T *p, int64_t n, const float v[8]) {
+  if (n >= 8) {
+    store8(p, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < n) store1(p + j, v[j]);
+  }
+}
+__device__ __forceinline__ void load_grad(const MuonMat &t, int64_t i, int64_t n, float scale, float g[8]) {
+  if (t.flags & MF_GRAD_BF16)
+    load_some((const uint16_t *)t.grad + i, n, g);
+  else
+    load_some((const float *)t.grad + i, n, g);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) g[j] *= scale;
+}
+// the update's direction from the gradient and the new momentum
+__device__ __forceinline__ float direction(const MuonArgs &a, float g, float m) {
+  return a.nesterov ? fmaf(a.beta, m, a.one_minus_beta * g) : m;
+}
+
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  return v;
+}
+
+// the new momentum, and the sum of squares of the direction by workgroup
+__global__ __launch_bounds__(256) void muon_sums_kernel(MuonArgs a) {
+  uint32_t group = blockIdx.x;
+  const MuonMat &t = mat_of(a, group, [](const MuonMat &x) { return x.sum_end; });
+  const int64_t n = (int64_t)t.rows * t.cols;
+  const float scale = a.grad_scale ? *a.grad_scale : 1.0f;
+  double sum = 0.0;
+  for (int64_t i = ((int64_t)group * 256 + threadIdx.x) * 8; i < n; i += (int64_t)t.sums * 2048) {
+    float g[8];
+    load_grad(t, i, n - i, scale, g);
+    if (t.m) {
+      float m[8];
+      load_some(t.m + i, n - i, m);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m[j] = fmaf(a.beta, m[j], a.one_minus_beta * g[j]);
+        g[j] = direction(a, g[j], m[j]);
+      }
+      store_some(t.m + i, n - i, m);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fma((double)g[j], (double)g[j], sum);
+  }
+  __shared__ double sums[4];
+  sum = wave_sum64(sum);
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) t.parts[group] = sums[0] + sums[1] + sums[2] + sums[3];
+}
+
+// X and its transpose in fp16, 64 x 64 elements to a workgroup, zeros beyond the tensor
+__global__ __launch_bounds__(256) void muon_form_kernel(MuonArgs a) {
+  uint32_t group = blockIdx.x;
+  const MuonMat &t = mat_of(a, group, [](const MuonMat &x) { return x.tile_end; });
+  __shared__ double sums[4];
+  __shared__ __attribute__((aligned(16))) _Float16 tile[64][72];
+  double sum = 0.0;
+  for (uint32_t i = threadIdx.x; i < t.sums; i += 256) sum += t.parts[i];
+  sum = wave_sum64(sum);
+  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  sum = sums[0] + sums[1] + sums[2] + sums[3];
+  const double by = sum > 0.0 ? (double)kMuonX / sqrt(sum) : 0.0;
+  const float scale = a.grad_scale ? *a.grad_scale : 1.0f;
+  const uint32_t across = t.cp / 64;
+  const int r0 = (int)(group / across) * 64, c0 = (int)(group % across) * 64;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = (threadIdx.x >> 3) + 32 * k, c = (threadIdx.x & 7) * 8;
+    const int n = r0 + r < t.rows ? t.cols - (c0 + c) : 0;
+    const int64_t i = (int64_t)(r0 + r) * t.cols + c0 + c;
+    half8 x = (half8)(_Float16)0.0f;
+    if (n > 0) {
+      float g[8], m[8];
+      if (t.m) {
+        load_some(t.m + i, n, m);
+        if (a.nesterov) load_grad(t, i, n, scale, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = direction(a, g[j], m[j]);
+      } else {
+        load_grad(t, i, n, scale, g);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) x[j] = (_Float16)(float)((double)g[j] * by);
+    }
+    *reinterpret_cast<half8 *>(t.direct + (int64_t)(r0 + r) * t.cp + c0 + c) = x;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) tile[c + j][r] = x[j];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = (threadIdx.x >> 3) + 32 * k, c = (threadIdx.x & 7) * 8;
+    *reinterpret_cast<half8 *>(t.turned + (int64_t)(c0 + r) * t.rp + r0 + c) = *reinterpret_cast<const half8 *>(&tile[r][c]);
+  }
+}
+
+// what the last product left, as update and applied to the parameter
+__global__ __launch_bounds__(256) void muon_update_kernel(MuonArgs a) {
+  uint32_t group = blockIdx.x;
+  const MuonMat &t = mat_of(a, group, [](const MuonMat &x) { return x.update_end; });
+  const int64_t n = (int64_t)t.rows * t.cols, start = (int64_t)group * kMuonChunk;
+  const int64_t row0 = start / t.cols;
+  const uint32_t col0 = (uint32_t)(start - row0 * t.cols);
+  float top = 0.0f;
+#pragma unroll 2
+  for (uint32_t o = threadIdx.x * 8; o < kMuonChunk; o += 2048) {
+    const int64_t i = start + o;
+    if (i >= n) break;
+    const uint32_t down = (col0 + o) / (uint32_t)t.cols;
+    uint32_t c = col0 + o - down * t.cols;
+    const _Float16 *x = t.direct + (row0 + down) * t.cp;
+    float u[8];
+    if (c + 8 <= (uint32_t)t.cols) {
+      typedef half8 __attribute__((aligned(2))) half8_at2;
+      const half8 q = *reinterpret_cast<const half8_at2 *>(x + c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = (float)q[j] * (1.0f / kMuonX);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        u[j] = i + j < n ? (float)x[c] * (1.0f / kMuonX) : 0.0f;
+        if (++c == (uint32_t)t.cols) {
+          c = 0;
+          x += t.cp;
+        }
+      }
+    }
+    if (t.update) store_some(t.update + i, n - i, u);
+    if (!t.param) continue;
+    float p[8];
+    if (t.flags & MF_PARAM_BF16)
+      load_some((const uint16_t *)t.param + i, n - i, p);
+    else
+      load_some((const float *)t.param + i, n - i, p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = fmaf(-t.step, u[j], p[j] * t.keep);
+    if (t.flags & MF_PARAM_BF16) {
+      if (a.sr) {
+        uint32_t w[4] = {(uint32_t)(i >> 3), t.index, a.step_lo, a.tag};
+        philox4x32_10(a.seed_lo, a.seed_hi, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = __uint_as_float((__float_as_uint(p[j]) + u16_of(w, j)) & 0xFFFF0000u);
+      }
+      store_some((uint16_t *)t.param + i, n - i, p);
+    } else {
+      store_some((float *)t.param + i, n - i, p);
+    }
+    if (t.copy) store_some(t.copy + i, n - i, p);
+    if (t.amax) {
+      const bool rounds = t.copy || (t.flags & MF_PARAM_BF16);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n - i) top = fmaxf(top, fabsf(rounds ? round_bf16(p[j]) : p[j]));
+    }
+  }
+  if (t.amax) fold_max(t.amax, top);
+}
+
+}  // namespace
+
+hipError_t launch_muon_sums(const MuonArgs &a, hipStream_t s) {
+  hipLaunchKernelGGL(muon_sums_kernel, dim3(a.mat[a.count - 1].sum_end), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+hipError_t launch_muon_form(const MuonArgs &a, hipStream_t s) {
+  hipLaunchKernelGGL(muon_form_kernel, dim3(a.mat[a.count - 1].tile_end), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+hipError_t launch_muon_update(const MuonArgs &a, hipStream_t s) {
+  hipLaunchKernelGGL(muon_update_kernel, dim3(a.mat[a.count - 1].update_end), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+hipError_t launch_muon_product(NsArgs &a, int tile, hipStream_t s) {
+  uint32_t end = 0;
+  for (int i = 0; i < a.count; ++i) {
+    const uint32_t m = a.mat[i].M / tile, n = a.mat[i].N / tile;
+    a.mat[i].end = end += a.symmetric ? m * (m + 1) / 2 : m * n;
+  }
+  if (tile == 256)
+    hipLaunchKernelGGL((ns_product_kernel<4>), dim3(end), dim3(256), 0, s, a);
+  else if (tile == 128)
+    hipLaunchKernelGGL((ns_product_kernel<2>), dim3(end), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((ns_product_kernel<1>), dim3(end), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

@@ -209,3 +209,92 @@ def test_gated_outputs_stand_apart(L):
     for out in ("dgate", "dup"):
         for place in (3, 4):
             assert _gated_back(L, **{out: _matrix(place, ld=128)}) == UNSUPPORTED
+
+
+def _muon_tensor(**kw):
+    a = dict(param=FAKE * 2, grad=FAKE * 3, m=FAKE * 4, copy=FAKE * 5, update=FAKE * 6, amax=FAKE * 7, rows=40, cols=64,
+             param_dtype=0, grad_dtype=1, weight_decay=0.1, scale=1.0)
+    a.update(kw)
+    return nv.nvfp4_muon_tensor(**a)
+
+
+def _muon_config(**kw):
+    a = dict(lr=0.01, momentum=0.95, nesterov=1, steps=5, a=3.4445, b=-4.775, c=2.0315, rounding=0, step=1, seed=0, grad_scale=None)
+    a.update(kw)
+    return nv.nvfp4_muon_config(**a)
+
+
+def _muon(L, tensors, config, ws=FAKE, nbytes=1 << 40):
+    arr = (nv.nvfp4_muon_tensor * len(tensors))(*tensors)
+    return L.nvfp4_muon(arr, len(tensors), ctypes.byref(config), ws, nbytes, None)
+
+
+NAN, INF = float("nan"), float("inf")
+MUON = [(dict(rows=-1), SHAPE), (dict(cols=-1), SHAPE), (dict(rows=(1 << 17) + 1), SHAPE), (dict(rows=1 << 17, cols=(1 << 16) + 1), SHAPE),
+        (dict(param_dtype=2), UNSUPPORTED), (dict(grad_dtype=-1), UNSUPPORTED), (dict(weight_decay=-0.1), VALUE),
+        (dict(weight_decay=NAN), VALUE), (dict(scale=INF), VALUE), (dict(grad=None), NULL), (dict(param=None), UNSUPPORTED),
+        (dict(param=None, copy=None, amax=None, update=None), NULL), (dict(grad=FAKE + 1), ALIGN), (dict(param=FAKE + 2), ALIGN),
+        (dict(m=FAKE + 2), ALIGN), (dict(copy=FAKE + 1), ALIGN), (dict(update=FAKE + 1), ALIGN), (dict(amax=FAKE + 2), ALIGN),
+        (dict(m=FAKE * 3), UNSUPPORTED), (dict(m=FAKE * 2), UNSUPPORTED), (dict(copy=FAKE * 2), UNSUPPORTED),
+        (dict(update=FAKE * 5), UNSUPPORTED)]
+
+
+@pytest.mark.parametrize("change,status", MUON, ids=str)
+def test_muon_tensors(L, change, status):
+    assert _muon(L, [_muon_tensor(rows=0), _muon_tensor(**change)], _muon_config()) == status
+
+
+CONFIGS = [(dict(lr=-1.0), VALUE), (dict(lr=NAN), VALUE), (dict(momentum=1.0), VALUE), (dict(momentum=-0.1), VALUE),
+           (dict(nesterov=2), UNSUPPORTED), (dict(rounding=2), UNSUPPORTED), (dict(steps=0), VALUE), (dict(steps=17), VALUE),
+           (dict(step=-1), VALUE), (dict(step=1 << 47), VALUE), (dict(a=NAN), VALUE), (dict(a=4.0, b=0.0, c=0.0), VALUE),
+           (dict(a=-4.0, b=0.0, c=0.0), VALUE), (dict(c=9.0), VALUE), (dict(b=-40.0), VALUE), (dict(c=INF), VALUE),
+           (dict(a=15.0, b=-12.0, c=0.0), VALUE), (dict(grad_scale=FAKE + 2), ALIGN)]
+
+
+@pytest.mark.parametrize("change,status", CONFIGS, ids=str)
+def test_muon_configs(L, change, status):
+    assert _muon(L, [_muon_tensor()], _muon_config(**change)) == status
+
+
+@pytest.mark.parametrize("abc", [(3.4445, -4.775, 2.0315), (2.0, -1.5, 0.5), (1.5, -0.5, 0.0), (1.875, -1.25, 0.375), (1.0, 0.0, 0.0), (0.0, 0.0, 0.0)])
+def test_muon_iterations_that_stay_bounded(L, abc):
+    a, b, c = abc
+    for steps in (1, 5, 16):
+        assert _muon(L, [_muon_tensor(rows=0)], _muon_config(a=a, b=b, c=c, steps=steps)) == 0  # nothing to do
+
+
+def test_muon_bound_is_the_iterations_own(L):
+    """The refusal goes by the largest singular value that the iteration can reach, here found on a grid."""
+    import random
+    r = random.Random(4)
+    for _ in range(300):
+        a, b, c = r.uniform(-4, 4), r.uniform(-8, 8), r.uniform(-4, 4)
+        steps, top, high = r.randrange(1, 5), 1.0, 0.0
+        worst = 0.0
+        for _ in range(steps):
+            grid = [top * i / 2000 for i in range(2001)]
+            high = max(high, max(abs(a + b * s * s + c * s ** 4) for s in grid))
+            top = max(s * abs(a + b * s * s + c * s ** 4) for s in grid)
+            worst = max(worst, top)
+            if worst > 3.5 or high > 14:
+                break
+        if abs(worst - 3.5) < 0.01 or abs(high - 14) < 0.05:
+            continue  # the grid cannot say
+        want = VALUE if worst > 3.5 or high > 14 else 0
+        assert _muon(L, [_muon_tensor(rows=0)], _muon_config(a=a, b=b, c=c, steps=steps)) == want, (a, b, c, steps, worst, high)
+
+
+def test_muon_workspace(L):
+    t = [_muon_tensor(), _muon_tensor(rows=0), _muon_tensor(rows=2000, cols=1600, grad=FAKE * 9)]
+    arr = (nv.nvfp4_muon_tensor * 3)(*t)
+    need = L.nvfp4_muon_workspace_bytes(arr, 3)
+    assert need >= 2 * (3 * 2048 * 1792 + 2 * 1792 * 1792)  # three of the iterate, two of its square
+    c = _muon_config()
+    assert _muon(L, t, c, None, need) == WORKSPACE
+    assert _muon(L, t, c, FAKE, need - 1) == WORKSPACE
+    assert _muon(L, t, c, FAKE + 8, need) == ALIGN
+    assert L.nvfp4_muon_workspace_bytes(None, 1) == 0 and L.nvfp4_muon_workspace_bytes(arr, 0) == 0
+    assert L.nvfp4_muon_workspace_bytes((nv.nvfp4_muon_tensor * 1)(_muon_tensor(rows=0)), 1) == 0
+    assert L.nvfp4_muon(None, 1, ctypes.byref(c), FAKE, need, None) == NULL
+    assert L.nvfp4_muon(arr, 3, None, FAKE, need, None) == NULL
+    assert L.nvfp4_muon(arr, 0, ctypes.byref(c), FAKE, need, None) == SHAPE
