@@ -273,11 +273,11 @@ size_t muon_buffers(const nvfp4_muon_tensor &t, int tile, char *base, size_t use
     return p;
   };
   o.parts = (double *)take(kMuonParts * sizeof(double));
-  o.x = (_Float16 *)take((size_t)(m * n) * 2);
-  o.xt[0] = (_Float16 *)take((size_t)(m * n) * 2);
-  o.xt[1] = (_Float16 *)take((size_t)(m * n) * 2);
-  o.a = (_Float16 *)take((size_t)(m * m) * 2);
-  o.b = (_Float16 *)take((size_t)(m * m) * 2);
+  o.x = (_Float16 *)take((size_t)(m * muon_ld(n)) * 2);
+  o.xt[0] = (_Float16 *)take((size_t)(n * muon_ld(m)) * 2);
+  o.xt[1] = (_Float16 *)take((size_t)(n * muon_ld(m)) * 2);
+  o.a = (_Float16 *)take((size_t)(m * muon_ld(m)) * 2);
+  o.b = (_Float16 *)take((size_t)(m * muon_ld(m)) * 2);
   return used;
 }
 constexpr int kTiles[3] = {256, 128, 64};

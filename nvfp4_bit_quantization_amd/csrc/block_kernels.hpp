@@ -71,6 +71,11 @@ constexpr int kMuonMats = 30;      // of one launch: what 4 KiB of arguments hol
 constexpr int kMuonChunk = 8192;   // elements of a workgroup of the sums and of the update
 constexpr int kMuonParts = 512;    // workgroups of a matrix's sum, at most
 
+// Elements between the rows of a matrix of n columns (n a multiple of 64): an odd
+// number of 128-byte lines, so that a column of lines is spread over the channels
+// of the L2 and of memory.
+__host__ __device__ inline int64_t muon_ld(int64_t n) { return (n / 64 | 1) * 64; }
+
 enum MuonFlags : uint32_t { MF_PARAM_BF16 = 1, MF_GRAD_BF16 = 2, MF_TURNED = 4 };
 
 struct MuonMat {
@@ -79,7 +84,7 @@ struct MuonMat {
   void *param;
   uint16_t *copy, *update;
   float *amax;
-  _Float16 *direct, *turned;  // [rp][cp] as the tensor stands, and [cp][rp]
+  _Float16 *direct, *turned;  // [rp][cp] as the tensor stands, and [cp][rp] (rows muon_ld apart)
   double *parts;
   int rows, cols, rp, cp;     // the tensor's, and padded
   float keep, step;           // 1 - lr * weight_decay, lr * scale
@@ -97,7 +102,7 @@ struct MuonArgs {
 static_assert(sizeof(MuonMat) == 120 && sizeof(MuonArgs) <= 4096, "kernel arguments");
 
 // D = alpha P Q^T + beta E + gamma I of every matrix, P [M][K], Q [N][K], D and E
-// [M][N], DT [N][M]; D or DT may be null.  Symmetric: P = Q and D = DT, and only
+// [M][N], DT [N][M], rows muon_ld apart; D or DT may be null.  Symmetric: P = Q and D = DT, and only
 // tiles on and below the diagonal are formed.
 struct NsMat {
   const _Float16 *p, *q, *e;

@@ -23,17 +23,24 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // ------------------------------------------------------------- products ----
 // Tiles of 64 T x 64 T by four waves, 2 x 2 of them, T x T blocks of 32 x 32 to a
-// wave; K-tiles of 32 (64 bytes of a row, in four chunks permuted within it) in
-// four LDS stages filled by direct transfers three K-tiles ahead.
-constexpr int kStages = 4;
+// wave.  K-tiles of 64: a row's slice is a whole 128-byte line (slices of 64 bytes
+// had each line fetched twice).  Its eight 16-byte chunks stand permuted by the
+// row, so that 16 rows' reads of one chunk fall on different banks.
+//
+// A slot of LDS holds one operand's rows of a K-tile; kSlots of them are filled in
+// turn, P's and Q's alternating, by direct transfers.  A wave reads fragments two
+// sub-steps (of 16 k) ahead, so that a K-tile's slots are free after half of its
+// products, and spreads the two slots' transfers over the next K-tile's worth of
+// them, one to a row of products: in bursts they held the waves up.
 template <int T>
 struct Ns {
   static constexpr int kTile = 64 * T;
-  static constexpr int kStageBytes = 2 * kTile * 64;
-  static constexpr int kMoves = 2 * T;                 // transfers of a wave to a stage
+  static constexpr int kSlots = 5;
+  static constexpr int kSlotBytes = kTile * 128;
+  static constexpr int kMoves = 2 * T;                 // transfers of a wave to a slot
   static constexpr int kStride = 32 * T + 8;           // floats between rows of an epilogue slab
   static constexpr int kSlab = 32 * kStride;
-  static constexpr int kLds = kStages * kStageBytes;
+  static constexpr int kLds = kSlots * kSlotBytes;
   static_assert(4 * kSlab * 4 <= kLds, "the epilogue's slabs");
 };
 
@@ -41,19 +48,21 @@ template <int T>
 struct NsFrags {
   half8 a[T], b[T];
 };
-template <int T>
-__device__ __forceinline__ void read_frags(NsFrags<T> &f, const uint8_t *stage, const uint32_t at[2 * T]) {
+// One sub-step: its products, with the fragments of the one after the next read
+// and a slot's transfers issued beneath them, row by row (left to itself, the
+// compiler puts reads right before their first use).
+template <int T, typename Move>
+__device__ __forceinline__ void multiply(f32x16 acc[T][T], const NsFrags<T> &f, NsFrags<T> &ahead, const uint8_t *p, const uint8_t *q,
+                                         Move move) {
 #pragma unroll
-  for (int i = 0; i < T; ++i) f.a[i] = *reinterpret_cast<const half8 *>(stage + at[i]);
-#pragma unroll
-  for (int i = 0; i < T; ++i) f.b[i] = *reinterpret_cast<const half8 *>(stage + at[T + i]);
-}
-template <int T>
-__device__ __forceinline__ void multiply(f32x16 acc[T][T], const NsFrags<T> &f) {
-#pragma unroll
-  for (int i = 0; i < T; ++i)
+  for (int i = 0; i < T; ++i) {
+    ahead.a[i] = *reinterpret_cast<const half8 *>(p + i * 4096);
+    ahead.b[i] = *reinterpret_cast<const half8 *>(q + i * 4096);
 #pragma unroll
     for (int j = 0; j < T; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+    move(i);
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
 __device__ __forceinline__ void slab_fence() { asm volatile("" ::: "memory"); }
@@ -114,23 +123,23 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : 2) void ns_product_kernel(NsArgs 
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const uint32_t wm = wave >> 1, wn = wave & 1, lr = lane & 31, h = lane >> 5;
 
-  // transfers: waves 0 and 1 fill the rows of P, 2 and 3 those of Q
-  const uint8_t *base = reinterpret_cast<const uint8_t *>(wave < 2 ? t.p + m0 * t.K : t.q + n0 * t.K);
+  // transfers: every wave a quarter of a slot
+  const int64_t ld = muon_ld(t.K);
+  const uint8_t *base_p = reinterpret_cast<const uint8_t *>(t.p + m0 * ld), *base_q = reinterpret_cast<const uint8_t *>(t.q + n0 * ld);
   uint32_t off[N::kMoves];
 #pragma unroll
   for (int i = 0; i < N::kMoves; ++i) {
-    const uint32_t q = (wave * N::kMoves + i) * 64 + lane, row = q >> 2;
-    off[i] = (row % N::kTile) * (uint32_t)(t.K * 2) + ((q & 3u) ^ swz(row)) * 16u;
+    const uint32_t q = (wave * N::kMoves + i) * 64 + lane, row = q >> 3;
+    off[i] = row * (uint32_t)(ld * 2) + ((q ^ (row >> 1)) & 7u) * 16u;
   }
-  // fragments: lane half h takes chunk 2 s + h of its row in sub-step s
-  uint32_t at0[2 * T], at1[2 * T];
+  // fragments: lane half h takes chunk 2 s + h of its row in sub-step s; a wave's
+  // blocks are 32 rows apart, so their permutations are one
+  uint32_t at_p[4], at_q[4];
 #pragma unroll
-  for (int i = 0; i < T; ++i) {
-    const uint32_t ra = wm * (32 * T) + i * 32 + lr, rb = N::kTile + wn * (32 * T) + i * 32 + lr;
-    at0[i] = (ra * 4 + (h ^ swz(ra))) * 16;
-    at1[i] = (ra * 4 + ((2 + h) ^ swz(ra))) * 16;
-    at0[T + i] = (rb * 4 + (h ^ swz(rb))) * 16;
-    at1[T + i] = (rb * 4 + ((2 + h) ^ swz(rb))) * 16;
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t chunk = ((2 * k + h) ^ ((lr >> 1) & 7u)) * 16;
+    at_p[k] = (wm * (32 * T) + lr) * 128 + chunk;
+    at_q[k] = (wn * (32 * T) + lr) * 128 + chunk;
   }
   f32x16 acc[T][T];
 #pragma unroll
@@ -140,37 +149,52 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : 2) void ns_product_kernel(NsArgs 
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  const uint32_t lds0 = lds_addr(lds), KT = (uint32_t)(t.K / 32), last = KT - 1;
-  const auto issue = [&](uint32_t kt, uint32_t stage) {  // past the end: the last K-tile again, into a stage nobody reads
-    const uint8_t *b = uniform_ptr(base + (uint64_t)(kt < last ? kt : last) * 64u);
-#pragma unroll
-    for (int i = 0; i < N::kMoves; ++i)
-      dma16(b, off[i], __builtin_amdgcn_readfirstlane(lds0 + stage * N::kStageBytes + (wave * N::kMoves + i) * 1024u));
+  const uint32_t lds0 = lds_addr(lds), KT = (uint32_t)(t.K / 64), last = KT - 1;
+  // transfer i of K-tile kt of one operand into a slot; past the end the last
+  // K-tile again, into a slot that nobody reads
+  const auto move = [&](const uint8_t *base, uint32_t kt, uint32_t slot, int i) {
+    dma16(uniform_ptr(base + (uint64_t)(kt < last ? kt : last) * 128u), off[i],
+          __builtin_amdgcn_readfirstlane(lds0 + slot * N::kSlotBytes + (wave * N::kMoves + i) * 1024u));
   };
-  issue(0, 0);
-  issue(1, 1);
-  issue(2, 2);
-  NVFP4_WAIT_VMCNT(2 * N::kMoves);  // this wave's part of K-tile 0 is in LDS
+  const auto after = [](uint32_t slot, uint32_t by) { return slot + by >= N::kSlots ? slot + by - N::kSlots : slot + by; };
+#pragma unroll
+  for (int u = 0; u < N::kSlots - 1; ++u)
+#pragma unroll
+    for (int i = 0; i < N::kMoves; ++i) move(u & 1 ? base_q : base_p, u / 2, u, i);
+  NVFP4_WAIT_VMCNT((N::kSlots - 3) * N::kMoves);  // this wave's part of K-tile 0 is in LDS
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-  NsFrags<T> f, g;
-  read_frags<T>(f, lds, at0);
+  NsFrags<T> f[4];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      f[k].a[i] = *reinterpret_cast<const half8 *>(lds + at_p[k] + i * 4096);
+      f[k].b[i] = *reinterpret_cast<const half8 *>(lds + N::kSlotBytes + at_q[k] + i * 4096);
+    }
+  // At the top of K-tile kt all slots but one, where Q's part of the K-tile before
+  // was, are full or on their way: it gets P's part of K-tile kt + kSlots / 2.
+  // Where P's part of this one is, Q's follows.
+  uint32_t slot = 0;
   for (uint32_t kt = 0; kt < KT; ++kt) {
-    const uint8_t *stage = lds + (kt & 3u) * N::kStageBytes;
-    read_frags<T>(g, stage, at1);
-    issue(kt + 3, (kt + 3) & 3u);  // its stage was read before the last barrier
-    multiply<T>(acc, f);
-    __builtin_amdgcn_sched_barrier(0);
-    NVFP4_WAIT_LGKM0();               // this wave's reads of the stage are complete
-    NVFP4_WAIT_VMCNT(2 * N::kMoves);  // its part of K-tile kt + 1 is in LDS
-    __builtin_amdgcn_s_barrier();     // every wave's
+    const uint32_t slot_q = after(slot, 1), free_q = after(slot, N::kSlots - 1);
+    const uint8_t *p = lds + slot * N::kSlotBytes, *q = lds + slot_q * N::kSlotBytes;
+    const uint32_t far = kt + N::kSlots / 2;
+    multiply<T>(acc, f[0], f[2], p + at_p[2], q + at_q[2], [&](int i) { move(base_p, far, free_q, i); });
+    multiply<T>(acc, f[1], f[3], p + at_p[3], q + at_q[3], [&](int i) { move(base_p, far, free_q, T + i); });
+    NVFP4_WAIT_LGKM0();                             // this wave's reads of the two slots are complete
+    NVFP4_WAIT_VMCNT((N::kSlots - 4) * N::kMoves);  // its part of K-tile kt + 1 is in LDS
+    __builtin_amdgcn_s_barrier();                   // every wave's: K-tile kt + 1 is there, these slots are free
     asm volatile("" ::: "memory");
-    read_frags<T>(f, lds + ((kt + 1) & 3u) * N::kStageBytes, at0);  // after the last K-tile: not used
-    multiply<T>(acc, g);
-    __builtin_amdgcn_sched_barrier(0);
+    const uint32_t next = after(slot, 2), next_q = after(slot, 3);
+    p = lds + next * N::kSlotBytes;  // after the last K-tile: what is read is not used
+    q = lds + next_q * N::kSlotBytes;
+    multiply<T>(acc, f[2], f[0], p + at_p[0], q + at_q[0], [&](int i) { move(base_q, far, slot, i); });
+    multiply<T>(acc, f[3], f[1], p + at_p[1], q + at_q[1], [&](int i) { move(base_q, far, slot, T + i); });
+    slot = next;
   }
   NVFP4_WAIT_VMCNT(0);
-  __syncthreads();  // no wave reads the stages, and no transfer writes them, any more
+  __syncthreads();  // no wave reads the slots, and no transfer writes them, any more
 
   float *slab = reinterpret_cast<float *>(lds) + wave * N::kSlab;
   const int64_t mw = m0 + wm * (32 * T), nw = n0 + wn * (32 * T);
@@ -182,7 +206,7 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : 2) void ns_product_kernel(NsArgs 
 #pragma unroll
         for (int r = 0; r < 16; ++r) slab[((r >> 2) * 8 + h * 4 + (r & 3)) * N::kStride + j * 32 + lr] = acc[i][j][r];
       slab_fence();
-      store_rows<T>(a, t.d, t.e, t.N, mw + i * 32, nw, slab, lane);
+      store_rows<T>(a, t.d, t.e, muon_ld(t.N), mw + i * 32, nw, slab, lane);
       slab_fence();
     }
   }
@@ -196,7 +220,7 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : 2) void ns_product_kernel(NsArgs 
           *reinterpret_cast<f32x4 *>(&slab[lr * N::kStride + i * 32 + q * 8 + h * 4]) =
               (f32x4){acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
       slab_fence();
-      store_rows<T>(a, t.dt, t.e, t.M, nw + j * 32, mw, slab, lane);
+      store_rows<T>(a, t.dt, t.e, muon_ld(t.M), nw + j * 32, mw, slab, lane);
       slab_fence();
     }
   }
@@ -317,7 +341,7 @@ __global__ __launch_bounds__(256) void muon_form_kernel(MuonArgs a) {
       for (int j = 0; j < 8; ++j)
         if (j < n) x[j] = (_Float16)(float)((double)g[j] * by);
     }
-    *reinterpret_cast<half8 *>(t.direct + (int64_t)(r0 + r) * t.cp + c0 + c) = x;
+    *reinterpret_cast<half8 *>(t.direct + (r0 + r) * muon_ld(t.cp) + c0 + c) = x;
 #pragma unroll
     for (int j = 0; j < 8; ++j) tile[c + j][r] = x[j];
   }
@@ -325,7 +349,7 @@ __global__ __launch_bounds__(256) void muon_form_kernel(MuonArgs a) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int r = (threadIdx.x >> 3) + 32 * k, c = (threadIdx.x & 7) * 8;
-    *reinterpret_cast<half8 *>(t.turned + (int64_t)(c0 + r) * t.rp + r0 + c) = *reinterpret_cast<const half8 *>(&tile[r][c]);
+    *reinterpret_cast<half8 *>(t.turned + (c0 + r) * muon_ld(t.rp) + r0 + c) = *reinterpret_cast<const half8 *>(&tile[r][c]);
   }
 }
 
@@ -343,7 +367,7 @@ __global__ __launch_bounds__(256) void muon_update_kernel(MuonArgs a) {
     if (i >= n) break;
     const uint32_t down = (col0 + o) / (uint32_t)t.cols;
     uint32_t c = col0 + o - down * t.cols;
-    const _Float16 *x = t.direct + (row0 + down) * t.cp;
+    const _Float16 *x = t.direct + (row0 + down) * muon_ld(t.cp);
     float u[8];
     if (c + 8 <= (uint32_t)t.cols) {
       typedef half8 __attribute__((aligned(2))) half8_at2;
@@ -356,7 +380,7 @@ __global__ __launch_bounds__(256) void muon_update_kernel(MuonArgs a) {
         u[j] = i + j < n ? (float)x[c] * (1.0f / kMuonX) : 0.0f;
         if (++c == (uint32_t)t.cols) {
           c = 0;
-          x += t.cp;
+          x += muon_ld(t.cp);
         }
       }
     }
