@@ -286,12 +286,10 @@ hipError_t muon_run(const nvfp4_muon_tensor *tensors, const MuonGroup &g, int ti
                     char *base, hipStream_t s) {
   MuonBuffers buf[kMuonMats];
   size_t used = 0;
-  uint32_t sums = 0, forms = 0, updates = 0;
   for (int i = 0; i < g.count; ++i) {
     const nvfp4_muon_tensor &t = tensors[g.index[i]];
     used = muon_buffers(t, tile, base, used, buf[i]);
     const bool turned = t.rows > t.cols;
-    const int64_t n = t.rows * t.cols, chunks = (n + kMuonChunk - 1) / kMuonChunk;
     MuonMat &d = a.mat[i];
     d.grad = t.grad;
     d.m = t.m;
@@ -311,10 +309,6 @@ hipError_t muon_run(const nvfp4_muon_tensor *tensors, const MuonGroup &g, int ti
     d.flags = (t.param_dtype == NVFP4_BF16 ? MF_PARAM_BF16 : 0u) | (t.grad_dtype == NVFP4_BF16 ? MF_GRAD_BF16 : 0u) |
               (turned ? MF_TURNED : 0u);
     d.index = (uint32_t)g.index[i];
-    d.sums = (uint32_t)(chunks < kMuonParts ? chunks : kMuonParts);
-    d.sum_end = sums += d.sums;
-    d.tile_end = forms += (uint32_t)(d.rp / 64) * (uint32_t)(d.cp / 64);
-    d.update_end = updates += (uint32_t)chunks;
   }
   a.count = g.count;
   hipError_t e = launch_muon_sums(a, s);
@@ -331,11 +325,11 @@ hipError_t muon_run(const nvfp4_muon_tensor *tensors, const MuonGroup &g, int ti
         NsMat &o = p.mat[i];
         const MuonBuffers &b = buf[i];
         if (stage == 0)
-          o = {b.x, b.x, nullptr, b.a, b.a, m, m, n, 0};
+          o = {b.x, b.x, nullptr, b.a, b.a, m, m, n};
         else if (stage == 1)
-          o = {b.a, b.a, b.a, b.b, b.b, m, m, m, 0};
+          o = {b.a, b.a, b.a, b.b, b.b, m, m, m};
         else
-          o = {b.b, b.xt[k & 1], nullptr, last && turned ? nullptr : b.x, last && !turned ? nullptr : b.xt[~k & 1], m, n, m, 0};
+          o = {b.b, b.xt[k & 1], nullptr, last && turned ? nullptr : b.x, last && !turned ? nullptr : b.xt[~k & 1], m, n, m};
       }
       p.symmetric = stage < 2;
       p.alpha = (float)(stage == 0 ? ka / (kx * kx) : stage == 1 ? c.c / ka : 1.0 / ka);

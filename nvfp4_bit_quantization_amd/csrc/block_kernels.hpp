@@ -89,17 +89,32 @@ struct MuonMat {
   int rows, cols, rp, cp;     // the tensor's, and padded
   float keep, step;           // 1 - lr * weight_decay, lr * scale
   uint32_t flags, index;
-  uint32_t sum_end, tile_end, update_end;  // workgroups of this and the earlier matrices of the launches
-  uint32_t sums;                           // workgroups of this one's sum
+  uint32_t sums;              // workgroups of its sum
 };
 struct MuonArgs {
   MuonMat mat[kMuonMats];
+  uint32_t end[kMuonMats];  // workgroups of a matrix and the earlier ones; past the last: 2^32 - 1
   int count, sr, nesterov;
   float beta, one_minus_beta;
   uint32_t seed_lo, seed_hi, step_lo, tag;
   const float *grad_scale;
 };
-static_assert(sizeof(MuonMat) == 120 && sizeof(MuonArgs) <= 4096, "kernel arguments");
+static_assert(sizeof(MuonMat) == 112 && sizeof(MuonArgs) <= 4096, "kernel arguments");
+
+// The matrix of a workgroup, whose number becomes that within the matrix: all
+// ends are loaded at once (one after another, 20 matrices took 2 us).
+__device__ __forceinline__ int muon_mat_of(const uint32_t end[kMuonMats], uint32_t &group) {
+  int which = 0;
+  uint32_t before = 0;
+#pragma unroll
+  for (int i = 0; i < kMuonMats; ++i) {
+    const bool past = group >= end[i];
+    which += past;
+    before = past ? end[i] : before;
+  }
+  group -= before;
+  return which;
+}
 
 // D = alpha P Q^T + beta E + gamma I of every matrix, P [M][K], Q [N][K], D and E
 // [M][N], DT [N][M], rows muon_ld apart; D or DT may be null.  Symmetric: P = Q and D = DT, and only
@@ -108,17 +123,18 @@ struct NsMat {
   const _Float16 *p, *q, *e;
   _Float16 *d, *dt;
   int M, N, K;
-  uint32_t end;  // tiles of this and the earlier matrices
 };
 struct NsArgs {
   NsMat mat[kMuonMats];
+  uint32_t end[kMuonMats];  // tiles of a matrix and the earlier ones; past the last: 2^32 - 1
   int count, symmetric;
   float alpha, beta, gamma;
 };
-hipError_t launch_muon_sums(const MuonArgs &a, hipStream_t s);
-hipError_t launch_muon_form(const MuonArgs &a, hipStream_t s);
-// tile: 64, 128 or 256 rows and columns of a workgroup; fills the ends
+// the launches fill the ends
+hipError_t launch_muon_sums(MuonArgs &a, hipStream_t s);
+hipError_t launch_muon_form(MuonArgs &a, hipStream_t s);
+// tile: 64, 128 or 256 rows and columns of a workgroup
 hipError_t launch_muon_product(NsArgs &a, int tile, hipStream_t s);
-hipError_t launch_muon_update(const MuonArgs &a, hipStream_t s);
+hipError_t launch_muon_update(MuonArgs &a, hipStream_t s);
 
 }  // namespace nvfp4

@@ -35,7 +35,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 template <int T>
 struct Ns {
   static constexpr int kTile = 64 * T;
-  static constexpr int kSlots = 5;
+  static constexpr int kSlots = T == 4 ? 5 : 9;
   static constexpr int kSlotBytes = kTile * 128;
   static constexpr int kMoves = 2 * T;                 // transfers of a wave to a slot
   static constexpr int kStride = 32 * T + 8;           // floats between rows of an epilogue slab
@@ -101,10 +101,7 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : 2) void ns_product_kernel(NsArgs 
   __shared__ __attribute__((aligned(16))) uint8_t lds[N::kLds];
   // the matrix and the tile
   uint32_t tile = xcd_tile(blockIdx.x, gridDim.x);
-  int which = 0;
-  while (tile >= a.mat[which].end) ++which;
-  const NsMat &t = a.mat[which];
-  if (which) tile -= a.mat[which - 1].end;
+  const NsMat &t = a.mat[muon_mat_of(a.end, tile)];
   int64_t m0, n0;
   if (a.symmetric) {  // tile = I (I + 1) / 2 + J, J <= I
     uint32_t i = (uint32_t)((sqrtf(8.0f * (float)tile + 1.0f) - 1.0f) * 0.5f);
@@ -227,15 +224,6 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : 2) void ns_product_kernel(NsArgs 
 }
 
 // ---------------------------------------------------------- elementwise ----
-// the matrix of a workgroup, and its number within it
-template <typename End>
-__device__ __forceinline__ const MuonMat &mat_of(const MuonArgs &a, uint32_t &group, End end) {
-  int which = 0;
-  while (group >= end(a.mat[which])) ++which;
-  if (which) group -= end(a.mat[which - 1]);
-  return a.mat[which];
-}
-
 // up to 8 elements from p, zero past `n`
 template <typename T>
 __device__ __forceinline__ void load_some(const T *p, int64_t n, float v[8]) {
@@ -278,7 +266,7 @@ __device__ __forceinline__ double wave_sum64(double v) {
 // the new momentum, and the sum of squares of the direction by workgroup
 __global__ __launch_bounds__(256) void muon_sums_kernel(MuonArgs a) {
   uint32_t group = blockIdx.x;
-  const MuonMat &t = mat_of(a, group, [](const MuonMat &x) { return x.sum_end; });
+  const MuonMat &t = a.mat[muon_mat_of(a.end, group)];
   const int64_t n = (int64_t)t.rows * t.cols;
   const float scale = a.grad_scale ? *a.grad_scale : 1.0f;
   double sum = 0.0;
@@ -308,7 +296,7 @@ __global__ __launch_bounds__(256) void muon_sums_kernel(MuonArgs a) {
 // X and its transpose in fp16, 64 x 64 elements to a workgroup, zeros beyond the tensor
 __global__ __launch_bounds__(256) void muon_form_kernel(MuonArgs a) {
   uint32_t group = blockIdx.x;
-  const MuonMat &t = mat_of(a, group, [](const MuonMat &x) { return x.tile_end; });
+  const MuonMat &t = a.mat[muon_mat_of(a.end, group)];
   __shared__ double sums[4];
   __shared__ __attribute__((aligned(16))) _Float16 tile[64][72];
   double sum = 0.0;
@@ -356,7 +344,7 @@ __global__ __launch_bounds__(256) void muon_form_kernel(MuonArgs a) {
 // what the last product left, as update and applied to the parameter
 __global__ __launch_bounds__(256) void muon_update_kernel(MuonArgs a) {
   uint32_t group = blockIdx.x;
-  const MuonMat &t = mat_of(a, group, [](const MuonMat &x) { return x.update_end; });
+  const MuonMat &t = a.mat[muon_mat_of(a.end, group)];
   const int64_t n = (int64_t)t.rows * t.cols, start = (int64_t)group * kMuonChunk;
   const int64_t row0 = start / t.cols;
   const uint32_t col0 = (uint32_t)(start - row0 * t.cols);
@@ -417,30 +405,44 @@ __global__ __launch_bounds__(256) void muon_update_kernel(MuonArgs a) {
 
 }  // namespace
 
-hipError_t launch_muon_sums(const MuonArgs &a, hipStream_t s) {
-  hipLaunchKernelGGL(muon_sums_kernel, dim3(a.mat[a.count - 1].sum_end), dim3(256), 0, s, a);
+namespace {
+
+template <typename Args, typename Count>
+uint32_t fill_ends(Args &a, Count count) {
+  uint32_t end = 0;
+  for (int i = 0; i < kMuonMats; ++i) a.end[i] = i < a.count ? end += count(a.mat[i]) : ~0u;
+  return end;
+}
+uint32_t chunks(const MuonMat &t) { return (uint32_t)(((int64_t)t.rows * t.cols + kMuonChunk - 1) / kMuonChunk); }
+
+}  // namespace
+
+hipError_t launch_muon_sums(MuonArgs &a, hipStream_t s) {
+  const uint32_t n = fill_ends(a, [](MuonMat &t) { return t.sums = chunks(t) < kMuonParts ? chunks(t) : kMuonParts; });
+  hipLaunchKernelGGL(muon_sums_kernel, dim3(n), dim3(256), 0, s, a);
   return hipGetLastError();
 }
-hipError_t launch_muon_form(const MuonArgs &a, hipStream_t s) {
-  hipLaunchKernelGGL(muon_form_kernel, dim3(a.mat[a.count - 1].tile_end), dim3(256), 0, s, a);
+hipError_t launch_muon_form(MuonArgs &a, hipStream_t s) {
+  const uint32_t n = fill_ends(a, [](const MuonMat &t) { return (uint32_t)(t.rp / 64) * (uint32_t)(t.cp / 64); });
+  hipLaunchKernelGGL(muon_form_kernel, dim3(n), dim3(256), 0, s, a);
   return hipGetLastError();
 }
-hipError_t launch_muon_update(const MuonArgs &a, hipStream_t s) {
-  hipLaunchKernelGGL(muon_update_kernel, dim3(a.mat[a.count - 1].update_end), dim3(256), 0, s, a);
+hipError_t launch_muon_update(MuonArgs &a, hipStream_t s) {
+  const uint32_t n = fill_ends(a, [](const MuonMat &t) { return chunks(t); });
+  hipLaunchKernelGGL(muon_update_kernel, dim3(n), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 hipError_t launch_muon_product(NsArgs &a, int tile, hipStream_t s) {
-  uint32_t end = 0;
-  for (int i = 0; i < a.count; ++i) {
-    const uint32_t m = a.mat[i].M / tile, n = a.mat[i].N / tile;
-    a.mat[i].end = end += a.symmetric ? m * (m + 1) / 2 : m * n;
-  }
+  const uint32_t n = fill_ends(a, [&](const NsMat &t) {
+    const uint32_t down = t.M / tile, across = t.N / tile;
+    return a.symmetric ? down * (down + 1) / 2 : down * across;
+  });
   if (tile == 256)
-    hipLaunchKernelGGL((ns_product_kernel<4>), dim3(end), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((ns_product_kernel<4>), dim3(n), dim3(256), 0, s, a);
   else if (tile == 128)
-    hipLaunchKernelGGL((ns_product_kernel<2>), dim3(end), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((ns_product_kernel<2>), dim3(n), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((ns_product_kernel<1>), dim3(end), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((ns_product_kernel<1>), dim3(n), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
