@@ -11,9 +11,9 @@
 // result is off by 1.2e-3 to 2e-3 of its norm, by rounding X, A and the
 // polynomial to 11 bits five times; bf16, the usual choice, is off by 8 times
 // that.  Powers of two keep the values in fp16's normal range (kMuonX, kMuonA).
+#include "block_device.hpp"
 #include "block_kernels.hpp"
 #include "gemm_device.hpp"
-#include "train_device.hpp"
 
 namespace nvfp4 {
 namespace {
@@ -400,7 +400,11 @@ __global__ __launch_bounds__(256) void muon_update_kernel(MuonArgs a) {
         if (j < n - i) top = fmaxf(top, fabsf(rounds ? round_bf16(p[j]) : p[j]));
     }
   }
-  if (t.amax) fold_max(t.amax, top);
+  if (t.amax) {
+    unsigned int *const out[1] = {reinterpret_cast<unsigned int *>(t.amax)};
+    const uint32_t bits[1] = {__float_as_uint(top)};
+    raise_maxima<1>(out, bits);
+  }
 }
 
 }  // namespace
