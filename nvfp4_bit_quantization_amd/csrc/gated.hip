@@ -218,6 +218,22 @@ __device__ __forceinline__ void grad_store(const GatedArgs &a, int64_t m0, int64
   const int c = lane % LANES * 8, first = lane / LANES;
   const int64_t n = n0 + (wave & 1) * (TN * 32) + c;
   const int64_t m = m0 + (wave >> 1) * (TM * 32);
+  // gate and up are read four rows of a lane ahead: one after another, 5120 x 20480
+  // outputs of 16384 rows took 3.15 ms instead of 2.71
+  constexpr int AT_ONCE = 4, PARTS = 32 / (ROWS * AT_ONCE);
+  uint4 gate[AT_ONCE], up[AT_ONCE];
+  const auto fetch = [&](int part) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) {
+      const int64_t row = m + (part * AT_ONCE + k) * ROWS + first;
+      gate[k] = up[k] = make_uint4(0, 0, 0, 0);
+      if (row < a.g.M && n < a.g.N) {
+        gate[k] = load_group(a.gate + row * a.ld_gate + n);
+        up[k] = load_group(a.up + row * a.ld_up + n);
+      }
+    }
+  };
+  fetch(0);
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
 #pragma unroll
@@ -226,37 +242,43 @@ __device__ __forceinline__ void grad_store(const GatedArgs &a, int64_t m0, int64
       for (int r = 0; r < 16; ++r)
         slab[((r >> 2) * 8 + (lane >> 5) * 4 + (r & 3)) * S + j * 32 + (lane & 31)] = acc[i][j][r];
     slab_fence();
-#pragma unroll 2
-    for (int r = first; r < 32; r += ROWS) {
-      const int64_t row = m + i * 32 + r;
-      const bool here = row < a.g.M && n < a.g.N;
-      uint4 g = make_uint4(0, 0, 0, 0), u = g;
-      if (here) {
-        g = load_group(a.gate + row * a.ld_gate + n);
-        u = load_group(a.up + row * a.ld_up + n);
-      }
-      float dg[8], du[8];
+#pragma unroll 1
+    for (int part = 0; part < PARTS; ++part) {
+      uint4 g[AT_ONCE], u[AT_ONCE];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float dh = epi_apply(slab[r * S + c + k], es);
-        float f, df;
-        act_grad<ACT>(bf16_at(g, k), f, df);
-        dg[k] = dh * bf16_at(u, k) * df;
-        du[k] = dh * f;
+      for (int k = 0; k < AT_ONCE; ++k) {
+        g[k] = gate[k];
+        u[k] = up[k];
       }
-      u32x4 gb = packed8(dg), ub = packed8(du);
-      if (here) {
-        store_past_caches(a.dgate + row * a.ld_dgate + n, gb);
-        store_past_caches(a.dup + row * a.ld_dup + n, ub);
-      } else {
-        gb = ub = (u32x4){0, 0, 0, 0};
-      }
-      fm[0].plain = top_of(fm[0].plain, gb);
-      fm[1].plain = top_of(fm[1].plain, ub);
-      if (rht) {
-        uint16_t *at = reinterpret_cast<uint16_t *>(slab + r * S) + c;
-        *reinterpret_cast<u32x4 *>(at) = gb;
-        *reinterpret_cast<u32x4 *>(at + TN * 32) = ub;
+      if (i * PARTS + part + 1 < TM * PARTS) fetch(i * PARTS + part + 1);
+#pragma unroll
+      for (int k = 0; k < AT_ONCE; ++k) {
+        const int r = (part * AT_ONCE + k) * ROWS + first;
+        const int64_t row = m + i * 32 + r;
+        const bool here = row < a.g.M && n < a.g.N;
+        float dg[8], du[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float dh = epi_apply(slab[r * S + c + e], es);
+          float f, df;
+          act_grad<ACT>(bf16_at(g[k], e), f, df);
+          dg[e] = dh * bf16_at(u[k], e) * df;
+          du[e] = dh * f;
+        }
+        u32x4 gb = packed8(dg), ub = packed8(du);
+        if (here) {
+          store_past_caches(a.dgate + row * a.ld_dgate + n, gb);
+          store_past_caches(a.dup + row * a.ld_dup + n, ub);
+        } else {
+          gb = ub = (u32x4){0, 0, 0, 0};
+        }
+        fm[0].plain = top_of(fm[0].plain, gb);
+        fm[1].plain = top_of(fm[1].plain, ub);
+        if (rht) {
+          uint16_t *at = reinterpret_cast<uint16_t *>(slab + r * S) + c;
+          *reinterpret_cast<u32x4 *>(at) = gb;
+          *reinterpret_cast<u32x4 *>(at + TN * 32) = ub;
+        }
       }
     }
     slab_fence();
@@ -404,7 +426,7 @@ struct Ragged {
 };
 
 template <bool BACK, int T>
-__global__ __launch_bounds__(kGThreads) void gated_generic_kernel(GatedArgs a) {
+__global__ __launch_bounds__(kGThreads, 2) void gated_generic_kernel(GatedArgs a) {
   using S = Ragged<T>;
   constexpr int kSlabs = kGThreads / 64 * Slab<T>::kFloats * 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * S::kBytes > kSlabs ? 2 * S::kBytes : kSlabs];
