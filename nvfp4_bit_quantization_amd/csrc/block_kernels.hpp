@@ -21,7 +21,7 @@ struct RopeSide {  // the query heads or the key heads
   int64_t x_b, x_t, x_h;           // elements between sequences, tokens, heads
   int64_t y_b, y_t, y_h, dx_b, dx_t, dx_h;
   int heads;
-  int per;      // heads of one token that a wave takes at a time, a power of two
+  int per;      // heads of a token that a wave takes at a time: a power of two that divides them
   int splits;   // waves that share a token's heads
   int groups;   // workgroups of this side
 };
@@ -39,7 +39,7 @@ struct RopeArgs {
   float eps, inv_dim, magnitude;
 };
 
-// lanes to a head (a power of two) for this layout, and the heads of a wave
+// lanes to a head, a power of two
 int rope_lanes(int units);
 // fills per, splits and groups of both sides from the sizes
 void rope_plan(RopeArgs &a);

@@ -6,9 +6,12 @@
 // them from the second, with interleaved layout 16 consecutive ones.  No element
 // leaves its lane; a norm's sum crosses the lanes of one head (8 at head_dim 128)
 // in DPP steps.  What is not rotated is held as pairs that turn by nothing.
-// The angles' sines are formed once for a token and used for all its heads: the
-// angle in turns is reduced in 64 bits (a 32-bit product is off by 0.06 rad at
-// position 1000000), the rest in 32.
+// A wave takes as many neighbouring heads of a token at a time as divide their
+// number, up to what fills its lanes (8 at head_dim 128), and as many tokens as
+// fill the rest: 40 heads go by eights of one token, 10 by twos of four, 5 of
+// eight tokens one by one.  The angles' sines, formed once for a token, serve all
+// the heads that the wave goes through.  The angle in turns is reduced in 64 bits
+// (a 32-bit product is off by 0.06 rad at position 1000000), the rest in 32.
 #include "block_kernels.hpp"
 #include "train_device.hpp"
 
@@ -127,12 +130,33 @@ __device__ __forceinline__ void turn(double turns, float magnitude, float &c, fl
   s = (k >= 2 ? -b : b) * magnitude;
 }
 
-// the place of token t in its sequence; false: it belongs to none
-__device__ __forceinline__ bool place_of(const RopeArgs &a, int64_t t, int64_t &b, int64_t &n, double &position) {
+// The places of a wave's tokens base + slot in their sequences; false: in none.
+// ends: cu[lane] of every lane, where 64 lanes hold all of cu.
+__device__ __forceinline__ bool place_of(const RopeArgs &a, int64_t base, int slot, int slots, int ends, int64_t &b, int64_t &n,
+                                         double &position) {
+  const int64_t t = base + slot;
   b = 0;
   n = t;
-  if (a.cu) {
-    int lo = 0, hi = a.batch;  // the last of cu[0 .. batch] that is <= t
+  if (!a.cu) {
+    if (a.batch > 1) {
+      b = (int64_t)((uint32_t)t / (uint32_t)a.tokens);
+      n = t - b * a.tokens;
+    }
+    position = a.positions && t < a.total ? (double)a.positions[t] : (double)n;
+    return true;
+  }
+  int which = -1, start = 0;  // the last sequence that begins at or before t
+  if (a.batch < 64) {
+    for (int k = 0; k < slots; ++k) {
+      const int begun = __popcll(__ballot((int)(threadIdx.x & 63u) <= a.batch && ends <= base + k)) - 1;
+      const int at = __builtin_amdgcn_readlane(ends, begun < 0 ? 0 : begun);
+      if (slot == k) {
+        which = begun;
+        start = at;
+      }
+    }
+  } else {
+    int lo = 0, hi = a.batch;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (a.cu[mid] <= t)
@@ -140,16 +164,11 @@ __device__ __forceinline__ bool place_of(const RopeArgs &a, int64_t t, int64_t &
       else
         hi = mid - 1;
     }
-    const int64_t start = a.cu[lo];
-    position = (double)(t - start);
-    return lo < a.batch && start <= t;
+    start = a.cu[lo];
+    which = start <= t ? lo : -1;
   }
-  if (a.batch > 1) {
-    b = (int64_t)((uint32_t)t / (uint32_t)a.tokens);
-    n = t - b * a.tokens;
-  }
-  position = a.positions ? (double)a.positions[t] : (double)n;
-  return true;
+  position = (double)(t - start);
+  return which >= 0 && which < a.batch;
 }
 
 template <typename W>
@@ -174,13 +193,13 @@ __device__ __forceinline__ void rotate(float v[2][8], const float c[8], const fl
 
 // L lanes to a head; I: interleaved pairs; G: the gradient; N: with a norm.
 template <typename TX, int L, bool I, bool G, bool N, bool R>
-__global__ __launch_bounds__(kWaves * 64) void rope_kernel(RopeArgs a) {
+__global__ __launch_bounds__(kWaves * 64, G ? 3 : 4) void rope_kernel(RopeArgs a) {
   const bool second = (int)blockIdx.x >= a.side[0].groups;
   const RopeSide &t = a.side[second];
   const int group = (int)blockIdx.x - (second ? a.side[0].groups : 0);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int u = lane & (L - 1), slot = lane / L;
-  const int per = t.per, at_once = (64 / L) / per;  // tokens of a wave at a time
+  const int per = t.per, at_once = 64 / L / per;  // heads and tokens of a wave at a time
+  const int u = lane & (L - 1), slot = lane / L / per, sub = lane / L % per;
   const Segments seg = segments(a, u);
   const bool used = u < a.units;
   float w[2][8], dw[2][8];
@@ -197,13 +216,15 @@ __global__ __launch_bounds__(kWaves * 64) void rope_kernel(RopeArgs a) {
     f[j] = seg.first >= 0 && p < a.rot / 2 ? a.freqs[p] * 0.15915494309189533577 : 0.0;
     if (G && N) dw[0][j] = dw[1][j] = 0.0f;
   }
-  const uint32_t item = group * kWaves + wave, items = t.groups * kWaves;
-  const int split = item % t.splits;
+  const int ends = a.cu && a.batch < 64 ? a.cu[min(lane, a.batch)] : 0;
+  const uint32_t item = __builtin_amdgcn_readfirstlane(group * kWaves + wave), items = t.groups * kWaves;
+  const int rounds = t.heads / per, share = (rounds + t.splits - 1) / t.splits;
+  const int h0 = (int)(item % t.splits) * share * per, h1 = min(t.heads, h0 + share * per);
   for (int64_t base = (int64_t)(item / t.splits) * at_once; base < a.total; base += (int64_t)(items / t.splits) * at_once) {
-    const int64_t token = base + slot / per;
     int64_t b, n;
     double position;
-    const bool live = used && token < a.total && place_of(a, token, b, n, position);
+    const bool placed = place_of(a, base, slot, at_once, ends, b, n, position);
+    const bool live = used && base + slot < a.total && placed;
     float c[8], s[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -211,17 +232,14 @@ __global__ __launch_bounds__(kWaves * 64) void rope_kernel(RopeArgs a) {
       s[j] = 0.0f;
       if (live && seg.first >= 0 && seg.first + j < a.rot / 2) turn(position * f[j], a.magnitude, c[j], s[j]);
     }
-    const TX *x = (const TX *)t.x + (live ? b * t.x_b + n * t.x_t : 0);
-    uint16_t *y = t.y + (live ? b * t.y_b + n * t.y_t : 0);
-    TX *dx = G ? (TX *)t.dx + (live ? b * t.dx_b + n * t.dx_t : 0) : nullptr;
-    int h = slot % per + split * per;
-    const int step = per * t.splits;
+    const TX *x = (const TX *)t.x + (live ? b * t.x_b + n * t.x_t + sub * t.x_h : 0);
+    uint16_t *y = t.y + (live ? b * t.y_b + n * t.y_t + sub * t.y_h : 0);
+    TX *dx = G ? (TX *)t.dx + (live ? b * t.dx_b + n * t.dx_t + sub * t.dx_h : 0) : nullptr;
     Raw<TX> rx[2];
     Raw<uint16_t> ry[2];
-    if (!G || N) fetch<R>(x + h * t.x_h, seg, live && h < t.heads, rx);
-    if (G) fetch<R>(y + h * t.y_h, seg, live && h < t.heads, ry);
-    for (; __any(live && h < t.heads); h += step) {
-      const bool here = live && h < t.heads;
+    if (!G || N) fetch<R>(x + h0 * t.x_h, seg, live, rx);
+    if (G) fetch<R>(y + h0 * t.y_h, seg, live, ry);
+    for (int h = h0; h < h1; h += per) {
       float v[2][8], g[2][8];
 #pragma unroll
       for (int k = 0; k < 2; ++k)
@@ -230,9 +248,9 @@ __global__ __launch_bounds__(kWaves * 64) void rope_kernel(RopeArgs a) {
           if (!G || N) v[k][j] = rx[k].at(j);
           if (G) g[k][j] = ry[k].at(j);
         }
-      const bool next = live && h + step < t.heads;
-      if (!G || N) fetch<R>(x + (h + step) * t.x_h, seg, next, rx);
-      if (G) fetch<R>(y + (h + step) * t.y_h, seg, next, ry);
+      const int next = h + per < h1 ? h + per : h;
+      if (!G || N) fetch<R>(x + next * t.x_h, seg, live, rx);
+      if (G) fetch<R>(y + next * t.y_h, seg, live, ry);
       float rstd = 1.0f;
       if (N) {
         float sum = 0.0f;
@@ -254,7 +272,7 @@ __global__ __launch_bounds__(kWaves * 64) void rope_kernel(RopeArgs a) {
             for (int j = 0; j < 8; ++j) v[k][j] *= w[k][j];
         }
         rotate(v, c, s, I, 1.0f);
-        if (here) put<R>(y + h * t.y_h, seg, v);
+        if (live) put<R>(y + h * t.y_h, seg, v);
         continue;
       }
       rotate(g, c, s, I, -1.0f);
@@ -274,7 +292,7 @@ __global__ __launch_bounds__(kWaves * 64) void rope_kernel(RopeArgs a) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) g[k][j] = rstd * fmaf(-dot, v[k][j], g[k][j]);
       }
-      if (here) put<R>(dx + h * t.dx_h, seg, g);
+      if (live) put<R>(dx + h * t.dx_h, seg, g);
     }
   }
   if (!G || !N || !t.dweight) return;
@@ -303,21 +321,24 @@ __global__ __launch_bounds__(kWaves * 64) void rope_kernel(RopeArgs a) {
   }
 }
 
-// dweight of both sides: 8 columns to a workgroup, 32 threads to a column over
+// dweight of both sides: 8 columns to a workgroup, 128 threads to a column over
 // the workgroups' parts, in a fixed order
-__global__ __launch_bounds__(256) void rope_reduce_kernel(RopeArgs a) {
+__global__ __launch_bounds__(1024) void rope_reduce_kernel(RopeArgs a) {
   const RopeSide &t = a.side[blockIdx.y];
   if (!t.dweight) return;
-  const int col = blockIdx.x * 8 + (threadIdx.x & 7), row = threadIdx.x >> 3;
+  const int col = blockIdx.x * 8 + (threadIdx.x & 7);
   float v = 0.0f;
-  for (int r = row; r < t.groups; r += 32) v += t.parts[(int64_t)r * a.dim + col];
-  __shared__ float sums[256];
-  sums[threadIdx.x] = v;
+#pragma unroll 8
+  for (int r = threadIdx.x >> 3; r < t.groups; r += 128) v += t.parts[(int64_t)r * a.dim + col];
+#pragma unroll
+  for (int o = 8; o < 64; o *= 2) v += __shfl_xor(v, o, 64);
+  __shared__ float sums[16][8];
+  if ((threadIdx.x & 63) < 8) sums[threadIdx.x >> 6][threadIdx.x & 7] = v;
   __syncthreads();
   if (threadIdx.x < 8) {
     v = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 32; ++r) v += sums[r * 8 + threadIdx.x];
+    for (int r = 0; r < 16; ++r) v += sums[r][threadIdx.x];
     t.dweight[col] = v;
   }
 }
@@ -358,25 +379,27 @@ hipError_t launch_typed(const RopeArgs &a, hipStream_t s) {
 
 }  // namespace
 
+constexpr int64_t kRopeWaves = 4096, kRopeGroups = 1280;
+
 int rope_lanes(int units) { return units <= 4 ? 4 : units <= 8 ? 8 : 16; }
 
 void rope_plan(RopeArgs &a) {
   const int slots = 64 / rope_lanes(a.units);
   for (RopeSide &t : a.side) {
-    t.per = 1;
-    t.splits = 1;
+    t.per = t.splits = 1;
     t.groups = 0;
     if (!t.heads) continue;
-    while (t.per < slots && t.per < t.heads) t.per *= 2;
-    const int64_t at_once = slots / t.per, waves = (a.total + at_once - 1) / at_once;
-    const int most = (t.heads + t.per - 1) / t.per;
-    // few tokens: a wave to each group of heads, so that no load waits for another's
-    if (waves * most <= 4096) t.splits = most;
-    int64_t groups = (waves * t.splits + kWaves - 1) / kWaves;
-    const int64_t cap = 1280;
-    if (groups > cap) groups = cap;
-    groups = (groups + t.splits - 1) / t.splits * t.splits;  // each split as often
-    t.groups = (int)(groups < 1 ? 1 : groups);
+    while (t.per < slots && t.heads % (2 * t.per) == 0) t.per *= 2;
+    const int64_t at_once = slots / t.per, blocks = (a.total + at_once - 1) / at_once, rounds = t.heads / t.per;
+    // heads are shared out until there are kRopeWaves waves, or one to a head
+    int64_t splits = blocks ? (kRopeWaves + blocks - 1) / blocks : 1;
+    if (splits > rounds) splits = rounds;
+    const int64_t share = (rounds + splits - 1) / splits;
+    t.splits = (int)((rounds + share - 1) / share);
+    int64_t groups = (blocks * t.splits + kWaves - 1) / kWaves;
+    if (groups > kRopeGroups) groups = kRopeGroups;
+    t.groups = (int)((groups + t.splits - 1) / t.splits * t.splits);  // each split as often
+    if (t.groups < 1) t.groups = 1;
   }
 }
 
@@ -387,7 +410,7 @@ hipError_t launch_rope(const RopeArgs &a, hipStream_t s) {
 hipError_t launch_rope_backward(const RopeArgs &a, hipStream_t s) {
   const hipError_t e = a.x_bf16 ? launch_typed<uint16_t, true>(a, s) : launch_typed<float, true>(a, s);
   if (e != hipSuccess || !(a.side[0].dweight || a.side[1].dweight)) return e;
-  hipLaunchKernelGGL(rope_reduce_kernel, dim3(a.dim / 8, 2), dim3(256), 0, s, a);
+  hipLaunchKernelGGL(rope_reduce_kernel, dim3(a.dim / 8, 2), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 
