@@ -32,13 +32,14 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // sub-steps (of 16 k) ahead, so that a K-tile's slots are free after half of its
 // products, and spreads the two slots' transfers over the next K-tile's worth of
 // them, one to a row of products: in bursts they held the waves up.
-template <int T>
+constexpr int slab_stride(int t) { return 32 * t + 8; }  // floats between rows of an epilogue slab
+template <int T, int SLOTS>
 struct Ns {
   static constexpr int kTile = 64 * T;
-  static constexpr int kSlots = T == 4 ? 5 : 9;
+  static constexpr int kSlots = SLOTS;
   static constexpr int kSlotBytes = kTile * 128;
   static constexpr int kMoves = 2 * T;                 // transfers of a wave to a slot
-  static constexpr int kStride = 32 * T + 8;           // floats between rows of an epilogue slab
+  static constexpr int kStride = slab_stride(T);
   static constexpr int kSlab = 32 * kStride;
   static constexpr int kLds = kSlots * kSlotBytes;
   static_assert(4 * kSlab * 4 <= kLds, "the epilogue's slabs");
@@ -67,37 +68,54 @@ __device__ __forceinline__ void multiply(f32x16 acc[T][T], const NsFrags<T> &f, 
 
 __device__ __forceinline__ void slab_fence() { asm volatile("" ::: "memory"); }
 
-// 32 rows of `row0` onwards, 32 T columns of `col0` onwards of the result, from a
-// slab of them
-template <int T>
+// One orientation of a wave's results: 32 rows at a time through its slab, from
+// which a lane takes 8 neighbouring columns.  E's elements at the same places are
+// read a slab ahead (in turn with the stores they made the square of a 5120 x 5120
+// matrix 22 us longer).  write(i) puts rows row0 + 32 i onwards into the slab.
+template <int T, typename Write>
 __device__ __forceinline__ void store_rows(const NsArgs &a, _Float16 *d, const _Float16 *e, int64_t ld, int64_t row0, int64_t col0,
-                                           const float *slab, uint32_t lane) {
-  constexpr int LANES = 4 * T, ROWS = 64 / LANES;
-  const int c = lane % LANES * 8;
-#pragma unroll 2
-  for (int r = lane / LANES; r < 32; r += ROWS) {
-    const int64_t at = (row0 + r) * ld + col0 + c;
-    float v[8];
+                                           const float *slab, uint32_t lane, Write write) {
+  constexpr int LANES = 4 * T, ROWS = 64 / LANES, TIMES = 32 / ROWS;
+  const int c = lane % LANES * 8, first = lane / LANES;
+  half8 x[TIMES];
+  const auto fetch = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = a.alpha * slab[r * Ns<T>::kStride + c + k];
+    for (int k = 0; k < TIMES; ++k) x[k] = *reinterpret_cast<const half8 *>(e + (row0 + i * 32 + k * ROWS + first) * ld + col0 + c);
+  };
+  if (e) fetch(0);
+#pragma unroll
+  for (int i = 0; i < T; ++i) {
+    write(i);
+    slab_fence();
+    float v[TIMES][8];
+#pragma unroll
+    for (int k = 0; k < TIMES; ++k)
+#pragma unroll
+      for (int b = 0; b < 8; ++b) v[k][b] = a.alpha * slab[(k * ROWS + first) * slab_stride(T) + c + b];
+    slab_fence();
     if (e) {
-      const half8 x = *reinterpret_cast<const half8 *>(e + at);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        v[k] = fmaf(a.beta, (float)x[k], v[k]);
-        if (row0 + r == col0 + c + k) v[k] += a.gamma;
-      }
+      for (int k = 0; k < TIMES; ++k)
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          v[k][b] = fmaf(a.beta, (float)x[k][b], v[k][b]);
+          if (row0 + i * 32 + k * ROWS + first == col0 + c + b) v[k][b] += a.gamma;
+        }
+      if (i + 1 < T) fetch(i + 1);
     }
-    half8 y;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = (_Float16)v[k];
-    *reinterpret_cast<half8 *>(d + at) = y;
+    for (int k = 0; k < TIMES; ++k) {
+      half8 y;
+#pragma unroll
+      for (int b = 0; b < 8; ++b) y[b] = (_Float16)v[k][b];
+      *reinterpret_cast<half8 *>(d + (row0 + i * 32 + k * ROWS + first) * ld + col0 + c) = y;
+    }
   }
 }
 
-template <int T>
+template <int T, int SLOTS>
 __global__ __launch_bounds__(256, T == 4 ? 1 : 2) void ns_product_kernel(NsArgs a) {
-  using N = Ns<T>;
+  using N = Ns<T, SLOTS>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[N::kLds];
   // the matrix and the tile
   uint32_t tile = xcd_tile(blockIdx.x, gridDim.x);
@@ -195,32 +213,22 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : 2) void ns_product_kernel(NsArgs 
 
   float *slab = reinterpret_cast<float *>(lds) + wave * N::kSlab;
   const int64_t mw = m0 + wm * (32 * T), nw = n0 + wn * (32 * T);
-  if (t.d) {
-#pragma unroll
-    for (int i = 0; i < T; ++i) {
+  if (t.d)
+    store_rows<T>(a, t.d, t.e, muon_ld(t.N), mw, nw, slab, lane, [&](int i) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < T; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) slab[((r >> 2) * 8 + h * 4 + (r & 3)) * N::kStride + j * 32 + lr] = acc[i][j][r];
-      slab_fence();
-      store_rows<T>(a, t.d, t.e, muon_ld(t.N), mw + i * 32, nw, slab, lane);
-      slab_fence();
-    }
-  }
-  if (t.dt && !(a.symmetric && m0 == n0)) {
-#pragma unroll
-    for (int j = 0; j < T; ++j) {
+    });
+  if (t.dt && !(a.symmetric && m0 == n0))
+    store_rows<T>(a, t.dt, t.e, muon_ld(t.M), nw, mw, slab, lane, [&](int j) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < T; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           *reinterpret_cast<f32x4 *>(&slab[lr * N::kStride + i * 32 + q * 8 + h * 4]) =
               (f32x4){acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-      slab_fence();
-      store_rows<T>(a, t.dt, t.e, muon_ld(t.M), nw + j * 32, mw, slab, lane);
-      slab_fence();
-    }
-  }
+    });
 }
 
 // ---------------------------------------------------------- elementwise ----
@@ -441,12 +449,17 @@ hipError_t launch_muon_product(NsArgs &a, int tile, hipStream_t s) {
     const uint32_t down = t.M / tile, across = t.N / tile;
     return a.symmetric ? down * (down + 1) / 2 : down * across;
   });
+  // Tiles of 128 that are no more than the compute units have all of LDS for
+  // transfers ahead, more share it by twos: 7 matrices of 1024 x 1152 take 19.5 and
+  // 23 us for the 252 tiles of a square, 34 and 27 for the 504 of the last product.
   if (tile == 256)
-    hipLaunchKernelGGL((ns_product_kernel<4>), dim3(n), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((ns_product_kernel<4, 5>), dim3(n), dim3(256), 0, s, a);
+  else if (tile == 128 && n > 256)
+    hipLaunchKernelGGL((ns_product_kernel<2, 5>), dim3(n), dim3(256), 0, s, a);
   else if (tile == 128)
-    hipLaunchKernelGGL((ns_product_kernel<2>), dim3(n), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((ns_product_kernel<2, 9>), dim3(n), dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL((ns_product_kernel<1>), dim3(n), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((ns_product_kernel<1, 9>), dim3(n), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
