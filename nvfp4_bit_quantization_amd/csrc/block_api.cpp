@@ -235,28 +235,63 @@ bool muon_bounded(const nvfp4_muon_config &c) {
 
 int64_t round_up(int64_t n, int64_t by) { return (n + by - 1) / by * by; }
 
-// rows and columns of a workgroup's tiles of this matrix
-int muon_tile(const nvfp4_muon_tensor &t) {
-  const int64_t m = t.rows < t.cols ? t.rows : t.cols;
-  return m >= 1536 ? 256 : m >= 512 ? 128 : 64;
+// What a matrix's sides are padded to multiples of: the largest tile that costs no
+// more than a sixteenth over the smallest's padding.
+int muon_pad(const nvfp4_muon_tensor &t) {
+  for (const int tile : {256, 128})
+    if (16 * round_up(t.rows, tile) * round_up(t.cols, tile) <= 17 * round_up(t.rows, 64) * round_up(t.cols, 64)) return tile;
+  return 64;
 }
 
-// The matrices [first, last) of the list that have one tile size, those of a group:
-// as many as a launch takes, or whose last product has eight rounds of tiles.
-// `bytes` of workspace are counted; with a base it is dealt out.
+// Tiles of a product of the group: those that take least by these times in us, as
+// measured (one product of 7 matrices of 1024 x 1152, 1 of 2048 x 2048, 1 of 4096 x
+// 4096 and others at every tile size): a fixed part, and per 64 of K the longer of
+// one tile's own time and what the chip needs for all of them, 256 at a time.
+// E. g. X X^T of 2048 x 2048: 46 us in tiles of 256, 21 of 128, 26 of 64; the last
+// product of 4096 x 4096: 124, 157, 279.
+int muon_tile(const NsArgs &p, int pad) {
+  struct Cost {
+    int tile;
+    double fixed, own, all;
+  };
+  constexpr Cost costs[3] = {{256, 8.0, 1.2, 1.7}, {128, 5.5, 0.46, 0.70}, {64, 4.0, 0.25, 0.29}};
+  double least = 0.0;
+  int best = 0;
+  for (const Cost &c : costs) {
+    if (c.tile > pad) continue;
+    int64_t tiles = 0, k = 0;
+    for (int i = 0; i < p.count; ++i) {
+      const int64_t down = p.mat[i].M / c.tile, across = p.mat[i].N / c.tile;
+      const int64_t n = p.symmetric ? down * (down + 1) / 2 : down * across;
+      tiles += n;
+      k += n * (p.mat[i].K / 64);
+    }
+    // a compute unit holds one of the large tiles, but several of the others
+    const double rounds = c.tile == 256 ? (double)((tiles + 255) / 256) : (double)tiles / 256.0;
+    const double us = c.fixed + (double)k / (double)tiles * fmax(c.own, rounds * c.all);
+    if (!best || us < least) {
+      best = c.tile;
+      least = us;
+    }
+  }
+  return best;
+}
+
+// The matrices of the list with one padding, from `from` on, that make a group: as
+// many as a launch takes, or 2^27 elements.
 struct MuonGroup {
   int64_t index[kMuonMats];
   int count = 0;
   int64_t next = 0;  // where to go on in the list
 };
-MuonGroup muon_group(const nvfp4_muon_tensor *tensors, int64_t n, int64_t from, int tile) {
+MuonGroup muon_group(const nvfp4_muon_tensor *tensors, int64_t n, int64_t from, int pad) {
   MuonGroup g;
-  int64_t tiles = 0, i = from;
-  for (; i < n && g.count < kMuonMats && tiles < 2048; ++i) {
+  int64_t elements = 0, i = from;
+  for (; i < n && g.count < kMuonMats && elements < ((int64_t)1 << 27); ++i) {
     const nvfp4_muon_tensor &t = tensors[i];
-    if (!t.rows || !t.cols || muon_tile(t) != tile) continue;
+    if (!t.rows || !t.cols || muon_pad(t) != pad) continue;
     g.index[g.count++] = i;
-    tiles += (t.rows + tile - 1) / tile * ((t.cols + tile - 1) / tile);
+    elements += t.rows * t.cols;
   }
   g.next = i;
   return g;
@@ -265,8 +300,8 @@ struct MuonBuffers {
   double *parts;
   _Float16 *x, *xt[2], *a, *b;
 };
-size_t muon_buffers(const nvfp4_muon_tensor &t, int tile, char *base, size_t used, MuonBuffers &o) {
-  const int64_t m = round_up(t.rows < t.cols ? t.rows : t.cols, tile), n = round_up(t.rows < t.cols ? t.cols : t.rows, tile);
+size_t muon_buffers(const nvfp4_muon_tensor &t, int pad, char *base, size_t used, MuonBuffers &o) {
+  const int64_t m = round_up(t.rows < t.cols ? t.rows : t.cols, pad), n = round_up(t.rows < t.cols ? t.cols : t.rows, pad);
   const auto take = [&](size_t bytes) {
     char *p = base ? base + used : nullptr;
     used += (bytes + 255) & ~(size_t)255;
@@ -280,15 +315,15 @@ size_t muon_buffers(const nvfp4_muon_tensor &t, int tile, char *base, size_t use
   o.b = (_Float16 *)take((size_t)(m * muon_ld(m)) * 2);
   return used;
 }
-constexpr int kTiles[3] = {256, 128, 64};
+constexpr int kPads[3] = {256, 128, 64};
 
-hipError_t muon_run(const nvfp4_muon_tensor *tensors, const MuonGroup &g, int tile, const nvfp4_muon_config &c, MuonArgs &a,
+hipError_t muon_run(const nvfp4_muon_tensor *tensors, const MuonGroup &g, int pad, const nvfp4_muon_config &c, MuonArgs &a,
                     char *base, hipStream_t s) {
   MuonBuffers buf[kMuonMats];
   size_t used = 0;
   for (int i = 0; i < g.count; ++i) {
     const nvfp4_muon_tensor &t = tensors[g.index[i]];
-    used = muon_buffers(t, tile, base, used, buf[i]);
+    used = muon_buffers(t, pad, base, used, buf[i]);
     const bool turned = t.rows > t.cols;
     MuonMat &d = a.mat[i];
     d.grad = t.grad;
@@ -302,8 +337,8 @@ hipError_t muon_run(const nvfp4_muon_tensor *tensors, const MuonGroup &g, int ti
     d.parts = buf[i].parts;
     d.rows = (int)t.rows;
     d.cols = (int)t.cols;
-    d.rp = (int)round_up(t.rows, tile);
-    d.cp = (int)round_up(t.cols, tile);
+    d.rp = (int)round_up(t.rows, pad);
+    d.cp = (int)round_up(t.cols, pad);
     d.keep = (float)(1.0 - (double)c.lr * t.weight_decay);
     d.step = (float)((double)c.lr * t.scale);
     d.flags = (t.param_dtype == NVFP4_BF16 ? MF_PARAM_BF16 : 0u) | (t.grad_dtype == NVFP4_BF16 ? MF_GRAD_BF16 : 0u) |
@@ -335,7 +370,7 @@ hipError_t muon_run(const nvfp4_muon_tensor *tensors, const MuonGroup &g, int ti
       p.alpha = (float)(stage == 0 ? ka / (kx * kx) : stage == 1 ? c.c / ka : 1.0 / ka);
       p.beta = (float)c.b;
       p.gamma = (float)(c.a * ka);
-      e = launch_muon_product(p, tile, s);
+      e = launch_muon_product(p, muon_tile(p, pad), s);
     }
   }
   for (int i = 0; i < g.count; ++i)
@@ -432,12 +467,12 @@ size_t nvfp4_muon_workspace_bytes(const nvfp4_muon_tensor *tensors, int64_t n_te
   for (int64_t i = 0; i < n_tensors; ++i)
     if (check_muon(tensors[i], false) != NVFP4_OK) return 0;
   size_t most = 0;
-  for (const int tile : kTiles)
+  for (const int pad : kPads)
     for (int64_t at = 0; at < n_tensors;) {
-      const MuonGroup g = muon_group(tensors, n_tensors, at, tile);
+      const MuonGroup g = muon_group(tensors, n_tensors, at, pad);
       size_t used = 0;
       MuonBuffers b;
-      for (int i = 0; i < g.count; ++i) used = muon_buffers(tensors[g.index[i]], tile, nullptr, used, b);
+      for (int i = 0; i < g.count; ++i) used = muon_buffers(tensors[g.index[i]], pad, nullptr, used, b);
       if (used > most) most = used;
       at = g.next;
     }
@@ -470,11 +505,11 @@ int nvfp4_muon(const nvfp4_muon_tensor *tensors, int64_t n_tensors, const nvfp4_
   a.tag = 0x4D550000u + (uint32_t)(c->step >> 32);
   a.grad_scale = c->grad_scale;
   hipStream_t s = (hipStream_t)stream;
-  for (const int tile : kTiles)
+  for (const int pad : kPads)
     for (int64_t at = 0; at < n_tensors;) {
-      const MuonGroup g = muon_group(tensors, n_tensors, at, tile);
+      const MuonGroup g = muon_group(tensors, n_tensors, at, pad);
       at = g.next;
-      if (g.count && muon_run(tensors, g, tile, *c, a, (char *)workspace, s) != hipSuccess) return NVFP4_E_HIP;
+      if (g.count && muon_run(tensors, g, pad, *c, a, (char *)workspace, s) != hipSuccess) return NVFP4_E_HIP;
     }
   return finish(hipSuccess, s);
 }

@@ -72,7 +72,7 @@ __device__ __forceinline__ void slab_fence() { asm volatile("" ::: "memory"); }
 // which a lane takes 8 neighbouring columns.  E's elements at the same places are
 // read a slab ahead (in turn with the stores they made the square of a 5120 x 5120
 // matrix 22 us longer).  write(i) puts rows row0 + 32 i onwards into the slab.
-template <int T, typename Write>
+template <int T, bool E, typename Write>
 __device__ __forceinline__ void store_rows(const NsArgs &a, _Float16 *d, const _Float16 *e, int64_t ld, int64_t row0, int64_t col0,
                                            const float *slab, uint32_t lane, Write write) {
   constexpr int LANES = 4 * T, ROWS = 64 / LANES, TIMES = 32 / ROWS;
@@ -82,7 +82,7 @@ __device__ __forceinline__ void store_rows(const NsArgs &a, _Float16 *d, const _
 #pragma unroll
     for (int k = 0; k < TIMES; ++k) x[k] = *reinterpret_cast<const half8 *>(e + (row0 + i * 32 + k * ROWS + first) * ld + col0 + c);
   };
-  if (e) fetch(0);
+  if (E) fetch(0);
 #pragma unroll
   for (int i = 0; i < T; ++i) {
     write(i);
@@ -93,7 +93,7 @@ __device__ __forceinline__ void store_rows(const NsArgs &a, _Float16 *d, const _
 #pragma unroll
       for (int b = 0; b < 8; ++b) v[k][b] = a.alpha * slab[(k * ROWS + first) * slab_stride(T) + c + b];
     slab_fence();
-    if (e) {
+    if (E) {
 #pragma unroll
       for (int k = 0; k < TIMES; ++k)
 #pragma unroll
@@ -113,7 +113,7 @@ __device__ __forceinline__ void store_rows(const NsArgs &a, _Float16 *d, const _
   }
 }
 
-template <int T, int SLOTS>
+template <int T, int SLOTS, bool E>
 __global__ __launch_bounds__(256, T == 4 ? 1 : 2) void ns_product_kernel(NsArgs a) {
   using N = Ns<T, SLOTS>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[N::kLds];
@@ -214,14 +214,14 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : 2) void ns_product_kernel(NsArgs 
   float *slab = reinterpret_cast<float *>(lds) + wave * N::kSlab;
   const int64_t mw = m0 + wm * (32 * T), nw = n0 + wn * (32 * T);
   if (t.d)
-    store_rows<T>(a, t.d, t.e, muon_ld(t.N), mw, nw, slab, lane, [&](int i) __attribute__((always_inline)) {
+    store_rows<T, E>(a, t.d, t.e, muon_ld(t.N), mw, nw, slab, lane, [&](int i) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < T; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) slab[((r >> 2) * 8 + h * 4 + (r & 3)) * N::kStride + j * 32 + lr] = acc[i][j][r];
     });
   if (t.dt && !(a.symmetric && m0 == n0))
-    store_rows<T>(a, t.dt, t.e, muon_ld(t.M), nw, mw, slab, lane, [&](int j) __attribute__((always_inline)) {
+    store_rows<T, E>(a, t.dt, t.e, muon_ld(t.M), nw, mw, slab, lane, [&](int j) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < T; ++i)
 #pragma unroll
@@ -425,6 +425,13 @@ uint32_t fill_ends(Args &a, Count count) {
   for (int i = 0; i < kMuonMats; ++i) a.end[i] = i < a.count ? end += count(a.mat[i]) : ~0u;
   return end;
 }
+template <int T, int SLOTS>
+void launch_product(const NsArgs &a, uint32_t n, hipStream_t s) {
+  if (a.mat[0].e)
+    hipLaunchKernelGGL((ns_product_kernel<T, SLOTS, true>), dim3(n), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((ns_product_kernel<T, SLOTS, false>), dim3(n), dim3(256), 0, s, a);
+}
 uint32_t chunks(const MuonMat &t) { return (uint32_t)(((int64_t)t.rows * t.cols + kMuonChunk - 1) / kMuonChunk); }
 
 }  // namespace
@@ -452,14 +459,17 @@ hipError_t launch_muon_product(NsArgs &a, int tile, hipStream_t s) {
   // Tiles of 128 that are no more than the compute units have all of LDS for
   // transfers ahead, more share it by twos: 7 matrices of 1024 x 1152 take 19.5 and
   // 23 us for the 252 tiles of a square, 34 and 27 for the 504 of the last product.
+  // Tiles of 64 likewise, by twos and fours.
   if (tile == 256)
-    hipLaunchKernelGGL((ns_product_kernel<4, 5>), dim3(n), dim3(256), 0, s, a);
+    launch_product<4, 5>(a, n, s);
   else if (tile == 128 && n > 256)
-    hipLaunchKernelGGL((ns_product_kernel<2, 5>), dim3(n), dim3(256), 0, s, a);
+    launch_product<2, 5>(a, n, s);
   else if (tile == 128)
-    hipLaunchKernelGGL((ns_product_kernel<2, 9>), dim3(n), dim3(256), 0, s, a);
+    launch_product<2, 9>(a, n, s);
+  else if (n > 512)
+    launch_product<1, 5>(a, n, s);
   else
-    hipLaunchKernelGGL((ns_product_kernel<1, 9>), dim3(n), dim3(256), 0, s, a);
+    launch_product<1, 9>(a, n, s);
   return hipGetLastError();
 }
 
