@@ -162,8 +162,11 @@ int check_matrix(const nvfp4_gated_matrix *t, int64_t cols) {
   return NVFP4_OK;
 }
 
-// one workgroup per 128 x 64 outputs at most: the grid counts its threads in 32 bits
-bool gated_grid_ok(int64_t M, int64_t N) { return (M / 16 + 1) * (N / 16 + 1) / 32 < ((int64_t)1 << 24); }
+// a launch counts its threads in 32 bits, 256 to a workgroup: of 16 columns (up to
+// 64 rows), or of at least 128 x 64 outputs
+bool gated_grid_ok(int64_t M, int64_t N) {
+  return (M <= 64 ? N / 16 : (M + 127) / 128 * ((N + 63) / 64)) < ((int64_t)1 << 24);
+}
 
 GatedArgs gated_args(const nvfp4_tensor *a, const nvfp4_tensor *b, int32_t activation, uint64_t rht_seed) {
   GatedArgs r = {};

@@ -181,6 +181,10 @@ def test_gated_shapes_and_activations(L):
     big = _tensor(1 << 24)
     assert _gated(L, a=big, g=big, u=big, h=_matrix(2, ld=1 << 24)) == SHAPE
     assert _gated_back(L, a=big, b=big) == SHAPE
+    wide = _tensor(1 << 28)
+    for rows in (16, 64):
+        assert _gated(L, a=_tensor(rows), g=wide, u=wide, h=_matrix(2, ld=1 << 28)) == SHAPE
+        assert _gated_back(L, a=_tensor(rows), b=wide) == SHAPE
 
 
 MATRICES = [(_matrix(0), NULL), (_matrix(9, ld=40), LD), (_matrix(9, ld=52), ALIGN), (nv.nvfp4_gated_matrix(FAKE + 8, 64, None, None), ALIGN),
