@@ -1050,33 +1050,43 @@ def _rope_tensor(t, like, device, what, dtype=None):
 
 
 def _rope_common(ref, freqs, positions, cu, q_weight, k_weight, k):
-    """(tail of the C arguments before the scalars, rot_dim, w_dtype, device) of the checked common inputs."""
+    """(tail of the C arguments before the scalars, w_dtype, device) of the checked common inputs."""
     import torch
-    shape, device = ref.shape, _on_device(ref, "q")
-    if len(shape) != (4 if cu is None else 3) and not (cu is None and positions is not None and len(shape) == 3):
+    shape, device = ref.shape, ref.get_device()
+    if device < 0:
+        raise ValueError("q: a device tensor is wanted")
+    if len(shape) == 4 and cu is None:
+        batch, tokens = shape[0], shape[1]
+    elif len(shape) == 3 and (cu is not None or positions is not None):
+        batch, tokens = 1, shape[0]
+    else:
         raise ValueError("q: [batch][tokens][heads][dim] is wanted, or [tokens][heads][dim] with cu or positions")
-    batch, tokens = (shape[0], shape[1]) if len(shape) == 4 else (1, shape[0])
+    at = begin = turns = rot = 0
     if positions is not None:
-        _vector(positions, batch * tokens, device, "positions", torch.int64)
-    if cu is not None:
-        if positions is not None:
+        if cu is not None:
             raise ValueError("positions or cu is wanted, not both")
-        _vector(cu, cu.numel(), device, "cu", torch.int32)
+        _vector(positions, batch * tokens, device, "positions", torch.int64)
+        at = positions.data_ptr()
+    elif cu is not None:
         batch = cu.numel() - 1
-    rot = 0
+        _vector(cu, batch + 1, device, "cu", torch.int32)
+        begin = cu.data_ptr()
+    elif batch == 0:
+        batch, tokens = 1, 0
     if freqs is not None:
-        rot = 2 * freqs.numel()
-        _vector(freqs, rot // 2, device, "freqs", torch.float64)
-    if k is not None and (q_weight is None) != (k_weight is None):
-        raise ValueError("weights: both or neither are wanted")
-    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _vector(w, shape[-1], device, what)
-            if q_weight is not None and w.dtype != q_weight.dtype:
-                raise TypeError("%s: %s is wanted, not %s" % (what, q_weight.dtype, w.dtype))
-    w_dtype = F32 if q_weight is None else _dtype(q_weight)
-    return (max(batch, 1) if cu is None else batch, tokens if batch else 0, _ptr(positions), _ptr(cu), _ptr(freqs), shape[-1],
-            rot), w_dtype, device
+        rot = freqs.numel()
+        _vector(freqs, rot, device, "freqs", torch.float64)
+        turns, rot = freqs.data_ptr(), 2 * rot
+    w_dtype = F32
+    if q_weight is not None:
+        _vector(q_weight, shape[-1], device, "q_weight")
+        w_dtype = _dtype(q_weight)
+    if k is not None:
+        if (q_weight is None) != (k_weight is None):
+            raise ValueError("weights: both or neither are wanted")
+        if k_weight is not None:
+            _vector(k_weight, shape[-1], device, "k_weight", q_weight.dtype)
+    return (batch, tokens, at, begin, turns, shape[-1], rot), w_dtype, device
 
 
 def nvfp4_qk_rope(q, k, q_out, k_out, freqs, positions=None, cu=None, q_weight=None, k_weight=None, eps=1e-6,
@@ -1117,7 +1127,8 @@ def qk_rope(q, k, freqs, positions=None, cu=None, q_weight=None, k_weight=None, 
     import torch
     common, w_dtype, device = _rope_common(q, freqs, positions, cu, q_weight, k_weight, k)
     dense = torch.contiguous_format
-    _rope_tensor(q, q.shape, device, "q")
+    if q.stride(-1) != 1:
+        raise ValueError("q: a contiguous last dimension is wanted")
     q_out, k_out = torch.empty_like(q, dtype=torch.bfloat16, memory_format=dense), None
     if k is not None:
         _rope_tensor(k, q.shape, device, "k", q.dtype)

@@ -174,9 +174,14 @@ __device__ __forceinline__ bool place_of(const RopeArgs &a, int64_t base, int sl
 template <typename W>
 __device__ __forceinline__ void load_weight(const W *w, const Segments &s, float out[2][8]) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+  for (int k = 0; k < 2; ++k) {
+    if (s.len[k] == 8) {
+      load8(w + s.at[k], out[k]);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) out[k][j] = j < s.len[k] ? load1(w + s.at[k] + j) : 0.0f;
+      for (int j = 0; j < 8; ++j) out[k][j] = j < s.len[k] ? load1(w + s.at[k] + j) : 0.0f;
+    }
+  }
 }
 
 // v turned by the lane's angles (forward) or back (s of the other sign)
@@ -225,6 +230,13 @@ __global__ __launch_bounds__(kWaves * 64, G ? 3 : 4) void rope_kernel(RopeArgs a
     double position;
     const bool placed = place_of(a, base, slot, at_once, ends, b, n, position);
     const bool live = used && base + slot < a.total && placed;
+    const TX *x = (const TX *)t.x + (live ? b * t.x_b + n * t.x_t + sub * t.x_h : 0);
+    uint16_t *y = t.y + (live ? b * t.y_b + n * t.y_t + sub * t.y_h : 0);
+    TX *dx = G ? (TX *)t.dx + (live ? b * t.dx_b + n * t.dx_t + sub * t.dx_h : 0) : nullptr;
+    Raw<TX> rx[2];  // the first heads are on their way while the angles are formed
+    Raw<uint16_t> ry[2];
+    if (!G || N) fetch<R>(x + h0 * t.x_h, seg, live, rx);
+    if (G) fetch<R>(y + h0 * t.y_h, seg, live, ry);
     float c[8], s[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -232,13 +244,6 @@ __global__ __launch_bounds__(kWaves * 64, G ? 3 : 4) void rope_kernel(RopeArgs a
       s[j] = 0.0f;
       if (live && seg.first >= 0 && seg.first + j < a.rot / 2) turn(position * f[j], a.magnitude, c[j], s[j]);
     }
-    const TX *x = (const TX *)t.x + (live ? b * t.x_b + n * t.x_t + sub * t.x_h : 0);
-    uint16_t *y = t.y + (live ? b * t.y_b + n * t.y_t + sub * t.y_h : 0);
-    TX *dx = G ? (TX *)t.dx + (live ? b * t.dx_b + n * t.dx_t + sub * t.dx_h : 0) : nullptr;
-    Raw<TX> rx[2];
-    Raw<uint16_t> ry[2];
-    if (!G || N) fetch<R>(x + h0 * t.x_h, seg, live, rx);
-    if (G) fetch<R>(y + h0 * t.y_h, seg, live, ry);
     for (int h = h0; h < h1; h += per) {
       float v[2][8], g[2][8];
 #pragma unroll
