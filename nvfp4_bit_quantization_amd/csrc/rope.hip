@@ -15,8 +15,8 @@
 //
 // Both passes are bound by memory: 2 x 8192 tokens of 40 + 8 heads of 128 bf16 move
 // 403 MB in 81 us (5.0 TB/s), the gradient 604 MB in 122 (4.9), where a copy of 2 GiB
-// reaches 4.9.  Few tokens take what a launch does: 5 us for 16.  Narrow heads with a
-// short rotated part are bound by the vector unit, most of it the angles.
+// reaches 4.9.  Few tokens take what a launch does: 5 us for 16.  4096 tokens are bound
+// by a wave's own chain (places, angles, three heads after another): half of it waits.
 #include "block_kernels.hpp"
 #include "train_device.hpp"
 
@@ -389,13 +389,13 @@ hipError_t launch_typed(const RopeArgs &a, hipStream_t s) {
 
 }  // namespace
 
-// Waves that share out heads where tokens are few (2048: 4096 packed tokens of 10 + 5
-// float32 heads of 80, backward, 28.7 us; 4096: 29.9), and workgroups of a side at
+// Waves that share out heads where tokens are few (1024: 4096 packed tokens of 10 + 5
+// float32 heads of 80, backward, 24.7 us; 2048: 28.7, 4096: 29.9), and workgroups of a side at
 // most, which then go on to further tokens: two to a compute unit keep the weights
 // and frequencies that they hold in use and leave no short last round (2 x 8192
 // tokens, 40 + 8 heads of 128: 80.9 us and 122 backward; 256: 109 and 130, 384: 88
 // and 128, 768: 87 and 129, 1280: 86 and 133).
-constexpr int64_t kRopeWaves = 2048, kRopeGroups = 512;
+constexpr int64_t kRopeWaves = 1024, kRopeGroups = 512;
 
 int rope_lanes(int units) { return units <= 4 ? 4 : units <= 8 ? 8 : 16; }
 
