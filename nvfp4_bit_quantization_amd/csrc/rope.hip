@@ -353,37 +353,35 @@ __global__ __launch_bounds__(1024) void rope_reduce_kernel(RopeArgs a) {
   }
 }
 
-// some segment is shorter than 8
+// some segment is shorter than 8 (heads are of multiples of 8)
 bool ragged(const RopeArgs &a) { return a.interleaved ? false : a.rot % 16 != 0; }
 
-template <typename TX, int L, bool I, bool G>
+template <typename TX, int L, bool I, bool G, bool R>
 void launch_of(const RopeArgs &a, dim3 grid, hipStream_t s) {
-  const bool n = a.side[0].weight || a.side[1].weight, r = ragged(a);
-  const dim3 block(kWaves * 64);
-  if (n && r)
-    hipLaunchKernelGGL((rope_kernel<TX, L, I, G, true, !I>), grid, block, 0, s, a);
-  else if (n)
-    hipLaunchKernelGGL((rope_kernel<TX, L, I, G, true, false>), grid, block, 0, s, a);
-  else if (r)
-    hipLaunchKernelGGL((rope_kernel<TX, L, I, G, false, !I>), grid, block, 0, s, a);
+  if (a.side[0].weight || a.side[1].weight)
+    hipLaunchKernelGGL((rope_kernel<TX, L, I, G, true, R>), grid, dim3(kWaves * 64), 0, s, a);
   else
-    hipLaunchKernelGGL((rope_kernel<TX, L, I, G, false, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((rope_kernel<TX, L, I, G, false, R>), grid, dim3(kWaves * 64), 0, s, a);
 }
 template <typename TX, bool G>
 hipError_t launch_typed(const RopeArgs &a, hipStream_t s) {
   const dim3 grid(a.side[0].groups + a.side[1].groups);
   const int l = rope_lanes(a.units);
-#define NVFP4_ROPE(L)                                                  \
-  if (l == L) {                                                        \
-    if (a.interleaved)                                                 \
-      launch_of<TX, L, true, G>(a, grid, s);                           \
-    else                                                               \
-      launch_of<TX, L, false, G>(a, grid, s);                          \
-  }
-  NVFP4_ROPE(4)
-  NVFP4_ROPE(8)
-  NVFP4_ROPE(16)
-#undef NVFP4_ROPE
+  const bool r = ragged(a);
+  if (a.interleaved && l == 4)
+    launch_of<TX, 4, true, G, false>(a, grid, s);
+  else if (a.interleaved)
+    launch_of<TX, 8, true, G, false>(a, grid, s);
+  else if (l == 4 && r)
+    launch_of<TX, 4, false, G, true>(a, grid, s);
+  else if (l == 4)
+    launch_of<TX, 4, false, G, false>(a, grid, s);
+  else if (l == 8 && r)
+    launch_of<TX, 8, false, G, true>(a, grid, s);
+  else if (l == 8)
+    launch_of<TX, 8, false, G, false>(a, grid, s);
+  else
+    launch_of<TX, 16, false, G, true>(a, grid, s);
   return hipGetLastError();
 }
 
@@ -397,6 +395,7 @@ hipError_t launch_typed(const RopeArgs &a, hipStream_t s) {
 // and 128, 768: 87 and 129, 1280: 86 and 133).
 constexpr int64_t kRopeWaves = 1024, kRopeGroups = 512;
 
+// up to 8 units of 16 elements; a ninth where a head of 128 has a segment cut short
 int rope_lanes(int units) { return units <= 4 ? 4 : units <= 8 ? 8 : 16; }
 
 void rope_plan(RopeArgs &a) {

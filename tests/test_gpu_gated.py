@@ -179,6 +179,61 @@ def test_in_place_and_strides(nv):
         assert torch.equal(wide[:m, 8:n + 8], h) and (wide[m:] == 5.0).all() and (wide[:, :8] == 5.0).all() and (wide[:, n + 8:] == 5.0).all()
 
 
+# (M, N, K) of the tiles of 256 rows: whole ones, then rows and columns that end inside a tile; K of one K-tile and of several
+LARGE = [(1024, 5120, 128), (1040, 5136, 128), (1040, 5136, 640)]
+LARGE_BACK = [(1024, 10240, 128), (1040, 10256, 128), (1040, 10256, 640)]
+
+
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+@pytest.mark.parametrize("kind", ["silu", "gelu", "gelu_tanh", "relu"])
+def test_forward_of_large_tiles(nv, shape, kind):
+    test_forward(nv, shape, kind)
+
+
+@pytest.mark.parametrize("shape", LARGE_BACK, ids=str)
+@pytest.mark.parametrize("kind", ["silu", "gelu", "gelu_tanh", "relu"])
+def test_gradient_of_large_tiles(nv, shape, kind):
+    test_gradient(nv, shape, kind)
+
+
+def test_large_tiles_maxima_places_and_graphs(nv):
+    """As the tests of these for the other sizes."""
+    say("gated large tiles")
+    (m, n, k), wide = LARGE[1], LARGE_BACK[1][1]
+    a, wg, wu = operand(nv, m, k, "row", 1), operand(nv, n, k, "2d", 2, k ** -0.5), operand(nv, n, k, "2d", 3, k ** -0.5)
+    top = torch.zeros(1, device="cuda")
+    h, gate, up = nv.gemm_gated(a, wg, wu, amax_rht_col=top, rht_seed=77)
+    want = nv.quantize(h, [nv.QuantSpec.of("col", "rtn", True, 0, 77)])[0].amax
+    assert abs(top.item() / want.item() - 1) < 2.0 ** -18
+    buffer = torch.full((m + 16, n + 24), 5.0, dtype=torch.bfloat16, device="cuda")
+    nv.nvfp4_gemm_gated(a, wg, wu, buffer[:m, 8:n + 8])
+    assert torch.equal(buffer[:m, 8:n + 8], h)
+    assert (buffer[m:] == 5.0).all() and (buffer[:, :8] == 5.0).all() and (buffer[:, n + 8:] == 5.0).all()
+    d, w = operand(nv, m, k, "row", 4, 1e-3), operand(nv, wide, k, "2d", 5)
+    both = torch.randn(m, 2 * wide, device="cuda").to(torch.bfloat16)
+    gate, up = both[:, :wide], both[:, wide:]
+    tops = torch.zeros(4, 1, device="cuda").unbind()
+    want = nv.gemm_gated_backward(d, w, gate, up, amax_gate=tops[0], amax_up=tops[1], amax_rht_gate=tops[2], amax_rht_up=tops[3],
+                                  rht_seed=77)
+    for t, plain, rht in ((want[0], tops[0], tops[2]), (want[1], tops[1], tops[3])):
+        assert plain.item() == t.abs().max().item()
+        assert abs(rht.item() / nv.quantize(t, [nv.QuantSpec.of("col", "rtn", True, 0, 77)])[0].amax.item() - 1) < 2.0 ** -18
+    turned = both.clone()
+    nv.nvfp4_gemm_gated_backward(d, w, turned[:, :wide], turned[:, wide:], turned[:, wide:], turned[:, :wide])
+    assert torch.equal(turned[:, wide:], want[0]) and torch.equal(turned[:, :wide], want[1])
+    s = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        held, held_grads = nv.gemm_gated(a, wg, wu), nv.gemm_gated_backward(d, w, gate, up)
+    for turn in range(3):
+        a.codes.copy_(a.codes.roll(1, 0))
+        d.codes.copy_(d.codes.roll(1, 0))
+        graph.replay()
+        now, grads = nv.gemm_gated(a, wg, wu), nv.gemm_gated_backward(d, w, gate, up)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip((*now, *grads), (*held, *held_grads)))
+
+
 def test_one_quantised_tensor_of_both_weights(nv):
     """Gate and up as the two halves of one quantised weight."""
     say("gated halves of one weight")

@@ -126,6 +126,21 @@ def test_many_matrices_at_once(nv):
             near(y, orthogonal(x.double()), str(tuple(x.shape)))
 
 
+# (matrices, rows, columns): lists whose products go in tiles of 256; of 128 and of 64, many to a compute unit, upright and flat
+LISTS = [(5, 2040, 2290), (5, 2290, 2040), (8, 1000, 1111), (20, 512, 500), (30, 300, 310), (20, 440, 445)]
+
+
+@pytest.mark.parametrize("count,rows,cols", LISTS, ids=str)
+def test_lists_of_one_size(nv, count, rows, cols):
+    say("orthogonalize a list", count, rows, cols)
+    xs = [matrix(rows, cols, 50 + i, torch.bfloat16 if i % 2 else torch.float32) for i in range(count)]
+    out = nv.orthogonalize(xs)
+    for i, (x, y) in enumerate(zip(xs, out)):
+        near(y, orthogonal(x.double()), "matrix %d" % i)
+    for x, y in zip(out, nv.orthogonalize(xs)):
+        assert torch.equal(x, y)
+
+
 def uniforms(n, index, step, seed):
     group = torch.arange((n + 7) // 8, device="cuda", dtype=torch.int64)
     low = 0xFFFFFFFF

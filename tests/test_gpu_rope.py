@@ -109,6 +109,18 @@ def test_forward_and_gradient(nv, case):
             assert dw is None
 
 
+# (dim, rot, interleaved): heads of up to 4, 8 and 16 lanes, with whole segments of 8 and with some cut short
+LAYOUTS = [(64, 64, False), (56, 16, False), (32, 20, False), (64, 12, False), (48, 30, True), (128, 128, False), (88, 48, False),
+           (80, 20, False), (128, 72, False), (128, 100, True), (72, 72, True), (128, 8, False), (128, 2, False)]
+
+
+@pytest.mark.parametrize("layout", LAYOUTS, ids=str)
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("dtype", [B, F], ids=str)
+def test_layouts(nv, layout, norm, dtype):
+    test_forward_and_gradient(nv, (21, 6, 3, *layout, norm, dtype, F))
+
+
 def test_gradient_against_differences(nv):
     """The gradient's product with a direction is what the definition changes along it."""
     say("rope differences")
