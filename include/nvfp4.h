@@ -702,7 +702,9 @@ typedef struct {
  * refused (NVFP4_E_VALUE).
  * Momentum, norm (binary64 sums) and parameters are binary32; the iteration's
  * matrices are held in fp16 with powers of two as scales, their products summed
- * in binary32: X is off by 1e-3 to 3e-3 of its norm.  bf16 params under NVFP4_SR add
+ * in binary32: X is off by 1e-3 to 3e-3 of its norm, by more (2e-2) where most
+ * singular values of u are below 2^-11 of its norm over the root of the smaller side,
+ * which rounding buries.  bf16 params under NVFP4_SR add
  * 16 uniform bits below the kept ones and truncate; those of element i (row-major)
  * of tensor index (its place in `tensors`) are half i & 1 of word (i mod 8) / 2 of
  * Philox4x32-10(key = seed, counter = (i / 8 mod 2^32, index, step mod 2^32,
@@ -713,7 +715,8 @@ typedef struct {
  *              scratch, 16-byte aligned, not initialised
  * Arrays need their elements' alignment.  lr, step and the other scalars are taken
  * at the call: a captured graph repeats them.  3 + 3 steps kernels for every group
- * of up to 30 matrices (fewer where they are large).
+ * of up to 30 matrices (fewer where they are large), up to 3 + 4 steps for those
+ * with a smaller side of 1024 and more and another half as long again.
  */
 int nvfp4_muon(const nvfp4_muon_tensor *tensors, int64_t n_tensors, const nvfp4_muon_config *config, void *workspace,
                size_t workspace_bytes, void *stream);

@@ -211,15 +211,17 @@ int check_muon(const nvfp4_muon_tensor &t, bool buffers) {
 
 // Whether the iteration's singular values, from [0, 1], stay where fp16 holds its
 // matrices: s p(s^2) is extreme at the ends and where its derivative vanishes,
-// p(s^2) at the ends and at s^2 = -b / 2 c.
-bool muon_bounded(const nvfp4_muon_config &c) {
+// p(s^2) at the ends and at s^2 = -b / 2 c.  most[k]: the largest |p| of step k.
+bool muon_bounded(const nvfp4_muon_config &c, double *most) {
   const auto p = [&](double q) { return c.a + q * (c.b + q * c.c); };
   double top = 1.0;
   for (int k = 0; k < c.steps; ++k) {
     double next = 0.0;
+    most[k] = 0.0;
     const auto look = [&](double q, bool turn) {
       if (!(q >= 0.0 && q <= top * top)) return true;
       if (!turn) next = fmax(next, sqrt(q) * fabs(p(q)));
+      most[k] = fmax(most[k], fabs(p(q)));
       return fabs(p(q)) <= 14.0;
     };
     bool good = look(0.0, false) && look(top * top, false);
@@ -244,6 +246,32 @@ int muon_pad(const nvfp4_muon_tensor &t) {
   for (const int tile : {256, 128})
     if (16 * round_up(t.rows, tile) * round_up(t.cols, tile) <= 17 * round_up(t.rows, 64) * round_up(t.cols, 64)) return tile;
   return 64;
+}
+
+// Whether steps of a matrix, m x n with m <= n, are chained.  The polynomials of
+// successive steps are all polynomials of the first one's A, so they commute: with
+// P = p(A) the next A is P A P, and a chain's steps are one product of X with the
+// product of their polynomials.  A step more in a chain costs four products of m x m,
+// three of them for A and the iterate's, and saves one of X with X and one with X
+// (of three steps of 5120 x 20480 that is half of all operations).  Five steps,
+// chained against not, in us: 1024 x 2048 196 against 201, 7 of 1024 x 4096 556, 740;
+// 2048 x 2048 404, 355; 2048 x 3500 458, 472; 2048 x 8192 588, 790; 2 of 5120 x 7680
+// 5890, 6720; 2 of 5120 x 20480 9540, 15770.  A's rounding is carried through a chain,
+// where its random signs add up to less of a large matrix: at m = 1024 and more the
+// result's error is that of single steps (1.9e-3 to 2.1e-3 for 2.0e-3), at 300 it is
+// up to one and a half times that, so that those go by single steps.
+bool muon_chained(const nvfp4_muon_tensor &t) {
+  const int64_t m = t.rows < t.cols ? t.rows : t.cols, n = t.rows < t.cols ? t.cols : t.rows;
+  return m >= 1024 && 2 * n >= 3 * m;
+}
+// The steps from k on that make a chain: three at first, then two (all five in one
+// chain, A's errors had grown past small singular values; two and then three doubled
+// the error where they fall off as 1 / i), with a product of at most 64 (kMuonQ).
+int muon_chain(int steps, int k, const double *most) {
+  int length = 1;
+  double top = most[k];
+  while (length < (k ? 2 : 3) && k + length < steps && top * most[k + length] <= 64.0) top *= most[k + length++];
+  return length;
 }
 
 // Tiles of a product of the group: those that take least by these times in us, as
@@ -280,19 +308,19 @@ int muon_tile(const NsArgs &p, int pad) {
   return best;
 }
 
-// The matrices of the list with one padding, from `from` on, that make a group: as
-// many as a launch takes, or 2^27 elements.
+// The matrices of the list with one padding, chained or not, from `from` on, that make
+// a group: as many as a launch takes, or 2^27 elements.
 struct MuonGroup {
   int64_t index[kMuonMats];
   int count = 0;
   int64_t next = 0;  // where to go on in the list
 };
-MuonGroup muon_group(const nvfp4_muon_tensor *tensors, int64_t n, int64_t from, int pad) {
+MuonGroup muon_group(const nvfp4_muon_tensor *tensors, int64_t n, int64_t from, int pad, bool chained) {
   MuonGroup g;
   int64_t elements = 0, i = from;
   for (; i < n && g.count < kMuonMats && elements < ((int64_t)1 << 27); ++i) {
     const nvfp4_muon_tensor &t = tensors[i];
-    if (!t.rows || !t.cols || muon_pad(t) != pad) continue;
+    if (!t.rows || !t.cols || muon_pad(t) != pad || muon_chained(t) != chained) continue;
     g.index[g.count++] = i;
     elements += t.rows * t.cols;
   }
@@ -301,7 +329,7 @@ MuonGroup muon_group(const nvfp4_muon_tensor *tensors, int64_t n, int64_t from, 
 }
 struct MuonBuffers {
   double *parts;
-  _Float16 *x, *xt[2], *a, *b;
+  _Float16 *x, *xt[2], *a, *q[2], *p;  // q[1] and p where steps are chained
 };
 size_t muon_buffers(const nvfp4_muon_tensor &t, int pad, char *base, size_t used, MuonBuffers &o) {
   const int64_t m = round_up(t.rows < t.cols ? t.rows : t.cols, pad), n = round_up(t.rows < t.cols ? t.cols : t.rows, pad);
@@ -315,13 +343,19 @@ size_t muon_buffers(const nvfp4_muon_tensor &t, int pad, char *base, size_t used
   o.xt[0] = (_Float16 *)take((size_t)(n * muon_ld(m)) * 2);
   o.xt[1] = (_Float16 *)take((size_t)(n * muon_ld(m)) * 2);
   o.a = (_Float16 *)take((size_t)(m * muon_ld(m)) * 2);
-  o.b = (_Float16 *)take((size_t)(m * muon_ld(m)) * 2);
+  o.q[0] = (_Float16 *)take((size_t)(m * muon_ld(m)) * 2);
+  o.q[1] = o.p = nullptr;
+  if (muon_chained(t)) {
+    o.q[1] = (_Float16 *)take((size_t)(m * muon_ld(m)) * 2);
+    o.p = (_Float16 *)take((size_t)(m * muon_ld(m)) * 2);
+  }
   return used;
 }
 constexpr int kPads[3] = {256, 128, 64};
+constexpr int kMuonSteps = 16;
 
-hipError_t muon_run(const nvfp4_muon_tensor *tensors, const MuonGroup &g, int pad, const nvfp4_muon_config &c, MuonArgs &a,
-                    char *base, hipStream_t s) {
+hipError_t muon_run(const nvfp4_muon_tensor *tensors, const MuonGroup &g, int pad, bool chained, const nvfp4_muon_config &c,
+                    const double *most, MuonArgs &a, char *base, hipStream_t s) {
   MuonBuffers buf[kMuonMats];
   size_t used = 0;
   for (int i = 0; i < g.count; ++i) {
@@ -351,33 +385,52 @@ hipError_t muon_run(const nvfp4_muon_tensor *tensors, const MuonGroup &g, int pa
   a.count = g.count;
   hipError_t e = launch_muon_sums(a, s);
   if (e == hipSuccess) e = launch_muon_form(a, s);
-  const double kx = kMuonX, ka = kMuonA;
-  for (int k = 0; k < c.steps && e == hipSuccess; ++k) {
-    NsArgs p = {};
-    p.count = g.count;
-    for (int stage = 0; stage < 3 && e == hipSuccess; ++stage) {
-      for (int i = 0; i < g.count; ++i) {
-        const MuonMat &t = a.mat[i];
-        const bool turned = t.flags & MF_TURNED, last = k + 1 == c.steps;
-        const int m = turned ? t.cp : t.rp, n = turned ? t.rp : t.cp;
-        NsMat &o = p.mat[i];
-        const MuonBuffers &b = buf[i];
-        if (stage == 0)
-          o = {b.x, b.x, nullptr, b.a, b.a, m, m, n};
-        else if (stage == 1)
-          o = {b.a, b.a, b.a, b.b, b.b, m, m, m};
-        else
-          o = {b.b, b.xt[k & 1], nullptr, last && turned ? nullptr : b.x, last && !turned ? nullptr : b.xt[~k & 1], m, n, m};
-      }
-      p.symmetric = stage < 2;
-      p.alpha = (float)(stage == 0 ? ka / (kx * kx) : stage == 1 ? c.c / ka : 1.0 / ka);
-      p.beta = (float)c.b;
-      p.gamma = (float)(c.a * ka);
-      e = launch_muon_product(p, muon_tile(p, pad), s);
+  NsArgs p = {};
+  p.count = g.count;
+  const double kx = kMuonX, ka = kMuonA, kq = kMuonQ;
+  p.beta = (float)c.b;
+  p.gamma = (float)(c.a * ka);
+  // one product of every matrix i: operands(buffers, m, n, turned)
+  const auto product = [&](bool symmetric, double alpha, const auto &operands) {
+    if (e != hipSuccess) return;
+    for (int i = 0; i < g.count; ++i) {
+      const MuonMat &t = a.mat[i];
+      const bool turned = t.flags & MF_TURNED;
+      p.mat[i] = operands(buf[i], turned ? t.cp : t.rp, turned ? t.rp : t.cp, turned);
     }
+    p.symmetric = symmetric;
+    p.alpha = (float)alpha;
+    e = launch_muon_product(p, muon_tile(p, pad), s);
+  };
+  int now = 0;  // the iterate's transpose is in xt[now]
+  for (int k = 0; k < c.steps && e == hipSuccess;) {
+    const int length = chained ? muon_chain(c.steps, k, most) : 1;
+    product(true, ka / (kx * kx), [](const MuonBuffers &b, int m, int n, bool) { return NsMat{b.x, b.x, nullptr, b.a, b.a, m, m, n}; });
+    int q = 0;  // the chain's product is in q[q], at first its first polynomial
+    for (int l = 0; l < length; ++l) {
+      const auto poly = [&](const MuonBuffers &b) { return l ? b.p : b.q[0]; };
+      product(true, c.c / ka, [&](const MuonBuffers &b, int m, int, bool) { return NsMat{b.a, b.a, b.a, poly(b), poly(b), m, m, m}; });
+      if (l) {
+        product(true, (l == 1 ? kq / ka : 1.0) / ka,
+                [&](const MuonBuffers &b, int m, int, bool) { return NsMat{b.p, b.q[q], nullptr, b.q[!q], b.q[!q], m, m, m}; });
+        q = !q;
+      }
+      if (l + 1 < length) {  // A = p(A) A p(A)
+        product(true, 1.0 / ka,
+                [&](const MuonBuffers &b, int m, int, bool) { return NsMat{poly(b), b.a, nullptr, b.q[!q], b.q[!q], m, m, m}; });
+        product(true, 1.0 / ka,
+                [&](const MuonBuffers &b, int m, int, bool) { return NsMat{poly(b), b.q[!q], nullptr, b.a, b.a, m, m, m}; });
+      }
+    }
+    k += length;
+    const bool last = k == c.steps;
+    product(false, 1.0 / (length > 1 ? kq : ka), [&](const MuonBuffers &b, int m, int n, bool turned) {
+      return NsMat{b.q[q], b.xt[now], nullptr, last && turned ? nullptr : b.x, last && !turned ? nullptr : b.xt[!now], m, n, m};
+    });
+    now = !now;
   }
   for (int i = 0; i < g.count; ++i)
-    if (a.mat[i].flags & MF_TURNED) a.mat[i].direct = buf[i].xt[c.steps & 1];
+    if (a.mat[i].flags & MF_TURNED) a.mat[i].direct = buf[i].xt[now];
   return e == hipSuccess ? launch_muon_update(a, s) : e;
 }
 
@@ -471,14 +524,15 @@ size_t nvfp4_muon_workspace_bytes(const nvfp4_muon_tensor *tensors, int64_t n_te
     if (check_muon(tensors[i], false) != NVFP4_OK) return 0;
   size_t most = 0;
   for (const int pad : kPads)
-    for (int64_t at = 0; at < n_tensors;) {
-      const MuonGroup g = muon_group(tensors, n_tensors, at, pad);
-      size_t used = 0;
-      MuonBuffers b;
-      for (int i = 0; i < g.count; ++i) used = muon_buffers(tensors[g.index[i]], pad, nullptr, used, b);
-      if (used > most) most = used;
-      at = g.next;
-    }
+    for (const bool chained : {false, true})
+      for (int64_t at = 0; at < n_tensors;) {
+        const MuonGroup g = muon_group(tensors, n_tensors, at, pad, chained);
+        size_t used = 0;
+        MuonBuffers b;
+        for (int i = 0; i < g.count; ++i) used = muon_buffers(tensors[g.index[i]], pad, nullptr, used, b);
+        if (used > most) most = used;
+        at = g.next;
+      }
   return most;
 }
 
@@ -486,9 +540,10 @@ int nvfp4_muon(const nvfp4_muon_tensor *tensors, int64_t n_tensors, const nvfp4_
                size_t workspace_bytes, void *stream) {
   if (!tensors || !c) return NVFP4_E_NULL;
   if (n_tensors < 1 || n_tensors >= ((int64_t)1 << 30)) return NVFP4_E_SHAPE;
+  double most[kMuonSteps];
   if ((c->rounding != NVFP4_RTN && c->rounding != NVFP4_SR) || (c->nesterov != 0 && c->nesterov != 1)) return NVFP4_E_UNSUPPORTED;
-  if (!(c->lr >= 0.0f) || !isfinite(c->lr) || !(c->momentum >= 0.0 && c->momentum < 1.0) || c->steps < 1 || c->steps > 16 ||
-      c->step < 0 || c->step >= ((int64_t)1 << 47) || !isfinite(c->a) || !isfinite(c->b) || !isfinite(c->c) || !muon_bounded(*c))
+  if (!(c->lr >= 0.0f) || !isfinite(c->lr) || !(c->momentum >= 0.0 && c->momentum < 1.0) || c->steps < 1 || c->steps > kMuonSteps ||
+      c->step < 0 || c->step >= ((int64_t)1 << 47) || !isfinite(c->a) || !isfinite(c->b) || !isfinite(c->c) || !muon_bounded(*c, most))
     return NVFP4_E_VALUE;
   if (!aligned(c->grad_scale, 4)) return NVFP4_E_ALIGN;
   for (int64_t i = 0; i < n_tensors; ++i)
@@ -509,11 +564,12 @@ int nvfp4_muon(const nvfp4_muon_tensor *tensors, int64_t n_tensors, const nvfp4_
   a.grad_scale = c->grad_scale;
   hipStream_t s = (hipStream_t)stream;
   for (const int pad : kPads)
-    for (int64_t at = 0; at < n_tensors;) {
-      const MuonGroup g = muon_group(tensors, n_tensors, at, pad);
-      at = g.next;
-      if (g.count && muon_run(tensors, g, pad, *c, a, (char *)workspace, s) != hipSuccess) return NVFP4_E_HIP;
-    }
+    for (const bool chained : {false, true})
+      for (int64_t at = 0; at < n_tensors;) {
+        const MuonGroup g = muon_group(tensors, n_tensors, at, pad, chained);
+        at = g.next;
+        if (g.count && muon_run(tensors, g, pad, chained, *c, most, a, (char *)workspace, s) != hipSuccess) return NVFP4_E_HIP;
+      }
   return finish(hipSuccess, s);
 }
 

@@ -67,6 +67,7 @@ hipError_t launch_gemm_gated_backward(const GatedArgs &a, hipStream_t s);
 // columns), padded with zeros to whole tiles, in fp16 times a power of two.
 constexpr float kMuonX = 1024.0f;  // of the iterate, whose singular values stay below 4
 constexpr float kMuonA = 2048.0f;  // of its square and of the polynomial in it, below 16
+constexpr float kMuonQ = 512.0f;   // of a product of polynomials, up to 64
 constexpr int kMuonMats = 30;      // of one launch: what 4 KiB of arguments hold
 constexpr int kMuonChunk = 8192;   // elements of a workgroup of the sums and of the update
 constexpr int kMuonParts = 512;    // workgroups of a matrix's sum, at most
@@ -117,8 +118,8 @@ __device__ __forceinline__ int muon_mat_of(const uint32_t end[kMuonMats], uint32
 }
 
 // D = alpha P Q^T + beta E + gamma I of every matrix, P [M][K], Q [N][K], D and E
-// [M][N], DT [N][M], rows muon_ld apart; D or DT may be null.  Symmetric: P = Q and D = DT, and only
-// tiles on and below the diagonal are formed.
+// [M][N], DT [N][M], rows muon_ld apart; D or DT may be null.  Symmetric: P Q^T is, D = DT, and
+// only tiles on and below the diagonal are formed.
 struct NsMat {
   const _Float16 *p, *q, *e;
   _Float16 *d, *dt;

@@ -141,6 +141,25 @@ def test_lists_of_one_size(nv, count, rows, cols):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("steps,abc", [(5, ABC), (1, ABC), (2, ABC), (3, ABC), (4, ABC), (6, ABC), (10, (1.5, -0.5, 0.0)), (3, (2.0, -1.5, 0.5)),
+                                       (3, (4.03, -8.6, 4.25))], ids=str)
+def test_long_matrices(nv, steps, abc):
+    """Sides far apart: polynomials are multiplied before the iterate is, as far as their sizes let them be."""
+    say("orthogonalize long", steps, abc)
+    xs = [matrix(1040, 2200, 60), matrix(2110, 1030, 61, torch.bfloat16), matrix(1024, 5000, 62), torch.zeros(2100, 1025, device="cuda")]
+    out = nv.orthogonalize(xs, steps=steps, coefficients=abc)
+    for x, y in zip(xs[:3], out):
+        near(y, orthogonal(x.double(), steps, abc), "%s" % (tuple(x.shape),), UPDATE if steps == 5 else 2 * UPDATE)
+    assert not out[3].any()
+    for x, y in zip(out, nv.orthogonalize(xs, steps=steps, coefficients=abc)):
+        assert torch.equal(x, y)
+    x = matrix(1030, 2110, 63)
+    x[100:300] = 0
+    y = nv.orthogonalize(x, steps=steps, coefficients=abc)
+    assert not y[100:300].any()
+    near(y, orthogonal(x.double(), steps, abc), "zero rows", UPDATE if steps == 5 else 2 * UPDATE)
+
+
 def uniforms(n, index, step, seed):
     group = torch.arange((n + 7) // 8, device="cuda", dtype=torch.int64)
     low = 0xFFFFFFFF
