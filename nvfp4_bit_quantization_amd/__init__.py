@@ -1364,10 +1364,22 @@ class MuonList:
         self.device = self.tensors[0].grad.get_device()
         if any(t.grad.get_device() != self.device for t in self.tensors):
             raise ValueError("the tensors are on several devices")
+        self.owner = {}  # of the buffers that are written: their tensor's index
+        for i, t in enumerate(self.tensors):
+            for b in (t.param, t.m, t.copy, t.update):
+                if b is not None and self.owner.setdefault(b.data_ptr(), i) != i and b.numel():
+                    raise ValueError("a buffer of tensor %d belongs to tensor %d too" % (i, self.owner[b.data_ptr()]))
+        for i, t in enumerate(self.tensors):
+            self._check_grad(i, t.grad)
         self.workspace_bytes = lib().nvfp4_muon_workspace_bytes(self.array, len(self.array))
+
+    def _check_grad(self, index: int, grad):
+        if grad.numel() and self.owner.get(grad.data_ptr(), index) != index:
+            raise ValueError("the gradient of tensor %d is written as a buffer of tensor %d" % (index, self.owner[grad.data_ptr()]))
 
     def set_grad(self, index: int, grad):
         t = self.tensors[index]
+        self._check_grad(index % len(self.tensors), grad)
         if grad.get_device() != self.device or grad.shape != t.grad.shape:
             raise ValueError("grad: a tensor of shape %s on device %d is wanted" % (tuple(t.grad.shape), self.device))
         old, t.grad = t.grad, grad

@@ -295,3 +295,20 @@ def test_python_refusals(nv):
             nv.muon([nv.MuonTensor(g.clone(), g, g.clone())], 0.01, **kw)
     with pytest.raises(nv.Nvfp4Error):
         nv.muon([nv.MuonTensor(None, g)], 0.01)  # nothing to write
+
+
+def test_buffers_of_two_tensors_are_refused(nv):
+    """What one tensor's step writes is no buffer of another's: their order within the call is not fixed."""
+    p, m, u, g = (matrix(16, 24, i) for i in range(4))
+    other, low = matrix(16, 24, 5), torch.zeros(16, 24, dtype=torch.bfloat16, device="cuda")
+    for a, b in ((dict(param=p), dict(param=p)), (dict(param=p, m=m), dict(param=u, m=m)), (dict(param=p, copy=low), dict(param=u, update=low)),
+                 (dict(param=g), dict(param=u))):
+        with pytest.raises(ValueError):
+            nv.muon([nv.MuonTensor(grad=other, **a), nv.MuonTensor(grad=g, **b)], 0.01)
+    one = nv.MuonList([nv.MuonTensor(p, g, m), nv.MuonTensor(u, g), nv.MuonTensor(torch.empty(0, 3, device="cuda"), torch.empty(0, 3, device="cuda")),
+                       nv.MuonTensor(torch.empty(0, 4, device="cuda"), torch.empty(0, 4, device="cuda"))])
+    for at in (1, -3):
+        with pytest.raises(ValueError):
+            one.set_grad(at, m)
+    one.set_grad(1, other)
+    nv.muon(one, 0.01)
