@@ -9,6 +9,14 @@
 // epilogue reads gate and up and writes their gradients; dh itself is not stored.
 // The pipeline is the plain GEMM's (gemm_tile.hpp); rows past M or N repeat the
 // last one and are not stored, so that only K has to fill its tiles there.
+//
+// Large calls are bound by the matrix instructions at the power the chip holds:
+// 16384 tokens, 5120 -> 2 x 20480 with h, gate and up stored, 4.87 to 5.14 ms (1.34 to
+// 1.41 PFLOP/s; the same products by themselves 1.27 at 5120 x 5120 x 8192, a
+// library's bf16 product of 8192^3 1.55), their gradient 2.7 to 2.8 ms (1.22 to 1.27: its
+// epilogue moves 2.7 GB).  16 tokens are bound by reading the weights: 106 MB in 28
+// to 39 us.  What fills few tiles (1008 x 2736 x 1040: 27 us, gradient 20) by a
+// compute unit's way through K, 1.2 us a workgroup and K-tile of 128, behind a launch.
 #include "block_device.hpp"
 #include "block_kernels.hpp"
 #include "gemm_tile.hpp"
@@ -24,12 +32,35 @@ __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf
 constexpr float kTanhScale = 1.595769122f;  // 2 sqrt(2 / pi): (1 + tanh(z)) / 2 = sigmoid(2 z)
 constexpr float kCubic = 0.044715f;
 
+// P(N > -x) for a normal N, with e = e^(-x^2 / 2): by symmetry from the upper tail at
+// a = |x|, which is e t poly(t) with t = 1 / (1 + 0.33 a).  The polynomial is a fit to
+// the tail's quotient by e t (over all a, of the relative error): within 2^-19 of the
+// tail up to a = 4, 2^-18 up to 8, where the exponent's rounding grows.  With the
+// library's erfcf, whose ranges a wave takes one after another, 1008 x 2736 x 1040 took 31
+// us for 27, its gradient 24 for 19, that of 16384 tokens, 5120 -> 20480, 3.14 ms for 2.78.
+__device__ __forceinline__ float normal_cdf(float x, float &e) {
+  const float a = fabsf(x), t = __builtin_amdgcn_rcpf(fmaf(0.33f, a, 1.0f));
+  e = __builtin_amdgcn_exp2f(-0.7213475204f * a * a);
+  float r = fmaf(t, 0.0332857408f, -0.105665021f);
+  r = fmaf(r, t, 0.0674313828f);
+  r = fmaf(r, t, 0.0334286168f);
+  r = fmaf(r, t, 0.0910049751f);
+  r = fmaf(r, t, 0.117216729f);
+  r = fmaf(r, t, 0.131646991f);
+  r = fmaf(r, t, 0.131651074f);
+  const float tail = e * (t * r);
+  return x > 0.0f ? 1.0f - tail : tail;
+}
+
 // the activation of x, and its derivative
 template <int ACT>
 __device__ __forceinline__ float act(float x) {
   if (ACT == NVFP4_SILU) return x * sigmoid(x);
   if (ACT == NVFP4_RELU) return fmaxf(x, 0.0f);
-  if (ACT == NVFP4_GELU) return x * (0.5f * erfcf(-0.7071067812f * x));
+  if (ACT == NVFP4_GELU) {
+    float e;
+    return x * normal_cdf(x, e);
+  }
   return x * sigmoid(kTanhScale * x * fmaf(kCubic * x, x, 1.0f));
 }
 template <int ACT>
@@ -42,9 +73,10 @@ __device__ __forceinline__ void act_grad(float x, float &f, float &df) {
     f = fmaxf(x, 0.0f);
     df = x > 0.0f ? 1.0f : 0.0f;
   } else if (ACT == NVFP4_GELU) {
-    const float p = 0.5f * erfcf(-0.7071067812f * x);
+    float e;
+    const float p = normal_cdf(x, e);
     f = x * p;
-    df = fmaf(x * 0.3989422804f, exp_of(-0.5f * x * x), p);
+    df = fmaf(x * 0.3989422804f, e, p);
   } else {
     const float p = sigmoid(kTanhScale * x * fmaf(kCubic * x, x, 1.0f));
     const float y = fminf(fmaxf(x, -64.0f), 64.0f);  // beyond, p (1 - p) is zero
@@ -327,6 +359,8 @@ __device__ __forceinline__ void origin(const GatedArgs &a, uint32_t tile, int64_
   n0 = (int64_t)(local / gm) * BN;
 }
 
+// Tiles of 256 x 256 products (256 x 128 columns of both weights): one workgroup to
+// a compute unit, 64 KiB of accumulators to a wave; 1.2 to 1.4 PFLOP/s.
 template <bool BACK>
 __global__ __launch_bounds__(kGThreads) void gated_fast_kernel(GatedArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kFStages * kFStageBytes];
@@ -349,7 +383,10 @@ __global__ __launch_bounds__(kGThreads) void gated_fast_kernel(GatedArgs a) {
 
 // Any K, and what fits no 32-bit offset: tiles of 64 T + 64 T operand rows and
 // K-tiles of 128, through registers three K-tiles ahead, in the LDS layout of the fast
-// path (codes in chunks permuted by row, then two scale dwords of each row).
+// path (codes in chunks permuted by row, then two scale dwords of each row).  Two
+// workgroups to a compute unit, whose waits overlap: 1008 x 2736 x 1040 has 344 tiles
+// forward and takes 26 us (with operands expanded to fp16 in LDS, shared by the waves,
+// 1008 x 2736 x 4112 took 77 us for 70).
 // Rows past the end repeat the last one.  A K that is no multiple of 128 ends in
 // a K-tile of zeros beyond it: only that one is loaded piece by piece.
 typedef uint4 __attribute__((aligned(8))) uint4_at8;

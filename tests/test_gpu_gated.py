@@ -292,3 +292,28 @@ def test_python_refusals(nv):
                  lambda: nv.nvfp4_gemm_gated_backward(a, w, x, x, x, x)):
         with pytest.raises(nv.Nvfp4Error):
             call()
+
+
+def test_gelu_over_all_gates(nv):
+    """Every finite bfloat16 gate: x P(N < x) and its derivative, the tail's relative error below 2^-16 while it is normal."""
+    say("gelu over all gates")
+    bits = torch.arange(1 << 16, device="cuda", dtype=torch.int32)
+    x = (bits - (bits >> 15 << 16)).to(torch.int16).view(torch.bfloat16)
+    x = torch.where(torch.isfinite(x), x, torch.zeros_like(x)).reshape(1024, 64).contiguous()
+    one = torch.zeros(1024, 16, device="cuda")
+    one[:, 0] = 1
+    a, w = (nv.quantize(t.to(torch.bfloat16), [nv.QuantSpec.of("row")])[0] for t in (one, one[:64]))
+    dh, e = product(nv, a, w)
+    unit = dh[0, 0].item()
+    assert (dh == unit).all()
+    dgate, dup = nv.gemm_gated_backward(a, w, x, torch.ones_like(x), activation="gelu")
+    d = x.double()
+    below = 0.5 * torch.special.erfc(-d / math.sqrt(2))  # (torch's ndtr is 1 + erf, which has no tail)
+    f = d * below * unit
+    tail = (d > -13) & (f.abs() > 1e-36)
+    assert ((dup.double() - f).abs()[tail] <= ((2.0 ** -8 + 2.0 ** -16) * f.abs())[tail]).all()
+    assert (dup.double()[d <= -13].abs() < 1e-35).all()
+    df = (below + d * torch.exp(-d * d / 2) / math.sqrt(2 * math.pi)) * unit
+    # the two terms cancel below 0: within 2^-16 of their sizes
+    size = (below + d.abs() * torch.exp(-d * d / 2) / math.sqrt(2 * math.pi)) * unit
+    assert ((dgate.double() - df).abs() <= 2.0 ** -8 * df.abs() + 2.0 ** -16 * size + 1e-36).all()
