@@ -279,13 +279,14 @@ int muon_chain(int steps, int k, const double *most) {
 // 4096 and others at every tile size): a fixed part, and per 64 of K the longer of
 // one tile's own time and what the chip needs for all of them, 256 at a time.
 // E. g. X X^T of 2048 x 2048: 46 us in tiles of 256, 21 of 128, 26 of 64; the last
-// product of 4096 x 4096: 124, 157, 279.
+// product of 4096 x 4096: 124, 157, 279.  (20 matrices of 512 x 512: 217 us; with a
+// fixed part of 5.5 for 128, that of small products alone, 233.)
 int muon_tile(const NsArgs &p, int pad) {
   struct Cost {
     int tile;
     double fixed, own, all;
   };
-  constexpr Cost costs[3] = {{256, 8.0, 1.2, 1.7}, {128, 5.5, 0.46, 0.70}, {64, 4.0, 0.25, 0.29}};
+  constexpr Cost costs[3] = {{256, 8.0, 1.2, 1.7}, {128, 7.5, 0.46, 0.70}, {64, 4.0, 0.25, 0.29}};
   double least = 0.0;
   int best = 0;
   for (const Cost &c : costs) {

@@ -127,7 +127,7 @@ def test_many_matrices_at_once(nv):
 
 
 # (matrices, rows, columns): lists whose products go in tiles of 256; of 128 and of 64, many to a compute unit, upright and flat
-LISTS = [(5, 2040, 2290), (5, 2290, 2040), (8, 1000, 1111), (20, 512, 500), (30, 300, 310), (20, 440, 445)]
+LISTS = [(5, 2040, 2290), (5, 2290, 2040), (7, 1000, 1111), (8, 1000, 1111), (20, 512, 500), (30, 300, 310), (20, 440, 445)]
 
 
 @pytest.mark.parametrize("count,rows,cols", LISTS, ids=str)
