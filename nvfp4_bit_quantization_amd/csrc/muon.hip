@@ -19,8 +19,8 @@
 // Large products are bound by the matrix instructions: X X^T of 5120 x 20480 runs at
 // 1.1 PFLOP/s with 79 % of the busy cycles theirs, where a library's product of
 // 8192^3 in fp16 reaches 1.49; the passes over momentum, gradient and parameter move
-// 5 TB/s.  Steps of two matrices of 5120 x 20480 take 10.5 ms (without chains 16.9), 1.2 of
-// them in those passes.  Small ones are bound by their launches, 5 to 14 us each: 182
+// 5 TB/s.  Steps of two matrices of 5120 x 20480 take 10.3 ms (without chains 16.9), 1.3 of
+// them in those passes.  Small ones are bound by their launches, 5 to 14 us each: 170
 // us for 20 matrices of 256 x 1024.
 #include "block_device.hpp"
 #include "block_kernels.hpp"
