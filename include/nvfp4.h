@@ -700,11 +700,16 @@ typedef struct {
  * 0.7 .. 1.2 in 5 steps.  Coefficients that can take a singular value of the
  * iteration, which starts in [0, 1], above 3.5, or |a + b s + c s^2| above 14, are
  * refused (NVFP4_E_VALUE).
- * Momentum, norm (binary64 sums) and parameters are binary32; the iteration's
- * matrices are held in fp16 with powers of two as scales, their products summed
- * in binary32: X is off by 1e-3 to 3e-3 of its norm, by more (2e-2) where most
- * singular values of u are below 2^-11 of its norm over the root of the smaller side,
- * which rounding buries.  bf16 params under NVFP4_SR add
+ * Momentum, norm (binary64 sums) and parameters are binary32; a value of the
+ * iteration's matrices is held as the sum of two fp16 (22 bits) with powers of two
+ * as scales, their products summed in binary32.  X is off about as much as with
+ * binary32 throughout: a rounding of the strong directions, 2^-22 of them, lies
+ * on the weak ones as well and grows with these, by up to a for a step.  After five
+ * steps with the coefficients above that is 1e-6 to 1e-5 of X's norm where singular
+ * values are alike or fall off as 1 / i, up to 5e-5 where they do as 1 / i^2 or there
+ * is one direction over noise of a hundredth, 4e-4 over noise of a ten thousandth
+ * (sides up to 20480; binary32 throughout: 1e-5, 8e-5 and 6e-4).  bf16 params under
+ * NVFP4_SR add
  * 16 uniform bits below the kept ones and truncate; those of element i (row-major)
  * of tensor index (its place in `tensors`) are half i & 1 of word (i mod 8) / 2 of
  * Philox4x32-10(key = seed, counter = (i / 8 mod 2^32, index, step mod 2^32,

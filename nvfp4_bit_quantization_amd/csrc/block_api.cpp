@@ -254,19 +254,21 @@ int muon_pad(const nvfp4_muon_tensor &t) {
 // product of their polynomials.  A step more in a chain costs four products of m x m,
 // three of them for A and the iterate's, and saves one of X with X and one with X
 // (of three steps of 5120 x 20480 that is half of all operations).  Five steps,
-// chained against not, in us: 1024 x 2048 196 against 201, 7 of 1024 x 4096 556, 740;
-// 2048 x 2048 404, 355; 2048 x 3500 458, 472; 2048 x 8192 588, 790; 2 of 5120 x 7680
-// 5890, 6720; 2 of 5120 x 20480 9540, 15770.  A's rounding is carried through a chain,
-// where its random signs add up to less of a large matrix: at m = 1024 and more the
-// result's error is that of single steps (1.9e-3 to 2.1e-3 for 2.0e-3), at 300 it is
-// up to one and a half times that, so that those go by single steps.
+// chained against not, in us: 1024 x 1536 326 against 313, 1024 x 2048 344, 353; 7 of
+// 1024 x 4096 1170, 1740; 2048 x 2048 870, 775; 2048 x 3500 1040, 1125; 2048 x 8192 1390,
+// 1970; 2 of 5120 x 7680 16500, 19100; 2 of 5120 x 20480 27000, 44800.  A's rounding is
+// carried through a chain: 1024 x 1536 and 2048 x 4096 come out off by 2.9e-6 and 3.7e-6
+// for normal matrices (single steps 2.1e-6, 2.9e-6; binary32 3.3e-6, 4.6e-6), by 2.1e-5
+// and 2.9e-5 (2.4e-5, 3.4e-5; 3.4e-5, 4.9e-5) with 1 / i^2 spectra and by 1.9e-5 and
+// 1.1e-5 (9e-6, 7e-6; 6e-6, 6e-6) where half of the directions are empty.  At m = 300
+// it is up to 1.9 times single steps' error; those go by single steps.
 bool muon_chained(const nvfp4_muon_tensor &t) {
   const int64_t m = t.rows < t.cols ? t.rows : t.cols, n = t.rows < t.cols ? t.cols : t.rows;
   return m >= 1024 && 2 * n >= 3 * m;
 }
 // The steps from k on that make a chain: three at first, then two (all five in one
-// chain, A's errors had grown past small singular values; two and then three doubled
-// the error where they fall off as 1 / i), with a product of at most 64 (kMuonQ).
+// chain carry A's errors past small singular values; two and then three doubled the
+// error where these fall off as 1 / i), with a product of at most 64 (kMuonQ).
 int muon_chain(int steps, int k, const double *most) {
   int length = 1;
   double top = most[k];
@@ -276,11 +278,11 @@ int muon_chain(int steps, int k, const double *most) {
 
 // Tiles of a product of the group: those that take least by these times in us, as
 // measured (one product of 7 matrices of 1024 x 1152, 1 of 2048 x 2048, 1 of 4096 x
-// 4096 and others at every tile size): a fixed part, and per 64 of K the longer of
-// one tile's own time and what the chip needs for all of them, 256 at a time.
-// E. g. X X^T of 2048 x 2048: 46 us in tiles of 256, 21 of 128, 26 of 64; the last
-// product of 4096 x 4096: 124, 157, 279.  (20 matrices of 512 x 512: 217 us; with a
-// fixed part of 5.5 for 128, that of small products alone, 233.)
+// 4096 and others at every tile size): a fixed part, and per 64 of K, each taken three
+// times, the longer of one tile's own time and what the chip needs for all of them,
+// 256 at a time.  E. g. X X^T of 2048 x 2048: 118 us in tiles of 256, 54 of 128, 63 of
+// 64; the last product of 4096 x 4096: 322, 386, 638; 20 matrices of 512 x 512: 379 us
+// by these tiles, all in 64 399, in 256 696.
 int muon_tile(const NsArgs &p, int pad) {
   struct Cost {
     int tile;
@@ -296,7 +298,7 @@ int muon_tile(const NsArgs &p, int pad) {
       const int64_t down = p.mat[i].M / c.tile, across = p.mat[i].N / c.tile;
       const int64_t n = p.symmetric ? down * (down + 1) / 2 : down * across;
       tiles += n;
-      k += n * (p.mat[i].K / 64);
+      k += n * (p.mat[i].K / 64) * 3;
     }
     // a compute unit holds one of the large tiles, but several of the others
     const double rounds = c.tile == 256 ? (double)((tiles + 255) / 256) : (double)tiles / 256.0;
@@ -340,15 +342,16 @@ size_t muon_buffers(const nvfp4_muon_tensor &t, int pad, char *base, size_t used
     return p;
   };
   o.parts = (double *)take(kMuonParts * sizeof(double));
-  o.x = (_Float16 *)take((size_t)(m * muon_ld(n)) * 2);
-  o.xt[0] = (_Float16 *)take((size_t)(n * muon_ld(m)) * 2);
-  o.xt[1] = (_Float16 *)take((size_t)(n * muon_ld(m)) * 2);
-  o.a = (_Float16 *)take((size_t)(m * muon_ld(m)) * 2);
-  o.q[0] = (_Float16 *)take((size_t)(m * muon_ld(m)) * 2);
+  const auto matrix = [&](int64_t rows, int64_t cols) { return (_Float16 *)take((size_t)(rows * muon_ld(cols)) * 4); };
+  o.x = matrix(m, n);
+  o.xt[0] = matrix(n, m);
+  o.xt[1] = matrix(n, m);
+  o.a = matrix(m, m);
+  o.q[0] = matrix(m, m);
   o.q[1] = o.p = nullptr;
   if (muon_chained(t)) {
-    o.q[1] = (_Float16 *)take((size_t)(m * muon_ld(m)) * 2);
-    o.p = (_Float16 *)take((size_t)(m * muon_ld(m)) * 2);
+    o.q[1] = matrix(m, m);
+    o.p = matrix(m, m);
   }
   return used;
 }

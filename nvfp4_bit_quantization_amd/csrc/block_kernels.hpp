@@ -64,10 +64,12 @@ hipError_t launch_gemm_gated_backward(const GatedArgs &a, hipStream_t s);
 
 // ---------------------------------------------------------------- muon ----
 // Matrices are worked on as m x n with m <= n ("turned" ones have more rows than
-// columns), padded with zeros to whole tiles, in fp16 times a power of two.
-constexpr float kMuonX = 1024.0f;  // of the iterate, whose singular values stay below 4
-constexpr float kMuonA = 2048.0f;  // of its square and of the polynomial in it, below 16
-constexpr float kMuonQ = 512.0f;   // of a product of polynomials, up to 64
+// columns), padded with zeros to whole tiles.  A value is held times a power of two
+// as the sum of two fp16, whose matrices stand one behind the other: 22 bits of it,
+// down to 2^-25.  The powers are the largest that keep the values below fp16's 65504.
+constexpr float kMuonX = 16384.0f;  // of the iterate, whose singular values stay below 3.5
+constexpr float kMuonA = 4096.0f;   // of its square and of the polynomial in it, up to 14
+constexpr float kMuonQ = 512.0f;    // of a product of polynomials, up to 64
 constexpr int kMuonMats = 30;      // of one launch: what 4 KiB of arguments hold
 constexpr int kMuonChunk = 8192;   // elements of a workgroup of the sums and of the update
 constexpr int kMuonParts = 512;    // workgroups of a matrix's sum, at most

@@ -8,20 +8,22 @@
 // "TN" (both operands contiguous in K), for which X is kept as it is and
 // transposed: the epilogue writes both.
 //
-// Operands are fp16, sums binary32.  Against the definition in 64 bits the
-// result is off by 1.2e-3 to 2e-3 of its norm, by rounding X, A and the
-// polynomial to 11 bits five times; bf16, the usual choice, is off by 8 times
-// that.  Powers of two keep the values in fp16's normal range (kMuonX, kMuonA).
-// Singular values that X's first rounding buries (below some 2^-11 of the norm
-// over the root of the smaller side) come out as the rounding's own: with ones that
-// fall off as 1 / i^2 the result is off by 2e-2.
+// A value is held as the sum of two fp16 (22 bits), a product formed of three:
+// both first parts and the two mixed ones, summed in binary32.  The iteration brings
+// weak directions to the size of strong ones, up to 485 times in five steps, and
+// with them what rounding the strong ones left there: with one fp16 to a value the
+// result was off by 1e-3 of its norm at best, by 2e-2 with one direction over noise
+// of a hundredth or singular values that fall off as 1 / i^2, by 0.15 over noise of a
+// ten thousandth.  So it is as an iteration in binary32 throughout, against 64 bits:
+// 5120 x 20480 normal, over noise of a hundredth and of a ten thousandth 3.9e-6, 4.9e-5
+// and 3.3e-4 (binary32: 1.1e-5, 8.3e-5, 6.0e-4); 2048 x 4096 with 1 / i^2 2.9e-5 (4.9e-5).
 //
-// Large products are bound by the matrix instructions: X X^T of 5120 x 20480 runs at
-// 1.1 PFLOP/s with 79 % of the busy cycles theirs, where a library's product of
-// 8192^3 in fp16 reaches 1.49; the passes over momentum, gradient and parameter move
-// 5 TB/s.  Steps of two matrices of 5120 x 20480 take 10.3 ms (without chains 16.9), 1.3 of
-// them in those passes.  Small ones are bound by their launches, 5 to 14 us each: 170
-// us for 20 matrices of 256 x 1024.
+// Large products are bound by the matrix instructions: of 5120 x 20480, X X^T runs
+// at 1.04 PFLOP/s of them, the product with X at 1.26 with 77 % of all cycles theirs,
+// where a library's product of 8192^3 in fp16 reaches 1.49; the passes over momentum,
+// gradient and parameter move 5 TB/s.  Steps of two matrices of 5120 x 20480 take 27.7 ms
+// (without chains 45), 1.5 of them in those passes.  Small ones are bound by their
+// launches, 8 to 21 us each: 290 us for 20 matrices of 256 x 1024.
 #include "block_device.hpp"
 #include "block_kernels.hpp"
 #include "gemm_device.hpp"
@@ -77,21 +79,36 @@ __device__ __forceinline__ void multiply(f32x16 acc[T][T], const NsFrags<T> &f, 
   }
 }
 
+// a value as the sum of two fp16: off by 2^-22 of it at most (2^-25, where that is more)
+__device__ __forceinline__ void two_parts(float v, half8 parts[2], int j) {
+  parts[0][j] = (_Float16)v;
+  parts[1][j] = (_Float16)(v - (float)parts[0][j]);
+}
+
 __device__ __forceinline__ void slab_fence() { asm volatile("" ::: "memory"); }
 
 // One orientation of a wave's results: 32 rows at a time through its slab, from
 // which a lane takes 8 neighbouring columns.  E's elements at the same places are
-// read a slab ahead (in turn with the stores they made the square of a 5120 x 5120
-// matrix 22 us longer).  write(i) puts rows row0 + 32 i onwards into the slab.
+// read a slab ahead (in turn with the stores, and of one fp16, they made the square
+// of a 5120 x 5120 matrix 22 us longer).  write(i) puts rows row0 + 32 i onwards into the slab.
+// plane: elements from a value's first part to its second, of D and E.
 template <int T, bool E, typename Write>
-__device__ __forceinline__ void store_rows(const NsArgs &a, _Float16 *d, const _Float16 *e, int64_t ld, int64_t row0, int64_t col0,
-                                           const float *slab, uint32_t lane, Write write) {
+__device__ __forceinline__ void store_rows(const NsArgs &a, _Float16 *d, const _Float16 *e, int64_t plane, int64_t ld, int64_t row0,
+                                           int64_t col0, const float *slab, uint32_t lane, Write write) {
   constexpr int LANES = 4 * T, ROWS = 64 / LANES, TIMES = 32 / ROWS;
   const int c = lane % LANES * 8, first = lane / LANES;
-  half8 x[TIMES];
+  // where the wave's elements begin, and the lane's from there on (with all of an
+  // address formed by lane, the large tiles of E spilled)
+  const int64_t at = row0 * ld + col0;
+  const uint32_t mine = (uint32_t)(first * ld) + c;
+  const int diagonal = (int)(row0 - col0) + first - c;  // of the lane's 8 columns, in its first row
+  half8 x[TIMES][2];
   const auto fetch = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
-    for (int k = 0; k < TIMES; ++k) x[k] = *reinterpret_cast<const half8 *>(e + (row0 + i * 32 + k * ROWS + first) * ld + col0 + c);
+    for (int k = 0; k < TIMES; ++k)
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+        x[k][part] = *reinterpret_cast<const half8 *>(e + (at + part * plane + (i * 32 + k * ROWS) * ld) + mine);
   };
   if (E) fetch(0);
 #pragma unroll
@@ -109,17 +126,19 @@ __device__ __forceinline__ void store_rows(const NsArgs &a, _Float16 *d, const _
       for (int k = 0; k < TIMES; ++k)
 #pragma unroll
         for (int b = 0; b < 8; ++b) {
-          v[k][b] = fmaf(a.beta, (float)x[k][b], v[k][b]);
-          if (row0 + i * 32 + k * ROWS + first == col0 + c + b) v[k][b] += a.gamma;
+          v[k][b] = fmaf(a.beta, (float)x[k][0][b] + (float)x[k][1][b], v[k][b]);
+          if (diagonal + i * 32 + k * ROWS == b) v[k][b] += a.gamma;
         }
       if (i + 1 < T) fetch(i + 1);
     }
 #pragma unroll
     for (int k = 0; k < TIMES; ++k) {
-      half8 y;
+      half8 y[2];
 #pragma unroll
-      for (int b = 0; b < 8; ++b) y[b] = (_Float16)v[k][b];
-      *reinterpret_cast<half8 *>(d + (row0 + i * 32 + k * ROWS + first) * ld + col0 + c) = y;
+      for (int b = 0; b < 8; ++b) two_parts(v[k][b], y, b);
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+        *reinterpret_cast<half8 *>(d + (at + part * plane + (i * 32 + k * ROWS) * ld) + mine) = y[part];
     }
   }
 }
@@ -175,18 +194,28 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : 2) void ns_product_kernel(NsArgs 
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-  const uint32_t lds0 = lds_addr(lds), KT = (uint32_t)(t.K / 64), last = KT - 1;
-  // transfer i of K-tile kt of one operand into a slot; past the end the last
-  // K-tile again, into a slot that nobody reads
-  const auto move = [&](const uint8_t *base, uint32_t kt, uint32_t slot, int i) {
-    dma16(uniform_ptr(base + (uint64_t)(kt < last ? kt : last) * 128u), off[i],
-          __builtin_amdgcn_readfirstlane(lds0 + slot * N::kSlotBytes + (wave * N::kMoves + i) * 1024u));
+  // Each K-tile is taken three times: both first parts, P's first with Q's second,
+  // P's second with Q's first (both second ones are 2^-22 of the first's).  Past the
+  // end the last again, into slots that nobody reads.
+  const uint32_t lds0 = lds_addr(lds), KT = 3u * (uint32_t)(t.K / 64), last = KT - 1;
+  const uint64_t second_p = (uint64_t)t.M * ld * 2, second_q = (uint64_t)t.N * ld * 2;
+  const auto from_p = [&](uint32_t kt) {
+    const uint32_t k = kt < last ? kt : last;
+    return base_p + (uint64_t)(k / 3u) * 128u + (k % 3u == 2u ? second_p : 0u);
+  };
+  const auto from_q = [&](uint32_t kt) {
+    const uint32_t k = kt < last ? kt : last;
+    return base_q + (uint64_t)(k / 3u) * 128u + (k % 3u == 1u ? second_q : 0u);
+  };
+  // transfer i of one operand's K-tile, which begins at `at`, into a slot
+  const auto move = [&](const uint8_t *at, uint32_t slot, int i) {
+    dma16(uniform_ptr(at), off[i], __builtin_amdgcn_readfirstlane(lds0 + slot * N::kSlotBytes + (wave * N::kMoves + i) * 1024u));
   };
   const auto after = [](uint32_t slot, uint32_t by) { return slot + by >= N::kSlots ? slot + by - N::kSlots : slot + by; };
 #pragma unroll
   for (int u = 0; u < N::kSlots - 1; ++u)
 #pragma unroll
-    for (int i = 0; i < N::kMoves; ++i) move(u & 1 ? base_q : base_p, u / 2, u, i);
+    for (int i = 0; i < N::kMoves; ++i) move(u & 1 ? from_q(u / 2) : from_p(u / 2), u, i);
   NVFP4_WAIT_VMCNT((N::kSlots - 3) * N::kMoves);  // this wave's part of K-tile 0 is in LDS
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
@@ -205,9 +234,9 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : 2) void ns_product_kernel(NsArgs 
   for (uint32_t kt = 0; kt < KT; ++kt) {
     const uint32_t slot_q = after(slot, 1), free_q = after(slot, N::kSlots - 1);
     const uint8_t *p = lds + slot * N::kSlotBytes, *q = lds + slot_q * N::kSlotBytes;
-    const uint32_t far = kt + N::kSlots / 2;
-    multiply<T>(acc, f[0], f[2], p + at_p[2], q + at_q[2], [&](int i) { move(base_p, far, free_q, i); });
-    multiply<T>(acc, f[1], f[3], p + at_p[3], q + at_q[3], [&](int i) { move(base_p, far, free_q, T + i); });
+    const uint8_t *far_p = from_p(kt + N::kSlots / 2), *far_q = from_q(kt + N::kSlots / 2);
+    multiply<T>(acc, f[0], f[2], p + at_p[2], q + at_q[2], [&](int i) { move(far_p, free_q, i); });
+    multiply<T>(acc, f[1], f[3], p + at_p[3], q + at_q[3], [&](int i) { move(far_p, free_q, T + i); });
     NVFP4_WAIT_LGKM0();                             // this wave's reads of the two slots are complete
     NVFP4_WAIT_VMCNT((N::kSlots - 4) * N::kMoves);  // its part of K-tile kt + 1 is in LDS
     __builtin_amdgcn_s_barrier();                   // every wave's: K-tile kt + 1 is there, these slots are free
@@ -215,8 +244,8 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : 2) void ns_product_kernel(NsArgs 
     const uint32_t next = after(slot, 2), next_q = after(slot, 3);
     p = lds + next * N::kSlotBytes;  // after the last K-tile: what is read is not used
     q = lds + next_q * N::kSlotBytes;
-    multiply<T>(acc, f[2], f[0], p + at_p[0], q + at_q[0], [&](int i) { move(base_q, far, slot, i); });
-    multiply<T>(acc, f[3], f[1], p + at_p[1], q + at_q[1], [&](int i) { move(base_q, far, slot, T + i); });
+    multiply<T>(acc, f[2], f[0], p + at_p[0], q + at_q[0], [&](int i) { move(far_q, slot, i); });
+    multiply<T>(acc, f[3], f[1], p + at_p[1], q + at_q[1], [&](int i) { move(far_q, slot, T + i); });
     slot = next;
   }
   NVFP4_WAIT_VMCNT(0);
@@ -225,14 +254,14 @@ __global__ __launch_bounds__(256, T == 4 ? 1 : 2) void ns_product_kernel(NsArgs 
   float *slab = reinterpret_cast<float *>(lds) + wave * N::kSlab;
   const int64_t mw = m0 + wm * (32 * T), nw = n0 + wn * (32 * T);
   if (t.d)
-    store_rows<T, E>(a, t.d, t.e, muon_ld(t.N), mw, nw, slab, lane, [&](int i) __attribute__((always_inline)) {
+    store_rows<T, E>(a, t.d, t.e, t.M * muon_ld(t.N), muon_ld(t.N), mw, nw, slab, lane, [&](int i) __attribute__((always_inline)) {
 #pragma unroll
       for (int j = 0; j < T; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) slab[((r >> 2) * 8 + h * 4 + (r & 3)) * N::kStride + j * 32 + lr] = acc[i][j][r];
     });
   if (t.dt && !(a.symmetric && m0 == n0))
-    store_rows<T, E>(a, t.dt, t.e, muon_ld(t.M), nw, mw, slab, lane, [&](int j) __attribute__((always_inline)) {
+    store_rows<T, E>(a, t.dt, t.e, t.N * muon_ld(t.M), muon_ld(t.M), nw, mw, slab, lane, [&](int j) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < T; ++i)
 #pragma unroll
@@ -312,12 +341,12 @@ __global__ __launch_bounds__(256) void muon_sums_kernel(MuonArgs a) {
   if (threadIdx.x == 0) t.parts[group] = sums[0] + sums[1] + sums[2] + sums[3];
 }
 
-// X and its transpose in fp16, 64 x 64 elements to a workgroup, zeros beyond the tensor
+// X and its transpose in two parts, 64 x 64 elements to a workgroup, zeros beyond the tensor
 __global__ __launch_bounds__(256) void muon_form_kernel(MuonArgs a) {
   uint32_t group = blockIdx.x;
   const MuonMat &t = a.mat[muon_mat_of(a.end, group)];
   __shared__ double sums[4];
-  __shared__ __attribute__((aligned(16))) _Float16 tile[64][72];
+  __shared__ __attribute__((aligned(16))) _Float16 tile[2][64][72];
   double sum = 0.0;
   for (uint32_t i = threadIdx.x; i < t.sums; i += 256) sum += t.parts[i];
   sum = wave_sum64(sum);
@@ -333,7 +362,7 @@ __global__ __launch_bounds__(256) void muon_form_kernel(MuonArgs a) {
     const int r = (threadIdx.x >> 3) + 32 * k, c = (threadIdx.x & 7) * 8;
     const int n = r0 + r < t.rows ? t.cols - (c0 + c) : 0;
     const int64_t i = (int64_t)(r0 + r) * t.cols + c0 + c;
-    half8 x = (half8)(_Float16)0.0f;
+    half8 x[2] = {(half8)(_Float16)0.0f, (half8)(_Float16)0.0f};
     if (n > 0) {
       float g[8], m[8];
       if (t.m) {
@@ -346,17 +375,23 @@ __global__ __launch_bounds__(256) void muon_form_kernel(MuonArgs a) {
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < n) x[j] = (_Float16)(float)((double)g[j] * by);
+        if (j < n) two_parts((float)((double)g[j] * by), x, j);
     }
-    *reinterpret_cast<half8 *>(t.direct + (r0 + r) * muon_ld(t.cp) + c0 + c) = x;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) tile[c + j][r] = x[j];
+    for (int part = 0; part < 2; ++part) {
+      *reinterpret_cast<half8 *>(t.direct + (part * t.rp + r0 + r) * muon_ld(t.cp) + c0 + c) = x[part];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) tile[part][c + j][r] = x[part][j];
+    }
   }
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int r = (threadIdx.x >> 3) + 32 * k, c = (threadIdx.x & 7) * 8;
-    *reinterpret_cast<half8 *>(t.turned + (c0 + r) * muon_ld(t.rp) + r0 + c) = *reinterpret_cast<const half8 *>(&tile[r][c]);
+#pragma unroll
+    for (int part = 0; part < 2; ++part)
+      *reinterpret_cast<half8 *>(t.turned + (part * t.cp + c0 + r) * muon_ld(t.rp) + r0 + c) =
+          *reinterpret_cast<const half8 *>(&tile[part][r][c]);
   }
 }
 
@@ -365,7 +400,7 @@ __global__ __launch_bounds__(256) void muon_update_kernel(MuonArgs a) {
   uint32_t group = blockIdx.x;
   const MuonMat &t = a.mat[muon_mat_of(a.end, group)];
   const int64_t n = (int64_t)t.rows * t.cols, start = (int64_t)group * kMuonChunk;
-  const int64_t row0 = start / t.cols;
+  const int64_t row0 = start / t.cols, plane = t.rp * muon_ld(t.cp);
   const uint32_t col0 = (uint32_t)(start - row0 * t.cols);
   float top = 0.0f;
 #pragma unroll 2
@@ -378,13 +413,13 @@ __global__ __launch_bounds__(256) void muon_update_kernel(MuonArgs a) {
     float u[8];
     if (c + 8 <= (uint32_t)t.cols) {
       typedef half8 __attribute__((aligned(2))) half8_at2;
-      const half8 q = *reinterpret_cast<const half8_at2 *>(x + c);
+      const half8 q = *reinterpret_cast<const half8_at2 *>(x + c), q2 = *reinterpret_cast<const half8_at2 *>(x + plane + c);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) u[j] = (float)q[j] * (1.0f / kMuonX);
+      for (int j = 0; j < 8; ++j) u[j] = ((float)q[j] + (float)q2[j]) * (1.0f / kMuonX);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        u[j] = i + j < n ? (float)x[c] * (1.0f / kMuonX) : 0.0f;
+        u[j] = i + j < n ? ((float)x[c] + (float)x[plane + c]) * (1.0f / kMuonX) : 0.0f;
         if (++c == (uint32_t)t.cols) {
           c = 0;
           x += muon_ld(t.cp);
@@ -468,8 +503,8 @@ hipError_t launch_muon_product(NsArgs &a, int tile, hipStream_t s) {
     return a.symmetric ? down * (down + 1) / 2 : down * across;
   });
   // Tiles of 128 that are no more than the compute units have all of LDS for
-  // transfers ahead, more share it by twos: 7 matrices of 1024 x 1152 take 19.5 and
-  // 23 us for the 252 tiles of a square, 34 and 27 for the 504 of the last product.
+  // transfers ahead, more share it by twos: 2048 x 2048 takes 54 and 56 us for the 136
+  // tiles of a square, 7 matrices of 1024 x 1152 61 and 54 for the 504 of the last product.
   // Tiles of 64 likewise, by twos and fours.
   if (tile == 256)
     launch_product<4, 5>(a, n, s);
