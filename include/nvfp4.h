@@ -237,6 +237,7 @@ int nvfp4_dequantize(const nvfp4_tensor *q, float *y, int64_t ld_y, void *stream
  *              (a late partial's flag may still be raised).
  * Operands are expanded exactly to fp16 in registers and multiplied on MFMA
  * with fp32 accumulation; the per-tensor scales are applied in the epilogue.
+ * Block scales may stand at any address; 4-byte aligned ones are quickest.
  */
 int nvfp4_gemm(const nvfp4_tensor *a, const nvfp4_tensor *b, void *c, int32_t c_dtype, int64_t ldc, void *workspace,
                size_t workspace_bytes, void *stream);
@@ -635,7 +636,8 @@ typedef struct {
  *   h : device bf16 [M][N], with the maxima that its quantisation needs, if wanted
  *   gate, up : NULL, or where the products are kept, rounded to bf16, for the
  *              gradient (their maxima have to be NULL)
- * M, N and K are multiples of 16; K a multiple of 128 is quickest.  Maxima are
+ * M, N and K are multiples of 16; K a multiple of 128 is quickest, with block scales
+ * 4-byte aligned (they may stand at any address).  Maxima are
  * raised by atomic maxima: the caller initialises them.  rht_seed: the signs of
  * amax_rht_col.  Outputs overlap neither each other nor the operands.
  */

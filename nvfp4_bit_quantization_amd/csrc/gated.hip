@@ -744,8 +744,9 @@ hipError_t launch(const GatedArgs &a, hipStream_t s) {
     return hipGetLastError();
   }
   const int64_t large = tiles(a, 256, BACK ? 256 : 128), small = tiles(a, 128, BACK ? 128 : 64);
-  // the pipeline's offsets have 32 bits
-  if (g.K % kFBK == 0 && g.K / 2 * (g.M > g.N ? g.M : g.N) < (1ll << 32) && (large + 255) / 256 * 640 <= small)
+  // the pipeline's offsets have 32 bits, and it moves scales by dwords
+  const bool fit = scales_fit(g.a_scales) && scales_fit(g.b_scales) && (BACK || scales_fit(a.u_scales));
+  if (g.K % kFBK == 0 && fit && g.K / 2 * (g.M > g.N ? g.M : g.N) < (1ll << 32) && (large + 255) / 256 * 640 <= small)
     hipLaunchKernelGGL((gated_fast_kernel<BACK>), dim3((uint32_t)large), block, 0, s, a);
   else
     hipLaunchKernelGGL((gated_generic_kernel<BACK, 2>), dim3((uint32_t)small), block, 0, s, a);

@@ -339,7 +339,7 @@ __global__ __launch_bounds__(kGThreads) void gemm_streamk_kernel(GemmArgs g, Str
 
 bool gemm_fast_ok(const GemmArgs &g) {
   return g.M % 256 == 0 && g.N % 256 == 0 && g.K % kFBK == 0 && g.K / 2 * (g.M > g.N ? g.M : g.N) < (1ll << 32) &&
-         g.ldc * 256 < (1ll << 31);
+         g.ldc * 256 < (1ll << 31) && scales_fit(g.a_scales) && scales_fit(g.b_scales);
 }
 
 size_t gemm_workspace_bytes(int cus) { return kGemmWsSlots + (size_t)cus * kGemmSlotBytes; }

@@ -265,6 +265,11 @@ constexpr int kFStageCodes = 512 * 64;         // bytes of codes per stage
 constexpr int kFStageBytes = kFStageCodes + 512 * 8;
 constexpr int kFStages = 3;
 
+// Whether the fast path may take a tensor's scales, which it transfers by dwords: a
+// row has K / 16 of them, a multiple of 8, so that all rows are aligned as the first
+// is.  (Codes are 16-byte aligned in every call.)
+inline bool scales_fit(const uint8_t *scales) { return ((uintptr_t)scales & 3u) == 0; }
+
 struct FastCtx {
   const uint8_t *cbase;  // codes of the operand this wave transfers (A: waves 0-1, B: waves 2-3)
   const uint8_t *sbase;  // its scales
