@@ -5,9 +5,22 @@
 
 namespace nvfp4 {
 
+// the largest of a wave's numbers, in each of its lanes
+__device__ __forceinline__ uint32_t wave_top(uint32_t v) {
+  const auto top = [](float a, float b) { return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b))); };
+  float f = __uint_as_float(v);  // only moved as such
+  f = top(f, dpp<0x128>(f));
+  f = top(f, dpp<0x124>(f));
+  f = top(f, dpp<0x122>(f));
+  f = top(f, dpp<0x121>(f));
+  f = swapped16(f, top);
+  f = swapped32(f, top);
+  return __float_as_uint(f);
+}
+
 // Raise up to N maxima (null: not wanted) to those of a workgroup of four waves:
-// bits[k] of every lane, patterns of non-negative floats, which order as their
-// values do.  Atomics on one address take some 8 ns each, whoever issues them: one
+// bits[k] of every lane, patterns of floats without their sign, which order as their
+// values do, with what is not a number above infinity: as numbers, so that it stays.  Atomics on one address take some 8 ns each, whoever issues them: one
 // to a wave made 43 of 71 us of a gated product of 16 rows (5120 waves).  So there
 // is one to a workgroup, and only where it raises what stands there; a maximum
 // does not depend on the order, nor on reading an older value first.
@@ -18,8 +31,8 @@ __device__ __forceinline__ void raise_maxima(unsigned int *const out[N], const u
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     if (!out[k]) continue;
-    const float top = wave_max(__uint_as_float(bits[k]));
-    if ((threadIdx.x & 63u) == 0) tops[k][wave] = __float_as_uint(top);
+    const uint32_t top = wave_top(bits[k]);
+    if ((threadIdx.x & 63u) == 0) tops[k][wave] = top;
   }
   __syncthreads();
 #pragma unroll

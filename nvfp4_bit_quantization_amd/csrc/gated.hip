@@ -56,7 +56,7 @@ __device__ __forceinline__ float normal_cdf(float x, float &e) {
 template <int ACT>
 __device__ __forceinline__ float act(float x) {
   if (ACT == NVFP4_SILU) return x * sigmoid(x);
-  if (ACT == NVFP4_RELU) return fmaxf(x, 0.0f);
+  if (ACT == NVFP4_RELU) return x <= 0.0f ? 0.0f : x;  // (a NaN stays one)
   if (ACT == NVFP4_GELU) {
     float e;
     return x * normal_cdf(x, e);
@@ -70,7 +70,7 @@ __device__ __forceinline__ void act_grad(float x, float &f, float &df) {
     f = x * p;
     df = p * fmaf(x, 1.0f - p, 1.0f);
   } else if (ACT == NVFP4_RELU) {
-    f = fmaxf(x, 0.0f);
+    f = x <= 0.0f ? 0.0f : x;
     df = x > 0.0f ? 1.0f : 0.0f;
   } else if (ACT == NVFP4_GELU) {
     float e;

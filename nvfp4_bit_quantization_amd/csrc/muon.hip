@@ -402,7 +402,7 @@ __global__ __launch_bounds__(256) void muon_update_kernel(MuonArgs a) {
   const int64_t n = (int64_t)t.rows * t.cols, start = (int64_t)group * kMuonChunk;
   const int64_t row0 = start / t.cols, plane = t.rp * muon_ld(t.cp);
   const uint32_t col0 = (uint32_t)(start - row0 * t.cols);
-  float top = 0.0f;
+  uint32_t top = 0;
 #pragma unroll 2
   for (uint32_t o = threadIdx.x * 8; o < kMuonChunk; o += 2048) {
     const int64_t i = start + o;
@@ -451,12 +451,12 @@ __global__ __launch_bounds__(256) void muon_update_kernel(MuonArgs a) {
       const bool rounds = t.copy || (t.flags & MF_PARAM_BF16);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < n - i) top = fmaxf(top, fabsf(rounds ? round_bf16(p[j]) : p[j]));
+        if (j < n - i) top = max(top, __float_as_uint(rounds ? round_bf16(p[j]) : p[j]) & 0x7FFFFFFFu);
     }
   }
   if (t.amax) {
     unsigned int *const out[1] = {reinterpret_cast<unsigned int *>(t.amax)};
-    const uint32_t bits[1] = {__float_as_uint(top)};
+    const uint32_t bits[1] = {top};
     raise_maxima<1>(out, bits);
   }
 }

@@ -1,0 +1,68 @@
+"""Block operators at the edges of what their contracts allow: values that are not
+finite in the maxima, batches and lists of nothing."""
+import pytest
+
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+B = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def nv():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import nvfp4_bit_quantization_amd as nv
+    nv.lib()
+    return nv
+
+
+def rand(*shape, seed=1, dtype=B, size=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * size).to(dtype)
+
+
+def quantised(nv, rows, cols, seed):
+    return nv.quantize(rand(rows, cols, seed=seed), [nv.QuantSpec.of("row")])[0]
+
+
+# few rows, tiles of 128, tiles of 256
+@pytest.mark.parametrize("rows,cols", [(48, 80), (208, 144), (8192, 2048)], ids=str)
+@pytest.mark.parametrize("activation", ["silu", "gelu", "gelu_tanh", "relu"])
+def test_maxima_of_gated_gradients_keep_a_nan(nv, rows, cols, activation):
+    """As nvfp4_gemm_amax's do: a gradient that is not a number is not hidden by the ones beside it, nor hides an infinity."""
+    say("gated gradient, NaN", rows, cols, activation)
+    dy, w = quantised(nv, rows, 128, 1), quantised(nv, cols, 128, 2)
+    gate, up = rand(rows, cols, seed=3), rand(rows, cols, seed=4)
+    top = torch.zeros(2, device="cuda")
+    gate[rows - 5, cols - 7] = float("nan")
+    dgate, dup = nv.gemm_gated_backward(dy, w, gate, up, activation, amax_gate=top[:1], amax_up=top[1:])
+    assert torch.isnan(dup[rows - 5, cols - 7]) and torch.isnan(top[1])
+    assert torch.isnan(dgate).any() == torch.isnan(top[0])
+    gate[rows - 5, cols - 7] = 1.0
+    up[rows - 5, cols - 7] = float("inf")
+    top.zero_()
+    dgate, dup = nv.gemm_gated_backward(dy, w, gate, up, activation, amax_gate=top[:1], amax_up=top[1:])
+    assert torch.isinf(dgate[rows - 5, cols - 7]) and torch.isinf(top[0]) and top[1] == dup.abs().max().float()
+
+
+@pytest.mark.parametrize("rows,cols", [(48, 80), (208, 144), (4096, 2048)], ids=str)
+def test_maxima_of_gated_products_keep_a_nan(nv, rows, cols):
+    """An operand's scale that is not a number reaches h's maximum."""
+    say("gated, NaN", rows, cols)
+    a, g, u = quantised(nv, rows, 2048, 1), quantised(nv, cols, 2048, 2), quantised(nv, cols, 2048, 3)
+    top = torch.zeros(1, device="cuda")
+    a.scales.view(-1)[rows // 2 * 128 + 3] = 0x7F
+    h, _, _ = nv.gemm_gated(a, g, u, keep=False, amax=top)
+    assert torch.isnan(h[rows // 2]).all() and torch.isnan(h).sum() == cols and torch.isnan(top)
+
+
+def test_maximum_of_a_step_keeps_a_nan(nv):
+    say("muon, NaN")
+    p, g = rand(70, 90, seed=5, dtype=torch.float32), rand(70, 90, seed=6, dtype=torch.float32)
+    g[3, 4] = float("nan")
+    top = torch.zeros(1, device="cuda")
+    nv.muon([nv.MuonTensor(p, g, amax=top)], 0.1)
+    assert torch.isnan(p).any() and torch.isnan(top)
