@@ -1071,7 +1071,7 @@ def _rope_common(ref, freqs, positions, cu, q_weight, k_weight, k):
         batch = cu.numel() - 1
         _vector(cu, batch + 1, device, "cu", torch.int32)
         begin = cu.data_ptr()
-    elif batch == 0:
+    if batch == 0 and cu is None:  # no sequences: one of no tokens
         batch, tokens = 1, 0
     if freqs is not None:
         rot = freqs.numel()

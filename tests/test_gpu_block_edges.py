@@ -66,3 +66,22 @@ def test_maximum_of_a_step_keeps_a_nan(nv):
     top = torch.zeros(1, device="cuda")
     nv.muon([nv.MuonTensor(p, g, amax=top)], 0.1)
     assert torch.isnan(p).any() and torch.isnan(top)
+
+
+@pytest.mark.parametrize("placed", [False, True], ids=["counted", "positions"])
+@pytest.mark.parametrize("norm", [False, True], ids=["plain", "norm"])
+def test_rotation_of_an_empty_batch(nv, placed, norm):
+    """No sequences, whether their tokens' positions are counted or given: empty results, zero gradients of the weights."""
+    say("rope, no sequences", placed, norm)
+    q, k = rand(0, 5, 8, 64), rand(0, 5, 2, 64)
+    freqs, _ = nv.rope_frequencies(64)
+    w = torch.ones(64, device="cuda") if norm else None
+    opts = dict(positions=torch.empty(0, dtype=torch.int64, device="cuda") if placed else None, q_weight=w, k_weight=w)
+    a, b = nv.qk_rope(q, k, freqs, **opts)
+    assert a.shape == q.shape and b.shape == k.shape
+    nv.nvfp4_qk_rope(q, k, a, b, freqs, **opts)
+    dq, dk, dqw, dkw = nv.qk_rope_backward(a, b, freqs, q, k, **opts)
+    assert dq.shape == q.shape and dk.shape == k.shape
+    assert not norm or not (dqw.any() or dkw.any())
+    with pytest.raises(ValueError):
+        nv.qk_rope(q, k, freqs, positions=torch.zeros(5, dtype=torch.int64, device="cuda"))
