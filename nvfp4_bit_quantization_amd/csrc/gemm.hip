@@ -24,6 +24,99 @@
 
 namespace nvfp4 {
 
+constexpr int kBK = 64;         // K per tile
+constexpr int kRowBytes = 48;   // LDS bytes per row: 32 bytes of codes + 16 pad (bank spread)
+
+__device__ __forceinline__ _Float16 scale_f16(uint32_t scales4, int blk) {
+  // E4M3 byte -> fp32 (exact) -> fp16 (exact: 2^-9 .. 448 are fp16 normals)
+  const uint32_t b = (scales4 >> (8 * blk)) & 0xFFu;
+  return (_Float16)e4m3_value(b);
+}
+
+// Each wave folds its maxima with one device-scope atomic maximum per tensor (bit
+// patterns of non-negative floats order like the values).
+__device__ __forceinline__ void fused_max_flush(const FusedMax &f, const GemmArgs &g) {
+  uint32_t mp = f.plain;
+  float mr = f.rht;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    mp = max(mp, (uint32_t)__shfl_xor((int)mp, off, 64));
+    mr = fmaxf(mr, __shfl_xor(mr, off, 64));
+  }
+  if ((threadIdx.x & 63u) == 0) {
+    if (g.amax_plain) atomicMax(g.amax_plain, mp << 16);
+    if (g.amax_rht) atomicMax(g.amax_rht, __float_as_uint(mr * 0.25f));  // the exact 1/4 of the transform
+  }
+}
+
+template <int TM, int TN>
+struct GemmTile {
+  static constexpr int BM = 64 * TM;
+  static constexpr int BN = 64 * TN;
+  static constexpr int ROWS = BM + BN;
+};
+
+// Global -> register staging of one K-tile: 32 bytes of codes and 4 scale bytes
+// for each of the BM + BN rows.  Rows past M/N and k-blocks past K read as 0.
+template <int TM, int TN>
+struct Stage {
+  static constexpr int ROWS = GemmTile<TM, TN>::ROWS;
+  static constexpr int CHUNKS = ROWS * 4;  // 8-byte chunks of codes
+  static constexpr int CPT = CHUNKS / kGThreads;
+  static constexpr int SPT = (ROWS + kGThreads - 1) / kGThreads;
+  uint2 code[CPT];
+  uint32_t scale[SPT];
+};
+
+template <int TM, int TN, typename Rows>
+__device__ __forceinline__ void stage_load(const Rows &src, int64_t kt, Stage<TM, TN> &st) {
+  constexpr int BM = GemmTile<TM, TN>::BM, ROWS = GemmTile<TM, TN>::ROWS;
+  const int64_t K = src.K(), kblocks = K / 16;
+#pragma unroll
+  for (int i = 0; i < Stage<TM, TN>::CPT; ++i) {
+    const int c = threadIdx.x + i * kGThreads;
+    const int row = c >> 2, part = c & 3;  // part = k-block within the tile
+    const RowRef ref = src.template ref<BM>(row);
+    const int64_t kb = kt * 4 + part;
+    uint2 v = make_uint2(0u, 0u);
+    if (ref.row < ref.rows && kb < kblocks) v = *reinterpret_cast<const uint2 *>(ref.codes + ref.row * (K / 2) + kb * 8);
+    st.code[i] = v;
+  }
+#pragma unroll
+  for (int i = 0; i < Stage<TM, TN>::SPT; ++i) {
+    const int row = threadIdx.x + i * kGThreads;
+    uint32_t w = 0;
+    if (row < ROWS) {
+      const RowRef ref = src.template ref<BM>(row);
+      if (ref.row < ref.rows) {
+        const uint8_t *p = ref.kind == 0 ? ref.scales + ref.row * kblocks : ref.scales + (ref.row / 16) * kblocks;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int64_t kb = kt * 4 + b;
+          if (kb < kblocks) w |= (uint32_t)p[kb] << (8 * b);
+        }
+      }
+    }
+    st.scale[i] = w;
+  }
+}
+
+template <int TM, int TN>
+__device__ __forceinline__ void stage_store(uint8_t *lcodes, uint32_t *lscales, const Stage<TM, TN> &st) {
+  constexpr int ROWS = GemmTile<TM, TN>::ROWS;
+#pragma unroll
+  for (int i = 0; i < Stage<TM, TN>::CPT; ++i) {
+    const int c = threadIdx.x + i * kGThreads;
+    const int row = c >> 2, part = c & 3;
+    *reinterpret_cast<uint2 *>(lcodes + row * kRowBytes + part * 8) = st.code[i];
+  }
+#pragma unroll
+  for (int i = 0; i < Stage<TM, TN>::SPT; ++i) {
+    const int row = threadIdx.x + i * kGThreads;
+    if (row < ROWS) lscales[row] = st.scale[i];
+  }
+}
+
 template <int TM, int TN>
 __global__ __launch_bounds__(kGThreads) void gemm_generic_kernel(GemmArgs g) {
   constexpr int BM = GemmTile<TM, TN>::BM, BN = GemmTile<TM, TN>::BN, ROWS = GemmTile<TM, TN>::ROWS;

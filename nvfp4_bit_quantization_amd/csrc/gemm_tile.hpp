@@ -1,6 +1,6 @@
 // Device code of the NVFP4-operand products (gfx950) that the plain GEMM and the
 // gated products share: operand expansion, per-tensor scales, producer-fused
-// maxima, the staging of ragged tiles and the pipelined 256x256 tile.
+// maxima, where a tile's rows come from and the pipelined 256x256 tile.
 #pragma once
 
 #include "gemm_device.hpp"
@@ -14,8 +14,6 @@ typedef _Float16 half8v __attribute__((ext_vector_type(8)));
 typedef float float16v __attribute__((ext_vector_type(16)));
 
 constexpr int kGThreads = 256;  // 4 waves as 2 x 2
-constexpr int kBK = 64;         // K per tile
-constexpr int kRowBytes = 48;   // LDS bytes per row: 32 bytes of codes + 16 pad (bank spread)
 
 // 8 codes in `q` with block scale `s` -> 8 exact fp16 operand values
 __device__ __forceinline__ half8v expand8(uint32_t q, _Float16 s) {
@@ -52,12 +50,6 @@ __device__ __forceinline__ EpiScale epi_scale(const GemmArgs &g) {
 
 __device__ __forceinline__ float epi_apply(float acc, const EpiScale &s) { return ldexpf(acc * s.inv_m, s.neg_e); }
 
-__device__ __forceinline__ _Float16 scale_f16(uint32_t scales4, int blk) {
-  // E4M3 byte -> fp32 (exact) -> fp16 (exact: 2^-9 .. 448 are fp16 normals)
-  const uint32_t b = (scales4 >> (8 * blk)) & 0xFFu;
-  return (_Float16)e4m3_value(b);
-}
-
 // ---------------------------------------------------------------------------
 // Producer-fused maxima of a bf16 output (nvfp4_gemm_amax): the per-tensor
 // maxima the quantisation of C needs, taken from the rounded outputs while
@@ -71,9 +63,8 @@ __device__ __forceinline__ _Float16 scale_f16(uint32_t scales4, int blk) {
 // serves directly as the K order of the B operand: K-step s takes r = 8s ..
 // 8s + 7, i.e. the rows rho(k) = (k & 3) | (h << 2) | ((k >> 2) << 3) of
 // group s, k = 8h + kk, and T's columns are permuted to match.  Products with
-// +-1 are exact; the sums are fp32.  Each wave folds its maxima with one
-// device-scope atomic maximum per tensor (bit patterns of non-negative floats
-// order like the values).
+// +-1 are exact; the sums are fp32.  How lanes' maxima are joined is the
+// launch's own.
 // ---------------------------------------------------------------------------
 typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
 
@@ -136,45 +127,13 @@ __device__ __forceinline__ void fused_max_block(FusedMax &f, const GemmArgs &g, 
   }
 }
 
-__device__ __forceinline__ void fused_max_flush(const FusedMax &f, const GemmArgs &g) {
-  uint32_t mp = f.plain;
-  float mr = f.rht;
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    mp = max(mp, (uint32_t)__shfl_xor((int)mp, off, 64));
-    mr = fmaxf(mr, __shfl_xor(mr, off, 64));
-  }
-  if ((threadIdx.x & 63u) == 0) {
-    if (g.amax_plain) atomicMax(g.amax_plain, mp << 16);
-    if (g.amax_rht) atomicMax(g.amax_rht, __float_as_uint(mr * 0.25f));  // the exact 1/4 of the transform
-  }
-}
-
-template <int TM, int TN>
-struct GemmTile {
-  static constexpr int BM = 64 * TM;
-  static constexpr int BN = 64 * TN;
-  static constexpr int ROWS = BM + BN;
-};
-
-// Global -> register staging of one K-tile: 32 bytes of codes and 4 scale bytes
-// for each of the BM + BN rows.  Rows past M/N and k-blocks past K read as 0.
-template <int TM, int TN>
-struct Stage {
-  static constexpr int ROWS = GemmTile<TM, TN>::ROWS;
-  static constexpr int CHUNKS = ROWS * 4;  // 8-byte chunks of codes
-  static constexpr int CPT = CHUNKS / kGThreads;
-  static constexpr int SPT = (ROWS + kGThreads - 1) / kGThreads;
-  uint2 code[CPT];
-  uint32_t scale[SPT];
-};
-
 // Where the rows of a tile's stage come from: its first A_ROWS rows are A's, the
 // others B's (PlainRows: rows m0 and n0 onwards of one A and one B).
 struct RowRef {
   const uint8_t *codes, *scales;
   int kind;
-  int64_t row, rows;  // beyond `rows` the operand is zero
+  int64_t row, rows;  // the tensor has `rows`: what stands for those beyond is the caller's to say (the
+                      // plain product takes zeros, the gated ones the last row, which they do not store)
 };
 struct PlainRows {
   const GemmArgs &g;
@@ -194,58 +153,10 @@ struct PlainRows {
   __device__ __forceinline__ int kind(uint32_t r) const { return r < 256 ? g.a_kind : g.b_kind; }
 };
 
-template <int TM, int TN, typename Rows>
-__device__ __forceinline__ void stage_load(const Rows &src, int64_t kt, Stage<TM, TN> &st) {
-  constexpr int BM = GemmTile<TM, TN>::BM, ROWS = GemmTile<TM, TN>::ROWS;
-  const int64_t K = src.K(), kblocks = K / 16;
-#pragma unroll
-  for (int i = 0; i < Stage<TM, TN>::CPT; ++i) {
-    const int c = threadIdx.x + i * kGThreads;
-    const int row = c >> 2, part = c & 3;  // part = k-block within the tile
-    const RowRef ref = src.template ref<BM>(row);
-    const int64_t kb = kt * 4 + part;
-    uint2 v = make_uint2(0u, 0u);
-    if (ref.row < ref.rows && kb < kblocks) v = *reinterpret_cast<const uint2 *>(ref.codes + ref.row * (K / 2) + kb * 8);
-    st.code[i] = v;
-  }
-#pragma unroll
-  for (int i = 0; i < Stage<TM, TN>::SPT; ++i) {
-    const int row = threadIdx.x + i * kGThreads;
-    uint32_t w = 0;
-    if (row < ROWS) {
-      const RowRef ref = src.template ref<BM>(row);
-      if (ref.row < ref.rows) {
-        const uint8_t *p = ref.kind == 0 ? ref.scales + ref.row * kblocks : ref.scales + (ref.row / 16) * kblocks;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int64_t kb = kt * 4 + b;
-          if (kb < kblocks) w |= (uint32_t)p[kb] << (8 * b);
-        }
-      }
-    }
-    st.scale[i] = w;
-  }
-}
-
-template <int TM, int TN>
-__device__ __forceinline__ void stage_store(uint8_t *lcodes, uint32_t *lscales, const Stage<TM, TN> &st) {
-  constexpr int ROWS = GemmTile<TM, TN>::ROWS;
-#pragma unroll
-  for (int i = 0; i < Stage<TM, TN>::CPT; ++i) {
-    const int c = threadIdx.x + i * kGThreads;
-    const int row = c >> 2, part = c & 3;
-    *reinterpret_cast<uint2 *>(lcodes + row * kRowBytes + part * 8) = st.code[i];
-  }
-#pragma unroll
-  for (int i = 0; i < Stage<TM, TN>::SPT; ++i) {
-    const int row = threadIdx.x + i * kGThreads;
-    if (row < ROWS) lscales[row] = st.scale[i];
-  }
-}
-
 // ===========================================================================
-// Fast path (M, N multiples of 256, K a multiple of 128): 256x256x128 tiles,
-// three LDS stages filled by direct global->LDS transfers.
+// Fast path (K a multiple of 128; M and N multiples of 256, or a row() that keeps to
+// the tensors' rows, as the gated products'): 256x256x128 tiles, three LDS stages
+// filled by direct global->LDS transfers.
 //
 // LDS stage layout (36 KiB): codes of the 256 A rows then the 256 B rows,
 // 64 bytes (one 128-wide K slice) per row in four 16-byte chunks stored in
