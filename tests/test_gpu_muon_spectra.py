@@ -99,3 +99,24 @@ def test_a_parameter_is_as_good_as_32_bits(nv):
         off = ((p.double() - want).norm() / want.norm()).item()
         print("off by %.2g" % off, flush=True)
         assert off <= 3 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("abc", [(3.5, 0.0, 0.0), (12.0, -24.0, 12.0), (-3.4, 0.0, 0.0)], ids=str)
+def test_iterations_at_the_bound(nv, abc):
+    """Singular values and polynomials as large as any that are taken: nothing leaves fp16's range.  One step: three
+    products' errors of the polynomial's terms, whose sizes add up to (|a| + 2 |b| + 3 |c|) with A's own in them."""
+    say("muon at the bound", abc)
+    one = torch.zeros(70, 90, device="cuda")
+    one[3, 5] = -2.0
+    row = torch.zeros(300, 400, device="cuda")
+    row[7] = torch.randn(400, generator=torch.Generator(device="cuda").manual_seed(3), device="cuda")
+    for x in (one, one.t().contiguous(), row, spectrum(("strong", 1, 1.0), 64, 200).float(), spectrum(("half", 1e-3), 200, 300).float()):
+        p = torch.zeros_like(x)
+        nv.muon([nv.MuonTensor(p, x, scale=1.0)], 1.0, nesterov=False, steps=1, coefficients=abc)
+        u = x.double() / x.double().norm()
+        u = u.t() if u.shape[0] > u.shape[1] else u
+        a = u @ u.t()
+        want = abc[0] * u + (abc[1] * a + abc[2] * (a @ a)) @ u
+        got = p.t() if p.shape[0] > p.shape[1] else p
+        room = (abs(abc[0]) + 2 * abs(abc[1]) + 3 * abs(abc[2])) * 3 * 2.0 ** -22
+        assert torch.isfinite(got).all() and (got.double() + want).norm() <= room  # (|u| = 1)
