@@ -1007,8 +1007,9 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_l
     position in a float64 tensor, for contexts longer by `factor` than the original_length that was trained on:
     scaling None: as they are; "linear": all slowed by the factor; "ntk": by a larger base, so that the slowest is slowed
     by the factor and the fastest is not; "yarn": by parts, pairs that turn less than beta_slow times in original_length
-    slowed, those that turn more than beta_fast times not, the others in proportion to their turns, with the magnitude
-    0.1 ln(factor) + 1."""
+    slowed, those that turn more than beta_fast times not, the others in proportion to their turns, as the method's paper has
+    it, with the magnitude 0.1 ln(factor) + 1.  Programs that go by a pair's index instead, in equal parts between the two
+    bounds, have other frequencies there: nvfp4_qk_rope takes any, those a model was trained with too."""
     import math
     import torch
     if rot_dim < 2 or rot_dim % 2:
