@@ -14,7 +14,7 @@
 // 16384 tokens, 5120 -> 2 x 20480 with h, gate and up stored, 4.87 to 5.14 ms (1.34 to
 // 1.41 PFLOP/s; the same products by themselves 1.27 at 5120 x 5120 x 8192, a
 // library's bf16 product of 8192^3 1.55), their gradient 2.7 to 2.8 ms (1.22 to 1.27: its
-// epilogue moves 2.7 GB).  16 tokens are bound by reading the weights: 106 MB in 28
+// epilogue moves 2.7 GB).  16 tokens are bound by reading the weights: 106 MB in 24
 // to 39 us.  What fills few tiles (1008 x 2736 x 1040: 27 us, gradient 20) by a
 // compute unit's way through K, 1.2 us a workgroup and K-tile of 128, behind a launch.
 #include "block_device.hpp"
@@ -722,7 +722,8 @@ __global__ __launch_bounds__(kGThreads) void gated_skinny_kernel(GatedArgs a) {
 int64_t tiles(const GatedArgs &a, int64_t bm, int64_t bn) { return (a.g.M + bm - 1) / bm * ((a.g.N + bn - 1) / bn); }
 
 // Which kernel.  Up to 64 rows the one that reads the weights once (20480 columns,
-// K 5120, forward: 16, 32, 64 rows in 28, 34, 67 us, in tiles of 128 rows 80).  Else
+// K 5120, forward: 16, 32, 64 rows in 24, 30, 46 us with the weights in the last-level
+// cache, 32, 42, 56 without; in tiles of 128 rows 77 and 80).  Else
 // the pipeline, where K fits its K-tiles and its large tiles leave few compute
 // units idle: a round of 256 of them takes as long as 640 of the small ones (two
 // to a compute unit).  Forward, K 5120: 256 x 20480 105 us against 126, 768 x 20480

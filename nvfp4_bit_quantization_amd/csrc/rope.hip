@@ -387,12 +387,18 @@ hipError_t launch_typed(const RopeArgs &a, hipStream_t s) {
 
 }  // namespace
 
-// Waves that share out heads where tokens are few (1024: 4096 packed tokens of 10 + 5
-// float32 heads of 80, backward, 24.7 us; 2048: 28.7, 4096: 29.9), and workgroups of a side at
-// most, which then go on to further tokens: two to a compute unit keep the weights
-// and frequencies that they hold in use and leave no short last round (2 x 8192
-// tokens, 40 + 8 heads of 128: 80.9 us and 122 backward; 256: 109 and 130, 384: 88
-// and 128, 768: 87 and 129, 1280: 86 and 133).
+// Waves that share out heads where tokens are few, and workgroups of a side at most,
+// which then go on to further tokens: two to a compute unit keep the weights and
+// frequencies that they hold in use and leave no short last round.  In us, by waves
+// 512, 1024, 2048, 4096: 10 + 5 float32 heads of 80, backward, 4096 tokens 30.0, 29.8,
+// 38.4, 35.9 and 8192 tokens 37.6, 37.7, 48.2, 50.6 (packed 4096: 24.7 for 1024, 28.7,
+// 29.9), forward 8192 tokens 19.1, 19.1, 19.3, 22.7; 40 + 8 heads of 128, 64 to 4096
+// tokens, the same within 0.5 with any.  By workgroups 256, 384, 512, 768, 1024: 40 + 8
+// heads of 128, 16384 tokens 108, 87, 78, 85, 84, backward 130, 129, 122, 127, 131; 65536
+// tokens 415, 331, 298, 320, 310, backward 489, 483, 460, 470, 477; 32768 tokens of 10 +
+// 5 float32 heads of 80, 84, 71, 59, 57, 58, backward 203, 193, 172, 172, 180; of 32 + 32
+// heads of 128, where both sides have as many, 210, 195, 200, 208, 199, backward 297, 304,
+// 332, 313, 309: there 512 is up to 12 % off the best.
 constexpr int64_t kRopeWaves = 1024, kRopeGroups = 512;
 
 // up to 8 units of 16 elements; a ninth where a head of 128 has a segment cut short
