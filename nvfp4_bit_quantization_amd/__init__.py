@@ -1154,6 +1154,13 @@ def _rope_backward(dq_out, dk_out, q, k, dq, dk, dq_weight, dk_weight, common, w
     _call("nvfp4_qk_rope_backward", device, a, _ptr(workspace), _nbytes(workspace), stream)
 
 
+def _rope_no_heads(dq_out, dk_out, dq_weight, dk_weight):
+    """A side of no heads is not looked at by the call: its weight's gradient is a sum of nothing."""
+    for dy, dw in ((dq_out, dq_weight), (dk_out, dk_weight)):
+        if dy is not None and dw is not None and dy.shape[-2] == 0:
+            dw.zero_()
+
+
 def _rope_backward_inputs(dq_out, dk_out, freqs, q, k, positions, cu, q_weight, k_weight):
     import torch
     common, w_dtype, device = _rope_common(dq_out, freqs, positions, cu, q_weight, k_weight, dk_out)
@@ -1190,6 +1197,8 @@ def nvfp4_qk_rope_backward(dq_out, dk_out, dq, dk, freqs, q=None, k=None, positi
             _vector(dw, dq.shape[-1], device, what, torch.float32)
     if workspace is not None:
         _scratch(workspace, device)
+    with _on_stream(stream):
+        _rope_no_heads(dq_out, dk_out, dq_weight, dk_weight)
     if stream is not None and workspace is None:
         with _on_stream(stream):
             _rope_backward(dq_out, dk_out, q, k, dq, dk, dq_weight, dk_weight, common, w_dtype, q_weight, k_weight, eps,
@@ -1218,6 +1227,7 @@ def qk_rope_backward(dq_out, dk_out, freqs, q=None, k=None, positions=None, cu=N
         dqw, dkw = _floats(2, dq.shape[-1], dq.device).unbind()
         if dk is None:
             dkw = None
+        _rope_no_heads(dq_out, dk_out, dqw, dkw)
     if workspace is not None:
         _scratch(workspace, device)
     _rope_backward(dq_out, dk_out, q, k, dq, dk, dqw, dkw, common, w_dtype, q_weight, k_weight, eps, interleaved, magnitude,

@@ -85,3 +85,30 @@ def test_rotation_of_an_empty_batch(nv, placed, norm):
     assert not norm or not (dqw.any() or dkw.any())
     with pytest.raises(ValueError):
         nv.qk_rope(q, k, freqs, positions=torch.zeros(5, dtype=torch.int64, device="cuda"))
+
+
+@pytest.mark.parametrize("heads,kv", [(0, 3), (3, 0)], ids=str)
+@pytest.mark.parametrize("given", [False, True], ids=["allocated", "given"])
+def test_weights_of_no_heads_have_a_gradient_of_zero(nv, heads, kv, given):
+    say("rope, a side of no heads", heads, kv, given)
+    both = rand(1, 9, 3, 64)
+    freqs, _ = nv.rope_frequencies(64)
+    w = torch.ones(64, device="cuda")
+    sides = [both[:, :, :n] for n in (heads, kv)]
+    opts = dict(q_weight=w, k_weight=w)
+    outs = nv.qk_rope(*sides, freqs, **opts)
+    want, _ = nv.qk_rope(both, None, freqs, q_weight=w)
+    assert torch.equal(outs[1 if kv else 0], want) and outs[0 if kv else 1].numel() == 0
+    _, _, dw, _ = nv.qk_rope_backward(want, None, freqs, both, None, q_weight=w)
+    for stream in (None, torch.cuda.Stream()):
+        torch.cuda.synchronize()
+        torch.full((4096,), float("nan"), device="cuda")  # (what an uninitialised result may find)
+        if given:
+            got = [torch.full((64,), 7.0, device="cuda") for _ in range(2)]
+            torch.cuda.synchronize()
+            nv.nvfp4_qk_rope_backward(*outs, *(torch.empty_like(t) for t in sides), freqs, *sides, dq_weight=got[0], dk_weight=got[1],
+                                      stream=stream, **opts)
+        else:
+            got = nv.qk_rope_backward(*outs, freqs, *sides, stream=stream, **opts)[2:]
+        torch.cuda.synchronize()
+        assert torch.equal(got[1 if kv else 0], dw) and not got[0 if kv else 1].any()
