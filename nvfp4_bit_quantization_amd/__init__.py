@@ -1250,11 +1250,20 @@ def _gated_matrix(t, shape, device, what, amax=None, amax_rht_col=None) -> bytes
 
 
 def _operands(*operands):
-    """Device of quantised operands that fit: all have one K, those after the first as many rows."""
+    """Device of quantised operands that fit: all have one K, those after the first as many rows, and their buffers hold
+    what their shapes say (halves of a quantised tensor are made by hand)."""
+    import torch
     device = operands[0].codes.get_device()
     for q in operands:
-        if q.codes.get_device() != device or q.scales.get_device() != device or device < 0:
+        codes, scales, S, n = q.codes, q.scales, q.global_scale, q.rows * q.cols
+        if codes.get_device() != device or scales.get_device() != device or S.get_device() != device or device < 0:
             raise ValueError("operands on one device are wanted")
+        if codes.nbytes < n // 2 or scales.nbytes < n // (256 if q.scale_kind == SCALE_2D16 else 16):
+            raise ValueError("an operand of %d x %d: its codes or scales are fewer" % (q.rows, q.cols))
+        if S.dtype != torch.float32 or S.nbytes < 4:
+            raise ValueError("operands: a float32 global scale is wanted")
+        if not codes.is_contiguous() or not scales.is_contiguous():
+            raise ValueError("operands: contiguous codes and scales are wanted")
         if q.cols != operands[0].cols or q.rows != operands[-1].rows and q is not operands[0]:
             raise ValueError("operands do not fit: %s" % ", ".join("%d x %d" % (o.rows, o.cols) for o in operands))
     return device

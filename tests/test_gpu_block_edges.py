@@ -112,3 +112,26 @@ def test_weights_of_no_heads_have_a_gradient_of_zero(nv, heads, kv, given):
             got = nv.qk_rope_backward(*outs, freqs, *sides, stream=stream, **opts)[2:]
         torch.cuda.synchronize()
         assert torch.equal(got[1 if kv else 0], dw) and not got[0 if kv else 1].any()
+
+
+def test_gated_operands_that_are_not_what_they_say_are_refused(nv):
+    """Before any launch: buffers that are too small, on other devices, with gaps."""
+    say("gated operands refused")
+    a, w, x = quantised(nv, 64, 128, 1), quantised(nv, 96, 128, 2), rand(64, 96)
+    two = nv.quantize(rand(96, 128), [nv.QuantSpec.of("2d")])[0]
+
+    def other(q, **kw):
+        kw = {**dict(codes=q.codes, scales=q.scales, global_scale=q.global_scale, amax=q.amax, rows=q.rows, cols=q.cols, scale_kind=q.scale_kind), **kw}
+        return nv.QTensor(**kw)
+
+    assert nv.gemm_gated(a, w, other(two))[0].shape == x.shape
+    more = other(w, codes=torch.cat([w.codes, w.codes]), scales=torch.cat([w.scales, w.scales]))  # (what lies behind is not read)
+    assert torch.equal(nv.gemm_gated(a, more, w)[0], nv.gemm_gated(a, w, w)[0])
+    for bad in (other(w, codes=w.codes[:95]), other(w, scales=w.scales[:95]), other(w, scales=w.scales.cpu()), other(w, global_scale=w.global_scale.cpu()),
+                other(w, global_scale=w.global_scale.double()), other(w, codes=torch.cat([w.codes, w.codes], 1)[:, :64]),
+                other(w, scales=torch.cat([w.scales, w.scales], 1)[:, :8]), other(w, global_scale=w.global_scale[:0]), other(two, scale_kind=nv.SCALE_1D16),
+                other(two, scales=two.scales[:5])):
+        for call in (lambda: nv.gemm_gated(a, bad, w), lambda: nv.gemm_gated(a, w, bad), lambda: nv.gemm_gated(bad, w, w),
+                     lambda: nv.gemm_gated_backward(a, bad, x, x)):
+            with pytest.raises(ValueError):
+                call()
