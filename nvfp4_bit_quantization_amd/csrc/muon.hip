@@ -19,7 +19,7 @@
 // and 3.3e-4 (binary32: 1.1e-5, 8.3e-5, 6.0e-4); 2048 x 4096 with 1 / i^2 2.9e-5 (4.9e-5).
 //
 // Large products are bound by the matrix instructions: of 5120 x 20480, X X^T runs
-// at 1.04 PFLOP/s of them, the product with X at 1.26 with 77 % of all cycles theirs,
+// at 1.19 PFLOP/s of them, the product with X at 1.24 with 76 % of all cycles theirs,
 // where a library's product of 8192^3 in fp16 reaches 1.49; the passes over momentum,
 // gradient and parameter move 5 TB/s.  Steps of two matrices of 5120 x 20480 take 27.7 ms
 // (without chains 45), 1.5 of them in those passes.  Small ones are bound by their
